@@ -405,6 +405,60 @@ ATTN_API attn_status sage_attention(const void* q, const void* k, const void* v,
                                     void* workspace, size_t workspace_bytes, attn_stream_t stream);
 
 /*
+ * attn_fwd_bf16_lse -- the BF16 forward for training: O and the row statistics that
+ * attn_bwd_bf16 forms the probabilities from again.
+ *   s[i, j] = softmax_scale * q_i . k_j for the keys j < limit(i), where
+ *   limit(i) = min(kv_len[b], causal ? i + 1 + Sk - Sq : Sk);
+ *   lse[i]  = log sum_j exp(s[i, j])          (natural logarithm)
+ *   O[i]    = sum_j exp(s[i, j] - lse[i]) v_j
+ * A row with limit(i) <= 0 sees no key: O = 0, lse = -inf.
+ *   q, o    : BF16 [B, Sq, Hq, 128], strides q_str / o_str
+ *   k, v    : BF16 [B, Sk, Hkv, 128], strides k_str / v_str; query head h reads key head
+ *             h / (Hq / Hkv); Hq a multiple of Hkv
+ *   lse     : float [B, Hq, Sq] output, contiguous
+ *   softmax_scale : finite, >= 0
+ *   causal  : 0 or 1; the last query sees the last key (Sk - Sq keys come before the first query)
+ *   kv_len  : device int32 [B] (4-byte aligned), each batch entry's number of keys, read on the
+ *             device and clamped to [0, Sk]; or NULL: Sk.  K and V past it may hold anything.
+ *             All other rows of Q, K and V must be finite.
+ * Probabilities are rounded to BF16 before the product with V, sums are FP32, O is rounded once.
+ * Enqueues one kernel on `stream`.  Sq and Sk in [1, 2^30].
+ */
+ATTN_API attn_status attn_fwd_bf16_lse(const void* q, const void* k, const void* v, void* o, float* lse, int B, int Sq,
+                                       int Sk, int Hq, int Hkv, int D, const int64_t q_str[3], const int64_t k_str[3],
+                                       const int64_t v_str[3], const int64_t o_str[3], float softmax_scale, int causal,
+                                       const int32_t* kv_len, attn_stream_t stream);
+
+/* attn_bwd_bf16_workspace_size -- bytes of device scratch attn_bwd_bf16 needs (0 for an empty problem). */
+ATTN_API size_t attn_bwd_bf16_workspace_size(int B, int Sq, int Sk, int Hq, int Hkv);
+
+/*
+ * attn_bwd_bf16 -- the gradients of attn_fwd_bf16_lse's O with respect to Q, K and V.
+ *   p[i, j]  = exp(s[i, j] - lse[i])          delta[i] = dout_i . o_i
+ *   dv_j     = sum_i p[i, j] dout_i           ds[i, j] = p[i, j] (dout_i . v_j - delta[i])
+ *   dk_j     = softmax_scale sum_i ds[i, j] q_i
+ *   dq_i     = softmax_scale sum_j ds[i, j] k_j
+ * sums over i also over the query heads that share a key head.  Rows without a key have dq = 0; keys that no
+ * query sees have dk = dv = 0; a row with one key has ds = 0.
+ *   dout    : BF16 [B, Sq, Hq, 128], finite, strides dout_str
+ *   q, k, v, softmax_scale, causal, kv_len : as given to the forward
+ *   o, lse  : as the forward wrote them
+ *   dq      : BF16 [B, Sq, Hq, 128] output; dk, dv : BF16 [B, Sk, Hkv, 128] outputs, every row written
+ *   workspace : at least attn_bwd_bf16_workspace_size(B, Sq, Sk, Hq, Hkv) bytes, 16-byte
+ *             aligned; overwritten, contents on entry do not matter
+ * p and ds are rounded to BF16 before the products that sum over them, sums are FP32 in a fixed
+ * order (no atomics: the same inputs give the same bits), each output is rounded once.
+ * Enqueues its kernels on `stream`; errors as attn_fwd_bf16_lse.
+ */
+ATTN_API attn_status attn_bwd_bf16(const void* dout, const void* q, const void* k, const void* v, const void* o,
+                                   const float* lse, void* dq, void* dk, void* dv, int B, int Sq, int Sk, int Hq,
+                                   int Hkv, int D, const int64_t dout_str[3], const int64_t q_str[3],
+                                   const int64_t k_str[3], const int64_t v_str[3], const int64_t o_str[3],
+                                   const int64_t dq_str[3], const int64_t dk_str[3], const int64_t dv_str[3],
+                                   float softmax_scale, int causal, const int32_t* kv_len, void* workspace,
+                                   size_t workspace_bytes, attn_stream_t stream);
+
+/*
  * attn_get_device_status -- synchronise `stream`, then read and clear the
  * device error words of all kernels.  ATTN_OK if no bounded wait ran out
  * since the last call, ATTN_ERR_DEVICE_TIMEOUT otherwise, ATTN_ERR_CUDA if

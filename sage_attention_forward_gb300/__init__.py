@@ -11,9 +11,12 @@ library has not been built, every call raises.
     sage_prepare(q, k, v, ...)        -> Prepared           (INT8 Q/K, e4m3 V, scales)
     sage_attn_fwd(prepared, S)        -> O
     sage_attention(q, k, v, ...)      -> O                 (prepare + fwd)
+    attn_fwd_bf16_lse(q, k, v, ...)   -> O, lse            (the forward for training)
+    attn_bwd_bf16(dout, q, k, v, O, lse, ...) -> dQ, dK, dV
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import math
 import os
@@ -24,7 +27,7 @@ import torch
 from .build import LIB as _LIB_PATH
 
 __all__ = ["AttnError", "attn_fwd_bf16", "sage_prepare", "sage_prepare_noalloc", "sage_attn_fwd", "sage_attention",
-           "Prepared", "e4m3_encode",
+           "Prepared", "e4m3_encode", "attn_fwd_bf16_lse", "attn_bwd_bf16", "attn_bwd_workspace",
            "sage_padded_len", "attn_get_device_status", "lib", "STATUS"]
 
 STATUS = {0: "ATTN_OK", 1: "ATTN_ERR_INVALID_ARG", 2: "ATTN_ERR_ALIGNMENT", 3: "ATTN_ERR_UNSUPPORTED",
@@ -101,6 +104,13 @@ def lib() -> ctypes.CDLL:
         L.attn_sm_clock_sample.restype = i
         L.sage_e4m3_encode.argtypes = [_vp, _vp, ctypes.c_int64, _vp]
         L.sage_e4m3_encode.restype = i
+        L.attn_fwd_bf16_lse.argtypes = [_vp] * 5 + [i] * 6 + [_I64x3] * 4 + [ctypes.c_float, i, _vp, _vp]
+        L.attn_fwd_bf16_lse.restype = i
+        L.attn_bwd_bf16_workspace_size.argtypes = [i] * 5
+        L.attn_bwd_bf16_workspace_size.restype = ctypes.c_size_t
+        L.attn_bwd_bf16.argtypes = [_vp] * 9 + [i] * 6 + [_I64x3] * 8 + [ctypes.c_float, i, _vp, _vp,
+                                                                       ctypes.c_size_t, _vp]
+        L.attn_bwd_bf16.restype = i
         L.attn_get_device_status.argtypes = [_vp]
         L.attn_get_device_status.restype = i
         L.attn_last_error.argtypes = []
@@ -393,6 +403,121 @@ def sage_attention(q, k, v, softmax_scale=None, q_norm_w=None, k_norm_w=None, rm
                                 _on_load_level(q_on_load, k_on_load), out.data_ptr(), os_, workspace.data_ptr(),
                                 workspace.numel(), _stream_ptr(stream)))
     return out
+
+
+@contextlib.contextmanager
+def _call_stream(t: torch.Tensor, stream):
+    """Makes t's device current and, when the caller names a stream, that stream: what the call
+    allocates then belongs to the stream its kernels run on.  Yields the stream's handle."""
+    if not t.is_cuda:
+        raise ValueError("tensors must be on a CUDA device")
+    with torch.cuda.device(t.device):
+        if stream is None:
+            yield torch.cuda.current_stream().cuda_stream
+        else:
+            if not hasattr(stream, "cuda_stream"):
+                stream = torch.cuda.ExternalStream(int(stream), device=t.device)
+            with torch.cuda.stream(stream):
+                yield stream.cuda_stream
+
+
+def _same_device(ref: torch.Tensor, **tensors) -> None:
+    for name, t in tensors.items():
+        if t is not None and t.device != ref.device:
+            raise ValueError(f"{name} is on {t.device}, expected {ref.device}")
+
+
+def _shaped(name: str, t: torch.Tensor, shape, dtype) -> None:
+    if tuple(t.shape) != tuple(shape) or t.dtype != dtype:
+        raise ValueError(f"{name} must be {tuple(shape)} {dtype}, got {tuple(t.shape)} {t.dtype}")
+
+
+def _train_shapes(q, k, v, kv_len):
+    for name, t in (("q", q), ("k", k), ("v", v)):
+        if t.dim() != 4:
+            raise ValueError(f"{name} must be [B, S, H, D], got {tuple(t.shape)}")
+    B, Sq, Hq, D = q.shape
+    Sk, Hkv = k.shape[1], k.shape[2]
+    _shaped("k", k, (B, Sk, Hkv, D), torch.bfloat16)
+    _shaped("v", v, (B, Sk, Hkv, D), torch.bfloat16)
+    if kv_len is not None:
+        _shaped("kv_len", kv_len, (B,), torch.int32)
+        if not kv_len.is_contiguous():
+            raise ValueError("kv_len must be contiguous")
+    _same_device(q, k=k, v=v, kv_len=kv_len)
+    return B, Sq, Sk, Hq, Hkv, D
+
+
+def _lse_arg(lse, B, Hq, Sq):
+    _shaped("lse", lse, (B, Hq, Sq), torch.float32)
+    if not lse.is_contiguous():
+        raise ValueError("lse must be contiguous")
+
+
+def attn_fwd_bf16_lse(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, softmax_scale: float | None = None,
+                      causal: bool = False, kv_len: torch.Tensor | None = None, out: torch.Tensor | None = None,
+                      lse: torch.Tensor | None = None, stream=None) -> tuple[torch.Tensor, torch.Tensor]:
+    """The BF16 forward for training: (O, lse), lse float32 [B, Hq, Sq] the rows' natural log-sum-exp.
+
+    q [B, Sq, Hq, 128], k and v [B, Sk, Hkv, 128] with Hq a multiple of Hkv.  causal: query i sees the keys
+    j <= i + Sk - Sq.  kv_len: int32 [B] on the device, each batch entry's number of keys (K and V past it
+    may hold anything).  A row that sees no key has O = 0 and lse = -inf."""
+    B, Sq, Sk, Hq, Hkv, D = _train_shapes(q, k, v, kv_len)
+    if softmax_scale is None:
+        softmax_scale = 1.0 / math.sqrt(D)
+    with _call_stream(q, stream) as st:
+        if out is None:
+            out = torch.empty((B, Sq, Hq, D), dtype=torch.bfloat16, device=q.device)
+        if lse is None:
+            lse = torch.empty((B, Hq, Sq), dtype=torch.float32, device=q.device)
+        _shaped("out", out, (B, Sq, Hq, D), torch.bfloat16)
+        _lse_arg(lse, B, Hq, Sq)
+        _same_device(q, out=out, lse=lse)
+        _check(lib().attn_fwd_bf16_lse(q.data_ptr(), k.data_ptr(), v.data_ptr(), out.data_ptr(), lse.data_ptr(), B, Sq,
+                                       Sk, Hq, Hkv, D, _bshd("q", q), _bshd("k", k), _bshd("v", v), _bshd("out", out),
+                                       float(softmax_scale), int(causal), None if kv_len is None else kv_len.data_ptr(),
+                                       st))
+    return out, lse
+
+
+def attn_bwd_workspace(B: int, Sq: int, Sk: int, Hq: int, Hkv: int, device) -> torch.Tensor:
+    return torch.empty(int(lib().attn_bwd_bf16_workspace_size(B, Sq, Sk, Hq, Hkv)), dtype=torch.uint8, device=device)
+
+
+def attn_bwd_bf16(dout: torch.Tensor, q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, out: torch.Tensor,
+                  lse: torch.Tensor, softmax_scale: float | None = None, causal: bool = False,
+                  kv_len: torch.Tensor | None = None, dq: torch.Tensor | None = None, dk: torch.Tensor | None = None,
+                  dv: torch.Tensor | None = None, workspace: torch.Tensor | None = None,
+                  stream=None) -> tuple[torch.Tensor, torch.Tensor, torch.Tensor]:
+    """(dQ, dK, dV) of attn_fwd_bf16_lse: dout is the gradient of its O; out and lse are what it returned,
+    the other arguments those it was given.  dK and dV are sums over the query heads that share a key head.
+    The same inputs give the same bits."""
+    B, Sq, Sk, Hq, Hkv, D = _train_shapes(q, k, v, kv_len)
+    if softmax_scale is None:
+        softmax_scale = 1.0 / math.sqrt(D)
+    _shaped("dout", dout, (B, Sq, Hq, D), torch.bfloat16)
+    _shaped("out", out, (B, Sq, Hq, D), torch.bfloat16)
+    _lse_arg(lse, B, Hq, Sq)
+    with _call_stream(q, stream) as st:
+        if dq is None:
+            dq = torch.empty((B, Sq, Hq, D), dtype=torch.bfloat16, device=q.device)
+        if dk is None:
+            dk = torch.empty((B, Sk, Hkv, D), dtype=torch.bfloat16, device=q.device)
+        if dv is None:
+            dv = torch.empty((B, Sk, Hkv, D), dtype=torch.bfloat16, device=q.device)
+        if workspace is None:
+            workspace = attn_bwd_workspace(B, Sq, Sk, Hq, Hkv, q.device)
+        _shaped("dq", dq, (B, Sq, Hq, D), torch.bfloat16)
+        _shaped("dk", dk, (B, Sk, Hkv, D), torch.bfloat16)
+        _shaped("dv", dv, (B, Sk, Hkv, D), torch.bfloat16)
+        _same_device(q, dout=dout, out=out, lse=lse, dq=dq, dk=dk, dv=dv, workspace=workspace)
+        _check(lib().attn_bwd_bf16(dout.data_ptr(), q.data_ptr(), k.data_ptr(), v.data_ptr(), out.data_ptr(),
+                                   lse.data_ptr(), dq.data_ptr(), dk.data_ptr(), dv.data_ptr(), B, Sq, Sk, Hq, Hkv, D,
+                                   _bshd("dout", dout), _bshd("q", q), _bshd("k", k), _bshd("v", v), _bshd("out", out),
+                                   _bshd("dq", dq), _bshd("dk", dk), _bshd("dv", dv), float(softmax_scale),
+                                   int(causal), None if kv_len is None else kv_len.data_ptr(), workspace.data_ptr(),
+                                   workspace.numel() * workspace.element_size(), st))
+    return dq, dk, dv
 
 
 def attn_selftest_wait_timeout(device=None, stream=None) -> str:

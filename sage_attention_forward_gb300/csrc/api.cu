@@ -707,6 +707,119 @@ attn_status sage_attention(const void* q, const void* k, const void* v, int B, i
   return ATTN_OK;
 }
 
+// ------------------------------------------------------------------ training
+// Shapes and mask of the training calls: *empty is set for B = 0 or no heads.
+static attn_status check_train(int B, int Sq, int Sk, int Hq, int Hkv, int D, int causal, const int32_t* kv_len,
+                               float softmax_scale, sa::TrainArgs& a, bool* empty) {
+  *empty = false;
+  if (D != 128) return fail(ATTN_ERR_UNSUPPORTED, "head dimension D=%d; only D=128 is supported", D);
+  if (B < 0 || Hq < 0 || Hkv < 0) return fail(ATTN_ERR_INVALID_ARG, "B=%d Hq=%d Hkv=%d must be >= 0", B, Hq, Hkv);
+  if (Sq < 1 || Sk < 1 || Sq > (1 << 30) || Sk > (1 << 30))
+    return fail(ATTN_ERR_INVALID_ARG, "Sq=%d Sk=%d must be in [1, 2^30]", Sq, Sk);
+  if ((Hq == 0) != (Hkv == 0) || (Hkv > 0 && Hq % Hkv != 0))
+    return fail(ATTN_ERR_INVALID_ARG, "Hq=%d must be a multiple of Hkv=%d", Hq, Hkv);
+  if (causal != 0 && causal != 1) return fail(ATTN_ERR_INVALID_ARG, "causal=%d must be 0 or 1", causal);
+  if (!(softmax_scale >= 0.0f && std::isfinite(softmax_scale)))
+    return fail(ATTN_ERR_INVALID_ARG, "softmax_scale must be finite and >= 0");
+  if (reinterpret_cast<uintptr_t>(kv_len) % 4 != 0) return fail(ATTN_ERR_ALIGNMENT, "kv_len is not 4-byte aligned");
+  if (B == 0 || Hq == 0) {
+    *empty = true;
+    return ATTN_OK;
+  }
+  TRY(check_grid(B, Hq, ((long long)Sq + 127) / 128 * 128));
+  TRY(check_grid(B, Hkv, ((long long)Sk + 127) / 128 * 128));
+  a.B = B;
+  a.Sq = Sq;
+  a.Sk = Sk;
+  a.Hq = Hq;
+  a.Hkv = Hkv;
+  a.scale = softmax_scale;
+  a.c_log2 = (float)((double)softmax_scale * kLog2e);
+  a.causal = causal;
+  a.kv_len = kv_len;
+  return ATTN_OK;
+}
+
+static attn_status check_buffer(const char* name, const void* ptr) {
+  if (ptr == nullptr) return fail(ATTN_ERR_INVALID_ARG, "%s is NULL", name);
+  if (!aligned16(ptr)) return fail(ATTN_ERR_ALIGNMENT, "%s is not 16-byte aligned", name);
+  return ATTN_OK;
+}
+
+attn_status attn_fwd_bf16_lse(const void* q, const void* k, const void* v, void* o, float* lse, int B, int Sq, int Sk,
+                              int Hq, int Hkv, int D, const int64_t q_str[3], const int64_t k_str[3],
+                              const int64_t v_str[3], const int64_t o_str[3], float softmax_scale, int causal,
+                              const int32_t* kv_len, attn_stream_t stream) {
+  bool empty = false;
+  sa::TrainArgs a;
+  TRY(check_train(B, Sq, Sk, Hq, Hkv, D, causal, kv_len, softmax_scale, a, &empty));
+  if (empty) return ATTN_OK;
+  long long qs[3], ks[3], vs[3], os[3];
+  TRY(check_strides("q", q, q_str, B, Sq, Hq, qs));
+  TRY(check_strides("k", k, k_str, B, Sk, Hkv, ks));
+  TRY(check_strides("v", v, v_str, B, Sk, Hkv, vs));
+  TRY(check_strides("o", o, o_str, B, Sq, Hq, os));
+  TRY(check_buffer("lse", lse));
+  TRY(check_device());
+  TRY(get_encoder());
+  CUtensorMap tq, tk, tv;
+  TRY(tmap_bhsd_bf16(&tq, q, B, Sq, Hq, qs));
+  TRY(tmap_bhsd_bf16(&tk, k, B, Sk, Hkv, ks));
+  TRY(tmap_bhsd_bf16(&tv, v, B, Sk, Hkv, vs));
+  cudaError_t e = sa::launch_attn_fwd_bf16_lse(tq, tk, tv, a, o, os, lse, (cudaStream_t)stream);
+  if (e != cudaSuccess) return fail_cuda(e, "attn_fwd_bf16_lse launch");
+  return ATTN_OK;
+}
+
+size_t attn_bwd_bf16_workspace_size(int B, int Sq, int Sk, int Hq, int Hkv) {
+  if (B < 1 || Sq < 1 || Sk < 1 || Hq < 1 || Hkv < 1) return 0;
+  return (size_t)2 * B * Hq * (size_t)sa::attn_bwd_padded_rows(Sq) * sizeof(float);
+}
+
+attn_status attn_bwd_bf16(const void* dout, const void* q, const void* k, const void* v, const void* o,
+                          const float* lse, void* dq, void* dk, void* dv, int B, int Sq, int Sk, int Hq, int Hkv,
+                          int D, const int64_t dout_str[3], const int64_t q_str[3], const int64_t k_str[3],
+                          const int64_t v_str[3], const int64_t o_str[3], const int64_t dq_str[3],
+                          const int64_t dk_str[3], const int64_t dv_str[3], float softmax_scale, int causal,
+                          const int32_t* kv_len, void* workspace, size_t workspace_bytes, attn_stream_t stream) {
+  bool empty = false;
+  sa::TrainArgs a;
+  TRY(check_train(B, Sq, Sk, Hq, Hkv, D, causal, kv_len, softmax_scale, a, &empty));
+  if (empty) return ATTN_OK;
+  long long qs[3], ks[3], vs[3];
+  sa::BwdTensors t;
+  TRY(check_strides("dout", dout, dout_str, B, Sq, Hq, t.dout_str));
+  TRY(check_strides("q", q, q_str, B, Sq, Hq, qs));
+  TRY(check_strides("k", k, k_str, B, Sk, Hkv, ks));
+  TRY(check_strides("v", v, v_str, B, Sk, Hkv, vs));
+  TRY(check_strides("o", o, o_str, B, Sq, Hq, t.o_str));
+  TRY(check_strides("dq", dq, dq_str, B, Sq, Hq, t.dq_str));
+  TRY(check_strides("dk", dk, dk_str, B, Sk, Hkv, t.dk_str));
+  TRY(check_strides("dv", dv, dv_str, B, Sk, Hkv, t.dv_str));
+  TRY(check_buffer("lse", lse));
+  TRY(check_buffer("workspace", workspace));
+  const size_t need = attn_bwd_bf16_workspace_size(B, Sq, Sk, Hq, Hkv);
+  if (workspace_bytes < need)
+    return fail(ATTN_ERR_INVALID_ARG, "attn_bwd_bf16: workspace_bytes=%zu < %zu required", workspace_bytes, need);
+  TRY(check_device());
+  TRY(get_encoder());
+  CUtensorMap tq, tk, tv, td;
+  TRY(tmap_bhsd_bf16(&tq, q, B, Sq, Hq, qs));
+  TRY(tmap_bhsd_bf16(&tk, k, B, Sk, Hkv, ks));
+  TRY(tmap_bhsd_bf16(&tv, v, B, Sk, Hkv, vs));
+  TRY(tmap_bhsd_bf16(&td, dout, B, Sq, Hq, t.dout_str));
+  t.o = o;
+  t.dout = dout;
+  t.lse = lse;
+  t.dq = dq;
+  t.dk = dk;
+  t.dv = dv;
+  cudaError_t e = sa::launch_attn_bwd_bf16(tq, tk, tv, td, a, t, reinterpret_cast<float*>(workspace),
+                                           (cudaStream_t)stream);
+  if (e != cudaSuccess) return fail_cuda(e, "attn_bwd_bf16 launch");
+  return ATTN_OK;
+}
+
 attn_status attn_selftest_wait_timeout(const void* q, const void* k, const void* v, void* o,
                                        attn_stream_t stream) {
   const int64_t st[3] = {128 * 128, 128, 128};   // [1, 128, 1, 128] contiguous
@@ -734,9 +847,13 @@ attn_status attn_selftest_wait_timeout(const void* q, const void* k, const void*
 attn_status attn_get_device_status(attn_stream_t stream) {
   cudaError_t e = cudaStreamSynchronize((cudaStream_t)stream);
   if (e != cudaSuccess) return fail_cuda(e, "cudaStreamSynchronize");
-  uint32_t w = 0;
+  // one word per translation unit with such kernels
+  uint32_t w = 0, lse = 0, bwd = 0;
   e = sa::read_and_clear_err_attn(&w);
+  if (e == cudaSuccess) e = sa::read_and_clear_err_lse(&lse);
+  if (e == cudaSuccess) e = sa::read_and_clear_err_bwd(&bwd);
   if (e != cudaSuccess) return fail_cuda(e, "reading the device error word");
+  w |= lse | bwd;
   if (w)
     return fail(ATTN_ERR_DEVICE_TIMEOUT,
                 "an attention kernel gave up on a bounded wait (bits 0x%x: 1 TMA load, 2 MMA commit, 4 hand-off; "

@@ -169,4 +169,56 @@ cudaError_t launch_sage_attn_pv16_qload(const CUtensorMap& tm_q_bf16, const CUte
                                         void* o, long long o_sb, long long o_ss, long long o_sh, int B, int S, int H,
                                         long long S_pad, cudaStream_t stream);
 
+// ------------------------------------------------------------------ training
+// What the forward with row statistics and the backward share (attn_lse.cu, attn_bwd.cu).
+struct TrainArgs {
+  int B, Sq, Sk, Hq, Hkv;
+  float scale;            // softmax_scale >= 0
+  float c_log2;           // softmax_scale * log2 e
+  int causal;             // query i sees the keys j <= i + Sk - Sq
+  const int* kv_len;      // device [B], or nullptr: Sk keys
+};
+// Q [B, Sq, Hq, 128], K and V [B, Sk, Hkv, 128] through BF16 tensor maps; lse [B, Hq, Sq].
+cudaError_t launch_attn_fwd_bf16_lse(const CUtensorMap& tm_q, const CUtensorMap& tm_k, const CUtensorMap& tm_v,
+                                     const TrainArgs& a, void* o, const long long o_str[3], float* lse,
+                                     cudaStream_t stream);
+cudaError_t read_and_clear_err_lse(uint32_t* out);
+
+struct BwdTensors {
+  const void *o, *dout;
+  const float* lse;
+  void *dq, *dk, *dv;
+  long long o_str[3], dout_str[3], dq_str[3], dk_str[3], dv_str[3];
+};
+// Query rows padded to whole tiles: the workspace is 2 * B * Hq * padded floats.
+long long attn_bwd_padded_rows(long long Sq);
+cudaError_t launch_attn_bwd_bf16(const CUtensorMap& tm_q, const CUtensorMap& tm_k, const CUtensorMap& tm_v,
+                                 const CUtensorMap& tm_d, const TrainArgs& a, const BwdTensors& t, float* workspace,
+                                 cudaStream_t stream);
+cudaError_t read_and_clear_err_bwd(uint32_t* out);
+
+// Heads along grid.y and, beyond 65535 of them, grid.z.
+inline dim3 heads_grid(long long tiles, int heads) {
+  const unsigned ny = (unsigned)(heads < 65535 ? heads : 65535);
+  return dim3((unsigned)tiles, ny, (heads + ny - 1) / ny);
+}
+
+// A launch as a programmatic dependent of the previous kernel in the stream: the kernel may set
+// up while that one finishes, and waits (griddep_wait) before it reads or writes what others do.
+template <class... P, class... A>
+cudaError_t launch_dependent(void (*kernel)(P...), dim3 grid, int threads, size_t smem, cudaStream_t stream,
+                             const A&... args) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3(threads, 1, 1);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kernel, args...);
+}
+
 }  // namespace sa
