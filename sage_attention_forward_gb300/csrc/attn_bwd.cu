@@ -37,9 +37,13 @@ namespace {
 
 using namespace tiles;
 
-constexpr int kThreads = 320;
-constexpr int kWarpLoad = 8;
-constexpr int kWarpMma = 9;
+// Four warpgroups share a tile's elementwise work, 32 of its 128 columns each: with two, of 64,
+// the tensor core waited on their latency (dK/dV 3408 cycles a tile pair against 2048 of products).
+constexpr int kGroups = 4;
+constexpr int kCols = kTile / kGroups;
+constexpr int kWarpLoad = 4 * kGroups;
+constexpr int kWarpMma = kWarpLoad + 1;
+constexpr int kThreads = 32 * (kWarpMma + 1);
 constexpr float kLog2e = 1.4426950408889634f;
 
 __device__ uint32_t g_err_bwd;
@@ -116,15 +120,40 @@ struct __align__(1024) SmemKV {
   uint8_t dout[2][kTileBytes];
   alignas(16) float neg_lse2[2][kTile];
   alignas(16) float neg_delta[2][kTile];
-  uint64_t kv_full;
+  WorkRing work;
+  uint64_t k_full, k_empty, v_full, v_empty;
   uint64_t q_full[2], q_empty[2];   // Q with the row statistics
   uint64_t d_full[2], d_empty[2];   // dO
   uint64_t s_full, dp_full;
-  uint64_t p_full[2], ds_full[2];   // queries [0, 64) and [64, 128) of P^T, dS^T stored in TMEM
-  uint64_t done;
+  uint64_t p_full[2], ds_full[2];   // queries [0, 64) and [64, 128) of P^T, dS^T stored in TMEM (two warpgroups each)
+  uint64_t acc_done;
+  uint64_t drain;
   uint32_t tmem_base;
   uint32_t abort_flag;
 };
+
+// One item: 128 keys of one key head, with the query tiles of the heads that share it.
+struct ItemKV {
+  int b, hk, key0, keys, first, n_q, n;   // n: products with a query tile, 0 when no query sees a key
+};
+__device__ __forceinline__ ItemKV item_kv(const BwdParams& p, const Work& w) {
+  ItemKV i;
+  const int bh = w.head;
+  i.b = bh / p.H;
+  i.hk = bh % p.H;
+  i.key0 = w.x * kTile;
+  i.n_q = (p.mask.Sq + kTile - 1) / kTile;
+  if (bh >= p.BH) {   // the last grid.z slice may run past B * H
+    i.keys = i.n = i.first = 0;
+    i.key0 = p.mask.Sk;
+    return i;
+  }
+  i.keys = key_count(p.mask, i.b);
+  // causal: query i sees key j when j <= i + Sk - Sq, so the tile's first key starts the queries
+  i.first = p.mask.causal ? max(i.key0 - (p.mask.Sk - p.mask.Sq), 0) / kTile : 0;
+  i.n = i.key0 < i.keys ? max(i.n_q - i.first, 0) * p.group : 0;
+  return i;
+}
 
 __global__ void __launch_bounds__(kThreads, 1)
     dkdv_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
@@ -132,27 +161,29 @@ __global__ void __launch_bounds__(kThreads, 1)
                 const BwdParams p) {
   extern __shared__ uint8_t smem_raw[];
   SmemKV& sm = *reinterpret_cast<SmemKV*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-  const int warp = threadIdx.x >> 5;
+  const int warp = __shfl_sync(0xffffffffu, (int)(threadIdx.x >> 5), 0);   // (known to be uniform)
   const int lane = threadIdx.x & 31;
-  const int bh = (int)(blockIdx.y + gridDim.y * blockIdx.z);
-  if (bh >= p.BH) return;   // the last grid.z slice may run past B * Hkv
-  const int key0 = blockIdx.x * kTile;
   volatile uint32_t* abort_flag = &sm.abort_flag;
   uint32_t* err = &g_err_bwd;
 
   if (threadIdx.x == 0) {
-    mbar_init(&sm.kv_full, 1);
+    work_init(sm.work, kWarpLoad + 1);
+    mbar_init(&sm.k_full, 1);
+    mbar_init(&sm.k_empty, 1);
+    mbar_init(&sm.v_full, 1);
+    mbar_init(&sm.v_empty, 1);
     for (int s = 0; s < 2; ++s) {
       mbar_init(&sm.q_full[s], 1);
       mbar_init(&sm.q_empty[s], 1);
       mbar_init(&sm.d_full[s], 1);
       mbar_init(&sm.d_empty[s], 1);
-      mbar_init(&sm.p_full[s], 4);
-      mbar_init(&sm.ds_full[s], 4);
+      mbar_init(&sm.p_full[s], 2 * kGroups);
+      mbar_init(&sm.ds_full[s], 2 * kGroups);
     }
     mbar_init(&sm.s_full, 1);
     mbar_init(&sm.dp_full, 1);
-    mbar_init(&sm.done, 1);
+    mbar_init(&sm.acc_done, 1);
+    mbar_init(&sm.drain, 1);
     sm.abort_flag = 0;
     fence_mbar_init();
   }
@@ -164,190 +195,278 @@ __global__ void __launch_bounds__(kThreads, 1)
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  const uint32_t tmem = sm.tmem_base;
-  const int b = bh / p.H, hk = bh % p.H;
-  const int keys = key_count(p.mask, b);
+  constexpr uint32_t tmem = 0;   // all 512 columns are this CTA's: they start at 0
   const int off = p.mask.Sk - p.mask.Sq;
-  const int n_q = (p.mask.Sq + kTile - 1) / kTile;
-  // causal: query i sees key j when j <= i + off, so the tile's first key starts the queries
-  const int first = p.mask.causal ? max(key0 - off, 0) / kTile : 0;
-  const int per_head = key0 < keys ? max(n_q - first, 0) : 0;
-  const int n = per_head * p.group;
 
   if (warp == kWarpLoad) {
-    if (lane == 0 && n > 0) {
+    if (lane == 0) {
       tma_prefetch_desc(&tm_q);
+      tma_prefetch_desc(&tm_k);
+      tma_prefetch_desc(&tm_v);
       tma_prefetch_desc(&tm_d);
-      mbar_arrive_expect_tx(&sm.kv_full, 2 * kTileBytes);
-      load_tile(sm.k, &tm_k, &sm.kv_full, key0, hk, b);
-      load_tile(sm.v, &tm_v, &sm.kv_full, key0, hk, b);
-      int q_issued = 0, d_issued = 0, t = first, h = hk * p.group;
-      for (int j = 0; j < n; ++j) {
-        const int slot = j & 1, use = j >> 1;
-        if (use > 0 && !mbar_wait<true>(&sm.q_empty[slot], (use - 1) & 1, abort_flag, err, kErrTimeoutSync)) break;
-        const long long at = ((long long)b * p.H * p.group + h) * p.Sq_pad + t * kTile;
-        mbar_arrive_expect_tx(&sm.q_full[slot], kTileBytes + 2 * kTile * 4);
-        load_tile(sm.q[slot], &tm_q, &sm.q_full[slot], t * kTile, h, b);
-        bulk_load(sm.neg_lse2[slot], p.neg_lse2 + at, kTile * 4, &sm.q_full[slot]);
-        bulk_load(sm.neg_delta[slot], p.neg_delta + at, kTile * 4, &sm.q_full[slot]);
-        q_issued = j + 1;
-        if (use > 0 && !mbar_wait<true>(&sm.d_empty[slot], (use - 1) & 1, abort_flag, err, kErrTimeoutSync)) break;
-        mbar_arrive_expect_tx(&sm.d_full[slot], kTileBytes);
-        load_tile(sm.dout[slot], &tm_d, &sm.d_full[slot], t * kTile, h, b);
-        d_issued = j + 1;
-        if (++t == n_q) {
-          t = first;
-          ++h;
+      int it = 0, items = 0, requests = 0, q_issued = 0, d_issued = 0, k_issued = 0, v_issued = 0;
+      auto load_item = [&](const ItemKV& i) -> bool {
+        if (items > 0 && !wait_one(&sm.k_empty, (items - 1) & 1, abort_flag, err, kErrTimeoutSync)) return false;
+        mbar_arrive_expect_tx(&sm.k_full, kTileBytes);
+        load_tile(sm.k, &tm_k, &sm.k_full, i.key0, i.hk, i.b);
+        ++k_issued;
+        int t = i.first, h = i.hk * p.group;
+        for (int j = 0; j < i.n; ++j, ++it) {
+          const int slot = it & 1, use = it >> 1;
+          if (use > 0 && !wait_one(&sm.q_empty[slot], (use - 1) & 1, abort_flag, err, kErrTimeoutSync)) return false;
+          const long long at = ((long long)i.b * p.H * p.group + h) * p.Sq_pad + t * kTile;
+          mbar_arrive_expect_tx(&sm.q_full[slot], kTileBytes + 2 * kTile * 4);
+          load_tile(sm.q[slot], &tm_q, &sm.q_full[slot], t * kTile, h, i.b);
+          bulk_load(sm.neg_lse2[slot], p.neg_lse2 + at, kTile * 4, &sm.q_full[slot]);
+          bulk_load(sm.neg_delta[slot], p.neg_delta + at, kTile * 4, &sm.q_full[slot]);
+          ++q_issued;
+          if (j == 0) {
+            if (items > 0 && !wait_one(&sm.v_empty, (items - 1) & 1, abort_flag, err, kErrTimeoutSync)) return false;
+            mbar_arrive_expect_tx(&sm.v_full, kTileBytes);
+            load_tile(sm.v, &tm_v, &sm.v_full, i.key0, i.hk, i.b);
+            ++v_issued;
+          }
+          if (use > 0 && !wait_one(&sm.d_empty[slot], (use - 1) & 1, abort_flag, err, kErrTimeoutSync)) return false;
+          mbar_arrive_expect_tx(&sm.d_full[slot], kTileBytes);
+          load_tile(sm.dout[slot], &tm_d, &sm.d_full[slot], t * kTile, h, i.b);
+          ++d_issued;
+          if (++t == i.n_q) {
+            t = i.first;
+            ++h;
+          }
         }
-      }
+        ++items;
+        return true;
+      };
+      Work w = first_work();
+      do {
+        if (!work_request(sm.work, w, abort_flag, err)) break;
+        ++requests;
+        const ItemKV i = item_kv(p, w);
+        if (i.n > 0 && !load_item(i)) break;
+      } while (work_next_load(sm.work, w, abort_flag, err));
       if (*abort_flag) {
-        mbar_wait_teardown(&sm.kv_full, 0);
-        for (int it = max(q_issued - 2, 0); it < q_issued; ++it) mbar_wait_teardown(&sm.q_full[it & 1], (it >> 1) & 1);
-        for (int it = max(d_issued - 2, 0); it < d_issued; ++it) mbar_wait_teardown(&sm.d_full[it & 1], (it >> 1) & 1);
+        // nothing may land in this CTA's shared memory after it has gone
+        work_teardown(sm.work, requests);
+        if (k_issued) mbar_wait_teardown(&sm.k_full, (k_issued - 1) & 1);
+        if (v_issued) mbar_wait_teardown(&sm.v_full, (v_issued - 1) & 1);
+        for (int i = max(q_issued - 2, 0); i < q_issued; ++i) mbar_wait_teardown(&sm.q_full[i & 1], (i >> 1) & 1);
+        for (int i = max(d_issued - 2, 0); i < d_issued; ++i) mbar_wait_teardown(&sm.d_full[i & 1], (i >> 1) & 1);
       }
     }
   } else if (warp == kWarpMma) {
-    if (n > 0) {
-      // the tensor core's order: dV(j) S(j+1) dK(j) dP(j+1).  S(j+1) overwrites P(j) and dP(j+1)
-      // dS(j) after the products that read them, and while the softmax warps work on one of
-      // the two chains S -> P -> dV and dP -> dS -> dK the tensor core works on the other.
-      const bool leader = elect_one();
-      const uint32_t tS = tmem, tDP = tmem + 128, tDV = tmem + 256, tDK = tmem + 384;
-      auto issue_s = [&](int j) -> bool {
-        if (!mbar_wait_warp<false>(&sm.q_full[j & 1], (j >> 1) & 1, abort_flag, err, kErrTimeoutTma)) return false;
-        tc_fence_after();
-        mma_tile_nt(tS, sm.k, sm.q[j & 1], leader);
-        if (leader) mma_commit(&sm.s_full);
-        return true;
-      };
-      auto issue_dp = [&](int j) -> bool {
-        if (!mbar_wait_warp<false>(&sm.d_full[j & 1], (j >> 1) & 1, abort_flag, err, kErrTimeoutTma)) return false;
-        tc_fence_after();
-        mma_tile_nt(tDP, sm.v, sm.dout[j & 1], leader);
-        if (leader) mma_commit(&sm.dp_full);
-        return true;
-      };
-      // acc += A B, A the two halves at columns a and a + 64, as their barriers complete
-      auto issue_acc = [&](uint32_t acc, uint32_t a, uint64_t* bars, const uint8_t* tile, int j) -> bool {
+    // The tensor core's order is dV(i) S(i+1) dK(i) dP(i+1), over the tile products i of all items:
+    // S(i+1) overwrites P(i) and dP(i+1) dS(i) after the products that read them, and while the
+    // softmax warps work on one of the two chains S -> P -> dV and dP -> dS -> dK the tensor core works
+    // on the other.  An item's first dV and dK overwrite the accumulators of the item before:
+    // the softmax warps published that P and dS after they had read them.
+    const bool leader = elect_one();
+    const uint32_t tS = tmem, tDP = tmem + 128, tDV = tmem + 256, tDK = tmem + 384;
+    auto make = [&](const Work& w) { return item_kv(p, w); };
+    Walk<ItemKV, decltype(make)> walk(make);
+    auto next_product = [&](bool wait) { return walk.next(wait, sm.work, lane, abort_flag, err); };
+    int k_items = 0, v_items = 0;
+    const uint32_t dk = desc_k(sm.k), dv = desc_k(sm.v), dq = desc_k(sm.q[0]), dd = desc_k(sm.dout[0]);
+    const uint32_t dq_mn = desc_mn(sm.q[0]), dd_mn = desc_mn(sm.dout[0]);
+    auto issue_s = [&](int i, int flags) -> bool {
+      if ((flags & kFirst) && !wait_warp(&sm.k_full, k_items++ & 1, abort_flag, err, kErrTimeoutTma)) return false;
+      if (!wait_warp(&sm.q_full[i & 1], (i >> 1) & 1, abort_flag, err, kErrTimeoutTma)) return false;
+      tc_fence_after();
+      mma_tile_nt(tS, dk, dq + kDescTile * (i & 1), leader);
+      if (leader) mma_commit(&sm.s_full);
+      if (leader && (flags & kLast)) mma_commit(&sm.k_empty);
+      return true;
+    };
+    auto issue_dp = [&](int i, int flags) -> bool {
+      if ((flags & kFirst) && !wait_warp(&sm.v_full, v_items++ & 1, abort_flag, err, kErrTimeoutTma)) return false;
+      if (!wait_warp(&sm.d_full[i & 1], (i >> 1) & 1, abort_flag, err, kErrTimeoutTma)) return false;
+      tc_fence_after();
+      mma_tile_nt(tDP, dv, dd + kDescTile * (i & 1), leader);
+      if (leader) mma_commit(&sm.dp_full);
+      if (leader && (flags & kLast)) mma_commit(&sm.v_empty);
+      return true;
+    };
+    // acc (+)= A B, A in kGroups pieces at columns a, a + kCols, ..., as the halves' barriers complete
+    auto issue_acc = [&](uint32_t acc, uint32_t a, uint64_t* bars, uint32_t tile_mn, int i, bool first) -> bool {
 #pragma unroll
-        for (int half = 0; half < 2; ++half) {
-          if (!mbar_wait_warp<false>(&bars[half], j & 1, abort_flag, err, kErrTimeoutSync)) return false;
-          tc_fence_after();
-          mma_tile_half_nn(acc, a + 64 * half, tile, half, j > 0 || half > 0, leader);
-        }
-        return true;
-      };
-      bool ok = mbar_wait_warp<false>(&sm.kv_full, 0, abort_flag, err, kErrTimeoutTma) && issue_s(0) && issue_dp(0);
-      for (int j = 0; j < n && ok; ++j) {
-        const int slot = j & 1;
-        ok = issue_acc(tDV, tS, sm.p_full, sm.dout[slot], j);
-        if (!ok) break;
-        if (leader) mma_commit(&sm.d_empty[slot]);   // (dP(j) was issued before)
-        if (j + 1 < n && !issue_s(j + 1)) break;
-        ok = issue_acc(tDK, tDP, sm.ds_full, sm.q[slot], j);
-        if (!ok) break;
-        if (leader) mma_commit(&sm.q_empty[slot]);
-        if (j + 1 < n && !issue_dp(j + 1)) break;
+      for (int half = 0; half < 2; ++half) {
+        if (!wait_warp(&bars[half], i & 1, abort_flag, err, kErrTimeoutSync)) return false;
+        tc_fence_after();
+#pragma unroll
+        for (int g = half * kGroups / 2; g < (half + 1) * kGroups / 2; ++g)
+          mma_tile_part_nn<kCols>(acc, a + kCols * g, tile_mn, g, !first || g > 0, leader);
       }
-      if (leader) mma_commit(&sm.done);
-      mbar_wait_teardown(&sm.done, 0);
+      return true;
+    };
+    int f0 = next_product(true);
+    bool ok = f0 == kEnd || (issue_s(0, f0) && issue_dp(0, f0));
+    for (int i = 0; ok && f0 != kEnd; ++i) {
+      const int slot = i & 1;
+      const bool last = f0 & kLast, first = f0 & kFirst;
+      int f1 = last ? kUnknown : next_product(true);
+      ok = issue_acc(tDV, tS, sm.p_full, dd_mn + kDescTile * slot, i, first);
+      if (!ok) break;
+      if (leader) mma_commit(&sm.d_empty[slot]);   // (dP(i) was issued before)
+      if (last) f1 = next_product(false);
+      ok = f1 <= kEnd || issue_s(i + 1, f1);
+      if (!ok) break;
+      ok = issue_acc(tDK, tDP, sm.ds_full, dq_mn + kDescTile * slot, i, first);
+      if (!ok) break;
+      if (leader) mma_commit(&sm.q_empty[slot]);
+      if (leader && last) mma_commit(&sm.acc_done);
+      if (f1 == kUnknown) {
+        f1 = next_product(true);
+        ok = f1 == kEnd || issue_s(i + 1, f1);
+        if (!ok) break;
+      }
+      ok = f1 == kEnd || issue_dp(i + 1, f1);
+      f0 = f1;
     }
+    if (leader) mma_commit(&sm.drain);
+    mbar_wait_teardown(&sm.drain, 0);
   } else {
-    // warpgroup `half` takes the queries [64 * half, 64 * half + 64) of each tile, a thread one key
-    const int half = warp >> 2, wq = warp & 3;
+    // Warpgroup g takes the queries [32 g, 32 g + 32) of each tile.  A thread has eight of these
+    // columns of four keys (rows lane / 4 + 8 r of its warp's 32), not 32 columns of one: the
+    // statistics, which belong to the columns, are then 8 values a thread and not 32 (the
+    // shared-memory reads of 32 took 420 cycles of the 1260 from a tile's S to its P).
+    const int g = warp >> 2, wq = warp & 3;
     const uint32_t lane_off = (uint32_t)(wq * 32) << 16;
-    const uint32_t tS = tmem + lane_off + 64 * half, tDP = tS + 128;
-    const int key = key0 + wq * 32 + lane;
+    const uint32_t tS = tmem + lane_off + kCols * g, tDP = tS + 128;
+    const int col = kCols * g + 2 * (lane & 3);   // the first of the thread's columns
+    constexpr uint32_t kLow = 16u << 16;          // the lower 16 of the warp's 32 TMEM lanes
     bool ok = true;
-    int t = first;
-    for (int j = 0; j < n; ++j) {
-      const int slot = j & 1;
-      // a tile on the diagonal: column c (query 128 t + 64 half + c) sees this key from c_min on.
-      // Key 0's first query sees key 0 alone; its ds is 0.
-      const int c_min = p.mask.causal ? key - off - (t * kTile + 64 * half) : 0;
-      const bool diag = p.mask.causal && key0 + kTile - 1 - off > t * kTile;   // uniform over the CTA
-      const int c_min_ds = key == 0 ? c_min + 1 : c_min;
-      float pr[64];
-      if (!mbar_wait_warp<false>(&sm.s_full, j & 1, abort_flag, err, kErrTimeoutMma)) { ok = false; break; }
-      tc_fence_after();
-      // (the MMA warp waited for this tile's Q and statistics, but their bytes are visible to a
-      // thread only through its own wait)
-      if (!mbar_wait_warp<false>(&sm.q_full[slot], (j >> 1) & 1, abort_flag, err, kErrTimeoutTma)) { ok = false; break; }
+    int it = 0, items = 0, turn = 0;
+    do {
       {
-        uint32_t a[2][32];
-        tmem_ld64(tS, a[0], a[1]);
-        uint32_t pk[32];
-        const float4* nl = reinterpret_cast<const float4*>(&sm.neg_lse2[slot][64 * half]);
+        const ItemKV item = item_kv(p, work_read(sm.work, turn));
+        const int key = item.key0 + wq * 32 + (lane >> 2);   // and the keys 8, 16, 24 after it
+        const int t_first = item.first, t_end = item.n_q;
+        int t = t_first;
+        for (int end = it + item.n; it != end; ++it) {
+          const int slot = it & 1;
+          // a tile on the diagonal: the thread's column 8 i + e sees its key r from
+          // 8 i + e >= 8 r + c_min on.  Key 0's first query sees key 0 alone; its ds is 0.
+          const int c_min = p.mask.causal ? key - off - t * kTile - col : -kTile;
+          const bool diag = __any_sync(0xffffffffu, c_min + 24 > 0);
+          float pr[2][16];
+          // (the MMA warp waited for this tile's Q and statistics, but their bytes are visible to a
+          // thread only through its own wait)
+          ok = mbar_wait_warp<false>(&sm.s_full, it & 1, abort_flag, err, kErrTimeoutMma) &&
+               mbar_wait_warp<false>(&sm.q_full[slot], (it >> 1) & 1, abort_flag, err, kErrTimeoutTma);
+          if (!ok) break;
+          tc_fence_after();
+          {
+            uint32_t a[2][16];
+            tmem_ld_16x32(tS, a[0]);
+            tmem_ld_16x32(tS + kLow, a[1]);
+            float2 m[4];
 #pragma unroll
-        for (int e = 0; e < 16; ++e) {
-          const float4 m = nl[e];
-          const uint32_t* s = &a[e >> 3][4 * (e & 7)];
-          float x0, x1, x2, x3;
-          ffma2(x0, x1, u2f(s[0]), u2f(s[1]), p.c_log2, p.c_log2, m.x, m.y);
-          ffma2(x2, x3, u2f(s[2]), u2f(s[3]), p.c_log2, p.c_log2, m.z, m.w);
-          pr[4 * e] = ex2_approx(x0);
-          pr[4 * e + 1] = ex2_approx(x1);
-          pr[4 * e + 2] = ex2_approx(x2);
-          pr[4 * e + 3] = ex2_approx(x3);
+            for (int i = 0; i < 4; ++i) m[i] = *reinterpret_cast<const float2*>(&sm.neg_lse2[slot][col + 8 * i]);
+            tmem_ld_wait();
+            tmem_reg_fence16(a[0]);
+            tmem_reg_fence16(a[1]);
+#pragma unroll
+            for (int r = 0; r < 4; ++r)
+#pragma unroll
+              for (int i = 0; i < 4; ++i) {
+                const int e = 4 * i + 2 * (r & 1);
+                float x0, x1;
+                ffma2(x0, x1, u2f(a[r >> 1][e]), u2f(a[r >> 1][e + 1]), p.c_log2, p.c_log2, m[i].x, m[i].y);
+                pr[r >> 1][e] = ex2_approx(x0);
+                pr[r >> 1][e + 1] = ex2_approx(x1);
+              }
+            if (diag) {
+#pragma unroll
+              for (int r = 0; r < 4; ++r)
+#pragma unroll
+                for (int c = 0; c < 8; ++c) {
+                  float& x = pr[r >> 1][4 * (c >> 1) + 2 * (r & 1) + (c & 1)];
+                  x = 8 * (c >> 1) + (c & 1) - 8 * r >= c_min ? x : 0.0f;
+                }
+            }
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+              uint32_t pk[8];
+#pragma unroll
+              for (int e = 0; e < 8; ++e) pk[e] = pack_bf16x2(pr[h][2 * e], pr[h][2 * e + 1]);
+              tmem_st_16x16(tS + h * kLow, pk);
+            }
+            tmem_st_wait();
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&sm.p_full[g >> 1]);
+          }
+          ok = mbar_wait_warp<false>(&sm.dp_full, it & 1, abort_flag, err, kErrTimeoutMma);
+          if (!ok) break;
+          tc_fence_after();
+          {
+            uint32_t a[2][16];
+            tmem_ld_16x32(tDP, a[0]);
+            tmem_ld_16x32(tDP + kLow, a[1]);
+            float2 d[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) d[i] = *reinterpret_cast<const float2*>(&sm.neg_delta[slot][col + 8 * i]);
+            tmem_ld_wait();
+            tmem_reg_fence16(a[0]);
+            tmem_reg_fence16(a[1]);
+#pragma unroll
+            for (int r = 0; r < 4; ++r)
+#pragma unroll
+              for (int i = 0; i < 4; ++i) {
+                const int e = 4 * i + 2 * (r & 1);
+                float x0, x1;
+                fadd2(x0, x1, u2f(a[r >> 1][e]), u2f(a[r >> 1][e + 1]), d[i].x, d[i].y);
+                fmul2(pr[r >> 1][e], pr[r >> 1][e + 1], pr[r >> 1][e], pr[r >> 1][e + 1], x0, x1);
+              }
+            if (diag) {
+              const int c_min_ds = key == 0 ? c_min + 1 : c_min;
+#pragma unroll
+              for (int r = 0; r < 4; ++r)
+#pragma unroll
+                for (int c = 0; c < 8; ++c) {
+                  float& x = pr[r >> 1][4 * (c >> 1) + 2 * (r & 1) + (c & 1)];
+                  x = 8 * (c >> 1) + (c & 1) - 8 * r >= (r == 0 ? c_min_ds : c_min) ? x : 0.0f;
+                }
+            }
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+              uint32_t pk[8];
+#pragma unroll
+              for (int e = 0; e < 8; ++e) pk[e] = pack_bf16x2(pr[h][2 * e], pr[h][2 * e + 1]);
+              tmem_st_16x16(tDP + h * kLow, pk);
+            }
+            tmem_st_wait();
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&sm.ds_full[g >> 1]);
+          }
+          if (++t == t_end) t = t_first;
         }
-        if (diag) {
-#pragma unroll
-          for (int c = 0; c < 64; ++c) pr[c] = c >= c_min ? pr[c] : 0.0f;
-        }
-#pragma unroll
-        for (int e = 0; e < 32; ++e) pk[e] = pack_bf16x2(pr[2 * e], pr[2 * e + 1]);
-        tmem_st32(tS, pk);
-        tmem_st_wait();
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&sm.p_full[half]);
       }
-      if (!mbar_wait_warp<false>(&sm.dp_full, j & 1, abort_flag, err, kErrTimeoutMma)) { ok = false; break; }
-      tc_fence_after();
-      {
-        uint32_t a[2][32];
-        tmem_ld64(tDP, a[0], a[1]);
-        uint32_t pk[32];
-        const float4* nd = reinterpret_cast<const float4*>(&sm.neg_delta[slot][64 * half]);
-        float ds[64];
-#pragma unroll
-        for (int e = 0; e < 16; ++e) {
-          const float4 d = nd[e];
-          const uint32_t* s = &a[e >> 3][4 * (e & 7)];
-          float x0, x1, x2, x3;
-          fadd2(x0, x1, u2f(s[0]), u2f(s[1]), d.x, d.y);
-          fadd2(x2, x3, u2f(s[2]), u2f(s[3]), d.z, d.w);
-          fmul2(ds[4 * e], ds[4 * e + 1], pr[4 * e], pr[4 * e + 1], x0, x1);
-          fmul2(ds[4 * e + 2], ds[4 * e + 3], pr[4 * e + 2], pr[4 * e + 3], x2, x3);
-        }
-        if (diag) {
-#pragma unroll
-          for (int c = 0; c < 64; ++c) ds[c] = c >= c_min_ds ? ds[c] : 0.0f;
-        }
-#pragma unroll
-        for (int e = 0; e < 32; ++e) pk[e] = pack_bf16x2(ds[2 * e], ds[2 * e + 1]);
-        tmem_st32(tDP, pk);
-        tmem_st_wait();
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&sm.ds_full[half]);
-      }
-      if (++t == n_q) t = first;
-    }
-    // warpgroup 0 stores dV, warpgroup 1 dK; keys that no query sees get zeros (their rows hold
-    // what the padding made of them), and a key alone in its batch entry has dK = 0
-    __nv_bfloat16* dst = half == 0 ? p.d1 + (long long)b * p.s1[0] + (long long)key * p.s1[1] + (long long)hk * p.s1[2]
-                                   : p.d0 + (long long)b * p.s0[0] + (long long)key * p.s0[1] + (long long)hk * p.s0[2];
-    const bool store = key < p.mask.Sk;
-    const bool zero = n == 0 || key >= keys || (half == 1 && keys == 1);
-    if (n > 0) {
-      ok = ok && mbar_wait_warp<true>(&sm.done, 0, abort_flag, err, kErrTimeoutMma);
-      if (ok) {
+      if (!ok) break;
+      // warpgroups 0 and 1 store dV's channels, 2 and 3 dK's; keys that no query sees get zeros (their
+      // rows hold what the padding made of them), and a key alone in its batch entry has dK = 0
+      const ItemKV done = item_kv(p, work_read(sm.work, turn));
+      const int which = g / (kGroups / 2), ch = (g % (kGroups / 2)) * 64;
+      const int row0 = done.key0 + wq * 32;
+      const long long* str = which == 0 ? p.s1 : p.s0;
+      uint32_t out[32] = {};
+      if (done.n > 0) {
+        ok = mbar_wait_warp<false>(&sm.acc_done, items++ & 1, abort_flag, err, kErrTimeoutMma);
+        if (!ok) break;
         tc_fence_after();
-        store_row_bf16(tmem + lane_off + 256 + 128 * half, dst, half == 0 ? 1.0f : p.scale, store && !zero);
+        load_row_bf16<64>(tmem + lane_off + 256 + 128 * which + ch, out, which == 0 ? 1.0f : p.scale);
+        tc_fence_before();
+        if (row0 + lane >= done.keys || (which == 1 && done.keys == 1)) {
+#pragma unroll
+          for (int e = 0; e < 32; ++e) out[e] = 0u;
+        }
       }
-    }
-    if (ok && store && zero) store_row_zero(dst);
+      store_rows<64>((which == 0 ? p.d1 : p.d0) + (long long)done.b * str[0] + (long long)row0 * str[1] +
+                         (long long)done.hk * str[2] + ch,
+                     str[1], out, p.mask.Sk - row0, lane);
+      work_release(sm.work, turn, lane);
+    } while (work_wait(sm.work, ++turn, abort_flag, err));
   }
 
   tc_fence_before();
@@ -355,7 +474,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   tc_fence_after();
   if (warp == kWarpMma) {
     __syncwarp();
-    tmem_dealloc(tmem, 512);
+    tmem_dealloc(sm.tmem_base, 512);
   }
 }
 
@@ -367,33 +486,58 @@ struct __align__(1024) SmemQ {
   uint8_t dout[kTileBytes];
   uint8_t k[kKRing][kTileBytes];
   uint8_t v[kVRing][kTileBytes];
-  uint64_t q_full, d_full;
+  WorkRing work;
+  uint64_t q_full, q_empty, d_full, d_empty;
+  uint64_t q_ready;      // Q in TMEM (every softmax warp's part)
   uint64_t k_full[kKRing], k_empty[kKRing];
   uint64_t v_full[kVRing], v_empty[kVRing];
-  uint64_t s_full[2], dp_full;
-  uint64_t ds_full[2];   // keys [0, 64) and [64, 128) of dS stored in TMEM
-  uint64_t done;
+  uint64_t s_full, s_free;     // S in TMEM; read by every softmax warp
+  uint64_t dp_full;
+  uint64_t ds_full, ds_free;   // dS stored in TMEM by every softmax warp; read by dQ's product
+  uint64_t acc_done;
+  uint64_t drain;
   uint32_t tmem_base;
   uint32_t abort_flag;
 };
+
+// One item: 128 queries of one query head, with the key tiles that they see.
+struct ItemQ {
+  int b, h, row0, keys, n;
+};
+__device__ __forceinline__ ItemQ item_q(const BwdParams& p, const Work& w) {
+  ItemQ i;
+  const int bh = w.head;
+  i.b = bh / p.H;
+  i.h = bh % p.H;
+  // the last queries have the most keys when the mask is causal: they start first
+  i.row0 = (p.mask.causal ? (int)(gridDim.x - 1 - w.x) : w.x) * kTile;
+  if (bh >= p.BH) {
+    i.keys = i.n = 0;
+    i.row0 = p.mask.Sq;
+    return i;
+  }
+  i.keys = key_count(p.mask, i.b);
+  i.n = (row_limit(p.mask, i.keys, min(i.row0 + kTile, p.mask.Sq) - 1) + kTile - 1) / kTile;
+  return i;
+}
 
 __global__ void __launch_bounds__(kThreads, 1)
     dq_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
               const __grid_constant__ CUtensorMap tm_v, const __grid_constant__ CUtensorMap tm_d, const BwdParams p) {
   extern __shared__ uint8_t smem_raw[];
   SmemQ& sm = *reinterpret_cast<SmemQ*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-  const int warp = threadIdx.x >> 5;
+  const int warp = __shfl_sync(0xffffffffu, (int)(threadIdx.x >> 5), 0);   // (known to be uniform)
   const int lane = threadIdx.x & 31;
-  const int bh = (int)(blockIdx.y + gridDim.y * blockIdx.z);
-  if (bh >= p.BH) return;   // the last grid.z slice may run past B * Hq
-  const int qb = p.mask.causal ? (int)(gridDim.x - 1 - blockIdx.x) : (int)blockIdx.x;
-  const int row0 = qb * kTile;
   volatile uint32_t* abort_flag = &sm.abort_flag;
   uint32_t* err = &g_err_bwd;
 
   if (threadIdx.x == 0) {
+    work_init(sm.work, kWarpLoad + 1);
     mbar_init(&sm.q_full, 1);
+    mbar_init(&sm.q_empty, kWarpLoad);
+    mbar_init(&sm.q_ready, kWarpLoad);
     mbar_init(&sm.d_full, 1);
+    mbar_init(&sm.d_empty, 1);
     for (int s = 0; s < kKRing; ++s) {
       mbar_init(&sm.k_full[s], 1);
       mbar_init(&sm.k_empty[s], 1);
@@ -402,12 +546,13 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_init(&sm.v_full[s], 1);
       mbar_init(&sm.v_empty[s], 1);
     }
-    for (int s = 0; s < 2; ++s) {
-      mbar_init(&sm.s_full[s], 1);
-      mbar_init(&sm.ds_full[s], 4);
-    }
+    mbar_init(&sm.s_full, 1);
+    mbar_init(&sm.s_free, kWarpLoad);
     mbar_init(&sm.dp_full, 1);
-    mbar_init(&sm.done, 1);
+    mbar_init(&sm.ds_full, kWarpLoad);
+    mbar_init(&sm.ds_free, 1);
+    mbar_init(&sm.acc_done, 1);
+    mbar_init(&sm.drain, 1);
     sm.abort_flag = 0;
     fence_mbar_init();
   }
@@ -419,158 +564,246 @@ __global__ void __launch_bounds__(kThreads, 1)
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  const uint32_t tmem = sm.tmem_base;
-  const int b = bh / p.H, h = bh % p.H, hk = h / p.group;
-  const int keys = key_count(p.mask, b);
-  const int last_row = min(row0 + kTile, p.mask.Sq) - 1;
-  const int n = (row_limit(p.mask, keys, last_row) + kTile - 1) / kTile;
+  // TMEM columns (all 512 are this CTA's: they start at 0); dS and Q take two values a column
+  constexpr uint32_t tS = 0, tDP = 128, tDS = 256, tQ = 320, tDQ = 384;
 
   if (warp == kWarpLoad) {
-    if (lane == 0 && n > 0) {
+    if (lane == 0) {
+      tma_prefetch_desc(&tm_q);
       tma_prefetch_desc(&tm_k);
       tma_prefetch_desc(&tm_v);
-      mbar_arrive_expect_tx(&sm.q_full, kTileBytes);
-      load_tile(sm.q, &tm_q, &sm.q_full, row0, h, b);
-      mbar_arrive_expect_tx(&sm.d_full, kTileBytes);
-      load_tile(sm.dout, &tm_d, &sm.d_full, row0, h, b);
-      int k_issued = 0, v_issued = 0;
-      for (int j = 0; j < n; ++j) {
-        {
-          const int slot = j % kKRing, use = j / kKRing;
-          if (use > 0 && !mbar_wait<true>(&sm.k_empty[slot], (use - 1) & 1, abort_flag, err, kErrTimeoutSync)) break;
-          mbar_arrive_expect_tx(&sm.k_full[slot], kTileBytes);
-          load_tile(sm.k[slot], &tm_k, &sm.k_full[slot], j * kTile, hk, b);
-          k_issued = j + 1;
+      tma_prefetch_desc(&tm_d);
+      int it = 0, items = 0, requests = 0, k_issued = 0, v_issued = 0, q_issued = 0, d_issued = 0;
+      auto load_item = [&](const ItemQ& i) -> bool {
+        const int hk = i.h / p.group;
+        for (int j = 0; j < i.n; ++j, ++it) {
+          if (j == 0) {
+            if (items > 0 && !wait_one(&sm.q_empty, (items - 1) & 1, abort_flag, err, kErrTimeoutSync)) return false;
+            mbar_arrive_expect_tx(&sm.q_full, kTileBytes);
+            load_tile(sm.q, &tm_q, &sm.q_full, i.row0, i.h, i.b);
+            ++q_issued;
+          }
+          {
+            const int slot = it % kKRing, use = it / kKRing;
+            if (use > 0 && !wait_one(&sm.k_empty[slot], (use - 1) & 1, abort_flag, err, kErrTimeoutSync)) return false;
+            mbar_arrive_expect_tx(&sm.k_full[slot], kTileBytes);
+            load_tile(sm.k[slot], &tm_k, &sm.k_full[slot], j * kTile, hk, i.b);
+            ++k_issued;
+          }
+          if (j == 0) {
+            if (items > 0 && !wait_one(&sm.d_empty, (items - 1) & 1, abort_flag, err, kErrTimeoutSync)) return false;
+            mbar_arrive_expect_tx(&sm.d_full, kTileBytes);
+            load_tile(sm.dout, &tm_d, &sm.d_full, i.row0, i.h, i.b);
+            ++d_issued;
+          }
+          {
+            const int slot = it % kVRing, use = it / kVRing;
+            if (use > 0 && !wait_one(&sm.v_empty[slot], (use - 1) & 1, abort_flag, err, kErrTimeoutSync)) return false;
+            mbar_arrive_expect_tx(&sm.v_full[slot], kTileBytes);
+            load_tile(sm.v[slot], &tm_v, &sm.v_full[slot], j * kTile, hk, i.b);
+            ++v_issued;
+          }
         }
-        {
-          const int slot = j % kVRing, use = j / kVRing;
-          if (use > 0 && !mbar_wait<true>(&sm.v_empty[slot], (use - 1) & 1, abort_flag, err, kErrTimeoutSync)) break;
-          mbar_arrive_expect_tx(&sm.v_full[slot], kTileBytes);
-          load_tile(sm.v[slot], &tm_v, &sm.v_full[slot], j * kTile, hk, b);
-          v_issued = j + 1;
-        }
-      }
+        ++items;
+        return true;
+      };
+      Work w = first_work();
+      do {
+        if (!work_request(sm.work, w, abort_flag, err)) break;
+        ++requests;
+        const ItemQ i = item_q(p, w);
+        if (i.n > 0 && !load_item(i)) break;
+      } while (work_next_load(sm.work, w, abort_flag, err));
       if (*abort_flag) {
-        mbar_wait_teardown(&sm.q_full, 0);
-        mbar_wait_teardown(&sm.d_full, 0);
-        for (int it = max(k_issued - kKRing, 0); it < k_issued; ++it)
-          mbar_wait_teardown(&sm.k_full[it % kKRing], (it / kKRing) & 1);
-        for (int it = max(v_issued - kVRing, 0); it < v_issued; ++it)
-          mbar_wait_teardown(&sm.v_full[it % kVRing], (it / kVRing) & 1);
+        work_teardown(sm.work, requests);
+        if (q_issued) mbar_wait_teardown(&sm.q_full, (q_issued - 1) & 1);
+        if (d_issued) mbar_wait_teardown(&sm.d_full, (d_issued - 1) & 1);
+        for (int i = max(k_issued - kKRing, 0); i < k_issued; ++i)
+          mbar_wait_teardown(&sm.k_full[i % kKRing], (i / kKRing) & 1);
+        for (int i = max(v_issued - kVRing, 0); i < v_issued; ++i)
+          mbar_wait_teardown(&sm.v_full[i % kVRing], (i / kVRing) & 1);
       }
     }
   } else if (warp == kWarpMma) {
-    if (n > 0) {
-      // S is formed two tiles ahead in two TMEM buffers; dS(j) takes S(j)'s place.  The tensor core's
-      // order is dP(j+1) dQ(j) S(j+2): the softmax warps have S(j+1) in hand meanwhile.
-      const bool leader = elect_one();
-      const uint32_t tDP = tmem + 256, tDQ = tmem + 384;
-      auto issue_s = [&](int j) -> bool {
-        const int slot = j % kKRing;
-        if (!mbar_wait_warp<false>(&sm.k_full[slot], (j / kKRing) & 1, abort_flag, err, kErrTimeoutTma)) return false;
-        if (keys < p.mask.Sk && (j + 1) * kTile > keys) clear_rows(sm.k[slot], keys - j * kTile, lane);
-        tc_fence_after();
-        mma_tile_nt(tmem + 128 * (j & 1), sm.q, sm.k[slot], leader);
-        if (leader) mma_commit(&sm.s_full[j & 1]);
-        return true;
-      };
-      auto issue_dp = [&](int j) -> bool {
-        const int slot = j % kVRing;
-        if (!mbar_wait_warp<false>(&sm.v_full[slot], (j / kVRing) & 1, abort_flag, err, kErrTimeoutTma)) return false;
-        tc_fence_after();
-        mma_tile_nt(tDP, sm.dout, sm.v[slot], leader);
-        if (leader) mma_commit(&sm.dp_full);
-        if (leader) mma_commit(&sm.v_empty[slot]);
-        return true;
-      };
-      bool ok = mbar_wait_warp<false>(&sm.q_full, 0, abort_flag, err, kErrTimeoutTma) && issue_s(0) &&
-                mbar_wait_warp<false>(&sm.d_full, 0, abort_flag, err, kErrTimeoutTma) && issue_dp(0) &&
-                (n < 2 || issue_s(1));
-      for (int j = 0; j < n && ok; ++j) {
-        ok = mbar_wait_warp<false>(&sm.ds_full[0], j & 1, abort_flag, err, kErrTimeoutSync) &&
-             mbar_wait_warp<false>(&sm.ds_full[1], j & 1, abort_flag, err, kErrTimeoutSync) &&
-             (j + 1 >= n || issue_dp(j + 1));
+    // The tensor core's order is S(i+1) dP(i+1) dQ(i), over the tile products i of all items.  S(i+1)
+    // starts when the softmax warps have S(i) in registers, dP(i+1) and dQ(i) when dS(i) is there, so
+    // that both chains run beside the elementwise work.  An item's first dQ overwrites the
+    // accumulator of the item before: the softmax warps published that dS after they had read it.
+    const bool leader = elect_one();
+    int q_items = 0, d_items = 0;
+    auto make = [&](const Work& w) { return item_q(p, w); };
+    Walk<ItemQ, decltype(make)> walk(make);
+    auto next_product = [&](bool wait) { return walk.next(wait, sm.work, lane, abort_flag, err); };
+    const uint32_t dd = desc_k(sm.dout), dk = desc_k(sm.k[0]), dv = desc_k(sm.v[0]), dk_mn = desc_mn(sm.k[0]);
+    auto issue_s = [&](int i, int flags) -> bool {
+      const int slot = i % kKRing;
+      const int keys = walk.item.keys;   // (S goes first over the items: the walk is at this product)
+      const int clear = keys < p.mask.Sk && walk.j * kTile > keys ? keys - (walk.j - 1) * kTile : kTile;
+      if ((flags & kFirst) && !wait_warp(&sm.q_ready, q_items++ & 1, abort_flag, err, kErrTimeoutSync)) return false;
+      if (!wait_warp(&sm.k_full[slot], (i / kKRing) & 1, abort_flag, err, kErrTimeoutTma)) return false;
+      if (clear < kTile) clear_rows(sm.k[slot], clear, lane);
+      if (i > 0 && !wait_warp(&sm.s_free, (i - 1) & 1, abort_flag, err, kErrTimeoutSync)) return false;
+      tc_fence_after();
+      mma_tile_nt_ts(tS, tQ, dk + kDescTile * slot, leader);
+      if (leader) mma_commit(&sm.s_full);
+      return true;
+    };
+    auto issue_dp = [&](int i, int flags) -> bool {
+      const int slot = i % kVRing;
+      if ((flags & kFirst) && !wait_warp(&sm.d_full, d_items++ & 1, abort_flag, err, kErrTimeoutTma)) return false;
+      if (!wait_warp(&sm.v_full[slot], (i / kVRing) & 1, abort_flag, err, kErrTimeoutTma)) return false;
+      tc_fence_after();
+      mma_tile_nt(tDP, dd, dv + kDescTile * slot, leader);
+      if (leader) mma_commit(&sm.dp_full);
+      if (leader) mma_commit(&sm.v_empty[slot]);
+      if (leader && (flags & kLast)) mma_commit(&sm.d_empty);
+      return true;
+    };
+    int f0 = next_product(true);
+    bool ok = f0 == kEnd || (issue_s(0, f0) && issue_dp(0, f0));
+    for (int i = 0; ok && f0 != kEnd; ++i) {
+      const int slot = i % kKRing;
+      const bool last = f0 & kLast, first = f0 & kFirst;
+      int f1 = kEnd;
+      if (!last) {
+        f1 = next_product(true);
+        ok = issue_s(i + 1, f1);
+        if (!ok) break;
+      }
+      ok = wait_warp(&sm.ds_full, i & 1, abort_flag, err, kErrTimeoutSync) && (last || issue_dp(i + 1, f1));
+      if (!ok) break;
+      tc_fence_after();
+      mma_tile_part_nn<kTile>(tDQ, tDS, dk_mn + kDescTile * slot, 0, !first, leader);
+      if (leader) mma_commit(&sm.k_empty[slot]);
+      if (leader) mma_commit(&sm.ds_free);
+      if (last) {
+        if (leader) mma_commit(&sm.acc_done);
+        f1 = next_product(true);
+        ok = f1 == kEnd || (issue_s(i + 1, f1) && issue_dp(i + 1, f1));
+      }
+      f0 = f1;
+    }
+    if (leader) mma_commit(&sm.drain);
+    mbar_wait_teardown(&sm.drain, 0);
+  } else {
+    // warpgroup g takes the keys [32 g, 32 g + 32) of each tile, a thread one query
+    const int g = warp >> 2, wq = warp & 3;
+    const uint32_t lane_off = (uint32_t)(wq * 32) << 16;
+    bool ok = true;
+    int it = 0, items = 0, turn = 0;
+    // Q from its tile in shared memory to TMEM, 32 channels of a row per thread: as the A operand
+    // from shared memory it would be read again for every key tile, at the full rate of shared
+    // memory while S runs.  (Row r's 16-byte piece c of a half is at c ^ (r & 7).)
+    auto copy_q = [&](int item) -> bool {
+      if (!mbar_wait_warp<false>(&sm.q_full, item & 1, abort_flag, err, kErrTimeoutTma)) return false;
+      const int r = wq * 32 + lane;
+      const uint8_t* src = sm.q + (g >> 1) * kHalfBytes + r * 128;
+      uint32_t x[16];
+#pragma unroll
+      for (int c = 0; c < 4; ++c) {
+        const uint4 v = *reinterpret_cast<const uint4*>(src + ((((g & 1) * 4 + c) ^ (r & 7)) << 4));
+        x[4 * c] = v.x;
+        x[4 * c + 1] = v.y;
+        x[4 * c + 2] = v.z;
+        x[4 * c + 3] = v.w;
+      }
+      tmem_st16(tQ + lane_off + 16 * g, x);
+      tmem_st_wait();
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) {
+        mbar_arrive(&sm.q_empty);
+        mbar_arrive(&sm.q_ready);
+      }
+      return true;
+    };
+    if (item_q(p, first_work()).n > 0) ok = copy_q(0);
+    bool more = ok;
+    while (more) {
+      const ItemQ item = item_q(p, work_read(sm.work, turn));
+      const int row = item.row0 + wq * 32 + lane;
+      // a row that sees one key has ds = 0: as a row that sees none
+      int limit = row_limit(p.mask, item.keys, row);
+      if (limit == 1) limit = 0;
+      int valid = limit - kCols * g;   // what is left of the keys that this row sees, from the group's first
+      float nl = 0.0f, nd = 0.0f;
+      if (item.n > 0) {   // (rows past Sq have their statistics in the padding)
+        const long long at = ((long long)item.b * p.H + item.h) * p.Sq_pad + row;
+        nl = __ldg(p.neg_lse2 + at);
+        nd = __ldg(p.neg_delta + at);
+      }
+      for (int end = it + item.n; it != end; ++it, valid -= kTile) {
+        const bool partial = __any_sync(0xffffffffu, valid < kCols);
+        float pr[kCols];
+        ok = mbar_wait_warp<false>(&sm.s_full, it & 1, abort_flag, err, kErrTimeoutMma);
         if (!ok) break;
         tc_fence_after();
-        const int slot = j % kKRing;
+        {
+          uint32_t a[kCols];
+          tmem_ld32(tS + lane_off + kCols * g, a);
+          tmem_ld_wait();
+          tmem_reg_fence(a);
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&sm.s_free);
 #pragma unroll
-        for (int half = 0; half < 2; ++half)
-          mma_tile_half_nn(tDQ, tmem + 128 * (j & 1) + 64 * half, sm.k[slot], half, j > 0 || half > 0, leader);
-        if (leader) mma_commit(&sm.k_empty[slot]);
-        ok = j + 2 >= n || issue_s(j + 2);
-      }
-      if (leader) mma_commit(&sm.done);
-      mbar_wait_teardown(&sm.done, 0);
-    }
-  } else {
-    // warpgroup `half` takes the keys [64 * half, 64 * half + 64) of each tile, a thread one query
-    const int half = warp >> 2, wq = warp & 3;
-    const uint32_t lane_off = (uint32_t)(wq * 32) << 16;
-    const uint32_t tS = tmem + lane_off + 64 * half, tDP = tS + 256;
-    const int row = row0 + wq * 32 + lane;
-    // a row that sees one key has ds = 0: as a row that sees none
-    int limit = row_limit(p.mask, keys, row);
-    if (limit == 1) limit = 0;
-    int whole = row_limit(p.mask, keys, row0 + wq * 32);
-    if (whole == 1) whole = 0;
-    // (rows past Sq have their statistics in the padding)
-    const float nl = __ldg(p.neg_lse2 + (long long)bh * p.Sq_pad + row);
-    const float nd = __ldg(p.neg_delta + (long long)bh * p.Sq_pad + row);
-    bool ok = true;
-    for (int j = 0; j < n; ++j) {
-      const bool partial = whole < (j + 1) * kTile;              // warp-uniform
-      const int valid = limit - j * kTile - 64 * half;           // this row sees the half's keys [0, valid)
-      const uint32_t tSj = tS + 128 * (j & 1);
-      float pr[64];
-      if (!mbar_wait_warp<false>(&sm.s_full[j & 1], (j >> 1) & 1, abort_flag, err, kErrTimeoutMma)) { ok = false; break; }
-      tc_fence_after();
-      {
-        uint32_t a[2][32];
-        tmem_ld64(tSj, a[0], a[1]);
+          for (int e = 0; e < kCols / 2; ++e) {
+            float x0, x1;
+            ffma2(x0, x1, u2f(a[2 * e]), u2f(a[2 * e + 1]), p.c_log2, p.c_log2, nl, nl);
+            pr[2 * e] = ex2_approx(x0);
+            pr[2 * e + 1] = ex2_approx(x1);
+          }
+        }
+        ok = mbar_wait_warp<false>(&sm.dp_full, it & 1, abort_flag, err, kErrTimeoutMma);
+        if (!ok) break;
+        tc_fence_after();
+        {
+          uint32_t a[kCols], pk[kCols / 2];
+          tmem_ld32(tDP + lane_off + kCols * g, a);
+          tmem_ld_wait();
+          tmem_reg_fence(a);
 #pragma unroll
-        for (int e = 0; e < 32; ++e) {
-          const uint32_t* s = &a[e >> 4][2 * (e & 15)];
-          float x0, x1;
-          ffma2(x0, x1, u2f(s[0]), u2f(s[1]), p.c_log2, p.c_log2, nl, nl);
-          pr[2 * e] = ex2_approx(x0);
-          pr[2 * e + 1] = ex2_approx(x1);
+          for (int e = 0; e < kCols / 2; ++e) {
+            float x0, x1;
+            fadd2(x0, x1, u2f(a[2 * e]), u2f(a[2 * e + 1]), nd, nd);
+            fmul2(pr[2 * e], pr[2 * e + 1], pr[2 * e], pr[2 * e + 1], x0, x1);
+          }
+          if (partial) {
+#pragma unroll
+            for (int c = 0; c < kCols; ++c) pr[c] = c < valid ? pr[c] : 0.0f;
+          }
+#pragma unroll
+          for (int e = 0; e < kCols / 2; ++e) pk[e] = pack_bf16x2(pr[2 * e], pr[2 * e + 1]);
+          ok = it == 0 || mbar_wait_warp<false>(&sm.ds_free, (it - 1) & 1, abort_flag, err, kErrTimeoutMma);
+          if (!ok) break;
+          tc_fence_after();
+          tmem_st16(tDS + lane_off + 16 * g, pk);
+          tmem_st_wait();
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&sm.ds_full);
         }
       }
-      if (!mbar_wait_warp<false>(&sm.dp_full, j & 1, abort_flag, err, kErrTimeoutMma)) { ok = false; break; }
-      tc_fence_after();
-      {
-        uint32_t a[2][32];
-        tmem_ld64(tDP, a[0], a[1]);
-        float ds[64];
-#pragma unroll
-        for (int e = 0; e < 32; ++e) {
-          const uint32_t* s = &a[e >> 4][2 * (e & 15)];
-          float x0, x1;
-          fadd2(x0, x1, u2f(s[0]), u2f(s[1]), nd, nd);
-          fmul2(ds[2 * e], ds[2 * e + 1], pr[2 * e], pr[2 * e + 1], x0, x1);
-        }
-        if (partial) {
-#pragma unroll
-          for (int c = 0; c < 64; ++c) ds[c] = c < valid ? ds[c] : 0.0f;
-        }
-        uint32_t pk[32];
-#pragma unroll
-        for (int e = 0; e < 32; ++e) pk[e] = pack_bf16x2(ds[2 * e], ds[2 * e + 1]);
-        tmem_st32(tSj, pk);
-        tmem_st_wait();
+      if (!ok) break;
+      // the next item's Q, so that its first S runs while this one's rows are stored
+      more = work_wait(sm.work, turn + 1, abort_flag, err);
+      if (more && item_q(p, work_read(sm.work, turn + 1)).n > 0) {
+        ok = copy_q(items + (item.n > 0 ? 1 : 0));
+        if (!ok) break;
+      }
+      // each warpgroup stores 32 of the rows' channels
+      uint32_t out[16] = {};
+      if (item.n > 0) {
+        ok = mbar_wait_warp<false>(&sm.acc_done, items++ & 1, abort_flag, err, kErrTimeoutMma);
+        if (!ok) break;
+        tc_fence_after();
+        load_row_bf16<32>(tDQ + lane_off + 32 * g, out, p.scale);
         tc_fence_before();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&sm.ds_full[half]);
       }
-    }
-    // each warpgroup stores 64 of the row's channels
-    __nv_bfloat16* dst = p.d0 + (long long)b * p.s0[0] + (long long)row * p.s0[1] + (long long)h * p.s0[2] + 64 * half;
-    const bool store = row < p.mask.Sq;
-    if (n == 0) {
-      if (store) store_row_zero<64>(dst);
-    } else if (ok && mbar_wait_warp<true>(&sm.done, 0, abort_flag, err, kErrTimeoutMma)) {
-      tc_fence_after();
-      store_row_bf16<64>(tmem + lane_off + 384 + 64 * half, dst, p.scale, store);
+      store_rows<32>(p.d0 + (long long)item.b * p.s0[0] + (long long)(row - lane) * p.s0[1] + (long long)item.h * p.s0[2] + 32 * g,
+                     p.s0[1], out, p.mask.Sq - (row - lane), lane);
+      work_release(sm.work, turn, lane);
+      ++turn;
     }
   }
 
@@ -579,7 +812,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   tc_fence_after();
   if (warp == kWarpMma) {
     __syncwarp();
-    tmem_dealloc(tmem, 512);
+    tmem_dealloc(sm.tmem_base, 512);
   }
 }
 

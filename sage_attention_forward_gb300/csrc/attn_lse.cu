@@ -37,13 +37,14 @@ struct __align__(1024) Smem {
   uint8_t q[kNQ][kTileBytes];
   uint8_t k[kStages][kTileBytes];
   uint8_t v[kStages][kTileBytes];
-  uint64_t q_full;
+  WorkRing work;
+  uint64_t q_full, q_empty;
   uint64_t k_full[kStages], k_empty[kStages];
   uint64_t v_full[kStages], v_empty[kStages];
   uint64_t s_full[kNQ];
   uint64_t p_full[kNQ][2];   // P_i keys [0, 64) and [64, 128) stored in TMEM
   uint64_t o_done[kNQ];
-  uint64_t mma_drain;
+  uint64_t drain;
   uint32_t tmem_base;
   uint32_t abort_flag;
 };
@@ -62,23 +63,41 @@ struct Params {
 __device__ __forceinline__ float u2f(uint32_t u) { return __uint_as_float(u); }
 __device__ __forceinline__ uint32_t f2u(float f) { return __float_as_uint(f); }
 
+// One item: two 128-row query tiles of one head, with the key tiles that they see.
+struct Item {
+  int b, h, row0, keys, n;   // n: key tiles; 0 when no row sees a key
+};
+__device__ __forceinline__ Item item_of(const Params& p, const Work& w) {
+  Item i;
+  const int bh = w.head;
+  i.b = bh / p.Hq;
+  i.h = bh % p.Hq;
+  // the last queries have the most keys when the mask is causal: they start first
+  i.row0 = (p.mask.causal ? (int)(gridDim.x - 1 - w.x) : w.x) * (kNQ * kTile);
+  if (bh >= p.BH) {   // the last grid.z slice may run past B * Hq
+    i.keys = i.n = 0;
+    i.row0 = p.mask.Sq;
+    return i;
+  }
+  i.keys = key_count(p.mask, i.b);
+  i.n = (row_limit(p.mask, i.keys, min(i.row0 + kNQ * kTile, p.mask.Sq) - 1) + kTile - 1) / kTile;
+  return i;
+}
+
 __global__ void __launch_bounds__(kThreads, 1)
     lse_fwd_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
                    const __grid_constant__ CUtensorMap tm_v, const Params p) {
   extern __shared__ uint8_t smem_raw[];
   Smem& sm = *reinterpret_cast<Smem*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-  const int warp = threadIdx.x >> 5;
+  const int warp = __shfl_sync(0xffffffffu, (int)(threadIdx.x >> 5), 0);   // (known to be uniform)
   const int lane = threadIdx.x & 31;
-  const int bh = (int)(blockIdx.y + gridDim.y * blockIdx.z);
-  if (bh >= p.BH) return;   // the last grid.z slice may run past B * Hq
-  // the last query block has the most keys when the mask is causal: it starts first
-  const int qb = p.mask.causal ? (int)(gridDim.x - 1 - blockIdx.x) : (int)blockIdx.x;
-  const int q_row0 = qb * (kNQ * kTile);
   volatile uint32_t* abort_flag = &sm.abort_flag;
   uint32_t* err = &g_err_lse;
 
   if (threadIdx.x == 0) {
+    work_init(sm.work, kWarpLoad + 1);
     mbar_init(&sm.q_full, 1);
+    mbar_init(&sm.q_empty, 1);
     for (int s = 0; s < kStages; ++s) {
       mbar_init(&sm.k_full[s], 1);
       mbar_init(&sm.k_empty[s], 1);
@@ -91,7 +110,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_init(&sm.p_full[i][1], 4);
       mbar_init(&sm.o_done[i], 1);
     }
-    mbar_init(&sm.mma_drain, 1);
+    mbar_init(&sm.drain, 1);
     sm.abort_flag = 0;
     fence_mbar_init();
   }
@@ -103,224 +122,268 @@ __global__ void __launch_bounds__(kThreads, 1)
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  const uint32_t tmem = sm.tmem_base;
-  const int b = bh / p.Hq, h = bh % p.Hq, hk = h / p.group;
-  const int keys = key_count(p.mask, b);
-  const int last_row = min(q_row0 + kNQ * kTile, p.mask.Sq) - 1;
-  const int n = (row_limit(p.mask, keys, last_row) + kTile - 1) / kTile;   // key tiles; 0: no row sees a key
+  constexpr uint32_t tmem = 0;   // all 512 columns are this CTA's: they start at 0
 
   if (warp == kWarpLoad) {
-    if (lane == 0 && n > 0) {
+    if (lane == 0) {
       tma_prefetch_desc(&tm_q);
       tma_prefetch_desc(&tm_k);
       tma_prefetch_desc(&tm_v);
-      mbar_arrive_expect_tx(&sm.q_full, kNQ * kTileBytes);
-      for (int i = 0; i < kNQ; ++i) load_tile(sm.q[i], &tm_q, &sm.q_full, q_row0 + i * kTile, h, b);
-      int k_issued = 0, v_issued = 0;
-      for (int j = 0; j < n; ++j) {
-        const int slot = j % kStages, use = j / kStages;
-        if (use > 0 && !mbar_wait<true>(&sm.k_empty[slot], (use - 1) & 1, abort_flag, err, kErrTimeoutSync)) break;
-        mbar_arrive_expect_tx(&sm.k_full[slot], kTileBytes);
-        load_tile(sm.k[slot], &tm_k, &sm.k_full[slot], j * kTile, hk, b);
-        k_issued = j + 1;
-        if (use > 0 && !mbar_wait<true>(&sm.v_empty[slot], (use - 1) & 1, abort_flag, err, kErrTimeoutSync)) break;
-        mbar_arrive_expect_tx(&sm.v_full[slot], kTileBytes);
-        load_tile(sm.v[slot], &tm_v, &sm.v_full[slot], j * kTile, hk, b);
-        v_issued = j + 1;
-      }
+      int it = 0, items = 0, requests = 0, q_issued = 0, k_issued = 0, v_issued = 0;
+      auto load_item = [&](const Item& i) -> bool {
+        const int hk = i.h / p.group;
+        if (items > 0 && !wait_one(&sm.q_empty, (items - 1) & 1, abort_flag, err, kErrTimeoutSync)) return false;
+        mbar_arrive_expect_tx(&sm.q_full, kNQ * kTileBytes);
+        for (int q = 0; q < kNQ; ++q) load_tile(sm.q[q], &tm_q, &sm.q_full, i.row0 + q * kTile, i.h, i.b);
+        ++q_issued;
+        for (int j = 0; j < i.n; ++j, ++it) {
+          const int slot = it % kStages, use = it / kStages;
+          if (use > 0 && !wait_one(&sm.k_empty[slot], (use - 1) & 1, abort_flag, err, kErrTimeoutSync)) return false;
+          mbar_arrive_expect_tx(&sm.k_full[slot], kTileBytes);
+          load_tile(sm.k[slot], &tm_k, &sm.k_full[slot], j * kTile, hk, i.b);
+          ++k_issued;
+          if (use > 0 && !wait_one(&sm.v_empty[slot], (use - 1) & 1, abort_flag, err, kErrTimeoutSync)) return false;
+          mbar_arrive_expect_tx(&sm.v_full[slot], kTileBytes);
+          load_tile(sm.v[slot], &tm_v, &sm.v_full[slot], j * kTile, hk, i.b);
+          ++v_issued;
+        }
+        ++items;
+        return true;
+      };
+      Work w = first_work();
+      do {
+        if (!work_request(sm.work, w, abort_flag, err)) break;
+        ++requests;
+        const Item i = item_of(p, w);
+        if (i.n > 0 && !load_item(i)) break;
+      } while (work_next_load(sm.work, w, abort_flag, err));
       if (*abort_flag) {
-        mbar_wait_teardown(&sm.q_full, 0);
-        for (int it = max(k_issued - kStages, 0); it < k_issued; ++it)
-          mbar_wait_teardown(&sm.k_full[it % kStages], (it / kStages) & 1);
-        for (int it = max(v_issued - kStages, 0); it < v_issued; ++it)
-          mbar_wait_teardown(&sm.v_full[it % kStages], (it / kStages) & 1);
+        // nothing may land in this CTA's shared memory after it has gone
+        work_teardown(sm.work, requests);
+        if (q_issued) mbar_wait_teardown(&sm.q_full, (q_issued - 1) & 1);
+        for (int i = max(k_issued - kStages, 0); i < k_issued; ++i)
+          mbar_wait_teardown(&sm.k_full[i % kStages], (i / kStages) & 1);
+        for (int i = max(v_issued - kStages, 0); i < v_issued; ++i)
+          mbar_wait_teardown(&sm.v_full[i % kStages], (i / kStages) & 1);
       }
     }
   } else if (warp == kWarpMma) {
-    if (n > 0) {
-      const bool leader = elect_one();
-      auto tS = [&](int i) { return tmem + 128u * (uint32_t)i; };
-      auto tO = [&](int i) { return tmem + 256u + 128u * (uint32_t)i; };
-      auto issue_pv = [&](int i, int slot, int j) -> bool {
+    // Over the key tiles i of all items: P_0 V(i), S_0(i+1), P_1 V(i), S_1(i+1).  An item's first
+    // P V overwrites the O of the item before: the softmax warps published that P after they had
+    // read it.
+    const bool leader = elect_one();
+    auto tS = [&](int q) { return tmem + 128u * (uint32_t)q; };
+    auto tO = [&](int q) { return tmem + 256u + 128u * (uint32_t)q; };
+    int q_items = 0;
+    auto make = [&](const Work& w) { return item_of(p, w); };
+    Walk<Item, decltype(make)> walk(make);
+    auto next_product = [&](bool wait) { return walk.next(wait, sm.work, lane, abort_flag, err); };
+    const uint32_t dq = desc_k(sm.q[0]), dk = desc_k(sm.k[0]), dv = desc_mn(sm.v[0]);
+    auto wait_qk = [&](int i, int flags) -> bool {
+      if ((flags & kFirst) && !wait_warp(&sm.q_full, q_items++ & 1, abort_flag, err, kErrTimeoutTma)) return false;
+      return wait_warp(&sm.k_full[i % kStages], (i / kStages) & 1, abort_flag, err, kErrTimeoutTma);
+    };
+    auto issue_s = [&](int q, int i, int flags) {
+      tc_fence_after();
+      mma_tile_nt(tS(q), dq + kDescTile * q, dk + kDescTile * (i % kStages), leader);
+      if (leader) mma_commit(&sm.s_full[q]);
+      if (leader && q == kNQ - 1) mma_commit(&sm.k_empty[i % kStages]);
+      if (leader && q == kNQ - 1 && (flags & kLast)) mma_commit(&sm.q_empty);
+    };
+    auto issue_pv = [&](int q, int i, bool first) -> bool {
+      const uint32_t v = dv + kDescTile * (i % kStages);
 #pragma unroll
-        for (int half = 0; half < 2; ++half) {
-          if (!mbar_wait_warp<false>(&sm.p_full[i][half], j & 1, abort_flag, err, kErrTimeoutSync)) return false;
-          tc_fence_after();
-          mma_tile_half_nn(tO(i), tS(i) + 32 * half, sm.v[slot], half, j > 0 || half > 0, leader);
-        }
-        if (leader) mma_commit(&sm.o_done[i]);
-        return true;
-      };
-      auto wait_k = [&](int t, int slot) -> bool {
-        return mbar_wait_warp<false>(&sm.k_full[slot], (t / kStages) & 1, abort_flag, err, kErrTimeoutTma);
-      };
-      bool ok = mbar_wait_warp<false>(&sm.q_full, 0, abort_flag, err, kErrTimeoutTma) && wait_k(0, 0);
-      if (ok) {
+      for (int half = 0; half < 2; ++half) {
+        if (!wait_warp(&sm.p_full[q][half], i & 1, abort_flag, err, kErrTimeoutSync)) return false;
         tc_fence_after();
-#pragma unroll
-        for (int i = 0; i < kNQ; ++i) {
-          mma_tile_nt(tS(i), sm.q[i], sm.k[0], leader);
-          if (leader) mma_commit(&sm.s_full[i]);
-        }
-        if (leader) mma_commit(&sm.k_empty[0]);
+        mma_tile_part_nn<64>(tO(q), tS(q) + 32 * half, v, half, !first || half > 0, leader);
       }
-      for (int j0 = 0; j0 < n && ok; j0 += kStages) {
-#pragma unroll
-        for (int u = 0; u < kStages; ++u) {
-          const int j = j0 + u;
-          if (j >= n || !ok) break;
-          const int slotV = u, slotK = (u + 1) % kStages;
-          const bool more = (j + 1 < n);
-          ok = mbar_wait_warp<false>(&sm.v_full[slotV], (j / kStages) & 1, abort_flag, err, kErrTimeoutTma);
-          if (!ok) break;
-          if (keys < p.mask.Sk && (j + 1) * kTile > keys) clear_rows(sm.v[slotV], keys - j * kTile, lane);
-#pragma unroll
-          for (int i = 0; i < kNQ; ++i) {
-            ok = issue_pv(i, slotV, j) && (!more || i > 0 || wait_k(j + 1, slotK));
-            if (!ok) break;
-            if (leader && i == kNQ - 1) mma_commit(&sm.v_empty[slotV]);
-            if (more) {
-              tc_fence_after();
-              mma_tile_nt(tS(i), sm.q[i], sm.k[slotK], leader);
-              if (leader) mma_commit(&sm.s_full[i]);
-              if (leader && i == kNQ - 1) mma_commit(&sm.k_empty[slotK]);
-            }
-          }
-        }
-      }
-      if (leader) mma_commit(&sm.mma_drain);
-      mbar_wait_teardown(&sm.mma_drain, 0);
+      if (leader) mma_commit(&sm.o_done[q]);
+      return true;
+    };
+    int f0 = next_product(true);
+    bool ok = f0 == kEnd || wait_qk(0, f0);
+    if (ok && f0 != kEnd) {
+      issue_s(0, 0, f0);
+      issue_s(1, 0, f0);
     }
+    for (int i = 0; ok && f0 != kEnd; ++i) {
+      const int keys = walk.item.keys;   // (the walk is at product i here)
+      const int clear = keys < p.mask.Sk && walk.j * kTile > keys ? keys - (walk.j - 1) * kTile : kTile;
+      const bool last = f0 & kLast, first = f0 & kFirst;
+      int f1 = last ? kUnknown : next_product(true);
+      ok = wait_warp(&sm.v_full[i % kStages], (i / kStages) & 1, abort_flag, err, kErrTimeoutTma);
+      if (!ok) break;
+      if (clear < kTile) clear_rows(sm.v[i % kStages], clear, lane);
+      ok = issue_pv(0, i, first);
+      if (!ok) break;
+      if (last) f1 = next_product(false);
+      if (f1 > kEnd) {
+        ok = wait_qk(i + 1, f1);
+        if (!ok) break;
+        issue_s(0, i + 1, f1);
+      }
+      ok = issue_pv(1, i, first);
+      if (!ok) break;
+      if (leader) mma_commit(&sm.v_empty[i % kStages]);
+      if (f1 == kUnknown) {
+        f1 = next_product(true);
+        if (f1 != kEnd) {
+          ok = wait_qk(i + 1, f1);
+          if (!ok) break;
+          issue_s(0, i + 1, f1);
+        }
+      }
+      if (f1 != kEnd) issue_s(1, i + 1, f1);
+      f0 = f1;
+    }
+    if (leader) mma_commit(&sm.drain);
+    mbar_wait_teardown(&sm.drain, 0);
   } else {
     const int i = warp >> 2, wq = warp & 3;
     const uint32_t lane_off = (uint32_t)(wq * 32) << 16;
     const uint32_t tS = tmem + lane_off + 128u * i;
     const uint32_t tO = tmem + lane_off + 256u + 128u * i;
-    const int grow = q_row0 + i * kTile + wq * 32 + lane;
-    const int limit = row_limit(p.mask, keys, grow);
-    // keys below this are seen by every row of the warp (limits grow with the row)
-    const int whole = row_limit(p.mask, keys, q_row0 + i * kTile + wq * 32);
     const float f = p.c_log2;
-    float m_used = -INFINITY, l = 0.0f;
     bool ok = true;
+    int it = 0, turn = 0;
+    do {
+      int n;
+      int valid;   // what is left of the keys that this row sees
+      {
+        const Item item = item_of(p, work_read(sm.work, turn));
+        n = item.n;
+        valid = row_limit(p.mask, item.keys, item.row0 + i * kTile + wq * 32 + lane);
+      }
+      float m_used = -INFINITY, l = 0.0f;
 
-    for (int j = 0; j < n; ++j) {
-      if (!mbar_wait_warp<false>(&sm.s_full[i], j & 1, abort_flag, err, kErrTimeoutMma)) { ok = false; break; }
-      tc_fence_after();
-      uint32_t s[128];
-      uint32_t(&s0)[32] = *reinterpret_cast<uint32_t(*)[32]>(&s[0]);
-      uint32_t(&s1)[32] = *reinterpret_cast<uint32_t(*)[32]>(&s[32]);
-      uint32_t(&s2)[32] = *reinterpret_cast<uint32_t(*)[32]>(&s[64]);
-      uint32_t(&s3)[32] = *reinterpret_cast<uint32_t(*)[32]>(&s[96]);
-      const bool partial = whole < (j + 1) * kTile;   // warp-uniform
-      const int valid = limit - j * kTile;            // this row sees the tile's keys [0, valid)
-      float r0, r1, r2, r3;
-      tmem_ld32_max(tS + 0, s0, r0);
-      tmem_ld32_max(tS + 32, s1, r1);
-      tmem_ld_wait();
-      tmem_reg_fence(s0);
-      tmem_reg_fence(s1);
-      tmem_reg_fence2f(r0, r1);
-      tmem_ld32_max(tS + 64, s2, r2);
-      tmem_ld32_max(tS + 96, s3, r3);
-      tmem_ld_wait();
-      tmem_reg_fence(s2);
-      tmem_reg_fence(s3);
-      tmem_reg_fence2f(r2, r3);
-      float m_cand;
-      if (!partial) {
-        m_cand = fmaxf(fmaxf(r0, r1), fmaxf(r2, r3)) * f;   // f >= 0
-      } else {
-#pragma unroll
-        for (int e = 0; e < 128; ++e)
-          if (e >= valid) s[e] = f2u(-INFINITY);
-        m_cand = fmaxf(fmaxf(max32(&s[0]), max32(&s[32])), fmaxf(max32(&s[64]), max32(&s[96])));
-        m_cand = m_cand == -INFINITY ? -INFINITY : m_cand * f;   // (0 * -inf is NaN)
-      }
-      const bool need = m_cand > m_used + kTau;
-      const float sc = need ? ex2_approx(m_used - m_cand) : 1.0f;
-      if (need) {
-        l *= sc;
-        m_used = m_cand;
-      }
-      float rs0 = 0.0f, rs1 = 0.0f;
-      auto p_section = [&](auto masked) {
-        constexpr bool kMasked = decltype(masked)::value;
-#pragma unroll
-        for (int blk = 0; blk < 4; ++blk) {
-          uint32_t pk[16];
-#pragma unroll
-          for (int e = 0; e < 16; ++e) {
-            const int c0 = 32 * blk + 2 * e;
-            float x0, x1;
-            ffma2(x0, x1, u2f(s[c0]), u2f(s[c0 + 1]), f, f, -m_used, -m_used);
-            float p0 = ex2_approx(x0), p1 = ex2_approx(x1);
-            if (kMasked) {
-              p0 = c0 < valid ? p0 : 0.0f;
-              p1 = c0 + 1 < valid ? p1 : 0.0f;
-            }
-            fadd2(rs0, rs1, rs0, rs1, p0, p1);
-            pk[e] = pack_bf16x2(p0, p1);
-          }
-          tmem_st16(tS + 16 * blk, pk);
-          if (blk & 1) {
-            if (blk == 1 && j > 0 && __any_sync(0xffffffffu, need)) {
-              // O_i must hold P_{j-1} V_{j-1} before it is rescaled, and be rescaled before
-              // the first half of P_j V_j accumulates into it
-              if (mbar_wait_warp<true>(&sm.o_done[i], (j - 1) & 1, abort_flag, err, kErrTimeoutMma)) {
-                tc_fence_after();
-                uint32_t oa[16], ob[16];
-                tmem_ld16(tO, oa);
-                tmem_ld_wait();
-                tmem_reg_fence16(oa);
-#pragma unroll
-                for (int c2 = 0; c2 < 8; c2 += 2) {
-                  tmem_ld16(tO + 16 * (c2 + 1), ob);
-#pragma unroll
-                  for (int e = 0; e < 16; ++e) oa[e] = f2u(u2f(oa[e]) * sc);
-                  tmem_st16(tO + 16 * c2, oa);
-                  tmem_ld_wait();
-                  tmem_reg_fence16(ob);
-                  if (c2 + 2 < 8) tmem_ld16(tO + 16 * (c2 + 2), oa);
-#pragma unroll
-                  for (int e = 0; e < 16; ++e) ob[e] = f2u(u2f(ob[e]) * sc);
-                  tmem_st16(tO + 16 * (c2 + 1), ob);
-                  if (c2 + 2 < 8) {
-                    tmem_ld_wait();
-                    tmem_reg_fence16(oa);
-                  }
-                }
-              } else {
-                ok = false;
-              }
-            }
-            tmem_st_wait();
-            tc_fence_before();
-            __syncwarp();
-            if (ok && lane == 0) mbar_arrive(&sm.p_full[i][blk >> 1]);
-          }
+      for (; n > 0; --n, ++it, valid -= kTile) {
+        if (!mbar_wait_warp<false>(&sm.s_full[i], it & 1, abort_flag, err, kErrTimeoutMma)) { ok = false; break; }
+        tc_fence_after();
+        uint32_t s[128];
+        uint32_t(&s0)[32] = *reinterpret_cast<uint32_t(*)[32]>(&s[0]);
+        uint32_t(&s1)[32] = *reinterpret_cast<uint32_t(*)[32]>(&s[32]);
+        uint32_t(&s2)[32] = *reinterpret_cast<uint32_t(*)[32]>(&s[64]);
+        uint32_t(&s3)[32] = *reinterpret_cast<uint32_t(*)[32]>(&s[96]);
+        const bool partial = __any_sync(0xffffffffu, valid < kTile);
+        float r0, r1, r2, r3;
+        tmem_ld32_max(tS + 0, s0, r0);
+        tmem_ld32_max(tS + 32, s1, r1);
+        tmem_ld_wait();
+        tmem_reg_fence(s0);
+        tmem_reg_fence(s1);
+        tmem_reg_fence2f(r0, r1);
+        tmem_ld32_max(tS + 64, s2, r2);
+        tmem_ld32_max(tS + 96, s3, r3);
+        tmem_ld_wait();
+        tmem_reg_fence(s2);
+        tmem_reg_fence(s3);
+        tmem_reg_fence2f(r2, r3);
+        float m_cand;
+        if (!partial) {
+          m_cand = fmaxf(fmaxf(r0, r1), fmaxf(r2, r3)) * f;   // f >= 0
+        } else {
+  #pragma unroll
+          for (int e = 0; e < 128; ++e)
+            if (e >= valid) s[e] = f2u(-INFINITY);
+          m_cand = fmaxf(fmaxf(max32(&s[0]), max32(&s[32])), fmaxf(max32(&s[64]), max32(&s[96])));
+          m_cand = m_cand == -INFINITY ? -INFINITY : m_cand * f;   // (0 * -inf is NaN)
         }
-      };
-      if (partial) p_section(std::true_type{});
-      else p_section(std::false_type{});
-      if (!ok) break;
-      l += rs0 + rs1;
-    }
-
-    const bool store = grow < p.mask.Sq;
-    __nv_bfloat16* dst = p.o + (long long)b * p.o_sb + (long long)grow * p.o_ss + (long long)h * p.o_sh;
-    float* lse = p.lse + (long long)bh * p.mask.Sq + grow;
-    if (n == 0) {
-      if (store) {
-        store_row_zero(dst);
-        *lse = -INFINITY;
+        const bool need = m_cand > m_used + kTau;
+        const float sc = need ? ex2_approx(m_used - m_cand) : 1.0f;
+        // (until a row's first key its O is zeros, or the item before's)
+        const bool scale = need && m_used > -INFINITY;
+        if (need) {
+          l *= sc;
+          m_used = m_cand;
+        }
+        float rs0 = 0.0f, rs1 = 0.0f;
+        auto p_section = [&](auto masked) {
+          constexpr bool kMasked = decltype(masked)::value;
+  #pragma unroll
+          for (int blk = 0; blk < 4; ++blk) {
+            uint32_t pk[16];
+  #pragma unroll
+            for (int e = 0; e < 16; ++e) {
+              const int c0 = 32 * blk + 2 * e;
+              float x0, x1;
+              ffma2(x0, x1, u2f(s[c0]), u2f(s[c0 + 1]), f, f, -m_used, -m_used);
+              float p0 = ex2_approx(x0), p1 = ex2_approx(x1);
+              if (kMasked) {
+                p0 = c0 < valid ? p0 : 0.0f;
+                p1 = c0 + 1 < valid ? p1 : 0.0f;
+              }
+              fadd2(rs0, rs1, rs0, rs1, p0, p1);
+              pk[e] = pack_bf16x2(p0, p1);
+            }
+            tmem_st16(tS + 16 * blk, pk);
+            if (blk & 1) {
+              if (blk == 1 && __any_sync(0xffffffffu, scale)) {
+                // O_i must hold P_{j-1} V_{j-1} before it is rescaled, and be rescaled before
+                // the first half of P_j V_j accumulates into it
+                if (mbar_wait_warp<true>(&sm.o_done[i], (it - 1) & 1, abort_flag, err, kErrTimeoutMma)) {
+                  tc_fence_after();
+                  uint32_t oa[16], ob[16];
+                  tmem_ld16(tO, oa);
+                  tmem_ld_wait();
+                  tmem_reg_fence16(oa);
+  #pragma unroll
+                  for (int c2 = 0; c2 < 8; c2 += 2) {
+                    tmem_ld16(tO + 16 * (c2 + 1), ob);
+  #pragma unroll
+                    for (int e = 0; e < 16; ++e) oa[e] = f2u(u2f(oa[e]) * sc);
+                    tmem_st16(tO + 16 * c2, oa);
+                    tmem_ld_wait();
+                    tmem_reg_fence16(ob);
+                    if (c2 + 2 < 8) tmem_ld16(tO + 16 * (c2 + 2), oa);
+  #pragma unroll
+                    for (int e = 0; e < 16; ++e) ob[e] = f2u(u2f(ob[e]) * sc);
+                    tmem_st16(tO + 16 * (c2 + 1), ob);
+                    if (c2 + 2 < 8) {
+                      tmem_ld_wait();
+                      tmem_reg_fence16(oa);
+                    }
+                  }
+                } else {
+                  ok = false;
+                }
+              }
+              tmem_st_wait();
+              tc_fence_before();
+              __syncwarp();
+              if (ok && lane == 0) mbar_arrive(&sm.p_full[i][blk >> 1]);
+            }
+          }
+        };
+        if (partial) p_section(std::true_type{});
+        else p_section(std::false_type{});
+        if (!ok) break;
+        l += rs0 + rs1;
       }
-    } else if (ok && mbar_wait_warp<true>(&sm.o_done[i], (n - 1) & 1, abort_flag, err, kErrTimeoutMma)) {
-      tc_fence_after();
-      // an empty row next to others: its probabilities, and so its O and l, are zeros
-      store_row_bf16(tO, dst, limit > 0 ? 1.0f / l : 0.0f, store);
-      if (store) *lse = limit > 0 ? kLn2 * (m_used + log2f(l)) : -INFINITY;
-    }
+
+      if (!ok) break;
+      const Item item = item_of(p, work_read(sm.work, turn));
+      const int row = item.row0 + i * kTile + wq * 32 + lane;
+      const bool some = row_limit(p.mask, item.keys, row) > 0;
+      if (item.n > 0) {
+        ok = mbar_wait_warp<true>(&sm.o_done[i], (it - 1) & 1, abort_flag, err, kErrTimeoutMma);
+        if (!ok) break;
+        tc_fence_after();
+      }
+      const int row0 = row - lane;
+      __nv_bfloat16* dst = p.o + (long long)item.b * p.o_sb + (long long)row0 * p.o_ss + (long long)item.h * p.o_sh;
+#pragma unroll
+      for (int half = 0; half < 2; ++half) {
+        uint32_t out[32] = {};
+        // (an empty row next to others: its probabilities, and so its O and l, are zeros)
+        if (item.n > 0) load_row_bf16<64>(tO + 64 * half, out, some ? 1.0f / l : 0.0f);
+        store_rows<64>(dst + 64 * half, p.o_ss, out, p.mask.Sq - row0, lane);
+      }
+      tc_fence_before();
+      if (row < p.mask.Sq)
+        p.lse[((long long)item.b * p.Hq + item.h) * p.mask.Sq + row] = some ? kLn2 * (m_used + log2f(l)) : -INFINITY;
+      work_release(sm.work, turn, lane);
+    } while (work_wait(sm.work, ++turn, abort_flag, err));
   }
 
   tc_fence_before();
@@ -328,7 +391,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   tc_fence_after();
   if (warp == kWarpMma) {
     __syncwarp();
-    tmem_dealloc(tmem, 512);
+    tmem_dealloc(sm.tmem_base, 512);
   }
 }
 

@@ -196,6 +196,16 @@ def test_long_axis(cuda_dev):
     check(*make(cuda_dev, 1, 3, 6000, 2, 1, seed=13), causal=True)
 
 
+@pytest.mark.parametrize("causal", [False, True])
+@pytest.mark.parametrize("B,Sq,Sk,Hq,Hkv,lens", [
+    (3, 300, 300, 64, 64, [300, 1, 0]), (2, 520, 200, 96, 32, [200, 130]), (5, 100, 700, 80, 40, [0, 700, 0, 129, 640]),
+    (1, 700, 1100, 100, 100, None)])
+def test_more_items_than_sms(cuda_dev, B, Sq, Sk, Hq, Hkv, lens, causal):
+    """Each CTA takes several items: long ones, short ones and empty ones after one another."""
+    n = None if lens is None else torch.tensor(lens, dtype=torch.int32, device=cuda_dev)
+    check(*make(cuda_dev, B, Sq, Sk, Hq, Hkv, seed=30 + B), causal=causal, kv_len=n)
+
+
 def test_empty_problem(cuda_dev):
     z = lambda *s: torch.empty(s, dtype=torch.bfloat16, device=cuda_dev)  # noqa: E731
     o, lse = sa.attn_fwd_bf16_lse(z(0, 30, 2, 128), z(0, 40, 2, 128), z(0, 40, 2, 128))
