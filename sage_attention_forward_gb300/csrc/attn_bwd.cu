@@ -42,8 +42,9 @@ using namespace tiles;
 constexpr int kGroups = 4;
 constexpr int kCols = kTile / kGroups;
 constexpr int kWarpLoad = 4 * kGroups;
-constexpr int kWarpMma = kWarpLoad + 1;
-constexpr int kThreads = 32 * (kWarpMma + 1);
+constexpr int kWarpMma = kWarpLoad + 1;   // and the next
+constexpr int kWarpClear = kWarpMma + 2;
+constexpr int kThreads = 32 * (kWarpClear + 1);
 constexpr float kLog2e = 1.4426950408889634f;
 
 __device__ uint32_t g_err_bwd;
@@ -167,7 +168,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   uint32_t* err = &g_err_bwd;
 
   if (threadIdx.x == 0) {
-    work_init(sm.work, kWarpLoad + 1);
+    work_init(sm.work, kWarpLoad + 1);   // readers: softmax, MMA
     mbar_init(&sm.k_full, 1);
     mbar_init(&sm.k_empty, 1);
     mbar_init(&sm.v_full, 1);
@@ -206,14 +207,14 @@ __global__ void __launch_bounds__(kThreads, 1)
       tma_prefetch_desc(&tm_d);
       int it = 0, items = 0, requests = 0, q_issued = 0, d_issued = 0, k_issued = 0, v_issued = 0;
       auto load_item = [&](const ItemKV& i) -> bool {
-        if (items > 0 && !wait_one(&sm.k_empty, (items - 1) & 1, abort_flag, err, kErrTimeoutSync)) return false;
+        if (items > 0 && !wait_sleep(&sm.k_empty, (items - 1) & 1, abort_flag, err, kErrTimeoutSync)) return false;
         mbar_arrive_expect_tx(&sm.k_full, kTileBytes);
         load_tile(sm.k, &tm_k, &sm.k_full, i.key0, i.hk, i.b);
         ++k_issued;
         int t = i.first, h = i.hk * p.group;
         for (int j = 0; j < i.n; ++j, ++it) {
           const int slot = it & 1, use = it >> 1;
-          if (use > 0 && !wait_one(&sm.q_empty[slot], (use - 1) & 1, abort_flag, err, kErrTimeoutSync)) return false;
+          if (use > 0 && !wait_sleep(&sm.q_empty[slot], (use - 1) & 1, abort_flag, err, kErrTimeoutSync)) return false;
           const long long at = ((long long)i.b * p.H * p.group + h) * p.Sq_pad + t * kTile;
           mbar_arrive_expect_tx(&sm.q_full[slot], kTileBytes + 2 * kTile * 4);
           load_tile(sm.q[slot], &tm_q, &sm.q_full[slot], t * kTile, h, i.b);
@@ -221,12 +222,12 @@ __global__ void __launch_bounds__(kThreads, 1)
           bulk_load(sm.neg_delta[slot], p.neg_delta + at, kTile * 4, &sm.q_full[slot]);
           ++q_issued;
           if (j == 0) {
-            if (items > 0 && !wait_one(&sm.v_empty, (items - 1) & 1, abort_flag, err, kErrTimeoutSync)) return false;
+            if (items > 0 && !wait_sleep(&sm.v_empty, (items - 1) & 1, abort_flag, err, kErrTimeoutSync)) return false;
             mbar_arrive_expect_tx(&sm.v_full, kTileBytes);
             load_tile(sm.v, &tm_v, &sm.v_full, i.key0, i.hk, i.b);
             ++v_issued;
           }
-          if (use > 0 && !wait_one(&sm.d_empty[slot], (use - 1) & 1, abort_flag, err, kErrTimeoutSync)) return false;
+          if (use > 0 && !wait_sleep(&sm.d_empty[slot], (use - 1) & 1, abort_flag, err, kErrTimeoutSync)) return false;
           mbar_arrive_expect_tx(&sm.d_full[slot], kTileBytes);
           load_tile(sm.dout[slot], &tm_d, &sm.d_full[slot], t * kTile, h, i.b);
           ++d_issued;
@@ -257,31 +258,35 @@ __global__ void __launch_bounds__(kThreads, 1)
   } else if (warp == kWarpMma) {
     // The tensor core's order is dV(i) S(i+1) dK(i) dP(i+1), over the tile products i of all items:
     // S(i+1) overwrites P(i) and dP(i+1) dS(i) after the products that read them, and while the
-    // softmax warps work on one of the two chains S -> P -> dV and dP -> dS -> dK the tensor core works
-    // on the other.  An item's first dV and dK overwrite the accumulators of the item before:
-    // the softmax warps published that P and dS after they had read them.
+    // softmax warps work on one of the two chains S -> P -> dV and dP -> dS -> dK the tensor core
+    // works on the other.  (A warp for each chain let their products alternate: 10 % slower.)  An
+    // item's first dV and dK overwrite the accumulators of the item before: the softmax warps
+    // published that P and dS after they had read them.
     const bool leader = elect_one();
-    const uint32_t tS = tmem, tDP = tmem + 128, tDV = tmem + 256, tDK = tmem + 384;
-    auto make = [&](const Work& w) { return item_kv(p, w); };
-    Walk<ItemKV, decltype(make)> walk(make);
-    auto next_product = [&](bool wait) { return walk.next(wait, sm.work, lane, abort_flag, err); };
-    int k_items = 0, v_items = 0;
+    constexpr uint32_t tS = 0, tDP = 128, tDV = 256, tDK = 384;
     const uint32_t dk = desc_k(sm.k), dv = desc_k(sm.v), dq = desc_k(sm.q[0]), dd = desc_k(sm.dout[0]);
     const uint32_t dq_mn = desc_mn(sm.q[0]), dd_mn = desc_mn(sm.dout[0]);
-    auto issue_s = [&](int i, int flags) -> bool {
+    int k_items = 0, v_items = 0;
+    auto make = [&](const Work& w) { return item_kv(p, w); };
+    Walk<ItemKV, decltype(make)> walk(make);
+    int f0 = walk.next(sm.work, lane, abort_flag, err);
+    // (a step's ring slots are compile-time constants, and so are the distances of its descriptors)
+    auto issue_s = [&](auto slot_c, int i, int flags) -> bool {
+      constexpr int slot = decltype(slot_c)::value;
       if ((flags & kFirst) && !wait_warp(&sm.k_full, k_items++ & 1, abort_flag, err, kErrTimeoutTma)) return false;
-      if (!wait_warp(&sm.q_full[i & 1], (i >> 1) & 1, abort_flag, err, kErrTimeoutTma)) return false;
+      if (!wait_warp(&sm.q_full[slot], (i >> 1) & 1, abort_flag, err, kErrTimeoutTma)) return false;
       tc_fence_after();
-      mma_tile_nt(tS, dk, dq + kDescTile * (i & 1), leader);
+      mma_tile_nt(tS, dk, dq + kDescTile * slot, leader);
       if (leader) mma_commit(&sm.s_full);
       if (leader && (flags & kLast)) mma_commit(&sm.k_empty);
       return true;
     };
-    auto issue_dp = [&](int i, int flags) -> bool {
+    auto issue_dp = [&](auto slot_c, int i, int flags) -> bool {
+      constexpr int slot = decltype(slot_c)::value;
       if ((flags & kFirst) && !wait_warp(&sm.v_full, v_items++ & 1, abort_flag, err, kErrTimeoutTma)) return false;
-      if (!wait_warp(&sm.d_full[i & 1], (i >> 1) & 1, abort_flag, err, kErrTimeoutTma)) return false;
+      if (!wait_warp(&sm.d_full[slot], (i >> 1) & 1, abort_flag, err, kErrTimeoutTma)) return false;
       tc_fence_after();
-      mma_tile_nt(tDP, dv, dd + kDescTile * (i & 1), leader);
+      mma_tile_nt(tDP, dv, dd + kDescTile * slot, leader);
       if (leader) mma_commit(&sm.dp_full);
       if (leader && (flags & kLast)) mma_commit(&sm.v_empty);
       return true;
@@ -298,33 +303,30 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       return true;
     };
-    int f0 = next_product(true);
-    bool ok = f0 == kEnd || (issue_s(0, f0) && issue_dp(0, f0));
-    for (int i = 0; ok && f0 != kEnd; ++i) {
-      const int slot = i & 1;
+    auto step = [&](auto slot_c, auto next_c, int i) -> bool {
+      constexpr int slot = decltype(slot_c)::value;
       const bool last = f0 & kLast, first = f0 & kFirst;
-      int f1 = last ? kUnknown : next_product(true);
-      ok = issue_acc(tDV, tS, sm.p_full, dd_mn + kDescTile * slot, i, first);
-      if (!ok) break;
+      if (!last) f0 = walk.next(sm.work, lane, abort_flag, err);
+      if (!issue_acc(tDV, tS, sm.p_full, dd_mn + kDescTile * slot, i, first)) return false;
       if (leader) mma_commit(&sm.d_empty[slot]);   // (dP(i) was issued before)
-      if (last) f1 = next_product(false);
-      ok = f1 <= kEnd || issue_s(i + 1, f1);
-      if (!ok) break;
-      ok = issue_acc(tDK, tDP, sm.ds_full, dq_mn + kDescTile * slot, i, first);
-      if (!ok) break;
+      if (!last && !issue_s(next_c, i + 1, f0)) return false;
+      if (!issue_acc(tDK, tDP, sm.ds_full, dq_mn + kDescTile * slot, i, first)) return false;
       if (leader) mma_commit(&sm.q_empty[slot]);
-      if (leader && last) mma_commit(&sm.acc_done);
-      if (f1 == kUnknown) {
-        f1 = next_product(true);
-        ok = f1 == kEnd || issue_s(i + 1, f1);
-        if (!ok) break;
-      }
-      ok = f1 == kEnd || issue_dp(i + 1, f1);
-      f0 = f1;
+      if (!last) return issue_dp(next_c, i + 1, f0);
+      if (leader) mma_commit(&sm.acc_done);
+      f0 = walk.next(sm.work, lane, abort_flag, err);
+      return f0 == kEnd || (issue_s(next_c, i + 1, f0) && issue_dp(next_c, i + 1, f0));
+    };
+    const std::integral_constant<int, 0> c0;
+    const std::integral_constant<int, 1> c1;
+    bool ok = f0 == kEnd || (issue_s(c0, 0, f0) && issue_dp(c0, 0, f0));
+    for (int i = 0; ok && f0 != kEnd; i += 2) {
+      ok = step(c0, c1, i);
+      if (ok && f0 != kEnd) ok = step(c1, c0, i + 1);
     }
     if (leader) mma_commit(&sm.drain);
     mbar_wait_teardown(&sm.drain, 0);
-  } else {
+  } else if (warp < kWarpLoad) {
     // Warpgroup g takes the queries [32 g, 32 g + 32) of each tile.  A thread has eight of these
     // columns of four keys (rows lane / 4 + 8 r of its warp's 32), not 32 columns of one: the
     // statistics, which belong to the columns, are then 8 values a thread and not 32 (the
@@ -489,7 +491,7 @@ struct __align__(1024) SmemQ {
   WorkRing work;
   uint64_t q_full, q_empty, d_full, d_empty;
   uint64_t q_ready;      // Q in TMEM (every softmax warp's part)
-  uint64_t k_full[kKRing], k_empty[kKRing];
+  uint64_t k_full[kKRing], k_empty[kKRing], k_clear[kKRing];
   uint64_t v_full[kVRing], v_empty[kVRing];
   uint64_t s_full, s_free;     // S in TMEM; read by every softmax warp
   uint64_t dp_full;
@@ -532,7 +534,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   uint32_t* err = &g_err_bwd;
 
   if (threadIdx.x == 0) {
-    work_init(sm.work, kWarpLoad + 1);
+    work_init(sm.work, kWarpLoad + 2 + (p.mask.kv_len != nullptr ? 1 : 0));   // readers: softmax, MMA, clear
     mbar_init(&sm.q_full, 1);
     mbar_init(&sm.q_empty, kWarpLoad);
     mbar_init(&sm.q_ready, kWarpLoad);
@@ -541,6 +543,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     for (int s = 0; s < kKRing; ++s) {
       mbar_init(&sm.k_full[s], 1);
       mbar_init(&sm.k_empty[s], 1);
+      mbar_init(&sm.k_clear[s], 1);
     }
     for (int s = 0; s < kVRing; ++s) {
       mbar_init(&sm.v_full[s], 1);
@@ -552,7 +555,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     mbar_init(&sm.ds_full, kWarpLoad);
     mbar_init(&sm.ds_free, 1);
     mbar_init(&sm.acc_done, 1);
-    mbar_init(&sm.drain, 1);
+    mbar_init(&sm.drain, 2);
     sm.abort_flag = 0;
     fence_mbar_init();
   }
@@ -578,27 +581,27 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int hk = i.h / p.group;
         for (int j = 0; j < i.n; ++j, ++it) {
           if (j == 0) {
-            if (items > 0 && !wait_one(&sm.q_empty, (items - 1) & 1, abort_flag, err, kErrTimeoutSync)) return false;
+            if (items > 0 && !wait_sleep(&sm.q_empty, (items - 1) & 1, abort_flag, err, kErrTimeoutSync)) return false;
             mbar_arrive_expect_tx(&sm.q_full, kTileBytes);
             load_tile(sm.q, &tm_q, &sm.q_full, i.row0, i.h, i.b);
             ++q_issued;
           }
           {
             const int slot = it % kKRing, use = it / kKRing;
-            if (use > 0 && !wait_one(&sm.k_empty[slot], (use - 1) & 1, abort_flag, err, kErrTimeoutSync)) return false;
+            if (use > 0 && !wait_sleep(&sm.k_empty[slot], (use - 1) & 1, abort_flag, err, kErrTimeoutSync)) return false;
             mbar_arrive_expect_tx(&sm.k_full[slot], kTileBytes);
             load_tile(sm.k[slot], &tm_k, &sm.k_full[slot], j * kTile, hk, i.b);
             ++k_issued;
           }
           if (j == 0) {
-            if (items > 0 && !wait_one(&sm.d_empty, (items - 1) & 1, abort_flag, err, kErrTimeoutSync)) return false;
+            if (items > 0 && !wait_sleep(&sm.d_empty, (items - 1) & 1, abort_flag, err, kErrTimeoutSync)) return false;
             mbar_arrive_expect_tx(&sm.d_full, kTileBytes);
             load_tile(sm.dout, &tm_d, &sm.d_full, i.row0, i.h, i.b);
             ++d_issued;
           }
           {
             const int slot = it % kVRing, use = it / kVRing;
-            if (use > 0 && !wait_one(&sm.v_empty[slot], (use - 1) & 1, abort_flag, err, kErrTimeoutSync)) return false;
+            if (use > 0 && !wait_sleep(&sm.v_empty[slot], (use - 1) & 1, abort_flag, err, kErrTimeoutSync)) return false;
             mbar_arrive_expect_tx(&sm.v_full[slot], kTileBytes);
             load_tile(sm.v[slot], &tm_v, &sm.v_full[slot], j * kTile, hk, i.b);
             ++v_issued;
@@ -624,68 +627,76 @@ __global__ void __launch_bounds__(kThreads, 1)
           mbar_wait_teardown(&sm.v_full[i % kVRing], (i / kVRing) & 1);
       }
     }
-  } else if (warp == kWarpMma) {
-    // The tensor core's order is S(i+1) dP(i+1) dQ(i), over the tile products i of all items.  S(i+1)
-    // starts when the softmax warps have S(i) in registers, dP(i+1) and dQ(i) when dS(i) is there, so
-    // that both chains run beside the elementwise work.  An item's first dQ overwrites the
-    // accumulator of the item before: the softmax warps published that dS after they had read it.
+  } else if (warp == kWarpMma || warp == kWarpMma + 1) {
+    // Two warps issue the products, over the tile products i of all items: one S(i+1) as soon as
+    // the softmax warps have S(i) in registers, the other dP(i+1) and dQ(i) when dS(i) is there.  An
+    // item's first dQ overwrites the accumulator of the item before: the softmax warps
+    // published that dS after they had read it.
     const bool leader = elect_one();
-    int q_items = 0, d_items = 0;
     auto make = [&](const Work& w) { return item_q(p, w); };
     Walk<ItemQ, decltype(make)> walk(make);
-    auto next_product = [&](bool wait) { return walk.next(wait, sm.work, lane, abort_flag, err); };
-    const uint32_t dd = desc_k(sm.dout), dk = desc_k(sm.k[0]), dv = desc_k(sm.v[0]), dk_mn = desc_mn(sm.k[0]);
-    auto issue_s = [&](int i, int flags) -> bool {
-      const int slot = i % kKRing;
-      const int keys = walk.item.keys;   // (S goes first over the items: the walk is at this product)
-      const int clear = keys < p.mask.Sk && walk.j * kTile > keys ? keys - (walk.j - 1) * kTile : kTile;
-      if ((flags & kFirst) && !wait_warp(&sm.q_ready, q_items++ & 1, abort_flag, err, kErrTimeoutSync)) return false;
-      if (!wait_warp(&sm.k_full[slot], (i / kKRing) & 1, abort_flag, err, kErrTimeoutTma)) return false;
-      if (clear < kTile) clear_rows(sm.k[slot], clear, lane);
-      if (i > 0 && !wait_warp(&sm.s_free, (i - 1) & 1, abort_flag, err, kErrTimeoutSync)) return false;
-      tc_fence_after();
-      mma_tile_nt_ts(tS, tQ, dk + kDescTile * slot, leader);
-      if (leader) mma_commit(&sm.s_full);
-      return true;
-    };
-    auto issue_dp = [&](int i, int flags) -> bool {
-      const int slot = i % kVRing;
-      if ((flags & kFirst) && !wait_warp(&sm.d_full, d_items++ & 1, abort_flag, err, kErrTimeoutTma)) return false;
-      if (!wait_warp(&sm.v_full[slot], (i / kVRing) & 1, abort_flag, err, kErrTimeoutTma)) return false;
-      tc_fence_after();
-      mma_tile_nt(tDP, dd, dv + kDescTile * slot, leader);
-      if (leader) mma_commit(&sm.dp_full);
-      if (leader) mma_commit(&sm.v_empty[slot]);
-      if (leader && (flags & kLast)) mma_commit(&sm.d_empty);
-      return true;
-    };
-    int f0 = next_product(true);
-    bool ok = f0 == kEnd || (issue_s(0, f0) && issue_dp(0, f0));
-    for (int i = 0; ok && f0 != kEnd; ++i) {
-      const int slot = i % kKRing;
-      const bool last = f0 & kLast, first = f0 & kFirst;
-      int f1 = kEnd;
-      if (!last) {
-        f1 = next_product(true);
-        ok = issue_s(i + 1, f1);
+    int items = 0;
+    int f0 = walk.next(sm.work, lane, abort_flag, err);
+    bool ok = true;
+    if (warp == kWarpMma) {
+      const uint32_t dk = desc_k(sm.k[0]);
+      for (int i = 0; f0 != kEnd; ++i) {
+        const int slot = i % kKRing;
+        ok = (!(f0 & kFirst) || wait_warp(&sm.q_ready, items++ & 1, abort_flag, err, kErrTimeoutSync)) &&
+             wait_warp(&sm.k_full[slot], (i / kKRing) & 1, abort_flag, err, kErrTimeoutTma) &&
+             (i == 0 || wait_warp(&sm.s_free, (i - 1) & 1, abort_flag, err, kErrTimeoutSync));
         if (!ok) break;
+        tc_fence_after();
+        mma_tile_nt_ts(tS, tQ, dk + kDescTile * slot, leader);
+        if (leader) mma_commit(&sm.s_full);
+        f0 = walk.next(sm.work, lane, abort_flag, err);
       }
-      ok = wait_warp(&sm.ds_full, i & 1, abort_flag, err, kErrTimeoutSync) && (last || issue_dp(i + 1, f1));
-      if (!ok) break;
-      tc_fence_after();
-      mma_tile_part_nn<kTile>(tDQ, tDS, dk_mn + kDescTile * slot, 0, !first, leader);
-      if (leader) mma_commit(&sm.k_empty[slot]);
-      if (leader) mma_commit(&sm.ds_free);
-      if (last) {
-        if (leader) mma_commit(&sm.acc_done);
-        f1 = next_product(true);
-        ok = f1 == kEnd || (issue_s(i + 1, f1) && issue_dp(i + 1, f1));
+    } else {
+      const uint32_t dd = desc_k(sm.dout), dv = desc_k(sm.v[0]), dk_mn = desc_mn(sm.k[0]);
+      uint32_t cleared = 0;   // parity of each slot's clear barrier
+      auto issue_dp = [&](int i, int flags) -> bool {
+        const int slot = i % kVRing;
+        if ((flags & kFirst) && !wait_warp(&sm.d_full, items++ & 1, abort_flag, err, kErrTimeoutTma)) return false;
+        if (!wait_warp(&sm.v_full[slot], (i / kVRing) & 1, abort_flag, err, kErrTimeoutTma)) return false;
+        tc_fence_after();
+        mma_tile_nt(tDP, dd, dv + kDescTile * slot, leader);
+        if (leader) mma_commit(&sm.dp_full);
+        if (leader) mma_commit(&sm.v_empty[slot]);
+        if (leader && (flags & kLast)) mma_commit(&sm.d_empty);
+        return true;
+      };
+      ok = f0 == kEnd || issue_dp(0, f0);
+      for (int i = 0; ok && f0 != kEnd; ++i) {
+        const int slot = i % kKRing;
+        const bool last = f0 & kLast, first = f0 & kFirst;
+        if (last) {
+          if (last_rows(p.mask, walk.item.keys, walk.item.n) < kTile) {
+            ok = wait_warp(&sm.k_clear[slot], (cleared >> slot) & 1, abort_flag, err, kErrTimeoutSync);
+            cleared ^= 1u << slot;
+          }
+        } else {
+          f0 = walk.next(sm.work, lane, abort_flag, err);
+        }
+        ok = ok && wait_warp(&sm.ds_full, i & 1, abort_flag, err, kErrTimeoutSync) && (last || issue_dp(i + 1, f0));
+        if (!ok) break;
+        tc_fence_after();
+        mma_tile_part_nn<kTile>(tDQ, tDS, dk_mn + kDescTile * slot, 0, !first, leader);
+        if (leader) mma_commit(&sm.ds_free);
+        if (leader) mma_commit(&sm.k_empty[slot]);   // (dS(i) followed S(i), the other reader of K(i))
+        if (last) {
+          if (leader) mma_commit(&sm.acc_done);
+          f0 = walk.next(sm.work, lane, abort_flag, err);
+          ok = f0 == kEnd || issue_dp(i + 1, f0);
+        }
       }
-      f0 = f1;
     }
     if (leader) mma_commit(&sm.drain);
     mbar_wait_teardown(&sm.drain, 0);
-  } else {
+  } else if (warp == kWarpClear) {
+    if (p.mask.kv_len != nullptr)
+      clear_warp<kKRing>(p.mask, [&](const Work& w) { return item_q(p, w); }, sm.work, sm.k, sm.k_full, sm.k_clear, lane,
+                         abort_flag, err);
+  } else if (warp < kWarpLoad) {
     // warpgroup g takes the keys [32 g, 32 g + 32) of each tile, a thread one query
     const int g = warp >> 2, wq = warp & 3;
     const uint32_t lane_off = (uint32_t)(wq * 32) << 16;

@@ -27,9 +27,10 @@ using namespace tiles;
 
 constexpr int kNQ = 2;
 constexpr int kStages = 2;
-constexpr int kThreads = 320;
 constexpr int kWarpLoad = 8;
 constexpr int kWarpMma = 9;
+constexpr int kWarpClear = 10;
+constexpr int kThreads = 352;
 constexpr float kTau = 64.0f;   // as the BF16 forward: p <= 2^64 stays far inside BF16's and FP32's range
 constexpr float kLn2 = 0.6931471805599453f;
 
@@ -40,7 +41,7 @@ struct __align__(1024) Smem {
   WorkRing work;
   uint64_t q_full, q_empty;
   uint64_t k_full[kStages], k_empty[kStages];
-  uint64_t v_full[kStages], v_empty[kStages];
+  uint64_t v_full[kStages], v_empty[kStages], v_clear[kStages];
   uint64_t s_full[kNQ];
   uint64_t p_full[kNQ][2];   // P_i keys [0, 64) and [64, 128) stored in TMEM
   uint64_t o_done[kNQ];
@@ -95,7 +96,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   uint32_t* err = &g_err_lse;
 
   if (threadIdx.x == 0) {
-    work_init(sm.work, kWarpLoad + 1);
+    work_init(sm.work, kWarpLoad + 1 + (p.mask.kv_len != nullptr ? 1 : 0));   // readers: softmax, MMA, clear
     mbar_init(&sm.q_full, 1);
     mbar_init(&sm.q_empty, 1);
     for (int s = 0; s < kStages; ++s) {
@@ -103,6 +104,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_init(&sm.k_empty[s], 1);
       mbar_init(&sm.v_full[s], 1);
       mbar_init(&sm.v_empty[s], 1);
+      mbar_init(&sm.v_clear[s], 1);
     }
     for (int i = 0; i < kNQ; ++i) {
       mbar_init(&sm.s_full[i], 1);
@@ -132,17 +134,17 @@ __global__ void __launch_bounds__(kThreads, 1)
       int it = 0, items = 0, requests = 0, q_issued = 0, k_issued = 0, v_issued = 0;
       auto load_item = [&](const Item& i) -> bool {
         const int hk = i.h / p.group;
-        if (items > 0 && !wait_one(&sm.q_empty, (items - 1) & 1, abort_flag, err, kErrTimeoutSync)) return false;
+        if (items > 0 && !wait_sleep(&sm.q_empty, (items - 1) & 1, abort_flag, err, kErrTimeoutSync)) return false;
         mbar_arrive_expect_tx(&sm.q_full, kNQ * kTileBytes);
         for (int q = 0; q < kNQ; ++q) load_tile(sm.q[q], &tm_q, &sm.q_full, i.row0 + q * kTile, i.h, i.b);
         ++q_issued;
         for (int j = 0; j < i.n; ++j, ++it) {
           const int slot = it % kStages, use = it / kStages;
-          if (use > 0 && !wait_one(&sm.k_empty[slot], (use - 1) & 1, abort_flag, err, kErrTimeoutSync)) return false;
+          if (use > 0 && !wait_sleep(&sm.k_empty[slot], (use - 1) & 1, abort_flag, err, kErrTimeoutSync)) return false;
           mbar_arrive_expect_tx(&sm.k_full[slot], kTileBytes);
           load_tile(sm.k[slot], &tm_k, &sm.k_full[slot], j * kTile, hk, i.b);
           ++k_issued;
-          if (use > 0 && !wait_one(&sm.v_empty[slot], (use - 1) & 1, abort_flag, err, kErrTimeoutSync)) return false;
+          if (use > 0 && !wait_sleep(&sm.v_empty[slot], (use - 1) & 1, abort_flag, err, kErrTimeoutSync)) return false;
           mbar_arrive_expect_tx(&sm.v_full[slot], kTileBytes);
           load_tile(sm.v[slot], &tm_v, &sm.v_full[slot], j * kTile, hk, i.b);
           ++v_issued;
@@ -168,78 +170,89 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
     }
   } else if (warp == kWarpMma) {
-    // Over the key tiles i of all items: P_0 V(i), S_0(i+1), P_1 V(i), S_1(i+1).  An item's first
-    // P V overwrites the O of the item before: the softmax warps published that P after they had
-    // read it.
+    // Over the key tiles i of all items: P_0 V(i), S_0(i+1), P_1 V(i), S_1(i+1), in this order: while
+    // one Q tile's softmax runs the tensor core works on the other.  (A warp for each tile let their
+    // products alternate, both S came late together, and a step took 3400 cycles instead of 2700.)
+    // S_q(i+1) overwrites P_q(i) after the product that reads it.  An item's first P V overwrites the
+    // O of the item before: the softmax warps published that P after they had read it.
     const bool leader = elect_one();
-    auto tS = [&](int q) { return tmem + 128u * (uint32_t)q; };
-    auto tO = [&](int q) { return tmem + 256u + 128u * (uint32_t)q; };
+    const uint32_t dq = desc_k(sm.q[0]), dk = desc_k(sm.k[0]), dv = desc_mn(sm.v[0]);
     int q_items = 0;
+    uint32_t cleared = 0;   // parity of each slot's clear barrier
     auto make = [&](const Work& w) { return item_of(p, w); };
     Walk<Item, decltype(make)> walk(make);
-    auto next_product = [&](bool wait) { return walk.next(wait, sm.work, lane, abort_flag, err); };
-    const uint32_t dq = desc_k(sm.q[0]), dk = desc_k(sm.k[0]), dv = desc_mn(sm.v[0]);
-    auto wait_qk = [&](int i, int flags) -> bool {
+    int f0 = walk.next(sm.work, lane, abort_flag, err);
+    // (a step's ring slots are compile-time constants, and so are the distances of its descriptors)
+    auto wait_qk = [&](auto slot_c, int i, int flags) -> bool {
+      constexpr int slot = decltype(slot_c)::value;
       if ((flags & kFirst) && !wait_warp(&sm.q_full, q_items++ & 1, abort_flag, err, kErrTimeoutTma)) return false;
-      return wait_warp(&sm.k_full[i % kStages], (i / kStages) & 1, abort_flag, err, kErrTimeoutTma);
+      return wait_warp(&sm.k_full[slot], (i / kStages) & 1, abort_flag, err, kErrTimeoutTma);
     };
-    auto issue_s = [&](int q, int i, int flags) {
+    auto issue_s = [&](auto slot_c, auto q_c, int flags) {
+      constexpr int slot = decltype(slot_c)::value, q = decltype(q_c)::value;
       tc_fence_after();
-      mma_tile_nt(tS(q), dq + kDescTile * q, dk + kDescTile * (i % kStages), leader);
+      mma_tile_nt(tmem + 128 * q, dq + kDescTile * q, dk + kDescTile * slot, leader);
       if (leader) mma_commit(&sm.s_full[q]);
-      if (leader && q == kNQ - 1) mma_commit(&sm.k_empty[i % kStages]);
+      if (leader && q == kNQ - 1) mma_commit(&sm.k_empty[slot]);
       if (leader && q == kNQ - 1 && (flags & kLast)) mma_commit(&sm.q_empty);
     };
-    auto issue_pv = [&](int q, int i, bool first) -> bool {
-      const uint32_t v = dv + kDescTile * (i % kStages);
+    auto issue_pv = [&](auto slot_c, auto q_c, int i, bool first) -> bool {
+      constexpr int slot = decltype(slot_c)::value, q = decltype(q_c)::value;
 #pragma unroll
       for (int half = 0; half < 2; ++half) {
         if (!wait_warp(&sm.p_full[q][half], i & 1, abort_flag, err, kErrTimeoutSync)) return false;
         tc_fence_after();
-        mma_tile_part_nn<64>(tO(q), tS(q) + 32 * half, v, half, !first || half > 0, leader);
+        mma_tile_part_nn<64>(tmem + 256 + 128 * q, tmem + 128 * q + 32 * half, dv + kDescTile * slot, half,
+                             !first || half > 0, leader);
       }
       if (leader) mma_commit(&sm.o_done[q]);
       return true;
     };
-    int f0 = next_product(true);
-    bool ok = f0 == kEnd || wait_qk(0, f0);
-    if (ok && f0 != kEnd) {
-      issue_s(0, 0, f0);
-      issue_s(1, 0, f0);
-    }
-    for (int i = 0; ok && f0 != kEnd; ++i) {
-      const int keys = walk.item.keys;   // (the walk is at product i here)
-      const int clear = keys < p.mask.Sk && walk.j * kTile > keys ? keys - (walk.j - 1) * kTile : kTile;
+    const std::integral_constant<int, 0> c0;
+    const std::integral_constant<int, 1> c1;
+    auto step = [&](auto slot_c, auto next_c, int i) -> bool {
+      constexpr int slot = decltype(slot_c)::value;
       const bool last = f0 & kLast, first = f0 & kFirst;
-      int f1 = last ? kUnknown : next_product(true);
-      ok = wait_warp(&sm.v_full[i % kStages], (i / kStages) & 1, abort_flag, err, kErrTimeoutTma);
-      if (!ok) break;
-      if (clear < kTile) clear_rows(sm.v[i % kStages], clear, lane);
-      ok = issue_pv(0, i, first);
-      if (!ok) break;
-      if (last) f1 = next_product(false);
-      if (f1 > kEnd) {
-        ok = wait_qk(i + 1, f1);
-        if (!ok) break;
-        issue_s(0, i + 1, f1);
+      const bool clear = last && last_rows(p.mask, walk.item.keys, walk.item.n) < kTile;
+      if (!last) f0 = walk.next(sm.work, lane, abort_flag, err);
+      if (!wait_warp(&sm.v_full[slot], (i / kStages) & 1, abort_flag, err, kErrTimeoutTma)) return false;
+      if (clear) {
+        if (!wait_warp(&sm.v_clear[slot], (cleared >> slot) & 1, abort_flag, err, kErrTimeoutSync)) return false;
+        cleared ^= 1u << slot;
       }
-      ok = issue_pv(1, i, first);
-      if (!ok) break;
-      if (leader) mma_commit(&sm.v_empty[i % kStages]);
-      if (f1 == kUnknown) {
-        f1 = next_product(true);
-        if (f1 != kEnd) {
-          ok = wait_qk(i + 1, f1);
-          if (!ok) break;
-          issue_s(0, i + 1, f1);
-        }
+      if (!issue_pv(slot_c, c0, i, first)) return false;
+      if (!last) {
+        if (!wait_qk(next_c, i + 1, f0)) return false;
+        issue_s(next_c, c0, f0);
       }
-      if (f1 != kEnd) issue_s(1, i + 1, f1);
-      f0 = f1;
+      if (!issue_pv(slot_c, c1, i, first)) return false;
+      if (leader) mma_commit(&sm.v_empty[slot]);
+      if (last) {
+        f0 = walk.next(sm.work, lane, abort_flag, err);
+        if (f0 == kEnd) return true;
+        if (!wait_qk(next_c, i + 1, f0)) return false;
+        issue_s(next_c, c0, f0);
+      }
+      issue_s(next_c, c1, f0);
+      return true;
+    };
+    static_assert(kStages == 2, "two copies of the step");
+    bool ok = f0 == kEnd || wait_qk(c0, 0, f0);
+    if (ok && f0 != kEnd) {
+      issue_s(c0, c0, f0);
+      issue_s(c0, c1, f0);
+    }
+    for (int i = 0; ok && f0 != kEnd; i += 2) {
+      ok = step(c0, c1, i);
+      if (ok && f0 != kEnd) ok = step(c1, c0, i + 1);
     }
     if (leader) mma_commit(&sm.drain);
     mbar_wait_teardown(&sm.drain, 0);
-  } else {
+  } else if (warp == kWarpClear) {
+    if (p.mask.kv_len != nullptr)
+      clear_warp<kStages>(p.mask, [&](const Work& w) { return item_of(p, w); }, sm.work, sm.v, sm.v_full, sm.v_clear,
+                          lane, abort_flag, err);
+  } else if (warp < kWarpLoad) {
     const int i = warp >> 2, wq = warp & 3;
     const uint32_t lane_off = (uint32_t)(wq * 32) << 16;
     const uint32_t tS = tmem + lane_off + 128u * i;

@@ -31,23 +31,21 @@ __device__ __forceinline__ int row_limit(const Mask& m, int keys, int i) {
   return m.causal ? max(min(keys, i + 1 + (m.Sk - m.Sq)), 0) : keys;
 }
 
-// The MMA and load warps wait through these: the slow path of a bounded wait is a call, which keeps
-// their loops within the instruction cache (inlined at every wait, and with the loops unrolled by
-// their rings, dQ took 2880 cycles a tile pair instead of 2320).
+// The bounded waits of the load warp's thread, which may sleep on its barriers, and of the MMA warps,
+// which wait as a whole.  The slow path is a call, so that the loops that wait stay small.
 static __device__ __noinline__ bool wait_slow(uint64_t* bar, uint32_t parity, volatile uint32_t* abort_flag,
                                               uint32_t* err_word, uint32_t err) {
   return mbar_wait<false>(bar, parity, abort_flag, err_word, err);
+}
+static __device__ __noinline__ bool wait_sleep(uint64_t* bar, uint32_t parity, volatile uint32_t* abort_flag,
+                                               uint32_t* err_word, uint32_t err) {
+  return mbar_wait<true>(bar, parity, abort_flag, err_word, err);
 }
 __device__ __forceinline__ bool wait_warp(uint64_t* bar, uint32_t parity, volatile uint32_t* abort_flag,
                                           uint32_t* err_word, uint32_t err) {
   bool ok = mbar_try_wait<false>(bar, parity);
   if (!ok) ok = wait_slow(bar, parity, abort_flag, err_word, err);
   return __all_sync(0xffffffffu, ok);
-}
-// One thread of the load warp, whose waits may sleep on their barriers.
-static __device__ __noinline__ bool wait_one(uint64_t* bar, uint32_t parity, volatile uint32_t* abort_flag,
-                                             uint32_t* err_word, uint32_t err) {
-  return mbar_wait<true>(bar, parity, abort_flag, err_word, err);
 }
 
 // ------------------------------------------------------------------ work
@@ -79,33 +77,32 @@ __device__ __forceinline__ void work_init(WorkRing& r, int reader_warps) {
     mbar_init(&r.empty[s], reader_warps);
   }
 }
-// One thread of the load warp: ask for the item after w.
+// The load warp's thread: ask for the item after w.
 __device__ __forceinline__ bool work_request(WorkRing& r, const Work& w, volatile uint32_t* abort_flag, uint32_t* err) {
   const int s = w.t % kWorkSlots, use = w.t / kWorkSlots;
-  if (use > 0 && !wait_one(&r.empty[s], (use - 1) & 1, abort_flag, err, kErrTimeoutSync)) return false;
+  if (use > 0 && !wait_sleep(&r.empty[s], (use - 1) & 1, abort_flag, err, kErrTimeoutSync)) return false;
   mbar_arrive_expect_tx(&r.full[s], 16);
   clc_try_cancel(&r.answer[s], &r.full[s]);
   return true;
 }
-// The same thread: the answer, w becomes it; false at the end (or after an abort).
-__device__ __forceinline__ bool work_next_load(WorkRing& r, Work& w, volatile uint32_t* abort_flag, uint32_t* err) {
-  const int s = w.t % kWorkSlots, use = w.t / kWorkSlots;
-  ++w.t;
-  return wait_one(&r.full[s], use & 1, abort_flag, err, kErrTimeoutSync) &&
-         work_answer(&r.answer[s], w);
-}
-// A whole reader warp: waits for the answer for item t > 0; whether there is such an item.
-__device__ __forceinline__ bool work_wait(WorkRing& r, int t, volatile uint32_t* abort_flag, uint32_t* err) {
-  const int s = (t - 1) % kWorkSlots, use = (t - 1) / kWorkSlots;
-  Work w;
-  return mbar_wait_warp<false>(&r.full[s], use & 1, abort_flag, err, kErrTimeoutSync) && work_answer(&r.answer[s], w);
-}
-// Item t, after work_wait.  A warp short of registers reads it again rather than keep it.
+// Item t, once its answer is there.  A warp short of registers reads it again rather than keep it.
 __device__ __forceinline__ Work work_read(WorkRing& r, int t) {
   Work w = first_work();
   if (t > 0) work_answer(&r.answer[(t - 1) % kWorkSlots], w);
   w.t = t;
   return w;
+}
+// The same thread: w becomes the next item; false at the end (or after an abort).
+__device__ __forceinline__ bool work_next_load(WorkRing& r, Work& w, volatile uint32_t* abort_flag, uint32_t* err) {
+  const int s = w.t % kWorkSlots, use = w.t / kWorkSlots;
+  ++w.t;
+  return wait_sleep(&r.full[s], use & 1, abort_flag, err, kErrTimeoutSync) && work_answer(&r.answer[s], w);
+}
+// A whole warp: waits for the answer for item t > 0; whether there is such an item.
+__device__ __forceinline__ bool work_wait(WorkRing& r, int t, volatile uint32_t* abort_flag, uint32_t* err) {
+  const int s = (t - 1) % kWorkSlots, use = (t - 1) / kWorkSlots;
+  Work w;
+  return mbar_wait_warp<false>(&r.full[s], use & 1, abort_flag, err, kErrTimeoutSync) && work_answer(&r.answer[s], w);
 }
 // The warp is done with item t's answer.
 __device__ __forceinline__ void work_release(WorkRing& r, int t, int lane) {
@@ -114,30 +111,15 @@ __device__ __forceinline__ void work_release(WorkRing& r, int t, int lane) {
   __syncwarp();
   if (lane == 0) mbar_arrive(&r.empty[(t - 1) % kWorkSlots]);
 }
-// All three: w becomes the next item.
-__device__ __forceinline__ bool work_next(WorkRing& r, Work& w, int lane, volatile uint32_t* abort_flag, uint32_t* err) {
-  if (!work_wait(r, w.t + 1, abort_flag, err)) return false;
-  w = work_read(r, w.t + 1);
-  work_release(r, w.t, lane);
-  return true;
-}
-// After an abort: the request after item w, if it was made, has landed.
+// After an abort: the last request has landed.
 __device__ __forceinline__ void work_teardown(WorkRing& r, int requests) {
   if (requests > 0) mbar_wait_teardown(&r.full[(requests - 1) % kWorkSlots], ((requests - 1) / kWorkSlots) & 1);
 }
 
-// Whether work_wait(r, t) would return at once (the same for the whole warp).
-__device__ __forceinline__ bool work_ready(WorkRing& r, int t) {
-  const int s = (t - 1) % kWorkSlots, use = (t - 1) / kWorkSlots;
-  return __all_sync(0xffffffffu, mbar_try_wait<false>(&r.full[s], use & 1));
-}
-
-// The MMA warp's walk over the tile products of all items, each known before it is issued.
-// An item's last product must be issued whole before the warp waits for another item: the softmax
-// warps hold their place in the ring until their item's end, so that a walk over several empty
-// items would otherwise wait for an answer that is not asked for before they get on.
-enum : int { kUnknown = -1, kEnd = 0, kValid = 1, kFirst = 2, kLast = 4 };
-__device__ __forceinline__ int uniform(int x) { return __shfl_sync(0xffffffffu, x, 0); }   // the same for the whole warp, and known to be
+// An MMA warp's walk over the tile products of all items.  It waits for an item's answer only
+// after it has issued all of the item before: the softmax warps hold their place in the ring until
+// their item's end, and further answers are not asked for until they get on.
+enum : int { kEnd = 0, kValid = 1, kFirst = 2, kLast = 4 };
 template <class Item, class Make>
 struct Walk {
   Work w;
@@ -145,21 +127,20 @@ struct Walk {
   int j;       // that product's number within it, from 1
   Make make;
   __device__ __forceinline__ explicit Walk(Make m) : w(first_work()), item(m(w)), j(0), make(m) { settle(); }
-  // (tcgen05.mma takes its descriptors from uniform registers: what the loop turns on must be uniform)
+  // (tcgen05.mma takes its operands from uniform registers: what the loop turns on is made uniform)
   __device__ __forceinline__ void settle() {
-    item.n = uniform(item.n);
-    item.keys = uniform(item.keys);
+    item.n = __shfl_sync(0xffffffffu, item.n, 0);
+    item.keys = __shfl_sync(0xffffffffu, item.keys, 0);
   }
-  // The next product's flags; kEnd after the last.  With wait = false an answer that is not there
-  // yet, or a next item without products, is kUnknown.
-  __device__ __forceinline__ int next(bool wait, WorkRing& r, int lane, volatile uint32_t* abort_flag, uint32_t* err) {
+  // the next product's flags; kEnd after the last
+  __device__ __forceinline__ int next(WorkRing& r, int lane, volatile uint32_t* abort_flag, uint32_t* err) {
     while (j == item.n) {
-      if (!wait && !work_ready(r, w.t + 1)) return kUnknown;
-      if (!work_next(r, w, lane, abort_flag, err)) return kEnd;
+      if (!work_wait(r, w.t + 1, abort_flag, err)) return kEnd;
+      w = work_read(r, w.t + 1);
+      work_release(r, w.t, lane);
       item = make(w);
       settle();
       j = 0;
-      if (!wait && item.n == 0) return kUnknown;
     }
     ++j;
     return kValid | (j == 1 ? kFirst : 0) | (j == item.n ? kLast : 0);
@@ -172,10 +153,15 @@ __device__ __forceinline__ void load_tile(uint8_t* dst, const void* tmap, uint64
   tma_load_4d(dst + kHalfBytes, tmap, bar, 64, row, h, b);
 }
 
-// A tile's rows [first, 128) set to zero by one warp, for the tensor core: rows past a batch
-// entry's last key meet probabilities of zero in the products, but hold whatever the caller's
-// padding holds, and 0 * NaN is NaN.  (The swizzle permutes a row's 16-byte pieces within the
-// row, so whole rows are contiguous.)  Call after the tile has landed.
+// Rows past a batch entry's last key meet probabilities of zero in the products that sum over the
+// keys, but hold whatever the caller's padding holds, and 0 * NaN is NaN: in the tile where an item's
+// keys end they are set to zero in shared memory.  That is one warp's work: it waits for every
+// tile of the ring in turn, clears where it has to, and tells the MMA threads by the slot's barrier.
+// (The swizzle permutes a row's 16-byte pieces within the row, so whole rows are contiguous.)
+// How many of the rows of an item's last tile are keys; kTile: nothing to clear.
+__device__ __forceinline__ int last_rows(const Mask& m, int keys, int n) {
+  return keys < m.Sk && n * kTile > keys ? keys - (n - 1) * kTile : kTile;
+}
 __device__ __forceinline__ void clear_rows(uint8_t* tile, int first, int lane) {
   for (int at = first * 128 + lane * 16; at < kHalfBytes; at += 32 * 16) {
     *reinterpret_cast<uint4*>(tile + at) = make_uint4(0u, 0u, 0u, 0u);
@@ -183,6 +169,25 @@ __device__ __forceinline__ void clear_rows(uint8_t* tile, int first, int lane) {
   }
   fence_proxy_async_smem();
   __syncwarp();
+}
+template <int kRing, class Make>
+__device__ __forceinline__ void clear_warp(const Mask& m, Make make, WorkRing& work, uint8_t (*tiles)[kTileBytes],
+                                           uint64_t* full, uint64_t* cleared, int lane, volatile uint32_t* abort_flag,
+                                           uint32_t* err) {
+  int it = 0, turn = 0;
+  do {
+    const auto item = make(work_read(work, turn));
+    work_release(work, turn, lane);
+    for (int end = it + item.n; it != end; ++it) {
+      const int slot = it % kRing;
+      if (!mbar_wait_warp<true>(&full[slot], (it / kRing) & 1, abort_flag, err, kErrTimeoutTma)) return;
+      const int rows = it + 1 == end ? last_rows(m, item.keys, item.n) : kTile;
+      if (rows < kTile) {
+        clear_rows(tiles[slot], rows, lane);
+        if (lane == 0) mbar_arrive(&cleared[slot]);
+      }
+    }
+  } while (work_wait(work, ++turn, abort_flag, err));
 }
 
 // The low word of a tile's shared-memory descriptor (the high word is the same for all): the rows
@@ -196,6 +201,9 @@ __device__ __forceinline__ uint32_t desc_mn(const uint8_t* tile) {
 }
 __device__ __forceinline__ uint64_t desc_of(uint32_t lo) { return ((uint64_t)kDescHi << 32) | lo; }
 
+// The products are issued by one lane of a warp that runs the loop as a whole: its descriptors and
+// loop state are then uniform.  (Issued from a branch that one thread takes, each product took the
+// forward 115 cycles instead of 80.)
 // D = A B^T over the 128 channels of two tiles in shared memory (scores, and dO V^T).
 __device__ __forceinline__ void mma_tile_nt(uint32_t d, uint32_t a_desc_k, uint32_t b_desc_k, bool leader) {
   constexpr uint32_t idesc = idesc_f32acc(kFmtBF16, kFmtBF16, false, false, kTile, kTile);
