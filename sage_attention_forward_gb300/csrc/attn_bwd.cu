@@ -114,17 +114,22 @@ struct BwdParams {
   int H, group, BH;         // heads of this grid (Hkv, or Hq), Hq / Hkv, B * H
 };
 
+// Q(i) is held from S(i) to dK(i), most of two steps, and S(i+2) follows dK(i) closely: with two
+// slots the products waited for Q.
+constexpr int kQRing = 3, kDRing = 2;
+
 struct __align__(1024) SmemKV {
   uint8_t k[kTileBytes];
   uint8_t v[kTileBytes];
-  uint8_t q[2][kTileBytes];
-  uint8_t dout[2][kTileBytes];
+  uint8_t q[kQRing][kTileBytes];
+  uint8_t dout[kDRing][kTileBytes];
   alignas(16) float neg_lse2[2][kTile];
   alignas(16) float neg_delta[2][kTile];
   WorkRing work;
   uint64_t k_full, k_empty, v_full, v_empty;
-  uint64_t q_full[2], q_empty[2];   // Q with the row statistics
-  uint64_t d_full[2], d_empty[2];   // dO
+  uint64_t q_full[kQRing], q_empty[kQRing];
+  uint64_t d_full[kDRing], d_empty[kDRing];
+  uint64_t r_full[2], r_empty[2];   // the row statistics
   uint64_t s_full, dp_full;
   uint64_t p_full[2], ds_full[2];   // queries [0, 64) and [64, 128) of P^T, dS^T stored in TMEM (two warpgroups each)
   uint64_t acc_done;
@@ -160,8 +165,9 @@ __global__ void __launch_bounds__(kThreads, 1)
     dkdv_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
                 const __grid_constant__ CUtensorMap tm_v, const __grid_constant__ CUtensorMap tm_d,
                 const BwdParams p) {
-  extern __shared__ uint8_t smem_raw[];
-  SmemKV& sm = *reinterpret_cast<SmemKV*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  extern __shared__ __align__(1024) uint8_t smem_raw[];
+  SmemKV& sm = *reinterpret_cast<SmemKV*>(smem_raw);
+  if (smem_misaligned(smem_raw, &g_err_bwd)) return;
   const int warp = __shfl_sync(0xffffffffu, (int)(threadIdx.x >> 5), 0);   // (known to be uniform)
   const int lane = threadIdx.x & 31;
   volatile uint32_t* abort_flag = &sm.abort_flag;
@@ -173,11 +179,17 @@ __global__ void __launch_bounds__(kThreads, 1)
     mbar_init(&sm.k_empty, 1);
     mbar_init(&sm.v_full, 1);
     mbar_init(&sm.v_empty, 1);
-    for (int s = 0; s < 2; ++s) {
+    for (int s = 0; s < kQRing; ++s) {
       mbar_init(&sm.q_full[s], 1);
       mbar_init(&sm.q_empty[s], 1);
+    }
+    for (int s = 0; s < kDRing; ++s) {
       mbar_init(&sm.d_full[s], 1);
       mbar_init(&sm.d_empty[s], 1);
+    }
+    for (int s = 0; s < 2; ++s) {
+      mbar_init(&sm.r_full[s], 1);
+      mbar_init(&sm.r_empty[s], kWarpLoad);
       mbar_init(&sm.p_full[s], 2 * kGroups);
       mbar_init(&sm.ds_full[s], 2 * kGroups);
     }
@@ -205,7 +217,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       tma_prefetch_desc(&tm_k);
       tma_prefetch_desc(&tm_v);
       tma_prefetch_desc(&tm_d);
-      int it = 0, items = 0, requests = 0, q_issued = 0, d_issued = 0, k_issued = 0, v_issued = 0;
+      int it = 0, items = 0, requests = 0, q_issued = 0, d_issued = 0, r_issued = 0, k_issued = 0, v_issued = 0;
       auto load_item = [&](const ItemKV& i) -> bool {
         if (items > 0 && !wait_sleep(&sm.k_empty, (items - 1) & 1, abort_flag, err, kErrTimeoutSync)) return false;
         mbar_arrive_expect_tx(&sm.k_full, kTileBytes);
@@ -213,13 +225,10 @@ __global__ void __launch_bounds__(kThreads, 1)
         ++k_issued;
         int t = i.first, h = i.hk * p.group;
         for (int j = 0; j < i.n; ++j, ++it) {
-          const int slot = it & 1, use = it >> 1;
-          if (use > 0 && !wait_sleep(&sm.q_empty[slot], (use - 1) & 1, abort_flag, err, kErrTimeoutSync)) return false;
-          const long long at = ((long long)i.b * p.H * p.group + h) * p.Sq_pad + t * kTile;
-          mbar_arrive_expect_tx(&sm.q_full[slot], kTileBytes + 2 * kTile * 4);
-          load_tile(sm.q[slot], &tm_q, &sm.q_full[slot], t * kTile, h, i.b);
-          bulk_load(sm.neg_lse2[slot], p.neg_lse2 + at, kTile * 4, &sm.q_full[slot]);
-          bulk_load(sm.neg_delta[slot], p.neg_delta + at, kTile * 4, &sm.q_full[slot]);
+          const int qs = it % kQRing, qu = it / kQRing, ds = it % kDRing, du = it / kDRing, rs = it & 1, ru = it >> 1;
+          if (qu > 0 && !wait_sleep(&sm.q_empty[qs], (qu - 1) & 1, abort_flag, err, kErrTimeoutSync)) return false;
+          mbar_arrive_expect_tx(&sm.q_full[qs], kTileBytes);
+          load_tile(sm.q[qs], &tm_q, &sm.q_full[qs], t * kTile, h, i.b);
           ++q_issued;
           if (j == 0) {
             if (items > 0 && !wait_sleep(&sm.v_empty, (items - 1) & 1, abort_flag, err, kErrTimeoutSync)) return false;
@@ -227,10 +236,16 @@ __global__ void __launch_bounds__(kThreads, 1)
             load_tile(sm.v, &tm_v, &sm.v_full, i.key0, i.hk, i.b);
             ++v_issued;
           }
-          if (use > 0 && !wait_sleep(&sm.d_empty[slot], (use - 1) & 1, abort_flag, err, kErrTimeoutSync)) return false;
-          mbar_arrive_expect_tx(&sm.d_full[slot], kTileBytes);
-          load_tile(sm.dout[slot], &tm_d, &sm.d_full[slot], t * kTile, h, i.b);
+          if (du > 0 && !wait_sleep(&sm.d_empty[ds], (du - 1) & 1, abort_flag, err, kErrTimeoutSync)) return false;
+          mbar_arrive_expect_tx(&sm.d_full[ds], kTileBytes);
+          load_tile(sm.dout[ds], &tm_d, &sm.d_full[ds], t * kTile, h, i.b);
           ++d_issued;
+          if (ru > 0 && !wait_sleep(&sm.r_empty[rs], (ru - 1) & 1, abort_flag, err, kErrTimeoutSync)) return false;
+          const long long at = ((long long)i.b * p.H * p.group + h) * p.Sq_pad + t * kTile;
+          mbar_arrive_expect_tx(&sm.r_full[rs], 2 * kTile * 4);
+          bulk_load(sm.neg_lse2[rs], p.neg_lse2 + at, kTile * 4, &sm.r_full[rs]);
+          bulk_load(sm.neg_delta[rs], p.neg_delta + at, kTile * 4, &sm.r_full[rs]);
+          ++r_issued;
           if (++t == i.n_q) {
             t = i.first;
             ++h;
@@ -251,8 +266,11 @@ __global__ void __launch_bounds__(kThreads, 1)
         work_teardown(sm.work, requests);
         if (k_issued) mbar_wait_teardown(&sm.k_full, (k_issued - 1) & 1);
         if (v_issued) mbar_wait_teardown(&sm.v_full, (v_issued - 1) & 1);
-        for (int i = max(q_issued - 2, 0); i < q_issued; ++i) mbar_wait_teardown(&sm.q_full[i & 1], (i >> 1) & 1);
-        for (int i = max(d_issued - 2, 0); i < d_issued; ++i) mbar_wait_teardown(&sm.d_full[i & 1], (i >> 1) & 1);
+        for (int i = max(q_issued - kQRing, 0); i < q_issued; ++i)
+          mbar_wait_teardown(&sm.q_full[i % kQRing], (i / kQRing) & 1);
+        for (int i = max(d_issued - kDRing, 0); i < d_issued; ++i)
+          mbar_wait_teardown(&sm.d_full[i % kDRing], (i / kDRing) & 1);
+        for (int i = max(r_issued - 2, 0); i < r_issued; ++i) mbar_wait_teardown(&sm.r_full[i & 1], (i >> 1) & 1);
       }
     }
   } else if (warp == kWarpMma) {
@@ -271,20 +289,20 @@ __global__ void __launch_bounds__(kThreads, 1)
     Walk<ItemKV, decltype(make)> walk(make);
     int f0 = walk.next(sm.work, lane, abort_flag, err);
     // (a step's ring slots are compile-time constants, and so are the distances of its descriptors)
-    auto issue_s = [&](auto slot_c, int i, int flags) -> bool {
-      constexpr int slot = decltype(slot_c)::value;
+    auto issue_s = [&](auto u_c, int i, int flags) -> bool {
+      constexpr int slot = decltype(u_c)::value % kQRing;
       if ((flags & kFirst) && !wait_warp(&sm.k_full, k_items++ & 1, abort_flag, err, kErrTimeoutTma)) return false;
-      if (!wait_warp(&sm.q_full[slot], (i >> 1) & 1, abort_flag, err, kErrTimeoutTma)) return false;
+      if (!wait_warp(&sm.q_full[slot], (i / kQRing) & 1, abort_flag, err, kErrTimeoutTma)) return false;
       tc_fence_after();
       mma_tile_nt(tS, dk, dq + kDescTile * slot, leader);
       if (leader) mma_commit(&sm.s_full);
       if (leader && (flags & kLast)) mma_commit(&sm.k_empty);
       return true;
     };
-    auto issue_dp = [&](auto slot_c, int i, int flags) -> bool {
-      constexpr int slot = decltype(slot_c)::value;
+    auto issue_dp = [&](auto u_c, int i, int flags) -> bool {
+      constexpr int slot = decltype(u_c)::value % kDRing;
       if ((flags & kFirst) && !wait_warp(&sm.v_full, v_items++ & 1, abort_flag, err, kErrTimeoutTma)) return false;
-      if (!wait_warp(&sm.d_full[slot], (i >> 1) & 1, abort_flag, err, kErrTimeoutTma)) return false;
+      if (!wait_warp(&sm.d_full[slot], (i / kDRing) & 1, abort_flag, err, kErrTimeoutTma)) return false;
       tc_fence_after();
       mma_tile_nt(tDP, dv, dd + kDescTile * slot, leader);
       if (leader) mma_commit(&sm.dp_full);
@@ -303,27 +321,33 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       return true;
     };
-    auto step = [&](auto slot_c, auto next_c, int i) -> bool {
-      constexpr int slot = decltype(slot_c)::value;
+    constexpr int kCopies = kQRing * kDRing;
+    auto step = [&](auto u_c, int i) -> bool {
+      constexpr int u = decltype(u_c)::value, qs = u % kQRing, ds = u % kDRing;
+      const std::integral_constant<int, (u + 1) % kCopies> next_c;
       const bool last = f0 & kLast, first = f0 & kFirst;
       if (!last) f0 = walk.next(sm.work, lane, abort_flag, err);
-      if (!issue_acc(tDV, tS, sm.p_full, dd_mn + kDescTile * slot, i, first)) return false;
-      if (leader) mma_commit(&sm.d_empty[slot]);   // (dP(i) was issued before)
+      if (!issue_acc(tDV, tS, sm.p_full, dd_mn + kDescTile * ds, i, first)) return false;
+      if (leader) mma_commit(&sm.d_empty[ds]);   // (dP(i) was issued before)
       if (!last && !issue_s(next_c, i + 1, f0)) return false;
-      if (!issue_acc(tDK, tDP, sm.ds_full, dq_mn + kDescTile * slot, i, first)) return false;
-      if (leader) mma_commit(&sm.q_empty[slot]);
+      if (!issue_acc(tDK, tDP, sm.ds_full, dq_mn + kDescTile * qs, i, first)) return false;
+      if (leader) mma_commit(&sm.q_empty[qs]);
       if (!last) return issue_dp(next_c, i + 1, f0);
       if (leader) mma_commit(&sm.acc_done);
       f0 = walk.next(sm.work, lane, abort_flag, err);
       return f0 == kEnd || (issue_s(next_c, i + 1, f0) && issue_dp(next_c, i + 1, f0));
     };
     const std::integral_constant<int, 0> c0;
-    const std::integral_constant<int, 1> c1;
     bool ok = f0 == kEnd || (issue_s(c0, 0, f0) && issue_dp(c0, 0, f0));
-    for (int i = 0; ok && f0 != kEnd; i += 2) {
-      ok = step(c0, c1, i);
-      if (ok && f0 != kEnd) ok = step(c1, c0, i + 1);
+    for (int i = 0; ok && f0 != kEnd; i += kCopies) {
+      ok = step(c0, i);
+      if (ok && f0 != kEnd) ok = step(std::integral_constant<int, 1>(), i + 1);
+      if (ok && f0 != kEnd) ok = step(std::integral_constant<int, 2>(), i + 2);
+      if (ok && f0 != kEnd) ok = step(std::integral_constant<int, 3>(), i + 3);
+      if (ok && f0 != kEnd) ok = step(std::integral_constant<int, 4>(), i + 4);
+      if (ok && f0 != kEnd) ok = step(std::integral_constant<int, 5>(), i + 5);
     }
+    static_assert(kCopies == 6, "six copies of the step");
     if (leader) mma_commit(&sm.drain);
     mbar_wait_teardown(&sm.drain, 0);
   } else if (warp < kWarpLoad) {
@@ -351,10 +375,8 @@ __global__ void __launch_bounds__(kThreads, 1)
           const int c_min = p.mask.causal ? key - off - t * kTile - col : -kTile;
           const bool diag = __any_sync(0xffffffffu, c_min + 24 > 0);
           float pr[2][16];
-          // (the MMA warp waited for this tile's Q and statistics, but their bytes are visible to a
-          // thread only through its own wait)
-          ok = mbar_wait_warp<false>(&sm.s_full, it & 1, abort_flag, err, kErrTimeoutMma) &&
-               mbar_wait_warp<false>(&sm.q_full[slot], (it >> 1) & 1, abort_flag, err, kErrTimeoutTma);
+          ok = mbar_wait_warp<false>(&sm.r_full[slot], (it >> 1) & 1, abort_flag, err, kErrTimeoutTma) &&
+               mbar_wait_warp<false>(&sm.s_full, it & 1, abort_flag, err, kErrTimeoutMma);
           if (!ok) break;
           tc_fence_after();
           {
@@ -440,7 +462,10 @@ __global__ void __launch_bounds__(kThreads, 1)
             tmem_st_wait();
             tc_fence_before();
             __syncwarp();
-            if (lane == 0) mbar_arrive(&sm.ds_full[g >> 1]);
+            if (lane == 0) {
+              mbar_arrive(&sm.ds_full[g >> 1]);
+              mbar_arrive(&sm.r_empty[slot]);
+            }
           }
           if (++t == t_end) t = t_first;
         }
@@ -526,8 +551,9 @@ __device__ __forceinline__ ItemQ item_q(const BwdParams& p, const Work& w) {
 __global__ void __launch_bounds__(kThreads, 1)
     dq_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
               const __grid_constant__ CUtensorMap tm_v, const __grid_constant__ CUtensorMap tm_d, const BwdParams p) {
-  extern __shared__ uint8_t smem_raw[];
-  SmemQ& sm = *reinterpret_cast<SmemQ*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  extern __shared__ __align__(1024) uint8_t smem_raw[];
+  SmemQ& sm = *reinterpret_cast<SmemQ*>(smem_raw);
+  if (smem_misaligned(smem_raw, &g_err_bwd)) return;
   const int warp = __shfl_sync(0xffffffffu, (int)(threadIdx.x >> 5), 0);   // (known to be uniform)
   const int lane = threadIdx.x & 31;
   volatile uint32_t* abort_flag = &sm.abort_flag;
@@ -827,8 +853,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
 }
 
-constexpr int kSmemKV = (int)sizeof(SmemKV) + 1024;
-constexpr int kSmemQ = (int)sizeof(SmemQ) + 1024;
+constexpr int kSmemKV = (int)sizeof(SmemKV);
+constexpr int kSmemQ = (int)sizeof(SmemQ);
 static_assert(kSmemKV <= 232448 && kSmemQ <= 232448, "227 KB of shared memory per CTA");
 
 }  // namespace

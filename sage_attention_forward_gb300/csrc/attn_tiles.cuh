@@ -48,6 +48,14 @@ __device__ __forceinline__ bool wait_warp(uint64_t* bar, uint32_t parity, volati
   return __all_sync(0xffffffffu, ok);
 }
 
+// The tiles' 128-byte swizzle wants them on 1024-byte boundaries.  Dynamic shared memory declared so
+// starts on one; should it not, the kernel says so and does nothing (there is no room to move up in).
+__device__ __forceinline__ bool smem_misaligned(const uint8_t* smem, uint32_t* err_word) {
+  if ((smem_u32(smem) & 1023u) == 0) return false;
+  if (threadIdx.x == 0) atomicOr(err_word, kErrSmemBase);
+  return true;
+}
+
 // ------------------------------------------------------------------ work
 // The kernels launch one CTA per work item and run as many as there are SMs: a CTA that has the
 // answer takes over an item whose CTA has not started, so that barriers, TMEM and descriptors are

@@ -16,6 +16,7 @@ enum : uint32_t {
   kErrTimeoutTma = 1u << 0,   // a TMA transfer never completed
   kErrTimeoutMma = 1u << 1,   // an MMA commit never arrived
   kErrTimeoutSync = 1u << 2,  // a producer/consumer hand-off never arrived
+  kErrSmemBase = 1u << 3,     // shared memory does not start on the boundary that a kernel needs
   kErrCheckTmemMax = 1u << 8, // check builds only: a tcgen05.ld.red maximum disagreed with the loaded values
 };
 
