@@ -458,6 +458,48 @@ ATTN_API attn_status attn_bwd_bf16(const void* dout, const void* q, const void* 
                                    float softmax_scale, int causal, const int32_t* kv_len, void* workspace,
                                    size_t workspace_bytes, attn_stream_t stream);
 
+/* Element types of layer norm's tensors. */
+typedef enum { ATTN_BF16 = 0, ATTN_F16 = 1, ATTN_F32 = 2 } attn_dtype;
+
+/*
+ * layer_norm_fwd -- layer norm over the N channels of each of B * S * H rows: of the heads of Q and
+ * K before attention (N = 128, rows where a fused projection left them), or of tokens (H = 1).
+ *   mean = sum x / N,  rstd = 1 / sqrt(sum (x - mean)^2 / N + eps),  y = (x - mean) rstd weight + bias
+ *   x, y    : dtype [B, S, H, N], element strides x_str / y_str (batch, sequence, head), channel
+ *             stride 1.  Any stride and alignment of the type; 16-byte accesses are used where
+ *             pointers, strides and N allow them.  x may have strides of 0; y may be x itself.
+ *   weight, bias : w_dtype [N], each or NULL (1 and 0).  w_dtype is dtype or ATTN_F32.
+ *   mean, rstd : float [B, S, H] outputs, contiguous
+ *   eps     : finite, >= 0;  1 <= N <= 16384;  B * S * H <= 2^30 rows (0: nothing is done)
+ * Everything between x and y is FP32; y is rounded once.  Enqueues one kernel on `stream`.
+ */
+ATTN_API attn_status layer_norm_fwd(const void* x, const void* weight, const void* bias, void* y, float* mean,
+                                    float* rstd, int B, int S, int H, int N, const int64_t x_str[3],
+                                    const int64_t y_str[3], float eps, int dtype, int w_dtype, attn_stream_t stream);
+
+/* layer_norm_bwd_workspace_size -- bytes of device scratch layer_norm_bwd needs for dweight and dbias. */
+ATTN_API size_t layer_norm_bwd_workspace_size(int B, int S, int H, int N);
+
+/*
+ * layer_norm_bwd -- the gradients of layer_norm_fwd, with g = dy weight and xhat = (x - mean) rstd:
+ *   dx = rstd (g - sum g / N - xhat sum (g xhat) / N)
+ *   dweight = sum over rows of dy xhat,  dbias = sum over rows of dy
+ *   dy, x   : dtype [B, S, H, N], strides dy_str / x_str (strides of 0 allowed)
+ *   weight  : as given to the forward, or NULL
+ *   mean, rstd : as the forward wrote them
+ *   dx      : dtype [B, S, H, N] output, strides dx_str; may be dy itself
+ *   dweight, dbias : w_dtype [N] outputs, both or neither (zeros when there are no rows)
+ *   workspace : at least layer_norm_bwd_workspace_size(B, S, H, N) bytes, 16-byte aligned; may be
+ *             NULL when dweight and dbias are
+ * FP32 throughout, sums over rows in a fixed order (the same inputs give the same bits); each result is
+ * rounded once.  Enqueues one kernel on `stream`, two with dweight and dbias.
+ */
+ATTN_API attn_status layer_norm_bwd(const void* dy, const void* x, const void* weight, const float* mean,
+                                    const float* rstd, void* dx, void* dweight, void* dbias, int B, int S, int H,
+                                    int N, const int64_t dy_str[3], const int64_t x_str[3], const int64_t dx_str[3],
+                                    int dtype, int w_dtype, void* workspace, size_t workspace_bytes,
+                                    attn_stream_t stream);
+
 /*
  * attn_get_device_status -- synchronise `stream`, then read and clear the
  * device error words of all kernels.  ATTN_OK if no bounded wait ran out

@@ -13,6 +13,8 @@ library has not been built, every call raises.
     sage_attention(q, k, v, ...)      -> O                 (prepare + fwd)
     attn_fwd_bf16_lse(q, k, v, ...)   -> O, lse            (the forward for training)
     attn_bwd_bf16(dout, q, k, v, O, lse, ...) -> dQ, dK, dV
+    layer_norm_fwd(x, weight, bias)   -> y, mean, rstd
+    layer_norm_bwd(dy, x, weight, mean, rstd) -> dx, dweight, dbias
 """
 from __future__ import annotations
 
@@ -28,6 +30,7 @@ from .build import LIB as _LIB_PATH
 
 __all__ = ["AttnError", "attn_fwd_bf16", "sage_prepare", "sage_prepare_noalloc", "sage_attn_fwd", "sage_attention",
            "Prepared", "e4m3_encode", "attn_fwd_bf16_lse", "attn_bwd_bf16", "attn_bwd_workspace",
+           "layer_norm_fwd", "layer_norm_bwd", "layer_norm_bwd_workspace",
            "sage_padded_len", "attn_get_device_status", "lib", "STATUS"]
 
 STATUS = {0: "ATTN_OK", 1: "ATTN_ERR_INVALID_ARG", 2: "ATTN_ERR_ALIGNMENT", 3: "ATTN_ERR_UNSUPPORTED",
@@ -111,6 +114,12 @@ def lib() -> ctypes.CDLL:
         L.attn_bwd_bf16.argtypes = [_vp] * 9 + [i] * 6 + [_I64x3] * 8 + [ctypes.c_float, i, _vp, _vp,
                                                                        ctypes.c_size_t, _vp]
         L.attn_bwd_bf16.restype = i
+        L.layer_norm_fwd.argtypes = [_vp] * 6 + [i] * 4 + [_I64x3] * 2 + [ctypes.c_float, i, i, _vp]
+        L.layer_norm_fwd.restype = i
+        L.layer_norm_bwd_workspace_size.argtypes = [i] * 4
+        L.layer_norm_bwd_workspace_size.restype = ctypes.c_size_t
+        L.layer_norm_bwd.argtypes = [_vp] * 8 + [i] * 4 + [_I64x3] * 3 + [i, i, _vp, ctypes.c_size_t, _vp]
+        L.layer_norm_bwd.restype = i
         L.attn_get_device_status.argtypes = [_vp]
         L.attn_get_device_status.restype = i
         L.attn_last_error.argtypes = []
@@ -518,6 +527,115 @@ def attn_bwd_bf16(dout: torch.Tensor, q: torch.Tensor, k: torch.Tensor, v: torch
                                    int(causal), None if kv_len is None else kv_len.data_ptr(), workspace.data_ptr(),
                                    workspace.numel() * workspace.element_size(), st))
     return dq, dk, dv
+
+
+_DTYPES = {torch.bfloat16: 0, torch.float16: 1, torch.float32: 2}
+
+
+def _norm_rows(name: str, t: torch.Tensor, like: torch.Tensor | None = None):
+    """(B, S, H, N) and the (b, s, h) strides of rows [..., N] of up to four dimensions."""
+    if t.dim() < 1 or t.dim() > 4:
+        raise ValueError(f"{name} must have one to four dimensions, got {tuple(t.shape)}")
+    if t.dtype not in _DTYPES:
+        raise ValueError(f"{name} must be bfloat16, float16 or float32, got {t.dtype}")
+    if like is not None:
+        _shaped(name, t, like.shape, like.dtype)
+    if t.stride(-1) != 1 and t.shape[-1] > 1:
+        raise ValueError(f"{name} must have unit channel stride")
+    lead = 4 - t.dim()
+    shape = (1,) * lead + tuple(t.shape)
+    strides = (0,) * lead + tuple(t.stride())
+    return shape, _I64x3(*strides[:3])
+
+
+def _norm_weight(name: str, w: torch.Tensor | None, x: torch.Tensor) -> None:
+    if w is None:
+        return
+    if w.dtype not in (x.dtype, torch.float32) or tuple(w.shape) != (x.shape[-1],) or not w.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous [{x.shape[-1]}] tensor of {x.dtype} or float32, got "
+                         f"{tuple(w.shape)} {w.dtype}")
+
+
+def _norm_stat(name: str, t: torch.Tensor, x: torch.Tensor) -> None:
+    _shaped(name, t, x.shape[:-1], torch.float32)
+    if not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
+
+
+def _ptr(t):
+    return None if t is None else t.data_ptr()
+
+
+def layer_norm_fwd(x: torch.Tensor, weight: torch.Tensor | None = None, bias: torch.Tensor | None = None,
+                   eps: float = 1e-6, out: torch.Tensor | None = None, mean: torch.Tensor | None = None,
+                   rstd: torch.Tensor | None = None,
+                   stream=None) -> tuple[torch.Tensor, torch.Tensor, torch.Tensor]:
+    """Layer norm over the last dimension of rows [..., N] (up to four dimensions, any strides of the
+    others): (y, mean, rstd), mean and rstd float32 [...].  BF16, FP16 or FP32; weight and bias of x's type or
+    float32, each optional.  N up to 16384."""
+    (B, S, H, N), xs = _norm_rows("x", x)
+    _norm_weight("weight", weight, x)
+    _norm_weight("bias", bias, x)
+    w_type = next((t.dtype for t in (weight, bias) if t is not None), x.dtype)
+    if weight is not None and bias is not None and bias.dtype != weight.dtype:
+        raise ValueError(f"weight is {weight.dtype}, bias {bias.dtype}: one type for both")
+    with _call_stream(x, stream) as st:
+        if out is None:
+            out = torch.empty(x.shape, dtype=x.dtype, device=x.device)
+        if mean is None:
+            mean = torch.empty(x.shape[:-1], dtype=torch.float32, device=x.device)
+        if rstd is None:
+            rstd = torch.empty(x.shape[:-1], dtype=torch.float32, device=x.device)
+        _, ys = _norm_rows("out", out, x)
+        _norm_stat("mean", mean, x)
+        _norm_stat("rstd", rstd, x)
+        _same_device(x, weight=weight, bias=bias, out=out, mean=mean, rstd=rstd)
+        _check(lib().layer_norm_fwd(x.data_ptr(), _ptr(weight), _ptr(bias), out.data_ptr(), mean.data_ptr(),
+                                    rstd.data_ptr(), B, S, H, N, xs, ys, float(eps), _DTYPES[x.dtype],
+                                    _DTYPES[w_type], st))
+    return out, mean, rstd
+
+
+def layer_norm_bwd_workspace(x_shape, device) -> torch.Tensor:
+    shape = (1,) * (4 - len(x_shape)) + tuple(x_shape)
+    return torch.empty(int(lib().layer_norm_bwd_workspace_size(*shape)), dtype=torch.uint8, device=device)
+
+
+def layer_norm_bwd(dy: torch.Tensor, x: torch.Tensor, weight: torch.Tensor | None, mean: torch.Tensor,
+                   rstd: torch.Tensor, dx: torch.Tensor | None = None, dweight: torch.Tensor | None = None,
+                   dbias: torch.Tensor | None = None, workspace: torch.Tensor | None = None,
+                   stream=None) -> tuple[torch.Tensor, torch.Tensor | None, torch.Tensor | None]:
+    """(dx, dweight, dbias) of layer_norm_fwd; mean and rstd are what it returned.  dweight and dbias have the
+    weight's type and are None without a weight (unless both are passed in, in x's type or float32).  The same
+    inputs give the same bits."""
+    (B, S, H, N), xs = _norm_rows("x", x)
+    _, dys = _norm_rows("dy", dy, x)
+    _norm_weight("weight", weight, x)
+    _norm_stat("mean", mean, x)
+    _norm_stat("rstd", rstd, x)
+    if (dweight is None) != (dbias is None):
+        raise ValueError("dweight and dbias must both be given or both be None")
+    with _call_stream(x, stream) as st:
+        if dx is None:
+            dx = torch.empty(x.shape, dtype=x.dtype, device=x.device)
+        if dweight is None and weight is not None:
+            dweight, dbias = (torch.empty((N,), dtype=weight.dtype, device=x.device) for _ in range(2))
+        _norm_weight("dweight", dweight, x)
+        _norm_weight("dbias", dbias, x)
+        w_type = next((t.dtype for t in (weight, dweight) if t is not None), x.dtype)
+        if any(t is not None and t.dtype != w_type for t in (dweight, dbias)):
+            raise ValueError(f"dweight and dbias must be {w_type}")
+        if workspace is None and dweight is not None:
+            workspace = torch.empty(int(lib().layer_norm_bwd_workspace_size(B, S, H, N)), dtype=torch.uint8,
+                                    device=x.device)
+        _, dxs = _norm_rows("dx", dx, x)
+        _same_device(x, dy=dy, weight=weight, mean=mean, rstd=rstd, dx=dx, dweight=dweight, dbias=dbias,
+                     workspace=workspace)
+        _check(lib().layer_norm_bwd(dy.data_ptr(), x.data_ptr(), _ptr(weight), mean.data_ptr(), rstd.data_ptr(),
+                                    dx.data_ptr(), _ptr(dweight), _ptr(dbias), B, S, H, N, dys, xs, dxs,
+                                    _DTYPES[x.dtype], _DTYPES[w_type], _ptr(workspace),
+                                    0 if workspace is None else workspace.numel() * workspace.element_size(), st))
+    return dx, dweight, dbias
 
 
 def attn_selftest_wait_timeout(device=None, stream=None) -> str:

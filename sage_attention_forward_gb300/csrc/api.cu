@@ -820,6 +820,123 @@ attn_status attn_bwd_bf16(const void* dout, const void* q, const void* k, const 
   return ATTN_OK;
 }
 
+// ------------------------------------------------------------------ layer norm
+// Strides of [B, S, H, N] rows in whole elements; 0 (the same row again) only where a tensor is read.
+static attn_status check_rows(const char* name, const void* ptr, int type, const int64_t* in, const sa::LayerNormArgs& a,
+                              bool read, long long out[3]) {
+  if (ptr == nullptr) return fail(ATTN_ERR_INVALID_ARG, "%s is NULL", name);
+  if (reinterpret_cast<uintptr_t>(ptr) % (type == ATTN_F32 ? 4 : 2) != 0)
+    return fail(ATTN_ERR_ALIGNMENT, "%s is not aligned to its type", name);
+  if (in == nullptr) return fail(ATTN_ERR_INVALID_ARG, "%s strides are NULL", name);
+  const int ext[3] = {a.B, a.S, a.H};
+  for (int i = 0; i < 3; ++i) {
+    const long long s = ext[i] == 1 ? 0 : in[i];
+    if (s < 0 || (s == 0 && ext[i] > 1 && !read) || s >= (1ll << 38))
+      return fail(ATTN_ERR_INVALID_ARG, "%s stride %lld of dimension %d is out of range", name, (long long)in[i], i);
+    out[i] = s;
+  }
+  return ATTN_OK;
+}
+
+static attn_status check_norm(const void* x, const void* w, const void* b, float* mean, float* rstd, int B, int S,
+                              int H, int N, const int64_t* x_str, int type, int w_type, sa::LayerNormArgs& a,
+                              bool* empty) {
+  *empty = false;
+  if (type < ATTN_BF16 || type > ATTN_F32) return fail(ATTN_ERR_INVALID_ARG, "dtype=%d is none of attn_dtype", type);
+  if (w_type != type && w_type != ATTN_F32)
+    return fail(ATTN_ERR_INVALID_ARG, "w_dtype=%d must be the rows' type or ATTN_F32", w_type);
+  if (B < 0 || S < 0 || H < 0) return fail(ATTN_ERR_INVALID_ARG, "B=%d S=%d H=%d must be >= 0", B, S, H);
+  if (N < 1 || N > 16384) return fail(ATTN_ERR_INVALID_ARG, "N=%d must be in [1, 16384]", N);
+  // (no overflow: a factor that makes it too large ends the product)
+  const long long bs = (long long)B * S;
+  if (bs > (1ll << 30) || bs * H > (1ll << 30)) return fail(ATTN_ERR_INVALID_ARG, "B*S*H must be at most 2^30 rows");
+  a.B = B;
+  a.S = S;
+  a.H = H;
+  a.N = N;
+  a.type = type;
+  a.w_type = w_type;
+  a.x = x;
+  a.w = w;
+  a.b = b;
+  a.mean = mean;
+  a.rstd = rstd;
+  if (B == 0 || S == 0 || H == 0) {
+    *empty = true;
+    return ATTN_OK;
+  }
+  TRY(check_rows("x", x, type, x_str, a, true, a.x_str));
+  const uintptr_t w_align = w_type == ATTN_F32 ? 4 : 2;
+  if (reinterpret_cast<uintptr_t>(w) % w_align != 0 || reinterpret_cast<uintptr_t>(b) % w_align != 0)
+    return fail(ATTN_ERR_ALIGNMENT, "weight or bias is not aligned to its type");
+  if (mean == nullptr || rstd == nullptr) return fail(ATTN_ERR_INVALID_ARG, "mean or rstd is NULL");
+  if (reinterpret_cast<uintptr_t>(mean) % 4 != 0 || reinterpret_cast<uintptr_t>(rstd) % 4 != 0)
+    return fail(ATTN_ERR_ALIGNMENT, "mean or rstd is not 4-byte aligned");
+  return ATTN_OK;
+}
+
+attn_status layer_norm_fwd(const void* x, const void* weight, const void* bias, void* y, float* mean, float* rstd,
+                           int B, int S, int H, int N, const int64_t x_str[3], const int64_t y_str[3], float eps,
+                           int dtype, int w_dtype, attn_stream_t stream) {
+  bool empty = false;
+  sa::LayerNormArgs a;
+  if (!(eps >= 0.0f && std::isfinite(eps))) return fail(ATTN_ERR_INVALID_ARG, "eps must be finite and >= 0");
+  TRY(check_norm(x, weight, bias, mean, rstd, B, S, H, N, x_str, dtype, w_dtype, a, &empty));
+  if (empty) return ATTN_OK;
+  a.eps = eps;
+  long long ys[3];
+  TRY(check_rows("y", y, dtype, y_str, a, false, ys));
+  TRY(check_device());
+  cudaError_t e = sa::launch_layer_norm_fwd(a, y, ys, (cudaStream_t)stream);
+  if (e != cudaSuccess) return fail_cuda(e, "layer_norm_fwd launch");
+  return ATTN_OK;
+}
+
+size_t layer_norm_bwd_workspace_size(int B, int S, int H, int N) {
+  if (B < 1 || S < 1 || H < 1 || N < 1 || N > 16384) return 0;
+  const long long bs = (long long)B * S;
+  if (bs > (1ll << 30) || bs * H > (1ll << 30)) return 0;
+  return sa::layer_norm_bwd_workspace((int)(bs * H), N);
+}
+
+attn_status layer_norm_bwd(const void* dy, const void* x, const void* weight, const float* mean, const float* rstd,
+                           void* dx, void* dweight, void* dbias, int B, int S, int H, int N, const int64_t dy_str[3],
+                           const int64_t x_str[3], const int64_t dx_str[3], int dtype, int w_dtype, void* workspace,
+                           size_t workspace_bytes, attn_stream_t stream) {
+  bool empty = false;
+  sa::LayerNormArgs a;
+  TRY(check_norm(x, weight, nullptr, const_cast<float*>(mean), const_cast<float*>(rstd), B, S, H, N, x_str, dtype,
+                 w_dtype, a, &empty));
+  a.eps = 0.0f;
+  if ((dweight == nullptr) != (dbias == nullptr))
+    return fail(ATTN_ERR_INVALID_ARG, "dweight and dbias must both be given or both be NULL");
+  const uintptr_t w_size = w_dtype == ATTN_F32 ? 4 : 2;
+  if (reinterpret_cast<uintptr_t>(dweight) % w_size != 0 || reinterpret_cast<uintptr_t>(dbias) % w_size != 0)
+    return fail(ATTN_ERR_ALIGNMENT, "dweight or dbias is not aligned to its type");
+  if (empty) {   // sums over no rows
+    if (dweight == nullptr) return ATTN_OK;
+    TRY(check_device());
+    cudaError_t e = cudaMemsetAsync(dweight, 0, w_size * N, (cudaStream_t)stream);
+    if (e == cudaSuccess) e = cudaMemsetAsync(dbias, 0, w_size * N, (cudaStream_t)stream);
+    if (e != cudaSuccess) return fail_cuda(e, "layer_norm_bwd");
+    return ATTN_OK;
+  }
+  long long ds[3], xs[3];
+  TRY(check_rows("dy", dy, dtype, dy_str, a, true, ds));
+  TRY(check_rows("dx", dx, dtype, dx_str, a, false, xs));
+  if (dweight != nullptr) {
+    TRY(check_buffer("workspace", workspace));
+    const size_t need = layer_norm_bwd_workspace_size(B, S, H, N);
+    if (workspace_bytes < need)
+      return fail(ATTN_ERR_INVALID_ARG, "layer_norm_bwd: workspace_bytes=%zu < %zu required", workspace_bytes, need);
+  }
+  TRY(check_device());
+  cudaError_t e = sa::launch_layer_norm_bwd(a, dy, ds, dx, xs, dweight, dbias, reinterpret_cast<float*>(workspace),
+                                            (cudaStream_t)stream);
+  if (e != cudaSuccess) return fail_cuda(e, "layer_norm_bwd launch");
+  return ATTN_OK;
+}
+
 attn_status attn_selftest_wait_timeout(const void* q, const void* k, const void* v, void* o,
                                        attn_stream_t stream) {
   const int64_t st[3] = {128 * 128, 128, 128};   // [1, 128, 1, 128] contiguous

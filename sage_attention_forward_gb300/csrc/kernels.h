@@ -197,6 +197,23 @@ cudaError_t launch_attn_bwd_bf16(const CUtensorMap& tm_q, const CUtensorMap& tm_
                                  cudaStream_t stream);
 cudaError_t read_and_clear_err_bwd(uint32_t* out);
 
+// Layer norm (layer_norm.cu).  Types of x, dy and the results, and of the weights.
+enum : int { kBF16 = 0, kF16 = 1, kF32 = 2 };
+struct LayerNormArgs {
+  const void *x, *w, *b;      // w, b: or nullptr
+  float *mean, *rstd;
+  int B, S, H, N;
+  long long x_str[3];         // element strides (b, s, h)
+  int type, w_type;
+  float eps;
+};
+size_t layer_norm_bwd_workspace(int rows, int N);
+cudaError_t launch_layer_norm_fwd(const LayerNormArgs& a, void* y, const long long y_str[3], cudaStream_t stream);
+// dw, db: both or neither.
+cudaError_t launch_layer_norm_bwd(const LayerNormArgs& a, const void* dy, const long long dy_str[3], void* dx,
+                                  const long long dx_str[3], void* dw, void* db, float* workspace,
+                                  cudaStream_t stream);
+
 // Heads along grid.y and, beyond 65535 of them, grid.z.
 inline dim3 heads_grid(long long tiles, int heads) {
   const unsigned ny = (unsigned)(heads < 65535 ? heads : 65535);
