@@ -22,6 +22,7 @@ import contextlib
 import ctypes
 import math
 import os
+from array import array
 from dataclasses import dataclass
 
 import torch
@@ -107,18 +108,17 @@ def lib() -> ctypes.CDLL:
         L.attn_sm_clock_sample.restype = i
         L.sage_e4m3_encode.argtypes = [_vp, _vp, ctypes.c_int64, _vp]
         L.sage_e4m3_encode.restype = i
-        L.attn_fwd_bf16_lse.argtypes = [_vp] * 5 + [i] * 6 + [_I64x3] * 4 + [ctypes.c_float, i, _vp, _vp]
+        L.attn_fwd_bf16_lse.argtypes = [_vp] * 5 + [i] * 6 + [_vp] * 4 + [ctypes.c_float, i, _vp, _vp]
         L.attn_fwd_bf16_lse.restype = i
         L.attn_bwd_bf16_workspace_size.argtypes = [i] * 5
         L.attn_bwd_bf16_workspace_size.restype = ctypes.c_size_t
-        L.attn_bwd_bf16.argtypes = [_vp] * 9 + [i] * 6 + [_I64x3] * 8 + [ctypes.c_float, i, _vp, _vp,
-                                                                       ctypes.c_size_t, _vp]
+        L.attn_bwd_bf16.argtypes = [_vp] * 9 + [i] * 6 + [_vp] * 8 + [ctypes.c_float, i, _vp, _vp, ctypes.c_size_t, _vp]
         L.attn_bwd_bf16.restype = i
-        L.layer_norm_fwd.argtypes = [_vp] * 6 + [i] * 4 + [_I64x3] * 2 + [ctypes.c_float, i, i, _vp]
+        L.layer_norm_fwd.argtypes = [_vp] * 6 + [i] * 4 + [_vp] * 2 + [ctypes.c_float, i, i, _vp]
         L.layer_norm_fwd.restype = i
         L.layer_norm_bwd_workspace_size.argtypes = [i] * 4
         L.layer_norm_bwd_workspace_size.restype = ctypes.c_size_t
-        L.layer_norm_bwd.argtypes = [_vp] * 8 + [i] * 4 + [_I64x3] * 3 + [i, i, _vp, ctypes.c_size_t, _vp]
+        L.layer_norm_bwd.argtypes = [_vp] * 8 + [i] * 4 + [_vp] * 3 + [i, i, _vp, ctypes.c_size_t, _vp]
         L.layer_norm_bwd.restype = i
         L.attn_get_device_status.argtypes = [_vp]
         L.attn_get_device_status.restype = i
@@ -414,53 +414,86 @@ def sage_attention(q, k, v, softmax_scale=None, q_norm_w=None, k_norm_w=None, rm
     return out
 
 
+# The training calls are made in every layer of every step, small ones too: their checks are written to
+# take little time (shapes, types and devices compared as they come, strides handed over in one array).
+def _current_stream(dev: int) -> int:
+    return torch.cuda.current_stream(dev).cuda_stream
+
+
+# (the same without making a Stream object of it, 3 us a call, where torch has it)
+_current_stream = getattr(torch._C, "_cuda_getCurrentRawStream", _current_stream)
+
+
+def _elsewhere(dev: int, stream) -> bool:
+    """Whether the call is for another device or stream than the current ones."""
+    return stream is not None or dev != torch.cuda.current_device()
+
+
 @contextlib.contextmanager
-def _call_stream(t: torch.Tensor, stream):
-    """Makes t's device current and, when the caller names a stream, that stream: what the call
-    allocates then belongs to the stream its kernels run on.  Yields the stream's handle."""
-    if not t.is_cuda:
-        raise ValueError("tensors must be on a CUDA device")
-    with torch.cuda.device(t.device):
+def _there(dev: int, stream):
+    """Makes device `dev` and, when the caller names one, `stream` current: what the call allocates then
+    belongs to the stream that its kernels run on."""
+    with torch.cuda.device(dev):
         if stream is None:
-            yield torch.cuda.current_stream().cuda_stream
+            yield
         else:
             if not hasattr(stream, "cuda_stream"):
-                stream = torch.cuda.ExternalStream(int(stream), device=t.device)
+                stream = torch.cuda.ExternalStream(int(stream), device=dev)
             with torch.cuda.stream(stream):
-                yield stream.cuda_stream
+                yield
 
 
-def _same_device(ref: torch.Tensor, **tensors) -> None:
-    for name, t in tensors.items():
-        if t is not None and t.device != ref.device:
-            raise ValueError(f"{name} is on {t.device}, expected {ref.device}")
+def _cuda_index(name: str, t: torch.Tensor) -> int:
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be a CUDA tensor")
+    return t.get_device()
 
 
-def _shaped(name: str, t: torch.Tensor, shape, dtype) -> None:
-    if tuple(t.shape) != tuple(shape) or t.dtype != dtype:
+def _expect(name: str, t: torch.Tensor, shape, dtype, dev: int) -> None:
+    if t.shape != shape or t.dtype is not dtype:
         raise ValueError(f"{name} must be {tuple(shape)} {dtype}, got {tuple(t.shape)} {t.dtype}")
+    if t.get_device() != dev:
+        raise ValueError(f"{name} is on {t.device}, expected cuda:{dev}")
+
+
+def _expect_dense(name: str, t: torch.Tensor, shape, dtype, dev: int) -> None:
+    _expect(name, t, shape, dtype, dev)
+    if not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
+
+
+def _scratch(name: str, t: torch.Tensor, dev: int) -> int:
+    """Bytes of a workspace tensor."""
+    if t.get_device() != dev or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous tensor on cuda:{dev}")
+    return t.numel() * t.element_size()
+
+
+def _strides(names: str, *tensors: torch.Tensor) -> array:
+    """The tensors' four strides each, one after the other; the last of each must be 1."""
+    out = array("q")
+    for t in tensors:
+        out.extend(t.stride())
+    for at in range(3, len(out), 4):
+        if out[at] != 1:
+            raise ValueError(f"{names.split()[at // 4]} must have unit channel stride")
+    return out
 
 
 def _train_shapes(q, k, v, kv_len):
-    for name, t in (("q", q), ("k", k), ("v", v)):
-        if t.dim() != 4:
-            raise ValueError(f"{name} must be [B, S, H, D], got {tuple(t.shape)}")
+    if q.dim() != 4 or k.dim() != 4:
+        raise ValueError(f"q and k must be [B, S, H, D], got {tuple(q.shape)} and {tuple(k.shape)}")
     B, Sq, Hq, D = q.shape
-    Sk, Hkv = k.shape[1], k.shape[2]
-    _shaped("k", k, (B, Sk, Hkv, D), torch.bfloat16)
-    _shaped("v", v, (B, Sk, Hkv, D), torch.bfloat16)
+    _, Sk, Hkv, _ = k.shape
+    dev = _cuda_index("q", q)
+    if q.dtype is not torch.bfloat16:
+        raise ValueError(f"q must be bfloat16, got {q.dtype}")
+    keys = (B, Sk, Hkv, D)
+    _expect("k", k, keys, torch.bfloat16, dev)
+    _expect("v", v, keys, torch.bfloat16, dev)
     if kv_len is not None:
-        _shaped("kv_len", kv_len, (B,), torch.int32)
-        if not kv_len.is_contiguous():
-            raise ValueError("kv_len must be contiguous")
-    _same_device(q, k=k, v=v, kv_len=kv_len)
-    return B, Sq, Sk, Hq, Hkv, D
-
-
-def _lse_arg(lse, B, Hq, Sq):
-    _shaped("lse", lse, (B, Hq, Sq), torch.float32)
-    if not lse.is_contiguous():
-        raise ValueError("lse must be contiguous")
+        _expect_dense("kv_len", kv_len, (B,), torch.int32, dev)
+    return B, Sq, Sk, Hq, Hkv, D, dev
 
 
 def attn_fwd_bf16_lse(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, softmax_scale: float | None = None,
@@ -471,21 +504,25 @@ def attn_fwd_bf16_lse(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, softmax
     q [B, Sq, Hq, 128], k and v [B, Sk, Hkv, 128] with Hq a multiple of Hkv.  causal: query i sees the keys
     j <= i + Sk - Sq.  kv_len: int32 [B] on the device, each batch entry's number of keys (K and V past it
     may hold anything).  A row that sees no key has O = 0 and lse = -inf."""
-    B, Sq, Sk, Hq, Hkv, D = _train_shapes(q, k, v, kv_len)
-    if softmax_scale is None:
-        softmax_scale = 1.0 / math.sqrt(D)
-    with _call_stream(q, stream) as st:
-        if out is None:
-            out = torch.empty((B, Sq, Hq, D), dtype=torch.bfloat16, device=q.device)
-        if lse is None:
-            lse = torch.empty((B, Hq, Sq), dtype=torch.float32, device=q.device)
-        _shaped("out", out, (B, Sq, Hq, D), torch.bfloat16)
-        _lse_arg(lse, B, Hq, Sq)
-        _same_device(q, out=out, lse=lse)
-        _check(lib().attn_fwd_bf16_lse(q.data_ptr(), k.data_ptr(), v.data_ptr(), out.data_ptr(), lse.data_ptr(), B, Sq,
-                                       Sk, Hq, Hkv, D, _bshd("q", q), _bshd("k", k), _bshd("v", v), _bshd("out", out),
-                                       float(softmax_scale), int(causal), None if kv_len is None else kv_len.data_ptr(),
-                                       st))
+    B, Sq, Sk, Hq, Hkv, D, dev = _train_shapes(q, k, v, kv_len)
+    if _elsewhere(dev, stream):
+        with _there(dev, stream):
+            return attn_fwd_bf16_lse(q, k, v, softmax_scale, causal, kv_len, out, lse)
+    rows = (B, Hq, Sq)
+    if out is None:
+        out = q.new_empty(q.shape)
+    else:
+        _expect("out", out, q.shape, torch.bfloat16, dev)
+    if lse is None:
+        lse = q.new_empty(rows, dtype=torch.float32)
+    else:
+        _expect_dense("lse", lse, rows, torch.float32, dev)
+    strides = _strides("q k v out", q, k, v, out)
+    at = strides.buffer_info()[0]
+    _check(lib().attn_fwd_bf16_lse(q.data_ptr(), k.data_ptr(), v.data_ptr(), out.data_ptr(), lse.data_ptr(), B, Sq, Sk,
+                                   Hq, Hkv, D, at, at + 32, at + 64, at + 96,
+                                   D ** -0.5 if softmax_scale is None else softmax_scale, causal,
+                                   None if kv_len is None else kv_len.data_ptr(), _current_stream(dev)))
     return out, lse
 
 
@@ -501,69 +538,70 @@ def attn_bwd_bf16(dout: torch.Tensor, q: torch.Tensor, k: torch.Tensor, v: torch
     """(dQ, dK, dV) of attn_fwd_bf16_lse: dout is the gradient of its O; out and lse are what it returned,
     the other arguments those it was given.  dK and dV are sums over the query heads that share a key head.
     The same inputs give the same bits."""
-    B, Sq, Sk, Hq, Hkv, D = _train_shapes(q, k, v, kv_len)
-    if softmax_scale is None:
-        softmax_scale = 1.0 / math.sqrt(D)
-    _shaped("dout", dout, (B, Sq, Hq, D), torch.bfloat16)
-    _shaped("out", out, (B, Sq, Hq, D), torch.bfloat16)
-    _lse_arg(lse, B, Hq, Sq)
-    with _call_stream(q, stream) as st:
-        if dq is None:
-            dq = torch.empty((B, Sq, Hq, D), dtype=torch.bfloat16, device=q.device)
-        if dk is None:
-            dk = torch.empty((B, Sk, Hkv, D), dtype=torch.bfloat16, device=q.device)
-        if dv is None:
-            dv = torch.empty((B, Sk, Hkv, D), dtype=torch.bfloat16, device=q.device)
-        if workspace is None:
-            workspace = attn_bwd_workspace(B, Sq, Sk, Hq, Hkv, q.device)
-        _shaped("dq", dq, (B, Sq, Hq, D), torch.bfloat16)
-        _shaped("dk", dk, (B, Sk, Hkv, D), torch.bfloat16)
-        _shaped("dv", dv, (B, Sk, Hkv, D), torch.bfloat16)
-        _same_device(q, dout=dout, out=out, lse=lse, dq=dq, dk=dk, dv=dv, workspace=workspace)
-        _check(lib().attn_bwd_bf16(dout.data_ptr(), q.data_ptr(), k.data_ptr(), v.data_ptr(), out.data_ptr(),
-                                   lse.data_ptr(), dq.data_ptr(), dk.data_ptr(), dv.data_ptr(), B, Sq, Sk, Hq, Hkv, D,
-                                   _bshd("dout", dout), _bshd("q", q), _bshd("k", k), _bshd("v", v), _bshd("out", out),
-                                   _bshd("dq", dq), _bshd("dk", dk), _bshd("dv", dv), float(softmax_scale),
-                                   int(causal), None if kv_len is None else kv_len.data_ptr(), workspace.data_ptr(),
-                                   workspace.numel() * workspace.element_size(), st))
+    B, Sq, Sk, Hq, Hkv, D, dev = _train_shapes(q, k, v, kv_len)
+    if _elsewhere(dev, stream):
+        with _there(dev, stream):
+            return attn_bwd_bf16(dout, q, k, v, out, lse, softmax_scale, causal, kv_len, dq, dk, dv, workspace)
+    _expect("dout", dout, q.shape, torch.bfloat16, dev)
+    _expect("out", out, q.shape, torch.bfloat16, dev)
+    _expect_dense("lse", lse, (B, Hq, Sq), torch.float32, dev)
+    if dq is None:
+        dq = q.new_empty(q.shape)
+    else:
+        _expect("dq", dq, q.shape, torch.bfloat16, dev)
+    if dk is None:
+        dk = q.new_empty(k.shape)
+    else:
+        _expect("dk", dk, k.shape, torch.bfloat16, dev)
+    if dv is None:
+        dv = q.new_empty(k.shape)
+    else:
+        _expect("dv", dv, k.shape, torch.bfloat16, dev)
+    if workspace is None:
+        workspace = q.new_empty(int(lib().attn_bwd_bf16_workspace_size(B, Sq, Sk, Hq, Hkv)), dtype=torch.uint8)
+    strides = _strides("dout q k v out dq dk dv", dout, q, k, v, out, dq, dk, dv)
+    at = strides.buffer_info()[0]
+    _check(lib().attn_bwd_bf16(dout.data_ptr(), q.data_ptr(), k.data_ptr(), v.data_ptr(), out.data_ptr(),
+                               lse.data_ptr(), dq.data_ptr(), dk.data_ptr(), dv.data_ptr(), B, Sq, Sk, Hq, Hkv, D, at,
+                               at + 32, at + 64, at + 96, at + 128, at + 160, at + 192, at + 224,
+                               D ** -0.5 if softmax_scale is None else softmax_scale, causal,
+                               None if kv_len is None else kv_len.data_ptr(), workspace.data_ptr(),
+                               _scratch("workspace", workspace, dev), _current_stream(dev)))
     return dq, dk, dv
 
 
 _DTYPES = {torch.bfloat16: 0, torch.float16: 1, torch.float32: 2}
 
 
-def _norm_rows(name: str, t: torch.Tensor, like: torch.Tensor | None = None):
-    """(B, S, H, N) and the (b, s, h) strides of rows [..., N] of up to four dimensions."""
-    if t.dim() < 1 or t.dim() > 4:
-        raise ValueError(f"{name} must have one to four dimensions, got {tuple(t.shape)}")
-    if t.dtype not in _DTYPES:
-        raise ValueError(f"{name} must be bfloat16, float16 or float32, got {t.dtype}")
-    if like is not None:
-        _shaped(name, t, like.shape, like.dtype)
-    if t.stride(-1) != 1 and t.shape[-1] > 1:
-        raise ValueError(f"{name} must have unit channel stride")
-    lead = 4 - t.dim()
-    shape = (1,) * lead + tuple(t.shape)
-    strides = (0,) * lead + tuple(t.stride())
-    return shape, _I64x3(*strides[:3])
+def _norm_rows(x: torch.Tensor):
+    """B, S, H, N, the number of missing leading dimensions, and the device of rows [..., N]."""
+    dim = x.dim()
+    if dim < 1 or dim > 4:
+        raise ValueError(f"rows must have one to four dimensions, got {tuple(x.shape)}")
+    if x.dtype not in _DTYPES:
+        raise ValueError(f"rows must be bfloat16, float16 or float32, got {x.dtype}")
+    dev = _cuda_index("x", x)
+    return (1,) * (4 - dim) + tuple(x.shape), dev
 
 
-def _norm_weight(name: str, w: torch.Tensor | None, x: torch.Tensor) -> None:
-    if w is None:
-        return
-    if w.dtype not in (x.dtype, torch.float32) or tuple(w.shape) != (x.shape[-1],) or not w.is_contiguous():
-        raise ValueError(f"{name} must be a contiguous [{x.shape[-1]}] tensor of {x.dtype} or float32, got "
-                         f"{tuple(w.shape)} {w.dtype}")
+def _norm_strides(names: str, *tensors: torch.Tensor) -> array:
+    """As _strides, for tensors of one to four dimensions; a single channel may have any stride."""
+    out = array("q")
+    for name, t in zip(names.split(), tensors):
+        st = t.stride()
+        if st[-1] != 1 and t.shape[-1] > 1:
+            raise ValueError(f"{name} must have unit channel stride")
+        for _ in range(4 - len(st)):
+            out.append(0)
+        out.extend(st)
+    return out
 
 
-def _norm_stat(name: str, t: torch.Tensor, x: torch.Tensor) -> None:
-    _shaped(name, t, x.shape[:-1], torch.float32)
-    if not t.is_contiguous():
-        raise ValueError(f"{name} must be contiguous")
-
-
-def _ptr(t):
-    return None if t is None else t.data_ptr()
+def _norm_weight(name: str, w: torch.Tensor, x: torch.Tensor, dev: int, dtype=None) -> None:
+    """w is [N] of x's type or float32 (or of the type given)."""
+    if dtype is None:
+        dtype = torch.float32 if w.dtype is torch.float32 else x.dtype
+    _expect_dense(name, w, x.shape[-1:], dtype, dev)
 
 
 def layer_norm_fwd(x: torch.Tensor, weight: torch.Tensor | None = None, bias: torch.Tensor | None = None,
@@ -573,26 +611,36 @@ def layer_norm_fwd(x: torch.Tensor, weight: torch.Tensor | None = None, bias: to
     """Layer norm over the last dimension of rows [..., N] (up to four dimensions, any strides of the
     others): (y, mean, rstd), mean and rstd float32 [...].  BF16, FP16 or FP32; weight and bias of x's type or
     float32, each optional.  N up to 16384."""
-    (B, S, H, N), xs = _norm_rows("x", x)
-    _norm_weight("weight", weight, x)
-    _norm_weight("bias", bias, x)
-    w_type = next((t.dtype for t in (weight, bias) if t is not None), x.dtype)
-    if weight is not None and bias is not None and bias.dtype != weight.dtype:
-        raise ValueError(f"weight is {weight.dtype}, bias {bias.dtype}: one type for both")
-    with _call_stream(x, stream) as st:
-        if out is None:
-            out = torch.empty(x.shape, dtype=x.dtype, device=x.device)
-        if mean is None:
-            mean = torch.empty(x.shape[:-1], dtype=torch.float32, device=x.device)
-        if rstd is None:
-            rstd = torch.empty(x.shape[:-1], dtype=torch.float32, device=x.device)
-        _, ys = _norm_rows("out", out, x)
-        _norm_stat("mean", mean, x)
-        _norm_stat("rstd", rstd, x)
-        _same_device(x, weight=weight, bias=bias, out=out, mean=mean, rstd=rstd)
-        _check(lib().layer_norm_fwd(x.data_ptr(), _ptr(weight), _ptr(bias), out.data_ptr(), mean.data_ptr(),
-                                    rstd.data_ptr(), B, S, H, N, xs, ys, float(eps), _DTYPES[x.dtype],
-                                    _DTYPES[w_type], st))
+    shape, dev = _norm_rows(x)
+    if _elsewhere(dev, stream):
+        with _there(dev, stream):
+            return layer_norm_fwd(x, weight, bias, eps, out, mean, rstd)
+    w_type = x.dtype
+    if weight is not None:
+        _norm_weight("weight", weight, x, dev)
+        w_type = weight.dtype
+    if bias is not None:
+        _norm_weight("bias", bias, x, dev, None if weight is None else w_type)
+        w_type = bias.dtype
+    stats = x.shape[:-1]
+    if out is None:
+        out = x.new_empty(x.shape)
+    else:
+        _expect("out", out, x.shape, x.dtype, dev)
+    if mean is None:
+        mean = x.new_empty(stats, dtype=torch.float32)
+    else:
+        _expect_dense("mean", mean, stats, torch.float32, dev)
+    if rstd is None:
+        rstd = x.new_empty(stats, dtype=torch.float32)
+    else:
+        _expect_dense("rstd", rstd, stats, torch.float32, dev)
+    strides = _norm_strides("x out", x, out)
+    at = strides.buffer_info()[0]
+    _check(lib().layer_norm_fwd(x.data_ptr(), None if weight is None else weight.data_ptr(),
+                                None if bias is None else bias.data_ptr(), out.data_ptr(), mean.data_ptr(),
+                                rstd.data_ptr(), *shape, at, at + 32, eps, _DTYPES[x.dtype], _DTYPES[w_type],
+                                _current_stream(dev)))
     return out, mean, rstd
 
 
@@ -608,33 +656,43 @@ def layer_norm_bwd(dy: torch.Tensor, x: torch.Tensor, weight: torch.Tensor | Non
     """(dx, dweight, dbias) of layer_norm_fwd; mean and rstd are what it returned.  dweight and dbias have the
     weight's type and are None without a weight (unless both are passed in, in x's type or float32).  The same
     inputs give the same bits."""
-    (B, S, H, N), xs = _norm_rows("x", x)
-    _, dys = _norm_rows("dy", dy, x)
-    _norm_weight("weight", weight, x)
-    _norm_stat("mean", mean, x)
-    _norm_stat("rstd", rstd, x)
+    shape, dev = _norm_rows(x)
+    if _elsewhere(dev, stream):
+        with _there(dev, stream):
+            return layer_norm_bwd(dy, x, weight, mean, rstd, dx, dweight, dbias, workspace)
+    _expect("dy", dy, x.shape, x.dtype, dev)
+    stats = x.shape[:-1]
+    _expect_dense("mean", mean, stats, torch.float32, dev)
+    _expect_dense("rstd", rstd, stats, torch.float32, dev)
     if (dweight is None) != (dbias is None):
         raise ValueError("dweight and dbias must both be given or both be None")
-    with _call_stream(x, stream) as st:
-        if dx is None:
-            dx = torch.empty(x.shape, dtype=x.dtype, device=x.device)
-        if dweight is None and weight is not None:
-            dweight, dbias = (torch.empty((N,), dtype=weight.dtype, device=x.device) for _ in range(2))
-        _norm_weight("dweight", dweight, x)
-        _norm_weight("dbias", dbias, x)
-        w_type = next((t.dtype for t in (weight, dweight) if t is not None), x.dtype)
-        if any(t is not None and t.dtype != w_type for t in (dweight, dbias)):
-            raise ValueError(f"dweight and dbias must be {w_type}")
-        if workspace is None and dweight is not None:
-            workspace = torch.empty(int(lib().layer_norm_bwd_workspace_size(B, S, H, N)), dtype=torch.uint8,
-                                    device=x.device)
-        _, dxs = _norm_rows("dx", dx, x)
-        _same_device(x, dy=dy, weight=weight, mean=mean, rstd=rstd, dx=dx, dweight=dweight, dbias=dbias,
-                     workspace=workspace)
-        _check(lib().layer_norm_bwd(dy.data_ptr(), x.data_ptr(), _ptr(weight), mean.data_ptr(), rstd.data_ptr(),
-                                    dx.data_ptr(), _ptr(dweight), _ptr(dbias), B, S, H, N, dys, xs, dxs,
-                                    _DTYPES[x.dtype], _DTYPES[w_type], _ptr(workspace),
-                                    0 if workspace is None else workspace.numel() * workspace.element_size(), st))
+    w_type = x.dtype
+    if weight is not None:
+        _norm_weight("weight", weight, x, dev)
+        w_type = weight.dtype
+    if dweight is not None:
+        _norm_weight("dweight", dweight, x, dev, None if weight is None else w_type)
+        w_type = dweight.dtype
+        _norm_weight("dbias", dbias, x, dev, w_type)
+    elif weight is not None:
+        dweight, dbias = weight.new_empty(shape[3:]), weight.new_empty(shape[3:])
+    if dx is None:
+        dx = x.new_empty(x.shape)
+    else:
+        _expect("dx", dx, x.shape, x.dtype, dev)
+    size = 0
+    if dweight is not None:
+        if workspace is None:
+            workspace = x.new_empty(int(lib().layer_norm_bwd_workspace_size(*shape)), dtype=torch.uint8)
+        size = _scratch("workspace", workspace, dev)
+    strides = _norm_strides("dy x dx", dy, x, dx)
+    at = strides.buffer_info()[0]
+    _check(lib().layer_norm_bwd(dy.data_ptr(), x.data_ptr(), None if weight is None else weight.data_ptr(),
+                                mean.data_ptr(), rstd.data_ptr(), dx.data_ptr(),
+                                None if dweight is None else dweight.data_ptr(),
+                                None if dbias is None else dbias.data_ptr(), *shape, at, at + 32, at + 64,
+                                _DTYPES[x.dtype], _DTYPES[w_type], workspace.data_ptr() if size else None, size,
+                                _current_stream(dev)))
     return dx, dweight, dbias
 
 

@@ -965,16 +965,17 @@ attn_status attn_get_device_status(attn_stream_t stream) {
   cudaError_t e = cudaStreamSynchronize((cudaStream_t)stream);
   if (e != cudaSuccess) return fail_cuda(e, "cudaStreamSynchronize");
   // one word per translation unit with such kernels
-  uint32_t w = 0, lse = 0, bwd = 0;
+  uint32_t w = 0, lse = 0, bwd = 0, norm = 0;
   e = sa::read_and_clear_err_attn(&w);
   if (e == cudaSuccess) e = sa::read_and_clear_err_lse(&lse);
   if (e == cudaSuccess) e = sa::read_and_clear_err_bwd(&bwd);
+  if (e == cudaSuccess) e = sa::read_and_clear_err_norm(&norm);
   if (e != cudaSuccess) return fail_cuda(e, "reading the device error word");
-  w |= lse | bwd;
+  w |= lse | bwd | norm;
   if (w)
     return fail(ATTN_ERR_DEVICE_TIMEOUT,
-                "an attention kernel gave up on a bounded wait (bits 0x%x: 1 TMA load, 2 MMA commit, 4 hand-off; "
-                "0x100 a check build's TMEM-maximum mismatch)", w);
+                "a kernel gave up on a bounded wait (bits 0x%x: 1 TMA load, 2 MMA commit, 4 hand-off, 8 shared memory "
+                "base; 0x100 a check build's TMEM-maximum mismatch)", w);
   return ATTN_OK;
 }
 

@@ -208,6 +208,7 @@ struct LayerNormArgs {
   float eps;
 };
 size_t layer_norm_bwd_workspace(int rows, int N);
+cudaError_t read_and_clear_err_norm(uint32_t* out);
 cudaError_t launch_layer_norm_fwd(const LayerNormArgs& a, void* y, const long long y_str[3], cudaStream_t stream);
 // dw, db: both or neither.
 cudaError_t launch_layer_norm_bwd(const LayerNormArgs& a, const void* dy, const long long dy_str[3], void* dx,

@@ -8,8 +8,8 @@
 // Both directions are bound by memory: the forward reads x and writes y, the backward reads x and
 // dy and writes dx, once each.  A row is held in registers, in 32 bits, between its statistics (two
 // passes over the registers, so that no square of a large mean is subtracted) and its result.
-// Rows of up to 512 channels take 4 to 32 lanes of a warp, 16 channels a lane; longer ones a CTA,
-// 16 channels a thread (32 above 8192).  CTAs walk over the rows: while a row is worked on the
+// Rows of up to 512 channels (256 in the backward) take 4 to 32 lanes of a warp, 16 (8) channels a lane;
+// longer ones a CTA, 16 channels a thread (32 above 8192).  CTAs walk over the rows: while a row is worked on the
 // next one's loads are under way, and in the backward pass a thread keeps the sums of dw and db
 // of its own channels in registers over all of its rows.  Each CTA writes its sums once to the
 // workspace, and a second kernel adds them up, in one fixed order: no atomics, the same bits every time.
@@ -26,20 +26,35 @@ namespace {
 struct Rows {
   long long str[3];   // element strides (b, s, h)
 };
+// n / d for n < 2^31 by a product (Granlund and Montgomery, "Division by invariant integers using
+// multiplication", 1994): d <= 2^shift, mul = ceil(2^(32 + shift) / d) - 2^32.
+struct Div {
+  uint32_t d, mul, shift;
+};
+Div make_div(int d) {
+  Div r = {(uint32_t)d, 0, 0};
+  while ((1ll << r.shift) < d) ++r.shift;
+  r.mul = (uint32_t)(((1ull << 32) * ((1ull << r.shift) - (uint64_t)d)) / (uint64_t)d + 1);
+  return r;
+}
+__device__ __forceinline__ int div_by(int n, const Div& d) {
+  return (int)((__umulhi((uint32_t)n, d.mul) + (uint32_t)n) >> d.shift);
+}
 struct LnParams {
   const void *x, *dy, *w, *b;
   void *y, *dx;
   float *mean, *rstd;             // outputs of the forward, inputs of the backward
   Rows xs, ys, dys, dxs;
-  int rows, S, H, N;
+  int rows, N;
+  Div S, H;
   float eps;
   int w_type;                     // type of w and b
   float* partial;                 // backward: [2][CTAs][N] sums of dw and db, or nullptr
 };
 
 __device__ __forceinline__ long long row_at(const LnParams& p, const Rows& r, int row) {
-  const int h = row % p.H, bs = row / p.H;
-  return (long long)(bs / p.S) * r.str[0] + (long long)(bs % p.S) * r.str[1] + (long long)h * r.str[2];
+  const int bs = div_by(row, p.H), h = row - bs * (int)p.H.d, b = div_by(bs, p.S), s = bs - b * (int)p.S.d;
+  return (long long)b * r.str[0] + (long long)s * r.str[1] + (long long)h * r.str[2];
 }
 
 template <class T>
@@ -47,18 +62,6 @@ struct Piece {   // 16 bytes
   static constexpr int kN = 16 / sizeof(T);
   T v[kN];
 };
-__device__ __forceinline__ float to_float(float x) { return x; }
-__device__ __forceinline__ float to_float(__half x) { return __half2float(x); }
-__device__ __forceinline__ float to_float(__nv_bfloat16 x) { return __bfloat162float(x); }
-template <class T>
-__device__ __forceinline__ T from_float(float x);
-template <>
-__device__ __forceinline__ float from_float(float x) { return x; }
-template <>
-__device__ __forceinline__ __half from_float(float x) { return __float2half_rn(x); }
-template <>
-__device__ __forceinline__ __nv_bfloat16 from_float(float x) { return __float2bfloat16_rn(x); }
-
 // The piece of channels [c, c + kN) of a row; channels past N are 0.  kVec: rows, strides and weights
 // allow 16-byte accesses, and N is a whole number of pieces.
 template <bool kVec, class T>
@@ -72,25 +75,45 @@ __device__ __forceinline__ uint4 load_piece(const T* row, int c, const LnParams&
     if (c + e < p.N) t.v[e] = row[c + e];
   return *reinterpret_cast<uint4*>(&t);
 }
+__device__ __forceinline__ void unpack_word(uint32_t w, float* x, __nv_bfloat16) {
+  x[0] = __uint_as_float(w << 16);
+  x[1] = __uint_as_float(w & 0xffff0000u);
+}
+__device__ __forceinline__ void unpack_word(uint32_t w, float* x, __half) {
+  const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&w));
+  x[0] = f.x;
+  x[1] = f.y;
+}
+__device__ __forceinline__ void unpack_word(uint32_t w, float* x, float) { x[0] = __uint_as_float(w); }
+template <class T>
+__device__ __forceinline__ void unpack(const uint4& raw, float* x) {
+  const uint32_t w[4] = {raw.x, raw.y, raw.z, raw.w};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) unpack_word(w[i], x + i * (4 / sizeof(T)), T());
+}
+__device__ __forceinline__ uint32_t pack_word(const float* x, __nv_bfloat16) { return pack_bf16x2(x[0], x[1]); }
+__device__ __forceinline__ uint32_t pack_word(const float* x, __half) {
+  const __half2 h = __floats2half2_rn(x[0], x[1]);
+  return *reinterpret_cast<const uint32_t*>(&h);
+}
+__device__ __forceinline__ uint32_t pack_word(const float* x, float) { return __float_as_uint(x[0]); }
+template <class T>
+__device__ __forceinline__ uint4 pack(const float* x) {
+  constexpr int k = 4 / sizeof(T);
+  return make_uint4(pack_word(x, T()), pack_word(x + k, T()), pack_word(x + 2 * k, T()), pack_word(x + 3 * k, T()));
+}
 template <bool kVec, class T>
 __device__ __forceinline__ void store_piece(T* row, int c, const float* x, const LnParams& p) {
   if (c >= p.N) return;
-  Piece<T> t;
-#pragma unroll
-  for (int e = 0; e < Piece<T>::kN; ++e) t.v[e] = from_float<T>(x[e]);
+  const uint4 raw = pack<T>(x);
   if (kVec) {
-    __stcs(reinterpret_cast<uint4*>(row + c), *reinterpret_cast<uint4*>(&t));
+    __stcs(reinterpret_cast<uint4*>(row + c), raw);
     return;
   }
+  const Piece<T> t = *reinterpret_cast<const Piece<T>*>(&raw);
 #pragma unroll
   for (int e = 0; e < Piece<T>::kN; ++e)
     if (c + e < p.N) row[c + e] = t.v[e];
-}
-template <class T>
-__device__ __forceinline__ void unpack(const uint4& raw, float* x) {
-  const Piece<T> t = *reinterpret_cast<const Piece<T>*>(&raw);
-#pragma unroll
-  for (int e = 0; e < Piece<T>::kN; ++e) x[e] = to_float(t.v[e]);
 }
 // kN weights (or biases) from channel c on; `other` where there are none.
 template <bool kVec, int kN>
@@ -175,6 +198,15 @@ __global__ void __launch_bounds__(kMax) ln_fwd_kernel(const LnParams p) {
   const int lane = S::lane(), step = S::step();
   int row = S::first(), turn = 0;
   const float inv_n = 1.0f / (float)p.N;
+  constexpr bool kHold = kValues <= 16;   // weights in registers, or again from L1 for each row
+  float w[kHold ? kValues : 1], b[kHold ? kValues : 1];
+  if (kHold) {
+#pragma unroll
+    for (int k = 0; k < kPieces; ++k) {
+      load_weights<kVec, kN>(p.w, (lane + k * S::width()) * kN, 1.0f, p, &w[kHold ? k * kN : 0]);
+      load_weights<kVec, kN>(p.b, (lane + k * S::width()) * kN, 0.0f, p, &b[kHold ? k * kN : 0]);
+    }
+  }
   uint4 raw[kPieces];
   auto load = [&](int r) {
     const T* x = reinterpret_cast<const T*>(p.x) + (r < p.rows ? row_at(p, p.xs, r) : 0);
@@ -191,20 +223,29 @@ __global__ void __launch_bounds__(kMax) ln_fwd_kernel(const LnParams p) {
 #pragma unroll
     for (int k = 0; k < kPieces; ++k) unpack<T>(raw[k], v + k * kN);
     load(row + step);
-    float sum[1] = {0.0f};
+    float sum[1], sum2[2] = {0.0f, 0.0f};
 #pragma unroll
-    for (int i = 0; i < kValues; ++i) sum[0] += v[i];   // (channels past N are 0)
+    for (int i = 0; i < kValues; i += 2) fadd2(sum2[0], sum2[1], sum2[0], sum2[1], v[i], v[i + 1]);   // (channels past N are 0)
+    sum[0] = sum2[0] + sum2[1];
     row_sums<kLanes>(sum, scratch, turn);
     const float mean = sum[0] * inv_n;
-    float sq[1] = {0.0f};
+    float sq[1], sq2[2] = {0.0f, 0.0f};
 #pragma unroll
-    for (int k = 0; k < kPieces; ++k)
+    for (int k = 0; k < kPieces; ++k) {
+      const int c = (lane + k * S::width()) * kN;
 #pragma unroll
-      for (int e = 0; e < kN; ++e) {
-        const bool in = (lane + k * S::width()) * kN + e < p.N;
-        v[k * kN + e] = in ? v[k * kN + e] - mean : 0.0f;
-        sq[0] = fmaf(v[k * kN + e], v[k * kN + e], sq[0]);
+      for (int e = k * kN; e < (k + 1) * kN; e += 2) {
+        fadd2(v[e], v[e + 1], v[e], v[e + 1], -mean, -mean);
+        if (!kVec) {
+          v[e] = c + e - k * kN < p.N ? v[e] : 0.0f;
+          v[e + 1] = c + e + 1 - k * kN < p.N ? v[e + 1] : 0.0f;
+        }
       }
+      if (kVec && c >= p.N) continue;
+#pragma unroll
+      for (int e = k * kN; e < (k + 1) * kN; e += 2) ffma2(sq2[0], sq2[1], v[e], v[e + 1], v[e], v[e + 1], sq2[0], sq2[1]);
+    }
+    sq[0] = sq2[0] + sq2[1];
     row_sums<kLanes>(sq, scratch, turn);
     const float rstd = 1.0f / sqrtf(sq[0] * inv_n + p.eps);
     if (row < p.rows) {
@@ -212,11 +253,17 @@ __global__ void __launch_bounds__(kMax) ln_fwd_kernel(const LnParams p) {
 #pragma unroll
       for (int k = 0; k < kPieces; ++k) {
         const int c = (lane + k * S::width()) * kN;
-        float ww[kN], bb[kN], out[kN];
-        load_weights<kVec, kN>(p.w, c, 1.0f, p, ww);   // (from L1: registers for them would halve the rows in flight)
-        load_weights<kVec, kN>(p.b, c, 0.0f, p, bb);
+        float ww[kHold ? 1 : kN], bb[kHold ? 1 : kN], out[kN];
+        if (!kHold) {
+          load_weights<kVec, kN>(p.w, c, 1.0f, p, ww);
+          load_weights<kVec, kN>(p.b, c, 0.0f, p, bb);
+        }
+        const float *pw = kHold ? &w[kHold ? k * kN : 0] : ww, *pb = kHold ? &b[kHold ? k * kN : 0] : bb;
 #pragma unroll
-        for (int e = 0; e < kN; ++e) out[e] = fmaf(v[k * kN + e] * rstd, ww[e], bb[e]);
+        for (int e = 0; e < kN; e += 2) {
+          fmul2(out[e], out[e + 1], v[k * kN + e], v[k * kN + e + 1], rstd, rstd);
+          ffma2(out[e], out[e + 1], out[e], out[e + 1], pw[e], pw[e + 1], pb[e], pb[e + 1]);
+        }
         store_piece<kVec, T>(y, c, out, p);
       }
       if (lane == 0) {
@@ -231,8 +278,8 @@ template <class T, bool kVec, int kLanes, int kValues, int kMax>
 __global__ void __launch_bounds__(kMax) ln_bwd_kernel(const LnParams p) {
   using S = Spread<kLanes>;
   constexpr int kN = Piece<T>::kN, kPieces = kValues / kN;
-  // the next row's loads are under way while a row is worked on; not with 32 channels a thread,
-  // where the registers do not reach
+  // the next row's loads are under way while a row is worked on; not with 32 channels a thread, where
+  // the registers do not reach
   constexpr bool kAhead = kValues <= 16, kWide = !kAhead;
   __shared__ float scratch[2][32][2];
   // a warp's rows: [warps][N], to add the warps up.  32 channels a thread: the thread's sums of dw and
@@ -242,21 +289,30 @@ __global__ void __launch_bounds__(kMax) ln_bwd_kernel(const LnParams p) {
   const int lane = S::lane(), step = S::step();
   int row = S::first(), turn = 0;
   const float inv_n = 1.0f / (float)p.N;
+  constexpr bool kHold = !kWide;   // weights in registers, or again from L1 for each row
+  float w[kHold ? kValues : 1];
+  if (kHold) {
+#pragma unroll
+    for (int k = 0; k < kPieces; ++k)
+      load_weights<kVec, kN>(p.w, (lane + k * S::width()) * kN, 1.0f, p, &w[kHold ? k * kN : 0]);
+  }
   float dw[kWide ? 1 : kValues] = {}, db[kWide ? 1 : kValues] = {};
   float* const wide = sums + threadIdx.x;
   if (kWide)
     for (int i = 0; i < 2 * kValues; ++i) wide[i * blockDim.x] = 0.0f;
-  uint4 rx[kPieces], rd[kPieces];
+  uint4 rx[kAhead ? kPieces : 1], rd[kAhead ? kPieces : 1];
   float mean, rstd;
   auto load = [&](int r) {
     const bool in = r < p.rows;
     const T* x = reinterpret_cast<const T*>(p.x) + (in ? row_at(p, p.xs, r) : 0);
     const T* d = reinterpret_cast<const T*>(p.dy) + (in ? row_at(p, p.dys, r) : 0);
+    if (kAhead) {
 #pragma unroll
-    for (int k = 0; k < kPieces; ++k) {
-      const int c = (lane + k * S::width()) * kN;
-      rx[k] = in ? load_piece<kVec, T>(x, c, p) : make_uint4(0u, 0u, 0u, 0u);
-      rd[k] = in ? load_piece<kVec, T>(d, c, p) : make_uint4(0u, 0u, 0u, 0u);
+      for (int k = 0; k < kPieces; ++k) {
+        const int c = (lane + k * S::width()) * kN;
+        rx[kAhead ? k : 0] = in ? load_piece<kVec, T>(x, c, p) : make_uint4(0u, 0u, 0u, 0u);
+        rd[kAhead ? k : 0] = in ? load_piece<kVec, T>(d, c, p) : make_uint4(0u, 0u, 0u, 0u);
+      }
     }
     mean = in ? __ldg(p.mean + r) : 0.0f;
     rstd = in ? __ldg(p.rstd + r) : 0.0f;
@@ -264,59 +320,76 @@ __global__ void __launch_bounds__(kMax) ln_bwd_kernel(const LnParams p) {
   load(row);
   for (int base = S::kWarp ? row - (int)((threadIdx.x & 31) / (S::kWarp ? kLanes : 1)) : row; base < p.rows;
        base += step, row += step) {
-    uint4 cx[kPieces], cd[kPieces];
+    uint4 cx[kAhead ? kPieces : 1], cd[kAhead ? kPieces : 1];
     const float m = mean, rs = rstd;
 #pragma unroll
-    for (int k = 0; k < kPieces; ++k) {
+    for (int k = 0; k < (kAhead ? kPieces : 0); ++k) {
       cx[k] = rx[k];
       cd[k] = rd[k];
     }
-    if (kAhead) load(row + step);
-    float s[2] = {0.0f, 0.0f};   // of g and of g xhat
-#pragma unroll
+    load(row + step);
+    // 32 channels a thread are not held: each pass reads the row, the second time from the caches
+    const T* const gx = reinterpret_cast<const T*>(p.x) + (kAhead ? 0 : row_at(p, p.xs, row));
+    const T* const gd = reinterpret_cast<const T*>(p.dy) + (kAhead ? 0 : row_at(p, p.dys, row));
+    // xhat and g of two channels; where there is no channel dy is 0, and so is g
+    auto pair = [&](const float* x, const float* d, const float* ww, float* xh, float* g) {
+      fadd2(xh[0], xh[1], x[0], x[1], -m, -m);
+      fmul2(xh[0], xh[1], xh[0], xh[1], rs, rs);
+      fmul2(g[0], g[1], d[0], d[1], ww[0], ww[1]);
+    };
+    float s[2], s0[2] = {0.0f, 0.0f}, s1[2] = {0.0f, 0.0f};   // sums of g and of g xhat
+#pragma unroll(kAhead ? kPieces : 1)
     for (int k = 0; k < kPieces; ++k) {
       const int c = (lane + k * S::width()) * kN;
-      float x[kN], d[kN], ww[kN];
-      unpack<T>(cx[k], x);
-      unpack<T>(cd[k], d);
-      load_weights<kVec, kN>(p.w, c, 1.0f, p, ww);
+      float x[kN], d[kN], ww[kHold ? 1 : kN];
+      unpack<T>(kAhead ? cx[kAhead ? k : 0] : load_piece<kVec, T>(gx, c, p), x);
+      unpack<T>(kAhead ? cd[kAhead ? k : 0] : load_piece<kVec, T>(gd, c, p), d);
+      if (!kHold) load_weights<kVec, kN>(p.w, (lane + k * S::width()) * kN, 1.0f, p, ww);
+      const float* pw = kHold ? &w[kHold ? k * kN : 0] : ww;
 #pragma unroll
-      for (int e = 0; e < kN; ++e) {
-        const float xh = (x[e] - m) * rs;      // (where there is no channel dy is 0)
-        const float g = d[e] * ww[e];
+      for (int e = 0; e < kN; e += 2) {
+        float xh[2], g[2];
+        pair(x + e, d + e, pw + e, xh, g);
         if (kWide) {
-          wide[(k * kN + e) * blockDim.x] += d[e] * xh;
-          wide[(kValues + k * kN + e) * blockDim.x] += d[e];
+#pragma unroll
+          for (int i = 0; i < 2; ++i) {
+            wide[(k * kN + e + i) * blockDim.x] += d[e + i] * xh[i];
+            wide[(kValues + k * kN + e + i) * blockDim.x] += d[e + i];
+          }
         } else {
-          float &a = dw[kWide ? 0 : k * kN + e], &b = db[kWide ? 0 : k * kN + e];
-          a = fmaf(d[e], xh, a);
-          b += d[e];
+          float *a = &dw[kWide ? 0 : k * kN + e], *b = &db[kWide ? 0 : k * kN + e];
+          ffma2(a[0], a[1], d[e], d[e + 1], xh[0], xh[1], a[0], a[1]);
+          fadd2(b[0], b[1], b[0], b[1], d[e], d[e + 1]);
         }
-        s[0] += g;
-        s[1] = fmaf(g, xh, s[1]);
+        fadd2(s0[0], s0[1], s0[0], s0[1], g[0], g[1]);
+        ffma2(s1[0], s1[1], g[0], g[1], xh[0], xh[1], s1[0], s1[1]);
       }
     }
+    s[0] = s0[0] + s0[1];
+    s[1] = s1[0] + s1[1];
     row_sums<kLanes>(s, scratch, turn);
-    const float s0 = s[0] * inv_n, s1 = s[1] * inv_n;
+    const float m0 = -s[0] * inv_n, m1 = -s[1] * inv_n;
     if (row < p.rows) {
       T* dx = reinterpret_cast<T*>(p.dx) + row_at(p, p.dxs, row);
-#pragma unroll
+#pragma unroll(kAhead ? kPieces : 1)
       for (int k = 0; k < kPieces; ++k) {
         const int c = (lane + k * S::width()) * kN;
-        float x[kN], d[kN], ww[kN], out[kN];
-        unpack<T>(cx[k], x);
-        unpack<T>(cd[k], d);
-        load_weights<kVec, kN>(p.w, c, 1.0f, p, ww);
+        float x[kN], d[kN], ww[kHold ? 1 : kN], out[kN];
+        unpack<T>(kAhead ? cx[kAhead ? k : 0] : load_piece<kVec, T>(gx, c, p), x);
+        unpack<T>(kAhead ? cd[kAhead ? k : 0] : load_piece<kVec, T>(gd, c, p), d);
+        if (!kHold) load_weights<kVec, kN>(p.w, c, 1.0f, p, ww);
+        const float* pw = kHold ? &w[kHold ? k * kN : 0] : ww;
 #pragma unroll
-        for (int e = 0; e < kN; ++e) {
-          const float xh = (x[e] - m) * rs;
-          const float g = d[e] * ww[e];
-          out[e] = rs * (g - s0 - xh * s1);
+        for (int e = 0; e < kN; e += 2) {
+          float xh[2], g[2];
+          pair(x + e, d + e, pw + e, xh, g);
+          ffma2(g[0], g[1], xh[0], xh[1], m1, m1, g[0], g[1]);
+          fadd2(g[0], g[1], g[0], g[1], m0, m0);
+          fmul2(out[e], out[e + 1], g[0], g[1], rs, rs);
         }
         store_piece<kVec, T>(dx, c, out, p);
       }
     }
-    if (!kAhead) load(row + step);
   }
   if (p.partial == nullptr) return;
   // this CTA's sums: [2][CTAs][N]
@@ -362,6 +435,215 @@ __global__ void __launch_bounds__(kMax) ln_bwd_kernel(const LnParams p) {
   }
 }
 
+// ------------------------------------------------------------------ rows of a CTA through shared memory
+// Rows that a CTA takes, of up to 8192 channels, that allow 16-byte accesses: one thread copies whole rows ahead into a ring
+// in shared memory (16 channels a thread are too few bytes under way otherwise: with the next row
+// in registers the forward reached 3.3 and the backward 2.1 of 6.7 TB/s).
+constexpr int kRing = 3;
+struct RowRing {
+  uint64_t full[kRing];
+  uint32_t abort_flag;
+};
+__device__ uint32_t g_err_norm;
+
+__device__ __forceinline__ void ring_init(RowRing& r) {
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < kRing; ++s) mbar_init(&r.full[s], 1);
+    r.abort_flag = 0;
+    fence_mbar_init();
+  }
+  griddep_wait();
+  __syncthreads();
+}
+// The row of turn i has landed.  Should the wait run out, that is recorded, and the rest of the kernel
+// works on what is there: every thread keeps to its barriers.
+__device__ __forceinline__ void ring_wait(RowRing& r, int i) {
+  mbar_wait<false>(&r.full[i % kRing], (i / kRing) & 1, &r.abort_flag, &g_err_norm, kErrTimeoutTma);
+}
+
+template <class T>
+__global__ void __launch_bounds__(768) ln_fwd_ring_kernel(const LnParams p) {
+  constexpr int kN = Piece<T>::kN, kValues = 16, kPieces = kValues / kN;
+  extern __shared__ __align__(16) uint8_t rows_smem[];   // [kRing][N]
+  __shared__ RowRing ring;
+  __shared__ float scratch[2][32][2];
+  const int tid = threadIdx.x, threads = blockDim.x, bytes = p.N * (int)sizeof(T);
+  ring_init(ring);
+  float w[kValues], b[kValues];
+#pragma unroll
+  for (int k = 0; k < kPieces; ++k) {
+    load_weights<true, kN>(p.w, (tid + k * threads) * kN, 1.0f, p, w + k * kN);
+    load_weights<true, kN>(p.b, (tid + k * threads) * kN, 0.0f, p, b + k * kN);
+  }
+  const float inv_n = 1.0f / (float)p.N;
+  int issued = 0, turn = 0;
+  auto issue = [&](int i) {   // (thread 0)
+    const int row = (int)blockIdx.x + i * (int)gridDim.x;
+    if (row >= p.rows) return;
+    mbar_arrive_expect_tx(&ring.full[i % kRing], bytes);
+    bulk_load(rows_smem + (i % kRing) * bytes, reinterpret_cast<const T*>(p.x) + row_at(p, p.xs, row), bytes,
+              &ring.full[i % kRing]);
+    ++issued;
+  };
+  if (tid == 0)
+    for (int i = 0; i < kRing; ++i) issue(i);
+  for (int row = blockIdx.x, i = 0; row < p.rows; row += gridDim.x, ++i) {
+    ring_wait(ring, i);
+    const uint4* src = reinterpret_cast<const uint4*>(rows_smem + (i % kRing) * bytes);
+    float v[kValues], sum[1], sum2[2] = {0.0f, 0.0f};
+#pragma unroll
+    for (int k = 0; k < kPieces; ++k) {
+      const int c = (tid + k * threads) * kN;
+      unpack<T>(c < p.N ? src[tid + k * threads] : make_uint4(0u, 0u, 0u, 0u), v + k * kN);
+    }
+#pragma unroll
+    for (int e = 0; e < kValues; e += 2) fadd2(sum2[0], sum2[1], sum2[0], sum2[1], v[e], v[e + 1]);
+    sum[0] = sum2[0] + sum2[1];
+    row_sums<0>(sum, scratch, turn);
+    if (tid == 0) issue(i + kRing);   // (all threads have read this row's place: they met in row_sums)
+    const float mean = sum[0] * inv_n;
+    float sq[1], sq2[2] = {0.0f, 0.0f};
+#pragma unroll
+    for (int k = 0; k < kPieces; ++k) {
+#pragma unroll
+      for (int e = k * kN; e < (k + 1) * kN; e += 2) fadd2(v[e], v[e + 1], v[e], v[e + 1], -mean, -mean);
+      if ((tid + k * threads) * kN >= p.N) continue;
+#pragma unroll
+      for (int e = k * kN; e < (k + 1) * kN; e += 2) ffma2(sq2[0], sq2[1], v[e], v[e + 1], v[e], v[e + 1], sq2[0], sq2[1]);
+    }
+    sq[0] = sq2[0] + sq2[1];
+    row_sums<0>(sq, scratch, turn);
+    const float rstd = 1.0f / sqrtf(sq[0] * inv_n + p.eps);
+    T* y = reinterpret_cast<T*>(p.y) + row_at(p, p.ys, row);
+#pragma unroll
+    for (int k = 0; k < kPieces; ++k) {
+      float out[kN];
+#pragma unroll
+      for (int e = 0; e < kN; e += 2) {
+        const int a = k * kN + e;
+        fmul2(out[e], out[e + 1], v[a], v[a + 1], rstd, rstd);
+        ffma2(out[e], out[e + 1], out[e], out[e + 1], w[a], w[a + 1], b[a], b[a + 1]);
+      }
+      store_piece<true, T>(y, (tid + k * threads) * kN, out, p);
+    }
+    if (tid == 0) {
+      p.mean[row] = mean;
+      p.rstd[row] = rstd;
+    }
+  }
+  if (tid == 0 && ring.abort_flag)   // nothing may land in this CTA's shared memory after it has gone
+    for (int i = issued > kRing ? issued - kRing : 0; i < issued; ++i)
+      mbar_wait_teardown(&ring.full[i % kRing], (i / kRing) & 1);
+}
+
+template <class T>
+__global__ void __launch_bounds__(640) ln_bwd_ring_kernel(const LnParams p) {
+  constexpr int kN = Piece<T>::kN, kValues = 16, kPieces = kValues / kN;
+  extern __shared__ __align__(16) uint8_t rows_smem[];   // [kRing][x and dy][N]
+  __shared__ RowRing ring;
+  __shared__ float scratch[2][32][2];
+  const int tid = threadIdx.x, threads = blockDim.x, bytes = p.N * (int)sizeof(T);
+  ring_init(ring);
+  float w[kValues], dw[kValues] = {}, db[kValues] = {};
+#pragma unroll
+  for (int k = 0; k < kPieces; ++k) load_weights<true, kN>(p.w, (tid + k * threads) * kN, 1.0f, p, w + k * kN);
+  const float inv_n = 1.0f / (float)p.N;
+  int issued = 0, turn = 0;
+  auto issue = [&](int i) {   // (thread 0)
+    const int row = (int)blockIdx.x + i * (int)gridDim.x;
+    if (row >= p.rows) return;
+    uint8_t* to = rows_smem + (i % kRing) * 2 * bytes;
+    uint64_t* bar = &ring.full[i % kRing];
+    mbar_arrive_expect_tx(bar, 2 * bytes);
+    bulk_load(to, reinterpret_cast<const T*>(p.x) + row_at(p, p.xs, row), bytes, bar);
+    bulk_load(to + bytes, reinterpret_cast<const T*>(p.dy) + row_at(p, p.dys, row), bytes, bar);
+    ++issued;
+  };
+  if (tid == 0)
+    for (int i = 0; i < kRing; ++i) issue(i);
+  float next_mean = 0.0f, next_rstd = 0.0f;
+  if ((int)blockIdx.x < p.rows) {
+    next_mean = __ldg(p.mean + blockIdx.x);
+    next_rstd = __ldg(p.rstd + blockIdx.x);
+  }
+  for (int row = blockIdx.x, i = 0; row < p.rows; row += gridDim.x, ++i) {
+    const float m = next_mean, rs = next_rstd;
+    if (row + (int)gridDim.x < p.rows) {
+      next_mean = __ldg(p.mean + row + gridDim.x);
+      next_rstd = __ldg(p.rstd + row + gridDim.x);
+    }
+    const uint4* sx = reinterpret_cast<const uint4*>(rows_smem + (i % kRing) * 2 * bytes);
+    const uint4* sd = reinterpret_cast<const uint4*>(rows_smem + (i % kRing) * 2 * bytes + bytes);
+    ring_wait(ring, i);
+    float s[2], s0[2] = {0.0f, 0.0f}, s1[2] = {0.0f, 0.0f};   // sums of g and of g xhat
+#pragma unroll
+    for (int k = 0; k < kPieces; ++k) {
+      const int at = tid + k * threads;
+      if (at * kN >= p.N) continue;
+      float x[kN], d[kN];
+      unpack<T>(sx[at], x);
+      unpack<T>(sd[at], d);
+#pragma unroll
+      for (int e = 0; e < kN; e += 2) {
+        const int a = k * kN + e;
+        float xh[2], g[2];
+        fadd2(xh[0], xh[1], x[e], x[e + 1], -m, -m);
+        fmul2(xh[0], xh[1], xh[0], xh[1], rs, rs);
+        fmul2(g[0], g[1], d[e], d[e + 1], w[a], w[a + 1]);
+        ffma2(dw[a], dw[a + 1], d[e], d[e + 1], xh[0], xh[1], dw[a], dw[a + 1]);
+        fadd2(db[a], db[a + 1], db[a], db[a + 1], d[e], d[e + 1]);
+        fadd2(s0[0], s0[1], s0[0], s0[1], g[0], g[1]);
+        ffma2(s1[0], s1[1], g[0], g[1], xh[0], xh[1], s1[0], s1[1]);
+      }
+    }
+    s[0] = s0[0] + s0[1];
+    s[1] = s1[0] + s1[1];
+    row_sums<0>(s, scratch, turn);
+    // (all threads have met: they are done with the row before this one, and its place is free)
+    if (tid == 0 && i > 0) issue(i - 1 + kRing);
+    const float m0 = -s[0] * inv_n, m1 = -s[1] * inv_n;
+    T* dx = reinterpret_cast<T*>(p.dx) + row_at(p, p.dxs, row);
+#pragma unroll
+    for (int k = 0; k < kPieces; ++k) {
+      const int at = tid + k * threads;
+      if (at * kN >= p.N) continue;
+      float x[kN], d[kN], out[kN];
+      unpack<T>(sx[at], x);
+      unpack<T>(sd[at], d);
+#pragma unroll
+      for (int e = 0; e < kN; e += 2) {
+        const int a = k * kN + e;
+        float xh[2], g[2];
+        fadd2(xh[0], xh[1], x[e], x[e + 1], -m, -m);
+        fmul2(xh[0], xh[1], xh[0], xh[1], rs, rs);
+        fmul2(g[0], g[1], d[e], d[e + 1], w[a], w[a + 1]);
+        ffma2(g[0], g[1], xh[0], xh[1], m1, m1, g[0], g[1]);
+        fadd2(g[0], g[1], g[0], g[1], m0, m0);
+        fmul2(out[e], out[e + 1], g[0], g[1], rs, rs);
+      }
+      store_piece<true, T>(dx, at * kN, out, p);
+    }
+  }
+  if (p.partial != nullptr) {   // this CTA's sums: [2][CTAs][N]
+    float* const to_w = p.partial + (long long)blockIdx.x * p.N;
+    float* const to_b = p.partial + ((long long)gridDim.x + blockIdx.x) * p.N;
+#pragma unroll
+    for (int k = 0; k < kPieces; ++k) {
+      const int c = (tid + k * threads) * kN;
+      if (c >= p.N) continue;
+#pragma unroll
+      for (int e = 0; e < kN; e += 4) {
+        const int a = k * kN + e;
+        *reinterpret_cast<float4*>(to_w + c + e) = make_float4(dw[a], dw[a + 1], dw[a + 2], dw[a + 3]);
+        *reinterpret_cast<float4*>(to_b + c + e) = make_float4(db[a], db[a + 1], db[a + 2], db[a + 3]);
+      }
+    }
+  }
+  if (tid == 0 && ring.abort_flag)
+    for (int i = issued > kRing ? issued - kRing : 0; i < issued; ++i)
+      mbar_wait_teardown(&ring.full[i % kRing], (i / kRing) & 1);
+}
+
 // dw and db from the CTAs' sums: a block takes 32 channels of one of them, its 32 warps every 32nd CTA.
 __global__ void __launch_bounds__(1024) ln_grad_kernel(const float* partial, int n_parts, int N, void* dw, void* db,
                                                        int type) {
@@ -385,7 +667,6 @@ __global__ void __launch_bounds__(1024) ln_grad_kernel(const float* partial, int
   else reinterpret_cast<__half*>(to)[out] = __float2half_rn(v);
 }
 
-constexpr int kBwdMax = 512;   // threads that the backward's registers are sized for
 struct Shape {
   int lanes, threads, ctas;
   bool wide;   // 32 channels a thread
@@ -394,8 +675,10 @@ struct Shape {
 Shape shape_of(int rows, int N, bool backward) {
   Shape s = {};
   constexpr int kSms = 152;
-  if (N <= 512) {
-    s.lanes = N <= 64 ? 4 : N <= 128 ? 8 : N <= 256 ? 16 : 32;
+  // 16 channels a lane, in the backward 8 (where the sums take two more registers a channel)
+  const int a_lane = backward ? 8 : 16;
+  if (N <= 32 * a_lane) {
+    s.lanes = N <= 4 * a_lane ? 4 : N <= 8 * a_lane ? 8 : N <= 16 * a_lane ? 16 : 32;
     s.threads = 256;
     const int per = s.threads / s.lanes;
     s.ctas = (rows + per - 1) / per;
@@ -405,15 +688,23 @@ Shape shape_of(int rows, int N, bool backward) {
     s.threads = ((N + per - 1) / per + 31) / 32 * 32;
     s.ctas = rows;
   }
-  const int per_sm = 2048 / s.threads;   // (what the registers leave is fewer)
-  const int cap = kSms * (backward ? (s.lanes ? 4 : per_sm < 2 ? 1 : per_sm < 8 ? per_sm / 2 : 4) : per_sm);
+  // CTAs that an SM holds by registers (what the launch bounds allow a thread) and, in the rings, by
+  // shared memory
+  const int regs = s.wide ? 128 : backward ? 96 : s.lanes ? 88 : 80;
+  int per_sm = 65536 / (regs * s.threads);
+  if (s.lanes == 0 && !s.wide) {
+    const int ring = kRing * (backward ? 2 : 1) * 4 * N;   // (of the widest type)
+    if (per_sm > 220000 / ring) per_sm = 220000 / ring;
+  }
+  if (per_sm < 1) per_sm = 1;
+  const int cap = kSms * per_sm;
   if (s.ctas > cap) s.ctas = cap;
   if (s.ctas < 1) s.ctas = 1;
   return s;
 }
 
 size_t bwd_smem(const Shape& s, int N) {
-  if (s.lanes > 0) return (size_t)(s.threads / 32) * N * sizeof(float);   // at most 16 KB
+  if (s.lanes > 0) return (size_t)(s.threads / 32) * N * sizeof(float);   // at most 8 KB
   return s.wide ? (size_t)64 * s.threads * sizeof(float) : 0;             // at most 128 KB
 }
 
@@ -421,7 +712,7 @@ template <class T, bool kVec, int kLanes, int kValues, bool kBackward>
 cudaError_t launch_one(const LnParams& p, const Shape& s, cudaStream_t stream) {
   const dim3 grid((unsigned)s.ctas);
   if constexpr (kBackward) {
-    auto* kernel = ln_bwd_kernel<T, kVec, kLanes, kValues, kBwdMax>;
+    auto* kernel = ln_bwd_kernel<T, kVec, kLanes, kValues, (kLanes > 0 ? 640 : 512)>;
     if constexpr (kValues == 32) {
       static ContextOnce attr_done;
       const cudaError_t e = attr_done.run([&] {
@@ -431,20 +722,33 @@ cudaError_t launch_one(const LnParams& p, const Shape& s, cudaStream_t stream) {
     }
     return launch_dependent(kernel, grid, s.threads, bwd_smem(s, p.N), stream, p);
   } else {
-    return launch_dependent(ln_fwd_kernel<T, kVec, kLanes, kValues, kValues == 32 ? 512 : 1024>, grid, s.threads, 0,
+    return launch_dependent(ln_fwd_kernel<T, kVec, kLanes, kValues, (kValues == 32 ? 512 : 704)>, grid, s.threads, 0,
                             stream, p);
   }
 }
+template <class T, bool kBackward>
+cudaError_t launch_ring(const LnParams& p, const Shape& s, cudaStream_t stream) {
+  static ContextOnce attr_done;
+  auto* kernel = kBackward ? ln_bwd_ring_kernel<T> : ln_fwd_ring_kernel<T>;
+  const cudaError_t e = attr_done.run([&] {
+    return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, 226 * 1024);
+  });
+  if (e != cudaSuccess) return e;
+  return launch_dependent(kernel, dim3((unsigned)s.ctas), s.threads,
+                          (size_t)kRing * (kBackward ? 2 : 1) * p.N * sizeof(T), stream, p);
+}
 template <class T, bool kVec, bool kBackward>
 cudaError_t launch_typed(const LnParams& p, const Shape& s, cudaStream_t stream) {
+  if constexpr (kVec)
+    if (s.lanes == 0 && !s.wide) return launch_ring<T, kBackward>(p, s, stream);
   switch (s.lanes) {
-    case 4: return launch_one<T, kVec, 4, 16, kBackward>(p, s, stream);
-    case 8: return launch_one<T, kVec, 8, 16, kBackward>(p, s, stream);
-    case 16: return launch_one<T, kVec, 16, 16, kBackward>(p, s, stream);
-    case 32: return launch_one<T, kVec, 32, 16, kBackward>(p, s, stream);
+    case 4: return launch_one<T, kVec, 4, kBackward ? 8 : 16, kBackward>(p, s, stream);
+    case 8: return launch_one<T, kVec, 8, kBackward ? 8 : 16, kBackward>(p, s, stream);
+    case 16: return launch_one<T, kVec, 16, kBackward ? 8 : 16, kBackward>(p, s, stream);
+    case 32: return launch_one<T, kVec, 32, kBackward ? 8 : 16, kBackward>(p, s, stream);
   }
-  return s.wide ? launch_one<T, kVec, 0, 32, kBackward>(p, s, stream)
-                : launch_one<T, kVec, 0, 16, kBackward>(p, s, stream);
+  if (s.wide) return launch_one<T, kVec, 0, 32, kBackward>(p, s, stream);
+  return launch_one<T, false, 0, 16, kBackward>(p, s, stream);
 }
 template <bool kBackward>
 cudaError_t launch_any(const LnParams& p, const Shape& s, int type, bool vec, cudaStream_t stream) {
@@ -463,8 +767,8 @@ LnParams params_of(const LayerNormArgs& a) {
   p.mean = a.mean;
   p.rstd = a.rstd;
   p.rows = a.B * a.S * a.H;
-  p.S = a.S;
-  p.H = a.H;
+  p.S = make_div(a.S);
+  p.H = make_div(a.H);
   p.N = a.N;
   p.eps = a.eps;
   p.w_type = a.w_type;
@@ -511,6 +815,13 @@ cudaError_t launch_layer_norm_bwd(const LayerNormArgs& a, const void* dy, const 
   if (e != cudaSuccess || dw == nullptr) return e;
   return launch_dependent(ln_grad_kernel, dim3((unsigned)(p.N + 31) / 32, 2), 1024, 0, stream,
                           static_cast<const float*>(workspace), s.ctas, p.N, dw, db, a.w_type);
+}
+
+cudaError_t read_and_clear_err_norm(uint32_t* out) {
+  cudaError_t e = cudaMemcpyFromSymbol(out, g_err_norm, sizeof(uint32_t));
+  if (e != cudaSuccess) return e;
+  const uint32_t zero = 0;
+  return cudaMemcpyToSymbol(g_err_norm, &zero, sizeof(uint32_t));
 }
 
 }  // namespace sa
