@@ -25,6 +25,7 @@ namespace {
 
 struct Rows {
   long long str[3];   // element strides (b, s, h)
+  int even;           // all rows are str[2] apart
 };
 // n / d for n < 2^31 by a product (Granlund and Montgomery, "Division by invariant integers using
 // multiplication", 1994): d <= 2^shift, mul = ceil(2^(32 + shift) / d) - 2^32.
@@ -50,11 +51,18 @@ struct LnParams {
   float eps;
   int w_type;                     // type of w and b
   float* partial;                 // backward: [2][CTAs][N] sums of dw and db, or nullptr
+  int ring;                       // backward through shared memory: rows in the ring
 };
 
-__device__ __forceinline__ long long row_at(const LnParams& p, const Rows& r, int row) {
+// Where a row starts, in elements.  (The backward's ring takes the general form: with the other one it
+// was slower up to 8192 channels, 400 us instead of 368 for 76112 x 5120.)
+__device__ __forceinline__ long long row_in_ring(const LnParams& p, const Rows& r, int row) {
   const int bs = div_by(row, p.H), h = row - bs * (int)p.H.d, b = div_by(bs, p.S), s = bs - b * (int)p.S.d;
   return (long long)b * r.str[0] + (long long)s * r.str[1] + (long long)h * r.str[2];
+}
+
+__device__ __forceinline__ long long row_at(const LnParams& p, const Rows& r, int row) {
+  return r.even ? (long long)row * r.str[2] : row_in_ring(p, r, row);
 }
 
 template <class T>
@@ -189,7 +197,8 @@ __device__ __forceinline__ void row_sums(float (&v)[kSums], float (*scratch)[32]
 }
 
 // kMax: the largest CTA (registers); kValues: channels a thread.
-template <class T, bool kVec, int kLanes, int kValues, int kMax>
+// kRows: rows whose loads are under way ahead of the one worked on.
+template <class T, bool kVec, int kLanes, int kValues, int kRows, int kMax>
 __global__ void __launch_bounds__(kMax) ln_fwd_kernel(const LnParams p) {
   using S = Spread<kLanes>;
   constexpr int kN = Piece<T>::kN, kPieces = kValues / kN;
@@ -207,22 +216,26 @@ __global__ void __launch_bounds__(kMax) ln_fwd_kernel(const LnParams p) {
       load_weights<kVec, kN>(p.b, (lane + k * S::width()) * kN, 0.0f, p, &b[kHold ? k * kN : 0]);
     }
   }
-  uint4 raw[kPieces];
-  auto load = [&](int r) {
+  uint4 raw[kRows][kPieces];
+  auto load = [&](uint4(&to)[kPieces], int r) {
     const T* x = reinterpret_cast<const T*>(p.x) + (r < p.rows ? row_at(p, p.xs, r) : 0);
 #pragma unroll
     for (int k = 0; k < kPieces; ++k)
-      raw[k] = r < p.rows ? load_piece<kVec, T>(x, (lane + k * S::width()) * kN, p) : make_uint4(0u, 0u, 0u, 0u);
+      to[k] = r < p.rows ? load_piece<kVec, T>(x, (lane + k * S::width()) * kN, p) : make_uint4(0u, 0u, 0u, 0u);
   };
-  load(row);
+#pragma unroll
+  for (int u = 0; u < kRows; ++u) load(raw[u], row + u * step);
   // (a warp's rows are consecutive: its lanes leave the loop together but for the last rows, whose
   // idle lanes work on zeros and store nothing)
-  for (int base = S::kWarp ? row - (int)((threadIdx.x & 31) / (S::kWarp ? kLanes : 1)) : row; base < p.rows;
-       base += step, row += step) {
+  int base = S::kWarp ? row - (int)((threadIdx.x & 31) / (S::kWarp ? kLanes : 1)) : row;
+  while (base < p.rows) {
+#pragma unroll
+  for (int u = 0; u < kRows; ++u, base += step, row += step) {
+    if (base >= p.rows) break;
     float v[kValues];
 #pragma unroll
-    for (int k = 0; k < kPieces; ++k) unpack<T>(raw[k], v + k * kN);
-    load(row + step);
+    for (int k = 0; k < kPieces; ++k) unpack<T>(raw[u][k], v + k * kN);
+    load(raw[u], row + kRows * step);
     float sum[1], sum2[2] = {0.0f, 0.0f};
 #pragma unroll
     for (int i = 0; i < kValues; i += 2) fadd2(sum2[0], sum2[1], sum2[0], sum2[1], v[i], v[i + 1]);   // (channels past N are 0)
@@ -272,9 +285,10 @@ __global__ void __launch_bounds__(kMax) ln_fwd_kernel(const LnParams p) {
       }
     }
   }
+  }
 }
 
-template <class T, bool kVec, int kLanes, int kValues, int kMax>
+template <class T, bool kVec, int kLanes, int kValues, int kRows, int kMax>
 __global__ void __launch_bounds__(kMax) ln_bwd_kernel(const LnParams p) {
   using S = Spread<kLanes>;
   constexpr int kN = Piece<T>::kN, kPieces = kValues / kN;
@@ -300,71 +314,74 @@ __global__ void __launch_bounds__(kMax) ln_bwd_kernel(const LnParams p) {
   float* const wide = sums + threadIdx.x;
   if (kWide)
     for (int i = 0; i < 2 * kValues; ++i) wide[i * blockDim.x] = 0.0f;
-  uint4 rx[kAhead ? kPieces : 1], rd[kAhead ? kPieces : 1];
-  float mean, rstd;
-  auto load = [&](int r) {
+  constexpr int kHeld = kAhead ? kPieces : 1;
+  uint4 rx[kRows][kHeld], rd[kRows][kHeld];
+  float mean[kRows], rstd[kRows];
+  auto load = [&](int u, int r) {
     const bool in = r < p.rows;
     const T* x = reinterpret_cast<const T*>(p.x) + (in ? row_at(p, p.xs, r) : 0);
     const T* d = reinterpret_cast<const T*>(p.dy) + (in ? row_at(p, p.dys, r) : 0);
     if (kAhead) {
 #pragma unroll
-      for (int k = 0; k < kPieces; ++k) {
+      for (int k = 0; k < kHeld; ++k) {
         const int c = (lane + k * S::width()) * kN;
-        rx[kAhead ? k : 0] = in ? load_piece<kVec, T>(x, c, p) : make_uint4(0u, 0u, 0u, 0u);
-        rd[kAhead ? k : 0] = in ? load_piece<kVec, T>(d, c, p) : make_uint4(0u, 0u, 0u, 0u);
+        rx[u][k] = in ? load_piece<kVec, T>(x, c, p) : make_uint4(0u, 0u, 0u, 0u);
+        rd[u][k] = in ? load_piece<kVec, T>(d, c, p) : make_uint4(0u, 0u, 0u, 0u);
       }
     }
-    mean = in ? __ldg(p.mean + r) : 0.0f;
-    rstd = in ? __ldg(p.rstd + r) : 0.0f;
+    mean[u] = in ? __ldg(p.mean + r) : 0.0f;
+    rstd[u] = in ? __ldg(p.rstd + r) : 0.0f;
   };
-  load(row);
-  for (int base = S::kWarp ? row - (int)((threadIdx.x & 31) / (S::kWarp ? kLanes : 1)) : row; base < p.rows;
-       base += step, row += step) {
-    uint4 cx[kAhead ? kPieces : 1], cd[kAhead ? kPieces : 1];
-    const float m = mean, rs = rstd;
 #pragma unroll
-    for (int k = 0; k < (kAhead ? kPieces : 0); ++k) {
-      cx[k] = rx[k];
-      cd[k] = rd[k];
-    }
-    load(row + step);
+  for (int u = 0; u < kRows; ++u) load(u, row + u * step);
+  int base = S::kWarp ? row - (int)((threadIdx.x & 31) / (S::kWarp ? kLanes : 1)) : row;
+  while (base < p.rows) {
+#pragma unroll
+  for (int u = 0; u < kRows; ++u, base += step, row += step) {
+    if (base >= p.rows) break;
+    const float m = mean[u], rs = rstd[u];
     // 32 channels a thread are not held: each pass reads the row, the second time from the caches
     const T* const gx = reinterpret_cast<const T*>(p.x) + (kAhead ? 0 : row_at(p, p.xs, row));
     const T* const gd = reinterpret_cast<const T*>(p.dy) + (kAhead ? 0 : row_at(p, p.dys, row));
-    // xhat and g of two channels; where there is no channel dy is 0, and so is g
-    auto pair = [&](const float* x, const float* d, const float* ww, float* xh, float* g) {
-      fadd2(xh[0], xh[1], x[0], x[1], -m, -m);
-      fmul2(xh[0], xh[1], xh[0], xh[1], rs, rs);
-      fmul2(g[0], g[1], d[0], d[1], ww[0], ww[1]);
+    // xhat and g of a piece's channels (where there is no channel dy is 0, and so is g)
+    float xh[kAhead ? kValues : kN], g[kAhead ? kValues : kN], d[kN];
+    auto piece = [&](int k, float* ph, float* pg) {
+      float x[kN], ww[kHold ? 1 : kN];
+      const int c = (lane + k * S::width()) * kN;
+      unpack<T>(kAhead ? rx[u][kAhead ? k : 0] : load_piece<kVec, T>(gx, c, p), x);
+      unpack<T>(kAhead ? rd[u][kAhead ? k : 0] : load_piece<kVec, T>(gd, c, p), d);
+      if (!kHold) load_weights<kVec, kN>(p.w, c, 1.0f, p, ww);
+      const float* pw = kHold ? &w[kHold ? k * kN : 0] : ww;
+#pragma unroll
+      for (int e = 0; e < kN; e += 2) {
+        fadd2(ph[e], ph[e + 1], x[e], x[e + 1], -m, -m);
+        fmul2(ph[e], ph[e + 1], ph[e], ph[e + 1], rs, rs);
+        fmul2(pg[e], pg[e + 1], d[e], d[e + 1], pw[e], pw[e + 1]);
+      }
     };
     float s[2], s0[2] = {0.0f, 0.0f}, s1[2] = {0.0f, 0.0f};   // sums of g and of g xhat
 #pragma unroll(kAhead ? kPieces : 1)
     for (int k = 0; k < kPieces; ++k) {
-      const int c = (lane + k * S::width()) * kN;
-      float x[kN], d[kN], ww[kHold ? 1 : kN];
-      unpack<T>(kAhead ? cx[kAhead ? k : 0] : load_piece<kVec, T>(gx, c, p), x);
-      unpack<T>(kAhead ? cd[kAhead ? k : 0] : load_piece<kVec, T>(gd, c, p), d);
-      if (!kHold) load_weights<kVec, kN>(p.w, (lane + k * S::width()) * kN, 1.0f, p, ww);
-      const float* pw = kHold ? &w[kHold ? k * kN : 0] : ww;
+      float *ph = xh + (kAhead ? k * kN : 0), *pg = g + (kAhead ? k * kN : 0);
+      piece(k, ph, pg);
 #pragma unroll
       for (int e = 0; e < kN; e += 2) {
-        float xh[2], g[2];
-        pair(x + e, d + e, pw + e, xh, g);
         if (kWide) {
 #pragma unroll
           for (int i = 0; i < 2; ++i) {
-            wide[(k * kN + e + i) * blockDim.x] += d[e + i] * xh[i];
+            wide[(k * kN + e + i) * blockDim.x] += d[e + i] * ph[e + i];
             wide[(kValues + k * kN + e + i) * blockDim.x] += d[e + i];
           }
         } else {
           float *a = &dw[kWide ? 0 : k * kN + e], *b = &db[kWide ? 0 : k * kN + e];
-          ffma2(a[0], a[1], d[e], d[e + 1], xh[0], xh[1], a[0], a[1]);
+          ffma2(a[0], a[1], d[e], d[e + 1], ph[e], ph[e + 1], a[0], a[1]);
           fadd2(b[0], b[1], b[0], b[1], d[e], d[e + 1]);
         }
-        fadd2(s0[0], s0[1], s0[0], s0[1], g[0], g[1]);
-        ffma2(s1[0], s1[1], g[0], g[1], xh[0], xh[1], s1[0], s1[1]);
+        fadd2(s0[0], s0[1], s0[0], s0[1], pg[e], pg[e + 1]);
+        ffma2(s1[0], s1[1], pg[e], pg[e + 1], ph[e], ph[e + 1], s1[0], s1[1]);
       }
     }
+    load(u, row + kRows * step);
     s[0] = s0[0] + s0[1];
     s[1] = s1[0] + s1[1];
     row_sums<kLanes>(s, scratch, turn);
@@ -373,23 +390,18 @@ __global__ void __launch_bounds__(kMax) ln_bwd_kernel(const LnParams p) {
       T* dx = reinterpret_cast<T*>(p.dx) + row_at(p, p.dxs, row);
 #pragma unroll(kAhead ? kPieces : 1)
       for (int k = 0; k < kPieces; ++k) {
-        const int c = (lane + k * S::width()) * kN;
-        float x[kN], d[kN], ww[kHold ? 1 : kN], out[kN];
-        unpack<T>(kAhead ? cx[kAhead ? k : 0] : load_piece<kVec, T>(gx, c, p), x);
-        unpack<T>(kAhead ? cd[kAhead ? k : 0] : load_piece<kVec, T>(gd, c, p), d);
-        if (!kHold) load_weights<kVec, kN>(p.w, c, 1.0f, p, ww);
-        const float* pw = kHold ? &w[kHold ? k * kN : 0] : ww;
+        float *ph = xh + (kAhead ? k * kN : 0), *pg = g + (kAhead ? k * kN : 0), out[kN];
+        if (!kAhead) piece(k, ph, pg);
 #pragma unroll
         for (int e = 0; e < kN; e += 2) {
-          float xh[2], g[2];
-          pair(x + e, d + e, pw + e, xh, g);
-          ffma2(g[0], g[1], xh[0], xh[1], m1, m1, g[0], g[1]);
-          fadd2(g[0], g[1], g[0], g[1], m0, m0);
-          fmul2(out[e], out[e + 1], g[0], g[1], rs, rs);
+          ffma2(pg[e], pg[e + 1], ph[e], ph[e + 1], m1, m1, pg[e], pg[e + 1]);
+          fadd2(pg[e], pg[e + 1], pg[e], pg[e + 1], m0, m0);
+          fmul2(out[e], out[e + 1], pg[e], pg[e + 1], rs, rs);
         }
-        store_piece<kVec, T>(dx, c, out, p);
+        store_piece<kVec, T>(dx, (lane + k * S::width()) * kN, out, p);
       }
     }
+  }
   }
   if (p.partial == nullptr) return;
   // this CTA's sums: [2][CTAs][N]
@@ -439,32 +451,35 @@ __global__ void __launch_bounds__(kMax) ln_bwd_kernel(const LnParams p) {
 // Rows that a CTA takes, of up to 8192 channels, that allow 16-byte accesses: one thread copies whole rows ahead into a ring
 // in shared memory (16 channels a thread are too few bytes under way otherwise: with the next row
 // in registers the forward reached 3.3 and the backward 2.1 of 6.7 TB/s).
-constexpr int kRing = 3;
+// The forward works on two rows at once (their sums share barriers and shuffles' latency) with the next
+// two under way; the backward, which reads its rows twice, on one of three, or of two where three would
+// leave room for fewer CTAs.
+constexpr int kMaxRing = 4;
 struct RowRing {
-  uint64_t full[kRing];
+  uint64_t full[kMaxRing];
   uint32_t abort_flag;
 };
 __device__ uint32_t g_err_norm;
 
 __device__ __forceinline__ void ring_init(RowRing& r) {
   if (threadIdx.x == 0) {
-    for (int s = 0; s < kRing; ++s) mbar_init(&r.full[s], 1);
+    for (int s = 0; s < kMaxRing; ++s) mbar_init(&r.full[s], 1);
     r.abort_flag = 0;
     fence_mbar_init();
   }
   griddep_wait();
   __syncthreads();
 }
-// The row of turn i has landed.  Should the wait run out, that is recorded, and the rest of the kernel
-// works on what is there: every thread keeps to its barriers.
-__device__ __forceinline__ void ring_wait(RowRing& r, int i) {
-  mbar_wait<false>(&r.full[i % kRing], (i / kRing) & 1, &r.abort_flag, &g_err_norm, kErrTimeoutTma);
+// The row in slot s has landed, for the (phase + 1)-th time.  Should the wait run out, that is recorded, and
+// the rest of the kernel works on what is there: every thread keeps to its barriers.
+__device__ __forceinline__ void ring_wait(RowRing& r, int s, int phase) {
+  mbar_wait<false>(&r.full[s], phase & 1, &r.abort_flag, &g_err_norm, kErrTimeoutTma);
 }
 
 template <class T>
-__global__ void __launch_bounds__(768) ln_fwd_ring_kernel(const LnParams p) {
+__global__ void __launch_bounds__(640) ln_fwd_ring_kernel(const LnParams p) {
   constexpr int kN = Piece<T>::kN, kValues = 16, kPieces = kValues / kN;
-  extern __shared__ __align__(16) uint8_t rows_smem[];   // [kRing][N]
+  extern __shared__ __align__(16) uint8_t rows_smem[];   // [2 turns][2 rows][N]
   __shared__ RowRing ring;
   __shared__ float scratch[2][32][2];
   const int tid = threadIdx.x, threads = blockDim.x, bytes = p.N * (int)sizeof(T);
@@ -477,110 +492,140 @@ __global__ void __launch_bounds__(768) ln_fwd_ring_kernel(const LnParams p) {
   }
   const float inv_n = 1.0f / (float)p.N;
   int issued = 0, turn = 0;
-  auto issue = [&](int i) {   // (thread 0)
-    const int row = (int)blockIdx.x + i * (int)gridDim.x;
-    if (row >= p.rows) return;
-    mbar_arrive_expect_tx(&ring.full[i % kRing], bytes);
-    bulk_load(rows_smem + (i % kRing) * bytes, reinterpret_cast<const T*>(p.x) + row_at(p, p.xs, row), bytes,
-              &ring.full[i % kRing]);
-    ++issued;
+  // (thread 0) the rows of turn i: the CTA's rows 2 i and 2 i + 1
+  auto issue = [&](int i) {
+#pragma unroll
+    for (int r = 0; r < 2; ++r) {
+      const long long row = (long long)blockIdx.x + (2ll * i + r) * gridDim.x;
+      if (row >= p.rows) return;
+      const int slot = 2 * (i & 1) + r;
+      mbar_arrive_expect_tx(&ring.full[slot], bytes);
+      bulk_load(rows_smem + slot * bytes, reinterpret_cast<const T*>(p.x) + row_at(p, p.xs, (int)row), bytes,
+                &ring.full[slot]);
+      ++issued;
+    }
   };
-  if (tid == 0)
-    for (int i = 0; i < kRing; ++i) issue(i);
-  for (int row = blockIdx.x, i = 0; row < p.rows; row += gridDim.x, ++i) {
-    ring_wait(ring, i);
-    const uint4* src = reinterpret_cast<const uint4*>(rows_smem + (i % kRing) * bytes);
-    float v[kValues], sum[1], sum2[2] = {0.0f, 0.0f};
+  if (tid == 0) {
+    issue(0);
+    issue(1);
+  }
+  for (int i = 0, row = blockIdx.x; row < p.rows; row += 2 * gridDim.x, ++i) {
+    const bool two = row + (int)gridDim.x < p.rows;   // (the last turn may have one row)
+    float v[2][kValues], sum[2];
 #pragma unroll
-    for (int k = 0; k < kPieces; ++k) {
-      const int c = (tid + k * threads) * kN;
-      unpack<T>(c < p.N ? src[tid + k * threads] : make_uint4(0u, 0u, 0u, 0u), v + k * kN);
-    }
+    for (int r = 0; r < 2; ++r) {
+      const int slot = 2 * (i & 1) + r;
+      if (r == 0 || two) ring_wait(ring, slot, i >> 1);
+      const uint4* src = reinterpret_cast<const uint4*>(rows_smem + slot * bytes);
 #pragma unroll
-    for (int e = 0; e < kValues; e += 2) fadd2(sum2[0], sum2[1], sum2[0], sum2[1], v[e], v[e + 1]);
-    sum[0] = sum2[0] + sum2[1];
-    row_sums<0>(sum, scratch, turn);
-    if (tid == 0) issue(i + kRing);   // (all threads have read this row's place: they met in row_sums)
-    const float mean = sum[0] * inv_n;
-    float sq[1], sq2[2] = {0.0f, 0.0f};
-#pragma unroll
-    for (int k = 0; k < kPieces; ++k) {
-#pragma unroll
-      for (int e = k * kN; e < (k + 1) * kN; e += 2) fadd2(v[e], v[e + 1], v[e], v[e + 1], -mean, -mean);
-      if ((tid + k * threads) * kN >= p.N) continue;
-#pragma unroll
-      for (int e = k * kN; e < (k + 1) * kN; e += 2) ffma2(sq2[0], sq2[1], v[e], v[e + 1], v[e], v[e + 1], sq2[0], sq2[1]);
-    }
-    sq[0] = sq2[0] + sq2[1];
-    row_sums<0>(sq, scratch, turn);
-    const float rstd = 1.0f / sqrtf(sq[0] * inv_n + p.eps);
-    T* y = reinterpret_cast<T*>(p.y) + row_at(p, p.ys, row);
-#pragma unroll
-    for (int k = 0; k < kPieces; ++k) {
-      float out[kN];
-#pragma unroll
-      for (int e = 0; e < kN; e += 2) {
-        const int a = k * kN + e;
-        fmul2(out[e], out[e + 1], v[a], v[a + 1], rstd, rstd);
-        ffma2(out[e], out[e + 1], out[e], out[e + 1], w[a], w[a + 1], b[a], b[a + 1]);
+      for (int k = 0; k < kPieces; ++k) {
+        const int at = tid + k * threads;
+        unpack<T>(at * kN < p.N && (r == 0 || two) ? src[at] : make_uint4(0u, 0u, 0u, 0u), v[r] + k * kN);
       }
-      store_piece<true, T>(y, (tid + k * threads) * kN, out, p);
+      float a[2] = {0.0f, 0.0f};
+#pragma unroll
+      for (int e = 0; e < kValues; e += 2) fadd2(a[0], a[1], a[0], a[1], v[r][e], v[r][e + 1]);
+      sum[r] = a[0] + a[1];
     }
-    if (tid == 0) {
-      p.mean[row] = mean;
-      p.rstd[row] = rstd;
+    row_sums<0>(sum, scratch, turn);
+    if (tid == 0) issue(i + 2);   // (all threads have read this turn's rows: they met in row_sums)
+    float sq[2], mean[2];
+#pragma unroll
+    for (int r = 0; r < 2; ++r) {
+      mean[r] = sum[r] * inv_n;
+      float a[2] = {0.0f, 0.0f};
+#pragma unroll
+      for (int k = 0; k < kPieces; ++k) {
+#pragma unroll
+        for (int e = k * kN; e < (k + 1) * kN; e += 2)
+          fadd2(v[r][e], v[r][e + 1], v[r][e], v[r][e + 1], -mean[r], -mean[r]);
+        if ((tid + k * threads) * kN >= p.N) continue;
+#pragma unroll
+        for (int e = k * kN; e < (k + 1) * kN; e += 2)
+          ffma2(a[0], a[1], v[r][e], v[r][e + 1], v[r][e], v[r][e + 1], a[0], a[1]);
+      }
+      sq[r] = a[0] + a[1];
+    }
+    row_sums<0>(sq, scratch, turn);
+#pragma unroll
+    for (int r = 0; r < 2; ++r) {
+      if (r == 1 && !two) break;
+      const int at = row + r * (int)gridDim.x;
+      const float rstd = 1.0f / sqrtf(sq[r] * inv_n + p.eps);
+      T* y = reinterpret_cast<T*>(p.y) + row_at(p, p.ys, at);
+#pragma unroll
+      for (int k = 0; k < kPieces; ++k) {
+        float out[kN];
+#pragma unroll
+        for (int e = 0; e < kN; e += 2) {
+          const int a = k * kN + e;
+          fmul2(out[e], out[e + 1], v[r][a], v[r][a + 1], rstd, rstd);
+          ffma2(out[e], out[e + 1], out[e], out[e + 1], w[a], w[a + 1], b[a], b[a + 1]);
+        }
+        store_piece<true, T>(y, (tid + k * threads) * kN, out, p);
+      }
+      if (tid == 0) {
+        p.mean[at] = mean[r];
+        p.rstd[at] = rstd;
+      }
     }
   }
   if (tid == 0 && ring.abort_flag)   // nothing may land in this CTA's shared memory after it has gone
-    for (int i = issued > kRing ? issued - kRing : 0; i < issued; ++i)
-      mbar_wait_teardown(&ring.full[i % kRing], (i / kRing) & 1);
+    for (int n = issued > 4 ? issued - 4 : 0; n < issued; ++n)   // (the n-th row goes to slot n % 4)
+      mbar_wait_teardown(&ring.full[n % 4], (n / 4) & 1);
 }
 
-template <class T>
-__global__ void __launch_bounds__(640) ln_bwd_ring_kernel(const LnParams p) {
-  constexpr int kN = Piece<T>::kN, kValues = 16, kPieces = kValues / kN;
-  extern __shared__ __align__(16) uint8_t rows_smem[];   // [kRing][x and dy][N]
+// kMax = 640, or 1024 for the 16-bit rows above 8192 channels, where the registers leave no room
+// to hold the weights.
+template <class T, int kMax>
+__global__ void __launch_bounds__(kMax) ln_bwd_ring_kernel(const LnParams p) {
+  constexpr int kValues = 16;
+  constexpr bool kHold = kMax <= 640;
+  constexpr int kN = Piece<T>::kN, kPieces = kValues / kN;
+  extern __shared__ __align__(16) uint8_t rows_smem[];   // [ring][x and dy][N]
   __shared__ RowRing ring;
   __shared__ float scratch[2][32][2];
   const int tid = threadIdx.x, threads = blockDim.x, bytes = p.N * (int)sizeof(T);
   ring_init(ring);
-  float w[kValues], dw[kValues] = {}, db[kValues] = {};
+  float w[kHold ? kValues : 1], dw[kValues] = {}, db[kValues] = {};
 #pragma unroll
-  for (int k = 0; k < kPieces; ++k) load_weights<true, kN>(p.w, (tid + k * threads) * kN, 1.0f, p, w + k * kN);
+  for (int k = 0; k < (kHold ? kPieces : 0); ++k) load_weights<true, kN>(p.w, (tid + k * threads) * kN, 1.0f, p, w + k * kN);
   const float inv_n = 1.0f / (float)p.N;
+  auto place = [&](const Rows& r, int row) { return kHold ? row_in_ring(p, r, row) : row_at(p, r, row); };
   int issued = 0, turn = 0;
-  auto issue = [&](int i) {   // (thread 0)
-    const int row = (int)blockIdx.x + i * (int)gridDim.x;
+  auto issue = [&](long long row, int slot) {   // (thread 0)
     if (row >= p.rows) return;
-    uint8_t* to = rows_smem + (i % kRing) * 2 * bytes;
-    uint64_t* bar = &ring.full[i % kRing];
+    uint8_t* to = rows_smem + slot * 2 * bytes;
+    uint64_t* bar = &ring.full[slot];
     mbar_arrive_expect_tx(bar, 2 * bytes);
-    bulk_load(to, reinterpret_cast<const T*>(p.x) + row_at(p, p.xs, row), bytes, bar);
-    bulk_load(to + bytes, reinterpret_cast<const T*>(p.dy) + row_at(p, p.dys, row), bytes, bar);
+    bulk_load(to, reinterpret_cast<const T*>(p.x) + place(p.xs, (int)row), bytes, bar);
+    bulk_load(to + bytes, reinterpret_cast<const T*>(p.dy) + place(p.dys, (int)row), bytes, bar);
     ++issued;
   };
   if (tid == 0)
-    for (int i = 0; i < kRing; ++i) issue(i);
+    for (int i = 0; i < p.ring; ++i) issue(blockIdx.x + (long long)i * gridDim.x, i);
   float next_mean = 0.0f, next_rstd = 0.0f;
   if ((int)blockIdx.x < p.rows) {
     next_mean = __ldg(p.mean + blockIdx.x);
     next_rstd = __ldg(p.rstd + blockIdx.x);
   }
-  for (int row = blockIdx.x, i = 0; row < p.rows; row += gridDim.x, ++i) {
+  for (int row = blockIdx.x, i = 0, slot = 0, phase = 0; row < p.rows; row += gridDim.x, ++i) {
     const float m = next_mean, rs = next_rstd;
     if (row + (int)gridDim.x < p.rows) {
       next_mean = __ldg(p.mean + row + gridDim.x);
       next_rstd = __ldg(p.rstd + row + gridDim.x);
     }
-    const uint4* sx = reinterpret_cast<const uint4*>(rows_smem + (i % kRing) * 2 * bytes);
-    const uint4* sd = reinterpret_cast<const uint4*>(rows_smem + (i % kRing) * 2 * bytes + bytes);
-    ring_wait(ring, i);
+    const uint4* sx = reinterpret_cast<const uint4*>(rows_smem + slot * 2 * bytes);
+    const uint4* sd = reinterpret_cast<const uint4*>(rows_smem + slot * 2 * bytes + bytes);
+    ring_wait(ring, slot, phase);
     float s[2], s0[2] = {0.0f, 0.0f}, s1[2] = {0.0f, 0.0f};   // sums of g and of g xhat
 #pragma unroll
     for (int k = 0; k < kPieces; ++k) {
       const int at = tid + k * threads;
       if (at * kN >= p.N) continue;
-      float x[kN], d[kN];
+      float x[kN], d[kN], lw[kHold ? 1 : kN];
+      if (!kHold) load_weights<true, kN>(p.w, at * kN, 1.0f, p, lw);
+      const float* pw = kHold ? &w[kHold ? k * kN : 0] : lw;
       unpack<T>(sx[at], x);
       unpack<T>(sd[at], d);
 #pragma unroll
@@ -589,7 +634,7 @@ __global__ void __launch_bounds__(640) ln_bwd_ring_kernel(const LnParams p) {
         float xh[2], g[2];
         fadd2(xh[0], xh[1], x[e], x[e + 1], -m, -m);
         fmul2(xh[0], xh[1], xh[0], xh[1], rs, rs);
-        fmul2(g[0], g[1], d[e], d[e + 1], w[a], w[a + 1]);
+        fmul2(g[0], g[1], d[e], d[e + 1], pw[e], pw[e + 1]);
         ffma2(dw[a], dw[a + 1], d[e], d[e + 1], xh[0], xh[1], dw[a], dw[a + 1]);
         fadd2(db[a], db[a + 1], db[a], db[a + 1], d[e], d[e + 1]);
         fadd2(s0[0], s0[1], s0[0], s0[1], g[0], g[1]);
@@ -600,28 +645,33 @@ __global__ void __launch_bounds__(640) ln_bwd_ring_kernel(const LnParams p) {
     s[1] = s1[0] + s1[1];
     row_sums<0>(s, scratch, turn);
     // (all threads have met: they are done with the row before this one, and its place is free)
-    if (tid == 0 && i > 0) issue(i - 1 + kRing);
+    if (tid == 0 && i > 0) issue(row + (long long)(p.ring - 1) * gridDim.x, slot == 0 ? p.ring - 1 : slot - 1);
     const float m0 = -s[0] * inv_n, m1 = -s[1] * inv_n;
-    T* dx = reinterpret_cast<T*>(p.dx) + row_at(p, p.dxs, row);
+    T* dx = reinterpret_cast<T*>(p.dx) + place(p.dxs, row);
 #pragma unroll
     for (int k = 0; k < kPieces; ++k) {
       const int at = tid + k * threads;
       if (at * kN >= p.N) continue;
-      float x[kN], d[kN], out[kN];
+      float x[kN], d[kN], out[kN], lw[kHold ? 1 : kN];
+      if (!kHold) load_weights<true, kN>(p.w, at * kN, 1.0f, p, lw);
+      const float* pw = kHold ? &w[kHold ? k * kN : 0] : lw;
       unpack<T>(sx[at], x);
       unpack<T>(sd[at], d);
 #pragma unroll
       for (int e = 0; e < kN; e += 2) {
-        const int a = k * kN + e;
         float xh[2], g[2];
         fadd2(xh[0], xh[1], x[e], x[e + 1], -m, -m);
         fmul2(xh[0], xh[1], xh[0], xh[1], rs, rs);
-        fmul2(g[0], g[1], d[e], d[e + 1], w[a], w[a + 1]);
+        fmul2(g[0], g[1], d[e], d[e + 1], pw[e], pw[e + 1]);
         ffma2(g[0], g[1], xh[0], xh[1], m1, m1, g[0], g[1]);
         fadd2(g[0], g[1], g[0], g[1], m0, m0);
         fmul2(out[e], out[e + 1], g[0], g[1], rs, rs);
       }
       store_piece<true, T>(dx, at * kN, out, p);
+    }
+    if (++slot == p.ring) {
+      slot = 0;
+      ++phase;
     }
   }
   if (p.partial != nullptr) {   // this CTA's sums: [2][CTAs][N]
@@ -640,8 +690,8 @@ __global__ void __launch_bounds__(640) ln_bwd_ring_kernel(const LnParams p) {
     }
   }
   if (tid == 0 && ring.abort_flag)
-    for (int i = issued > kRing ? issued - kRing : 0; i < issued; ++i)
-      mbar_wait_teardown(&ring.full[i % kRing], (i / kRing) & 1);
+    for (int i = issued > p.ring ? issued - p.ring : 0; i < issued; ++i)
+      mbar_wait_teardown(&ring.full[i % p.ring], (i / p.ring) & 1);
 }
 
 // dw and db from the CTAs' sums: a block takes 32 channels of one of them, its 32 warps every 32nd CTA.
@@ -667,6 +717,9 @@ __global__ void __launch_bounds__(1024) ln_grad_kernel(const float* partial, int
   else reinterpret_cast<__half*>(to)[out] = __float2half_rn(v);
 }
 
+// Rows of a warp under way ahead of the one worked on: as many as the registers hold.
+template <class T, bool kVec, bool kBackward>
+constexpr int kWarpRows = !kVec ? 1 : sizeof(T) == 2 ? 3 : kBackward ? 2 : 1;
 struct Shape {
   int lanes, threads, ctas;
   bool wide;   // 32 channels a thread
@@ -684,18 +737,13 @@ Shape shape_of(int rows, int N, bool backward) {
     s.ctas = (rows + per - 1) / per;
   } else {
     s.wide = N > 8192;
-    const int per = s.wide ? 32 : 16;
+    const int per = s.wide && !backward ? 32 : 16;   // (the backward's wide rows: see below)
     s.threads = ((N + per - 1) / per + 31) / 32 * 32;
     s.ctas = rows;
   }
-  // CTAs that an SM holds by registers (what the launch bounds allow a thread) and, in the rings, by
-  // shared memory
-  const int regs = s.wide ? 128 : backward ? 96 : s.lanes ? 88 : 80;
+  // CTAs that an SM holds by their registers (what the launch bounds allow a thread)
+  const int regs = backward && s.wide ? 64 : s.wide ? 128 : 96;
   int per_sm = 65536 / (regs * s.threads);
-  if (s.lanes == 0 && !s.wide) {
-    const int ring = kRing * (backward ? 2 : 1) * 4 * N;   // (of the widest type)
-    if (per_sm > 220000 / ring) per_sm = 220000 / ring;
-  }
   if (per_sm < 1) per_sm = 1;
   const int cap = kSms * per_sm;
   if (s.ctas > cap) s.ctas = cap;
@@ -712,7 +760,7 @@ template <class T, bool kVec, int kLanes, int kValues, bool kBackward>
 cudaError_t launch_one(const LnParams& p, const Shape& s, cudaStream_t stream) {
   const dim3 grid((unsigned)s.ctas);
   if constexpr (kBackward) {
-    auto* kernel = ln_bwd_kernel<T, kVec, kLanes, kValues, (kLanes > 0 ? 640 : 512)>;
+    auto* kernel = ln_bwd_kernel<T, kVec, kLanes, kValues, (kLanes > 0 ? kWarpRows<T, kVec, true> : 1), (kLanes > 0 ? 640 : 512)>;
     if constexpr (kValues == 32) {
       static ContextOnce attr_done;
       const cudaError_t e = attr_done.run([&] {
@@ -722,32 +770,39 @@ cudaError_t launch_one(const LnParams& p, const Shape& s, cudaStream_t stream) {
     }
     return launch_dependent(kernel, grid, s.threads, bwd_smem(s, p.N), stream, p);
   } else {
-    return launch_dependent(ln_fwd_kernel<T, kVec, kLanes, kValues, (kValues == 32 ? 512 : 704)>, grid, s.threads, 0,
+    return launch_dependent(ln_fwd_kernel<T, kVec, kLanes, kValues, (kLanes > 0 ? kWarpRows<T, kVec, false> : 1), (kValues == 32 ? 512 : 640)>, grid, s.threads, 0,
                             stream, p);
   }
 }
 template <class T, bool kBackward>
 cudaError_t launch_ring(const LnParams& p, const Shape& s, cudaStream_t stream) {
-  static ContextOnce attr_done;
-  auto* kernel = kBackward ? ln_bwd_ring_kernel<T> : ln_fwd_ring_kernel<T>;
-  const cudaError_t e = attr_done.run([&] {
-    return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, 226 * 1024);
+  static ContextOnce attr_done[2];
+  auto* kernel = !kBackward ? ln_fwd_ring_kernel<T> : s.wide ? ln_bwd_ring_kernel<T, 1024> : ln_bwd_ring_kernel<T, 640>;
+  const cudaError_t e = attr_done[s.wide].run([&] {
+    return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, 220 * 1024);
   });
   if (e != cudaSuccess) return e;
-  return launch_dependent(kernel, dim3((unsigned)s.ctas), s.threads,
-                          (size_t)kRing * (kBackward ? 2 : 1) * p.N * sizeof(T), stream, p);
+  const size_t row = (size_t)p.N * sizeof(T);   // at most 32 KB
+  LnParams q = p;
+  const int per_sm = s.wide ? 1 : 65536 / (96 * s.threads);
+  q.ring = 6 * row * per_sm <= 220 * 1024 ? 3 : 2;
+  return launch_dependent(kernel, dim3((unsigned)s.ctas), s.threads, kBackward ? 2 * q.ring * row : 4 * row, stream, q);
 }
 template <class T, bool kVec, bool kBackward>
 cudaError_t launch_typed(const LnParams& p, const Shape& s, cudaStream_t stream) {
   if constexpr (kVec)
-    if (s.lanes == 0 && !s.wide) return launch_ring<T, kBackward>(p, s, stream);
+    if (s.lanes == 0 && (!s.wide || (kBackward && sizeof(T) == 2))) return launch_ring<T, kBackward>(p, s, stream);
   switch (s.lanes) {
     case 4: return launch_one<T, kVec, 4, kBackward ? 8 : 16, kBackward>(p, s, stream);
     case 8: return launch_one<T, kVec, 8, kBackward ? 8 : 16, kBackward>(p, s, stream);
     case 16: return launch_one<T, kVec, 16, kBackward ? 8 : 16, kBackward>(p, s, stream);
     case 32: return launch_one<T, kVec, 32, kBackward ? 8 : 16, kBackward>(p, s, stream);
   }
-  if (s.wide) return launch_one<T, kVec, 0, 32, kBackward>(p, s, stream);
+  if (s.wide) {   // 32 channels a thread, in the backward too
+    Shape t = s;
+    t.threads = ((p.N + 31) / 32 + 31) / 32 * 32;
+    return launch_one<T, kVec, 0, 32, kBackward>(p, t, stream);
+  }
   return launch_one<T, false, 0, 16, kBackward>(p, s, stream);
 }
 template <bool kBackward>
@@ -779,8 +834,12 @@ bool whole(const void* ptr, const long long* str, const LayerNormArgs& a) {
   return (reinterpret_cast<uintptr_t>(ptr) & 15u) == 0 && (a.B == 1 || str[0] % n == 0) && (a.S == 1 || str[1] % n == 0) &&
          (a.H == 1 || str[2] % n == 0);
 }
-void set_rows(Rows& r, const long long* str) {
+void set_rows(Rows& r, const long long* str, const LayerNormArgs& a) {
   for (int i = 0; i < 3; ++i) r.str[i] = str[i];
+  // (the stride of a dimension of one says nothing)
+  if (a.H == 1) r.str[2] = a.S > 1 ? r.str[1] : r.str[0];
+  r.even = (a.H == 1 || a.S == 1 || r.str[1] == a.H * r.str[2]) &&
+           (a.B == 1 || (a.H == 1 && a.S == 1) || r.str[0] == (long long)a.S * a.H * r.str[2]);
 }
 
 }  // namespace
@@ -790,8 +849,8 @@ size_t layer_norm_bwd_workspace(int rows, int N) { return (size_t)2 * shape_of(r
 cudaError_t launch_layer_norm_fwd(const LayerNormArgs& a, void* y, const long long y_str[3], cudaStream_t stream) {
   LnParams p = params_of(a);
   p.y = y;
-  set_rows(p.xs, a.x_str);
-  set_rows(p.ys, y_str);
+  set_rows(p.xs, a.x_str, a);
+  set_rows(p.ys, y_str, a);
   const bool w16 = ((reinterpret_cast<uintptr_t>(a.w) | reinterpret_cast<uintptr_t>(a.b)) & 15u) == 0;
   const bool vec = a.N % (a.type == kF32 ? 4 : 8) == 0 && whole(a.x, a.x_str, a) && whole(y, y_str, a) && w16;
   return launch_any<false>(p, shape_of(p.rows, p.N, false), a.type, vec, stream);
@@ -803,9 +862,9 @@ cudaError_t launch_layer_norm_bwd(const LayerNormArgs& a, const void* dy, const 
   LnParams p = params_of(a);
   p.dy = dy;
   p.dx = dx;
-  set_rows(p.xs, a.x_str);
-  set_rows(p.dys, dy_str);
-  set_rows(p.dxs, dx_str);
+  set_rows(p.xs, a.x_str, a);
+  set_rows(p.dys, dy_str, a);
+  set_rows(p.dxs, dx_str, a);
   const bool w16 = (reinterpret_cast<uintptr_t>(a.w) & 15u) == 0;
   const bool vec = a.N % (a.type == kF32 ? 4 : 8) == 0 && whole(a.x, a.x_str, a) && whole(dy, dy_str, a) &&
                    whole(dx, dx_str, a) && w16;
