@@ -111,7 +111,8 @@ struct BwdParams {
   int Sq_pad;
   __nv_bfloat16 *d0, *d1;   // dQ; or dK and dV
   long long s0[3], s1[3];   // their element strides (b, s, h)
-  int H, group, BH;         // heads of this grid (Hkv, or Hq), Hq / Hkv, B * H
+  int H, group;             // heads of this grid (Hkv, or Hq), Hq / Hkv
+  Order order;
 };
 
 // Q(i) is held from S(i) to dK(i), most of two steps, and S(i+2) follows dK(i) closely: with two
@@ -144,16 +145,12 @@ struct ItemKV {
 };
 __device__ __forceinline__ ItemKV item_kv(const BwdParams& p, const Work& w) {
   ItemKV i;
-  const int bh = w.head;
-  i.b = bh / p.H;
-  i.hk = bh % p.H;
-  i.key0 = w.x * kTile;
+  int tile, head;
+  work_place(p.order, w, tile, head);
+  i.b = head / p.H;
+  i.hk = head % p.H;
+  i.key0 = tile * kTile;
   i.n_q = (p.mask.Sq + kTile - 1) / kTile;
-  if (bh >= p.BH) {   // the last grid.z slice may run past B * H
-    i.keys = i.n = i.first = 0;
-    i.key0 = p.mask.Sk;
-    return i;
-  }
   i.keys = key_count(p.mask, i.b);
   // causal: query i sees key j when j <= i + Sk - Sq, so the tile's first key starts the queries
   i.first = p.mask.causal ? max(i.key0 - (p.mask.Sk - p.mask.Sq), 0) / kTile : 0;
@@ -533,16 +530,12 @@ struct ItemQ {
 };
 __device__ __forceinline__ ItemQ item_q(const BwdParams& p, const Work& w) {
   ItemQ i;
-  const int bh = w.head;
-  i.b = bh / p.H;
-  i.h = bh % p.H;
+  int tile, head;
+  work_place(p.order, w, tile, head);
+  i.b = head / p.H;
+  i.h = head % p.H;
   // the last queries have the most keys when the mask is causal: they start first
-  i.row0 = (p.mask.causal ? (int)(gridDim.x - 1 - w.x) : w.x) * kTile;
-  if (bh >= p.BH) {
-    i.keys = i.n = 0;
-    i.row0 = p.mask.Sq;
-    return i;
-  }
+  i.row0 = (p.mask.causal ? p.order.tiles - 1 - tile : tile) * kTile;
   i.keys = key_count(p.mask, i.b);
   i.n = (row_limit(p.mask, i.keys, min(i.row0 + kTile, p.mask.Sq) - 1) + kTile - 1) / kTile;
   return i;
@@ -901,22 +894,23 @@ cudaError_t launch_attn_bwd_bf16(const CUtensorMap& tm_q, const CUtensorMap& tm_
   p.Sq_pad = Sq_pad;
   p.group = a.Hq / a.Hkv;
   p.H = a.Hkv;
-  p.BH = a.B * a.Hkv;
+  const int k_tiles = (a.Sk + kTile - 1) / kTile, q_tiles = Sq_pad / kTile;
+  p.order = {k_tiles, a.B * a.Hkv, a.causal ? causal_group(k_tiles, a.B * a.Hkv) : 1};
   p.d0 = reinterpret_cast<__nv_bfloat16*>(t.dk);
   p.d1 = reinterpret_cast<__nv_bfloat16*>(t.dv);
   for (int i = 0; i < 3; ++i) {
     p.s0[i] = t.dk_str[i];
     p.s1[i] = t.dv_str[i];
   }
-  e = launch_dependent(dkdv_kernel, heads_grid((a.Sk + kTile - 1) / kTile, p.BH), kThreads, kSmemKV, stream, tm_q,
+  e = launch_dependent(dkdv_kernel, dim3((unsigned)k_tiles * (unsigned)p.order.heads), kThreads, kSmemKV, stream, tm_q,
                        tm_k, tm_v, tm_d, p);
   if (e != cudaSuccess) return e;
   p.H = a.Hq;
-  p.BH = a.B * a.Hq;
+  p.order = {q_tiles, a.B * a.Hq, a.causal ? causal_group(q_tiles, a.B * a.Hq) : 1};
   p.d0 = reinterpret_cast<__nv_bfloat16*>(t.dq);
   p.d1 = nullptr;
   for (int i = 0; i < 3; ++i) p.s0[i] = t.dq_str[i];
-  return launch_dependent(dq_kernel, heads_grid((a.Sq + kTile - 1) / kTile, p.BH), kThreads, kSmemQ, stream, tm_q,
+  return launch_dependent(dq_kernel, dim3((unsigned)q_tiles * (unsigned)p.order.heads), kThreads, kSmemQ, stream, tm_q,
                           tm_k, tm_v, tm_d, p);
 }
 

@@ -58,7 +58,8 @@ struct Params {
   __nv_bfloat16* o;
   long long o_sb, o_ss, o_sh;
   float* lse;     // [B, Hq, Sq]
-  int Hq, group, BH;
+  int Hq, group;
+  Order order;
 };
 
 __device__ __forceinline__ float u2f(uint32_t u) { return __uint_as_float(u); }
@@ -70,16 +71,12 @@ struct Item {
 };
 __device__ __forceinline__ Item item_of(const Params& p, const Work& w) {
   Item i;
-  const int bh = w.head;
-  i.b = bh / p.Hq;
-  i.h = bh % p.Hq;
+  int tile, head;
+  work_place(p.order, w, tile, head);
+  i.b = head / p.Hq;
+  i.h = head % p.Hq;
   // the last queries have the most keys when the mask is causal: they start first
-  i.row0 = (p.mask.causal ? (int)(gridDim.x - 1 - w.x) : w.x) * (kNQ * kTile);
-  if (bh >= p.BH) {   // the last grid.z slice may run past B * Hq
-    i.keys = i.n = 0;
-    i.row0 = p.mask.Sq;
-    return i;
-  }
+  i.row0 = (p.mask.causal ? p.order.tiles - 1 - tile : tile) * (kNQ * kTile);
   i.keys = key_count(p.mask, i.b);
   i.n = (row_limit(p.mask, i.keys, min(i.row0 + kNQ * kTile, p.mask.Sq) - 1) + kTile - 1) / kTile;
   return i;
@@ -430,9 +427,10 @@ cudaError_t launch_attn_fwd_bf16_lse(const CUtensorMap& tm_q, const CUtensorMap&
   p.lse = lse;
   p.Hq = a.Hq;
   p.group = a.Hq / a.Hkv;
-  p.BH = a.B * a.Hq;
-  return launch_dependent(lse_fwd_kernel, heads_grid((a.Sq + kNQ * kTile - 1) / (kNQ * kTile), p.BH), kThreads,
-                          kSmemBytes, stream, tm_q, tm_k, tm_v, p);
+  const int tiles = (a.Sq + kNQ * kTile - 1) / (kNQ * kTile), heads = a.B * a.Hq;
+  p.order = {tiles, heads, a.causal ? causal_group(tiles, heads) : 1};
+  return launch_dependent(lse_fwd_kernel, dim3((unsigned)tiles * (unsigned)heads), kThreads, kSmemBytes, stream, tm_q,
+                          tm_k, tm_v, p);
 }
 
 cudaError_t read_and_clear_err_lse(uint32_t* out) {

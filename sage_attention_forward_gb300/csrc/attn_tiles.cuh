@@ -68,16 +68,27 @@ struct WorkRing {
   uint64_t full[kWorkSlots], empty[kWorkSlots];
 };
 struct Work {
-  int x, head;   // the item's place in the grid (heads_grid)
-  int t;         // how many came before it in this CTA
+  int index;   // the item's place in the grid
+  int t;       // how many came before it in this CTA
 };
-__device__ __forceinline__ Work first_work() { return {(int)blockIdx.x, (int)(blockIdx.y + gridDim.y * blockIdx.z), 0}; }
+__device__ __forceinline__ Work first_work() { return {(int)blockIdx.x, 0}; }
 __device__ __forceinline__ bool work_answer(const uint4* answer, Work& w) {
   uint32_t x = 0, y = 0, z = 0;
   if (!clc_answer(answer, x, y, z)) return false;
-  w.x = (int)x;
-  w.head = (int)(y + gridDim.y * z);
+  w.index = (int)x;
   return true;
+}
+// Items are (tile, head); `group` heads go together, tile by tile: one head after another (group = 1) keeps
+// few heads' tiles in L2, and where a causal mask makes the first tiles of a head the longest
+// items, several heads' long ones come before their short ones, so that the grid ends with short ones.
+struct Order {
+  int tiles, heads, group;
+};
+__device__ __forceinline__ void work_place(const Order& o, const Work& w, int& tile, int& head) {
+  const int first = w.index / (o.group * o.tiles) * o.group;   // the group's first head
+  const int at = w.index - first * o.tiles, n = min(o.group, o.heads - first);
+  tile = at / n;
+  head = first + at % n;
 }
 __device__ __forceinline__ void work_init(WorkRing& r, int reader_warps) {
   for (int s = 0; s < kWorkSlots; ++s) {

@@ -215,10 +215,11 @@ cudaError_t launch_layer_norm_bwd(const LayerNormArgs& a, const void* dy, const 
                                   const long long dx_str[3], void* dw, void* db, float* workspace,
                                   cudaStream_t stream);
 
-// Heads along grid.y and, beyond 65535 of them, grid.z.
-inline dim3 heads_grid(long long tiles, int heads) {
-  const unsigned ny = (unsigned)(heads < 65535 ? heads : 65535);
-  return dim3((unsigned)tiles, ny, (heads + ny - 1) / ny);
+// Heads that go together in the grid under a causal mask: four items per SM, so that the items in hand
+// at the grid's end are a group's short ones.
+inline int causal_group(int tiles, int heads) {
+  const int want = (4 * 152 + tiles - 1) / tiles;
+  return want < heads ? want : heads;
 }
 
 // A launch as a programmatic dependent of the previous kernel in the stream: the kernel may set
