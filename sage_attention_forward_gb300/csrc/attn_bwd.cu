@@ -11,14 +11,16 @@
 // one key has p = 1 whatever its score, so its ds is 0; it is set so, and not left to the
 // rounding of dp - delta.
 //
-// Three kernels, no atomics: every sum has one order.
-//   rows_kernel   -lse * log2 e and -delta of each row, padded to whole tiles (-inf and 0 there,
-//                 and for empty rows: their probabilities come out as 0).  Reads dO and O once.
-//   dkdv_kernel   one CTA per (128 keys, key head): K and V stay in shared memory, Q and dO tiles
-//                 stream by.  The transposed scores S^T = K Q^T and dP^T = V dO^T leave P^T and
-//                 dS^T in TMEM as the A operands of dV += P^T dO and dK += dS^T Q.
-//   dq_kernel     one CTA per (128 queries, query head): Q and dO stay, K and V stream by:
-//                 S = Q K^T, dP = dO V^T, dQ += dS K.
+// Two kernels, no atomics: every sum has one order.
+//   dq_kernel     one item per (128 queries, query head): Q and dO stay, K and V stream by:
+//                 S = Q K^T, dP = dO V^T, dQ += dS K.  It forms delta of its rows from dO, which it has,
+//                 and O, and leaves -lse * log2 e and -delta in the workspace, padded to whole tiles
+//                 (-inf and 0 there and for empty rows: their probabilities come out as 0).
+//   dkdv_kernel   one item per (128 keys, key head): K and V stay in shared memory, Q and dO tiles
+//                 stream by with those statistics.  The transposed scores S^T = K Q^T and
+//                 dP^T = V dO^T leave P^T and dS^T in TMEM as the A operands of dV += P^T dO and
+//                 dK += dS^T Q.
+// (A kernel of its own for the statistics read dO once more: 48 us of 386 at 16896 queries on 512 keys.)
 // Seven products of a tile pair against five if one kernel did both, but a dQ that several CTAs
 // add into needs either atomics, whose order changes the result, or 64 KB of FP32 traffic a
 // tile pair: at 2560 cycles a pair and 152 SMs that is 7 TB/s of reductions in L2.
@@ -51,64 +53,17 @@ __device__ uint32_t g_err_bwd;
 
 __device__ __forceinline__ float u2f(uint32_t u) { return __uint_as_float(u); }
 
-// ------------------------------------------------------------------ row statistics
-struct RowsParams {
-  const __nv_bfloat16* o;
-  const __nv_bfloat16* dout;
-  long long o_s[3], d_s[3];   // element strides (b, s, h)
-  const float* lse;           // [B, Hq, Sq]
-  float* neg_lse2;            // [B * Hq, Sq_pad]
-  float* neg_delta;
-  int Sq, Sq_pad, Hq;
-  long long rows;             // B * Hq * Sq_pad
-};
-
-// Half a warp per row, 16 bytes of O and dO per thread.  Consecutive rows of a warp are
-// consecutive heads of one token, which are neighbours in memory in the usual layout.
-__global__ void __launch_bounds__(256) rows_kernel(const RowsParams p) {
-  griddep_wait();
-  const int sub = threadIdx.x & 15;
-  const long long step = (long long)gridDim.x * 16;
-  for (long long it = (long long)blockIdx.x * 16 + (threadIdx.x >> 4); it < p.rows; it += step) {
-    const int h = (int)(it % p.Hq);
-    const long long bs = it / p.Hq;
-    const int s = (int)(bs % p.Sq_pad), b = (int)(bs / p.Sq_pad);
-    const long long out = ((long long)b * p.Hq + h) * p.Sq_pad + s;
-    float nl = -INFINITY, nd = 0.0f;
-    if (s < p.Sq) {
-      const uint4 x = __ldg(reinterpret_cast<const uint4*>(p.o + b * p.o_s[0] + s * p.o_s[1] + h * p.o_s[2]) + sub);
-      const uint4 y = __ldg(reinterpret_cast<const uint4*>(p.dout + b * p.d_s[0] + s * p.d_s[1] + h * p.d_s[2]) + sub);
-      const uint32_t xs[4] = {x.x, x.y, x.z, x.w}, ys[4] = {y.x, y.y, y.z, y.w};
-      float a = 0.0f;
-#pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        a = fmaf(u2f(xs[e] << 16), u2f(ys[e] << 16), a);
-        a = fmaf(u2f(xs[e] & 0xffff0000u), u2f(ys[e] & 0xffff0000u), a);
-      }
-      const uint32_t half = 0xffffu << (threadIdx.x & 16);   // a row's 16 threads are in step with one another
-#pragma unroll
-      for (int d = 8; d >= 1; d >>= 1) a += __shfl_xor_sync(half, a, d);
-      const float lse = __ldg(p.lse + ((long long)b * p.Hq + h) * p.Sq + s);
-      if (lse != -INFINITY) {
-        nl = -lse * kLog2e;
-        nd = -a;
-      }
-    }
-    if (sub == 0) {
-      p.neg_lse2[out] = nl;
-      p.neg_delta[out] = nd;
-    }
-  }
-}
-
 // ------------------------------------------------------------------ dK, dV
 struct BwdParams {
   Mask mask;
   float c_log2;           // softmax_scale * log2 e
   float scale;            // softmax_scale
-  const float* neg_lse2;  // [B * Hq, Sq_pad]
-  const float* neg_delta;
+  float* neg_lse2;        // [B * Hq, Sq_pad]: written by dq_kernel, read by dkdv_kernel
+  float* neg_delta;
   int Sq_pad;
+  const __nv_bfloat16* o;   // (dq_kernel)
+  long long o_s[3];
+  const float* lse;         // [B, Hq, Sq]
   __nv_bfloat16 *d0, *d1;   // dQ; or dK and dV
   long long s0[3], s1[3];   // their element strides (b, s, h)
   int H, group;             // heads of this grid (Hkv, or Hq), Hq / Hkv
@@ -518,6 +473,8 @@ struct __align__(1024) SmemQ {
   uint64_t s_full, s_free;     // S in TMEM; read by every softmax warp
   uint64_t dp_full;
   uint64_t ds_full, ds_free;   // dS stored in TMEM by every softmax warp; read by dQ's product
+  float delta[kGroups][kTile];   // each warpgroup's part of the rows' sums
+  uint64_t delta_full;
   uint64_t acc_done;
   uint64_t drain;
   uint32_t tmem_base;
@@ -558,7 +515,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     mbar_init(&sm.q_empty, kWarpLoad);
     mbar_init(&sm.q_ready, kWarpLoad);
     mbar_init(&sm.d_full, 1);
-    mbar_init(&sm.d_empty, 1);
+    mbar_init(&sm.d_empty, 1 + kWarpLoad);   // the last dP, and every softmax warp's part of delta
     for (int s = 0; s < kKRing; ++s) {
       mbar_init(&sm.k_full[s], 1);
       mbar_init(&sm.k_empty[s], 1);
@@ -573,6 +530,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     mbar_init(&sm.dp_full, 1);
     mbar_init(&sm.ds_full, kWarpLoad);
     mbar_init(&sm.ds_free, 1);
+    mbar_init(&sm.delta_full, kWarpLoad);
     mbar_init(&sm.acc_done, 1);
     mbar_init(&sm.drain, 2);
     sm.abort_flag = 0;
@@ -721,14 +679,10 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint32_t lane_off = (uint32_t)(wq * 32) << 16;
     bool ok = true;
     int it = 0, items = 0, turn = 0;
-    // Q from its tile in shared memory to TMEM, 32 channels of a row per thread: as the A operand
-    // from shared memory it would be read again for every key tile, at the full rate of shared
-    // memory while S runs.  (Row r's 16-byte piece c of a half is at c ^ (r & 7).)
-    auto copy_q = [&](int item) -> bool {
-      if (!mbar_wait_warp<false>(&sm.q_full, item & 1, abort_flag, err, kErrTimeoutTma)) return false;
-      const int r = wq * 32 + lane;
-      const uint8_t* src = sm.q + (g >> 1) * kHalfBytes + r * 128;
-      uint32_t x[16];
+    const int r = wq * 32 + lane;   // the thread's row of a tile
+    // the warpgroup's 32 channels of the row in a tile (row r's 16-byte piece c of a half is at c ^ (r & 7))
+    auto tile_row = [&](const uint8_t* tile, uint32_t (&x)[16]) {
+      const uint8_t* src = tile + (g >> 1) * kHalfBytes + r * 128;
 #pragma unroll
       for (int c = 0; c < 4; ++c) {
         const uint4 v = *reinterpret_cast<const uint4*>(src + ((((g & 1) * 4 + c) ^ (r & 7)) << 4));
@@ -737,6 +691,15 @@ __global__ void __launch_bounds__(kThreads, 1)
         x[4 * c + 2] = v.z;
         x[4 * c + 3] = v.w;
       }
+    };
+    // Q from its tile in shared memory to TMEM: as the A operand from shared memory it would be read
+    // again for every key tile, at the full rate of shared memory while S runs.  With it the loads of
+    // the row's O are started.
+    uint4 o4[4];
+    auto begin_item = [&](int n, const ItemQ& item) -> bool {
+      if (!mbar_wait_warp<false>(&sm.q_full, n & 1, abort_flag, err, kErrTimeoutTma)) return false;
+      uint32_t x[16];
+      tile_row(sm.q, x);
       tmem_st16(tQ + lane_off + 16 * g, x);
       tmem_st_wait();
       tc_fence_before();
@@ -745,24 +708,70 @@ __global__ void __launch_bounds__(kThreads, 1)
         mbar_arrive(&sm.q_empty);
         mbar_arrive(&sm.q_ready);
       }
+      const int row = item.row0 + r;
+      const uint4* src = reinterpret_cast<const uint4*>(p.o + (long long)item.b * p.o_s[0] + (long long)row * p.o_s[1] +
+                                                        (long long)item.h * p.o_s[2] + 32 * g);
+#pragma unroll
+      for (int c = 0; c < 4; ++c) o4[c] = row < p.mask.Sq ? __ldg(src + c) : make_uint4(0u, 0u, 0u, 0u);
       return true;
     };
-    if (item_q(p, first_work()).n > 0) ok = copy_q(0);
+    // -delta of the row, from the O in registers and dO's tile
+    auto find_delta = [&](int n, float& neg_delta) -> bool {
+      if (!mbar_wait_warp<false>(&sm.d_full, n & 1, abort_flag, err, kErrTimeoutTma)) return false;
+      uint32_t x[16];
+      tile_row(sm.dout, x);
+      float a = 0.0f;
+#pragma unroll
+      for (int c = 0; c < 4; ++c) {
+        const uint32_t o[4] = {o4[c].x, o4[c].y, o4[c].z, o4[c].w};
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          a = fmaf(u2f(o[e] << 16), u2f(x[4 * c + e] << 16), a);
+          a = fmaf(u2f(o[e] & 0xffff0000u), u2f(x[4 * c + e] & 0xffff0000u), a);
+        }
+      }
+      sm.delta[g][r] = a;
+      __syncwarp();
+      if (lane == 0) {
+        mbar_arrive(&sm.d_empty);
+        mbar_arrive(&sm.delta_full);
+      }
+      // (the parts are next written in the next item, which no warp comes to before all have dS of this one)
+      if (!mbar_wait_warp<false>(&sm.delta_full, n & 1, abort_flag, err, kErrTimeoutSync)) return false;
+      neg_delta = -((sm.delta[0][r] + sm.delta[1][r]) + (sm.delta[2][r] + sm.delta[3][r]));
+      return true;
+    };
+    static_assert(kGroups == 4, "four parts of delta");
+    {
+      const ItemQ item = item_q(p, first_work());
+      if (item.n > 0) ok = begin_item(0, item);
+    }
     bool more = ok;
     while (more) {
-      const ItemQ item = item_q(p, work_read(sm.work, turn));
-      const int row = item.row0 + wq * 32 + lane;
-      // a row that sees one key has ds = 0: as a row that sees none
-      int limit = row_limit(p.mask, item.keys, row);
-      if (limit == 1) limit = 0;
-      int valid = limit - kCols * g;   // what is left of the keys that this row sees, from the group's first
-      float nl = 0.0f, nd = 0.0f;
-      if (item.n > 0) {   // (rows past Sq have their statistics in the padding)
-        const long long at = ((long long)item.b * p.H + item.h) * p.Sq_pad + row;
-        nl = __ldg(p.neg_lse2 + at);
-        nd = __ldg(p.neg_delta + at);
+      int n, valid;   // products left, and what is left of the keys that this row sees, from the group's first
+      float nl = -INFINITY, nd = 0.0f;
+      {
+        const ItemQ item = item_q(p, work_read(sm.work, turn));
+        const int row = item.row0 + r;
+        n = item.n;
+        // a row that sees one key has ds = 0: as a row that sees none
+        valid = row_limit(p.mask, item.keys, row);
+        if (valid == 1) valid = 0;
+        valid -= kCols * g;
+        if (n > 0) {
+          const long long head = (long long)item.b * p.H + item.h;
+          const float lse = row < p.mask.Sq ? __ldg(p.lse + head * p.mask.Sq + row) : -INFINITY;
+          ok = find_delta(items, nd);
+          if (lse == -INFINITY) nd = 0.0f;
+          else nl = -lse * kLog2e;
+          if (g == 0) {
+            p.neg_lse2[head * p.Sq_pad + row] = nl;
+            p.neg_delta[head * p.Sq_pad + row] = nd;
+          }
+        }
       }
-      for (int end = it + item.n; it != end; ++it, valid -= kTile) {
+      if (!ok) break;
+      for (; n > 0; --n, ++it, valid -= kTile) {
         const bool partial = __any_sync(0xffffffffu, valid < kCols);
         float pr[kCols];
         ok = mbar_wait_warp<false>(&sm.s_full, it & 1, abort_flag, err, kErrTimeoutMma);
@@ -816,9 +825,11 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       if (!ok) break;
       // the next item's Q, so that its first S runs while this one's rows are stored
+      const ItemQ item = item_q(p, work_read(sm.work, turn));
       more = work_wait(sm.work, turn + 1, abort_flag, err);
-      if (more && item_q(p, work_read(sm.work, turn + 1)).n > 0) {
-        ok = copy_q(items + (item.n > 0 ? 1 : 0));
+      if (more) {
+        const ItemQ next = item_q(p, work_read(sm.work, turn + 1));
+        if (next.n > 0) ok = begin_item(items + (item.n > 0 ? 1 : 0), next);
         if (!ok) break;
       }
       // each warpgroup stores 32 of the rows' channels
@@ -830,8 +841,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         load_row_bf16<32>(tDQ + lane_off + 32 * g, out, p.scale);
         tc_fence_before();
       }
-      store_rows<32>(p.d0 + (long long)item.b * p.s0[0] + (long long)(row - lane) * p.s0[1] + (long long)item.h * p.s0[2] + 32 * g,
-                     p.s0[1], out, p.mask.Sq - (row - lane), lane);
+      store_rows<32>(p.d0 + (long long)item.b * p.s0[0] + (long long)(item.row0 + wq * 32) * p.s0[1] + (long long)item.h * p.s0[2] + 32 * g,
+                     p.s0[1], out, p.mask.Sq - (item.row0 + wq * 32), lane);
       work_release(sm.work, turn, lane);
       ++turn;
     }
@@ -865,36 +876,30 @@ cudaError_t launch_attn_bwd_bf16(const CUtensorMap& tm_q, const CUtensorMap& tm_
   });
   if (e != cudaSuccess) return e;
   const int Sq_pad = (int)attn_bwd_padded_rows(a.Sq);
-  RowsParams r;
-  r.o = reinterpret_cast<const __nv_bfloat16*>(t.o);
-  r.dout = reinterpret_cast<const __nv_bfloat16*>(t.dout);
-  for (int i = 0; i < 3; ++i) {
-    r.o_s[i] = t.o_str[i];
-    r.d_s[i] = t.dout_str[i];
-  }
-  r.lse = t.lse;
-  r.neg_lse2 = workspace;
-  r.rows = (long long)a.B * a.Hq * Sq_pad;
-  r.neg_delta = workspace + r.rows;
-  r.Sq = a.Sq;
-  r.Sq_pad = Sq_pad;
-  r.Hq = a.Hq;
-  long long blocks = (r.rows + 15) / 16;
-  const long long cap = (long long)device_sm_count() * 16;
-  if (blocks > cap) blocks = cap;
-  e = launch_dependent(rows_kernel, dim3((unsigned)blocks), 256, 0, stream, r);
-  if (e != cudaSuccess) return e;
-
   BwdParams p;
   p.mask = {a.kv_len, a.causal, a.Sq, a.Sk};
   p.c_log2 = a.c_log2;
   p.scale = a.scale;
-  p.neg_lse2 = r.neg_lse2;
-  p.neg_delta = r.neg_delta;
+  p.neg_lse2 = workspace;
+  p.neg_delta = workspace + (long long)a.B * a.Hq * Sq_pad;
   p.Sq_pad = Sq_pad;
   p.group = a.Hq / a.Hkv;
-  p.H = a.Hkv;
+  p.o = reinterpret_cast<const __nv_bfloat16*>(t.o);
+  p.lse = t.lse;
   const int k_tiles = (a.Sk + kTile - 1) / kTile, q_tiles = Sq_pad / kTile;
+  p.H = a.Hq;
+  p.order = {q_tiles, a.B * a.Hq, a.causal ? causal_group(q_tiles, a.B * a.Hq) : 1};
+  p.d0 = reinterpret_cast<__nv_bfloat16*>(t.dq);
+  p.d1 = nullptr;
+  for (int i = 0; i < 3; ++i) {
+    p.o_s[i] = t.o_str[i];
+    p.s0[i] = t.dq_str[i];
+    p.s1[i] = 0;
+  }
+  e = launch_dependent(dq_kernel, dim3((unsigned)q_tiles * (unsigned)p.order.heads), kThreads, kSmemQ, stream, tm_q,
+                       tm_k, tm_v, tm_d, p);
+  if (e != cudaSuccess) return e;
+  p.H = a.Hkv;
   p.order = {k_tiles, a.B * a.Hkv, a.causal ? causal_group(k_tiles, a.B * a.Hkv) : 1};
   p.d0 = reinterpret_cast<__nv_bfloat16*>(t.dk);
   p.d1 = reinterpret_cast<__nv_bfloat16*>(t.dv);
@@ -902,16 +907,8 @@ cudaError_t launch_attn_bwd_bf16(const CUtensorMap& tm_q, const CUtensorMap& tm_
     p.s0[i] = t.dk_str[i];
     p.s1[i] = t.dv_str[i];
   }
-  e = launch_dependent(dkdv_kernel, dim3((unsigned)k_tiles * (unsigned)p.order.heads), kThreads, kSmemKV, stream, tm_q,
-                       tm_k, tm_v, tm_d, p);
-  if (e != cudaSuccess) return e;
-  p.H = a.Hq;
-  p.order = {q_tiles, a.B * a.Hq, a.causal ? causal_group(q_tiles, a.B * a.Hq) : 1};
-  p.d0 = reinterpret_cast<__nv_bfloat16*>(t.dq);
-  p.d1 = nullptr;
-  for (int i = 0; i < 3; ++i) p.s0[i] = t.dq_str[i];
-  return launch_dependent(dq_kernel, dim3((unsigned)q_tiles * (unsigned)p.order.heads), kThreads, kSmemQ, stream, tm_q,
-                          tm_k, tm_v, tm_d, p);
+  return launch_dependent(dkdv_kernel, dim3((unsigned)k_tiles * (unsigned)p.order.heads), kThreads, kSmemKV, stream,
+                          tm_q, tm_k, tm_v, tm_d, p);
 }
 
 cudaError_t read_and_clear_err_bwd(uint32_t* out) {
