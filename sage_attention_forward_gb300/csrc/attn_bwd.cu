@@ -67,6 +67,7 @@ struct BwdParams {
   __nv_bfloat16 *d0, *d1;   // dQ; or dK and dV
   long long s0[3], s1[3];   // their element strides (b, s, h)
   int H, group;             // heads of this grid (Hkv, or Hq), Hq / Hkv
+  Div by_H, by_group;
   Order order;
 };
 
@@ -102,8 +103,8 @@ __device__ __forceinline__ ItemKV item_kv(const BwdParams& p, const Work& w) {
   ItemKV i;
   int tile, head;
   work_place(p.order, w, tile, head);
-  i.b = head / p.H;
-  i.hk = head % p.H;
+  i.b = div_by(head, p.by_H);
+  i.hk = head - i.b * p.H;
   i.key0 = tile * kTile;
   i.n_q = (p.mask.Sq + kTile - 1) / kTile;
   i.keys = key_count(p.mask, i.b);
@@ -208,7 +209,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       };
       Work w = first_work();
       do {
-        if (!work_request(sm.work, w, abort_flag, err)) break;
+        if (!work_request(sm.work, w.t + 1, abort_flag, err)) break;
         ++requests;
         const ItemKV i = item_kv(p, w);
         if (i.n > 0 && !load_item(i)) break;
@@ -489,8 +490,8 @@ __device__ __forceinline__ ItemQ item_q(const BwdParams& p, const Work& w) {
   ItemQ i;
   int tile, head;
   work_place(p.order, w, tile, head);
-  i.b = head / p.H;
-  i.h = head % p.H;
+  i.b = div_by(head, p.by_H);
+  i.h = head - i.b * p.H;
   // the last queries have the most keys when the mask is causal: they start first
   i.row0 = (p.mask.causal ? p.order.tiles - 1 - tile : tile) * kTile;
   i.keys = key_count(p.mask, i.b);
@@ -553,47 +554,61 @@ __global__ void __launch_bounds__(kThreads, 1)
       tma_prefetch_desc(&tm_k);
       tma_prefetch_desc(&tm_v);
       tma_prefetch_desc(&tm_d);
-      int it = 0, items = 0, requests = 0, k_issued = 0, v_issued = 0, q_issued = 0, d_issued = 0;
-      auto load_item = [&](const ItemQ& i) -> bool {
-        const int hk = i.h / p.group;
-        for (int j = 0; j < i.n; ++j, ++it) {
-          if (j == 0) {
-            if (items > 0 && !wait_sleep(&sm.q_empty, (items - 1) & 1, abort_flag, err, kErrTimeoutSync)) return false;
-            mbar_arrive_expect_tx(&sm.q_full, kTileBytes);
-            load_tile(sm.q, &tm_q, &sm.q_full, i.row0, i.h, i.b);
-            ++q_issued;
-          }
-          {
-            const int slot = it % kKRing, use = it / kKRing;
-            if (use > 0 && !wait_sleep(&sm.k_empty[slot], (use - 1) & 1, abort_flag, err, kErrTimeoutSync)) return false;
-            mbar_arrive_expect_tx(&sm.k_full[slot], kTileBytes);
-            load_tile(sm.k[slot], &tm_k, &sm.k_full[slot], j * kTile, hk, i.b);
-            ++k_issued;
-          }
-          if (j == 0) {
-            if (items > 0 && !wait_sleep(&sm.d_empty, (items - 1) & 1, abort_flag, err, kErrTimeoutSync)) return false;
-            mbar_arrive_expect_tx(&sm.d_full, kTileBytes);
-            load_tile(sm.dout, &tm_d, &sm.d_full, i.row0, i.h, i.b);
-            ++d_issued;
-          }
-          {
-            const int slot = it % kVRing, use = it / kVRing;
-            if (use > 0 && !wait_sleep(&sm.v_empty[slot], (use - 1) & 1, abort_flag, err, kErrTimeoutSync)) return false;
-            mbar_arrive_expect_tx(&sm.v_full[slot], kTileBytes);
-            load_tile(sm.v[slot], &tm_v, &sm.v_full[slot], j * kTile, hk, i.b);
-            ++v_issued;
-          }
+      int it = 0, requests = 0, k_issued = 0, v_issued = 0, q_issued = 0, d_issued = 0;
+      // Q(t+1) is loaded while item t runs: its place is free since the softmax warps copied Q(t).  So item
+      // t + 1 is looked up after the first two K and V tiles of item t, and item t + 2 asked for then.
+      auto load_q = [&](const ItemQ& i) -> bool {
+        if (q_issued > 0 && !wait_sleep(&sm.q_empty, (q_issued - 1) & 1, abort_flag, err, kErrTimeoutSync)) return false;
+        mbar_arrive_expect_tx(&sm.q_full, kTileBytes);
+        load_tile(sm.q, &tm_q, &sm.q_full, i.row0, i.h, i.b);
+        ++q_issued;
+        return true;
+      };
+      auto load_kv = [&](const ItemQ& i, int j) -> bool {
+        const int hk = div_by(i.h, p.by_group);
+        {
+          const int slot = it % kKRing, use = it / kKRing;
+          if (use > 0 && !wait_sleep(&sm.k_empty[slot], (use - 1) & 1, abort_flag, err, kErrTimeoutSync)) return false;
+          mbar_arrive_expect_tx(&sm.k_full[slot], kTileBytes);
+          load_tile(sm.k[slot], &tm_k, &sm.k_full[slot], j * kTile, hk, i.b);
+          ++k_issued;
         }
-        ++items;
+        if (j == 0) {
+          if (d_issued > 0 && !wait_sleep(&sm.d_empty, (d_issued - 1) & 1, abort_flag, err, kErrTimeoutSync)) return false;
+          mbar_arrive_expect_tx(&sm.d_full, kTileBytes);
+          load_tile(sm.dout, &tm_d, &sm.d_full, i.row0, i.h, i.b);
+          ++d_issued;
+        }
+        {
+          const int slot = it % kVRing, use = it / kVRing;
+          if (use > 0 && !wait_sleep(&sm.v_empty[slot], (use - 1) & 1, abort_flag, err, kErrTimeoutSync)) return false;
+          mbar_arrive_expect_tx(&sm.v_full[slot], kTileBytes);
+          load_tile(sm.v[slot], &tm_v, &sm.v_full[slot], j * kTile, hk, i.b);
+          ++v_issued;
+        }
+        ++it;
         return true;
       };
       Work w = first_work();
-      do {
-        if (!work_request(sm.work, w, abort_flag, err)) break;
-        ++requests;
-        const ItemQ i = item_q(p, w);
-        if (i.n > 0 && !load_item(i)) break;
-      } while (work_next_load(sm.work, w, abort_flag, err));
+      ItemQ item = item_q(p, w), next = item;
+      bool ok = work_request(sm.work, 1, abort_flag, err), more = true;
+      if (ok) ++requests;
+      if (ok && item.n > 0) ok = load_q(item);
+      while (ok && more) {
+        const int early = min(item.n, 2);
+        for (int j = 0; ok && j < early; ++j) ok = load_kv(item, j);
+        if (!ok) break;
+        more = work_next_load(sm.work, w, abort_flag, err);
+        if (more) {
+          ok = work_request(sm.work, w.t + 1, abort_flag, err);
+          if (!ok) break;
+          ++requests;
+          next = item_q(p, w);
+          if (next.n > 0) ok = load_q(next);
+        }
+        for (int j = early; ok && j < item.n; ++j) ok = load_kv(item, j);
+        item = next;
+      }
       if (*abort_flag) {
         work_teardown(sm.work, requests);
         if (q_issued) mbar_wait_teardown(&sm.q_full, (q_issued - 1) & 1);
@@ -888,7 +903,9 @@ cudaError_t launch_attn_bwd_bf16(const CUtensorMap& tm_q, const CUtensorMap& tm_
   p.lse = t.lse;
   const int k_tiles = (a.Sk + kTile - 1) / kTile, q_tiles = Sq_pad / kTile;
   p.H = a.Hq;
-  p.order = {q_tiles, a.B * a.Hq, a.causal ? causal_group(q_tiles, a.B * a.Hq) : 1};
+  p.by_H = make_div(p.H);
+  p.by_group = make_div(p.group);
+  p.order = make_order(q_tiles, a.B * a.Hq, a.causal);
   p.d0 = reinterpret_cast<__nv_bfloat16*>(t.dq);
   p.d1 = nullptr;
   for (int i = 0; i < 3; ++i) {
@@ -896,18 +913,19 @@ cudaError_t launch_attn_bwd_bf16(const CUtensorMap& tm_q, const CUtensorMap& tm_
     p.s0[i] = t.dq_str[i];
     p.s1[i] = 0;
   }
-  e = launch_dependent(dq_kernel, dim3((unsigned)q_tiles * (unsigned)p.order.heads), kThreads, kSmemQ, stream, tm_q,
+  e = launch_dependent(dq_kernel, dim3((unsigned)p.order.items), kThreads, kSmemQ, stream, tm_q,
                        tm_k, tm_v, tm_d, p);
   if (e != cudaSuccess) return e;
   p.H = a.Hkv;
-  p.order = {k_tiles, a.B * a.Hkv, a.causal ? causal_group(k_tiles, a.B * a.Hkv) : 1};
+  p.by_H = make_div(p.H);
+  p.order = make_order(k_tiles, a.B * a.Hkv, a.causal);
   p.d0 = reinterpret_cast<__nv_bfloat16*>(t.dk);
   p.d1 = reinterpret_cast<__nv_bfloat16*>(t.dv);
   for (int i = 0; i < 3; ++i) {
     p.s0[i] = t.dk_str[i];
     p.s1[i] = t.dv_str[i];
   }
-  return launch_dependent(dkdv_kernel, dim3((unsigned)k_tiles * (unsigned)p.order.heads), kThreads, kSmemKV, stream,
+  return launch_dependent(dkdv_kernel, dim3((unsigned)p.order.items), kThreads, kSmemKV, stream,
                           tm_q, tm_k, tm_v, tm_d, p);
 }
 

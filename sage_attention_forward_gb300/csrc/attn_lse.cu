@@ -59,6 +59,7 @@ struct Params {
   long long o_sb, o_ss, o_sh;
   float* lse;     // [B, Hq, Sq]
   int Hq, group;
+  Div by_Hq, by_group;
   Order order;
 };
 
@@ -73,8 +74,8 @@ __device__ __forceinline__ Item item_of(const Params& p, const Work& w) {
   Item i;
   int tile, head;
   work_place(p.order, w, tile, head);
-  i.b = head / p.Hq;
-  i.h = head % p.Hq;
+  i.b = div_by(head, p.by_Hq);
+  i.h = head - i.b * p.Hq;
   // the last queries have the most keys when the mask is causal: they start first
   i.row0 = (p.mask.causal ? p.order.tiles - 1 - tile : tile) * (kNQ * kTile);
   i.keys = key_count(p.mask, i.b);
@@ -130,7 +131,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       tma_prefetch_desc(&tm_v);
       int it = 0, items = 0, requests = 0, q_issued = 0, k_issued = 0, v_issued = 0;
       auto load_item = [&](const Item& i) -> bool {
-        const int hk = i.h / p.group;
+        const int hk = div_by(i.h, p.by_group);
         if (items > 0 && !wait_sleep(&sm.q_empty, (items - 1) & 1, abort_flag, err, kErrTimeoutSync)) return false;
         mbar_arrive_expect_tx(&sm.q_full, kNQ * kTileBytes);
         for (int q = 0; q < kNQ; ++q) load_tile(sm.q[q], &tm_q, &sm.q_full, i.row0 + q * kTile, i.h, i.b);
@@ -151,7 +152,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       };
       Work w = first_work();
       do {
-        if (!work_request(sm.work, w, abort_flag, err)) break;
+        if (!work_request(sm.work, w.t + 1, abort_flag, err)) break;
         ++requests;
         const Item i = item_of(p, w);
         if (i.n > 0 && !load_item(i)) break;
@@ -427,10 +428,11 @@ cudaError_t launch_attn_fwd_bf16_lse(const CUtensorMap& tm_q, const CUtensorMap&
   p.lse = lse;
   p.Hq = a.Hq;
   p.group = a.Hq / a.Hkv;
-  const int tiles = (a.Sq + kNQ * kTile - 1) / (kNQ * kTile), heads = a.B * a.Hq;
-  p.order = {tiles, heads, a.causal ? causal_group(tiles, heads) : 1};
-  return launch_dependent(lse_fwd_kernel, dim3((unsigned)tiles * (unsigned)heads), kThreads, kSmemBytes, stream, tm_q,
-                          tm_k, tm_v, p);
+  p.by_Hq = make_div(a.Hq);
+  p.by_group = make_div(p.group);
+  p.order = make_order((a.Sq + kNQ * kTile - 1) / (kNQ * kTile), a.B * a.Hq, a.causal);
+  return launch_dependent(lse_fwd_kernel, dim3((unsigned)p.order.items), kThreads, kSmemBytes, stream, tm_q, tm_k, tm_v,
+                          p);
 }
 
 cudaError_t read_and_clear_err_lse(uint32_t* out) {

@@ -8,6 +8,7 @@
 
 #include <cstdint>
 
+#include "kernels.h"
 #include "ptx.cuh"
 
 namespace sa {
@@ -61,7 +62,7 @@ __device__ __forceinline__ bool smem_misaligned(const uint8_t* smem, uint32_t* e
 // answer takes over an item whose CTA has not started, so that barriers, TMEM and descriptors are
 // set up once, and the next item's loads and first products run under the last one's end
 // (a CTA of its own costs about 14 K cycles outside its main loop).  Items start in grid order.
-// The load warp asks for item t + 1 when it starts item t; every warp reads the answers in turn.
+// The load warp asks for the next item ahead of time; every warp reads the answers in turn.
 constexpr int kWorkSlots = 4;
 struct WorkRing {
   alignas(16) uint4 answer[kWorkSlots];
@@ -78,17 +79,12 @@ __device__ __forceinline__ bool work_answer(const uint4* answer, Work& w) {
   w.index = (int)x;
   return true;
 }
-// Items are (tile, head); `group` heads go together, tile by tile: one head after another (group = 1) keeps
-// few heads' tiles in L2, and where a causal mask makes the first tiles of a head the longest
-// items, several heads' long ones come before their short ones, so that the grid ends with short ones.
-struct Order {
-  int tiles, heads, group;
-};
+// (by products: five divisions of each role at each item took about 1000 cycles)
 __device__ __forceinline__ void work_place(const Order& o, const Work& w, int& tile, int& head) {
-  const int first = w.index / (o.group * o.tiles) * o.group;   // the group's first head
-  const int at = w.index - first * o.tiles, n = min(o.group, o.heads - first);
-  tile = at / n;
-  head = first + at % n;
+  const int g = div_by(w.index, o.by_group), first = g * o.group, at = w.index - g * (int)o.by_group.d;
+  const bool rest = first + o.group > o.heads;
+  tile = div_by(at, rest ? o.by_rest : o.by_heads);
+  head = first + at - tile * (int)(rest ? o.by_rest.d : o.by_heads.d);
 }
 __device__ __forceinline__ void work_init(WorkRing& r, int reader_warps) {
   for (int s = 0; s < kWorkSlots; ++s) {
@@ -96,9 +92,9 @@ __device__ __forceinline__ void work_init(WorkRing& r, int reader_warps) {
     mbar_init(&r.empty[s], reader_warps);
   }
 }
-// The load warp's thread: ask for the item after w.
-__device__ __forceinline__ bool work_request(WorkRing& r, const Work& w, volatile uint32_t* abort_flag, uint32_t* err) {
-  const int s = w.t % kWorkSlots, use = w.t / kWorkSlots;
+// The load warp's thread: ask for item t > 0 (and for no other before that one's answer has been read).
+__device__ __forceinline__ bool work_request(WorkRing& r, int t, volatile uint32_t* abort_flag, uint32_t* err) {
+  const int s = (t - 1) % kWorkSlots, use = (t - 1) / kWorkSlots;
   if (use > 0 && !wait_sleep(&r.empty[s], (use - 1) & 1, abort_flag, err, kErrTimeoutSync)) return false;
   mbar_arrive_expect_tx(&r.full[s], 16);
   clc_try_cancel(&r.answer[s], &r.full[s]);

@@ -169,6 +169,23 @@ cudaError_t launch_sage_attn_pv16_qload(const CUtensorMap& tm_q_bf16, const CUte
                                         void* o, long long o_sb, long long o_ss, long long o_sh, int B, int S, int H,
                                         long long S_pad, cudaStream_t stream);
 
+// n / d for n < 2^31 by a product (Granlund and Montgomery, "Division by invariant integers using
+// multiplication", 1994): d <= 2^shift, mul = floor(2^32 (2^shift - d) / d) + 1.
+struct Div {
+  uint32_t d, mul, shift;
+};
+inline Div make_div(int d) {
+  Div r = {(uint32_t)d, 0, 0};
+  while ((1ll << r.shift) < d) ++r.shift;
+  r.mul = (uint32_t)(((1ull << 32) * ((1ull << r.shift) - (uint64_t)d)) / (uint64_t)d + 1);
+  return r;
+}
+#ifdef __CUDACC__
+__device__ __forceinline__ int div_by(int n, const Div& d) {
+  return (int)((__umulhi((uint32_t)n, d.mul) + (uint32_t)n) >> d.shift);
+}
+#endif
+
 // ------------------------------------------------------------------ training
 // What the forward with row statistics and the backward share (attn_lse.cu, attn_bwd.cu).
 struct TrainArgs {
@@ -215,11 +232,25 @@ cudaError_t launch_layer_norm_bwd(const LayerNormArgs& a, const void* dy, const 
                                   const long long dx_str[3], void* dw, void* db, float* workspace,
                                   cudaStream_t stream);
 
-// Heads that go together in the grid under a causal mask: four items per SM, so that the items in hand
-// at the grid's end are a group's short ones.
-inline int causal_group(int tiles, int heads) {
+// The order of a grid's items (tile, head): `group` heads go together, tile by tile.  One head after another
+// (group = 1) keeps few heads' tiles in L2.  Where a causal mask makes the first tiles of a head the longest
+// items, several heads' long ones come before their short ones, so that the grid ends with short
+// ones: four items per SM go together.
+struct Order {
+  int tiles, heads, group, items;
+  Div by_group, by_heads, by_rest;   // a group's items; its heads; the heads of a last, smaller group
+};
+inline Order make_order(int tiles, int heads, bool causal) {
+  Order o;
   const int want = (4 * 152 + tiles - 1) / tiles;
-  return want < heads ? want : heads;
+  o.tiles = tiles;
+  o.heads = heads;
+  o.group = !causal ? 1 : want < heads ? want : heads;
+  o.items = tiles * heads;
+  o.by_group = make_div(o.group * tiles);
+  o.by_heads = make_div(o.group);
+  o.by_rest = make_div(heads % o.group ? heads % o.group : o.group);
+  return o;
 }
 
 // A launch as a programmatic dependent of the previous kernel in the stream: the kernel may set

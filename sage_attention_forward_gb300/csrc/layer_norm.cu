@@ -27,20 +27,6 @@ struct Rows {
   long long str[3];   // element strides (b, s, h)
   int even;           // all rows are str[2] apart
 };
-// n / d for n < 2^31 by a product (Granlund and Montgomery, "Division by invariant integers using
-// multiplication", 1994): d <= 2^shift, mul = ceil(2^(32 + shift) / d) - 2^32.
-struct Div {
-  uint32_t d, mul, shift;
-};
-Div make_div(int d) {
-  Div r = {(uint32_t)d, 0, 0};
-  while ((1ll << r.shift) < d) ++r.shift;
-  r.mul = (uint32_t)(((1ull << 32) * ((1ull << r.shift) - (uint64_t)d)) / (uint64_t)d + 1);
-  return r;
-}
-__device__ __forceinline__ int div_by(int n, const Div& d) {
-  return (int)((__umulhi((uint32_t)n, d.mul) + (uint32_t)n) >> d.shift);
-}
 struct LnParams {
   const void *x, *dy, *w, *b;
   void *y, *dx;
