@@ -412,10 +412,10 @@ ATTN_API attn_status sage_attention(const void* q, const void* k, const void* v,
  *   lse[i]  = log sum_j exp(s[i, j])          (natural logarithm)
  *   O[i]    = sum_j exp(s[i, j] - lse[i]) v_j
  * A row with limit(i) <= 0 sees no key: O = 0, lse = -inf.
- *   q, o    : BF16 [B, Sq, Hq, 128], strides q_str / o_str
+ *   q, o    : BF16 [B, Sq, Hq, 128], strides q_str / o_str; o overlaps no input
  *   k, v    : BF16 [B, Sk, Hkv, 128], strides k_str / v_str; query head h reads key head
  *             h / (Hq / Hkv); Hq a multiple of Hkv
- *   lse     : float [B, Hq, Sq] output, contiguous
+ *   lse     : float [B, Hq, Sq] output, contiguous, 16-byte aligned
  *   softmax_scale : finite, >= 0
  *   causal  : 0 or 1; the last query sees the last key (Sk - Sq keys come before the first query)
  *   kv_len  : device int32 [B] (4-byte aligned), each batch entry's number of keys, read on the
@@ -443,7 +443,8 @@ ATTN_API size_t attn_bwd_bf16_workspace_size(int B, int Sq, int Sk, int Hq, int 
  *   dout    : BF16 [B, Sq, Hq, 128], finite, strides dout_str
  *   q, k, v, softmax_scale, causal, kv_len : as given to the forward
  *   o, lse  : as the forward wrote them
- *   dq      : BF16 [B, Sq, Hq, 128] output; dk, dv : BF16 [B, Sk, Hkv, 128] outputs, every row written
+ *   dq      : BF16 [B, Sq, Hq, 128] output; dk, dv : BF16 [B, Sk, Hkv, 128] outputs, every row
+ *             written; they overlap neither the inputs nor one another
  *   workspace : at least attn_bwd_bf16_workspace_size(B, Sq, Sk, Hq, Hkv) bytes, 16-byte
  *             aligned; overwritten, contents on entry do not matter
  * p and ds are rounded to BF16 before the products that sum over them, sums are FP32 in a fixed

@@ -760,6 +760,7 @@ attn_status attn_fwd_bf16_lse(const void* q, const void* k, const void* v, void*
   TRY(check_strides("v", v, v_str, B, Sk, Hkv, vs));
   TRY(check_strides("o", o, o_str, B, Sq, Hq, os));
   TRY(check_buffer("lse", lse));
+  if (o == q || o == k || o == v) return fail(ATTN_ERR_INVALID_ARG, "attn_fwd_bf16_lse: o must overlap no input");
   TRY(check_device());
   TRY(get_encoder());
   CUtensorMap tq, tk, tv;
@@ -798,6 +799,11 @@ attn_status attn_bwd_bf16(const void* dout, const void* q, const void* k, const 
   TRY(check_strides("dv", dv, dv_str, B, Sk, Hkv, t.dv_str));
   TRY(check_buffer("lse", lse));
   TRY(check_buffer("workspace", workspace));
+  // dK and dV are formed from the inputs after dQ has been written
+  bool shared = dq == dk || dq == dv || dk == dv;
+  for (const void* in : {dout, q, k, v, o}) shared = shared || dq == in || dk == in || dv == in;
+  if (shared)
+    return fail(ATTN_ERR_INVALID_ARG, "attn_bwd_bf16: dq, dk and dv must overlap neither the inputs nor one another");
   const size_t need = attn_bwd_bf16_workspace_size(B, Sq, Sk, Hq, Hkv);
   if (workspace_bytes < need)
     return fail(ATTN_ERR_INVALID_ARG, "attn_bwd_bf16: workspace_bytes=%zu < %zu required", workspace_bytes, need);
