@@ -108,18 +108,18 @@ def lib() -> ctypes.CDLL:
         L.attn_sm_clock_sample.restype = i
         L.sage_e4m3_encode.argtypes = [_vp, _vp, ctypes.c_int64, _vp]
         L.sage_e4m3_encode.restype = i
-        L.attn_fwd_bf16_lse.argtypes = [_vp] * 5 + [i] * 6 + [_vp] * 4 + [ctypes.c_float, i, _vp, _vp]
-        L.attn_fwd_bf16_lse.restype = i
-        L.attn_bwd_bf16_workspace_size.argtypes = [i] * 5
-        L.attn_bwd_bf16_workspace_size.restype = ctypes.c_size_t
-        L.attn_bwd_bf16.argtypes = [_vp] * 9 + [i] * 6 + [_vp] * 8 + [ctypes.c_float, i, _vp, _vp, ctypes.c_size_t, _vp]
-        L.attn_bwd_bf16.restype = i
-        L.layer_norm_fwd.argtypes = [_vp] * 6 + [i] * 4 + [_vp] * 2 + [ctypes.c_float, i, i, _vp]
-        L.layer_norm_fwd.restype = i
-        L.layer_norm_bwd_workspace_size.argtypes = [i] * 4
-        L.layer_norm_bwd_workspace_size.restype = ctypes.c_size_t
-        L.layer_norm_bwd.argtypes = [_vp] * 8 + [i] * 4 + [_vp] * 3 + [i, i, _vp, ctypes.c_size_t, _vp]
-        L.layer_norm_bwd.restype = i
+        # (translation units of their own: a library may be linked without them, whose calls then raise)
+        size, f32 = ctypes.c_size_t, ctypes.c_float
+        for name, res, args in (
+                ("attn_fwd_bf16_lse", i, [_vp] * 5 + [i] * 6 + [_vp] * 4 + [f32, i, _vp, _vp]),
+                ("attn_bwd_bf16_workspace_size", size, [i] * 5),
+                ("attn_bwd_bf16", i, [_vp] * 9 + [i] * 6 + [_vp] * 8 + [f32, i, _vp, _vp, size, _vp]),
+                ("layer_norm_fwd", i, [_vp] * 6 + [i] * 4 + [_vp] * 2 + [f32, i, i, _vp]),
+                ("layer_norm_bwd_workspace_size", size, [i] * 4),
+                ("layer_norm_bwd", i, [_vp] * 8 + [i] * 4 + [_vp] * 3 + [i, i, _vp, size, _vp])):
+            if hasattr(L, name):
+                fn = getattr(L, name)
+                fn.argtypes, fn.restype = args, res
         L.attn_get_device_status.argtypes = [_vp]
         L.attn_get_device_status.restype = i
         L.attn_last_error.argtypes = []
@@ -415,7 +415,8 @@ def sage_attention(q, k, v, softmax_scale=None, q_norm_w=None, k_norm_w=None, rm
 
 
 # The training calls are made in every layer of every step, small ones too: their checks are written to
-# take little time (shapes, types and devices compared as they come, strides handed over in one array).
+# take little time (shapes, types and devices compared as they come, strides handed over in one array;
+# torch.empty takes half the time of a tensor's new_empty, 1.5 us).
 def _current_stream(dev: int) -> int:
     return torch.cuda.current_stream(dev).cuda_stream
 
@@ -510,11 +511,11 @@ def attn_fwd_bf16_lse(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, softmax
             return attn_fwd_bf16_lse(q, k, v, softmax_scale, causal, kv_len, out, lse)
     rows = (B, Hq, Sq)
     if out is None:
-        out = q.new_empty(q.shape)
+        out = torch.empty(q.shape, dtype=torch.bfloat16, device=dev)
     else:
         _expect("out", out, q.shape, torch.bfloat16, dev)
     if lse is None:
-        lse = q.new_empty(rows, dtype=torch.float32)
+        lse = torch.empty(rows, dtype=torch.float32, device=dev)
     else:
         _expect_dense("lse", lse, rows, torch.float32, dev)
     strides = _strides("q k v out", q, k, v, out)
@@ -527,7 +528,8 @@ def attn_fwd_bf16_lse(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, softmax
 
 
 def attn_bwd_workspace(B: int, Sq: int, Sk: int, Hq: int, Hkv: int, device) -> torch.Tensor:
-    return torch.empty(int(lib().attn_bwd_bf16_workspace_size(B, Sq, Sk, Hq, Hkv)), dtype=torch.uint8, device=device)
+    """Scratch for attn_bwd_bf16 of these shapes; calls on different streams need one each."""
+    return torch.empty(lib().attn_bwd_bf16_workspace_size(B, Sq, Sk, Hq, Hkv), dtype=torch.uint8, device=device)
 
 
 def attn_bwd_bf16(dout: torch.Tensor, q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, out: torch.Tensor,
@@ -546,19 +548,19 @@ def attn_bwd_bf16(dout: torch.Tensor, q: torch.Tensor, k: torch.Tensor, v: torch
     _expect("out", out, q.shape, torch.bfloat16, dev)
     _expect_dense("lse", lse, (B, Hq, Sq), torch.float32, dev)
     if dq is None:
-        dq = q.new_empty(q.shape)
+        dq = torch.empty(q.shape, dtype=torch.bfloat16, device=dev)
     else:
         _expect("dq", dq, q.shape, torch.bfloat16, dev)
     if dk is None:
-        dk = q.new_empty(k.shape)
+        dk = torch.empty(k.shape, dtype=torch.bfloat16, device=dev)
     else:
         _expect("dk", dk, k.shape, torch.bfloat16, dev)
     if dv is None:
-        dv = q.new_empty(k.shape)
+        dv = torch.empty(k.shape, dtype=torch.bfloat16, device=dev)
     else:
         _expect("dv", dv, k.shape, torch.bfloat16, dev)
     if workspace is None:
-        workspace = q.new_empty(int(lib().attn_bwd_bf16_workspace_size(B, Sq, Sk, Hq, Hkv)), dtype=torch.uint8)
+        workspace = attn_bwd_workspace(B, Sq, Sk, Hq, Hkv, dev)
     strides = _strides("dout q k v out dq dk dv", dout, q, k, v, out, dq, dk, dv)
     at = strides.buffer_info()[0]
     _check(lib().attn_bwd_bf16(dout.data_ptr(), q.data_ptr(), k.data_ptr(), v.data_ptr(), out.data_ptr(),
@@ -624,15 +626,15 @@ def layer_norm_fwd(x: torch.Tensor, weight: torch.Tensor | None = None, bias: to
         w_type = bias.dtype
     stats = x.shape[:-1]
     if out is None:
-        out = x.new_empty(x.shape)
+        out = torch.empty(x.shape, dtype=x.dtype, device=dev)
     else:
         _expect("out", out, x.shape, x.dtype, dev)
     if mean is None:
-        mean = x.new_empty(stats, dtype=torch.float32)
+        mean = torch.empty(stats, dtype=torch.float32, device=dev)
     else:
         _expect_dense("mean", mean, stats, torch.float32, dev)
     if rstd is None:
-        rstd = x.new_empty(stats, dtype=torch.float32)
+        rstd = torch.empty(stats, dtype=torch.float32, device=dev)
     else:
         _expect_dense("rstd", rstd, stats, torch.float32, dev)
     strides = _norm_strides("x out", x, out)
@@ -645,8 +647,9 @@ def layer_norm_fwd(x: torch.Tensor, weight: torch.Tensor | None = None, bias: to
 
 
 def layer_norm_bwd_workspace(x_shape, device) -> torch.Tensor:
+    """Scratch for layer_norm_bwd of rows of this shape; calls on different streams need one each."""
     shape = (1,) * (4 - len(x_shape)) + tuple(x_shape)
-    return torch.empty(int(lib().layer_norm_bwd_workspace_size(*shape)), dtype=torch.uint8, device=device)
+    return torch.empty(lib().layer_norm_bwd_workspace_size(*shape), dtype=torch.uint8, device=device)
 
 
 def layer_norm_bwd(dy: torch.Tensor, x: torch.Tensor, weight: torch.Tensor | None, mean: torch.Tensor,
@@ -675,15 +678,16 @@ def layer_norm_bwd(dy: torch.Tensor, x: torch.Tensor, weight: torch.Tensor | Non
         w_type = dweight.dtype
         _norm_weight("dbias", dbias, x, dev, w_type)
     elif weight is not None:
-        dweight, dbias = weight.new_empty(shape[3:]), weight.new_empty(shape[3:])
+        dweight = torch.empty(shape[3:], dtype=w_type, device=dev)
+        dbias = torch.empty(shape[3:], dtype=w_type, device=dev)
     if dx is None:
-        dx = x.new_empty(x.shape)
+        dx = torch.empty(x.shape, dtype=x.dtype, device=dev)
     else:
         _expect("dx", dx, x.shape, x.dtype, dev)
     size = 0
     if dweight is not None:
         if workspace is None:
-            workspace = x.new_empty(int(lib().layer_norm_bwd_workspace_size(*shape)), dtype=torch.uint8)
+            workspace = layer_norm_bwd_workspace(shape, dev)
         size = _scratch("workspace", workspace, dev)
     strides = _norm_strides("dy x dx", dy, x, dx)
     at = strides.buffer_info()[0]

@@ -18,8 +18,8 @@ ROOT = os.path.dirname(HERE)
 CSRC = os.path.join(HERE, "csrc")
 OUT_DIR = os.path.join(HERE, "_build")
 LIB = os.path.join(OUT_DIR, "libsageattn.so")
-SOURCES = ["api.cu", "attn_fwd.cu", "sage_prepare.cu", "attn_lse.cu", "attn_bwd.cu", "layer_norm.cu"]
-HEADERS = ["ptx.cuh", "kernels.h", "qk_quant.cuh", "attn_tiles.cuh"]
+SOURCES = ["api.cu", "attn_fwd.cu", "sage_prepare.cu", "api_train.cu", "attn_lse.cu", "attn_bwd.cu", "layer_norm.cu"]
+HEADERS = ["ptx.cuh", "kernels.h", "api_checks.h", "qk_quant.cuh", "attn_tiles.cuh"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
 

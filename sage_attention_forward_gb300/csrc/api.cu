@@ -11,9 +11,11 @@
 #include <mutex>
 
 #include "../../include/sageattn.h"
+#include "api_checks.h"
 #include "kernels.h"
 
-namespace {
+namespace sa {
+namespace api {
 
 thread_local char g_msg[512] = "";
 
@@ -28,8 +30,6 @@ attn_status fail(attn_status s, const char* fmt, ...) {
 attn_status fail_cuda(cudaError_t e, const char* what) {
   return fail(ATTN_ERR_CUDA, "%s: %s (%s)", what, cudaGetErrorName(e), cudaGetErrorString(e));
 }
-
-constexpr double kLog2e = 1.4426950408889634;
 
 // ------------------------------------------------------------------ device check
 constexpr int kMaxDevices = 64;
@@ -118,8 +118,6 @@ attn_status tmap_bytes_3d(CUtensorMap* m, const void* ptr, long long n0, long lo
 }
 
 // ------------------------------------------------------------------ validation
-bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
-
 // The kernels run one CTA per (head, 128 padded positions) at most, numbered along
 // grid.x: B * H * S_pad / 128 must stay below 2^31.
 attn_status check_grid(int B, int H, long long S_pad) {
@@ -164,9 +162,19 @@ attn_status check_strides(const char* name, const void* ptr, const int64_t* in, 
   return ATTN_OK;
 }
 
+}  // namespace api
+
+namespace {
+ErrReader g_err_reader[8];   // (zeros before any translation unit's constructors run)
+int g_err_readers = 0;
 }  // namespace
 
-namespace sa {
+bool add_err_reader(ErrReader read) {
+  if (g_err_readers >= (int)(sizeof(g_err_reader) / sizeof(g_err_reader[0]))) return false;
+  g_err_reader[g_err_readers++] = read;
+  return true;
+}
+
 namespace {
 PFN_cuCtxGetCurrent_v4000 g_ctx_current = nullptr;
 PFN_cuCtxGetId_v12000 g_ctx_id = nullptr;
@@ -216,15 +224,7 @@ int device_sm_count() {
 }
 }  // namespace sa
 
-namespace {
-
-#define TRY(x)                          \
-  do {                                  \
-    attn_status _s = (x);               \
-    if (_s != ATTN_OK) return _s;       \
-  } while (0)
-
-}  // namespace
+using namespace sa::api;
 
 extern "C" {
 
@@ -707,242 +707,6 @@ attn_status sage_attention(const void* q, const void* k, const void* v, int B, i
   return ATTN_OK;
 }
 
-// ------------------------------------------------------------------ training
-// Shapes and mask of the training calls: *empty is set for B = 0 or no heads.
-static attn_status check_train(int B, int Sq, int Sk, int Hq, int Hkv, int D, int causal, const int32_t* kv_len,
-                               float softmax_scale, sa::TrainArgs& a, bool* empty) {
-  *empty = false;
-  if (D != 128) return fail(ATTN_ERR_UNSUPPORTED, "head dimension D=%d; only D=128 is supported", D);
-  if (B < 0 || Hq < 0 || Hkv < 0) return fail(ATTN_ERR_INVALID_ARG, "B=%d Hq=%d Hkv=%d must be >= 0", B, Hq, Hkv);
-  if (Sq < 1 || Sk < 1 || Sq > (1 << 30) || Sk > (1 << 30))
-    return fail(ATTN_ERR_INVALID_ARG, "Sq=%d Sk=%d must be in [1, 2^30]", Sq, Sk);
-  if ((Hq == 0) != (Hkv == 0) || (Hkv > 0 && Hq % Hkv != 0))
-    return fail(ATTN_ERR_INVALID_ARG, "Hq=%d must be a multiple of Hkv=%d", Hq, Hkv);
-  if (causal != 0 && causal != 1) return fail(ATTN_ERR_INVALID_ARG, "causal=%d must be 0 or 1", causal);
-  if (!(softmax_scale >= 0.0f && std::isfinite(softmax_scale)))
-    return fail(ATTN_ERR_INVALID_ARG, "softmax_scale must be finite and >= 0");
-  if (reinterpret_cast<uintptr_t>(kv_len) % 4 != 0) return fail(ATTN_ERR_ALIGNMENT, "kv_len is not 4-byte aligned");
-  if (B == 0 || Hq == 0) {
-    *empty = true;
-    return ATTN_OK;
-  }
-  TRY(check_grid(B, Hq, ((long long)Sq + 127) / 128 * 128));
-  TRY(check_grid(B, Hkv, ((long long)Sk + 127) / 128 * 128));
-  a.B = B;
-  a.Sq = Sq;
-  a.Sk = Sk;
-  a.Hq = Hq;
-  a.Hkv = Hkv;
-  a.scale = softmax_scale;
-  a.c_log2 = (float)((double)softmax_scale * kLog2e);
-  a.causal = causal;
-  a.kv_len = kv_len;
-  return ATTN_OK;
-}
-
-static attn_status check_buffer(const char* name, const void* ptr) {
-  if (ptr == nullptr) return fail(ATTN_ERR_INVALID_ARG, "%s is NULL", name);
-  if (!aligned16(ptr)) return fail(ATTN_ERR_ALIGNMENT, "%s is not 16-byte aligned", name);
-  return ATTN_OK;
-}
-
-attn_status attn_fwd_bf16_lse(const void* q, const void* k, const void* v, void* o, float* lse, int B, int Sq, int Sk,
-                              int Hq, int Hkv, int D, const int64_t q_str[3], const int64_t k_str[3],
-                              const int64_t v_str[3], const int64_t o_str[3], float softmax_scale, int causal,
-                              const int32_t* kv_len, attn_stream_t stream) {
-  bool empty = false;
-  sa::TrainArgs a;
-  TRY(check_train(B, Sq, Sk, Hq, Hkv, D, causal, kv_len, softmax_scale, a, &empty));
-  if (empty) return ATTN_OK;
-  long long qs[3], ks[3], vs[3], os[3];
-  TRY(check_strides("q", q, q_str, B, Sq, Hq, qs));
-  TRY(check_strides("k", k, k_str, B, Sk, Hkv, ks));
-  TRY(check_strides("v", v, v_str, B, Sk, Hkv, vs));
-  TRY(check_strides("o", o, o_str, B, Sq, Hq, os));
-  TRY(check_buffer("lse", lse));
-  if (o == q || o == k || o == v) return fail(ATTN_ERR_INVALID_ARG, "attn_fwd_bf16_lse: o must overlap no input");
-  TRY(check_device());
-  TRY(get_encoder());
-  CUtensorMap tq, tk, tv;
-  TRY(tmap_bhsd_bf16(&tq, q, B, Sq, Hq, qs));
-  TRY(tmap_bhsd_bf16(&tk, k, B, Sk, Hkv, ks));
-  TRY(tmap_bhsd_bf16(&tv, v, B, Sk, Hkv, vs));
-  cudaError_t e = sa::launch_attn_fwd_bf16_lse(tq, tk, tv, a, o, os, lse, (cudaStream_t)stream);
-  if (e != cudaSuccess) return fail_cuda(e, "attn_fwd_bf16_lse launch");
-  return ATTN_OK;
-}
-
-size_t attn_bwd_bf16_workspace_size(int B, int Sq, int Sk, int Hq, int Hkv) {
-  if (B < 1 || Sq < 1 || Sk < 1 || Hq < 1 || Hkv < 1) return 0;
-  return (size_t)2 * B * Hq * (size_t)sa::attn_bwd_padded_rows(Sq) * sizeof(float);
-}
-
-attn_status attn_bwd_bf16(const void* dout, const void* q, const void* k, const void* v, const void* o,
-                          const float* lse, void* dq, void* dk, void* dv, int B, int Sq, int Sk, int Hq, int Hkv,
-                          int D, const int64_t dout_str[3], const int64_t q_str[3], const int64_t k_str[3],
-                          const int64_t v_str[3], const int64_t o_str[3], const int64_t dq_str[3],
-                          const int64_t dk_str[3], const int64_t dv_str[3], float softmax_scale, int causal,
-                          const int32_t* kv_len, void* workspace, size_t workspace_bytes, attn_stream_t stream) {
-  bool empty = false;
-  sa::TrainArgs a;
-  TRY(check_train(B, Sq, Sk, Hq, Hkv, D, causal, kv_len, softmax_scale, a, &empty));
-  if (empty) return ATTN_OK;
-  long long qs[3], ks[3], vs[3];
-  sa::BwdTensors t;
-  TRY(check_strides("dout", dout, dout_str, B, Sq, Hq, t.dout_str));
-  TRY(check_strides("q", q, q_str, B, Sq, Hq, qs));
-  TRY(check_strides("k", k, k_str, B, Sk, Hkv, ks));
-  TRY(check_strides("v", v, v_str, B, Sk, Hkv, vs));
-  TRY(check_strides("o", o, o_str, B, Sq, Hq, t.o_str));
-  TRY(check_strides("dq", dq, dq_str, B, Sq, Hq, t.dq_str));
-  TRY(check_strides("dk", dk, dk_str, B, Sk, Hkv, t.dk_str));
-  TRY(check_strides("dv", dv, dv_str, B, Sk, Hkv, t.dv_str));
-  TRY(check_buffer("lse", lse));
-  TRY(check_buffer("workspace", workspace));
-  // dK and dV are formed from the inputs after dQ has been written
-  bool shared = dq == dk || dq == dv || dk == dv;
-  for (const void* in : {dout, q, k, v, o}) shared = shared || dq == in || dk == in || dv == in;
-  if (shared)
-    return fail(ATTN_ERR_INVALID_ARG, "attn_bwd_bf16: dq, dk and dv must overlap neither the inputs nor one another");
-  const size_t need = attn_bwd_bf16_workspace_size(B, Sq, Sk, Hq, Hkv);
-  if (workspace_bytes < need)
-    return fail(ATTN_ERR_INVALID_ARG, "attn_bwd_bf16: workspace_bytes=%zu < %zu required", workspace_bytes, need);
-  TRY(check_device());
-  TRY(get_encoder());
-  CUtensorMap tq, tk, tv, td;
-  TRY(tmap_bhsd_bf16(&tq, q, B, Sq, Hq, qs));
-  TRY(tmap_bhsd_bf16(&tk, k, B, Sk, Hkv, ks));
-  TRY(tmap_bhsd_bf16(&tv, v, B, Sk, Hkv, vs));
-  TRY(tmap_bhsd_bf16(&td, dout, B, Sq, Hq, t.dout_str));
-  t.o = o;
-  t.dout = dout;
-  t.lse = lse;
-  t.dq = dq;
-  t.dk = dk;
-  t.dv = dv;
-  cudaError_t e = sa::launch_attn_bwd_bf16(tq, tk, tv, td, a, t, reinterpret_cast<float*>(workspace),
-                                           (cudaStream_t)stream);
-  if (e != cudaSuccess) return fail_cuda(e, "attn_bwd_bf16 launch");
-  return ATTN_OK;
-}
-
-// ------------------------------------------------------------------ layer norm
-// Strides of [B, S, H, N] rows in whole elements; 0 (the same row again) only where a tensor is read.
-static attn_status check_rows(const char* name, const void* ptr, int type, const int64_t* in, const sa::LayerNormArgs& a,
-                              bool read, long long out[3]) {
-  if (ptr == nullptr) return fail(ATTN_ERR_INVALID_ARG, "%s is NULL", name);
-  if (reinterpret_cast<uintptr_t>(ptr) % (type == ATTN_F32 ? 4 : 2) != 0)
-    return fail(ATTN_ERR_ALIGNMENT, "%s is not aligned to its type", name);
-  if (in == nullptr) return fail(ATTN_ERR_INVALID_ARG, "%s strides are NULL", name);
-  const int ext[3] = {a.B, a.S, a.H};
-  for (int i = 0; i < 3; ++i) {
-    const long long s = ext[i] == 1 ? 0 : in[i];
-    if (s < 0 || (s == 0 && ext[i] > 1 && !read) || s >= (1ll << 38))
-      return fail(ATTN_ERR_INVALID_ARG, "%s stride %lld of dimension %d is out of range", name, (long long)in[i], i);
-    out[i] = s;
-  }
-  return ATTN_OK;
-}
-
-static attn_status check_norm(const void* x, const void* w, const void* b, float* mean, float* rstd, int B, int S,
-                              int H, int N, const int64_t* x_str, int type, int w_type, sa::LayerNormArgs& a,
-                              bool* empty) {
-  *empty = false;
-  if (type < ATTN_BF16 || type > ATTN_F32) return fail(ATTN_ERR_INVALID_ARG, "dtype=%d is none of attn_dtype", type);
-  if (w_type != type && w_type != ATTN_F32)
-    return fail(ATTN_ERR_INVALID_ARG, "w_dtype=%d must be the rows' type or ATTN_F32", w_type);
-  if (B < 0 || S < 0 || H < 0) return fail(ATTN_ERR_INVALID_ARG, "B=%d S=%d H=%d must be >= 0", B, S, H);
-  if (N < 1 || N > 16384) return fail(ATTN_ERR_INVALID_ARG, "N=%d must be in [1, 16384]", N);
-  // (no overflow: a factor that makes it too large ends the product)
-  const long long bs = (long long)B * S;
-  if (bs > (1ll << 30) || bs * H > (1ll << 30)) return fail(ATTN_ERR_INVALID_ARG, "B*S*H must be at most 2^30 rows");
-  a.B = B;
-  a.S = S;
-  a.H = H;
-  a.N = N;
-  a.type = type;
-  a.w_type = w_type;
-  a.x = x;
-  a.w = w;
-  a.b = b;
-  a.mean = mean;
-  a.rstd = rstd;
-  if (B == 0 || S == 0 || H == 0) {
-    *empty = true;
-    return ATTN_OK;
-  }
-  TRY(check_rows("x", x, type, x_str, a, true, a.x_str));
-  const uintptr_t w_align = w_type == ATTN_F32 ? 4 : 2;
-  if (reinterpret_cast<uintptr_t>(w) % w_align != 0 || reinterpret_cast<uintptr_t>(b) % w_align != 0)
-    return fail(ATTN_ERR_ALIGNMENT, "weight or bias is not aligned to its type");
-  if (mean == nullptr || rstd == nullptr) return fail(ATTN_ERR_INVALID_ARG, "mean or rstd is NULL");
-  if (reinterpret_cast<uintptr_t>(mean) % 4 != 0 || reinterpret_cast<uintptr_t>(rstd) % 4 != 0)
-    return fail(ATTN_ERR_ALIGNMENT, "mean or rstd is not 4-byte aligned");
-  return ATTN_OK;
-}
-
-attn_status layer_norm_fwd(const void* x, const void* weight, const void* bias, void* y, float* mean, float* rstd,
-                           int B, int S, int H, int N, const int64_t x_str[3], const int64_t y_str[3], float eps,
-                           int dtype, int w_dtype, attn_stream_t stream) {
-  bool empty = false;
-  sa::LayerNormArgs a;
-  if (!(eps >= 0.0f && std::isfinite(eps))) return fail(ATTN_ERR_INVALID_ARG, "eps must be finite and >= 0");
-  TRY(check_norm(x, weight, bias, mean, rstd, B, S, H, N, x_str, dtype, w_dtype, a, &empty));
-  if (empty) return ATTN_OK;
-  a.eps = eps;
-  long long ys[3];
-  TRY(check_rows("y", y, dtype, y_str, a, false, ys));
-  TRY(check_device());
-  cudaError_t e = sa::launch_layer_norm_fwd(a, y, ys, (cudaStream_t)stream);
-  if (e != cudaSuccess) return fail_cuda(e, "layer_norm_fwd launch");
-  return ATTN_OK;
-}
-
-size_t layer_norm_bwd_workspace_size(int B, int S, int H, int N) {
-  if (B < 1 || S < 1 || H < 1 || N < 1 || N > 16384) return 0;
-  const long long bs = (long long)B * S;
-  if (bs > (1ll << 30) || bs * H > (1ll << 30)) return 0;
-  return sa::layer_norm_bwd_workspace((int)(bs * H), N);
-}
-
-attn_status layer_norm_bwd(const void* dy, const void* x, const void* weight, const float* mean, const float* rstd,
-                           void* dx, void* dweight, void* dbias, int B, int S, int H, int N, const int64_t dy_str[3],
-                           const int64_t x_str[3], const int64_t dx_str[3], int dtype, int w_dtype, void* workspace,
-                           size_t workspace_bytes, attn_stream_t stream) {
-  bool empty = false;
-  sa::LayerNormArgs a;
-  TRY(check_norm(x, weight, nullptr, const_cast<float*>(mean), const_cast<float*>(rstd), B, S, H, N, x_str, dtype,
-                 w_dtype, a, &empty));
-  a.eps = 0.0f;
-  if ((dweight == nullptr) != (dbias == nullptr))
-    return fail(ATTN_ERR_INVALID_ARG, "dweight and dbias must both be given or both be NULL");
-  const uintptr_t w_size = w_dtype == ATTN_F32 ? 4 : 2;
-  if (reinterpret_cast<uintptr_t>(dweight) % w_size != 0 || reinterpret_cast<uintptr_t>(dbias) % w_size != 0)
-    return fail(ATTN_ERR_ALIGNMENT, "dweight or dbias is not aligned to its type");
-  if (empty) {   // sums over no rows
-    if (dweight == nullptr) return ATTN_OK;
-    TRY(check_device());
-    cudaError_t e = cudaMemsetAsync(dweight, 0, w_size * N, (cudaStream_t)stream);
-    if (e == cudaSuccess) e = cudaMemsetAsync(dbias, 0, w_size * N, (cudaStream_t)stream);
-    if (e != cudaSuccess) return fail_cuda(e, "layer_norm_bwd");
-    return ATTN_OK;
-  }
-  long long ds[3], xs[3];
-  TRY(check_rows("dy", dy, dtype, dy_str, a, true, ds));
-  TRY(check_rows("dx", dx, dtype, dx_str, a, false, xs));
-  if (dweight != nullptr) {
-    TRY(check_buffer("workspace", workspace));
-    const size_t need = layer_norm_bwd_workspace_size(B, S, H, N);
-    if (workspace_bytes < need)
-      return fail(ATTN_ERR_INVALID_ARG, "layer_norm_bwd: workspace_bytes=%zu < %zu required", workspace_bytes, need);
-  }
-  TRY(check_device());
-  cudaError_t e = sa::launch_layer_norm_bwd(a, dy, ds, dx, xs, dweight, dbias, reinterpret_cast<float*>(workspace),
-                                            (cudaStream_t)stream);
-  if (e != cudaSuccess) return fail_cuda(e, "layer_norm_bwd launch");
-  return ATTN_OK;
-}
-
 attn_status attn_selftest_wait_timeout(const void* q, const void* k, const void* v, void* o,
                                        attn_stream_t stream) {
   const int64_t st[3] = {128 * 128, 128, 128};   // [1, 128, 1, 128] contiguous
@@ -970,14 +734,14 @@ attn_status attn_selftest_wait_timeout(const void* q, const void* k, const void*
 attn_status attn_get_device_status(attn_stream_t stream) {
   cudaError_t e = cudaStreamSynchronize((cudaStream_t)stream);
   if (e != cudaSuccess) return fail_cuda(e, "cudaStreamSynchronize");
-  // one word per translation unit with such kernels
-  uint32_t w = 0, lse = 0, bwd = 0, norm = 0;
+  uint32_t w = 0;
   e = sa::read_and_clear_err_attn(&w);
-  if (e == cudaSuccess) e = sa::read_and_clear_err_lse(&lse);
-  if (e == cudaSuccess) e = sa::read_and_clear_err_bwd(&bwd);
-  if (e == cudaSuccess) e = sa::read_and_clear_err_norm(&norm);
+  for (int i = 0; e == cudaSuccess && i < sa::g_err_readers; ++i) {
+    uint32_t more = 0;
+    e = sa::g_err_reader[i](&more);
+    w |= more;
+  }
   if (e != cudaSuccess) return fail_cuda(e, "reading the device error word");
-  w |= lse | bwd | norm;
   if (w)
     return fail(ATTN_ERR_DEVICE_TIMEOUT,
                 "a kernel gave up on a bounded wait (bits 0x%x: 1 TMA load, 2 MMA commit, 4 hand-off, 8 shared memory "

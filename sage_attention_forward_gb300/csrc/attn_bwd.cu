@@ -61,9 +61,7 @@ struct BwdParams {
   float* neg_lse2;        // [B * Hq, Sq_pad]: written by dq_kernel, read by dkdv_kernel
   float* neg_delta;
   int Sq_pad;
-  const __nv_bfloat16* o;   // (dq_kernel)
-  long long o_s[3];
-  const float* lse;         // [B, Hq, Sq]
+  const float* lse;         // [B, Hq, Sq] (dq_kernel)
   __nv_bfloat16 *d0, *d1;   // dQ; or dK and dV
   long long s0[3], s1[3];   // their element strides (b, s, h)
   int H, group;             // heads of this grid (Hkv, or Hq), Hq / Hkv
@@ -462,12 +460,12 @@ __global__ void __launch_bounds__(kThreads, 1)
 constexpr int kKRing = 3, kVRing = 2;
 
 struct __align__(1024) SmemQ {
-  uint8_t q[kTileBytes];
+  uint8_t q[kTileBytes];   // Q, then O
   uint8_t dout[kTileBytes];
   uint8_t k[kKRing][kTileBytes];
   uint8_t v[kVRing][kTileBytes];
   WorkRing work;
-  uint64_t q_full, q_empty, d_full, d_empty;
+  uint64_t q_full, q_empty, o_full, o_empty, d_full, d_empty;
   uint64_t q_ready;      // Q in TMEM (every softmax warp's part)
   uint64_t k_full[kKRing], k_empty[kKRing], k_clear[kKRing];
   uint64_t v_full[kVRing], v_empty[kVRing];
@@ -501,7 +499,8 @@ __device__ __forceinline__ ItemQ item_q(const BwdParams& p, const Work& w) {
 
 __global__ void __launch_bounds__(kThreads, 1)
     dq_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
-              const __grid_constant__ CUtensorMap tm_v, const __grid_constant__ CUtensorMap tm_d, const BwdParams p) {
+              const __grid_constant__ CUtensorMap tm_v, const __grid_constant__ CUtensorMap tm_d,
+              const __grid_constant__ CUtensorMap tm_o, const BwdParams p) {
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   SmemQ& sm = *reinterpret_cast<SmemQ*>(smem_raw);
   if (smem_misaligned(smem_raw, &g_err_bwd)) return;
@@ -515,6 +514,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     mbar_init(&sm.q_full, 1);
     mbar_init(&sm.q_empty, kWarpLoad);
     mbar_init(&sm.q_ready, kWarpLoad);
+    mbar_init(&sm.o_full, 1);
+    mbar_init(&sm.o_empty, kWarpLoad);
     mbar_init(&sm.d_full, 1);
     mbar_init(&sm.d_empty, 1 + kWarpLoad);   // the last dP, and every softmax warp's part of delta
     for (int s = 0; s < kKRing; ++s) {
@@ -554,14 +555,23 @@ __global__ void __launch_bounds__(kThreads, 1)
       tma_prefetch_desc(&tm_k);
       tma_prefetch_desc(&tm_v);
       tma_prefetch_desc(&tm_d);
-      int it = 0, requests = 0, k_issued = 0, v_issued = 0, q_issued = 0, d_issued = 0;
-      // Q(t+1) is loaded while item t runs: its place is free since the softmax warps copied Q(t).  So item
-      // t + 1 is looked up after the first two K and V tiles of item t, and item t + 2 asked for then.
+      tma_prefetch_desc(&tm_o);
+      int it = 0, requests = 0, k_issued = 0, v_issued = 0, q_issued = 0, o_issued = 0, d_issued = 0;
+      // One place holds Q(t), from which the softmax warps copy it to TMEM, then O(t), of which they form delta,
+      // then Q(t+1): it is loaded while item t runs.  So item t + 1 is looked up after the first two K and V tiles
+      // of item t, and item t + 2 asked for then.
       auto load_q = [&](const ItemQ& i) -> bool {
-        if (q_issued > 0 && !wait_sleep(&sm.q_empty, (q_issued - 1) & 1, abort_flag, err, kErrTimeoutSync)) return false;
+        if (o_issued > 0 && !wait_sleep(&sm.o_empty, (o_issued - 1) & 1, abort_flag, err, kErrTimeoutSync)) return false;
         mbar_arrive_expect_tx(&sm.q_full, kTileBytes);
         load_tile(sm.q, &tm_q, &sm.q_full, i.row0, i.h, i.b);
         ++q_issued;
+        return true;
+      };
+      auto load_o = [&](const ItemQ& i) -> bool {
+        if (!wait_sleep(&sm.q_empty, o_issued & 1, abort_flag, err, kErrTimeoutSync)) return false;
+        mbar_arrive_expect_tx(&sm.o_full, kTileBytes);
+        load_tile(sm.q, &tm_o, &sm.o_full, i.row0, i.h, i.b);
+        ++o_issued;
         return true;
       };
       auto load_kv = [&](const ItemQ& i, int j) -> bool {
@@ -587,7 +597,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           ++v_issued;
         }
         ++it;
-        return true;
+        return j > 0 || load_o(i);
       };
       Work w = first_work();
       ItemQ item = item_q(p, w), next = item;
@@ -612,6 +622,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (*abort_flag) {
         work_teardown(sm.work, requests);
         if (q_issued) mbar_wait_teardown(&sm.q_full, (q_issued - 1) & 1);
+        if (o_issued) mbar_wait_teardown(&sm.o_full, (o_issued - 1) & 1);
         if (d_issued) mbar_wait_teardown(&sm.d_full, (d_issued - 1) & 1);
         for (int i = max(k_issued - kKRing, 0); i < k_issued; ++i)
           mbar_wait_teardown(&sm.k_full[i % kKRing], (i / kKRing) & 1);
@@ -708,9 +719,9 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
     };
     // Q from its tile in shared memory to TMEM: as the A operand from shared memory it would be read
-    // again for every key tile, at the full rate of shared memory while S runs.  With it the loads of
-    // the row's O are started.
-    uint4 o4[4];
+    // again for every key tile, at the full rate of shared memory while S runs.  With it the load of
+    // the row's log-sum-exp is started.
+    float lse = -INFINITY;
     auto begin_item = [&](int n, const ItemQ& item) -> bool {
       if (!mbar_wait_warp<false>(&sm.q_full, n & 1, abort_flag, err, kErrTimeoutTma)) return false;
       uint32_t x[16];
@@ -724,31 +735,28 @@ __global__ void __launch_bounds__(kThreads, 1)
         mbar_arrive(&sm.q_ready);
       }
       const int row = item.row0 + r;
-      const uint4* src = reinterpret_cast<const uint4*>(p.o + (long long)item.b * p.o_s[0] + (long long)row * p.o_s[1] +
-                                                        (long long)item.h * p.o_s[2] + 32 * g);
-#pragma unroll
-      for (int c = 0; c < 4; ++c) o4[c] = row < p.mask.Sq ? __ldg(src + c) : make_uint4(0u, 0u, 0u, 0u);
+      lse = row < p.mask.Sq ? __ldg(p.lse + ((long long)item.b * p.H + item.h) * p.mask.Sq + row) : -INFINITY;
       return true;
     };
-    // -delta of the row, from the O in registers and dO's tile
+    // -delta of the row, from O's tile and dO's
     auto find_delta = [&](int n, float& neg_delta) -> bool {
-      if (!mbar_wait_warp<false>(&sm.d_full, n & 1, abort_flag, err, kErrTimeoutTma)) return false;
-      uint32_t x[16];
+      if (!mbar_wait_warp<false>(&sm.d_full, n & 1, abort_flag, err, kErrTimeoutTma) ||
+          !mbar_wait_warp<false>(&sm.o_full, n & 1, abort_flag, err, kErrTimeoutTma))
+        return false;
+      uint32_t x[16], y[16];
       tile_row(sm.dout, x);
+      tile_row(sm.q, y);
       float a = 0.0f;
 #pragma unroll
-      for (int c = 0; c < 4; ++c) {
-        const uint32_t o[4] = {o4[c].x, o4[c].y, o4[c].z, o4[c].w};
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          a = fmaf(u2f(o[e] << 16), u2f(x[4 * c + e] << 16), a);
-          a = fmaf(u2f(o[e] & 0xffff0000u), u2f(x[4 * c + e] & 0xffff0000u), a);
-        }
+      for (int c = 0; c < 16; ++c) {
+        a = fmaf(u2f(y[c] << 16), u2f(x[c] << 16), a);
+        a = fmaf(u2f(y[c] & 0xffff0000u), u2f(x[c] & 0xffff0000u), a);
       }
       sm.delta[g][r] = a;
       __syncwarp();
       if (lane == 0) {
         mbar_arrive(&sm.d_empty);
+        mbar_arrive(&sm.o_empty);
         mbar_arrive(&sm.delta_full);
       }
       // (the parts are next written in the next item, which no warp comes to before all have dS of this one)
@@ -775,7 +783,6 @@ __global__ void __launch_bounds__(kThreads, 1)
         valid -= kCols * g;
         if (n > 0) {
           const long long head = (long long)item.b * p.H + item.h;
-          const float lse = row < p.mask.Sq ? __ldg(p.lse + head * p.mask.Sq + row) : -INFINITY;
           ok = find_delta(items, nd);
           if (lse == -INFINITY) nd = 0.0f;
           else nl = -lse * kLog2e;
@@ -881,8 +888,8 @@ static_assert(kSmemKV <= 232448 && kSmemQ <= 232448, "227 KB of shared memory pe
 long long attn_bwd_padded_rows(long long Sq) { return (Sq + kTile - 1) / kTile * kTile; }
 
 cudaError_t launch_attn_bwd_bf16(const CUtensorMap& tm_q, const CUtensorMap& tm_k, const CUtensorMap& tm_v,
-                                 const CUtensorMap& tm_d, const TrainArgs& a, const BwdTensors& t, float* workspace,
-                                 cudaStream_t stream) {
+                                 const CUtensorMap& tm_d, const CUtensorMap& tm_o, const TrainArgs& a,
+                                 const BwdTensors& t, float* workspace, cudaStream_t stream) {
   static ContextOnce attr_done;
   cudaError_t e = attr_done.run([] {
     cudaError_t r = cudaFuncSetAttribute(dkdv_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemKV);
@@ -899,7 +906,6 @@ cudaError_t launch_attn_bwd_bf16(const CUtensorMap& tm_q, const CUtensorMap& tm_
   p.neg_delta = workspace + (long long)a.B * a.Hq * Sq_pad;
   p.Sq_pad = Sq_pad;
   p.group = a.Hq / a.Hkv;
-  p.o = reinterpret_cast<const __nv_bfloat16*>(t.o);
   p.lse = t.lse;
   const int k_tiles = (a.Sk + kTile - 1) / kTile, q_tiles = Sq_pad / kTile;
   p.H = a.Hq;
@@ -909,12 +915,11 @@ cudaError_t launch_attn_bwd_bf16(const CUtensorMap& tm_q, const CUtensorMap& tm_
   p.d0 = reinterpret_cast<__nv_bfloat16*>(t.dq);
   p.d1 = nullptr;
   for (int i = 0; i < 3; ++i) {
-    p.o_s[i] = t.o_str[i];
     p.s0[i] = t.dq_str[i];
     p.s1[i] = 0;
   }
-  e = launch_dependent(dq_kernel, dim3((unsigned)p.order.items), kThreads, kSmemQ, stream, tm_q,
-                       tm_k, tm_v, tm_d, p);
+  e = launch_dependent(dq_kernel, dim3((unsigned)p.order.items), kThreads, kSmemQ, stream, tm_q, tm_k, tm_v, tm_d,
+                       tm_o, p);
   if (e != cudaSuccess) return e;
   p.H = a.Hkv;
   p.by_H = make_div(p.H);
@@ -929,11 +934,12 @@ cudaError_t launch_attn_bwd_bf16(const CUtensorMap& tm_q, const CUtensorMap& tm_
                           tm_q, tm_k, tm_v, tm_d, p);
 }
 
-cudaError_t read_and_clear_err_bwd(uint32_t* out) {
+static cudaError_t read_and_clear_err_bwd(uint32_t* out) {
   cudaError_t e = cudaMemcpyFromSymbol(out, g_err_bwd, sizeof(uint32_t));
   if (e != cudaSuccess) return e;
   const uint32_t zero = 0;
   return cudaMemcpyToSymbol(g_err_bwd, &zero, sizeof(uint32_t));
 }
+static const bool err_reader_added = add_err_reader(read_and_clear_err_bwd);
 
 }  // namespace sa

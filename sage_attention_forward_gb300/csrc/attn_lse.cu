@@ -435,11 +435,12 @@ cudaError_t launch_attn_fwd_bf16_lse(const CUtensorMap& tm_q, const CUtensorMap&
                           p);
 }
 
-cudaError_t read_and_clear_err_lse(uint32_t* out) {
+static cudaError_t read_and_clear_err_lse(uint32_t* out) {
   cudaError_t e = cudaMemcpyFromSymbol(out, g_err_lse, sizeof(uint32_t));
   if (e != cudaSuccess) return e;
   const uint32_t zero = 0;
   return cudaMemcpyToSymbol(g_err_lse, &zero, sizeof(uint32_t));
 }
+static const bool err_reader_added = add_err_reader(read_and_clear_err_lse);
 
 }  // namespace sa

@@ -80,6 +80,9 @@ cudaError_t launch_attn_fwd_bf16(const CUtensorMap& tm_q, const CUtensorMap& tm_
 cudaError_t launch_sm_clock_probe(unsigned long long* out, int n_slots, int num_sms, cudaStream_t stream);
 // The device error word all three modes record bounded-wait timeouts in.
 cudaError_t read_and_clear_err_attn(uint32_t* out);
+// Other translation units with bounded waits add the reader of their error word when the library is loaded.
+using ErrReader = cudaError_t (*)(uint32_t* out);
+bool add_err_reader(ErrReader read);
 
 // Sage prepare (sage_prepare.cu)
 struct PrepareArgs {
@@ -199,20 +202,17 @@ struct TrainArgs {
 cudaError_t launch_attn_fwd_bf16_lse(const CUtensorMap& tm_q, const CUtensorMap& tm_k, const CUtensorMap& tm_v,
                                      const TrainArgs& a, void* o, const long long o_str[3], float* lse,
                                      cudaStream_t stream);
-cudaError_t read_and_clear_err_lse(uint32_t* out);
 
 struct BwdTensors {
-  const void *o, *dout;
   const float* lse;
   void *dq, *dk, *dv;
-  long long o_str[3], dout_str[3], dq_str[3], dk_str[3], dv_str[3];
+  long long dq_str[3], dk_str[3], dv_str[3];
 };
 // Query rows padded to whole tiles: the workspace is 2 * B * Hq * padded floats.
 long long attn_bwd_padded_rows(long long Sq);
 cudaError_t launch_attn_bwd_bf16(const CUtensorMap& tm_q, const CUtensorMap& tm_k, const CUtensorMap& tm_v,
-                                 const CUtensorMap& tm_d, const TrainArgs& a, const BwdTensors& t, float* workspace,
-                                 cudaStream_t stream);
-cudaError_t read_and_clear_err_bwd(uint32_t* out);
+                                 const CUtensorMap& tm_d, const CUtensorMap& tm_o, const TrainArgs& a,
+                                 const BwdTensors& t, float* workspace, cudaStream_t stream);
 
 // Layer norm (layer_norm.cu).  Types of x, dy and the results, and of the weights.
 enum : int { kBF16 = 0, kF16 = 1, kF32 = 2 };
@@ -225,7 +225,6 @@ struct LayerNormArgs {
   float eps;
 };
 size_t layer_norm_bwd_workspace(int rows, int N);
-cudaError_t read_and_clear_err_norm(uint32_t* out);
 cudaError_t launch_layer_norm_fwd(const LayerNormArgs& a, void* y, const long long y_str[3], cudaStream_t stream);
 // dw, db: both or neither.
 cudaError_t launch_layer_norm_bwd(const LayerNormArgs& a, const void* dy, const long long dy_str[3], void* dx,

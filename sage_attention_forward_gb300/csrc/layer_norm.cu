@@ -862,11 +862,12 @@ cudaError_t launch_layer_norm_bwd(const LayerNormArgs& a, const void* dy, const 
                           static_cast<const float*>(workspace), s.ctas, p.N, dw, db, a.w_type);
 }
 
-cudaError_t read_and_clear_err_norm(uint32_t* out) {
+static cudaError_t read_and_clear_err_norm(uint32_t* out) {
   cudaError_t e = cudaMemcpyFromSymbol(out, g_err_norm, sizeof(uint32_t));
   if (e != cudaSuccess) return e;
   const uint32_t zero = 0;
   return cudaMemcpyToSymbol(g_err_norm, &zero, sizeof(uint32_t));
 }
+static const bool err_reader_added = add_err_reader(read_and_clear_err_norm);
 
 }  // namespace sa
