@@ -76,8 +76,10 @@ attn_status attn_fwd_bf16_lse(const void* q, const void* k, const void* v, void*
 }
 
 size_t attn_bwd_bf16_workspace_size(int B, int Sq, int Sk, int Hq, int Hkv) {
-  if (B < 1 || Sq < 1 || Sk < 1 || Hq < 1 || Hkv < 1) return 0;
-  return (size_t)2 * B * Hq * (size_t)sa::attn_bwd_padded_rows(Sq) * sizeof(float);
+  bool empty = false;
+  sa::TrainArgs a;
+  if (check_train(B, Sq, Sk, Hq, Hkv, 128, 0, nullptr, 0.0f, a, &empty) != ATTN_OK || empty) return 0;
+  return sa::attn_bwd_workspace(a);
 }
 
 attn_status attn_bwd_bf16(const void* dout, const void* q, const void* k, const void* v, const void* o,
@@ -107,7 +109,7 @@ attn_status attn_bwd_bf16(const void* dout, const void* q, const void* k, const 
   for (const void* in : {dout, q, k, v, o}) shared = shared || dq == in || dk == in || dv == in;
   if (shared)
     return fail(ATTN_ERR_INVALID_ARG, "attn_bwd_bf16: dq, dk and dv must overlap neither the inputs nor one another");
-  const size_t need = attn_bwd_bf16_workspace_size(B, Sq, Sk, Hq, Hkv);
+  const size_t need = sa::attn_bwd_workspace(a);
   if (workspace_bytes < need)
     return fail(ATTN_ERR_INVALID_ARG, "attn_bwd_bf16: workspace_bytes=%zu < %zu required", workspace_bytes, need);
   TRY(check_device());

@@ -29,6 +29,8 @@
 // P forms dS); every sum is FP32.
 #include <cuda_runtime.h>
 
+#include <algorithm>
+#include <cmath>
 #include <type_traits>
 
 #include "attn_tiles.cuh"
@@ -47,6 +49,11 @@ constexpr int kWarpLoad = 4 * kGroups;
 constexpr int kWarpMma = kWarpLoad + 1;   // and the next
 constexpr int kWarpClear = kWarpMma + 2;
 constexpr int kThreads = 32 * (kWarpClear + 1);
+// Products before an item's last at which the load warp, itself two or three ahead of the tensor core, asks
+// for the next item: early enough to hide the answer's way, and late, because an SM that has asked has to
+// take what it got (asked for at the start of the item, 256 items of unequal length left the
+// first SMs with a second long one: 409 us of a backward in place of 332).
+constexpr int kAskAhead = 5;
 constexpr float kLog2e = 1.4426950408889634f;
 
 __device__ uint32_t g_err_bwd;
@@ -67,6 +74,11 @@ struct BwdParams {
   int H, group;             // heads of this grid (Hkv, or Hq), Hq / Hkv
   Div by_H, by_group;
   Order order;
+  // dkdv_kernel: the parts that a key tile's products are divided into, each an item; with more than
+  // one, their sums as FP32 [unit][part][dV, dK][32 pieces of four channels][128 keys][4]
+  int parts;
+  Div by_parts;
+  float4* partial;
 };
 
 // Q(i) is held from S(i) to dK(i), most of two steps, and S(i+2) follows dK(i) closely: with two
@@ -93,13 +105,15 @@ struct __align__(1024) SmemKV {
   uint32_t abort_flag;
 };
 
-// One item: 128 keys of one key head, with the query tiles of the heads that share it.
-struct ItemKV {
+// 128 keys of one key head (a unit), with the query tiles of the heads that share it.
+struct UnitKV {
   int b, hk, key0, keys, first, n_q, n;   // n: products with a query tile, 0 when no query sees a key
 };
-__device__ __forceinline__ ItemKV item_kv(const BwdParams& p, const Work& w) {
-  ItemKV i;
+__device__ __forceinline__ UnitKV unit_kv(const BwdParams& p, int index) {
+  UnitKV i;
   int tile, head;
+  Work w;
+  w.index = index;
   work_place(p.order, w, tile, head);
   i.b = div_by(head, p.by_H);
   i.hk = head - i.b * p.H;
@@ -111,7 +125,33 @@ __device__ __forceinline__ ItemKV item_kv(const BwdParams& p, const Work& w) {
   i.n = i.key0 < i.keys ? max(i.n_q - i.first, 0) * p.group : 0;
   return i;
 }
+// Products of each part but the last of a unit with n (parts without any stay unwritten).
+__device__ __forceinline__ int part_length(const BwdParams& p, int n) { return div_by(n + p.parts - 1, p.by_parts); }
 
+// One item: a part of a unit, from query tile t of the h-th head that shares the keys on.
+struct ItemKV : UnitKV {
+  int t, h;
+};
+template <bool kParts>
+__device__ __forceinline__ ItemKV item_kv(const BwdParams& p, const Work& w) {
+  ItemKV i;
+  const int unit = kParts ? div_by(w.index, p.by_parts) : w.index;
+  static_cast<UnitKV&>(i) = unit_kv(p, unit);
+  i.t = i.first;
+  i.h = 0;
+  if (kParts) {
+    const int len = part_length(p, i.n), start = (w.index - unit * p.parts) * len;
+    i.n = max(min(i.n - start, len), 0);
+    if (i.n > 0) {
+      i.h = start / (i.n_q - i.first);
+      i.t = i.first + start % (i.n_q - i.first);
+    }
+  }
+  return i;
+}
+
+// kParts: units in parts (the other form has not their code: with it the loop took 3 % longer).
+template <bool kParts>
 __global__ void __launch_bounds__(kThreads, 1)
     dkdv_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
                 const __grid_constant__ CUtensorMap tm_v, const __grid_constant__ CUtensorMap tm_d,
@@ -169,13 +209,21 @@ __global__ void __launch_bounds__(kThreads, 1)
       tma_prefetch_desc(&tm_v);
       tma_prefetch_desc(&tm_d);
       int it = 0, items = 0, requests = 0, q_issued = 0, d_issued = 0, r_issued = 0, k_issued = 0, v_issued = 0;
+      Work w = first_work();
+      auto ask_next = [&]() -> bool {
+        if (!work_request(sm.work, w.t + 1, abort_flag, err)) return false;
+        ++requests;
+        return true;
+      };
       auto load_item = [&](const ItemKV& i) -> bool {
         if (items > 0 && !wait_sleep(&sm.k_empty, (items - 1) & 1, abort_flag, err, kErrTimeoutSync)) return false;
         mbar_arrive_expect_tx(&sm.k_full, kTileBytes);
         load_tile(sm.k, &tm_k, &sm.k_full, i.key0, i.hk, i.b);
         ++k_issued;
-        int t = i.first, h = i.hk * p.group;
+        int t = i.t, h = i.hk * p.group + i.h;
+        const int ask = max(i.n - kAskAhead, 0);
         for (int j = 0; j < i.n; ++j, ++it) {
+          if (j == ask && !ask_next()) return false;
           const int qs = it % kQRing, qu = it / kQRing, ds = it % kDRing, du = it / kDRing, rs = it & 1, ru = it >> 1;
           if (qu > 0 && !wait_sleep(&sm.q_empty[qs], (qu - 1) & 1, abort_flag, err, kErrTimeoutSync)) return false;
           mbar_arrive_expect_tx(&sm.q_full[qs], kTileBytes);
@@ -205,12 +253,9 @@ __global__ void __launch_bounds__(kThreads, 1)
         ++items;
         return true;
       };
-      Work w = first_work();
       do {
-        if (!work_request(sm.work, w.t + 1, abort_flag, err)) break;
-        ++requests;
-        const ItemKV i = item_kv(p, w);
-        if (i.n > 0 && !load_item(i)) break;
+        const ItemKV i = item_kv<kParts>(p, w);
+        if (!(i.n > 0 ? load_item(i) : ask_next())) break;
       } while (work_next_load(sm.work, w, abort_flag, err));
       if (*abort_flag) {
         // nothing may land in this CTA's shared memory after it has gone
@@ -236,7 +281,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint32_t dk = desc_k(sm.k), dv = desc_k(sm.v), dq = desc_k(sm.q[0]), dd = desc_k(sm.dout[0]);
     const uint32_t dq_mn = desc_mn(sm.q[0]), dd_mn = desc_mn(sm.dout[0]);
     int k_items = 0, v_items = 0;
-    auto make = [&](const Work& w) { return item_kv(p, w); };
+    auto make = [&](const Work& w) { return item_kv<kParts>(p, w); };
     Walk<ItemKV, decltype(make)> walk(make);
     int f0 = walk.next(sm.work, lane, abort_flag, err);
     // (a step's ring slots are compile-time constants, and so are the distances of its descriptors)
@@ -315,10 +360,10 @@ __global__ void __launch_bounds__(kThreads, 1)
     int it = 0, items = 0, turn = 0;
     do {
       {
-        const ItemKV item = item_kv(p, work_read(sm.work, turn));
+        const ItemKV item = item_kv<kParts>(p, work_read(sm.work, turn));
         const int key = item.key0 + wq * 32 + (lane >> 2);   // and the keys 8, 16, 24 after it
         const int t_first = item.first, t_end = item.n_q;
-        int t = t_first;
+        int t = item.t;
         for (int end = it + item.n; it != end; ++it) {
           const int slot = it & 1;
           // a tile on the diagonal: the thread's column 8 i + e sees its key r from
@@ -424,25 +469,45 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (!ok) break;
       // warpgroups 0 and 1 store dV's channels, 2 and 3 dK's; keys that no query sees get zeros (their
       // rows hold what the padding made of them), and a key alone in its batch entry has dK = 0
-      const ItemKV done = item_kv(p, work_read(sm.work, turn));
+      const ItemKV done = item_kv<kParts>(p, work_read(sm.work, turn));
       const int which = g / (kGroups / 2), ch = (g % (kGroups / 2)) * 64;
       const int row0 = done.key0 + wq * 32;
       const long long* str = which == 0 ? p.s1 : p.s0;
-      uint32_t out[32] = {};
+      const uint32_t acc = tmem + lane_off + 256 + 128 * which + ch;
       if (done.n > 0) {
         ok = mbar_wait_warp<false>(&sm.acc_done, items++ & 1, abort_flag, err, kErrTimeoutMma);
         if (!ok) break;
         tc_fence_after();
-        load_row_bf16<64>(tmem + lane_off + 256 + 128 * which + ch, out, which == 0 ? 1.0f : p.scale);
-        tc_fence_before();
-        if (row0 + lane >= done.keys || (which == 1 && done.keys == 1)) {
+      }
+      if (!kParts) {
+        uint32_t out[32] = {};
+        if (done.n > 0) {
+          load_row_bf16<64>(acc, out, which == 0 ? 1.0f : p.scale);
+          if (row0 + lane >= done.keys || (which == 1 && done.keys == 1)) {
 #pragma unroll
-          for (int e = 0; e < 32; ++e) out[e] = 0u;
+            for (int e = 0; e < 32; ++e) out[e] = 0u;
+          }
+        }
+        store_rows<64>((which == 0 ? p.d1 : p.d0) + (long long)done.b * str[0] + (long long)row0 * str[1] +
+                           (long long)done.hk * str[2] + ch,
+                       str[1], out, p.mask.Sk - row0, lane);
+      } else if (done.n > 0) {
+        // (a piece of four channels of a warp's rows is one contiguous store)
+        float4* dst = p.partial + ((long long)work_read(sm.work, turn).index * 2 + which) * (32 * kTile) +
+                      (ch / 4) * kTile + wq * 32 + lane;
+#pragma unroll
+        for (int cc = 0; cc < 2; ++cc) {
+          uint32_t a[32];
+          tmem_ld32(acc + 32 * cc, a);
+          tmem_ld_wait();
+          tmem_reg_fence(a);
+#pragma unroll
+          for (int e = 0; e < 8; ++e)
+            dst[(8 * cc + e) * kTile] =
+                make_float4(u2f(a[4 * e]), u2f(a[4 * e + 1]), u2f(a[4 * e + 2]), u2f(a[4 * e + 3]));
         }
       }
-      store_rows<64>((which == 0 ? p.d1 : p.d0) + (long long)done.b * str[0] + (long long)row0 * str[1] +
-                         (long long)done.hk * str[2] + ch,
-                     str[1], out, p.mask.Sk - row0, lane);
+      tc_fence_before();
       work_release(sm.work, turn, lane);
     } while (work_wait(sm.work, ++turn, abort_flag, err));
   }
@@ -454,6 +519,44 @@ __global__ void __launch_bounds__(kThreads, 1)
     __syncwarp();
     tmem_dealloc(sm.tmem_base, 512);
   }
+}
+
+// The parts of a unit's dV and dK in their order, rounded once.  A thread has eight channels of a key.
+constexpr int kJoinThreads = 256;
+constexpr int kJoinBlocks = 2 * kTile * (128 / 8) / kJoinThreads;   // of a unit
+__global__ void __launch_bounds__(kJoinThreads) join_kernel(const BwdParams p) {
+  griddep_wait();
+  const int index = blockIdx.x / kJoinBlocks, at = (blockIdx.x % kJoinBlocks) * kJoinThreads + threadIdx.x;
+  const UnitKV u = unit_kv(p, index);
+  // four lanes have 32 channels of a key, a warp eight keys
+  const int key = (at >> 2) % kTile, rest = (at >> 2) / kTile, c8 = (at & 3) + 4 * (rest & 3), which = rest >> 2;
+  if (u.key0 + key >= p.mask.Sk) return;
+  float sum[8] = {};
+  if (u.n > 0 && u.key0 + key < u.keys && !(which == 1 && u.keys == 1)) {
+    const int len = part_length(p, u.n);
+    const float4* src = p.partial + ((long long)index * p.parts * 2 + which) * (32 * kTile) + 2 * c8 * kTile + key;
+#pragma unroll 4
+    for (int done = 0; done < u.n; done += len, src += 2 * 32 * kTile) {
+      const float4 x = __ldcg(src), y = __ldcg(src + kTile);
+      sum[0] += x.x;
+      sum[1] += x.y;
+      sum[2] += x.z;
+      sum[3] += x.w;
+      sum[4] += y.x;
+      sum[5] += y.y;
+      sum[6] += y.z;
+      sum[7] += y.w;
+    }
+  }
+  const float f = which == 0 ? 1.0f : p.scale;
+  const long long* str = which == 0 ? p.s1 : p.s0;
+  uint4 out;
+  out.x = pack_bf16x2(sum[0] * f, sum[1] * f);
+  out.y = pack_bf16x2(sum[2] * f, sum[3] * f);
+  out.z = pack_bf16x2(sum[4] * f, sum[5] * f);
+  out.w = pack_bf16x2(sum[6] * f, sum[7] * f);
+  *reinterpret_cast<uint4*>((which == 0 ? p.d1 : p.d0) + (long long)u.b * str[0] + (long long)(u.key0 + key) * str[1] +
+                            (long long)u.hk * str[2] + 8 * c8) = out;
 }
 
 // ------------------------------------------------------------------ dQ
@@ -558,8 +661,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       tma_prefetch_desc(&tm_o);
       int it = 0, requests = 0, k_issued = 0, v_issued = 0, q_issued = 0, o_issued = 0, d_issued = 0;
       // One place holds Q(t), from which the softmax warps copy it to TMEM, then O(t), of which they form delta,
-      // then Q(t+1): it is loaded while item t runs.  So item t + 1 is looked up after the first two K and V tiles
-      // of item t, and item t + 2 asked for then.
+      // then Q(t+1): it is loaded while item t runs.  So item t + 1 is looked up before the last two K and V tiles
+      // of item t.
       auto load_q = [&](const ItemQ& i) -> bool {
         if (o_issued > 0 && !wait_sleep(&sm.o_empty, (o_issued - 1) & 1, abort_flag, err, kErrTimeoutSync)) return false;
         mbar_arrive_expect_tx(&sm.q_full, kTileBytes);
@@ -600,23 +703,22 @@ __global__ void __launch_bounds__(kThreads, 1)
         return j > 0 || load_o(i);
       };
       Work w = first_work();
-      ItemQ item = item_q(p, w), next = item;
-      bool ok = work_request(sm.work, 1, abort_flag, err), more = true;
-      if (ok) ++requests;
-      if (ok && item.n > 0) ok = load_q(item);
+      ItemQ item = item_q(p, w);
+      bool ok = item.n == 0 || load_q(item), more = true;
       while (ok && more) {
-        const int early = min(item.n, 2);
-        for (int j = 0; ok && j < early; ++j) ok = load_kv(item, j);
-        if (!ok) break;
-        more = work_next_load(sm.work, w, abort_flag, err);
-        if (more) {
-          ok = work_request(sm.work, w.t + 1, abort_flag, err);
-          if (!ok) break;
-          ++requests;
-          next = item_q(p, w);
-          if (next.n > 0) ok = load_q(next);
+        ItemQ next = item;
+        const int ask = max(item.n - kAskAhead, 0), look = max(item.n - 2, min(item.n, 2));
+        for (int j = 0; ok && j <= item.n; ++j) {
+          if (j == ask) {
+            ok = work_request(sm.work, w.t + 1, abort_flag, err);
+            if (ok) ++requests;
+          }
+          if (ok && j == look && (more = work_next_load(sm.work, w, abort_flag, err))) {
+            next = item_q(p, w);
+            ok = next.n == 0 || load_q(next);
+          }
+          ok = ok && (j == item.n || load_kv(item, j));
         }
-        for (int j = early; ok && j < item.n; ++j) ok = load_kv(item, j);
         item = next;
       }
       if (*abort_flag) {
@@ -883,16 +985,65 @@ constexpr int kSmemKV = (int)sizeof(SmemKV);
 constexpr int kSmemQ = (int)sizeof(SmemQ);
 static_assert(kSmemKV <= 232448 && kSmemQ <= 232448, "227 KB of shared memory per CTA");
 
+// Parts of each unit of dK and dV: with fewer units than a few per SM, whole units leave SMs idle at the end.
+// Times are in products of a tile pair (1.3 us): an item costs two besides its products (first loads and
+// results), the parts' sums 0.027 each to write and read, the kernel that joins them two.  The
+// products' own time is at least an SM's share of them all, and, as the longest items start
+// first, k + 1 times the length of item 152 k: one SM has that many as long.  Backward with 1 part and
+// with the parts chosen: 96 units of 132 products 350 and 303 us (3 parts); 16 of 64: 107 and 39 (9); 8 of 128:
+// 224 and 70 (19); causal, 64 of up to 128: 223 and 105 (4); 256 of up to 128: 332, and 344 with 2, so 1.
+constexpr int kSms = 152, kMostRounds = 8;
+int kv_parts(const TrainArgs& a) {
+  const int tiles = (a.Sk + kTile - 1) / kTile, n_q = (a.Sq + kTile - 1) / kTile, group = a.Hq / a.Hkv;
+  const int off = a.Sk - a.Sq;
+  const long long heads = (long long)a.B * a.Hkv, units = tiles * heads;
+  if (units > kMostRounds * kSms / 2) return 1;
+  // products of a unit of tile t: that many of the tiles of a head's queries see it
+  auto length = [&](long long t) {
+    const long long first = a.causal ? std::max(t * kTile - off, 0ll) / kTile : 0;
+    return (double)group * (double)std::max(n_q - first, 0ll);
+  };
+  double total = 0;
+  for (int t = 0; t < tiles; ++t) total += length(t) * (double)heads;
+  int best = 1;
+  double least = 0;
+  for (int rounds = 0; rounds <= kMostRounds; ++rounds) {
+    const long long parts = rounds == 0 ? 1 : std::min(rounds * kSms / units, (long long)length(0));
+    if (rounds > 0 && parts <= best) continue;
+    const long long items = units * parts;
+    double products = total / kSms;
+    int k = 0;
+    for (; (long long)k * kSms < items; ++k)
+      products = std::max(products, (k + 1) * std::ceil(length(k * kSms / (heads * parts)) / (double)parts));
+    const double time = products + 2 * k + (parts > 1 ? 2 + 0.027 * (double)items : 0);
+    if (rounds == 0 || time < least) {
+      least = time;
+      best = (int)parts;
+    }
+  }
+  return best;
+}
+
 }  // namespace
 
-long long attn_bwd_padded_rows(long long Sq) { return (Sq + kTile - 1) / kTile * kTile; }
+static long long attn_bwd_padded_rows(long long Sq) { return (Sq + kTile - 1) / kTile * kTile; }
+
+size_t attn_bwd_workspace(TrainArgs a) {
+  const size_t rows = (size_t)2 * a.B * a.Hq * (size_t)attn_bwd_padded_rows(a.Sq) * sizeof(float);
+  int parts = 1;
+  for (a.causal = 0; a.causal < 2; ++a.causal) parts = std::max(parts, kv_parts(a));
+  const size_t units = (size_t)((a.Sk + kTile - 1) / kTile) * a.B * a.Hkv;
+  return rows + (parts > 1 ? units * parts * 2 * kTile * 128 * sizeof(float) : 0);
+}
 
 cudaError_t launch_attn_bwd_bf16(const CUtensorMap& tm_q, const CUtensorMap& tm_k, const CUtensorMap& tm_v,
                                  const CUtensorMap& tm_d, const CUtensorMap& tm_o, const TrainArgs& a,
                                  const BwdTensors& t, float* workspace, cudaStream_t stream) {
   static ContextOnce attr_done;
   cudaError_t e = attr_done.run([] {
-    cudaError_t r = cudaFuncSetAttribute(dkdv_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemKV);
+    cudaError_t r = cudaFuncSetAttribute(dkdv_kernel<false>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemKV);
+    if (r != cudaSuccess) return r;
+    r = cudaFuncSetAttribute(dkdv_kernel<true>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemKV);
     if (r != cudaSuccess) return r;
     return cudaFuncSetAttribute(dq_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemQ);
   });
@@ -914,6 +1065,9 @@ cudaError_t launch_attn_bwd_bf16(const CUtensorMap& tm_q, const CUtensorMap& tm_
   p.order = make_order(q_tiles, a.B * a.Hq, a.causal);
   p.d0 = reinterpret_cast<__nv_bfloat16*>(t.dq);
   p.d1 = nullptr;
+  p.parts = 1;
+  p.by_parts = make_div(1);
+  p.partial = nullptr;
   for (int i = 0; i < 3; ++i) {
     p.s0[i] = t.dq_str[i];
     p.s1[i] = 0;
@@ -924,14 +1078,22 @@ cudaError_t launch_attn_bwd_bf16(const CUtensorMap& tm_q, const CUtensorMap& tm_
   p.H = a.Hkv;
   p.by_H = make_div(p.H);
   p.order = make_order(k_tiles, a.B * a.Hkv, a.causal);
+  p.parts = kv_parts(a);
+  p.by_parts = make_div(p.parts);
+  p.partial = reinterpret_cast<float4*>(p.neg_delta + (long long)a.B * a.Hq * Sq_pad);
   p.d0 = reinterpret_cast<__nv_bfloat16*>(t.dk);
   p.d1 = reinterpret_cast<__nv_bfloat16*>(t.dv);
   for (int i = 0; i < 3; ++i) {
     p.s0[i] = t.dk_str[i];
     p.s1[i] = t.dv_str[i];
   }
-  return launch_dependent(dkdv_kernel, dim3((unsigned)p.order.items), kThreads, kSmemKV, stream,
-                          tm_q, tm_k, tm_v, tm_d, p);
+  if (p.parts == 1)
+    return launch_dependent(dkdv_kernel<false>, dim3((unsigned)p.order.items), kThreads, kSmemKV, stream, tm_q, tm_k,
+                            tm_v, tm_d, p);
+  e = launch_dependent(dkdv_kernel<true>, dim3((unsigned)(p.order.items * p.parts)), kThreads, kSmemKV, stream, tm_q,
+                       tm_k, tm_v, tm_d, p);
+  if (e != cudaSuccess) return e;
+  return launch_dependent(join_kernel, dim3((unsigned)(p.order.items * kJoinBlocks)), kJoinThreads, 0, stream, p);
 }
 
 static cudaError_t read_and_clear_err_bwd(uint32_t* out) {

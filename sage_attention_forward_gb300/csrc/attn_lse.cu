@@ -50,6 +50,10 @@ struct __align__(1024) Smem {
   uint32_t abort_flag;
 };
 
+// Key tiles before an item's last at which the load warp asks for the next item: early enough to hide the
+// answer's way, and late, because an SM that has asked has to take what it got.
+constexpr int kAskAhead = 4;
+
 __device__ uint32_t g_err_lse;
 
 struct Params {
@@ -130,13 +134,21 @@ __global__ void __launch_bounds__(kThreads, 1)
       tma_prefetch_desc(&tm_k);
       tma_prefetch_desc(&tm_v);
       int it = 0, items = 0, requests = 0, q_issued = 0, k_issued = 0, v_issued = 0;
+      Work w = first_work();
+      auto ask_next = [&]() -> bool {
+        if (!work_request(sm.work, w.t + 1, abort_flag, err)) return false;
+        ++requests;
+        return true;
+      };
       auto load_item = [&](const Item& i) -> bool {
         const int hk = div_by(i.h, p.by_group);
         if (items > 0 && !wait_sleep(&sm.q_empty, (items - 1) & 1, abort_flag, err, kErrTimeoutSync)) return false;
         mbar_arrive_expect_tx(&sm.q_full, kNQ * kTileBytes);
         for (int q = 0; q < kNQ; ++q) load_tile(sm.q[q], &tm_q, &sm.q_full, i.row0 + q * kTile, i.h, i.b);
         ++q_issued;
+        const int ask = max(i.n - kAskAhead, 0);
         for (int j = 0; j < i.n; ++j, ++it) {
+          if (j == ask && !ask_next()) return false;
           const int slot = it % kStages, use = it / kStages;
           if (use > 0 && !wait_sleep(&sm.k_empty[slot], (use - 1) & 1, abort_flag, err, kErrTimeoutSync)) return false;
           mbar_arrive_expect_tx(&sm.k_full[slot], kTileBytes);
@@ -150,12 +162,9 @@ __global__ void __launch_bounds__(kThreads, 1)
         ++items;
         return true;
       };
-      Work w = first_work();
       do {
-        if (!work_request(sm.work, w.t + 1, abort_flag, err)) break;
-        ++requests;
         const Item i = item_of(p, w);
-        if (i.n > 0 && !load_item(i)) break;
+        if (!(i.n > 0 ? load_item(i) : ask_next())) break;
       } while (work_next_load(sm.work, w, abort_flag, err));
       if (*abort_flag) {
         // nothing may land in this CTA's shared memory after it has gone

@@ -208,8 +208,8 @@ struct BwdTensors {
   void *dq, *dk, *dv;
   long long dq_str[3], dk_str[3], dv_str[3];
 };
-// Query rows padded to whole tiles: the workspace is 2 * B * Hq * padded floats.
-long long attn_bwd_padded_rows(long long Sq);
+// Bytes of workspace for these shapes, whatever the mask.
+size_t attn_bwd_workspace(TrainArgs a);
 cudaError_t launch_attn_bwd_bf16(const CUtensorMap& tm_q, const CUtensorMap& tm_k, const CUtensorMap& tm_v,
                                  const CUtensorMap& tm_d, const CUtensorMap& tm_o, const TrainArgs& a,
                                  const BwdTensors& t, float* workspace, cudaStream_t stream);

@@ -212,3 +212,19 @@ def test_empty_problem(cuda_dev):
     assert o.shape == (0, 30, 2, 128) and lse.shape == (0, 2, 30)
     dq, dk, dv = sa.attn_bwd_bf16(o, z(0, 30, 2, 128), z(0, 40, 2, 128), z(0, 40, 2, 128), o, lse)
     assert dq.shape == o.shape and dk.shape == dv.shape == (0, 40, 2, 128)
+
+
+@pytest.mark.parametrize("causal", [False, True])
+@pytest.mark.parametrize("B,Sq,Sk,Hq,Hkv,lens", [
+    (1, 2000, 130, 4, 2, None), (1, 1500, 128, 3, 3, [77]), (2, 1111, 257, 4, 1, [257, 0]), (1, 700, 1, 8, 1, None),
+    (1, 130, 400, 40, 1, [300]), (1, 3000, 300, 2, 1, [1])])
+def test_divided_sums(cuda_dev, B, Sq, Sk, Hq, Hkv, lens, causal):
+    """Few key tiles and many products: dK and dV are formed in parts, which the workspace holds."""
+    rows = 2 * B * Hq * ((Sq + 127) // 128 * 128) * 4
+    assert sa.attn_bwd_workspace(B, Sq, Sk, Hq, Hkv, "cpu").numel() > rows
+    kv_len = None if lens is None else torch.tensor(lens, dtype=torch.int32, device=cuda_dev)
+    q, k, v, d = make(cuda_dev, B, Sq, Sk, Hq, Hkv, seed=Sq)
+    o, lse, got = check(q, k, v, d, causal=causal, kv_len=kv_len)
+    again = sa.attn_bwd_bf16(d, q, k, v, o, lse, causal=causal, kv_len=kv_len)
+    for a, b in zip(got, again):
+        assert torch.equal(a, b)
