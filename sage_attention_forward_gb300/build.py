@@ -18,7 +18,8 @@ ROOT = os.path.dirname(HERE)
 CSRC = os.path.join(HERE, "csrc")
 OUT_DIR = os.path.join(HERE, "_build")
 LIB = os.path.join(OUT_DIR, "libsageattn.so")
-SOURCES = ["api.cu", "attn_fwd.cu", "sage_prepare.cu", "api_train.cu", "attn_lse.cu", "attn_bwd.cu", "layer_norm.cu"]
+SOURCES = ["api.cu", "attn_fwd.cu", "sage_prepare.cu", "attn_lse.cu", "attn_bwd.cu", "layer_norm.cu"]
+HOST_SOURCES = ["api_train.cpp"]   # no kernels
 HEADERS = ["ptx.cuh", "kernels.h", "api_checks.h", "qk_quant.cuh", "attn_tiles.cuh"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
@@ -47,9 +48,9 @@ def build(force: bool = False, verbose: bool = False, extra_flags=()) -> str:
     os.makedirs(OUT_DIR, exist_ok=True)
     hdrs = [os.path.join(CSRC, h) for h in HEADERS] + [os.path.join(ROOT, "include", "sageattn.h")]
     objs, jobs = [], []
-    for src in SOURCES:
+    for src in SOURCES + HOST_SOURCES:
         s = os.path.join(CSRC, src)
-        o = os.path.join(OUT_DIR, src.replace(".cu", ".o"))
+        o = os.path.join(OUT_DIR, os.path.splitext(src)[0] + ".o")
         objs.append(o)
         if force or _stale(o, [s] + hdrs):
             cmd = [nvcc()] + _flags(extra_flags) + ["-c", s, "-o", o]
