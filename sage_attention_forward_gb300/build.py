@@ -20,7 +20,7 @@ OUT_DIR = os.path.join(HERE, "_build")
 LIB = os.path.join(OUT_DIR, "libsageattn.so")
 SOURCES = ["api.cu", "attn_fwd.cu", "sage_prepare.cu", "attn_lse.cu", "attn_bwd.cu", "layer_norm.cu"]
 HOST_SOURCES = ["api_train.cpp"]   # no kernels
-HEADERS = ["ptx.cuh", "kernels.h", "api_checks.h", "qk_quant.cuh", "attn_tiles.cuh"]
+HEADERS = ["ptx.cuh", "ptx_train.cuh", "kernels.h", "api_checks.h", "qk_quant.cuh", "attn_tiles.cuh"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
 

@@ -9,7 +9,7 @@
 #include <cstdint>
 
 #include "kernels.h"
-#include "ptx.cuh"
+#include "ptx_train.cuh"
 
 namespace sa {
 namespace tiles {

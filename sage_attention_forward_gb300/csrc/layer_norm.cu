@@ -18,7 +18,7 @@
 #include <cuda_runtime.h>
 
 #include "kernels.h"
-#include "ptx.cuh"
+#include "ptx_train.cuh"
 
 namespace sa {
 namespace {

@@ -1,0 +1,73 @@
+// sm_103a instructions of the training kernels that the forward's (ptx.cuh) do without.
+#pragma once
+
+#include "ptx.cuh"
+
+namespace sa {
+
+// A bit of the device error words beside ptx.cuh's: shared memory does not start on the boundary that a kernel needs.
+constexpr uint32_t kErrSmemBase = 1u << 3;
+
+// ----------------------------------------------------------------- work stealing
+// A running CTA may take the place of one that has not started: try_cancel asks for one, writes the
+// answer (16 bytes) to shared memory and completes on `bar`.  clc_answer tells whether a CTA was
+// taken over, and its index in the grid.  After an answer of false no further request is made.
+__device__ __forceinline__ void clc_try_cancel(uint4* answer, uint64_t* bar) {
+  asm volatile("clusterlaunchcontrol.try_cancel.async.shared::cta.mbarrier::complete_tx::bytes.b128 [%0], [%1];" ::"r"(
+                   smem_u32(answer)),
+               "r"(smem_u32(bar))
+               : "memory");
+}
+__device__ __forceinline__ bool clc_answer(const uint4* answer, uint32_t& x, uint32_t& y, uint32_t& z) {
+  uint32_t ok;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t.reg .b128 r;\n\t"
+      "ld.shared.b128 r, [%4];\n\t"
+      "clusterlaunchcontrol.query_cancel.is_canceled.pred.b128 p, r;\n\t"
+      "selp.u32 %3, 1, 0, p;\n\t"
+      "@p clusterlaunchcontrol.query_cancel.get_first_ctaid.v4.b32.b128 {%0, %1, %2, _}, r;\n\t}"
+      : "+r"(x), "+r"(y), "+r"(z), "=r"(ok)
+      : "r"(smem_u32(answer))
+      : "memory");
+  return ok != 0;
+}
+
+// ----------------------------------------------------------------- copies
+// Contiguous copy of `bytes` (a multiple of 16, both addresses 16-byte aligned) into shared
+// memory, completing on `bar`.
+__device__ __forceinline__ void bulk_load(void* dst, const void* src, uint32_t bytes, uint64_t* bar) {
+  asm volatile(
+      "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(smem_u32(dst)),
+      "l"(reinterpret_cast<uint64_t>(src)), "r"(bytes), "r"(smem_u32(bar))
+      : "memory");
+}
+
+// ----------------------------------------------------------------- TMEM
+// 16 lanes x 32 columns (four groups of 8): thread T gets, of group i, columns 8i + 2 (T % 4) and
+// the next, lane T / 4 in r[4i], r[4i + 1] and lane T / 4 + 8 in r[4i + 2], r[4i + 3].
+__device__ __forceinline__ void tmem_ld_16x32(uint32_t taddr, uint32_t (&r)[16]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.16x256b.x4.b32 "
+      "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
+        "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+      : "r"(taddr));
+}
+// 16 lanes x 16 columns (four groups of 4): thread T gives column 4i + T % 4, lane T / 4 from r[2i]
+// and lane T / 4 + 8 from r[2i + 1] -- tmem_ld_16x32's values, packed two to a column.
+__device__ __forceinline__ void tmem_st_16x16(uint32_t taddr, const uint32_t (&r)[8]) {
+  asm volatile("tcgen05.st.sync.aligned.16x128b.x4.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"r"(taddr),
+               "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
+               : "memory");
+}
+
+// ----------------------------------------------------------------- packed FP32
+__device__ __forceinline__ void fmul2(float& d0, float& d1, float a0, float a1, float b0, float b1) {
+  asm("{\n\t.reg .b64 ra, rb, rd;\n\t"
+      "mov.b64 ra, {%2, %3};\n\tmov.b64 rb, {%4, %5};\n\t"
+      "mul.rn.f32x2 rd, ra, rb;\n\tmov.b64 {%0, %1}, rd;\n\t}"
+      : "=f"(d0), "=f"(d1)
+      : "f"(a0), "f"(a1), "f"(b0), "f"(b1));
+}
+
+}  // namespace sa
