@@ -76,11 +76,11 @@ attn_status get_encoder() {
 }
 
 // BF16 [B, S, H, 128] with element strides (b, s, h): a 4-D map (d, s, h, b),
-// box 64 channels (128 bytes, 128-byte swizzle) x 128 rows.  Rows past S read as zero.
-attn_status tmap_bhsd_bf16(CUtensorMap* m, const void* ptr, int B, int S, int H, const long long str[3]) {
+// box 64 channels (128 bytes, 128-byte swizzle) x `rows` rows.  Rows past S read as zero.
+attn_status tmap_bhsd_bf16(CUtensorMap* m, const void* ptr, int B, int S, int H, const long long str[3], int rows) {
   cuuint64_t dims[4] = {128, (cuuint64_t)S, (cuuint64_t)H, (cuuint64_t)B};
   cuuint64_t strides[3] = {(cuuint64_t)str[1] * 2, (cuuint64_t)str[2] * 2, (cuuint64_t)str[0] * 2};
-  cuuint32_t box[4] = {64, 128, 1, 1};
+  cuuint32_t box[4] = {64, (cuuint32_t)rows, 1, 1};
   cuuint32_t es[4] = {1, 1, 1, 1};
   CUresult r = g_encode(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<void*>(ptr), dims, strides, box, es,
                         CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,

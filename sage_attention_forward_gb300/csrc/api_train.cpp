@@ -66,11 +66,12 @@ attn_status attn_fwd_bf16_lse(const void* q, const void* k, const void* v, void*
   if (o == q || o == k || o == v) return fail(ATTN_ERR_INVALID_ARG, "attn_fwd_bf16_lse: o must overlap no input");
   TRY(check_device());
   TRY(get_encoder());
-  CUtensorMap tq, tk, tv;
+  CUtensorMap tq, tk, tv, to;
   TRY(tmap_bhsd_bf16(&tq, q, B, Sq, Hq, qs));
   TRY(tmap_bhsd_bf16(&tk, k, B, Sk, Hkv, ks));
   TRY(tmap_bhsd_bf16(&tv, v, B, Sk, Hkv, vs));
-  cudaError_t e = sa::launch_attn_fwd_bf16_lse(tq, tk, tv, a, o, os, lse, (cudaStream_t)stream);
+  TRY(tmap_bhsd_bf16(&to, o, B, Sq, Hq, os, 32));
+  cudaError_t e = sa::launch_attn_fwd_bf16_lse(tq, tk, tv, to, a, lse, (cudaStream_t)stream);
   if (e != cudaSuccess) return fail_cuda(e, "attn_fwd_bf16_lse launch");
   return ATTN_OK;
 }

@@ -199,9 +199,9 @@ struct TrainArgs {
   const int* kv_len;      // device [B], or nullptr: Sk keys
 };
 // Q [B, Sq, Hq, 128], K and V [B, Sk, Hkv, 128] through BF16 tensor maps; lse [B, Hq, Sq].
+// tm_o: boxes of 32 rows.
 cudaError_t launch_attn_fwd_bf16_lse(const CUtensorMap& tm_q, const CUtensorMap& tm_k, const CUtensorMap& tm_v,
-                                     const TrainArgs& a, void* o, const long long o_str[3], float* lse,
-                                     cudaStream_t stream);
+                                     const CUtensorMap& tm_o, const TrainArgs& a, float* lse, cudaStream_t stream);
 
 struct BwdTensors {
   const float* lse;
