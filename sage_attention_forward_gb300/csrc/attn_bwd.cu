@@ -840,30 +840,35 @@ __global__ void __launch_bounds__(kThreads, 1)
       lse = row < p.mask.Sq ? __ldg(p.lse + ((long long)item.b * p.H + item.h) * p.mask.Sq + row) : -INFINITY;
       return true;
     };
-    // -delta of the row, from O's tile and dO's
-    auto find_delta = [&](int n, float& neg_delta) -> bool {
+    // -delta of the row from the warpgroups' parts.  (They are next written in the next item, whose S and O
+    // no warp sees before all have begun it.)
+    auto sum_parts = [&](int n, float part, float& neg_delta) -> bool {
+      sm.delta[g][r] = part;
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&sm.delta_full);
+      if (!mbar_wait_warp<false>(&sm.delta_full, n & 1, abort_flag, err, kErrTimeoutSync)) return false;
+      neg_delta = -((sm.delta[0][r] + sm.delta[1][r]) + (sm.delta[2][r] + sm.delta[3][r]));
+      return true;
+    };
+    // the warpgroup's part of delta, from O's tile and dO's
+    auto find_part = [&](int n, float& part) -> bool {
       if (!mbar_wait_warp<false>(&sm.d_full, n & 1, abort_flag, err, kErrTimeoutTma) ||
           !mbar_wait_warp<false>(&sm.o_full, n & 1, abort_flag, err, kErrTimeoutTma))
         return false;
       uint32_t x[16], y[16];
       tile_row(sm.dout, x);
       tile_row(sm.q, y);
-      float a = 0.0f;
+      part = 0.0f;
 #pragma unroll
       for (int c = 0; c < 16; ++c) {
-        a = fmaf(u2f(y[c] << 16), u2f(x[c] << 16), a);
-        a = fmaf(u2f(y[c] & 0xffff0000u), u2f(x[c] & 0xffff0000u), a);
+        part = fmaf(u2f(y[c] << 16), u2f(x[c] << 16), part);
+        part = fmaf(u2f(y[c] & 0xffff0000u), u2f(x[c] & 0xffff0000u), part);
       }
-      sm.delta[g][r] = a;
       __syncwarp();
       if (lane == 0) {
         mbar_arrive(&sm.d_empty);
         mbar_arrive(&sm.o_empty);
-        mbar_arrive(&sm.delta_full);
       }
-      // (the parts are next written in the next item, which no warp comes to before all have dS of this one)
-      if (!mbar_wait_warp<false>(&sm.delta_full, n & 1, abort_flag, err, kErrTimeoutSync)) return false;
-      neg_delta = -((sm.delta[0][r] + sm.delta[1][r]) + (sm.delta[2][r] + sm.delta[3][r]));
       return true;
     };
     static_assert(kGroups == 4, "four parts of delta");
@@ -875,31 +880,41 @@ __global__ void __launch_bounds__(kThreads, 1)
     while (more) {
       int n, valid;   // products left, and what is left of the keys that this row sees, from the group's first
       float nl = -INFINITY, nd = 0.0f;
+      float* delta_at;
+      // With all keys in one tile delta is formed as sum p dp: O's rounding, and that of the P that it was formed
+      // with, weigh most where the sums are short (dQ and dK of 2 to 5 keys were off by up to 0.0045 of their
+      // norm, and are by 0.0025, of which the rounding of the results is 0.0017).
+      bool one_tile;
       {
         const ItemQ item = item_q(p, work_read(sm.work, turn));
         const int row = item.row0 + r;
         n = item.n;
+        one_tile = n == 1;
         // a row that sees one key has ds = 0: as a row that sees none
         valid = row_limit(p.mask, item.keys, row);
         if (valid == 1) valid = 0;
         valid -= kCols * g;
+        const long long at = ((long long)item.b * p.H + item.h) * p.Sq_pad + row;
+        delta_at = p.neg_delta + at;
         if (n > 0) {
-          const long long head = (long long)item.b * p.H + item.h;
-          ok = find_delta(items, nd);
+          float part;
+          ok = find_part(items, part) && (one_tile || sum_parts(items, part, nd));
           if (lse == -INFINITY) nd = 0.0f;
           else nl = -lse * kLog2e;
           if (g == 0) {
-            p.neg_lse2[head * p.Sq_pad + row] = nl;
-            p.neg_delta[head * p.Sq_pad + row] = nd;
+            p.neg_lse2[at] = nl;
+            if (!one_tile) *delta_at = nd;
           }
         }
       }
       if (!ok) break;
-      for (; n > 0; --n, ++it, valid -= kTile) {
+      // (a copy of each without the other's code: with it the loop took 1.5 % longer)
+      auto product = [&](auto one_c) -> bool {
+        constexpr bool kOneTile = decltype(one_c)::value;
         const bool partial = __any_sync(0xffffffffu, valid < kCols);
         float pr[kCols];
         ok = mbar_wait_warp<false>(&sm.s_full, it & 1, abort_flag, err, kErrTimeoutMma);
-        if (!ok) break;
+        if (!ok) return false;
         tc_fence_after();
         {
           uint32_t a[kCols];
@@ -918,13 +933,21 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
         }
         ok = mbar_wait_warp<false>(&sm.dp_full, it & 1, abort_flag, err, kErrTimeoutMma);
-        if (!ok) break;
+        if (!ok) return false;
         tc_fence_after();
         {
           uint32_t a[kCols], pk[kCols / 2];
           tmem_ld32(tDP + lane_off + kCols * g, a);
           tmem_ld_wait();
           tmem_reg_fence(a);
+          if (kOneTile) {
+            float part = 0.0f;
+#pragma unroll
+            for (int c = 0; c < kCols; ++c) part += c < valid ? pr[c] * u2f(a[c]) : 0.0f;
+            ok = sum_parts(items, part, nd);
+            if (!ok) return false;
+            if (g == 0) *delta_at = nd;
+          }
 #pragma unroll
           for (int e = 0; e < kCols / 2; ++e) {
             float x0, x1;
@@ -938,7 +961,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
           for (int e = 0; e < kCols / 2; ++e) pk[e] = pack_bf16x2(pr[2 * e], pr[2 * e + 1]);
           ok = it == 0 || mbar_wait_warp<false>(&sm.ds_free, (it - 1) & 1, abort_flag, err, kErrTimeoutMma);
-          if (!ok) break;
+          if (!ok) return false;
           tc_fence_after();
           tmem_st16(tDS + lane_off + 16 * g, pk);
           tmem_st_wait();
@@ -946,6 +969,13 @@ __global__ void __launch_bounds__(kThreads, 1)
           __syncwarp();
           if (lane == 0) mbar_arrive(&sm.ds_full);
         }
+        return true;
+      };
+      if (one_tile) {
+        ok = product(std::true_type());
+        ++it;
+      } else {
+        for (; ok && n > 0; --n, ++it, valid -= kTile) ok = product(std::false_type());
       }
       if (!ok) break;
       // the next item's Q, so that its first S runs while this one's rows are stored
