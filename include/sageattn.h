@@ -29,6 +29,12 @@
  *                   gfx1201_sage_attention op), the prepared tensors kept in
  *                   the caller's workspace.
  *
+ * For training: attn_fwd_bf16_lse (the BF16 forward that also leaves each row's
+ * log-sum-exp; cross-attention lengths, shared key heads, causal masks and key
+ * counts per batch entry), attn_bwd_bf16 (dQ, dK, dV of it, the probabilities
+ * formed again), layer_norm_fwd and layer_norm_bwd (over head channels or tokens,
+ * with the gradients of weight and bias).
+ *
  * Beyond those: sage_prepare_smooth_k (K smoothing before the INT8
  * quantisation), sage_prepare_smoothed with sage_attn_fwd_smooth_q and
  * sage_attn_fwd_pv16_smooth_q (Q smoothing with its correction term) and
@@ -434,19 +440,19 @@ ATTN_API size_t attn_bwd_bf16_workspace_size(int B, int Sq, int Sk, int Hq, int 
 
 /*
  * attn_bwd_bf16 -- the gradients of attn_fwd_bf16_lse's O with respect to Q, K and V.
- *   p[i, j]  = exp(s[i, j] - lse[i])          delta[i] = dout_i . o_i
+ *   p[i, j]  = exp(s[i, j] - lse[i])          delta[i] = dout_i . o_i  (or sum_j p dout_i . v_j)
  *   dv_j     = sum_i p[i, j] dout_i           ds[i, j] = p[i, j] (dout_i . v_j - delta[i])
  *   dk_j     = softmax_scale sum_i ds[i, j] q_i
  *   dq_i     = softmax_scale sum_j ds[i, j] k_j
  * sums over i also over the query heads that share a key head.  Rows without a key have dq = 0; keys that no
  * query sees have dk = dv = 0; a row with one key has ds = 0.
- *   dout    : BF16 [B, Sq, Hq, 128], finite, strides dout_str
+ *   dout    : BF16 [B, Sq, Hq, 128], finite, strides dout_str (positive, as all of these tensors')
  *   q, k, v, softmax_scale, causal, kv_len : as given to the forward
  *   o, lse  : as the forward wrote them
  *   dq      : BF16 [B, Sq, Hq, 128] output; dk, dv : BF16 [B, Sk, Hkv, 128] outputs, every row
  *             written; they overlap neither the inputs nor one another
  *   workspace : at least attn_bwd_bf16_workspace_size(B, Sq, Sk, Hq, Hkv) bytes, 16-byte
- *             aligned; overwritten, contents on entry do not matter
+ *             aligned; overwritten, contents on entry do not matter; one for each call under way
  * p and ds are rounded to BF16 before the products that sum over them, sums are FP32 in a fixed
  * order (no atomics: the same inputs give the same bits), each output is rounded once.
  * Enqueues its kernels on `stream`; errors as attn_fwd_bf16_lse.
