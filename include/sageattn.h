@@ -453,7 +453,8 @@ ATTN_API size_t attn_bwd_bf16_workspace_size(int B, int Sq, int Sk, int Hq, int 
  *             written; they overlap neither the inputs nor one another
  *   workspace : at least attn_bwd_bf16_workspace_size(B, Sq, Sk, Hq, Hkv) bytes, 16-byte
  *             aligned; overwritten, contents on entry do not matter; one for each call under way
- * p and ds are rounded to BF16 before the products that sum over them, sums are FP32 in a fixed
+ * p and ds are rounded to BF16 before the products that sum over them (for dq so that a row of ds keeps
+ * the sum 0, and the keys' mean stays out of it), sums are FP32 in a fixed
  * order (no atomics: the same inputs give the same bits), each output is rounded once.
  * Enqueues its kernels on `stream`; errors as attn_fwd_bf16_lse.
  */

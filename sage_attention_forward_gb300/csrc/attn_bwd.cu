@@ -15,7 +15,8 @@
 //   dq_kernel     one item per (128 queries, query head): Q and dO stay, K and V stream by:
 //                 S = Q K^T, dP = dO V^T, dQ += dS K.  It forms delta of its rows from dO, which it has,
 //                 and O, and leaves -lse * log2 e and -delta in the workspace, padded to whole tiles
-//                 (-inf and 0 there and for empty rows: their probabilities come out as 0).
+//                 (-inf and 0 there and for empty rows: their probabilities come out as 0).  Its key tiles come
+//                 last first.
 //   dkdv_kernel   one item per (128 keys, key head): K and V stay in shared memory, Q and dO tiles
 //                 stream by with those statistics.  The transposed scores S^T = K Q^T and
 //                 dP^T = V dO^T leave P^T and dS^T in TMEM as the A operands of dV += P^T dO and
@@ -55,6 +56,7 @@ constexpr int kThreads = 32 * (kWarpClear + 1);
 // first SMs with a second long one: 409 us of a backward in place of 332).
 constexpr int kAskAhead = 5;
 constexpr float kLog2e = 1.4426950408889634f;
+constexpr float kLeastSum = 1e-6f;   // (dq_kernel) of a row's probabilities in a tile, to be divided by
 
 __device__ uint32_t g_err_bwd;
 
@@ -576,7 +578,7 @@ struct __align__(1024) SmemQ {
   uint64_t dp_full;
   uint64_t ds_full, ds_free;   // dS stored in TMEM by every softmax warp; read by dQ's product
   float delta[kGroups][kTile];   // each warpgroup's part of the rows' sums
-  uint64_t delta_full;
+  uint64_t delta_full, rest_full;
   uint64_t acc_done;
   uint64_t drain;
   uint32_t tmem_base;
@@ -636,6 +638,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     mbar_init(&sm.ds_full, kWarpLoad);
     mbar_init(&sm.ds_free, 1);
     mbar_init(&sm.delta_full, kWarpLoad);
+    mbar_init(&sm.rest_full, kWarpLoad);
     mbar_init(&sm.acc_done, 1);
     mbar_init(&sm.drain, 2);
     sm.abort_flag = 0;
@@ -683,7 +686,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           const int slot = it % kKRing, use = it / kKRing;
           if (use > 0 && !wait_sleep(&sm.k_empty[slot], (use - 1) & 1, abort_flag, err, kErrTimeoutSync)) return false;
           mbar_arrive_expect_tx(&sm.k_full[slot], kTileBytes);
-          load_tile(sm.k[slot], &tm_k, &sm.k_full[slot], j * kTile, hk, i.b);
+          load_tile(sm.k[slot], &tm_k, &sm.k_full[slot], (i.n - 1 - j) * kTile, hk, i.b);
           ++k_issued;
         }
         if (j == 0) {
@@ -696,7 +699,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           const int slot = it % kVRing, use = it / kVRing;
           if (use > 0 && !wait_sleep(&sm.v_empty[slot], (use - 1) & 1, abort_flag, err, kErrTimeoutSync)) return false;
           mbar_arrive_expect_tx(&sm.v_full[slot], kTileBytes);
-          load_tile(sm.v[slot], &tm_v, &sm.v_full[slot], j * kTile, hk, i.b);
+          load_tile(sm.v[slot], &tm_v, &sm.v_full[slot], (i.n - 1 - j) * kTile, hk, i.b);
           ++v_issued;
         }
         ++it;
@@ -774,14 +777,11 @@ __global__ void __launch_bounds__(kThreads, 1)
       for (int i = 0; ok && f0 != kEnd; ++i) {
         const int slot = i % kKRing;
         const bool last = f0 & kLast, first = f0 & kFirst;
-        if (last) {
-          if (last_rows(p.mask, walk.item.keys, walk.item.n) < kTile) {
-            ok = wait_warp(&sm.k_clear[slot], (cleared >> slot) & 1, abort_flag, err, kErrTimeoutSync);
-            cleared ^= 1u << slot;
-          }
-        } else {
-          f0 = walk.next(sm.work, lane, abort_flag, err);
+        if (first && last_rows(p.mask, walk.item.keys, walk.item.n) < kTile) {
+          ok = wait_warp(&sm.k_clear[slot], (cleared >> slot) & 1, abort_flag, err, kErrTimeoutSync);
+          cleared ^= 1u << slot;
         }
+        if (!last) f0 = walk.next(sm.work, lane, abort_flag, err);
         ok = ok && wait_warp(&sm.ds_full, i & 1, abort_flag, err, kErrTimeoutSync) && (last || issue_dp(i + 1, f0));
         if (!ok) break;
         tc_fence_after();
@@ -799,7 +799,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     mbar_wait_teardown(&sm.drain, 0);
   } else if (warp == kWarpClear) {
     if (p.mask.kv_len != nullptr)
-      clear_warp<kKRing>(p.mask, [&](const Work& w) { return item_q(p, w); }, sm.work, sm.k, sm.k_full, sm.k_clear, lane,
+      clear_warp<kKRing, true>(p.mask, [&](const Work& w) { return item_q(p, w); }, sm.work, sm.k, sm.k_full, sm.k_clear, lane,
                          abort_flag, err);
   } else if (warp < kWarpLoad) {
     // warpgroup g takes the keys [32 g, 32 g + 32) of each tile, a thread one query
@@ -842,12 +842,37 @@ __global__ void __launch_bounds__(kThreads, 1)
     };
     // -delta of the row from the warpgroups' parts.  (They are next written in the next item, whose S and O
     // no warp sees before all have begun it.)
-    auto sum_parts = [&](int n, float part, float& neg_delta) -> bool {
+    int sums = 0;   // so far (items of one tile have none)
+    auto sum_parts = [&](float part, float& neg_delta) -> bool {
       sm.delta[g][r] = part;
       __syncwarp();
       if (lane == 0) mbar_arrive(&sm.delta_full);
-      if (!mbar_wait_warp<false>(&sm.delta_full, n & 1, abort_flag, err, kErrTimeoutSync)) return false;
+      if (!mbar_wait_warp<false>(&sm.delta_full, sums++ & 1, abort_flag, err, kErrTimeoutSync)) return false;
       neg_delta = -((sm.delta[0][r] + sm.delta[1][r]) + (sm.delta[2][r] + sm.delta[3][r]));
+      return true;
+    };
+    // The sums of the warpgroups' x and y, in columns of S that each has read (the next S is not
+    // issued before all softmax warps have begun the next item).
+    auto sum_rest = [&](int n, float& x, float& y) -> bool {
+      tmem_st2(tS + lane_off + kCols * g, __float_as_uint(x), __float_as_uint(y));
+      tmem_st_wait();
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&sm.rest_full);
+      if (!mbar_wait_warp<false>(&sm.rest_full, n & 1, abort_flag, err, kErrTimeoutSync)) return false;
+      tc_fence_after();
+      uint32_t v[kGroups][2];
+#pragma unroll
+      for (int i = 0; i < kGroups; ++i) tmem_ld2(tS + lane_off + kCols * i, v[i]);
+      tmem_ld_wait();
+      x = y = 0.0f;
+#pragma unroll
+      for (int i = 0; i < kGroups; ++i) {
+        asm volatile("" : "+r"(v[i][0]), "+r"(v[i][1]));   // (not read before the wait)
+        x += u2f(v[i][0]);
+        y += u2f(v[i][1]);
+      }
+      tc_fence_before();
       return true;
     };
     // the warpgroup's part of delta, from O's tile and dO's
@@ -878,12 +903,9 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     bool more = ok;
     while (more) {
-      int n, valid;   // products left, and what is left of the keys that this row sees, from the group's first
+      int n, valid;   // products left, and the keys that this row sees from the group's first of the tile on
       float nl = -INFINITY, nd = 0.0f;
       float* delta_at;
-      // With all keys in one tile delta is formed as sum p dp: O's rounding, and that of the P that it was formed
-      // with, weigh most where the sums are short (dQ and dK of 2 to 5 keys were off by up to 0.0045 of their
-      // norm, and are by 0.0025, of which the rounding of the results is 0.0017).
       bool one_tile;
       {
         const ItemQ item = item_q(p, work_read(sm.work, turn));
@@ -893,12 +915,12 @@ __global__ void __launch_bounds__(kThreads, 1)
         // a row that sees one key has ds = 0: as a row that sees none
         valid = row_limit(p.mask, item.keys, row);
         if (valid == 1) valid = 0;
-        valid -= kCols * g;
+        valid -= kCols * g + (n - 1) * kTile;   // (an item's key tiles come last first)
         const long long at = ((long long)item.b * p.H + item.h) * p.Sq_pad + row;
         delta_at = p.neg_delta + at;
         if (n > 0) {
           float part;
-          ok = find_part(items, part) && (one_tile || sum_parts(items, part, nd));
+          ok = find_part(items, part) && (one_tile || sum_parts(part, nd));
           if (lse == -INFINITY) nd = 0.0f;
           else nl = -lse * kLog2e;
           if (g == 0) {
@@ -908,9 +930,17 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
       }
       if (!ok) break;
+      // A row of dS has the sum 0.  The rounding of its elements, of O in delta and of the P that O was formed with
+      // leave it some other sum, by which a mean of the keys that is not 0 comes into dQ.  So the
+      // item's last tile, the first 128 keys, all of which a row sees that sees any other tile, takes the delta that
+      // makes the sum 0 with what has been rounded so far: delta + rest / sum p.  dQ's error, of its norm, at 1200
+      // keys with a mean of 0, 0.5, 1 and 4 times their spread: 0.0024, 0.0028, 0.0037 and 0.0123 without this
+      // and 0.0024, 0.0024, 0.0025 and 0.0033 with it (0.0017 is the rounding of dQ); with one tile, where delta itself
+      // is formed so, and 2 keys 0.0045 and 0.0024.  It takes 2 to 4 % of the backward's time.
+      float rest = 0.0f;
       // (a copy of each without the other's code: with it the loop took 1.5 % longer)
-      auto product = [&](auto one_c) -> bool {
-        constexpr bool kOneTile = decltype(one_c)::value;
+      auto product = [&](auto last_c) -> bool {
+        constexpr bool kLast = decltype(last_c)::value;
         const bool partial = __any_sync(0xffffffffu, valid < kCols);
         float pr[kCols];
         ok = mbar_wait_warp<false>(&sm.s_full, it & 1, abort_flag, err, kErrTimeoutMma);
@@ -932,6 +962,17 @@ __global__ void __launch_bounds__(kThreads, 1)
             pr[2 * e + 1] = ex2_approx(x1);
           }
         }
+        float sum = 0.0f;
+        if (kLast) {
+          float s0 = 0.0f, s1 = 0.0f;
+          if (partial) {
+#pragma unroll
+            for (int c = 0; c < kCols; ++c) pr[c] = c < valid ? pr[c] : 0.0f;
+          }
+#pragma unroll
+          for (int e = 0; e < kCols / 2; ++e) fadd2(s0, s1, s0, s1, pr[2 * e], pr[2 * e + 1]);
+          sum = s0 + s1;
+        }
         ok = mbar_wait_warp<false>(&sm.dp_full, it & 1, abort_flag, err, kErrTimeoutMma);
         if (!ok) return false;
         tc_fence_after();
@@ -940,13 +981,23 @@ __global__ void __launch_bounds__(kThreads, 1)
           tmem_ld32(tDP + lane_off + kCols * g, a);
           tmem_ld_wait();
           tmem_reg_fence(a);
-          if (kOneTile) {
-            float part = 0.0f;
+          if (kLast) {
+            if (partial) {   // (dP of a key that is none may be anything)
 #pragma unroll
-            for (int c = 0; c < kCols; ++c) part += c < valid ? pr[c] * u2f(a[c]) : 0.0f;
-            ok = sum_parts(items, part, nd);
+              for (int c = 0; c < kCols; ++c) a[c] = c < valid ? a[c] : 0u;
+            }
+            float r0 = 0.0f, r1 = 0.0f;
+#pragma unroll
+            for (int e = 0; e < kCols / 2; ++e) {
+              float x0, x1;
+              fadd2(x0, x1, u2f(a[2 * e]), u2f(a[2 * e + 1]), nd, nd);
+              ffma2(r0, r1, pr[2 * e], pr[2 * e + 1], x0, x1, r0, r1);
+            }
+            rest += r0 + r1;
+            ok = sum_rest(items, rest, sum);
             if (!ok) return false;
-            if (g == 0) *delta_at = nd;
+            if (sum > kLeastSum) nd -= rest / sum;
+            if (one_tile && g == 0) *delta_at = nd;
           }
 #pragma unroll
           for (int e = 0; e < kCols / 2; ++e) {
@@ -954,7 +1005,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             fadd2(x0, x1, u2f(a[2 * e]), u2f(a[2 * e + 1]), nd, nd);
             fmul2(pr[2 * e], pr[2 * e + 1], pr[2 * e], pr[2 * e + 1], x0, x1);
           }
-          if (partial) {
+          if (!kLast && partial) {
 #pragma unroll
             for (int c = 0; c < kCols; ++c) pr[c] = c < valid ? pr[c] : 0.0f;
           }
@@ -968,14 +1019,19 @@ __global__ void __launch_bounds__(kThreads, 1)
           tc_fence_before();
           __syncwarp();
           if (lane == 0) mbar_arrive(&sm.ds_full);
+          if (!kLast) {
+            float r0 = 0.0f, r1 = 0.0f;
+#pragma unroll
+            for (int e = 0; e < kCols / 2; ++e) fadd2(r0, r1, r0, r1, u2f(pk[e] << 16), u2f(pk[e] & 0xffff0000u));
+            rest += r0 + r1;
+          }
         }
         return true;
       };
-      if (one_tile) {
+      for (; ok && n > 1; --n, ++it, valid += kTile) ok = product(std::false_type());
+      if (ok && n > 0) {
         ok = product(std::true_type());
         ++it;
-      } else {
-        for (; ok && n > 0; --n, ++it, valid -= kTile) ok = product(std::false_type());
       }
       if (!ok) break;
       // the next item's Q, so that its first S runs while this one's rows are stored

@@ -265,7 +265,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     mbar_wait_teardown(&sm.drain, 0);
   } else if (warp == kWarpClear) {
     if (p.mask.kv_len != nullptr)
-      clear_warp<kStages>(p.mask, [&](const Work& w) { return item_of(p, w); }, sm.work, sm.v, sm.v_full, sm.v_clear,
+      clear_warp<kStages, false>(p.mask, [&](const Work& w) { return item_of(p, w); }, sm.work, sm.v, sm.v_full, sm.v_clear,
                           lane, abort_flag, err);
   } else if (warp < kWarpLoad) {
     const int i = warp >> 2, wq = warp & 3;

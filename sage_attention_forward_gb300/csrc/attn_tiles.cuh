@@ -185,7 +185,8 @@ __device__ __forceinline__ void clear_rows(uint8_t* tile, int first, int lane) {
   fence_proxy_async_smem();
   __syncwarp();
 }
-template <int kRing, class Make>
+// kFirst: an item's first tile is the one where its keys end, and not its last.
+template <int kRing, bool kFirst, class Make>
 __device__ __forceinline__ void clear_warp(const Mask& m, Make make, WorkRing& work, uint8_t (*tiles)[kTileBytes],
                                            uint64_t* full, uint64_t* cleared, int lane, volatile uint32_t* abort_flag,
                                            uint32_t* err) {
@@ -193,10 +194,10 @@ __device__ __forceinline__ void clear_warp(const Mask& m, Make make, WorkRing& w
   do {
     const auto item = make(work_read(work, turn));
     work_release(work, turn, lane);
-    for (int end = it + item.n; it != end; ++it) {
+    for (int begin = it, end = it + item.n; it != end; ++it) {
       const int slot = it % kRing;
       if (!mbar_wait_warp<true>(&full[slot], (it / kRing) & 1, abort_flag, err, kErrTimeoutTma)) return;
-      const int rows = it + 1 == end ? last_rows(m, item.keys, item.n) : kTile;
+      const int rows = (kFirst ? it == begin : it + 1 == end) ? last_rows(m, item.keys, item.n) : kTile;
       if (rows < kTile) {
         clear_rows(tiles[slot], rows, lane);
         if (lane == 0) mbar_arrive(&cleared[slot]);

@@ -14,7 +14,9 @@ Bounds, from the kernels' arithmetic (u = 2^-8, half a BF16 step; everything els
   delta     sum_d |dO_d| times O's own bound, and 2^-16 sum_d |dO_d O_d|.
   dp        2^-16 sum_d |dO_d v_d|.
   ds        p (e_delta + e_dp) + |ds| (u + e_p).
-  dQ, dK    scale times the sums of ds's bound times |K|, |Q|, and u of the result.
+  dQ, dK    scale times the sums of ds's bound times |K|, |Q|, and u of the result.  In dQ a row that sees more
+            than 128 keys has the sum of its ds's errors, whose bound is the sum of theirs, taken off
+            again in the first 128, in proportion to p: that bound times the mean of |K| there.
 The FP32 sums over rows or keys add at most 2^-23 per addition of the sum of magnitudes, which
 2^-12 of it covers up to 2000 terms; that is added to u everywhere as `acc`.
 """
@@ -100,6 +102,11 @@ class Reference:
         lone = (self.lim == 1)[:, None, :, None]   # ds is exactly 0 there
         e_ds = torch.where(lone, torch.zeros_like(e_ds), e_ds)
         self.dq_tol = (self.scale * e_ds @ self.k.abs()).permute(0, 2, 1, 3) + U * self.dq.abs() + 1e-37
+        if self.p.shape[-1] > 128:
+            p0 = self.p[..., :128]
+            mean = (p0 @ self.k[..., :128, :].abs()) / p0.sum(-1, keepdim=True).clamp_min(1e-6)
+            spread = self.scale * e_ds.sum(-1, keepdim=True) * mean
+            self.dq_tol += torch.where(self.lim[:, None, :, None] > 128, spread, 0 * spread).permute(0, 2, 1, 3)
         self.dk_tol = self.shared(self.scale * e_ds.transpose(-1, -2) @ self.q.abs()) + U * self.dk.abs() + 1e-37
         self.dv_tol = self.shared((self.p * rel).transpose(-1, -2) @ d.abs()) + U * self.dv.abs() + 1e-37
         return self.dq, self.dk, self.dv
