@@ -923,10 +923,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           ok = find_part(items, part) && (one_tile || sum_parts(part, nd));
           if (lse == -INFINITY) nd = 0.0f;
           else nl = -lse * kLog2e;
-          if (g == 0) {
-            p.neg_lse2[at] = nl;
-            if (!one_tile) *delta_at = nd;
-          }
+          if (g == 0) p.neg_lse2[at] = nl;
         }
       }
       if (!ok) break;
@@ -996,8 +993,9 @@ __global__ void __launch_bounds__(kThreads, 1)
             rest += r0 + r1;
             ok = sum_rest(items, rest, sum);
             if (!ok) return false;
+            // (with all of the row's p, whose sum is 1, this is delta as sum p dp, for dkdv_kernel)
+            if (g == 0) *delta_at = nd - rest;
             if (sum > kLeastSum) nd -= rest / sum;
-            if (one_tile && g == 0) *delta_at = nd;
           }
 #pragma unroll
           for (int e = 0; e < kCols / 2; ++e) {

@@ -19,7 +19,7 @@ def make(dev, B, Sq, Sk, Hq, Hkv, seed=0, gain=1.0):
     return tuple(t.to(torch.bfloat16) for t in (q, k, v, d))
 
 
-def check(q, k, v, d, scale=None, causal=False, kv_len=None, grads=True, ref_args=None):
+def check(q, k, v, d, scale=None, causal=False, kv_len=None, grads=True, ref_args=None, cosine=True):
     o, lse = sa.attn_fwd_bf16_lse(q, k, v, softmax_scale=scale, causal=causal, kv_len=kv_len)
     got = sa.attn_bwd_bf16(d, q, k, v, o, lse, softmax_scale=scale, causal=causal, kv_len=kv_len) if grads else ()
     torch.cuda.synchronize()
@@ -35,7 +35,7 @@ def check(q, k, v, d, scale=None, causal=False, kv_len=None, grads=True, ref_arg
             far[name] = worst(t, getattr(ref, name), getattr(ref, name + "_tol"))
             want = getattr(ref, name)
             cos = float((t.double() * want).sum() / (t.double().norm() * want.norm() + 1e-300))
-            assert float(want.norm()) < 1e-12 or cos > 0.9999, (name, cos)
+            assert not cosine or float(want.norm()) < 1e-12 or cos > 0.9999, (name, cos)
     print(far)
     assert max(far.values()) <= 1.0, far
     return o, lse, got
@@ -271,3 +271,86 @@ def test_keys_with_a_mean(cuda_dev, offset):
     err = float((got[0].double() - ref.dq).norm() / ref.dq.norm())
     print(err)
     assert err <= 1.1 * 2.0 ** -8 * math.sqrt((2 + offset ** 2 * 128 / 1200) / 3)
+
+
+def test_key_counts_out_of_range_are_clamped(cuda_dev):
+    q, k, v, d = make(cuda_dev, 3, 150, 140, 4, 2, seed=9)
+    wild = torch.tensor([-7, 10 ** 9, 133], dtype=torch.int32, device=cuda_dev)
+    tame = torch.tensor([0, 140, 133], dtype=torch.int32, device=cuda_dev)
+    for causal in (False, True):
+        a = check(q, k, v, d, causal=causal, kv_len=tame)
+        o, lse = sa.attn_fwd_bf16_lse(q, k, v, causal=causal, kv_len=wild)
+        b = sa.attn_bwd_bf16(d, q, k, v, o, lse, causal=causal, kv_len=wild)
+        assert torch.equal(o, a[0]) and torch.equal(lse, a[1])
+        for x, y in zip(a[2], b):
+            assert torch.equal(x, y)
+
+
+def test_more_heads_than_a_grid_dimension(cuda_dev):
+    """70000 (batch entry, head) pairs of a few rows each, against four of them at a time."""
+    B, H = 700, 100
+    q, k, v, d = make(cuda_dev, B, 5, 3, H, H, seed=10)
+    o, lse = sa.attn_fwd_bf16_lse(q, k, v, causal=True)
+    got = (o, lse.transpose(1, 2), *sa.attn_bwd_bf16(d, q, k, v, o, lse, causal=True))
+    for b in (0, 1, 327, 654, 655, 656, B - 1):
+        part = [t[b:b + 1, :, 60:64] for t in (q, k, v, d)]
+        po, plse = sa.attn_fwd_bf16_lse(*part[:3], causal=True)
+        want = (po, plse.transpose(1, 2), *sa.attn_bwd_bf16(part[3], *part[:3], po, plse, causal=True))
+        for x, y in zip(got, want):
+            assert torch.equal(x[b:b + 1, :, 60:64], y)
+    sa.attn_get_device_status()
+
+
+def test_strides_past_32_bits(cuda_dev):
+    """Batch entries 2^31 and more elements apart, of the inputs and of every output."""
+    B, Sq, Sk, H, far = 2, 200, 300, 2, (1 << 31) + 1024
+    store = torch.empty(far + (1 << 20), dtype=torch.bfloat16, device=cuda_dev)
+    used = 0
+
+    def spread(t):
+        nonlocal used
+        S, heads = t.shape[1], t.shape[2]
+        out = store.as_strided((B, S, heads, 128), (far, heads * 128, 128, 1), used)
+        used += S * heads * 128
+        out.copy_(t)
+        return out
+
+    tensors = make(cuda_dev, B, Sq, Sk, H, H, seed=11)
+    q, k, v, d = (spread(t) for t in tensors)
+    o = spread(torch.zeros_like(tensors[0]))
+    grads = [spread(torch.zeros_like(t)) for t in tensors[:3]]
+    _, lse = sa.attn_fwd_bf16_lse(q, k, v, causal=True, out=o)
+    sa.attn_bwd_bf16(d, q, k, v, o, lse, causal=True, dq=grads[0], dk=grads[1], dv=grads[2])
+    wo, wlse, want = check(*tensors, causal=True)
+    assert used <= 1 << 20 and torch.equal(o, wo) and torch.equal(lse, wlse)
+    for x, y in zip(grads, want):
+        assert torch.equal(x, y)
+
+
+def test_one_tensor_as_queries_keys_and_values(cuda_dev):
+    """Within the bounds.  A row's own key has nearly all of its probability here (scores of 11 against 1), so that
+    dp - delta is of the size of the rounding of O in delta, and dQ of that of its error: the bounds count
+    that (e_delta times |k|), a cosine of 0.9999 does not follow from them."""
+    x, _, _, d = make(cuda_dev, 1, 260, 260, 3, 3, seed=12)
+    check(x, x, x, d, causal=True, cosine=False)
+
+
+def test_two_streams_at_once(cuda_dev):
+    """Calls under way on two streams, each with its own outputs and workspace, give what they give alone."""
+    cases = [make(cuda_dev, 1, 1500, 1500, 4, 2, seed=20 + i) for i in range(2)]
+    alone = []
+    for q, k, v, d in cases:
+        o, lse = sa.attn_fwd_bf16_lse(q, k, v, causal=True)
+        alone.append((o, lse, *sa.attn_bwd_bf16(d, q, k, v, o, lse, causal=True)))
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in cases]
+    for _ in range(5):
+        got = []
+        for (q, k, v, d), s in zip(cases, streams):
+            o, lse = sa.attn_fwd_bf16_lse(q, k, v, causal=True, stream=s)
+            got.append((o, lse, *sa.attn_bwd_bf16(d, q, k, v, o, lse, causal=True, stream=s)))
+        torch.cuda.synchronize()
+        for a, b in zip(alone, got):
+            for x, y in zip(a, b):
+                assert torch.equal(x, y)
+    sa.attn_get_device_status()

@@ -225,3 +225,44 @@ def test_gradient_matches_differences(cuda_dev):
         up[at], down[at] = args[at] + 1e-5 * d, args[at] - 1e-5 * d
         # h^2 of a third derivative of order 1e3; FP32 gradients: 48 terms' 2^-24 each over 960 values of order 1
         assert abs((f(*up) - f(*down)) / 2e-5 - float((grad.double() * d).sum())) < 1e-3
+
+
+@pytest.mark.parametrize("N", [128, 130, 1000, 9000])
+def test_strides_past_32_bits(cuda_dev, N):
+    """Rows 2^31 and more elements apart in the inputs and outputs."""
+    far = (1 << 31) + 64
+    store = torch.empty(far + (1 << 18), dtype=torch.bfloat16, device=cuda_dev)
+    x, dy, w, b = make(cuda_dev, (2, 3, N), torch.bfloat16, torch.float32, 77)
+    pitch = (N + 15) // 16 * 16   # (whole 16-byte pieces where N allows them)
+    at = [0]
+
+    def spread(t):
+        out = store.as_strided(t.shape, (far, pitch, 1), at[0])
+        at[0] += 3 * pitch
+        return out.copy_(t)
+
+    sx, sdy, sy, sdx = spread(x), spread(dy), spread(torch.zeros_like(x)), spread(torch.zeros_like(x))
+    assert at[0] <= 1 << 18
+    _, mean, rstd = sa.layer_norm_fwd(sx, w, b, 1e-5, out=sy)
+    _, dw, db = sa.layer_norm_bwd(sdy, sx, w, mean, rstd, dx=sdx)
+    torch.cuda.synchronize()
+    check_fwd(x, w, b, 1e-5, (sy, mean, rstd))
+    check_bwd(dy, x, w, mean, rstd, (sdx, dw, db))
+
+
+def test_infinities_stay_in_their_row(cuda_dev):
+    """A row of NaN or infinities changes no other row's y and dx, also where rows share a warp."""
+    for N in (64, 128, 2000):
+        x, dy, w, b = make(cuda_dev, (67, N), torch.bfloat16, torch.bfloat16, 78)
+        bad = x.clone()
+        bad[5] = float("nan")
+        bad[33, 1] = float("inf")
+        keep = torch.ones(67, dtype=torch.bool, device=cuda_dev)
+        keep[5] = keep[33] = False
+        y, mean, rstd = sa.layer_norm_fwd(x, w, b)
+        by, bmean, brstd = sa.layer_norm_fwd(bad, w, b)
+        dx, _, _ = sa.layer_norm_bwd(dy, x, w, mean, rstd)
+        bdx, _, _ = sa.layer_norm_bwd(dy, bad, w, bmean, brstd)
+        for good, other in ((y, by), (mean, bmean), (rstd, brstd), (dx, bdx)):
+            assert torch.equal(good[keep], other[keep])
+        assert bool(by[5].isnan().all()) and bool(by[33].isnan().any())

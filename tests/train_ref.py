@@ -11,7 +11,9 @@ Bounds, from the kernels' arithmetic (u = 2^-8, half a BF16 step; everything els
             (u + 2 max e_p) A|V| + u |O|,  A|V| = sum_j p_j |v_j|.
   p (bwd)   relative e_s + e_lse + 2^-20.
   dV        sum_i p |dO| (u + e_p) + u |dV|.
-  delta     sum_d |dO_d| times O's own bound, and 2^-16 sum_d |dO_d O_d|.
+  delta     sum_d |dO_d| times O's own bound, and 2^-16 sum_d |dO_d O_d|.  (Formed from the sum of a row's rounded
+            dS instead, it is off by u sum_j |ds| <= u sum_j p (|dp| + |delta|), which is no more: sum_j p |dp| <=
+            |dO| A|V|, and |delta| <= |dO| |O|.)
   dp        2^-16 sum_d |dO_d v_d|.
   ds        p (e_delta + e_dp) + |ds| (u + e_p).
   dQ, dK    scale times the sums of ds's bound times |K|, |Q|, and u of the result.  In dQ a row that sees more
