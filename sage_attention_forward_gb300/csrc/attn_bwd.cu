@@ -13,10 +13,10 @@
 //
 // Two kernels, no atomics: every sum has one order.
 //   dq_kernel     one item per (128 queries, query head): Q and dO stay, K and V stream by:
-//                 S = Q K^T, dP = dO V^T, dQ += dS K.  It forms delta of its rows from dO, which it has,
-//                 and O, and leaves -lse * log2 e and -delta in the workspace, padded to whole tiles
-//                 (-inf and 0 there and for empty rows: their probabilities come out as 0).  Its key tiles come
-//                 last first.
+//                 S = Q K^T, dP = dO V^T, dQ += dS K, its key tiles last first.  It forms delta of its
+//                 rows from dO, which it has, and O, and at the end again from the sums of their dS; it leaves
+//                 -lse * log2 e and the better -delta in the workspace, padded to whole tiles (-inf and 0 there
+//                 and for empty rows: their probabilities come out as 0).
 //   dkdv_kernel   one item per (128 keys, key head): K and V stay in shared memory, Q and dO tiles
 //                 stream by with those statistics.  The transposed scores S^T = K Q^T and
 //                 dP^T = V dO^T leave P^T and dS^T in TMEM as the A operands of dV += P^T dO and
