@@ -477,7 +477,8 @@ typedef enum { ATTN_BF16 = 0, ATTN_F16 = 1, ATTN_F32 = 2 } attn_dtype;
  *   mean = sum x / N,  rstd = 1 / sqrt(sum (x - mean)^2 / N + eps),  y = (x - mean) rstd weight + bias
  *   x, y    : dtype [B, S, H, N], element strides x_str / y_str (batch, sequence, head), channel
  *             stride 1.  Any stride and alignment of the type; 16-byte accesses are used where
- *             pointers, strides and N allow them.  x may have strides of 0; y may be x itself.
+ *             pointers, strides and N allow them, or all rows are equally far apart and x's and y's as
+ *             far from 16 bytes.  x may have strides of 0; y may be x itself.
  *   weight, bias : w_dtype [N], each or NULL (1 and 0).  w_dtype is dtype or ATTN_F32.
  *   mean, rstd : float [B, S, H] outputs, contiguous
  *   eps     : finite, >= 0;  1 <= N <= 16384;  B * S * H <= 2^30 rows (0: nothing is done)

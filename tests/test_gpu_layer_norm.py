@@ -266,3 +266,37 @@ def test_infinities_stay_in_their_row(cuda_dev):
         for good, other in ((y, by), (mean, bmean), (rstd, brstd), (dx, bdx)):
             assert torch.equal(good[keep], other[keep])
         assert bool(by[5].isnan().all()) and bool(by[33].isnan().any())
+
+
+@pytest.mark.parametrize("dtype,wtype", TYPES)
+@pytest.mark.parametrize("rows,N,gap,start", [(1, 513, 0, 0), (1, 1773, 0, 3), (7, 259, 0, 1), (7, 515, 1, 0), (900, 1773, 0, 5),
+                                              (1300, 1001, 3, 1), (300, 6345, 0, 0), (40, 8177, 2, 7), (20, 8191, 0, 1),
+                                              (2000, 517, 8, 2), (9, 1022, 0, 1)])
+def test_rows_off_16_bytes(cuda_dev, rows, N, gap, start, dtype, wtype):
+    """Rows that start and end anywhere, with NaN between them and around the tensor: nothing of it comes into the
+    results, and what lies between and around the outputs' rows stays as it was."""
+    x, dy, w, b = make(cuda_dev, (rows, N), dtype, wtype, rows + N)
+    pitch, size = N + gap, start + rows * (N + gap) + 16
+
+    def spread(t):
+        store = torch.full((size,), float("nan"), dtype=dtype, device=cuda_dev)
+        view = store.as_strided((rows, N), (pitch, 1), start)
+        if t is not None:
+            view.copy_(t)
+        return store, view
+
+    (_, vx), (_, vdy), (sy, vy), (sdx, vdx) = spread(x), spread(dy), spread(None), spread(None)
+    _, mean, rstd = sa.layer_norm_fwd(vx, w, b, 1e-5, out=vy)
+    check_fwd(x, w, b, 1e-5, (vy, mean, rstd))
+    _, dw, db = sa.layer_norm_bwd(vdy, vx, w, mean, rstd, dx=vdx)
+    check_bwd(dy, x, w, mean, rstd, (vdx, dw, db))
+    for store, view in ((sy, vy), (sdx, vdx)):
+        view.fill_(float("nan"))
+        assert bool(store.isnan().all())
+    # in place, and the same bits again
+    _, again, _ = sa.layer_norm_bwd(vdy, vx, w, mean, rstd, dx=vdy)
+    assert torch.equal(dw, again)
+    check_bwd(dy, x, w, mean, rstd, (vdy, dw, db))
+    sa.layer_norm_fwd(vx, w, b, 1e-5, out=vx)
+    check_fwd(x, w, b, 1e-5, (vx, mean, rstd))
+    sa.attn_get_device_status()
