@@ -649,8 +649,8 @@ __global__ void __launch_bounds__(kShift ? 512 : 640) ln_fwd_ring_kernel(const L
       mbar_wait_teardown(&ring.full[n % 4], (n / 4) & 1);
 }
 
-// kMax = 640, or 1024 for the 16-bit rows above 8192 channels, where the registers leave no room
-// to hold the weights.
+// kMax = 640, or 1024 for the rows above 8192 channels, where the registers leave no room to hold the weights
+// (12000 x 12288 FP32, with a row read again from the caches 781 us, so 343).
 template <class T, int kMax, bool kShift>
 __global__ void __launch_bounds__(kMax) ln_bwd_ring_kernel(const LnParams p) {
   constexpr int kValues = 16;
@@ -864,31 +864,33 @@ cudaError_t launch_one(const LnParams& p, const Shape& s, cudaStream_t stream) {
                             stream, p);
   }
 }
-// kShift: rows by pieces of memory (RowPieces); false where a CTA has not the threads for them.
+constexpr int kRingBytes = 220 * 1024;
+// kShift: rows by pieces of memory (RowPieces); false where a CTA has not the threads for them, or the ring not the
+// room for two rows.
 template <class T, bool kShift, bool kBackward>
 bool fits_ring(const LnParams& p, Shape& s, LnParams& q) {
   constexpr int kN = 16 / (int)sizeof(T);
   const int pieces = kShift ? (p.N + 2 * (kN - 1)) / kN : p.N / kN;   // at most
-  if (s.lanes > 0 || (s.wide && (kShift || !kBackward || sizeof(T) == 4))) return false;
+  if (s.lanes > 0 || (s.wide && (kShift || !kBackward || 4 * 16 * pieces > kRingBytes))) return false;
   while (s.threads * 16 < pieces * kN) s.threads += 32;
   if (s.threads > (s.wide ? 1024 : kShift ? 512 : 640)) return false;
   q = p;
-  q.slot = 16 * pieces;   // at most 32 KB and a piece
+  q.slot = 16 * pieces;
   return true;
 }
 template <class T, bool kShift, bool kBackward>
 cudaError_t launch_ring(LnParams& q, const Shape& s, cudaStream_t stream) {
   static ContextOnce attr_done[2];
   auto* kernel = !kBackward ? ln_fwd_ring_kernel<T, kShift> : ln_bwd_ring_kernel<T, kShift ? 512 : 640, kShift>;
-  if constexpr (kBackward && !kShift && sizeof(T) == 2)
+  if constexpr (kBackward && !kShift)
     if (s.wide) kernel = ln_bwd_ring_kernel<T, 1024, false>;
   const cudaError_t e = attr_done[s.wide].run([&] {
-    return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, 220 * 1024);
+    return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kRingBytes);
   });
   if (e != cudaSuccess) return e;
   const size_t row = q.slot;
   const int per_sm = s.wide ? 1 : 65536 / (96 * s.threads);
-  q.ring = 6 * row * per_sm <= 220 * 1024 ? 3 : 2;
+  q.ring = 6 * row * per_sm <= (size_t)kRingBytes ? 3 : 2;
   return launch_dependent(kernel, dim3((unsigned)s.ctas), s.threads, kBackward ? 2 * q.ring * row : 4 * row, stream, q);
 }
 // shift: all rows of a tensor are equally far apart, and all tensors start at one distance from 16 bytes.  s: its CTAs

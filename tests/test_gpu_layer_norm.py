@@ -300,3 +300,14 @@ def test_rows_off_16_bytes(cuda_dev, rows, N, gap, start, dtype, wtype):
     sa.layer_norm_fwd(vx, w, b, 1e-5, out=vx)
     check_fwd(x, w, b, 1e-5, (vx, mean, rstd))
     sa.attn_get_device_status()
+
+
+@pytest.mark.parametrize("N", [8200, 12288, 14080, 14084, 16384])
+@pytest.mark.parametrize("rows", [5, 700])
+def test_wide_rows_of_32_bits(cuda_dev, rows, N):
+    """Two rows of x and dy in shared memory, up to what it holds, and past that."""
+    x, dy, w, b = make(cuda_dev, (rows, N), torch.float32, torch.float32, N)
+    y, mean, rstd = sa.layer_norm_fwd(x, w, b, 1e-6)
+    check_fwd(x, w, b, 1e-6, (y, mean, rstd))
+    check_bwd(dy, x, w, mean, rstd, sa.layer_norm_bwd(dy, x, w, mean, rstd))
+    sa.attn_get_device_status()
