@@ -311,3 +311,14 @@ def test_wide_rows_of_32_bits(cuda_dev, rows, N):
     check_fwd(x, w, b, 1e-6, (y, mean, rstd))
     check_bwd(dy, x, w, mean, rstd, sa.layer_norm_bwd(dy, x, w, mean, rstd))
     sa.attn_get_device_status()
+
+
+@pytest.mark.parametrize("dtype,wtype", TYPES)
+@pytest.mark.parametrize("N", [8192, 8200, 9000, 10240, 10248])
+def test_where_the_forms_change(cuda_dev, N, dtype, wtype):
+    """Around the largest rows of each form of the ring."""
+    x, dy, w, b = make(cuda_dev, (321, N), dtype, wtype, N)
+    y, mean, rstd = sa.layer_norm_fwd(x, w, b, 1e-6)
+    check_fwd(x, w, b, 1e-6, (y, mean, rstd))
+    check_bwd(dy, x, w, mean, rstd, sa.layer_norm_bwd(dy, x, w, mean, rstd))
+    sa.attn_get_device_status()
