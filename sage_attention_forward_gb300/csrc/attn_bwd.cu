@@ -799,8 +799,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     mbar_wait_teardown(&sm.drain, 0);
   } else if (warp == kWarpClear) {
     if (p.mask.kv_len != nullptr)
-      clear_warp<kKRing, true>(p.mask, [&](const Work& w) { return item_q(p, w); }, sm.work, sm.k, sm.k_full, sm.k_clear, lane,
-                         abort_flag, err);
+      clear_warp<kKRing, true>(p.mask, [&](const Work& w) { return item_q(p, w); }, sm.work, sm.k, sm.k_full,
+                               sm.k_clear, lane, abort_flag, err);
   } else if (warp < kWarpLoad) {
     // warpgroup g takes the keys [32 g, 32 g + 32) of each tile, a thread one query
     const int g = warp >> 2, wq = warp & 3;
@@ -1049,8 +1049,10 @@ __global__ void __launch_bounds__(kThreads, 1)
         load_row_bf16<32>(tDQ + lane_off + 32 * g, out, p.scale);
         tc_fence_before();
       }
-      store_rows<32>(p.d0 + (long long)item.b * p.s0[0] + (long long)(item.row0 + wq * 32) * p.s0[1] + (long long)item.h * p.s0[2] + 32 * g,
-                     p.s0[1], out, p.mask.Sq - (item.row0 + wq * 32), lane);
+      const int first = item.row0 + wq * 32;
+      store_rows<32>(p.d0 + (long long)item.b * p.s0[0] + (long long)first * p.s0[1] + (long long)item.h * p.s0[2] +
+                         32 * g,
+                     p.s0[1], out, p.mask.Sq - first, lane);
       work_release(sm.work, turn, lane);
       ++turn;
     }

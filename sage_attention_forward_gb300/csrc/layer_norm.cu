@@ -10,10 +10,11 @@
 // passes over the registers, so that no square of a large mean is subtracted) and its result.
 // Rows of up to 512 channels (256 in the backward) take 4 to 32 lanes of a warp, 16 (8) channels a lane;
 // longer ones a CTA, 16 channels a thread, through a ring of rows in shared memory where their alignment
-// allows it (20000 x 9000 BF16 without it, 32 channels a thread: 237 us forward and 320 backward, so 129 and 196).  CTAs walk over the rows: while a row is worked on the
-// next one's loads are under way, and in the backward pass a thread keeps the sums of dw and db
-// of its own channels in registers over all of its rows.  Each CTA writes its sums once to the
-// workspace, and a second kernel adds them up, in one fixed order: no atomics, the same bits every time.
+// allows it (20000 x 9000 BF16 without it, 32 channels a thread: 237 us forward and 320 backward, so 129
+// and 196).  CTAs walk over the rows: while a row is worked on the next one's loads are under way, and in
+// the backward pass a thread keeps the sums of dw and db of its own channels in registers over all of its
+// rows.  Each CTA writes its sums once to the workspace, and a second kernel adds them up, in one fixed
+// order: no atomics, the same bits every time.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
@@ -436,8 +437,8 @@ __global__ void __launch_bounds__(kMax) ln_bwd_kernel(const LnParams p) {
 }
 
 // ------------------------------------------------------------------ rows of a CTA through shared memory
-// Rows that a CTA takes, of up to 10240 channels (in the backward up to 16384), that allow 16-byte accesses: one thread copies whole rows ahead into a ring
-// in shared memory (16 channels a thread are too few bytes under way otherwise: with the next row
+// Rows that a CTA takes, of up to 10240 channels (in the backward up to 16384), that allow 16-byte
+// accesses: one thread copies whole rows ahead into a ring in shared memory (16 channels a thread are too few bytes under way otherwise: with the next row
 // in registers the forward reached 3.3 and the backward 2.1 of 6.7 TB/s).
 // The forward works on two rows at once (their sums share barriers and shuffles' latency) with the next
 // two under way; the backward, which reads its rows twice, on one of three, or of two where three would
@@ -649,8 +650,8 @@ __global__ void __launch_bounds__(kShift ? 512 : 640) ln_fwd_ring_kernel(const L
       mbar_wait_teardown(&ring.full[n % 4], (n / 4) & 1);
 }
 
-// kMax = 640 (512 with kShift), or 1024 for the rows above 10240 channels, where the registers leave no room to hold the weights
-// (12000 x 12288 FP32, with a row read again from the caches 781 us, so 343).
+// kMax = 640 (512 with kShift), or 1024 for the rows above 10240 channels, where the registers leave no
+// room to hold the weights (12000 x 12288 FP32, with a row read again from the caches 781 us, so 343).
 template <class T, int kMax, bool kShift>
 __global__ void __launch_bounds__(kMax) ln_bwd_ring_kernel(const LnParams p) {
   constexpr int kValues = 16;
