@@ -625,7 +625,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     mbar_init(&sm.d_empty, 1 + kWarpLoad);   // the last dP, and every softmax warp's part of delta
     for (int s = 0; s < kKRing; ++s) {
       mbar_init(&sm.k_full[s], 1);
-      mbar_init(&sm.k_empty[s], 1);
+      mbar_init(&sm.k_empty[s], tile_releasers(p.mask));
       mbar_init(&sm.k_clear[s], 1);
     }
     for (int s = 0; s < kVRing; ++s) {
@@ -800,7 +800,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   } else if (warp == kWarpClear) {
     if (p.mask.kv_len != nullptr)
       clear_warp<kKRing, true>(p.mask, [&](const Work& w) { return item_q(p, w); }, sm.work, sm.k, sm.k_full,
-                               sm.k_clear, lane, abort_flag, err);
+                               sm.k_empty, sm.k_clear, lane, abort_flag, err);
   } else if (warp < kWarpLoad) {
     // warpgroup g takes the keys [32 g, 32 g + 32) of each tile, a thread one query
     const int g = warp >> 2, wq = warp & 3;

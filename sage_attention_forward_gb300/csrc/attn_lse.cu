@@ -104,7 +104,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_init(&sm.k_full[s], 1);
       mbar_init(&sm.k_empty[s], 1);
       mbar_init(&sm.v_full[s], 1);
-      mbar_init(&sm.v_empty[s], 1);
+      mbar_init(&sm.v_empty[s], tile_releasers(p.mask));
       mbar_init(&sm.v_clear[s], 1);
     }
     for (int i = 0; i < kNQ; ++i) {
@@ -265,8 +265,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     mbar_wait_teardown(&sm.drain, 0);
   } else if (warp == kWarpClear) {
     if (p.mask.kv_len != nullptr)
-      clear_warp<kStages, false>(p.mask, [&](const Work& w) { return item_of(p, w); }, sm.work, sm.v, sm.v_full, sm.v_clear,
-                          lane, abort_flag, err);
+      clear_warp<kStages, false>(p.mask, [&](const Work& w) { return item_of(p, w); }, sm.work, sm.v, sm.v_full,
+                                 sm.v_empty, sm.v_clear, lane, abort_flag, err);
   } else if (warp < kWarpLoad) {
     const int i = warp >> 2, wq = warp & 3;
     const uint32_t lane_off = (uint32_t)(wq * 32) << 16;

@@ -171,12 +171,16 @@ __device__ __forceinline__ void load_tile(uint8_t* dst, const void* tmap, uint64
 // Rows past a batch entry's last key meet probabilities of zero in the products that sum over the
 // keys, but hold whatever the caller's padding holds, and 0 * NaN is NaN: in the tile where an item's
 // keys end they are set to zero in shared memory.  That is one warp's work: it waits for every
-// tile of the ring in turn, clears where it has to, and tells the MMA threads by the slot's barrier.
+// tile of the ring in turn, clears where it has to, and tells the MMA threads by the slot's barrier.  A slot is
+// loaded again only when this warp, too, is done with it: a turn of the ring behind the products, it would take
+// another tile's phase for its own.
 // (The swizzle permutes a row's 16-byte pieces within the row, so whole rows are contiguous.)
 // How many of the rows of an item's last tile are keys; kTile: nothing to clear.
 __device__ __forceinline__ int last_rows(const Mask& m, int keys, int n) {
   return keys < m.Sk && n * kTile > keys ? keys - (n - 1) * kTile : kTile;
 }
+// Arrivals that empty a slot of the ring whose tiles are cleared: the products', and the clearing warp's.
+__device__ __forceinline__ int tile_releasers(const Mask& m) { return m.kv_len != nullptr ? 2 : 1; }
 __device__ __forceinline__ void clear_rows(uint8_t* tile, int first, int lane) {
   for (int at = first * 128 + lane * 16; at < kHalfBytes; at += 32 * 16) {
     *reinterpret_cast<uint4*>(tile + at) = make_uint4(0u, 0u, 0u, 0u);
@@ -188,8 +192,8 @@ __device__ __forceinline__ void clear_rows(uint8_t* tile, int first, int lane) {
 // kFirst: an item's first tile is the one where its keys end, and not its last.
 template <int kRing, bool kFirst, class Make>
 __device__ __forceinline__ void clear_warp(const Mask& m, Make make, WorkRing& work, uint8_t (*tiles)[kTileBytes],
-                                           uint64_t* full, uint64_t* cleared, int lane, volatile uint32_t* abort_flag,
-                                           uint32_t* err) {
+                                           uint64_t* full, uint64_t* empty, uint64_t* cleared, int lane,
+                                           volatile uint32_t* abort_flag, uint32_t* err) {
   int it = 0, turn = 0;
   do {
     const auto item = make(work_read(work, turn));
@@ -202,6 +206,7 @@ __device__ __forceinline__ void clear_warp(const Mask& m, Make make, WorkRing& w
         clear_rows(tiles[slot], rows, lane);
         if (lane == 0) mbar_arrive(&cleared[slot]);
       }
+      if (lane == 0) mbar_arrive(&empty[slot]);
     }
   } while (work_wait(work, ++turn, abort_flag, err));
 }
