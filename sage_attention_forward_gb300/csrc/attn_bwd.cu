@@ -229,8 +229,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           const int qs = it % kQRing, qu = it / kQRing, ds = it % kDRing, du = it / kDRing, rs = it & 1, ru = it >> 1;
           if (qu > 0 && !wait_sleep(&sm.q_empty[qs], (qu - 1) & 1, abort_flag, err, kErrTimeoutSync)) return false;
           mbar_arrive_expect_tx(&sm.q_full[qs], kTileBytes);
-          load_tile(sm.q[qs], &tm_q, &sm.q_full[qs], t * kTile, h, i.b);
-          ++q_issued;
+          if (!withheld(q_issued++)) load_tile(sm.q[qs], &tm_q, &sm.q_full[qs], t * kTile, h, i.b);
           if (j == 0) {
             if (items > 0 && !wait_sleep(&sm.v_empty, (items - 1) & 1, abort_flag, err, kErrTimeoutSync)) return false;
             mbar_arrive_expect_tx(&sm.v_full, kTileBytes);
@@ -686,8 +685,8 @@ __global__ void __launch_bounds__(kThreads, 1)
           const int slot = it % kKRing, use = it / kKRing;
           if (use > 0 && !wait_sleep(&sm.k_empty[slot], (use - 1) & 1, abort_flag, err, kErrTimeoutSync)) return false;
           mbar_arrive_expect_tx(&sm.k_full[slot], kTileBytes);
-          load_tile(sm.k[slot], &tm_k, &sm.k_full[slot], (i.n - 1 - j) * kTile, hk, i.b);
-          ++k_issued;
+          if (!withheld(k_issued++))
+            load_tile(sm.k[slot], &tm_k, &sm.k_full[slot], (i.n - 1 - j) * kTile, hk, i.b);
         }
         if (j == 0) {
           if (d_issued > 0 && !wait_sleep(&sm.d_empty, (d_issued - 1) & 1, abort_flag, err, kErrTimeoutSync)) return false;

@@ -162,8 +162,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           const int slot = (it + j) % kStages, use = (it + j) / kStages;
           if (use > 0 && !wait_sleep(&sm.v_empty[slot], (use - 1) & 1, abort_flag, err, kErrTimeoutSync)) return false;
           mbar_arrive_expect_tx(&sm.v_full[slot], kTileBytes);
-          load_tile(sm.v[slot], &tm_v, &sm.v_full[slot], j * kTile, hk, i.b);
-          ++v_issued;
+          if (!withheld(v_issued++)) load_tile(sm.v[slot], &tm_v, &sm.v_full[slot], j * kTile, hk, i.b);
           if (j + 1 < i.n && !load_k(i, j + 1, hk)) return false;
         }
         it += i.n;

@@ -460,9 +460,10 @@ __device__ __forceinline__ void ring_init(RowRing& r) {
   __syncthreads();
 }
 // The row in slot s has landed, for the (phase + 1)-th time.  Should the wait run out, that is recorded, and
-// the rest of the kernel works on what is there: every thread keeps to its barriers.
-__device__ __forceinline__ void ring_wait(RowRing& r, int s, int phase) {
-  mbar_wait<false>(&r.full[s], phase & 1, &r.abort_flag, &g_err_norm, kErrTimeoutTma);
+// the rest of the kernel works on what is there: every thread keeps to its barriers.  The thread that loads loads
+// nothing more then: a slot whose row has not landed is not asked for another one.
+__device__ __forceinline__ bool ring_wait(RowRing& r, int s, int phase) {
+  return mbar_wait<false>(&r.full[s], phase & 1, &r.abort_flag, &g_err_norm, kErrTimeoutTma);
 }
 
 // Rows that do not start and end on 16 bytes (an odd N) go through the same rings by whole 16-byte pieces of
@@ -571,11 +572,12 @@ __global__ void __launch_bounds__(kShift ? 512 : 640) ln_fwd_ring_kernel(const L
       if (row >= p.rows) return;
       const int slot = 2 * (i & 1) + r;
       mbar_arrive_expect_tx(&ring.full[slot], pieces.bytes(p, (int)row));
+      if (withheld(issued++)) continue;
       pieces.load(p, rows_smem + slot * p.slot, reinterpret_cast<const T*>(p.x) + row_at(p, p.xs, (int)row), (int)row,
                   &ring.full[slot]);
-      ++issued;
     }
   };
+  bool landed = true;   // all rows that were waited for
   if (tid == 0) {
     issue(0);
     issue(1);
@@ -586,7 +588,7 @@ __global__ void __launch_bounds__(kShift ? 512 : 640) ln_fwd_ring_kernel(const L
 #pragma unroll
     for (int r = 0; r < 2; ++r) {
       const int slot = 2 * (i & 1) + r;
-      if (r == 0 || two) ring_wait(ring, slot, i >> 1);
+      if (r == 0 || two) landed = ring_wait(ring, slot, i >> 1) && landed;
       const uint4* src = reinterpret_cast<const uint4*>(rows_smem + slot * p.slot);
       const int in_row = row + r * (int)gridDim.x;
       const T* x = reinterpret_cast<const T*>(p.x) + (kShift && (r == 0 || two) ? row_at(p, p.xs, in_row) : 0);
@@ -602,7 +604,7 @@ __global__ void __launch_bounds__(kShift ? 512 : 640) ln_fwd_ring_kernel(const L
       sum[r] = a[0] + a[1];
     }
     row_sums<0>(sum, scratch, turn);
-    if (tid == 0) issue(i + 2);   // (all threads have read this turn's rows: they met in row_sums)
+    if (tid == 0 && landed) issue(i + 2);   // (all threads have read this turn's rows: they met in row_sums)
     float sq[2], mean[2];
 #pragma unroll
     for (int r = 0; r < 2; ++r) {
@@ -645,7 +647,7 @@ __global__ void __launch_bounds__(kShift ? 512 : 640) ln_fwd_ring_kernel(const L
       }
     }
   }
-  if (tid == 0 && ring.abort_flag)   // nothing may land in this CTA's shared memory after it has gone
+  if (tid == 0 && !landed)   // nothing may land in this CTA's shared memory after it has gone
     for (int n = issued > 4 ? issued - 4 : 0; n < issued; ++n)   // (the n-th row goes to slot n % 4)
       mbar_wait_teardown(&ring.full[n % 4], (n / 4) & 1);
 }
@@ -674,10 +676,11 @@ __global__ void __launch_bounds__(kMax) ln_bwd_ring_kernel(const LnParams p) {
     uint8_t* to = rows_smem + slot * 2 * bytes;
     uint64_t* bar = &ring.full[slot];
     mbar_arrive_expect_tx(bar, 2 * pieces.bytes(p, (int)row));
+    if (withheld(issued++)) return;
     pieces.load(p, to, reinterpret_cast<const T*>(p.x) + place(p.xs, (int)row), (int)row, bar);
     pieces.load(p, to + bytes, reinterpret_cast<const T*>(p.dy) + place(p.dys, (int)row), (int)row, bar);
-    ++issued;
   };
+  bool landed = true;   // all rows that were waited for
   if (tid == 0)
     for (int i = 0; i < p.ring; ++i) issue(blockIdx.x + (long long)i * gridDim.x, i);
   float next_mean = 0.0f, next_rstd = 0.0f;
@@ -695,7 +698,7 @@ __global__ void __launch_bounds__(kMax) ln_bwd_ring_kernel(const LnParams p) {
     const uint4* sd = reinterpret_cast<const uint4*>(rows_smem + slot * 2 * bytes + bytes);
     const T* const gx = reinterpret_cast<const T*>(p.x) + (kShift ? place(p.xs, row) : 0);
     const T* const gd = reinterpret_cast<const T*>(p.dy) + (kShift ? place(p.dys, row) : 0);
-    ring_wait(ring, slot, phase);
+    landed = ring_wait(ring, slot, phase) && landed;
     float s[2], s0[2] = {0.0f, 0.0f}, s1[2] = {0.0f, 0.0f};   // sums of g and of g xhat
 #pragma unroll
     for (int k = 0; k < kPieces; ++k) {
@@ -725,7 +728,7 @@ __global__ void __launch_bounds__(kMax) ln_bwd_ring_kernel(const LnParams p) {
     s[1] = s1[0] + s1[1];
     row_sums<0>(s, scratch, turn);
     // (all threads have met: they are done with the row before this one, and its place is free)
-    if (tid == 0 && i > 0) issue(row + (long long)(p.ring - 1) * gridDim.x, slot == 0 ? p.ring - 1 : slot - 1);
+    if (tid == 0 && i > 0 && landed) issue(row + (long long)(p.ring - 1) * gridDim.x, slot == 0 ? p.ring - 1 : slot - 1);
     const float m0 = -s[0] * inv_n, m1 = -s[1] * inv_n;
     T* dx = reinterpret_cast<T*>(p.dx) + place(p.dxs, row);
 #pragma unroll
@@ -780,7 +783,7 @@ __global__ void __launch_bounds__(kMax) ln_bwd_ring_kernel(const LnParams p) {
       }
     }
   }
-  if (tid == 0 && ring.abort_flag)
+  if (tid == 0 && !landed)
     for (int i = issued > p.ring ? issued - p.ring : 0; i < issued; ++i)
       mbar_wait_teardown(&ring.full[i % p.ring], (i / p.ring) & 1);
 }

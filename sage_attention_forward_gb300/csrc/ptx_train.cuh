@@ -8,6 +8,14 @@ namespace sa {
 // A bit of the device error words beside ptx.cuh's: shared memory does not start on the boundary that a kernel needs.
 constexpr uint32_t kErrSmemBase = 1u << 3;
 
+// Check builds: a CTA's load with this number (of the rows, or of one operand's tiles) is announced and not made, so that
+// the wait for it runs out (tests of the failure path).
+#ifdef SAGEATTN_CHECK_WITHHOLD
+__device__ __forceinline__ bool withheld(int load) { return load == SAGEATTN_CHECK_WITHHOLD; }
+#else
+__device__ __forceinline__ bool withheld(int) { return false; }
+#endif
+
 // ----------------------------------------------------------------- work stealing
 // A running CTA may take the place of one that has not started: try_cancel asks for one, writes the
 // answer (16 bytes) to shared memory and completes on `bar`.  clc_answer tells whether a CTA was
