@@ -166,12 +166,13 @@ attn_status check_strides(const char* name, const void* ptr, const int64_t* in, 
 
 namespace {
 ErrReader g_err_reader[8];   // (zeros before any translation unit's constructors run)
-int g_err_readers = 0;
+constexpr int kMostErrReaders = (int)(sizeof(g_err_reader) / sizeof(g_err_reader[0]));
+int g_err_readers = 0;       // (more than there is room for: attn_get_device_status says so)
 }  // namespace
 
 bool add_err_reader(ErrReader read) {
-  if (g_err_readers >= (int)(sizeof(g_err_reader) / sizeof(g_err_reader[0]))) return false;
-  g_err_reader[g_err_readers++] = read;
+  if (g_err_readers++ >= kMostErrReaders) return false;
+  g_err_reader[g_err_readers - 1] = read;
   return true;
 }
 
@@ -732,6 +733,9 @@ attn_status attn_selftest_wait_timeout(const void* q, const void* k, const void*
 }
 
 attn_status attn_get_device_status(attn_stream_t stream) {
+  if (sa::g_err_readers > sa::kMostErrReaders)
+    return fail(ATTN_ERR_UNSUPPORTED, "%d error words are registered, %d are read", sa::g_err_readers,
+                sa::kMostErrReaders);
   cudaError_t e = cudaStreamSynchronize((cudaStream_t)stream);
   if (e != cudaSuccess) return fail_cuda(e, "cudaStreamSynchronize");
   uint32_t w = 0;
