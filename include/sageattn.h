@@ -456,8 +456,10 @@ ATTN_API size_t attn_bwd_bf16_workspace_size(int B, int Sq, int Sk, int Hq, int 
  * p and ds are rounded to BF16 before the products that sum over them (for dq so that a row of ds keeps
  * the sum 0, and the keys' mean stays out of it), sums are FP32 in a fixed
  * order (no atomics: the same inputs give the same bits), each output is rounded once.
- * dq of a row with more than 128 keys starts from delta = dout . o: where nearly all of its probability is
- * one key's, dout . v - delta is of the size of o's BF16 rounding, and dq is only as exact as that.
+ * dq of a row with more than 128 keys starts from delta = dout . o, which o's BF16 rounding moves by some e.  What
+ * that leaves in the sum of the row's ds is taken off again, from its first 128 keys and from a key with more
+ * than half of its probability; dq is then off by softmax_scale e times the distance of those keys' mean from the
+ * row's mean key (each weighted by p).
  * Enqueues its kernels on `stream`; errors as attn_fwd_bf16_lse.
  */
 ATTN_API attn_status attn_bwd_bf16(const void* dout, const void* q, const void* k, const void* v, const void* o,

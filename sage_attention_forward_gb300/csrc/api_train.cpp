@@ -121,6 +121,8 @@ attn_status attn_bwd_bf16(const void* dout, const void* q, const void* k, const 
   TRY(tmap_bhsd_bf16(&tv, v, B, Sk, Hkv, vs));
   TRY(tmap_bhsd_bf16(&td, dout, B, Sq, Hq, ds));
   TRY(tmap_bhsd_bf16(&to, o, B, Sq, Hq, os));
+  t.k = k;
+  for (int i = 0; i < 3; ++i) t.k_str[i] = ks[i];
   t.lse = lse;
   t.dq = dq;
   t.dk = dk;

@@ -56,6 +56,7 @@ constexpr int kThreads = 32 * (kWarpClear + 1);
 // first SMs with a second long one: 409 us of a backward in place of 332).
 constexpr int kAskAhead = 5;
 constexpr float kLog2e = 1.4426950408889634f;
+constexpr float kHot = 0.51f;        // (dq_kernel) a key with more of a row's probability is its only one, roundings and all
 constexpr float kLeastSum = 1e-6f;   // (dq_kernel) of a row's probabilities in a tile, to be divided by
 
 __device__ uint32_t g_err_bwd;
@@ -71,6 +72,8 @@ struct BwdParams {
   float* neg_delta;
   int Sq_pad;
   const float* lse;         // [B, Hq, Sq] (dq_kernel)
+  const __nv_bfloat16* k;   // (dq_kernel) K, for the keys that take their row's rest
+  long long k_str[3];
   __nv_bfloat16 *d0, *d1;   // dQ; or dK and dV
   long long s0[3], s1[3];   // their element strides (b, s, h)
   int H, group;             // heads of this grid (Hkv, or Hq), Hq / Hkv
@@ -577,6 +580,7 @@ struct __align__(1024) SmemQ {
   uint64_t dp_full;
   uint64_t ds_full, ds_free;   // dS stored in TMEM by every softmax warp; read by dQ's product
   float delta[kGroups][kTile];   // each warpgroup's part of the rows' sums
+  int hot[kTile];                // each row's key with more than half of its probability
   uint64_t delta_full, rest_full;
   uint64_t acc_done;
   uint64_t drain;
@@ -805,7 +809,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int g = warp >> 2, wq = warp & 3;
     const uint32_t lane_off = (uint32_t)(wq * 32) << 16;
     bool ok = true;
-    int it = 0, items = 0, turn = 0;
+    int it = 0, turn = 0;
+    uint32_t par = 0;   // parities: bit 0 of the items done that have keys, bit 1 of those with several tiles
     const int r = wq * 32 + lane;   // the thread's row of a tile
     // the warpgroup's 32 channels of the row in a tile (row r's 16-byte piece c of a half is at c ^ (r & 7))
     auto tile_row = [&](const uint8_t* tile, uint32_t (&x)[16]) {
@@ -820,11 +825,9 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
     };
     // Q from its tile in shared memory to TMEM: as the A operand from shared memory it would be read
-    // again for every key tile, at the full rate of shared memory while S runs.  With it the load of
-    // the row's log-sum-exp is started.
-    float lse = -INFINITY;
-    auto begin_item = [&](int n, const ItemQ& item) -> bool {
-      if (!mbar_wait_warp<false>(&sm.q_full, n & 1, abort_flag, err, kErrTimeoutTma)) return false;
+    // again for every key tile, at the full rate of shared memory while S runs.
+    auto begin_item = [&](uint32_t parity) -> bool {
+      if (!mbar_wait_warp<false>(&sm.q_full, parity, abort_flag, err, kErrTimeoutTma)) return false;
       uint32_t x[16];
       tile_row(sm.q, x);
       tmem_st16(tQ + lane_off + 16 * g, x);
@@ -835,30 +838,28 @@ __global__ void __launch_bounds__(kThreads, 1)
         mbar_arrive(&sm.q_empty);
         mbar_arrive(&sm.q_ready);
       }
-      const int row = item.row0 + r;
-      lse = row < p.mask.Sq ? __ldg(p.lse + ((long long)item.b * p.H + item.h) * p.mask.Sq + row) : -INFINITY;
       return true;
     };
     // -delta of the row from the warpgroups' parts.  (They are next written in the next item, whose S and O
     // no warp sees before all have begun it.)
-    int sums = 0;   // so far (items of one tile have none)
     auto sum_parts = [&](float part, float& neg_delta) -> bool {
       sm.delta[g][r] = part;
       __syncwarp();
       if (lane == 0) mbar_arrive(&sm.delta_full);
-      if (!mbar_wait_warp<false>(&sm.delta_full, sums++ & 1, abort_flag, err, kErrTimeoutSync)) return false;
+      if (!mbar_wait_warp<false>(&sm.delta_full, (par >> 1) & 1, abort_flag, err, kErrTimeoutSync)) return false;
+      par ^= 2u;
       neg_delta = -((sm.delta[0][r] + sm.delta[1][r]) + (sm.delta[2][r] + sm.delta[3][r]));
       return true;
     };
     // The sums of the warpgroups' x and y, in columns of S that each has read (the next S is not
     // issued before all softmax warps have begun the next item).
-    auto sum_rest = [&](int n, float& x, float& y) -> bool {
+    auto sum_rest = [&](float& x, float& y) -> bool {
       tmem_st2(tS + lane_off + kCols * g, __float_as_uint(x), __float_as_uint(y));
       tmem_st_wait();
       tc_fence_before();
       __syncwarp();
       if (lane == 0) mbar_arrive(&sm.rest_full);
-      if (!mbar_wait_warp<false>(&sm.rest_full, n & 1, abort_flag, err, kErrTimeoutSync)) return false;
+      if (!mbar_wait_warp<false>(&sm.rest_full, par & 1, abort_flag, err, kErrTimeoutSync)) return false;
       tc_fence_after();
       uint32_t v[kGroups][2];
 #pragma unroll
@@ -875,9 +876,9 @@ __global__ void __launch_bounds__(kThreads, 1)
       return true;
     };
     // the warpgroup's part of delta, from O's tile and dO's
-    auto find_part = [&](int n, float& part) -> bool {
-      if (!mbar_wait_warp<false>(&sm.d_full, n & 1, abort_flag, err, kErrTimeoutTma) ||
-          !mbar_wait_warp<false>(&sm.o_full, n & 1, abort_flag, err, kErrTimeoutTma))
+    auto find_part = [&](float& part) -> bool {
+      if (!mbar_wait_warp<false>(&sm.d_full, par & 1, abort_flag, err, kErrTimeoutTma) ||
+          !mbar_wait_warp<false>(&sm.o_full, par & 1, abort_flag, err, kErrTimeoutTma))
         return false;
       uint32_t x[16], y[16];
       tile_row(sm.dout, x);
@@ -898,28 +899,27 @@ __global__ void __launch_bounds__(kThreads, 1)
     static_assert(kGroups == 4, "four parts of delta");
     {
       const ItemQ item = item_q(p, first_work());
-      if (item.n > 0) ok = begin_item(0, item);
+      if (item.n > 0) ok = begin_item(0);
     }
     bool more = ok;
     while (more) {
       int n, valid;   // products left, and the keys that this row sees from the group's first of the tile on
       float nl = -INFINITY, nd = 0.0f;
-      float* delta_at;
-      bool one_tile;
       {
         const ItemQ item = item_q(p, work_read(sm.work, turn));
         const int row = item.row0 + r;
         n = item.n;
-        one_tile = n == 1;
+        const bool one_tile = n == 1;
         // a row that sees one key has ds = 0: as a row that sees none
         valid = row_limit(p.mask, item.keys, row);
         if (valid == 1) valid = 0;
         valid -= kCols * g + (n - 1) * kTile;   // (an item's key tiles come last first)
         const long long at = ((long long)item.b * p.H + item.h) * p.Sq_pad + row;
-        delta_at = p.neg_delta + at;
         if (n > 0) {
+          const float lse =
+              row < p.mask.Sq ? __ldg(p.lse + ((long long)item.b * p.H + item.h) * p.mask.Sq + row) : -INFINITY;
           float part;
-          ok = find_part(items, part) && (one_tile || sum_parts(part, nd));
+          ok = find_part(part) && (one_tile || sum_parts(part, nd));
           if (lse == -INFINITY) nd = 0.0f;
           else nl = -lse * kLog2e;
           if (g == 0) p.neg_lse2[at] = nl;
@@ -933,7 +933,14 @@ __global__ void __launch_bounds__(kThreads, 1)
       // keys with a mean of 0, 0.5, 1 and 4 times their spread: 0.0024, 0.0028, 0.0037 and 0.0123 without this
       // and 0.0024, 0.0024, 0.0025 and 0.0033 with it (0.0017 is the rounding of dQ); with one tile, where delta itself
       // is formed so, and 2 keys 0.0045 and 0.0024.  It takes 2 to 4 % of the backward's time.
-      float rest = 0.0f;
+      // A key with more than half of a row's probability has most of that rest, and its dP - delta may be no larger than
+      // O's rounding: where it is in another tile it takes 1 / (1 + sum p) of the rest, by itself at the item's end, as
+      // a multiple of its K off dQ.  There is at most one such key in a row.  Where all the rest went to the first tile,
+      // dQ was off by 0.17 and 0.07 of its norm with 260 and 1000 queries equal to keys, and by all of it where every
+      // row has nearly all its probability on one key beyond the tile; so by 0.0020 to 0.0028 (at most 1 % of
+      // the backward's time: 16896 queries on 512 keys 317 -> 320 us).
+      float rest = 0.0f, better = 0.0f;   // better: with all of the row's p, whose sum is 1, -delta as sum p dp
+      int hot = -1;   // that key: its warpgroup's, and from the last product on the row's
       // (a copy of each without the other's code: with it the loop took 1.5 % longer)
       auto product = [&](auto last_c) -> bool {
         constexpr bool kLast = decltype(last_c)::value;
@@ -944,9 +951,12 @@ __global__ void __launch_bounds__(kThreads, 1)
         tc_fence_after();
         {
           uint32_t a[kCols];
-          tmem_ld32(tS + lane_off + kCols * g, a);
+          float top = 0.0f;
+          if (kLast) tmem_ld32(tS + lane_off + kCols * g, a);
+          else tmem_ld32_max(tS + lane_off + kCols * g, a, top);
           tmem_ld_wait();
           tmem_reg_fence(a);
+          if (!kLast) asm volatile("" : "+f"(top));   // (not read before the wait)
           tc_fence_before();
           __syncwarp();
           if (lane == 0) mbar_arrive(&sm.s_free);
@@ -956,6 +966,13 @@ __global__ void __launch_bounds__(kThreads, 1)
             ffma2(x0, x1, u2f(a[2 * e]), u2f(a[2 * e + 1]), p.c_log2, p.c_log2, nl, nl);
             pr[2 * e] = ex2_approx(x0);
             pr[2 * e + 1] = ex2_approx(x1);
+          }
+          if (!kLast && fmaf(top, p.c_log2, nl) > -1.0f) {   // (top may be that of a key that the row does not see)
+            int at = -1;
+#pragma unroll
+            for (int c = 0; c < kCols; ++c)
+              if (c < valid && pr[c] > kHot) at = c;
+            if (at >= 0) hot = (n - 1) * kTile + kCols * g + at;
           }
         }
         float sum = 0.0f;
@@ -990,11 +1007,19 @@ __global__ void __launch_bounds__(kThreads, 1)
               ffma2(r0, r1, pr[2 * e], pr[2 * e + 1], x0, x1, r0, r1);
             }
             rest += r0 + r1;
-            ok = sum_rest(items, rest, sum);
+            if (hot >= 0) {
+              sm.hot[r] = hot;
+              sum += 2.0f;   // (a row's sum is at most 1, but for its rounding)
+            }
+            ok = sum_rest(rest, sum);
             if (!ok) return false;
-            // (with all of the row's p, whose sum is 1, this is delta as sum p dp, for dkdv_kernel)
-            if (g == 0) *delta_at = nd - rest;
-            if (sum > kLeastSum) nd -= rest / sum;
+            if (sum > 1.5f) {
+              sum -= 1.0f;
+              hot = sm.hot[r];
+            }
+            better = nd - rest;
+            rest = sum > kLeastSum ? rest / sum : 0.0f;
+            nd -= rest;
           }
 #pragma unroll
           for (int e = 0; e < kCols / 2; ++e) {
@@ -1033,19 +1058,43 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (!ok) break;
       // the next item's Q, so that its first S runs while this one's rows are stored
       const ItemQ item = item_q(p, work_read(sm.work, turn));
+      if (g == 0 && item.n > 0)   // (for dkdv_kernel)
+        p.neg_delta[((long long)item.b * p.H + item.h) * p.Sq_pad + item.row0 + r] = better;
       more = work_wait(sm.work, turn + 1, abort_flag, err);
       if (more) {
         const ItemQ next = item_q(p, work_read(sm.work, turn + 1));
-        if (next.n > 0) ok = begin_item(items + (item.n > 0 ? 1 : 0), next);
+        if (next.n > 0) ok = begin_item((par ^ (item.n > 0 ? 1u : 0u)) & 1);
         if (!ok) break;
       }
       // each warpgroup stores 32 of the rows' channels
       uint32_t out[16] = {};
       if (item.n > 0) {
-        ok = mbar_wait_warp<false>(&sm.acc_done, items++ & 1, abort_flag, err, kErrTimeoutMma);
+        ok = mbar_wait_warp<false>(&sm.acc_done, par & 1, abort_flag, err, kErrTimeoutMma);
         if (!ok) break;
+        par ^= 1u;
         tc_fence_after();
-        load_row_bf16<32>(tDQ + lane_off + 32 * g, out, p.scale);
+        if (!__any_sync(0xffffffffu, hot >= 0)) {
+          load_row_bf16<32>(tDQ + lane_off + 32 * g, out, p.scale);
+        } else {
+          const uint4* k = nullptr;
+          if (hot >= 0)
+            k = reinterpret_cast<const uint4*>(p.k + (long long)item.b * p.k_str[0] + (long long)hot * p.k_str[1] +
+                                               (long long)div_by(item.h, p.by_group) * p.k_str[2] + 32 * g);
+#pragma unroll
+          for (int c = 0; c < 4; ++c) {   // (8 channels at a time, for the registers)
+            uint32_t a[8];
+            tmem_ld8(tDQ + lane_off + 32 * g + 8 * c, a);
+            const uint4 v = k != nullptr ? __ldg(k + c) : make_uint4(0u, 0u, 0u, 0u);
+            const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+            tmem_ld_wait();
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              asm volatile("" : "+r"(a[2 * e]), "+r"(a[2 * e + 1]));   // (not read before the wait)
+              out[4 * c + e] = pack_bf16x2(fmaf(-rest, u2f(w[e] << 16), u2f(a[2 * e])) * p.scale,
+                                           fmaf(-rest, u2f(w[e] & 0xffff0000u), u2f(a[2 * e + 1])) * p.scale);
+            }
+          }
+        }
         tc_fence_before();
       }
       const int first = item.row0 + wq * 32;
@@ -1143,6 +1192,7 @@ cudaError_t launch_attn_bwd_bf16(const CUtensorMap& tm_q, const CUtensorMap& tm_
   p.Sq_pad = Sq_pad;
   p.group = a.Hq / a.Hkv;
   p.lse = t.lse;
+  p.k = reinterpret_cast<const __nv_bfloat16*>(t.k);
   const int k_tiles = (a.Sk + kTile - 1) / kTile, q_tiles = Sq_pad / kTile;
   p.H = a.Hq;
   p.by_H = make_div(p.H);
@@ -1154,6 +1204,7 @@ cudaError_t launch_attn_bwd_bf16(const CUtensorMap& tm_q, const CUtensorMap& tm_
   p.by_parts = make_div(1);
   p.partial = nullptr;
   for (int i = 0; i < 3; ++i) {
+    p.k_str[i] = t.k_str[i];
     p.s0[i] = t.dq_str[i];
     p.s1[i] = 0;
   }

@@ -204,6 +204,8 @@ cudaError_t launch_attn_fwd_bf16_lse(const CUtensorMap& tm_q, const CUtensorMap&
                                      const CUtensorMap& tm_o, const TrainArgs& a, float* lse, cudaStream_t stream);
 
 struct BwdTensors {
+  const void* k;
+  long long k_str[3];
   const float* lse;
   void *dq, *dk, *dv;
   long long dq_str[3], dk_str[3], dv_str[3];

@@ -70,6 +70,12 @@ __device__ __forceinline__ void tmem_ld2(uint32_t taddr, uint32_t (&r)[2]) {
 __device__ __forceinline__ void tmem_st2(uint32_t taddr, uint32_t x, uint32_t y) {
   asm volatile("tcgen05.st.sync.aligned.32x32b.x2.b32 [%0], {%1, %2};" ::"r"(taddr), "r"(x), "r"(y) : "memory");
 }
+// Eight columns of the warp's 32 lanes.
+__device__ __forceinline__ void tmem_ld8(uint32_t taddr, uint32_t (&r)[8]) {
+  asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7])
+               : "r"(taddr));
+}
 // 16 lanes x 32 columns (four groups of 8): thread T gets, of group i, columns 8i + 2 (T % 4) and
 // the next, lane T / 4 in r[4i], r[4i + 1] and lane T / 4 + 8 in r[4i + 2], r[4i + 3].
 __device__ __forceinline__ void tmem_ld_16x32(uint32_t taddr, uint32_t (&r)[16]) {
