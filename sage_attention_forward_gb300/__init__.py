@@ -481,12 +481,19 @@ def _strides(names: str, *tensors: torch.Tensor) -> array:
     return out
 
 
+def _sizes(*sizes) -> None:
+    """Sizes reach the library as C ints, to which ctypes would cut them without a word."""
+    if max(sizes) > 0x7fffffff:
+        raise ValueError(f"sizes must be below 2^31, got {tuple(sizes)}")
+
+
 def _train_shapes(q, k, v, kv_len):
     if q.dim() != 4 or k.dim() != 4:
         raise ValueError(f"q and k must be [B, S, H, D], got {tuple(q.shape)} and {tuple(k.shape)}")
     B, Sq, Hq, D = q.shape
     _, Sk, Hkv, _ = k.shape
     dev = _cuda_index("q", q)
+    _sizes(B, Sq, Sk, Hq, Hkv, D)
     if q.dtype is not torch.bfloat16:
         raise ValueError(f"q must be bfloat16, got {q.dtype}")
     keys = (B, Sk, Hkv, D)
@@ -529,6 +536,7 @@ def attn_fwd_bf16_lse(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, softmax
 
 def attn_bwd_workspace(B: int, Sq: int, Sk: int, Hq: int, Hkv: int, device) -> torch.Tensor:
     """Scratch for attn_bwd_bf16 of these shapes; calls on different streams need one each."""
+    _sizes(B, Sq, Sk, Hq, Hkv)
     return torch.empty(lib().attn_bwd_bf16_workspace_size(B, Sq, Sk, Hq, Hkv), dtype=torch.uint8, device=device)
 
 
@@ -583,6 +591,7 @@ def _norm_rows(x: torch.Tensor):
     if x.dtype not in _DTYPES:
         raise ValueError(f"rows must be bfloat16, float16 or float32, got {x.dtype}")
     dev = _cuda_index("x", x)
+    _sizes(*x.shape)
     return (1,) * (4 - dim) + tuple(x.shape), dev
 
 
@@ -649,6 +658,7 @@ def layer_norm_fwd(x: torch.Tensor, weight: torch.Tensor | None = None, bias: to
 def layer_norm_bwd_workspace(x_shape, device) -> torch.Tensor:
     """Scratch for layer_norm_bwd of rows of this shape; calls on different streams need one each."""
     shape = (1,) * (4 - len(x_shape)) + tuple(x_shape)
+    _sizes(*shape)
     return torch.empty(lib().layer_norm_bwd_workspace_size(*shape), dtype=torch.uint8, device=device)
 
 
