@@ -480,7 +480,8 @@ typedef enum { ATTN_BF16 = 0, ATTN_F16 = 1, ATTN_F32 = 2 } attn_dtype;
  *   x, y    : dtype [B, S, H, N], element strides x_str / y_str (batch, sequence, head), channel
  *             stride 1.  Any stride and alignment of the type; 16-byte accesses are used where
  *             pointers, strides and N allow them, or all rows are equally far apart and x's and y's as
- *             far from 16 bytes.  x may have strides of 0; y may be x itself.
+ *             far from 16 bytes.  x may have strides of 0; y may be x itself (pointer and strides), and
+ *             overlaps it nowhere otherwise.
  *   weight, bias : w_dtype [N], each or NULL (1 and 0).  w_dtype is dtype or ATTN_F32.
  *   mean, rstd : float [B, S, H] outputs, contiguous
  *   eps     : finite, >= 0;  1 <= N <= 16384;  B * S * H <= 2^30 rows (0: nothing is done)
@@ -500,7 +501,8 @@ ATTN_API size_t layer_norm_bwd_workspace_size(int B, int S, int H, int N);
  *   dy, x   : dtype [B, S, H, N], strides dy_str / x_str (strides of 0 allowed)
  *   weight  : as given to the forward, or NULL
  *   mean, rstd : as the forward wrote them
- *   dx      : dtype [B, S, H, N] output, strides dx_str; may be dy itself
+ *   dx      : dtype [B, S, H, N] output, strides dx_str; may be dy itself or x itself (pointer and strides),
+ *             and overlaps them nowhere otherwise
  *   dweight, dbias : w_dtype [N] outputs, both or neither (zeros when there are no rows)
  *   workspace : at least layer_norm_bwd_workspace_size(B, S, H, N) bytes, 16-byte aligned; may be
  *             NULL when dweight and dbias are

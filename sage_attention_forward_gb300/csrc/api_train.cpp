@@ -1,5 +1,6 @@
 // C ABI of the training operators (declared in include/sageattn.h): argument validation, TMA tensor
 // maps and kernel launches.  No allocation happens here.
+#include <algorithm>
 #include <cmath>
 
 #include "../../include/sageattn.h"
@@ -7,6 +8,76 @@
 #include "kernels.h"
 
 using namespace sa::api;
+
+// ------------------------------------------------------------------ tensors that share memory
+namespace {
+
+// Rows of `row` bytes from ptr on, ext[i] of them str[i] bytes apart in dimension i.
+struct Rows {
+  uintptr_t ptr;
+  long long ext[3], str[3], row, span;   // span: bytes from the first row's start to the last one's end, or 0
+};
+Rows rows_of(const void* ptr, int B, int S, int H, int n, int size, const long long str[3]) {
+  Rows r = {reinterpret_cast<uintptr_t>(ptr), {B, S, H}, {}, (long long)n * size, 0};
+  double span = 0;
+  for (int i = 0; i < 3; ++i) {
+    r.str[i] = r.ext[i] > 1 ? str[i] * size : 0;
+    span += (double)(r.ext[i] - 1) * (double)r.str[i];
+  }
+  // (larger than any memory: nothing to compare, and nothing below overflows)
+  if (span < 0x1p56) r.span = (r.ext[0] - 1) * r.str[0] + (r.ext[1] - 1) * r.str[1] + (r.ext[2] - 1) * r.str[2] + r.row;
+  return r;
+}
+bool same(const Rows& a, const Rows& b) {
+  return a.ptr == b.ptr && std::equal(a.str, a.str + 3, b.str) && std::equal(a.ext, a.ext + 3, b.ext) && a.row == b.row;
+}
+
+// Whether `at` plus a sum of multiples of steps[0..n), largest step first, each multiple in its range, can come to between
+// -room and room.  steps_left bounds the search: slices of one buffer, whose steps lie within one another, take
+// two or three tries a step.  (Undecided is taken for no.)
+struct Step {
+  long long by, lo, hi;
+};
+bool meets(const Step* steps, int n, long long at, long long room, int& steps_left) {
+  if (n == 0) return -room < at && at < room;
+  long long lo = 0, hi = 0;   // what the steps after this one can add
+  for (int i = 1; i < n; ++i) {
+    lo += steps[i].by * steps[i].lo;
+    hi += steps[i].by * steps[i].hi;
+  }
+  auto down = [](long long a, long long b) { return a / b - (a % b < 0 ? 1 : 0); };
+  const long long first = std::max(steps->lo, -down(at + hi + room - 1, steps->by));
+  const long long last = std::min(steps->hi, down(room - 1 - at - lo, steps->by));
+  for (long long x = first; x <= last; ++x) {
+    if (--steps_left < 0) return false;
+    if (meets(steps + 1, n - 1, at + x * steps->by, room, steps_left)) return true;
+  }
+  return false;
+}
+
+// Whether a row of a and a row of b (of one length) have a byte in common.
+bool share_memory(const Rows& a, const Rows& b) {
+  if (a.span == 0 || b.span == 0 || a.ptr + a.span <= b.ptr || b.ptr + b.span <= a.ptr) return false;
+  Step steps[6];
+  int n = 0;
+  auto add = [&](long long by, long long lo, long long hi) {
+    if (by == 0) return;
+    int i = 0;
+    while (i < n && steps[i].by != by) ++i;
+    if (i == n) steps[n++] = {by, 0, 0};
+    steps[i].lo += lo;
+    steps[i].hi += hi;
+  };
+  for (int i = 0; i < 3; ++i) {
+    add(a.str[i], 1 - a.ext[i], 0);
+    add(b.str[i], 0, b.ext[i] - 1);
+  }
+  std::sort(steps, steps + n, [](const Step& x, const Step& y) { return x.by > y.by; });
+  int steps_left = 10000;
+  return meets(steps, n, (long long)(b.ptr - a.ptr), a.row, steps_left);
+}
+
+}  // namespace
 
 extern "C" {
 
@@ -63,7 +134,10 @@ attn_status attn_fwd_bf16_lse(const void* q, const void* k, const void* v, void*
   TRY(check_strides("v", v, v_str, B, Sk, Hkv, vs));
   TRY(check_strides("o", o, o_str, B, Sq, Hq, os));
   TRY(check_buffer("lse", lse));
-  if (o == q || o == k || o == v) return fail(ATTN_ERR_INVALID_ARG, "attn_fwd_bf16_lse: o must overlap no input");
+  const Rows o_rows = rows_of(o, B, Sq, Hq, D, 2, os);
+  if (share_memory(o_rows, rows_of(q, B, Sq, Hq, D, 2, qs)) || share_memory(o_rows, rows_of(k, B, Sk, Hkv, D, 2, ks)) ||
+      share_memory(o_rows, rows_of(v, B, Sk, Hkv, D, 2, vs)))
+    return fail(ATTN_ERR_INVALID_ARG, "attn_fwd_bf16_lse: o must overlap no input");
   TRY(check_device());
   TRY(get_encoder());
   CUtensorMap tq, tk, tv, to;
@@ -106,8 +180,14 @@ attn_status attn_bwd_bf16(const void* dout, const void* q, const void* k, const 
   TRY(check_buffer("lse", lse));
   TRY(check_buffer("workspace", workspace));
   // dK and dV are formed from the inputs after dQ has been written
-  bool shared = dq == dk || dq == dv || dk == dv;
-  for (const void* in : {dout, q, k, v, o}) shared = shared || dq == in || dk == in || dv == in;
+  const Rows out[3] = {rows_of(dq, B, Sq, Hq, D, 2, t.dq_str), rows_of(dk, B, Sk, Hkv, D, 2, t.dk_str),
+                       rows_of(dv, B, Sk, Hkv, D, 2, t.dv_str)};
+  const Rows in[5] = {rows_of(dout, B, Sq, Hq, D, 2, ds), rows_of(q, B, Sq, Hq, D, 2, qs),
+                      rows_of(k, B, Sk, Hkv, D, 2, ks), rows_of(v, B, Sk, Hkv, D, 2, vs),
+                      rows_of(o, B, Sq, Hq, D, 2, os)};
+  bool shared = share_memory(out[0], out[1]) || share_memory(out[0], out[2]) || share_memory(out[1], out[2]);
+  for (const Rows& x : out)
+    for (const Rows& y : in) shared = shared || share_memory(x, y);
   if (shared)
     return fail(ATTN_ERR_INVALID_ARG, "attn_bwd_bf16: dq, dk and dv must overlap neither the inputs nor one another");
   const size_t need = sa::attn_bwd_workspace(a);
@@ -199,6 +279,10 @@ attn_status layer_norm_fwd(const void* x, const void* weight, const void* bias, 
   a.eps = eps;
   long long ys[3];
   TRY(check_rows("y", y, dtype, y_str, a, false, ys));
+  const int size = dtype == ATTN_F32 ? 4 : 2;
+  const Rows x_rows = rows_of(x, B, S, H, N, size, a.x_str), y_rows = rows_of(y, B, S, H, N, size, ys);
+  if (!same(x_rows, y_rows) && share_memory(x_rows, y_rows))
+    return fail(ATTN_ERR_INVALID_ARG, "layer_norm_fwd: y must be x itself or overlap it nowhere");
   TRY(check_device());
   cudaError_t e = sa::launch_layer_norm_fwd(a, y, ys, (cudaStream_t)stream);
   if (e != cudaSuccess) return fail_cuda(e, "layer_norm_fwd launch");
@@ -243,6 +327,11 @@ attn_status layer_norm_bwd(const void* dy, const void* x, const void* weight, co
     if (workspace_bytes < need)
       return fail(ATTN_ERR_INVALID_ARG, "layer_norm_bwd: workspace_bytes=%zu < %zu required", workspace_bytes, need);
   }
+  const int size = dtype == ATTN_F32 ? 4 : 2;
+  const Rows dx_rows = rows_of(dx, B, S, H, N, size, xs);
+  for (const Rows& in : {rows_of(dy, B, S, H, N, size, ds), rows_of(x, B, S, H, N, size, a.x_str)})
+    if (!same(dx_rows, in) && share_memory(dx_rows, in))
+      return fail(ATTN_ERR_INVALID_ARG, "layer_norm_bwd: dx must be dy or x itself or overlap them nowhere");
   TRY(check_device());
   cudaError_t e = sa::launch_layer_norm_bwd(a, dy, ds, dx, xs, dweight, dbias, reinterpret_cast<float*>(workspace),
                                             (cudaStream_t)stream);

@@ -1,0 +1,24 @@
+"""Calls of the training operators that the documentation allows and the other tests do not make."""
+import pytest
+import torch
+
+import sage_attention_forward_gb300 as sa
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("rows,N", [(700, 128), (300, 129), (400, 1000), (900, 1773), (700, 5120), (320, 9000), (200, 12288),
+                                    (40, 16384)])
+def test_layer_norm_gradient_over_its_input(cuda_dev, rows, N, dtype):
+    """dx in x's place: the same bits as in a tensor of its own."""
+    g = torch.Generator(device=cuda_dev).manual_seed(N)
+    x, dy = (torch.randn((rows, N), generator=g, device=cuda_dev).to(dtype) for _ in range(2))
+    w = torch.randn(N, generator=g, device=cuda_dev).to(dtype)
+    _, mean, rstd = sa.layer_norm_fwd(x, w, w)
+    want = sa.layer_norm_bwd(dy, x, w, mean, rstd)
+    x2 = x.clone()
+    got = sa.layer_norm_bwd(dy, x2, w, mean, rstd, dx=x2)
+    torch.cuda.synchronize()
+    sa.attn_get_device_status()
+    assert got[0] is x2 and all(torch.equal(a, b) for a, b in zip(got, want))
