@@ -434,12 +434,14 @@ def _elsewhere(dev: int, stream) -> bool:
 def _there(dev: int, stream):
     """Makes device `dev` and, when the caller names one, `stream` current: what the call allocates then
     belongs to the stream that its kernels run on."""
+    if isinstance(stream, torch.cuda.Stream) and stream.device.index != dev:
+        raise ValueError(f"stream is on {stream.device}, the tensors are on cuda:{dev}")
     with torch.cuda.device(dev):
         if stream is None:
             yield
         else:
-            if not hasattr(stream, "cuda_stream"):
-                stream = torch.cuda.ExternalStream(int(stream), device=dev)
+            if not isinstance(stream, torch.cuda.Stream):
+                stream = torch.cuda.ExternalStream(getattr(stream, "cuda_stream", stream), device=dev)
             with torch.cuda.stream(stream):
                 yield
 

@@ -22,3 +22,25 @@ def test_layer_norm_gradient_over_its_input(cuda_dev, rows, N, dtype):
     torch.cuda.synchronize()
     sa.attn_get_device_status()
     assert got[0] is x2 and all(torch.equal(a, b) for a, b in zip(got, want))
+
+
+def test_streams_by_handle(cuda_dev):
+    """A stream as torch's object, as its handle, as another library's object, and the default stream's handle."""
+    class Other:
+        def __init__(self, handle):
+            self.cuda_stream = handle
+
+    g = torch.Generator(device=cuda_dev).manual_seed(3)
+    q, k, v, d = (torch.randn((1, 200, 2, 128), generator=g, device=cuda_dev).to(torch.bfloat16) for _ in range(4))
+    s = torch.cuda.Stream()
+    results = []
+    for stream in (None, s, s.cuda_stream, Other(s.cuda_stream), 0):
+        torch.cuda.synchronize()
+        y, mean, rstd = sa.layer_norm_fwd(q, stream=stream)
+        o, lse = sa.attn_fwd_bf16_lse(y, k, v, stream=stream)
+        grads = sa.attn_bwd_bf16(d, y, k, v, o, lse, stream=stream)
+        dx, _, _ = sa.layer_norm_bwd(grads[0], q, None, mean, rstd, stream=stream)
+        torch.cuda.synchronize()
+        results.append((y, mean, rstd, o, lse, *grads, dx))
+    for r in results[1:]:
+        assert all(torch.equal(a, b) for a, b in zip(r, results[0]))

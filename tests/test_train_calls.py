@@ -55,3 +55,24 @@ def test_ordinary_sizes_reach_the_library(on_meta):
     q = meta(1, 5, 2, 128)
     with pytest.raises(sa.AttnError, match="q is NULL"):
         sa.attn_fwd_bf16_lse(q, q, q, out=q, lse=meta(1, 2, 5, dtype=torch.float32))
+
+
+class OtherDevicesStream:
+    """What the binding looks at of a stream, without a GPU."""
+    device = torch.device("cuda", 1)
+    cuda_stream = 4096
+
+
+@pytest.mark.parametrize("call", ["layer_norm_fwd", "layer_norm_bwd", "attn_fwd_bf16_lse", "attn_bwd_bf16"])
+def test_a_stream_of_another_device(monkeypatch, call):
+    """torch makes a stream's device current with it, and the call would run on some stream of the tensors' device."""
+    monkeypatch.setattr(sa, "_cuda_index", lambda name, t: 0)
+    monkeypatch.setattr(sa, "_expect", lambda *a: None)
+    monkeypatch.setattr(torch.cuda, "current_device", lambda: 0)
+    monkeypatch.setattr(torch.cuda, "Stream", OtherDevicesStream)
+    q = meta(1, 5, 2, 128)
+    lse = meta(1, 2, 5, dtype=torch.float32)
+    args = {"layer_norm_fwd": (q,), "layer_norm_bwd": (q, q, None, lse, lse), "attn_fwd_bf16_lse": (q, q, q),
+            "attn_bwd_bf16": (q, q, q, q, q, lse)}[call]
+    with pytest.raises(ValueError, match="stream is on cuda:1"):
+        getattr(sa, call)(*args, stream=OtherDevicesStream())
