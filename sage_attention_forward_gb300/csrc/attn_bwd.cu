@@ -60,6 +60,7 @@ constexpr float kHot = 0.51f;        // (dq_kernel) a key with more of a row's p
 constexpr float kLeastSum = 1e-6f;   // (dq_kernel) of a row's probabilities in a tile, to be divided by
 
 __device__ uint32_t g_err_bwd;
+std::atomic<bool> g_launched{false};
 
 __device__ __forceinline__ float u2f(uint32_t u) { return __uint_as_float(u); }
 
@@ -1208,6 +1209,7 @@ cudaError_t launch_attn_bwd_bf16(const CUtensorMap& tm_q, const CUtensorMap& tm_
     p.s0[i] = t.dq_str[i];
     p.s1[i] = 0;
   }
+  g_launched.store(true, std::memory_order_relaxed);
   e = launch_dependent(dq_kernel, dim3((unsigned)p.order.items), kThreads, kSmemQ, stream, tm_q, tm_k, tm_v, tm_d,
                        tm_o, p);
   if (e != cudaSuccess) return e;
@@ -1232,12 +1234,7 @@ cudaError_t launch_attn_bwd_bf16(const CUtensorMap& tm_q, const CUtensorMap& tm_
   return launch_dependent(join_kernel, dim3((unsigned)(p.order.items * kJoinBlocks)), kJoinThreads, 0, stream, p);
 }
 
-static cudaError_t read_and_clear_err_bwd(uint32_t* out) {
-  cudaError_t e = cudaMemcpyFromSymbol(out, g_err_bwd, sizeof(uint32_t));
-  if (e != cudaSuccess) return e;
-  const uint32_t zero = 0;
-  return cudaMemcpyToSymbol(g_err_bwd, &zero, sizeof(uint32_t));
-}
-static const bool err_reader_added = add_err_reader(read_and_clear_err_bwd);
+static const bool err_reader_added =
+    add_err_reader([](uint32_t* out) { return read_and_clear_err(g_err_bwd, g_launched, out); });
 
 }  // namespace sa

@@ -56,6 +56,7 @@ struct __align__(1024) Smem {
 constexpr int kAskAhead = 4;
 
 __device__ uint32_t g_err_lse;
+std::atomic<bool> g_launched{false};
 
 struct Params {
   Mask mask;
@@ -454,16 +455,12 @@ cudaError_t launch_attn_fwd_bf16_lse(const CUtensorMap& tm_q, const CUtensorMap&
   p.by_Hq = make_div(a.Hq);
   p.by_group = make_div(p.group);
   p.order = make_order((a.Sq + kNQ * kTile - 1) / (kNQ * kTile), a.B * a.Hq, a.causal);
+  g_launched.store(true, std::memory_order_relaxed);
   return launch_dependent(lse_fwd_kernel, dim3((unsigned)p.order.items), kThreads, kSmemBytes, stream, tm_q, tm_k, tm_v,
                           tm_o, p);
 }
 
-static cudaError_t read_and_clear_err_lse(uint32_t* out) {
-  cudaError_t e = cudaMemcpyFromSymbol(out, g_err_lse, sizeof(uint32_t));
-  if (e != cudaSuccess) return e;
-  const uint32_t zero = 0;
-  return cudaMemcpyToSymbol(g_err_lse, &zero, sizeof(uint32_t));
-}
-static const bool err_reader_added = add_err_reader(read_and_clear_err_lse);
+static const bool err_reader_added =
+    add_err_reader([](uint32_t* out) { return read_and_clear_err(g_err_lse, g_launched, out); });
 
 }  // namespace sa

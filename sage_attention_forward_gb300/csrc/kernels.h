@@ -3,6 +3,7 @@
 
 #include <cuda.h>
 #include <cuda_runtime.h>
+#include <atomic>
 #include <cstddef>
 #include <cstdint>
 #include <mutex>
@@ -83,6 +84,18 @@ cudaError_t read_and_clear_err_attn(uint32_t* out);
 // Other translation units with bounded waits add the reader of their error word when the library is loaded.
 using ErrReader = cudaError_t (*)(uint32_t* out);
 bool add_err_reader(ErrReader read);
+// Reads such a word, and clears it if it is set.  launched: a kernel that may set it has been launched; until then there is
+// nothing to read, and reading it would load the unit's kernels (the first status call 58 us, with three more
+// units' words read 1770; later ones 18 and 56).
+template <class Word>
+cudaError_t read_and_clear_err(Word& word, const std::atomic<bool>& launched, uint32_t* out) {
+  *out = 0;
+  if (!launched.load(std::memory_order_relaxed)) return cudaSuccess;
+  cudaError_t e = cudaMemcpyFromSymbol(out, word, sizeof(uint32_t));
+  if (e != cudaSuccess || *out == 0) return e;
+  const uint32_t zero = 0;
+  return cudaMemcpyToSymbol(word, &zero, sizeof(uint32_t));
+}
 
 // Sage prepare (sage_prepare.cu)
 struct PrepareArgs {

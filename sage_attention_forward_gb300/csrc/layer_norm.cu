@@ -449,6 +449,7 @@ struct RowRing {
   uint32_t abort_flag;
 };
 __device__ uint32_t g_err_norm;
+std::atomic<bool> g_launched{false};   // a kernel with a ring
 
 __device__ __forceinline__ void ring_init(RowRing& r) {
   if (threadIdx.x == 0) {
@@ -899,6 +900,7 @@ cudaError_t launch_ring(LnParams& q, const Shape& s, cudaStream_t stream) {
   const size_t row = q.slot;
   const int per_sm = s.wide ? 1 : 65536 / (96 * s.threads);
   q.ring = 6 * row * per_sm <= (size_t)kRingBytes ? 3 : 2;
+  g_launched.store(true, std::memory_order_relaxed);
   return launch_dependent(kernel, dim3((unsigned)s.ctas), s.threads, kBackward ? 2 * q.ring * row : 4 * row, stream, q);
 }
 // shift: all rows of a tensor are equally far apart, and all tensors start at one distance from 16 bytes.  s: its CTAs
@@ -1019,12 +1021,7 @@ cudaError_t launch_layer_norm_bwd(const LayerNormArgs& a, const void* dy, const 
                           static_cast<const float*>(workspace), s.ctas, p.N, dw, db, a.w_type);
 }
 
-static cudaError_t read_and_clear_err_norm(uint32_t* out) {
-  cudaError_t e = cudaMemcpyFromSymbol(out, g_err_norm, sizeof(uint32_t));
-  if (e != cudaSuccess) return e;
-  const uint32_t zero = 0;
-  return cudaMemcpyToSymbol(g_err_norm, &zero, sizeof(uint32_t));
-}
-static const bool err_reader_added = add_err_reader(read_and_clear_err_norm);
+static const bool err_reader_added =
+    add_err_reader([](uint32_t* out) { return read_and_clear_err(g_err_norm, g_launched, out); });
 
 }  // namespace sa
