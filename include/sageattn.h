@@ -446,9 +446,13 @@ ATTN_API size_t attn_bwd_bf16_workspace_size(int B, int Sq, int Sk, int Hq, int 
  *   dq_i     = softmax_scale sum_j ds[i, j] k_j
  * sums over i also over the query heads that share a key head.  Rows without a key have dq = 0; keys that no
  * query sees have dk = dv = 0; a row with one key has ds = 0.
- *   dout    : BF16 [B, Sq, Hq, 128], finite, strides dout_str (positive, as all of these tensors')
+ *   dout    : BF16 [B, Sq, Hq, 128], finite, strides dout_str (positive, as all of these tensors': the
+ *             expanded gradient of a plain sum has to be made a tensor of its own first)
  *   q, k, v, softmax_scale, causal, kv_len : as given to the forward
- *   o, lse  : as the forward wrote them
+ *   o, lse  : as the forward wrote them, from these keys: a row's probabilities add up to 1, and dq and dk
+ *             rely on it (the sum of a row of ds is made 0, delta formed from it).  An o and lse merged from
+ *             calls over parts of the keys, with each part's gradients taken by a call of its own, give wrong
+ *             dq and dk; nothing here can tell.
  *   dq      : BF16 [B, Sq, Hq, 128] output; dk, dv : BF16 [B, Sk, Hkv, 128] outputs, every row
  *             written; they overlap neither the inputs nor one another
  *   workspace : at least attn_bwd_bf16_workspace_size(B, Sq, Sk, Hq, Hkv) bytes, 16-byte

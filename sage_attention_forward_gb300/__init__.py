@@ -550,7 +550,8 @@ def attn_bwd_bf16(dout: torch.Tensor, q: torch.Tensor, k: torch.Tensor, v: torch
                   stream=None) -> tuple[torch.Tensor, torch.Tensor, torch.Tensor]:
     """(dQ, dK, dV) of attn_fwd_bf16_lse: dout is the gradient of its O; out and lse are what it returned,
     the other arguments those it was given.  dK and dV are sums over the query heads that share a key head.
-    The same inputs give the same bits."""
+    The same inputs give the same bits.  An out and lse merged from calls over parts of the keys are not accepted
+    (each row's probabilities have to add up to 1 over the keys given); an expanded dout (a stride of 0) is refused."""
     B, Sq, Sk, Hq, Hkv, D, dev = _train_shapes(q, k, v, kv_len)
     if _elsewhere(dev, stream):
         with _there(dev, stream):
