@@ -648,6 +648,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     sm.abort_flag = 0;
     fence_mbar_init();
   }
+  // (a key of the tensor at all times: an lse that is not the forward's can make a row's sum look as if it had one)
+  if (threadIdx.x < kTile) sm.hot[threadIdx.x] = 0;
   if (warp == kWarpMma) {
     tmem_alloc(&sm.tmem_base, 512);
     tmem_relinquish();

@@ -44,3 +44,19 @@ def test_streams_by_handle(cuda_dev):
         results.append((y, mean, rstd, o, lse, *grads, dx))
     for r in results[1:]:
         assert all(torch.equal(a, b) for a, b in zip(r, results[0]))
+
+
+@pytest.mark.parametrize("value", [0.0, -30.0, -1e4, 40.0, float("inf"), float("nan")])
+@pytest.mark.parametrize("Sq,Sk", [(300, 700), (500, 128), (5, 3)])
+def test_an_lse_of_another_call(cuda_dev, Sq, Sk, value):
+    """Not the forward's: the gradients may be anything then, but they come, and the next call's are right."""
+    g = torch.Generator(device=cuda_dev).manual_seed(4)
+    r = lambda *s: torch.randn(s, generator=g, device=cuda_dev).to(torch.bfloat16)   # noqa: E731
+    q, k, v, d = r(2, Sq, 4, 128), r(2, Sk, 2, 128), r(2, Sk, 2, 128), r(2, Sq, 4, 128)
+    o, lse = sa.attn_fwd_bf16_lse(q, k, v)
+    want = sa.attn_bwd_bf16(d, q, k, v, o, lse)
+    sa.attn_bwd_bf16(d, q, k, v, o, torch.full_like(lse, value))
+    got = sa.attn_bwd_bf16(d, q, k, v, o, lse)
+    torch.cuda.synchronize()
+    sa.attn_get_device_status()
+    assert all(torch.equal(a, b) for a, b in zip(got, want))
