@@ -1127,8 +1127,8 @@ static_assert(kSmemKV <= 232448 && kSmemQ <= 232448, "227 KB of shared memory pe
 // results), the parts' sums 0.027 each to write and read, the kernel that joins them two.  The
 // products' own time is at least an SM's share of them all, and, as the longest items start
 // first, k + 1 times the length of item 152 k: one SM has that many as long.  Backward with 1 part and
-// with the parts chosen: 96 units of 132 products 350 and 303 us (3 parts); 16 of 64: 107 and 39 (9); 8 of 128:
-// 224 and 70 (19); causal, 64 of up to 128: 223 and 105 (4); 256 of up to 128: 332, and 344 with 2, so 1.
+// with the parts chosen: 96 units of 132 products 352 and 312 us (3 parts); 16 of 64: 104 and 40 (9); 8 of 128:
+// 185 and 44 (19); causal, 64 of up to 128: 212 and 109 (4); 256 of up to 128: 342, and 4 % more with 2, so 1.
 constexpr int kSms = 152, kMostRounds = 8;
 int kv_parts(const TrainArgs& a) {
   const int tiles = (a.Sk + kTile - 1) / kTile, n_q = (a.Sq + kTile - 1) / kTile, group = a.Hq / a.Hkv;

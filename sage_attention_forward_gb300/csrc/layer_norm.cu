@@ -437,9 +437,10 @@ __global__ void __launch_bounds__(kMax) ln_bwd_kernel(const LnParams p) {
 }
 
 // ------------------------------------------------------------------ rows of a CTA through shared memory
-// Rows that a CTA takes, of up to 10240 channels (in the backward up to 16384), that allow 16-byte
-// accesses: one thread copies whole rows ahead into a ring in shared memory (16 channels a thread are too few bytes under way otherwise: with the next row
-// in registers the forward reached 3.3 and the backward 2.1 of 6.7 TB/s).
+// Rows that a CTA takes, of up to 10240 channels (in the backward up to 16384, in FP32 up to 14080: two rows of x and dy
+// have to fit), that allow 16-byte accesses: one thread copies whole rows ahead into a ring in shared memory (16 channels
+// a thread are too few bytes under way otherwise: with the next row in registers the forward reached 3.3 and the
+// backward 2.1 of 6.7 TB/s).
 // The forward works on two rows at once (their sums share barriers and shuffles' latency) with the next
 // two under way; the backward, which reads its rows twice, on one of three, or of two where three would
 // leave room for fewer CTAs.
