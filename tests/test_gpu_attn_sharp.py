@@ -75,3 +75,20 @@ def test_strided_keys(cuda_dev):
     assert float((ref.p[..., 128:].amax(-1) > 0.5).double().mean()) > 0.5
     heads_first = x.permute(2, 0, 3, 1, 4).contiguous().permute(1, 3, 0, 2, 4)   # [.., S, 3, H, D] by heads
     check(heads_first[:, :, 0], heads_first[:, :, 1], heads_first[:, :, 2], d)
+
+
+def test_keys_past_32_bits(cuda_dev):
+    """K's rows 2^31 and more elements after its first: the same bits as from a tensor of its own."""
+    x, _, _, d = bf(*make(cuda_dev, 2, 300, 300, 2, 2, 16))
+    far = (1 << 31) + 256
+    store = torch.empty(far + x[0].numel(), dtype=torch.bfloat16, device=cuda_dev)
+    k = store.as_strided(x.shape, (far, *x.stride()[1:]), 0)
+    k.copy_(x)
+    o, lse = sa.attn_fwd_bf16_lse(x, k, x)
+    got = sa.attn_bwd_bf16(d, x, k, x, o, lse)
+    want = sa.attn_bwd_bf16(d, x, x, x, *sa.attn_fwd_bf16_lse(x, x, x))
+    torch.cuda.synchronize()
+    sa.attn_get_device_status()
+    assert all(torch.equal(a, b) for a, b in zip(got, want))
+    ref = Reference(x, x, x)
+    assert float((ref.p[:, :, 128:, 128:].amax(-1) > 0.5).double().mean()) > 0.5
