@@ -162,11 +162,11 @@ def frequencies(case):
 
 
 def places(case, g):
-    """int32 positions: [B, S] of consecutive tokens, or [S, 3] of a grid of frames, rows and columns."""
+    """int32 positions: [B, S] of consecutive tokens, or [1, S, 3] of a grid of frames, rows and columns."""
     s = torch.arange(case["S"], device="cuda", dtype=torch.int32)
     if case["axes"]:
         side = max(1, int(math.sqrt(case["S"] / 4)))
-        return torch.stack([s // (side * side), s // side % side, s % side], dim=-1).contiguous()
+        return torch.stack([s // (side * side), s // side % side, s % side], dim=-1)[None]
     first = torch.zeros((case["B"], 1), dtype=torch.int32, device="cuda")
     if case["start"]:
         first = torch.randint(0, case["start"], (case["B"], 1), generator=g, device="cuda", dtype=torch.int32)
@@ -275,8 +275,6 @@ def cos_sin(state):
     """[B or 1, S, 1, R / 2] in 32 bits, from angles in 64."""
     pos, w = state["pos"].double(), state["w"]
     angle = pos.index_select(-1, state["axis"]) * w if state["case"]["axes"] else pos[..., None] * w
-    if angle.dim() == 2:
-        angle = angle[None]
     m = state["magnitude"]
     return (angle.cos() * m).float()[:, :, None], (angle.sin() * m).float()[:, :, None]
 
@@ -405,7 +403,7 @@ def turned(x, state, sign):
     if pos.dim() == 2 and not case["axes"]:
         angle = torch.einsum("bs,r->bsr", pos, state["w"])
     else:
-        angle = torch.stack([pos[:, a] for a in state["axis"].tolist()], dim=-1)[None] * state["w"]
+        angle = torch.stack([pos[0, :, a] for a in state["axis"].tolist()], dim=-1)[None] * state["w"]
     e = torch.polar(torch.full_like(angle, state["magnitude"]), sign * angle)[:, :, None]
     head = x[..., :case["R"]]
     if case["interleaved"]:
