@@ -35,6 +35,9 @@
  * formed again), layer_norm_fwd and layer_norm_bwd (over head channels or tokens,
  * with the gradients of weight and bias).
  *
+ * Between a projection and attention: rope_fwd, rope_bwd (rotary positions), qk_norm_rope_fwd and qk_norm_rope_bwd
+ * (the norm of each head of Q and K with the rotation in the same pass).
+ *
  * Beyond those: sage_prepare_smooth_k (K smoothing before the INT8
  * quantisation), sage_prepare_smoothed with sage_attn_fwd_smooth_q and
  * sage_attn_fwd_pv16_smooth_q (Q smoothing with its correction term) and
@@ -518,6 +521,80 @@ ATTN_API attn_status layer_norm_bwd(const void* dy, const void* x, const void* w
                                     int N, const int64_t dy_str[3], const int64_t x_str[3], const int64_t dx_str[3],
                                     int dtype, int w_dtype, void* workspace, size_t workspace_bytes,
                                     attn_stream_t stream);
+
+/*
+ * rope_fwd -- rotary positions of Q and K, out of place or in place.  Of each head's N channels the first rope_dim
+ * are rotated in pairs, the others pass through:
+ *   half (interleaved = 0)   pair i is channels (i, i + rope_dim / 2)
+ *   interleaved = 1          pair i is channels (2 i, 2 i + 1)
+ *   (a, b) -> magnitude (a cos t - b sin t, b cos t + a sin t),  t = 2 pi freq[i] position / 2^64
+ *   q, k    : dtype [B, S, Hq, N] and [B, S, Hk, N], element strides q_str / k_str (batch, sequence, head), channel
+ *             stride 1; any alignment of the type, strides of 0 allowed.  Hq or Hk may be 0 (its pointers are not
+ *             looked at).  16-byte accesses are used where pointers and strides allow them, N is a multiple of
+ *             16 and, in the half layout, rope_dim is one.
+ *   q_out, k_out : the same shapes, strides qo_str / ko_str; each may be its input itself (pointer and strides) and
+ *             overlaps no tensor otherwise
+ *   pos     : device int32 positions of (batch, token, axis), element strides pos_str (0 where one row serves all), or
+ *             NULL: the token's place in the sequence.  Any int32, negative ones too.
+ *   axes    : position axes in pos, 1 to 4 (video: frame, row, column)
+ *   freq    : device uint64 [rope_dim / 2]: turns a position times 2^64, rounded, modulo 2^64; the two lowest bits are
+ *             the pair's axis (an axis past the last one is the last).  The product with a position wraps to the angle's
+ *             fraction of a turn, off by at most 2^-31 turns for every int32 position.
+ *   magnitude : finite factor of cosine and sine (1, or the attention factor of a scaled rotation)
+ *   1 <= N <= 512, rope_dim even, 0 <= rope_dim <= N, B * S * (Hq + Hk) <= 2^30 rows (0: nothing is done)
+ * FP32 between load and store, each result rounded once.  Enqueues one kernel on `stream`.
+ */
+ATTN_API attn_status rope_fwd(const void* q, const void* k, void* q_out, void* k_out, int B, int S, int Hq, int Hk, int N,
+                              const int64_t q_str[3], const int64_t k_str[3], const int64_t qo_str[3],
+                              const int64_t ko_str[3], const int32_t* pos, const int64_t pos_str[3], int axes,
+                              const uint64_t* freq, int rope_dim, int interleaved, float magnitude, int dtype,
+                              attn_stream_t stream);
+
+/* rope_bwd -- the gradients of rope_fwd: the rotation by the negated angles.  Arguments as rope_fwd. */
+ATTN_API attn_status rope_bwd(const void* dq_out, const void* dk_out, void* dq, void* dk, int B, int S, int Hq, int Hk,
+                              int N, const int64_t dqo_str[3], const int64_t dko_str[3], const int64_t dq_str[3],
+                              const int64_t dk_str[3], const int32_t* pos, const int64_t pos_str[3], int axes,
+                              const uint64_t* freq, int rope_dim, int interleaved, float magnitude, int dtype,
+                              attn_stream_t stream);
+
+/*
+ * qk_norm_rope_fwd -- the norm of each head of Q and K and its rotation in one pass:
+ *   r = 1 / sqrt(sum x^2 / N + eps),  y = rope(x r weight)
+ *   q_weight, k_weight : w_dtype [N], each or NULL (1).  w_dtype is dtype or ATTN_F32.
+ *   eps     : finite, >= 0
+ *   the rest as rope_fwd (rope_dim = 0: the norm alone, freq and pos are not looked at)
+ * FP32 between load and store, each result rounded once.  Enqueues one kernel on `stream`.
+ */
+ATTN_API attn_status qk_norm_rope_fwd(const void* q, const void* k, const void* q_weight, const void* k_weight,
+                                      void* q_out, void* k_out, int B, int S, int Hq, int Hk, int N,
+                                      const int64_t q_str[3], const int64_t k_str[3], const int64_t qo_str[3],
+                                      const int64_t ko_str[3], float eps, const int32_t* pos, const int64_t pos_str[3],
+                                      int axes, const uint64_t* freq, int rope_dim, int interleaved, float magnitude,
+                                      int dtype, int w_dtype, attn_stream_t stream);
+
+/* qk_norm_rope_bwd_workspace_size -- bytes of device scratch qk_norm_rope_bwd needs for the weights' gradients. */
+ATTN_API size_t qk_norm_rope_bwd_workspace_size(int B, int S, int Hq, int Hk, int N);
+
+/*
+ * qk_norm_rope_bwd -- the gradients of qk_norm_rope_fwd, with g = dy rotated back and xhat = x r (r is formed again):
+ *   dx = r (g weight - xhat sum(g weight xhat) / N),   dweight = sum over rows of g xhat
+ *   dq_out, dk_out, q, k : dtype [B, S, H, N], strides as rope_fwd's inputs
+ *   q_weight, k_weight, eps, pos, freq, ... : as given to the forward
+ *   dq, dk  : outputs; each may be its own dq_out (dk_out) or q (k) itself and overlaps no tensor otherwise
+ *   dq_weight, dk_weight : w_dtype [N] outputs, each or NULL (zeros where there are no rows)
+ *   workspace : at least qk_norm_rope_bwd_workspace_size(B, S, Hq, Hk, N) bytes, 16-byte aligned; overwritten; one for
+ *             each call under way; may be NULL when both weight gradients are
+ * FP32 throughout, sums over rows in a fixed order (the same inputs give the same bits); each result is rounded
+ * once.  Enqueues one kernel on `stream`, two with a weight's gradient.
+ */
+ATTN_API attn_status qk_norm_rope_bwd(const void* dq_out, const void* dk_out, const void* q, const void* k,
+                                      const void* q_weight, const void* k_weight, void* dq, void* dk, void* dq_weight,
+                                      void* dk_weight, int B, int S, int Hq, int Hk, int N, const int64_t dqo_str[3],
+                                      const int64_t dko_str[3], const int64_t q_str[3], const int64_t k_str[3],
+                                      const int64_t dq_str[3], const int64_t dk_str[3], float eps, const int32_t* pos,
+                                      const int64_t pos_str[3], int axes, const uint64_t* freq, int rope_dim,
+                                      int interleaved, float magnitude, int dtype, int w_dtype, void* workspace,
+                                      size_t workspace_bytes, attn_stream_t stream);
 
 /*
  * attn_get_device_status -- synchronise `stream`, then read and clear the

@@ -15,6 +15,10 @@ library has not been built, every call raises.
     attn_bwd_bf16(dout, q, k, v, O, lse, ...) -> dQ, dK, dV
     layer_norm_fwd(x, weight, bias)   -> y, mean, rstd
     layer_norm_bwd(dy, x, weight, mean, rstd) -> dx, dweight, dbias
+    rope_frequencies(rope_dim, ...)   -> freq, magnitude    (what the rotations take)
+    rope_fwd(q, k, freq, positions)   -> q', k'             (rotary positions; rope_bwd: their gradients)
+    qk_norm_rope_fwd(q, k, q_weight, k_weight, freq, positions) -> q', k'
+    qk_norm_rope_bwd(dq', dk', q, k, q_weight, k_weight, freq, positions) -> dq, dk, dq_weight, dk_weight
 """
 from __future__ import annotations
 
@@ -31,7 +35,8 @@ from .build import LIB as _LIB_PATH
 
 __all__ = ["AttnError", "attn_fwd_bf16", "sage_prepare", "sage_prepare_noalloc", "sage_attn_fwd", "sage_attention",
            "Prepared", "e4m3_encode", "attn_fwd_bf16_lse", "attn_bwd_bf16", "attn_bwd_workspace",
-           "layer_norm_fwd", "layer_norm_bwd", "layer_norm_bwd_workspace",
+           "layer_norm_fwd", "layer_norm_bwd", "layer_norm_bwd_workspace", "rope_frequencies",
+           "rope_fwd", "rope_bwd", "qk_norm_rope_fwd", "qk_norm_rope_bwd", "qk_norm_rope_bwd_workspace",
            "sage_padded_len", "attn_get_device_status", "lib", "STATUS"]
 
 STATUS = {0: "ATTN_OK", 1: "ATTN_ERR_INVALID_ARG", 2: "ATTN_ERR_ALIGNMENT", 3: "ATTN_ERR_UNSUPPORTED",
@@ -116,7 +121,13 @@ def lib() -> ctypes.CDLL:
                 ("attn_bwd_bf16", i, [_vp] * 9 + [i] * 6 + [_vp] * 8 + [f32, i, _vp, _vp, size, _vp]),
                 ("layer_norm_fwd", i, [_vp] * 6 + [i] * 4 + [_vp] * 2 + [f32, i, i, _vp]),
                 ("layer_norm_bwd_workspace_size", size, [i] * 4),
-                ("layer_norm_bwd", i, [_vp] * 8 + [i] * 4 + [_vp] * 3 + [i, i, _vp, size, _vp])):
+                ("layer_norm_bwd", i, [_vp] * 8 + [i] * 4 + [_vp] * 3 + [i, i, _vp, size, _vp]),
+                ("rope_fwd", i, [_vp] * 4 + [i] * 5 + [_vp] * 6 + [i, _vp, i, i, f32, i, _vp]),
+                ("rope_bwd", i, [_vp] * 4 + [i] * 5 + [_vp] * 6 + [i, _vp, i, i, f32, i, _vp]),
+                ("qk_norm_rope_fwd", i, [_vp] * 6 + [i] * 5 + [_vp] * 4 + [f32, _vp, _vp, i, _vp, i, i, f32, i, i, _vp]),
+                ("qk_norm_rope_bwd_workspace_size", size, [i] * 5),
+                ("qk_norm_rope_bwd", i, [_vp] * 10 + [i] * 5 + [_vp] * 6 + [f32, _vp, _vp, i, _vp, i, i, f32, i, i, _vp,
+                                                                            size, _vp])):
             if hasattr(L, name):
                 fn = getattr(L, name)
                 fn.argtypes, fn.restype = args, res
@@ -713,6 +724,244 @@ def layer_norm_bwd(dy: torch.Tensor, x: torch.Tensor, weight: torch.Tensor | Non
                                 _DTYPES[x.dtype], _DTYPES[w_type], workspace.data_ptr() if size else None, size,
                                 _current_stream(dev)))
     return dx, dweight, dbias
+
+
+def rope_frequencies(rope_dim: int, theta: float = 10000.0, axes=None, scaling: dict | None = None,
+                     device="cuda") -> tuple[torch.Tensor, float]:
+    """What the rotations take: (freq, magnitude), freq int64 [rope_dim / 2] on `device` (turns a position in 2^-64, the
+    axis in the two lowest bits).  Made once and kept.
+
+    axes: channels of each position axis, up to four even numbers that add up to rope_dim (None: one axis).  Pair i of an
+    axis of n channels turns by w = theta^(-2 i / n) radians a position, which `scaling` changes:
+      {"kind": "linear", "factor": f}      w / f
+      {"kind": "ntk", "factor": f}         theta f^(n / (n - 2)) in place of theta
+      {"kind": "bands", "factor": f, "length": L, "low": 1, "high": 4}
+                                           keep w + (1 - keep) w / f, keep = (turns - low) / (high - low) in [0, 1], turns =
+                                           those that a pair makes over the L positions trained on
+      {"kind": "yarn", "factor": f, "length": L, "slow": 1, "fast": 32, "magnitude": 0.1 log f + 1}
+                                           the same with keep = log(turns / slow) / log(fast / slow); cosine and sine
+                                           times the magnitude"""
+    if rope_dim < 0 or rope_dim % 2:
+        raise ValueError(f"rope_dim must be even and >= 0, got {rope_dim}")
+    axes = (rope_dim,) if axes is None else tuple(axes)
+    if not 1 <= len(axes) <= 4 or sum(axes) != rope_dim or any(n < 0 or n % 2 for n in axes):
+        raise ValueError(f"axes must be one to four even numbers that add up to {rope_dim}, got {axes}")
+    if not (theta > 0 and math.isfinite(theta)):
+        raise ValueError(f"theta must be positive, got {theta}")
+    known = {"linear": {}, "ntk": {}, "bands": {"low": 1.0, "high": 4.0}, "yarn": {"slow": 1.0, "fast": 32.0}}
+    scale = dict(scaling or {"kind": "linear", "factor": 1.0})
+    kind, f = scale.pop("kind", None), float(scale.pop("factor", 1.0))
+    if kind not in known or not (f > 0 and math.isfinite(f)):
+        raise ValueError(f"scaling must name one of {sorted(known)} and a positive factor, got {scaling}")
+    magnitude, turns, ends = 1.0, 1.0, dict(known[kind])
+    if kind in ("bands", "yarn"):
+        turns = float(scale.pop("length")) / (2 * math.pi) if "length" in scale else 0.0
+        magnitude = 1.0 if kind == "bands" else float(scale.pop("magnitude", 0.1 * math.log(f) + 1.0 if f > 1 else 1.0))
+        for name in ends:
+            ends[name] = float(scale.pop(name, ends[name]))
+        below, above = ends.values()
+        if not (turns > 0 and 0 < below < above and math.isfinite(magnitude)):
+            raise ValueError(f"scaling needs a length and bounds in order, got {scaling}")
+    if scale:
+        raise ValueError(f"scaling {kind!r} does not take {sorted(scale)}")
+    out = []
+    for axis, n in enumerate(axes):
+        base = theta * f ** (n / (n - 2)) if kind == "ntk" and n > 2 else theta
+        for i in range(n // 2):
+            w = base ** (-2 * i / n)
+            if kind == "linear":
+                w /= f
+            elif kind != "ntk":
+                x = turns * w
+                keep = (x - below) / (above - below) if kind == "bands" else math.log(x / below) / math.log(above / below)
+                keep = min(1.0, max(0.0, keep))
+                w = keep * w + (1.0 - keep) * w / f
+            t = round(w / (2 * math.pi) * 2.0 ** 64) % 2 ** 64 & ~3 | axis
+            out.append(t - 2 ** 64 if t >= 2 ** 63 else t)
+    return torch.tensor(out, dtype=torch.int64, device=device), magnitude
+
+
+def _rope_args(q, k, freq, positions):
+    """Sizes, the device, and what positions come to: (sizes, N, dev, pointer, strides, axes)."""
+    if q.dim() != 4:
+        raise ValueError(f"rows must be [B, S, H, N], got {tuple(q.shape)}")
+    if q.dtype not in _DTYPES:
+        raise ValueError(f"rows must be bfloat16, float16 or float32, got {q.dtype}")
+    B, S, Hq, N = q.shape
+    dev = _cuda_index("q", q)
+    Hk = 0
+    if k is not None:
+        if k.dim() != 4:
+            raise ValueError(f"rows must be [B, S, H, N], got {tuple(k.shape)}")
+        Hk = k.shape[2]
+        _expect("k", k, (B, S, Hk, N), q.dtype, dev)
+    if q.numel() > 0x7fffffff or (k is not None and k.numel() > 0x7fffffff):
+        _sizes(B, S, Hq, Hk, N)
+    if freq is not None:
+        _expect_dense("freq", freq, freq.shape[:1], torch.int64, dev)
+    if positions is None:
+        return (B, S, Hq, Hk, N), dev, None, None, 1
+    if positions.dtype is not torch.int32:
+        raise ValueError(f"positions must be int32, got {positions.dtype}")
+    if positions.get_device() != dev:
+        raise ValueError(f"positions is on {positions.device}, expected cuda:{dev}")
+    shape, st = positions.shape, positions.stride()
+    if len(shape) == 1 and shape[0] == S:
+        strides, axes = (0, st[0], 0), 1
+    elif len(shape) in (2, 3) and shape[0] in (1, B) and shape[1] == S and (len(shape) == 2 or 1 <= shape[2] <= 4):
+        axes = shape[2] if len(shape) == 3 else 1
+        strides = (0 if shape[0] == 1 else st[0], st[1], st[2] if axes > 1 else 0)
+    else:
+        raise ValueError(f"positions must be [{S}], [{B}, {S}] or [{B}, {S}, axes], got {tuple(shape)}")
+    return (B, S, Hq, Hk, N), dev, positions.data_ptr(), array("q", strides), axes
+
+
+def _rope_outputs(names: str, dev: int, *pairs):
+    """The outputs, made where they are not given: of each (rows, output)."""
+    out = []
+    for name, (x, o) in zip(names.split(), pairs):
+        if x is None:
+            if o is not None:
+                raise ValueError(f"{name} was given without its rows")
+        elif o is None:
+            o = torch.empty(x.shape, dtype=x.dtype, device=dev)
+        else:
+            _expect(name, o, x.shape, x.dtype, dev)
+        out.append(o)
+    return out
+
+
+def _ptr(t):
+    return None if t is None else t.data_ptr()
+
+
+def _rope_strides(names: str, *tensors):
+    """Addresses of the tensors' strides (None for a missing one) and the array that holds them."""
+    given = [(n, t) for n, t in zip(names.split(), tensors) if t is not None]
+    held = _norm_strides(" ".join(n for n, _ in given), *(t for _, t in given))
+    at = held.buffer_info()[0]
+    out = []
+    for t in tensors:
+        out.append(None if t is None else at)
+        at += 0 if t is None else 32
+    return out, held
+
+
+def _rope(call: str, q, k, freq, positions, interleaved, magnitude, q_out, k_out, stream):
+    sizes, dev, pos, pos_strides, axes = _rope_args(q, k, freq, positions)
+    if _elsewhere(dev, stream):
+        with _there(dev, stream):
+            return _rope(call, q, k, freq, positions, interleaved, magnitude, q_out, k_out, None)
+    q_out, k_out = _rope_outputs("q_out k_out", dev, (q, q_out), (k, k_out))
+    at, _held = _rope_strides("q k q_out k_out", q, k, q_out, k_out)
+    _check(getattr(lib(), call)(q.data_ptr(), _ptr(k), q_out.data_ptr(), _ptr(k_out), *sizes, *at, pos,
+                                pos_strides.buffer_info()[0] if pos_strides else None, axes, freq.data_ptr(),
+                                2 * freq.shape[0], interleaved, magnitude, _DTYPES[q.dtype], _current_stream(dev)))
+    return q_out, k_out
+
+
+def rope_fwd(q: torch.Tensor, k: torch.Tensor | None, freq: torch.Tensor, positions: torch.Tensor | None = None,
+             interleaved: bool = False, magnitude: float = 1.0, q_out: torch.Tensor | None = None,
+             k_out: torch.Tensor | None = None, stream=None) -> tuple[torch.Tensor, torch.Tensor | None]:
+    """Rotary positions of q [B, S, Hq, N] and k [B, S, Hk, N] (or None): (q', k').  BF16, FP16 or FP32, N up to 512, any
+    strides; the first 2 len(freq) channels of a head are rotated, the others pass through.
+
+    freq, magnitude: from rope_frequencies.  positions: int32 [S], [B, S] or [B, S, axes] (B may be 1); None: 0 to S - 1.
+    interleaved: pairs of neighbouring channels; else of the two halves of the rotated part.  q_out and k_out may be q
+    and k themselves."""
+    return _rope("rope_fwd", q, k, freq, positions, interleaved, magnitude, q_out, k_out, stream)
+
+
+def rope_bwd(dq_out: torch.Tensor, dk_out: torch.Tensor | None, freq: torch.Tensor,
+             positions: torch.Tensor | None = None, interleaved: bool = False, magnitude: float = 1.0,
+             dq: torch.Tensor | None = None, dk: torch.Tensor | None = None,
+             stream=None) -> tuple[torch.Tensor, torch.Tensor | None]:
+    """The gradients of rope_fwd, (dq, dk), from those of its outputs; the other arguments as it was given them."""
+    return _rope("rope_bwd", dq_out, dk_out, freq, positions, interleaved, magnitude, dq, dk, stream)
+
+
+def _rope_weights(q, q_weight, k_weight, dev: int) -> torch.dtype:
+    """The type of the weights, each [N] of the rows' type or float32."""
+    w_type = q.dtype
+    if q_weight is not None:
+        _norm_weight("q_weight", q_weight, q, dev)
+        w_type = q_weight.dtype
+    if k_weight is not None:
+        _norm_weight("k_weight", k_weight, q, dev, None if q_weight is None else w_type)
+        w_type = k_weight.dtype
+    return w_type
+
+
+def qk_norm_rope_fwd(q: torch.Tensor, k: torch.Tensor | None, q_weight: torch.Tensor | None,
+                     k_weight: torch.Tensor | None, freq: torch.Tensor | None, positions: torch.Tensor | None = None,
+                     eps: float = 1e-6, interleaved: bool = False, magnitude: float = 1.0,
+                     q_out: torch.Tensor | None = None, k_out: torch.Tensor | None = None,
+                     stream=None) -> tuple[torch.Tensor, torch.Tensor | None]:
+    """The RMS norm of each head of q and k, times its weight [N] (or None), and the rotation of rope_fwd, in one pass:
+    (q', k').  freq None: the norm alone."""
+    sizes, dev, pos, pos_strides, axes = _rope_args(q, k, freq, positions)
+    if _elsewhere(dev, stream):
+        with _there(dev, stream):
+            return qk_norm_rope_fwd(q, k, q_weight, k_weight, freq, positions, eps, interleaved, magnitude, q_out, k_out)
+    w_type = _rope_weights(q, q_weight, k_weight, dev)
+    q_out, k_out = _rope_outputs("q_out k_out", dev, (q, q_out), (k, k_out))
+    at, _held = _rope_strides("q k q_out k_out", q, k, q_out, k_out)
+    _check(lib().qk_norm_rope_fwd(q.data_ptr(), _ptr(k), _ptr(q_weight), _ptr(k_weight), q_out.data_ptr(), _ptr(k_out),
+                                  *sizes, *at, eps, pos, pos_strides.buffer_info()[0] if pos_strides else None, axes,
+                                  _ptr(freq), 0 if freq is None else 2 * freq.shape[0], interleaved, magnitude,
+                                  _DTYPES[q.dtype], _DTYPES[w_type], _current_stream(dev)))
+    return q_out, k_out
+
+
+def qk_norm_rope_bwd_workspace(q_shape, kv_heads: int, device) -> torch.Tensor:
+    """Scratch for qk_norm_rope_bwd of q [B, S, Hq, N] and that many heads of k; calls on different streams need one
+    each."""
+    B, S, Hq, N = q_shape
+    _sizes(B, S, Hq, kv_heads, N)
+    return torch.empty(lib().qk_norm_rope_bwd_workspace_size(B, S, Hq, kv_heads, N), dtype=torch.uint8, device=device)
+
+
+def qk_norm_rope_bwd(dq_out: torch.Tensor, dk_out: torch.Tensor | None, q: torch.Tensor, k: torch.Tensor | None,
+                     q_weight: torch.Tensor | None, k_weight: torch.Tensor | None, freq: torch.Tensor | None,
+                     positions: torch.Tensor | None = None, eps: float = 1e-6, interleaved: bool = False,
+                     magnitude: float = 1.0, dq: torch.Tensor | None = None, dk: torch.Tensor | None = None,
+                     dq_weight: torch.Tensor | None = None, dk_weight: torch.Tensor | None = None,
+                     workspace: torch.Tensor | None = None, stream=None):
+    """(dq, dk, dq_weight, dk_weight) of qk_norm_rope_fwd: dq_out and dk_out are the gradients of its outputs, the other
+    arguments those it was given.  A weight's gradient has its type and is None without the weight.  The same inputs give
+    the same bits."""
+    sizes, dev, pos, pos_strides, axes = _rope_args(q, k, freq, positions)
+    if _elsewhere(dev, stream):
+        with _there(dev, stream):
+            return qk_norm_rope_bwd(dq_out, dk_out, q, k, q_weight, k_weight, freq, positions, eps, interleaved,
+                                    magnitude, dq, dk, dq_weight, dk_weight, workspace)
+    _expect("dq_out", dq_out, q.shape, q.dtype, dev)
+    if k is None:
+        if not (dk_out is None and k_weight is None):
+            raise ValueError("dk_out and k_weight must be None without k")
+    else:
+        _expect("dk_out", dk_out, k.shape, q.dtype, dev)
+    w_type = _rope_weights(q, q_weight, k_weight, dev)
+    dq, dk = _rope_outputs("dq dk", dev, (q, dq), (k, dk))
+    grads = []
+    for name, w, dw in (("dq_weight", q_weight, dq_weight), ("dk_weight", k_weight, dk_weight)):
+        if w is None and dw is not None:
+            raise ValueError(f"{name} was given without its weight")
+        if dw is not None:
+            _norm_weight(name, dw, q, dev, w_type)
+        grads.append(torch.empty(w.shape, dtype=w_type, device=dev) if w is not None and dw is None else dw)
+    size = 0
+    if q_weight is not None or k_weight is not None:
+        if workspace is None:
+            workspace = qk_norm_rope_bwd_workspace(q.shape, sizes[3], dev)
+        size = _scratch("workspace", workspace, dev)
+    at, _held = _rope_strides("dq_out dk_out q k dq dk", dq_out, dk_out, q, k, dq, dk)
+    _check(lib().qk_norm_rope_bwd(dq_out.data_ptr(), _ptr(dk_out), q.data_ptr(), _ptr(k), _ptr(q_weight), _ptr(k_weight),
+                                  dq.data_ptr(), _ptr(dk), _ptr(grads[0]), _ptr(grads[1]), *sizes, *at, eps, pos,
+                                  pos_strides.buffer_info()[0] if pos_strides else None, axes, _ptr(freq),
+                                  0 if freq is None else 2 * freq.shape[0], interleaved, magnitude, _DTYPES[q.dtype],
+                                  _DTYPES[w_type], workspace.data_ptr() if size else None, size, _current_stream(dev)))
+    return dq, dk, grads[0], grads[1]
 
 
 def attn_selftest_wait_timeout(device=None, stream=None) -> str:

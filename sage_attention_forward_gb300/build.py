@@ -18,9 +18,11 @@ ROOT = os.path.dirname(HERE)
 CSRC = os.path.join(HERE, "csrc")
 OUT_DIR = os.path.join(HERE, "_build")
 LIB = os.path.join(OUT_DIR, "libsageattn.so")
-SOURCES = ["api.cu", "attn_fwd.cu", "sage_prepare.cu", "attn_lse.cu", "attn_bwd.cu", "layer_norm.cu"]
-HOST_SOURCES = ["api_train.cpp"]   # no kernels
-HEADERS = ["ptx.cuh", "ptx_train.cuh", "kernels.h", "api_checks.h", "qk_quant.cuh", "attn_tiles.cuh"]
+SOURCES = ["api.cu", "attn_fwd.cu", "sage_prepare.cu", "attn_lse.cu", "attn_bwd.cu", "layer_norm.cu", "qk_rope.cu",
+           "qk_rope_bwd.cu"]
+HOST_SOURCES = ["api_train.cpp", "api_rope.cpp"]   # no kernels
+HEADERS = ["ptx.cuh", "ptx_train.cuh", "kernels.h", "api_checks.h", "api_overlap.h", "qk_quant.cuh", "attn_tiles.cuh",
+           "pieces.cuh", "qk_rope.cuh"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
 

@@ -246,6 +246,30 @@ cudaError_t launch_layer_norm_bwd(const LayerNormArgs& a, const void* dy, const 
                                   const long long dx_str[3], void* dw, void* db, float* workspace,
                                   cudaStream_t stream);
 
+// Rotary positions of Q and K, with or without their norm (qk_rope.cu, qk_rope_bwd.cu).
+struct RopeArgs {
+  struct Side {
+    const void *x, *dy;       // dy: backward of the norm with the rotation
+    void* y;                  // the result: y, or dx
+    const void* w;            // weight [N] of the norm, or nullptr
+    void* dw;                 // its gradient, or nullptr
+    int H;
+    long long x_str[3], dy_str[3], y_str[3];   // element strides (b, s, h)
+  } side[2];                  // Q, K (H = 0: none)
+  int B, S, N, R;             // the first R of N channels are rotated
+  const int* pos;             // or nullptr: the place in the sequence
+  long long pos_str[3];       // element strides (b, s, axis)
+  int axes;
+  const unsigned long long* freq;   // [R / 2]: turns a position in 2^-64, the two lowest bits the axis
+  int interleaved, inverse;
+  float magnitude, eps;
+  int type, w_type;
+};
+cudaError_t launch_rope_fwd(const RopeArgs& a, bool norm, cudaStream_t stream);
+// CTAs whose sums of dw the workspace holds; the same for any strides and weights.
+int rope_bwd_ctas(int B, int S, int Hq, int Hk);
+cudaError_t launch_qk_norm_rope_bwd(const RopeArgs& a, float* workspace, cudaStream_t stream);
+
 // The order of a grid's items (tile, head): `group` heads go together, tile by tile.  One head after another
 // (group = 1) keeps few heads' tiles in L2.  Where a causal mask makes the first tiles of a head the longest
 // items, several heads' long ones come before their short ones, so that the grid ends with short

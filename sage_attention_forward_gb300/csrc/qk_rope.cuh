@@ -1,0 +1,280 @@
+// What the rotation of Q and K, and their norm with the rotation, share in both directions.
+//
+//   angle(t, i) = position(t, axis(i)) w_i         y = m (a cos - b sin, b cos + a sin) of each pair (a, b) of channels
+//
+// Frequencies come as turns a position in units of 2^-64, so that the whole turns of an angle fall off in the
+// product of two integers: the remainder is exact to 2^-33 turns for any position of 31 bits, without tables of
+// cosines in memory and without 64-bit floating point (of which an SM has little).  A warp forms the cosines of one
+// token once, in shared memory, and takes them for all of the token's heads.
+#pragma once
+
+#include <type_traits>
+
+#include "kernels.h"
+#include "pieces.cuh"
+
+namespace sa {
+
+constexpr int kRopeThreads = 256, kRopeWarps = kRopeThreads / 32;
+
+struct RopeSide {
+  const void *x, *dy;             // dy: backward of the norm (the rotation's own backward reads x)
+  void* y;                        // y, or dx
+  const void* w;
+  float* partial;                 // backward: [CTAs][N] sums of dw, or nullptr
+  long long xs[3], ds[3], ys[3];  // element strides (b, s, h)
+  int heads, parts;               // parts: units that a token's heads are divided into
+};
+struct RopeParams {
+  RopeSide side[2];               // Q and K
+  const int* pos;                 // or nullptr: the place in the sequence
+  const unsigned long long* freq;
+  long long pos_str[3];           // element strides (b, s, axis)
+  int tokens, N, pairs, axes;
+  int per_unit;                   // heads of a unit
+  int table;                      // cosines and sines of a warp
+  int lanes, slots;               // lanes a row, rows a warp takes at a time
+  Div S, by_parts;                // by_parts: units of a token
+  float magnitude, eps, inv_n;
+  int inverse, w_type, w_vec;     // w_vec: weights by 16 bytes
+};
+
+// Where a lane's pairs are.  kHalf, kNext: 16-byte pieces, eight pairs a lane (R a multiple of 16 for kHalf);
+// kAny: pairs lane, lane + 32, ... by the channel.
+enum RopeMap : int { kHalf = 0, kNext = 1, kAny = 2, kAnyNext = 3 };
+
+template <class T, int kMap, int kPairs>
+struct RopeLane {
+  static constexpr bool kVec = kMap == kHalf || kMap == kNext;
+  static constexpr int kPieces = kVec ? (int)sizeof(T) : 1;   // 16-byte pieces of a lane's 16 channels
+  struct Raw {
+    uint4 piece[kVec ? kPieces : 1];
+    T a[kVec ? 1 : kPairs], b[kVec ? 1 : kPairs];
+  };
+  int l, ca, cb, last;   // kVec: first channels of the two runs of eight; last: N
+
+  __device__ __forceinline__ RopeLane(const RopeParams& p, int lane) {
+    l = kVec ? lane % p.lanes : lane;
+    last = p.N;
+    const bool turned = kMap == kHalf && 8 * l < p.pairs;
+    ca = turned ? 8 * l : 16 * l;
+    cb = turned ? p.pairs + 8 * l : 16 * l + 8;
+  }
+  // kVec: the lane has channels of a row
+  __device__ __forceinline__ bool some() const { return !kVec || 16 * l < last; }
+  __device__ __forceinline__ int pair(int i) const { return kVec ? 8 * l + i : l + 32 * i; }
+  __device__ __forceinline__ int first(int i, int pairs) const {
+    if (kMap == kHalf) return ca + i;
+    if (kMap == kNext) return 16 * l + 2 * i;
+    const int v = pair(i);
+    return kMap == kAny && v < pairs ? v : 2 * v;
+  }
+  __device__ __forceinline__ int second(int i, int pairs) const {
+    if (kMap == kHalf) return cb + i;
+    if (kMap == kNext) return 16 * l + 2 * i + 1;
+    const int v = pair(i);
+    return kMap == kAny && v < pairs ? v + pairs : 2 * v + 1;
+  }
+  __device__ __forceinline__ void load(const T* row, int pairs, Raw& r) const {
+    if constexpr (kVec) {
+      constexpr int half = kPieces / 2;
+#pragma unroll
+      for (int k = 0; k < half; ++k) {
+        r.piece[k] = __ldcs(reinterpret_cast<const uint4*>(row + ca) + k);
+        r.piece[half + k] = __ldcs(reinterpret_cast<const uint4*>(row + cb) + k);
+      }
+    } else {
+#pragma unroll
+      for (int i = 0; i < kPairs; ++i) {
+        const int a = first(i, pairs), b = second(i, pairs);
+        r.a[i] = a < last ? row[a] : T(0.0f);
+        r.b[i] = b < last ? row[b] : T(0.0f);
+      }
+    }
+  }
+  __device__ __forceinline__ void values(const Raw& r, float (&a)[kPairs], float (&b)[kPairs]) const {
+    if constexpr (kVec) {
+      float x[16];
+#pragma unroll
+      for (int k = 0; k < kPieces; ++k) unpack<T>(r.piece[k], x + k * Piece<T>::kN);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        a[i] = kMap == kHalf ? x[i] : x[2 * i];
+        b[i] = kMap == kHalf ? x[8 + i] : x[2 * i + 1];
+      }
+    } else {
+#pragma unroll
+      for (int i = 0; i < kPairs; ++i) {
+        a[i] = (float)r.a[i];
+        b[i] = (float)r.b[i];
+      }
+    }
+  }
+  __device__ __forceinline__ void store(T* row, int pairs, const float (&a)[kPairs], const float (&b)[kPairs]) const {
+    if constexpr (kVec) {
+      float x[16];
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        x[kMap == kHalf ? i : 2 * i] = a[i];
+        x[kMap == kHalf ? 8 + i : 2 * i + 1] = b[i];
+      }
+      constexpr int half = kPieces / 2;
+#pragma unroll
+      for (int k = 0; k < half; ++k) {
+        __stcs(reinterpret_cast<uint4*>(row + ca) + k, pack<T>(x + k * Piece<T>::kN));
+        __stcs(reinterpret_cast<uint4*>(row + cb) + k, pack<T>(x + (half + k) * Piece<T>::kN));
+      }
+    } else {
+#pragma unroll
+      for (int i = 0; i < kPairs; ++i) {
+        const int ia = first(i, pairs), ib = second(i, pairs);
+        if (ia < last) row[ia] = T(a[i]);
+        if (ib < last) row[ib] = T(b[i]);
+      }
+    }
+  }
+  // The weights of the lane's channels (1 without weights, or where there is no channel).
+  // Those of pair i in v[2 i], v[2 i + 1].
+  __device__ __forceinline__ void weights(const void* w, const RopeParams& p, float (&v)[2 * kPairs]) const {
+    float a[kPairs], b[kPairs];
+    weights(w, p, a, b);
+#pragma unroll
+    for (int i = 0; i < kPairs; ++i) {
+      v[2 * i] = a[i];
+      v[2 * i + 1] = b[i];
+    }
+  }
+  __device__ __forceinline__ void weights(const void* w, const RopeParams& p, float (&a)[kPairs],
+                                          float (&b)[kPairs]) const {
+#pragma unroll
+    for (int i = 0; i < kPairs; ++i) a[i] = b[i] = 1.0f;
+    if (w == nullptr || !some()) return;
+    if constexpr (kVec) {
+      if (p.w_vec) {
+        if (p.w_type == kF32) {
+          RopeLane<float, kMap, 8>(p, l).take(reinterpret_cast<const float*>(w), p.pairs, a, b);
+        } else {
+          take(reinterpret_cast<const T*>(w), p.pairs, a, b);
+        }
+        return;
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < kPairs; ++i) {
+      const int ia = first(i, p.pairs), ib = second(i, p.pairs);
+      if (p.w_type == kF32) {
+        const float* f = reinterpret_cast<const float*>(w);
+        if (ia < last) a[i] = f[ia];
+        if (ib < last) b[i] = f[ib];
+      } else {
+        const T* f = reinterpret_cast<const T*>(w);
+        if (ia < last) a[i] = (float)f[ia];
+        if (ib < last) b[i] = (float)f[ib];
+      }
+    }
+  }
+  __device__ __forceinline__ void take(const T* row, int pairs, float (&a)[kPairs], float (&b)[kPairs]) const {
+    Raw r;
+    load(row, pairs, r);
+    values(r, a, b);
+  }
+};
+
+// Cosine and sine (times the magnitude) of a token's pairs, to `table`; the sine negated for the backward.  kVec: in the
+// order in which lanes read them, [4][lanes] of two pairs; else pair by pair.
+template <bool kVec>
+__device__ __forceinline__ void rope_table(const RopeParams& p, int b, int s, int lane, float2* table) {
+  __syncwarp();   // the last token's are no longer read
+  for (int i = lane; i < p.pairs; i += 32) {
+    const unsigned long long f = __ldg(p.freq + i);
+    int at = s;
+    if (p.pos != nullptr) {
+      const int axis = min((int)(f & 3), p.axes - 1);
+      at = __ldg(p.pos + b * p.pos_str[0] + s * p.pos_str[1] + axis * p.pos_str[2]);
+    }
+    const unsigned long long turns = (unsigned long long)(long long)at * (f & ~3ull);
+    float sn, cs;   // of half turns in [-1, 1)
+    sincospif((float)(int)(turns >> 32) * 0x1p-31f, &sn, &cs);
+    table[kVec ? ((i % 8 / 2) * p.lanes + i / 8) * 2 + i % 2 : i] = make_float2(cs * p.magnitude, sn * (p.inverse ? -p.magnitude : p.magnitude));
+  }
+  __syncwarp();
+}
+
+// Sum over the lanes of a row (a power of two of them).
+__device__ __forceinline__ float rope_row_sum(float v, int lanes) {
+  for (int o = 1; o < lanes; o <<= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+  return v;
+}
+
+// Calls f with the map and the pairs a lane for this problem, as constants.
+template <class F>
+cudaError_t with_rope_map(bool vec, bool next, int N, F&& f) {
+  auto with = [&](auto half, auto nxt, auto pairs) { return next ? f(nxt, pairs) : f(half, pairs); };
+  using std::integral_constant;
+  constexpr integral_constant<int, kAny> any{};
+  constexpr integral_constant<int, kAnyNext> any_next{};
+  if (vec) return with(integral_constant<int, kHalf>{}, integral_constant<int, kNext>{}, integral_constant<int, 8>{});
+  if (N <= 128) return with(any, any_next, integral_constant<int, 2>{});
+  if (N <= 256) return with(any, any_next, integral_constant<int, 4>{});
+  return with(any, any_next, integral_constant<int, 8>{});
+}
+
+// 16-byte accesses are possible, with eight pairs a lane; lanes a row and rows a warp.
+inline bool rope_shape(RopeParams& p, const RopeArgs& a, bool norm) {
+  const int piece = a.type == kF32 ? 4 : 8;
+  bool vec = a.N % 16 == 0 && (a.interleaved || a.R % 16 == 0);
+  for (int i = 0; i < 2; ++i) {
+    const RopeArgs::Side& s = a.side[i];
+    if (s.H == 0) continue;
+    const void* ptr[3] = {s.x, s.dy, s.y};
+    const long long* str[3] = {s.x_str, s.dy_str, s.y_str};
+    for (int k = 0; k < 3; ++k) {
+      if (ptr[k] == nullptr) continue;
+      vec = vec && (reinterpret_cast<uintptr_t>(ptr[k]) & 15u) == 0 && (a.B == 1 || str[k][0] % piece == 0) &&
+            (a.S == 1 || str[k][1] % piece == 0) && (s.H == 1 || str[k][2] % piece == 0);
+    }
+  }
+  p.lanes = 32;
+  if (vec) {
+    p.lanes = a.N / 16;
+    if (norm)   // the row's sums go over a power of two of lanes
+      while ((p.lanes & (p.lanes - 1)) != 0) ++p.lanes;
+  }
+  p.slots = 32 / p.lanes;
+  p.table = vec ? 8 * p.lanes : p.pairs;
+  return vec;
+}
+
+inline void rope_params(RopeParams& p, const RopeArgs& a) {
+  p.w_vec = 1;
+  for (int i = 0; i < 2; ++i) {
+    const RopeArgs::Side& s = a.side[i];
+    p.w_vec = p.w_vec && (reinterpret_cast<uintptr_t>(s.w) & 15u) == 0;
+    p.side[i].x = s.x;
+    p.side[i].dy = s.dy;
+    p.side[i].y = s.y;
+    p.side[i].w = s.w;
+    p.side[i].partial = nullptr;
+    p.side[i].heads = s.H;
+    for (int k = 0; k < 3; ++k) {
+      p.side[i].xs[k] = s.x_str[k];
+      p.side[i].ds[k] = s.dy_str[k];
+      p.side[i].ys[k] = s.y_str[k];
+      p.pos_str[k] = a.pos_str[k];
+    }
+  }
+  p.pos = a.pos;
+  p.freq = a.freq;
+  p.tokens = a.B * a.S;
+  p.N = a.N;
+  p.pairs = a.R / 2;
+  p.axes = a.axes;
+  p.S = make_div(a.S);
+  p.magnitude = a.magnitude;
+  p.eps = a.eps;
+  p.inv_n = 1.0f / (float)a.N;
+  p.inverse = a.inverse;
+  p.w_type = a.w_type;
+}
+
+}  // namespace sa

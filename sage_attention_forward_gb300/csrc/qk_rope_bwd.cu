@@ -1,0 +1,233 @@
+// Backward of the norm of Q and K with the rotation, sm_103a.
+//
+//   g = rope^T(dy),  xhat = x r,  r = 1 / sqrt(sum x^2 / N + eps), formed again from x
+//   dx = r (g w - xhat sum(g w xhat) / N),   dw = sum over rows of g xhat
+//
+// Bound by memory: x and dy are read and dx written once.  Units and lanes as in the forward (qk_rope.cu), but CTAs walk
+// over the units, first Q's, then K's, and a lane keeps the sums of dw of its own 16 channels in registers over all of
+// its rows.  Each CTA writes its sums once to the workspace; a second kernel adds them up in one fixed order: no atomics,
+// the same bits every time.
+#include <cuda_runtime.h>
+
+#include "qk_rope.cuh"
+
+namespace sa {
+namespace {
+
+// (volatile: held in registers over the rows, weights and cosines would spill)
+__device__ __forceinline__ float4 load_shared(const float4* at) {
+  float4 v;
+  asm volatile("ld.shared.v4.f32 {%0, %1, %2, %3}, [%4];"
+               : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
+               : "r"(smem_u32(at)));
+  return v;
+}
+
+__device__ __forceinline__ float2 load_shared(const float2* at) {
+  float2 v;
+  asm volatile("ld.shared.v2.f32 {%0, %1}, [%2];" : "=f"(v.x), "=f"(v.y) : "r"(smem_u32(at)));
+  return v;
+}
+
+template <class T, int kMap, int kPairs>
+__global__ void __launch_bounds__(kRopeThreads, kMap >= kAny && kPairs == 8 ? 1 : 2) rope_bwd_kernel(const __grid_constant__ RopeParams p) {
+  using L = RopeLane<T, kMap, kPairs>;
+  constexpr int kAhead = sizeof(T) == 4 || (!L::kVec && kPairs == 8) ? 1 : 2;
+  // the weights by lanes, [kPairs / 2][lanes] of four (registers do not reach for them); then the tables,
+  // [warps][p.table], or at the end the warps' sums, [warps][N]
+  extern __shared__ float4 shared[];
+  float2* const tables = reinterpret_cast<float2*>(shared + kPairs / 2 * 32);
+  griddep_wait();
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const L ln(p, lane);
+  const int slot = L::kVec ? lane / p.lanes : 0;
+  const bool mine = slot < p.slots && ln.some();
+  float2* const table = tables + warp * p.table;
+  float* const sums = reinterpret_cast<float*>(tables);
+
+  for (int which = 0; which < 2; ++which) {
+    const RopeSide& sd = p.side[which];
+    if (sd.heads == 0) continue;
+    float da[kPairs] = {}, db[kPairs] = {};
+    if (warp == 0 && slot == 0) {
+      float w[2 * kPairs];
+      ln.weights(sd.w, p, w);
+#pragma unroll
+      for (int k = 0; k < kPairs / 2; ++k)
+        shared[k * p.lanes + ln.l] = make_float4(w[4 * k], w[4 * k + 1], w[4 * k + 2], w[4 * k + 3]);
+    }
+    __syncthreads();
+    const int units = p.tokens * sd.parts;
+    for (int unit = blockIdx.x * kRopeWarps + warp; unit < units; unit += gridDim.x * kRopeWarps) {
+      const int token = sd.parts == 1 ? unit : unit / sd.parts, first = (unit - token * sd.parts) * p.per_unit;
+      const int end = min(first + p.per_unit, sd.heads);
+      const int b = div_by(token, p.S), s = token - b * (int)p.S.d;
+      const T* const x = reinterpret_cast<const T*>(sd.x) + b * sd.xs[0] + s * sd.xs[1];
+      const T* const dy = reinterpret_cast<const T*>(sd.dy) + b * sd.ds[0] + s * sd.ds[1];
+      T* const dx = reinterpret_cast<T*>(sd.y) + b * sd.ys[0] + s * sd.ys[1];
+      typename L::Raw rx[kAhead], rd[kAhead];
+      auto load = [&](int u, int h) {
+        if (mine && h < end) {
+          ln.load(x + h * sd.xs[2], p.pairs, rx[u]);
+          ln.load(dy + h * sd.ds[2], p.pairs, rd[u]);
+        }
+      };
+      int h = first + slot;
+#pragma unroll
+      for (int u = 0; u < kAhead; ++u) load(u, h + u * p.slots);
+      rope_table<L::kVec>(p, b, s, lane, table);
+      for (int base = first; base < end; base += kAhead * p.slots) {
+#pragma unroll
+        for (int u = 0; u < kAhead; ++u, h += p.slots) {
+          if (base + u * p.slots >= end) break;
+          float a[kPairs], c[kPairs], ga[kPairs], gc[kPairs];
+          const bool in = mine && h < end;
+          if (in) {
+            ln.values(rx[u], a, c);
+            ln.values(rd[u], ga, gc);
+          } else {
+#pragma unroll
+            for (int i = 0; i < kPairs; ++i) a[i] = c[i] = ga[i] = gc[i] = 0.0f;
+          }
+          load(u, h + kAhead * p.slots);
+          float sum = 0.0f;
+#pragma unroll
+          for (int i = 0; i < kPairs; ++i) sum = fmaf(a[i], a[i], fmaf(c[i], c[i], sum));
+          const float r = rsqrtf(fmaf(rope_row_sum(sum, p.lanes), p.inv_n, p.eps));
+          float dot = 0.0f;
+#pragma unroll
+          for (int k = 0; k < kPairs / 2; ++k) {
+            const float4 w = load_shared(shared + k * p.lanes + ln.l);
+            float2 t[2];   // cosines and sines
+            if (L::kVec) {
+              const float4 two = load_shared(reinterpret_cast<const float4*>(table) + k * p.lanes + ln.l);
+              t[0] = make_float2(two.x, two.y);
+              t[1] = make_float2(two.z, two.w);
+            } else {
+#pragma unroll
+              for (int e = 0; e < 2; ++e)
+                if (ln.pair(2 * k + e) < p.pairs) t[e] = load_shared(table + ln.pair(2 * k + e));
+            }
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+              const int i = 2 * k + e;
+              if (ln.pair(i) < p.pairs) {
+                const float g0 = ga[i];
+                ga[i] = g0 * t[e].x - gc[i] * t[e].y;
+                gc[i] = gc[i] * t[e].x + g0 * t[e].y;
+              }
+              a[i] *= r;
+              c[i] *= r;
+              da[i] = fmaf(ga[i], a[i], da[i]);
+              db[i] = fmaf(gc[i], c[i], db[i]);
+              ga[i] *= e ? w.z : w.x;
+              gc[i] *= e ? w.w : w.y;
+              dot = fmaf(ga[i], a[i], fmaf(gc[i], c[i], dot));
+            }
+          }
+          dot = rope_row_sum(dot, p.lanes) * p.inv_n;
+          if (in) {
+#pragma unroll
+            for (int i = 0; i < kPairs; ++i) {
+              a[i] = r * (ga[i] - a[i] * dot);
+              c[i] = r * (gc[i] - c[i] * dot);
+            }
+            ln.store(dx + h * sd.ys[2], p.pairs, a, c);
+          }
+        }
+      }
+    }
+    if (sd.partial == nullptr) continue;
+    // the warp's slots, then the CTA's warps, in order
+    for (int o = p.lanes; o < 32; o <<= 1) {
+#pragma unroll
+      for (int i = 0; i < kPairs; ++i) {
+        da[i] += __shfl_xor_sync(0xffffffffu, da[i], o);
+        db[i] += __shfl_xor_sync(0xffffffffu, db[i], o);
+      }
+    }
+    __syncthreads();   // the tables, or Q's sums, are no longer read
+    if (slot == 0 && ln.some()) {
+#pragma unroll
+      for (int i = 0; i < kPairs; ++i) {
+        const int ia = ln.first(i, p.pairs), ib = ln.second(i, p.pairs);
+        if (ia < p.N) sums[warp * p.N + ia] = da[i];
+        if (ib < p.N) sums[warp * p.N + ib] = db[i];
+      }
+    }
+    __syncthreads();
+    for (int c = threadIdx.x; c < p.N; c += kRopeThreads) {
+      float v = 0.0f;
+#pragma unroll
+      for (int w = 0; w < kRopeWarps; ++w) v += sums[w * p.N + c];
+      sd.partial[(long long)blockIdx.x * p.N + c] = v;
+    }
+    __syncthreads();   // before the tables are written again
+  }
+}
+
+// dw of 32 channels of Q (blockIdx.y = 0) or K: 32 threads a channel, each over its share of the CTAs in order.
+__global__ void __launch_bounds__(1024) rope_grad_kernel(const float* q_parts, const float* k_parts, int n_parts, int N,
+                                                         void* dqw, void* dkw, int type) {
+  __shared__ float sum[32][33];
+  griddep_wait();
+  const float* const parts = blockIdx.y ? k_parts : q_parts;
+  void* const out = blockIdx.y ? dkw : dqw;
+  if (parts == nullptr) return;
+  const int c = blockIdx.x * 32 + (threadIdx.x & 31), g = threadIdx.x >> 5;
+  float v = 0.0f;
+  if (c < N)
+    for (int i = g; i < n_parts; i += 32) v += parts[(long long)i * N + c];
+  sum[g][threadIdx.x & 31] = v;
+  __syncthreads();
+  v = sum[threadIdx.x & 31][g];
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+  const int mine = blockIdx.x * 32 + g;
+  if ((threadIdx.x & 31) != 0 || mine >= N) return;
+  if (type == kF32) reinterpret_cast<float*>(out)[mine] = v;
+  else if (type == kBF16) reinterpret_cast<__nv_bfloat16*>(out)[mine] = __float2bfloat16(v);
+  else reinterpret_cast<__half*>(out)[mine] = __float2half(v);
+}
+
+template <class T>
+cudaError_t launch_bwd(const RopeParams& p, int ctas, bool vec, bool next, cudaStream_t stream) {
+  return with_rope_map(vec, next, p.N, [&](auto map, auto pairs) {
+    const size_t tables = (size_t)kRopeWarps * p.table * sizeof(float2), sums = (size_t)kRopeWarps * p.N * sizeof(float);
+    constexpr int kPairs = decltype(pairs)::value;
+    return launch_dependent(rope_bwd_kernel<T, decltype(map)::value, kPairs>, dim3((unsigned)ctas), kRopeThreads,
+                            kPairs / 2 * 32 * sizeof(float4) + (tables > sums ? tables : sums), stream, p);
+  });
+}
+
+}  // namespace
+
+int rope_bwd_ctas(int B, int S, int Hq, int Hk) {
+  const long long warps = ((long long)B * S * (Hq > Hk ? Hq : Hk) + 3) / 4;
+  const long long ctas = (warps + kRopeWarps - 1) / kRopeWarps;
+  return ctas < 2 * 152 ? (int)ctas : 2 * 152;
+}
+
+cudaError_t launch_qk_norm_rope_bwd(const RopeArgs& a, float* workspace, cudaStream_t stream) {
+  RopeParams p;
+  rope_params(p, a);
+  const bool vec = rope_shape(p, a, true);
+  const int ctas = rope_bwd_ctas(a.B, a.S, a.side[0].H, a.side[1].H);
+  const int heads = a.side[0].H > a.side[1].H ? a.side[0].H : a.side[1].H;
+  p.per_unit = (heads + p.slots - 1) / p.slots * p.slots;
+  while (p.per_unit > p.slots && (long long)p.tokens * ((heads + p.per_unit - 1) / p.per_unit) < 152 * 32)
+    p.per_unit = (p.per_unit / 2 + p.slots - 1) / p.slots * p.slots;
+  for (int i = 0; i < 2; ++i) {
+    p.side[i].parts = (a.side[i].H + p.per_unit - 1) / p.per_unit;
+    if (a.side[i].H > 0 && a.side[i].dw != nullptr) p.side[i].partial = workspace + (size_t)i * ctas * a.N;
+  }
+  cudaError_t e = a.type == kF32    ? launch_bwd<float>(p, ctas, vec, a.interleaved, stream)
+                  : a.type == kBF16 ? launch_bwd<__nv_bfloat16>(p, ctas, vec, a.interleaved, stream)
+                                    : launch_bwd<__half>(p, ctas, vec, a.interleaved, stream);
+  if (e != cudaSuccess || (p.side[0].partial == nullptr && p.side[1].partial == nullptr)) return e;
+  return launch_dependent(rope_grad_kernel, dim3((unsigned)(a.N + 31) / 32, 2), 1024, 0, stream,
+                          static_cast<const float*>(p.side[0].partial), static_cast<const float*>(p.side[1].partial), ctas,
+                          a.N, a.side[0].dw, a.side[1].dw, a.w_type);
+}
+
+}  // namespace sa
