@@ -36,7 +36,8 @@
  * with the gradients of weight and bias).
  *
  * Between a projection and attention: rope_fwd, rope_bwd (rotary positions), qk_norm_rope_fwd and qk_norm_rope_bwd
- * (the norm of each head of Q and K with the rotation in the same pass).
+ * (the norm of each head of Q and K with the rotation in the same pass).  For serving: kv4_write, kv4_read (a paged
+ * K/V cache in 4 bits) and attn_fwd_kv4 (attention of one or a few tokens of each request over it).
  *
  * Beyond those: sage_prepare_smooth_k (K smoothing before the INT8
  * quantisation), sage_prepare_smoothed with sage_attn_fwd_smooth_q and
@@ -595,6 +596,76 @@ ATTN_API attn_status qk_norm_rope_bwd(const void* dq_out, const void* dk_out, co
                                       const int64_t pos_str[3], int axes, const uint64_t* freq, int rope_dim,
                                       int interleaved, float magnitude, int dtype, int w_dtype, void* workspace,
                                       size_t workspace_bytes, attn_stream_t stream);
+
+/*
+ * The K/V cache in 4 bits: 4.5 bits a value, 144 bytes a token and key head for K and V together.
+ *   cache   : device [num_pages, Hkv, page_size / 16, 2304 bytes], contiguous, 16-byte aligned, owned by the caller
+ *             (kv4_cache_size bytes).  A record of 2304 bytes holds 16 tokens:
+ *               bytes [0, 1024)     K's codes, 64 bytes a token; of them, the 32-bit word 4 t + g holds channels
+ *                                   32 g + 8 t + i at its bits 4 i (t, g = 0..3, i = 0..7)
+ *               bytes [1024, 2048)  V's codes; token j's are 8 bytes each at 1024 + 512 (j / 8) + 16 (4 r + j % 8 / 2) +
+ *                                   8 (j % 2), r = 0..7: four 16-bit values, g = 0..3, with channels 32 g + 4 r + i at
+ *                                   bits 4 i (i = 0..3)
+ *               bytes [2048, 2304)  16 bytes a token: BF16 scales of K's four groups of 32 channels, then of V's
+ *             A code c stands for (c - 8) scale.  scale = -x / 8, x the group's value of largest magnitude (the positive
+ *             one of two; a group below 2^-100 is zeros), exact in BF16; c - 8 = the nearest integer to value / scale,
+ *             ties to even, within [-8, 7].
+ *   page_table : device int32 [B, max_pages], rows table_str elements apart: token j of request b is in page
+ *             page_table[b, j / page_size].  An entry outside [0, num_pages) has no page: what is written there is dropped,
+ *             its tokens read as zeros, and attention does not see their keys.  max_pages * page_size <= 2^30.
+ *   page_size : a positive multiple of 16
+ */
+/* kv4_cache_size -- bytes of a cache. */
+ATTN_API size_t kv4_cache_size(int num_pages, int Hkv, int page_size);
+
+/*
+ * kv4_write -- quantise K and V of new tokens into the cache: token i < count[b] of request b becomes its token
+ * start[b] + i.  Tokens before 0 or past the table's row are dropped; no byte of another token is written.
+ *   k, v    : const BF16 [B, S, Hkv, 128], finite (rows from count[b] on may hold anything), strides k_str / v_str
+ *   start   : device int32 [B];  count : device int32 [B], clamped to [0, S], or NULL: S
+ * No two tokens of a call may have one place (requests may share the pages that they only read).  B, S or Hkv of 0:
+ * nothing is done.  Enqueues one kernel on `stream`.
+ */
+ATTN_API attn_status kv4_write(const void* k, const void* v, void* cache, int num_pages, int page_size,
+                               const int32_t* page_table, int64_t table_str, int max_pages, const int32_t* start,
+                               const int32_t* count, int B, int S, int Hkv, int D, const int64_t k_str[3],
+                               const int64_t v_str[3], attn_stream_t stream);
+
+/*
+ * kv4_read -- the values that tokens start[b] + i, i < count[b], of each request stand for, rounded to BF16 once; zeros
+ * for i >= count[b] and for tokens without a place.  For prompts in pieces: a request's cached keys beside new ones in
+ * attn_fwd_bf16_lse.
+ *   k, v    : BF16 [B, S, Hkv, 128] outputs, strides k_str / v_str; every row is written; they do not overlap
+ *   the rest as kv4_write
+ */
+ATTN_API attn_status kv4_read(const void* cache, int num_pages, int page_size, const int32_t* page_table,
+                              int64_t table_str, int max_pages, const int32_t* start, const int32_t* count, void* k, void* v,
+                              int B, int S, int Hkv, int D, const int64_t k_str[3], const int64_t v_str[3],
+                              attn_stream_t stream);
+
+/* attn_fwd_kv4_workspace_size -- bytes of device scratch attn_fwd_kv4 needs (0 for an empty problem). */
+ATTN_API size_t attn_fwd_kv4_workspace_size(int B, int Sq, int Hq, int Hkv, int max_pages, int page_size);
+
+/*
+ * attn_fwd_kv4 -- attention of the last Sq tokens of each request over its cache:
+ *   query i of request b sees the keys j < kv_len[b], with causal those j < kv_len[b] - Sq + i + 1
+ *   lse, O  : as attn_fwd_bf16_lse, of the values that the cache stands for; a row that sees no key has O = 0, lse = -inf
+ *   q, o    : BF16 [B, Sq, Hq, 128], strides q_str / o_str, q finite; o does not overlap q
+ *   lse     : float [B, Hq, Sq] output, contiguous
+ *   kv_len  : device int32 [B], each request's tokens in the cache, the new ones included; clamped to
+ *             [0, max_pages * page_size].  Hq a multiple of Hkv; query head h reads key head h / (Hq / Hkv).
+ *   causal  : 0 or 1
+ *   workspace : at least attn_fwd_kv4_workspace_size bytes, 16-byte aligned; overwritten; one for each call under way
+ * Made for one or a few tokens a request: 16 queries (Sq * Hq / Hkv) share one read of the cache, more read it again.
+ * For a long piece of a prompt, kv4_read and attn_fwd_bf16_lse.  Q takes part in FP16 with its row's largest magnitude
+ * scaled into [1, 2), products with the codes are exact, P times V's scale is rounded to BF16, sums are FP32 in a fixed
+ * order (the same inputs give the same bits), O is rounded once.  Enqueues two kernels on `stream`.
+ */
+ATTN_API attn_status attn_fwd_kv4(const void* q, const void* cache, int num_pages, int page_size,
+                                  const int32_t* page_table, int64_t table_str, int max_pages, const int32_t* kv_len,
+                                  void* o, float* lse, int B, int Sq, int Hq, int Hkv, int D, const int64_t q_str[3],
+                                  const int64_t o_str[3], float softmax_scale, int causal, void* workspace,
+                                  size_t workspace_bytes, attn_stream_t stream);
 
 /*
  * attn_get_device_status -- synchronise `stream`, then read and clear the

@@ -19,6 +19,9 @@ library has not been built, every call raises.
     rope_fwd(q, k, freq, positions)   -> q', k'             (rotary positions; rope_bwd: their gradients)
     qk_norm_rope_fwd(q, k, q_weight, k_weight, freq, positions) -> q', k'
     qk_norm_rope_bwd(dq', dk', q, k, q_weight, k_weight, freq, positions) -> dq, dk, dq_weight, dk_weight
+    kv4_cache(num_pages, kv_heads, page_size) -> cache      (a paged K/V cache in 4 bits)
+    kv4_write(k, v, cache, page_table, start), kv4_read(cache, page_table, start, S) -> k, v
+    attn_fwd_kv4(q, cache, page_table, kv_len) -> O, lse    (one or a few tokens of each request over it)
 """
 from __future__ import annotations
 
@@ -37,6 +40,7 @@ __all__ = ["AttnError", "attn_fwd_bf16", "sage_prepare", "sage_prepare_noalloc",
            "Prepared", "e4m3_encode", "attn_fwd_bf16_lse", "attn_bwd_bf16", "attn_bwd_workspace",
            "layer_norm_fwd", "layer_norm_bwd", "layer_norm_bwd_workspace", "rope_frequencies",
            "rope_fwd", "rope_bwd", "qk_norm_rope_fwd", "qk_norm_rope_bwd", "qk_norm_rope_bwd_workspace",
+           "kv4_cache", "kv4_write", "kv4_read", "attn_fwd_kv4", "attn_fwd_kv4_workspace",
            "sage_padded_len", "attn_get_device_status", "lib", "STATUS"]
 
 STATUS = {0: "ATTN_OK", 1: "ATTN_ERR_INVALID_ARG", 2: "ATTN_ERR_ALIGNMENT", 3: "ATTN_ERR_UNSUPPORTED",
@@ -127,7 +131,13 @@ def lib() -> ctypes.CDLL:
                 ("qk_norm_rope_fwd", i, [_vp] * 6 + [i] * 5 + [_vp] * 4 + [f32, _vp, _vp, i, _vp, i, i, f32, i, i, _vp]),
                 ("qk_norm_rope_bwd_workspace_size", size, [i] * 5),
                 ("qk_norm_rope_bwd", i, [_vp] * 10 + [i] * 5 + [_vp] * 6 + [f32, _vp, _vp, i, _vp, i, i, f32, i, i, _vp,
-                                                                            size, _vp])):
+                                                                            size, _vp]),
+                ("kv4_cache_size", size, [i] * 3),
+                ("kv4_write", i, [_vp] * 3 + [i, i, _vp, ctypes.c_int64, i, _vp, _vp] + [i] * 4 + [_vp] * 3),
+                ("kv4_read", i, [_vp, i, i, _vp, ctypes.c_int64, i, _vp, _vp, _vp, _vp] + [i] * 4 + [_vp] * 3),
+                ("attn_fwd_kv4_workspace_size", size, [i] * 6),
+                ("attn_fwd_kv4", i, [_vp, _vp, i, i, _vp, ctypes.c_int64, i, _vp, _vp, _vp] + [i] * 5
+                 + [_vp, _vp, f32, i, _vp, size, _vp])):
             if hasattr(L, name):
                 fn = getattr(L, name)
                 fn.argtypes, fn.restype = args, res
@@ -962,6 +972,139 @@ def qk_norm_rope_bwd(dq_out: torch.Tensor, dk_out: torch.Tensor | None, q: torch
                                   0 if freq is None else 2 * freq.shape[0], interleaved, magnitude, _DTYPES[q.dtype],
                                   _DTYPES[w_type], workspace.data_ptr() if size else None, size, _current_stream(dev)))
     return dq, dk, grads[0], grads[1]
+
+
+_KV4_RECORD = 2304   # bytes of 16 tokens of a key head, K and V
+
+
+def kv4_cache(num_pages: int, kv_heads: int, page_size: int, device="cuda") -> torch.Tensor:
+    """A K/V cache in 4 bits: uint8 [num_pages, kv_heads, page_size / 16, 2304], 144 bytes a token and head.  page_size: a
+    multiple of 16.  Tokens that were never written are zeros."""
+    if page_size < 16 or page_size % 16:
+        raise ValueError(f"page_size must be a positive multiple of 16, got {page_size}")
+    return torch.zeros((num_pages, kv_heads, page_size // 16, _KV4_RECORD), dtype=torch.uint8, device=device)
+
+
+def _kv4_args(cache, page_table, B: int):
+    """(pages, heads, page size, table's row stride, pages a request, device)."""
+    dev = _cuda_index("cache", cache)
+    if cache.dim() != 4 or cache.shape[3] != _KV4_RECORD or cache.dtype is not torch.uint8 or not cache.is_contiguous():
+        raise ValueError(f"cache must be contiguous uint8 [pages, heads, page_size / 16, {_KV4_RECORD}], got "
+                         f"{tuple(cache.shape)} {cache.dtype}")
+    if page_table.dim() != 2:
+        raise ValueError(f"page_table must be [B, pages], got {tuple(page_table.shape)}")
+    most = page_table.shape[1]
+    _expect("page_table", page_table, (B, most), torch.int32, dev)
+    if most > 1 and page_table.stride(1) != 1:
+        raise ValueError("page_table must have unit stride along a request's pages")
+    pages, heads, tiles, _ = cache.shape
+    if max(pages, heads, 16 * tiles, B, most) > 0x7fffffff:
+        _sizes(pages, heads, 16 * tiles, B, most)
+    return pages, heads, 16 * tiles, page_table.stride(0), most, dev
+
+
+def _kv4_rows(name: str, t: torch.Tensor, shape, dev: int):
+    _expect(name, t, shape, torch.bfloat16, dev)
+
+
+def kv4_write(k: torch.Tensor, v: torch.Tensor, cache: torch.Tensor, page_table: torch.Tensor, start: torch.Tensor,
+              count: torch.Tensor | None = None, stream=None) -> None:
+    """Quantise k and v, BF16 [B, S, kv_heads, 128], into the cache: token i of request b becomes its token start[b] + i.
+
+    page_table: int32 [B, pages], the request's pages in order (an entry that is no page of the cache: its tokens are
+    dropped).  start, count: int32 [B] on the device; tokens from count[b] on are padding (None: all are real).  Groups of 32
+    channels share a BF16 scale, -x / 8 with x the value of largest magnitude; nothing of other tokens is written."""
+    if k.dim() != 4:
+        raise ValueError(f"k must be [B, S, H, D], got {tuple(k.shape)}")
+    B, S, _, D = k.shape
+    pages, heads, page_size, table_str, most, dev = _kv4_args(cache, page_table, B)
+    if _elsewhere(dev, stream):
+        with _there(dev, stream):
+            return kv4_write(k, v, cache, page_table, start, count)
+    _sizes(S, D)
+    _kv4_rows("k", k, (B, S, heads, D), dev)
+    _kv4_rows("v", v, (B, S, heads, D), dev)
+    _expect_dense("start", start, (B,), torch.int32, dev)
+    if count is not None:
+        _expect_dense("count", count, (B,), torch.int32, dev)
+    strides = _strides("k v", k, v)
+    at = strides.buffer_info()[0]
+    _check(lib().kv4_write(k.data_ptr(), v.data_ptr(), cache.data_ptr(), pages, page_size, page_table.data_ptr(), table_str,
+                           most, start.data_ptr(), _ptr(count), B, S, heads, D, at, at + 32, _current_stream(dev)))
+
+
+def kv4_read(cache: torch.Tensor, page_table: torch.Tensor, start: torch.Tensor, S: int,
+             count: torch.Tensor | None = None, k: torch.Tensor | None = None, v: torch.Tensor | None = None,
+             stream=None) -> tuple[torch.Tensor, torch.Tensor]:
+    """(K, V), BF16 [B, S, kv_heads, 128]: what tokens start[b] to start[b] + S - 1 of each request stand for; zeros from
+    count[b] on and where there is no page."""
+    B = page_table.shape[0]
+    pages, heads, page_size, table_str, most, dev = _kv4_args(cache, page_table, B)
+    if _elsewhere(dev, stream):
+        with _there(dev, stream):
+            return kv4_read(cache, page_table, start, S, count, k, v)
+    _sizes(S)
+    shape = (B, S, heads, 128)
+    k = torch.empty(shape, dtype=torch.bfloat16, device=dev) if k is None else k
+    v = torch.empty(shape, dtype=torch.bfloat16, device=dev) if v is None else v
+    _kv4_rows("k", k, shape, dev)
+    _kv4_rows("v", v, shape, dev)
+    _expect_dense("start", start, (B,), torch.int32, dev)
+    if count is not None:
+        _expect_dense("count", count, (B,), torch.int32, dev)
+    strides = _strides("k v", k, v)
+    at = strides.buffer_info()[0]
+    _check(lib().kv4_read(cache.data_ptr(), pages, page_size, page_table.data_ptr(), table_str, most, start.data_ptr(),
+                          _ptr(count), k.data_ptr(), v.data_ptr(), B, S, heads, 128, at, at + 32, _current_stream(dev)))
+    return k, v
+
+
+def attn_fwd_kv4_workspace(B: int, Sq: int, Hq: int, cache: torch.Tensor, page_table: torch.Tensor) -> torch.Tensor:
+    """Scratch for attn_fwd_kv4 of these shapes; calls on different streams need one each."""
+    _, heads, page_size, _, most, dev = _kv4_args(cache, page_table, B)
+    _sizes(Sq, Hq)
+    return torch.empty(lib().attn_fwd_kv4_workspace_size(B, Sq, Hq, heads, most, page_size), dtype=torch.uint8, device=dev)
+
+
+def attn_fwd_kv4(q: torch.Tensor, cache: torch.Tensor, page_table: torch.Tensor, kv_len: torch.Tensor,
+                 softmax_scale: float | None = None, causal: bool = True, out: torch.Tensor | None = None,
+                 lse: torch.Tensor | None = None, workspace: torch.Tensor | None = None,
+                 stream=None) -> tuple[torch.Tensor, torch.Tensor]:
+    """(O, lse) of the last Sq tokens of each request, q BF16 [B, Sq, Hq, 128], over its cache in 4 bits; lse float32
+    [B, Hq, Sq] the rows' natural log-sum-exp.
+
+    kv_len: int32 [B] on the device, the request's tokens in the cache, the new ones included.  causal: query i sees the keys
+    j <= kv_len[b] - Sq + i.  Hq a multiple of the cache's heads.  A row that sees no key has O = 0 and lse = -inf.  One or
+    a few tokens a request; for long pieces of a prompt see kv4_read.  The same inputs give the same bits."""
+    if q.dim() != 4:
+        raise ValueError(f"q must be [B, S, H, D], got {tuple(q.shape)}")
+    B, Sq, Hq, D = q.shape
+    pages, heads, page_size, table_str, most, dev = _kv4_args(cache, page_table, B)
+    if _elsewhere(dev, stream):
+        with _there(dev, stream):
+            return attn_fwd_kv4(q, cache, page_table, kv_len, softmax_scale, causal, out, lse, workspace)
+    _sizes(Sq, Hq, D)
+    _kv4_rows("q", q, q.shape, dev)
+    _expect_dense("kv_len", kv_len, (B,), torch.int32, dev)
+    if out is None:
+        out = torch.empty(q.shape, dtype=torch.bfloat16, device=dev)
+    else:
+        _expect("out", out, q.shape, torch.bfloat16, dev)
+    rows = (B, Hq, Sq)
+    if lse is None:
+        lse = torch.empty(rows, dtype=torch.float32, device=dev)
+    else:
+        _expect_dense("lse", lse, rows, torch.float32, dev)
+    if workspace is None:
+        workspace = torch.empty(lib().attn_fwd_kv4_workspace_size(B, Sq, Hq, heads, most, page_size), dtype=torch.uint8,
+                                device=dev)
+    strides = _strides("q out", q, out)
+    at = strides.buffer_info()[0]
+    _check(lib().attn_fwd_kv4(q.data_ptr(), cache.data_ptr(), pages, page_size, page_table.data_ptr(), table_str, most,
+                              kv_len.data_ptr(), out.data_ptr(), lse.data_ptr(), B, Sq, Hq, heads, D, at, at + 32,
+                              D ** -0.5 if softmax_scale is None else softmax_scale, causal, workspace.data_ptr(),
+                              _scratch("workspace", workspace, dev), _current_stream(dev)))
+    return out, lse
 
 
 def attn_selftest_wait_timeout(device=None, stream=None) -> str:

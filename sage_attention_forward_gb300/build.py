@@ -19,10 +19,10 @@ CSRC = os.path.join(HERE, "csrc")
 OUT_DIR = os.path.join(HERE, "_build")
 LIB = os.path.join(OUT_DIR, "libsageattn.so")
 SOURCES = ["api.cu", "attn_fwd.cu", "sage_prepare.cu", "attn_lse.cu", "attn_bwd.cu", "layer_norm.cu", "qk_rope.cu",
-           "qk_rope_bwd.cu"]
-HOST_SOURCES = ["api_train.cpp", "api_rope.cpp"]   # no kernels
+           "qk_rope_bwd.cu", "kv4_cache.cu", "kv4_attn.cu"]
+HOST_SOURCES = ["api_train.cpp", "api_rope.cpp", "api_kv4.cpp"]   # no kernels
 HEADERS = ["ptx.cuh", "ptx_train.cuh", "kernels.h", "api_checks.h", "api_overlap.h", "qk_quant.cuh", "attn_tiles.cuh",
-           "pieces.cuh", "qk_rope.cuh"]
+           "pieces.cuh", "qk_rope.cuh", "kv4.cuh"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
 

@@ -270,6 +270,33 @@ cudaError_t launch_rope_fwd(const RopeArgs& a, bool norm, cudaStream_t stream);
 int rope_bwd_ctas(int B, int S, int Hq, int Hk);
 cudaError_t launch_qk_norm_rope_bwd(const RopeArgs& a, float* workspace, cudaStream_t stream);
 
+// The K/V cache in 4 bits (kv4_cache.cu, kv4_attn.cu).
+struct Kv4Args {
+  void* cache;                  // [num_pages][Hkv][page_size / 16][2304 bytes]
+  const int* table;             // [B][max_pages], rows table_str apart
+  long long table_str;
+  int num_pages, max_pages, page_size, B, S, Hkv;
+  // writing and reading
+  const void *k = nullptr, *v = nullptr;      // BF16 [B, S, Hkv, 128]
+  void *k_out = nullptr, *v_out = nullptr;
+  long long k_str[3], v_str[3];
+  const int *start = nullptr, *count = nullptr;
+  // attention: S queries of a request
+  const void* q = nullptr;
+  void* o = nullptr;
+  float* lse = nullptr;         // [B, Hq, S]
+  const int* kv_len = nullptr;
+  int Hq = 0, causal = 0;
+  long long q_str[3], o_str[3];
+  float c_log2 = 0.0f;          // softmax_scale log2 e
+};
+// Records that S tokens from anywhere on can touch.
+inline int kv4_tiles(int S) { return (int)(((long long)S + 14) / 16 + 1); }
+cudaError_t launch_kv4_write(const Kv4Args& a, cudaStream_t stream);
+cudaError_t launch_kv4_read(const Kv4Args& a, cudaStream_t stream);
+size_t attn_kv4_workspace(int B, int S, int Hq, int Hkv, int max_pages, int page_size);
+cudaError_t launch_attn_kv4(const Kv4Args& a, void* workspace, cudaStream_t stream);
+
 // The order of a grid's items (tile, head): `group` heads go together, tile by tile.  One head after another
 // (group = 1) keeps few heads' tiles in L2.  Where a causal mask makes the first tiles of a head the longest
 // items, several heads' long ones come before their short ones, so that the grid ends with short
