@@ -657,9 +657,9 @@ ATTN_API size_t attn_fwd_kv4_workspace_size(int B, int Sq, int Hq, int Hkv, int 
  *   causal  : 0 or 1
  *   workspace : at least attn_fwd_kv4_workspace_size bytes, 16-byte aligned; overwritten; one for each call under way
  * Made for one or a few tokens a request: 16 queries (Sq * Hq / Hkv) share one read of the cache, more read it again.
- * For a long piece of a prompt, kv4_read and attn_fwd_bf16_lse.  Q takes part in FP16 with its row's largest magnitude
- * scaled into [1, 2), products with the codes are exact, P times V's scale is rounded to BF16, sums are FP32 in a fixed
- * order (the same inputs give the same bits), O is rounded once.  Enqueues two kernels on `stream`.
+ * For a long piece of a prompt, kv4_read and attn_fwd_bf16_lse.  Q takes part as two e4m3 terms: a row's values
+ * keep 8 bits down to 2^-14 of its largest, smaller ones are off by up to 2^-22 of it.  Products with the codes are exact, P
+ * times V's scale is rounded to BF16, sums are FP32 in a fixed order (the same inputs give the same bits), O is rounded once.  Enqueues two kernels on `stream`.
  */
 ATTN_API attn_status attn_fwd_kv4(const void* q, const void* cache, int num_pages, int page_size,
                                   const int32_t* page_table, int64_t table_str, int max_pages, const int32_t* kv_len,

@@ -2,15 +2,16 @@
 //
 // Bound by memory: 144 bytes of cache a token and key head, read once for all queries that share the head.
 //
-// Products.  Keys (and V's channels) are the rows of mma.m16n8k16, the queries of a key head (tokens x heads that share it)
-// its columns, eight at a time: with few queries no part of a product is empty.  Codes become matrix operands without a
-// conversion: four bits put into the mantissa of a constant are the value constant + code (FP16 256 + c and 16 + c for K, BF16
-// 16 + c for V; one shift and one masked insert for two values).  What the constants add is taken off exactly: for K the
-// accumulators start at -(constant + 8) q summed over the channels, a product of the same operands; for V a product with
-// rows of 24s gives 24 sum p for each group of channels.
-//   S^T = sum_g scale_K[key, g] (codes_g q_g)        four products of 32 channels, scaled in FP32
-//   O^T[group g] = sum_j codes (p_j scale_V[j, g])   P is scaled for each group in FP32, then rounded to BF16 once
-// Q becomes FP16 with its row's largest magnitude in [1, 2): its own 8 bits stay (below 2^-24 of that magnitude they round).
+// Products.  Keys (and V's channels) are the rows of the mma, the queries of a key head (tokens x heads that share it) its
+// columns: with few queries no part of a product is empty, and each code is unpacked once for all of them.
+//   S^T = sum_g scale_K[key, g] (codes_g q_g)        m16n8k32 in e4m3, one for each 32 channels, scaled in FP32
+//   O^T[group g] = sum_j codes (p_j scale_V[j, g])   m16n8k16 in BF16; P is scaled for each group in FP32, then rounded once
+// A 4-bit code in the low half of a byte is the e4m3 value code / 512, subnormal or not: K's codes become operands by a mask
+// and a shift, eight of them at a time.  Q, scaled so that its row's largest magnitude is in [128, 256), is the sum of two
+// e4m3 terms, 4 bits of it and the 4 bits below (kept 32 times as large); the terms are neighbouring columns, so that a lane has
+// both parts of its scores.  What is below 2^-16 of the row's largest magnitude rounds.  The codes' bias of 8 is taken off by
+// accumulators that start at -8 q summed over the channels, a product of the same operands.  V's codes are put into the
+// mantissa of BF16 128 and 136 subtracted, exactly.
 //
 // Work.  The records of all requests and heads are one line of work; each CTA takes an equal share of it, found from the
 // lengths on the device, so that ragged batches are balanced and a graph serves any lengths.  A CTA's warps take its
@@ -28,6 +29,7 @@ namespace {
 constexpr int kWarps = 4, kThreads = kWarps * 32;
 constexpr int kStages = 4;
 constexpr int kLeast = 4;           // records a CTA takes at least
+constexpr float kLow = 32.0f;       // Q's second term is kept this much larger
 constexpr float kSlack = 8.0f;      // a row's reference maximum is raised when one passes it by more (log2 units)
 constexpr int kDim = 128;
 
@@ -58,12 +60,14 @@ template <int kLeft>
 __device__ __forceinline__ void cp_async_wait() {
   asm volatile("cp.async.wait_group %0;" ::"n"(kLeft) : "memory");
 }
-__device__ __forceinline__ void mma_f16(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
-                                        uint32_t b1) {
+// d = a b + (c0, c1) for both of a lane's rows
+__device__ __forceinline__ void mma_e4m3(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
+                                         uint32_t b1, float c0, float c1) {
   asm volatile(
-      "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
-      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
-      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+      "mma.sync.aligned.m16n8k32.row.col.f32.e4m3.e4m3.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+      "{%10, %11, %10, %11};"
+      : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(c0), "f"(c1));
 }
 __device__ __forceinline__ void mma_bf16(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
                                          uint32_t b1) {
@@ -78,27 +82,25 @@ __device__ __forceinline__ uint32_t transpose8(uint32_t x) {
   asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
   return y;
 }
-// (x & mask) | bits
-template <uint32_t kMask, uint32_t kBits>
-__device__ __forceinline__ uint32_t insert(uint32_t x) {
-  uint32_t y;
-  asm("lop3.b32 %0, %1, %2, %3, 0xEA;" : "=r"(y) : "r"(x), "n"(kMask), "n"(kBits));
-  return y;
-}
-// K: eight codes as FP16 pairs (i, i + 4): 256 + c for i = 0 and 2, 16 + c for i = 1 and 3.
-__device__ __forceinline__ void k_pairs(uint32_t w, uint32_t (&a)[4]) {
-  const uint32_t x = w << 2, y = w >> 6;
-  a[0] = insert<0x003c003cu, 0x5c005c00u>(x);
-  a[1] = insert<0x03c003c0u, 0x4c004c00u>(x);
-  a[2] = insert<0x003c003cu, 0x5c005c00u>(y);
-  a[3] = insert<0x03c003c0u, 0x4c004c00u>(y);
-}
-// V: four codes of each of two tokens as BF16 pairs 16 + c.
+// V: four codes of each of two tokens, 4 bits each in halves of x, as BF16 pairs of code - 8.
 __device__ __forceinline__ void v_pairs(uint32_t x, uint32_t (&a)[4]) {
-  a[0] = insert<0x00780078u, 0x41804180u>(x << 3);
-  a[1] = insert<0x00780078u, 0x41804180u>(x >> 1);
-  a[2] = insert<0x00780078u, 0x41804180u>(x >> 5);
-  a[3] = insert<0x00780078u, 0x41804180u>(x >> 9);
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    uint32_t y;
+    asm("lop3.b32 %0, %1, 0x000f000f, 0x43004300, 0xEA;" : "=r"(y) : "r"(x >> (4 * i)));   // (x & mask) | 128
+    asm("fma.rn.bf16x2 %0, %1, %2, %3;" : "=r"(a[i]) : "r"(y), "r"(0x3f803f80u), "r"(0xc308c308u));   // y - 136
+  }
+}
+// Two values as e4m3 (a in the low byte), and back.
+__device__ __forceinline__ uint32_t e4m3_pair(float a, float b) {
+  unsigned short d;
+  asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(d) : "f"(b), "f"(a));
+  return d;
+}
+__device__ __forceinline__ float2 of_e4m3_pair(uint32_t d) {
+  uint32_t h;
+  asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h) : "h"((unsigned short)d));
+  return __half22float2(*reinterpret_cast<const __half2*>(&h));
 }
 __device__ __forceinline__ void scales_of(uint32_t w, float& a, float& b) {
   a = __uint_as_float(w << 16);
@@ -107,10 +109,6 @@ __device__ __forceinline__ void scales_of(uint32_t w, float& a, float& b) {
 
 __device__ __forceinline__ int tokens_of(const AttnParams& p, int b) { return min(max(__ldg(p.kv_len + b), 0), p.capacity); }
 
-// The line of work: request b's records, once for each of its segments.
-struct Line {
-  long long total, share;   // records, and those of a CTA
-};
 // Sums v over the CTA's threads up to and including this one; total: all of them.
 __device__ __forceinline__ long long scan(long long v, long long* warp_sums, long long& total) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
@@ -131,18 +129,13 @@ __device__ __forceinline__ long long scan(long long v, long long* warp_sums, lon
   return v;
 }
 
-template <int kCols>   // columns of eight queries
-struct Tile {
-  float o[4][2][kCols][4];   // [group][pair of channel rows][column]: O^T
-  float sum[kCols][4];       // 24 sum p scale of group r (the lane's row) for the lane's two queries
-  float m[kCols][2], l[kCols][2];
-};
-
-template <int kCols>
-__global__ void __launch_bounds__(kThreads, kCols == 1 ? 3 : 2) kv4_attn_kernel(const __grid_constant__ AttnParams p) {
-  constexpr int kRows = 8 * kCols;
+// kFours: queries of a CTA, four at a time (1, 2 or 4).
+template <int kFours>
+__global__ void __launch_bounds__(kThreads, kFours == 1 ? 4 : kFours == 2 ? 3 : 2) kv4_attn_kernel(const __grid_constant__ AttnParams p) {
+  constexpr int kRows = 4 * kFours;
+  constexpr int kCols = (kFours + 1) / 2;                  // columns of eight in the product with V
   constexpr int kRing = kStages * kKvRecord;
-  constexpr int kJoin = (kRows * kDim + 2 * kRows) * 4;   // a warp's O, m and l
+  constexpr int kJoin = (kRows * kDim + 2 * kRows) * 4;    // a warp's O, m and l
   __shared__ __align__(16) unsigned char ring[kWarps][kRing > kJoin ? kRing : kJoin];
   __shared__ long long warp_sums[kWarps];
   __shared__ long long s_before;
@@ -209,13 +202,13 @@ __global__ void __launch_bounds__(kThreads, kCols == 1 ? 3 : 2) kv4_attn_kernel(
     const int head = div_by(seg, p.by_row_tiles), row0 = (seg - head * p.row_tiles) * kRows;
     at = seg_start + hi;
 
-    // queries: B operands of K's products, and the constants' part of them
-    uint32_t qf[kCols][4][4];
-    float off[kCols][4][2], factor[kCols][2];
-    int limit[kCols][2], all = len;   // keys before `all` are seen by every query of the tile
+    // queries: the column of this lane holds one of two terms of query r / 2 (of each four)
+    uint32_t qf[kFours][4][2];
+    float off[kFours][4][2], factor[kFours];
+    int limit[kFours], all = len;   // keys before `all` are seen by every query of the tile
 #pragma unroll
-    for (int n = 0; n < kCols; ++n) {
-      const int row = row0 + 8 * n + r;
+    for (int n = 0; n < kFours; ++n) {
+      const int row = row0 + 4 * n + (r >> 1);
       const int s = div_by(row, p.G), g0 = row - s * (int)p.G.d;
       uint4 raw[4] = {};
       if (row < p.rows) {
@@ -227,65 +220,80 @@ __global__ void __launch_bounds__(kThreads, kCols == 1 ? 3 : 2) kv4_attn_kernel(
       float top = 0.0f;
 #pragma unroll
       for (int g = 0; g < 4; ++g) {
-        const uint32_t w[4] = {raw[g].x, raw[g].y, raw[g].z, raw[g].w};
+        float x[8];
+        unpack<__nv_bfloat16>(raw[g], x);
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          float x, y;
-          scales_of(w[i], x, y);
-          top = fmaxf(top, fmaxf(fabsf(x), fabsf(y)));
-        }
+        for (int i = 0; i < 8; ++i) top = fmaxf(top, fabsf(x[i]));
       }
       top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
       top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
-      const int e = min(max((int)(__float_as_uint(top) >> 23), 27), 253);
-      const float down = __uint_as_float((uint32_t)(254 - e) << 23);
+      const int e = max((int)(__float_as_uint(top) >> 23), 27);
+      const float to = __uint_as_float((uint32_t)(261 - e) << 23);   // 2^7 over the power of two in `top`
 #pragma unroll
       for (int g = 0; g < 4; ++g) {
         float x[8];
         unpack<__nv_bfloat16>(raw[g], x);
+        uint32_t term[4];   // of channels (0, 2), (4, 6), (1, 3), (5, 7)
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-          const __half2 h = __floats2half2_rn(x[i] * down, x[i + 4] * down);
-          qf[n][g][i] = *reinterpret_cast<const uint32_t*>(&h);
+          const int c = 4 * (i & 1) + (i >> 1);
+          const float u = x[c] * to, v = x[c + 2] * to;
+          term[i] = e4m3_pair(u, v);
+          const float2 high = of_e4m3_pair(term[i]);
+          if (r & 1) term[i] = e4m3_pair((u - high.x) * kLow, (v - high.y) * kLow);
         }
-        float d[4] = {};
-        mma_f16(d, 0xdc20dc20u, 0xdc20dc20u, 0xce00ce00u, 0xce00ce00u, qf[n][g][0], qf[n][g][1]);   // -264, -24
-        mma_f16(d, 0xdc20dc20u, 0xdc20dc20u, 0xce00ce00u, 0xce00ce00u, qf[n][g][2], qf[n][g][3]);
+        qf[n][g][0] = term[0] | term[1] << 16;
+        qf[n][g][1] = term[2] | term[3] << 16;
+        float d[4];
+        mma_e4m3(d, 0x88888888u, 0x88888888u, 0x88888888u, 0x88888888u, qf[n][g][0], qf[n][g][1], 0.0f, 0.0f);   // -8 / 512
         off[n][g][0] = d[0];
         off[n][g][1] = d[1];
       }
-      const float up = __uint_as_float((uint32_t)e << 23) * p.c_log2;
-#pragma unroll
-      for (int c = 0; c < 2; ++c) {
-        const int col = 2 * t + c, at_row = row0 + 8 * n + col;
-        factor[n][c] = __shfl_sync(0xffffffffu, up, col * 4);
-        const int tok = div_by(at_row, p.G);
-        limit[n][c] = p.causal ? min(len, len - p.S + tok + 1) : len;
-      }
+      // (codes are 1 / 512 of themselves, q 2^7 over its power of two)
+      const float up = __uint_as_float((uint32_t)e << 23) * (4.0f * p.c_log2);
+      factor[n] = __shfl_sync(0xffffffffu, up, 8 * t);
+      const int tok = div_by(row0 + 4 * n + t, p.G);
+      limit[n] = p.causal ? min(len, len - p.S + tok + 1) : len;
     }
     if (p.causal) all = max(0, min(len, len - p.S + div_by(row0, p.G) + 1));
 
-    Tile<kCols> acc = {};
+    // [group][pair of channel rows][column]; kFours = 1: columns 2 t and 2 t + 1 are query t with the scales of an even
+    // and of an odd group, one of which counts; else queries t and t + 4 of eight
+    float acc[4][2][kCols][4] = {};
+    float m[kFours], l[kFours];
 #pragma unroll
-    for (int n = 0; n < kCols; ++n) acc.m[n][0] = acc.m[n][1] = -INFINITY;
+    for (int n = 0; n < kFours; ++n) {
+      m[n] = -INFINITY;
+      l[n] = 0.0f;
+    }
 
-    // the warp's records: lo + warp, and every kWarps-th from there
+    // the warp's records, one after another: [first, last)
+    const int first = lo + (int)((long long)(hi - lo) * warp / kWarps);
+    const int last = lo + (int)((long long)(hi - lo) * (warp + 1) / kWarps);
     unsigned char* const mine = ring[warp];
     uint32_t there = 0;                               // bit of a slot: its record has a page
-    int to_load = lo + warp;
-    int page = to_load < hi ? kv_page(p.pages, b, to_load) : -1;
+    int to_load = first, left = 0, page = -1;         // left: records of the current page
+    const unsigned char* from = nullptr;
+    int next = first < last ? kv_page(p.pages, b, first) : -1;
     auto load = [&](int slot) {
-      there &= ~(1u << slot);
-      if (to_load < hi) {
+      if (to_load < last) {
+        if (left == 0) {
+          page = next;
+          left = (int)p.pages.tiles.d - (to_load - div_by(to_load, p.pages.tiles) * (int)p.pages.tiles.d);
+          if (page >= 0) from = kv_record(p.pages, page, head, to_load) + lane * 16;
+          if (to_load + left < last) next = kv_page(p.pages, b, to_load + left);
+        }
+        there &= ~(1u << slot);
         if (page >= 0) {
           there |= 1u << slot;
-          const unsigned char* const from = kv_record(p.pages, page, head, to_load);
+          unsigned char* const into = mine + slot * kKvRecord + lane * 16;
 #pragma unroll
           for (int i = 0; i < 5; ++i)
-            if (i < 4 || lane < 16) cp_async16(mine + slot * kKvRecord + (lane + 32 * i) * 16, from + (lane + 32 * i) * 16);
+            if (i < 4 || lane < 16) cp_async16(into + i * 512, from + i * 512);
+          from += kKvRecord;
         }
-        to_load += kWarps;
-        if (to_load < hi) page = kv_page(p.pages, b, to_load);
+        ++to_load;
+        --left;
       }
       cp_async_commit();
     };
@@ -293,24 +301,23 @@ __global__ void __launch_bounds__(kThreads, kCols == 1 ? 3 : 2) kv4_attn_kernel(
     for (int i = 0; i < kStages - 1; ++i) load(i);
 
     int slot = 0;
-    for (int tile = lo + warp; tile < hi; tile += kWarps) {
+#pragma unroll 1
+    for (int tile = first; tile < last; ++tile) {
       cp_async_wait<kStages - 2>();
       __syncwarp();
       const bool held = (there >> slot) & 1;
       const unsigned char* const rec = mine + slot * kKvRecord;
-      const int into = slot == 0 ? kStages - 1 : slot - 1;
+      load(slot == 0 ? kStages - 1 : slot - 1);   // (read by all lanes before the warp was last together)
       slot = slot + 1 == kStages ? 0 : slot + 1;
-      if (!held) {   // no page: its keys are not there
-        load(into);
-        continue;
-      }
+      if (!held) continue;   // no page: its keys are not there
       const uint4 k0 = *reinterpret_cast<const uint4*>(rec + lane * 16), k1 = *reinterpret_cast<const uint4*>(rec + 512 + lane * 16);
       const uint4 s0 = *reinterpret_cast<const uint4*>(rec + kKvScales + r * 16);
       const uint4 s1 = *reinterpret_cast<const uint4*>(rec + kKvScales + 128 + r * 16);
-      load(into);   // (read by all lanes before the warp was last together)
+      const uint4 v0 = *reinterpret_cast<const uint4*>(rec + kKvV + lane * 16);
+      const uint4 v1 = *reinterpret_cast<const uint4*>(rec + kKvV + 512 + lane * 16);
 
-      // scores
-      float sc[kCols][4] = {};
+      // scores of keys r and r + 8 for query t of each four
+      float sc[kFours][2] = {};
       {
         const uint32_t w0[4] = {k0.x, k0.y, k0.z, k0.w}, w1[4] = {k1.x, k1.y, k1.z, k1.w};
         float ks[2][4];
@@ -320,66 +327,54 @@ __global__ void __launch_bounds__(kThreads, kCols == 1 ? 3 : 2) kv4_attn_kernel(
         scales_of(s1.y, ks[1][2], ks[1][3]);
 #pragma unroll
         for (int g = 0; g < 4; ++g) {
-          uint32_t a[4], c[4];
-          k_pairs(w0[g], a);
-          k_pairs(w1[g], c);
+          const uint32_t a0 = w0[g] & 0x0f0f0f0fu, a1 = w1[g] & 0x0f0f0f0fu;
+          const uint32_t a2 = (w0[g] >> 4) & 0x0f0f0f0fu, a3 = (w1[g] >> 4) & 0x0f0f0f0fu;
 #pragma unroll
-          for (int n = 0; n < kCols; ++n) {
-            float d[4] = {off[n][g][0], off[n][g][1], off[n][g][0], off[n][g][1]};
-            mma_f16(d, a[0], c[0], a[1], c[1], qf[n][g][0], qf[n][g][1]);
-            mma_f16(d, a[2], c[2], a[3], c[3], qf[n][g][2], qf[n][g][3]);
-#pragma unroll
-            for (int i = 0; i < 4; ++i) sc[n][i] = fmaf(ks[i >> 1][g], d[i], sc[n][i]);
+          for (int n = 0; n < kFours; ++n) {
+            float d[4];
+            mma_e4m3(d, a0, a1, a2, a3, qf[n][g][0], qf[n][g][1], off[n][g][0], off[n][g][1]);
+            sc[n][0] = fmaf(ks[0][g], fmaf(d[1], 1.0f / kLow, d[0]), sc[n][0]);
+            sc[n][1] = fmaf(ks[1][g], fmaf(d[3], 1.0f / kLow, d[2]), sc[n][1]);
           }
         }
       }
       const bool edge = (tile + 1) * kKvTile > all;
       bool raise = false;
 #pragma unroll
-      for (int n = 0; n < kCols; ++n) {
+      for (int n = 0; n < kFours; ++n) {
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          sc[n][i] *= factor[n][i & 1];
-          if (edge && tile * kKvTile + r + 8 * (i >> 1) >= limit[n][i & 1]) sc[n][i] = -INFINITY;
+        for (int h = 0; h < 2; ++h) {
+          sc[n][h] *= factor[n];
+          if (edge && tile * kKvTile + r + 8 * h >= limit[n]) sc[n][h] = -INFINITY;
         }
-#pragma unroll
-        for (int c = 0; c < 2; ++c) raise = raise || fmaxf(sc[n][c], sc[n][2 + c]) > acc.m[n][c] + kSlack;
+        raise = raise || fmaxf(sc[n][0], sc[n][1]) > m[n] + kSlack;
       }
       if (__any_sync(0xffffffffu, raise)) {
 #pragma unroll
-        for (int n = 0; n < kCols; ++n) {
+        for (int n = 0; n < kFours; ++n) {
+          float top = fmaxf(fmaxf(sc[n][0], sc[n][1]), m[n]);
 #pragma unroll
-          for (int c = 0; c < 2; ++c) {
-            float top = fmaxf(fmaxf(sc[n][c], sc[n][2 + c]), acc.m[n][c]);
+          for (int o = 4; o < 32; o <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+          const float shrink = top == -INFINITY ? 1.0f : ex2_approx(m[n] - top);
+          m[n] = top;
+          l[n] *= shrink;
 #pragma unroll
-            for (int o = 4; o < 32; o <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
-            const float shrink = top == -INFINITY ? 1.0f : ex2_approx(acc.m[n][c] - top);
-            acc.m[n][c] = top;
-            acc.l[n][c] *= shrink;
+          for (int g = 0; g < 4; ++g)
 #pragma unroll
-            for (int i = c; i < 4; i += 2) {
-              acc.sum[n][i] *= shrink;
+            for (int u = 0; u < 2; ++u)
 #pragma unroll
-              for (int g = 0; g < 4; ++g) {
-                acc.o[g][0][n][i] *= shrink;
-                acc.o[g][1][n][i] *= shrink;
-              }
-            }
-          }
+              for (int i = 0; i < 4; ++i)
+                if (kFours == 1 || (i & 1) == (n & 1)) acc[g][u][n / 2][i] *= shrink;
         }
       }
-      const uint4 v0 = *reinterpret_cast<const uint4*>(rec + kKvV + lane * 16);
-      const uint4 v1 = *reinterpret_cast<const uint4*>(rec + kKvV + 512 + lane * 16);
 #pragma unroll
-      for (int n = 0; n < kCols; ++n) {
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const float m = acc.m[n][i & 1];
-          sc[n][i] = ex2_approx(sc[n][i] - (m == -INFINITY ? 0.0f : m));
-          acc.l[n][i & 1] += sc[n][i];
-        }
+      for (int n = 0; n < kFours; ++n) {
+        const float at_m = m[n] == -INFINITY ? 0.0f : m[n];
+        sc[n][0] = ex2_approx(sc[n][0] - at_m);
+        sc[n][1] = ex2_approx(sc[n][1] - at_m);
+        l[n] += sc[n][0] + sc[n][1];
       }
-      // what a token without a key holds as scales may be anything
+      // what a token that is not there holds as scales may be anything
       float vs[2][4];
       scales_of(s0.z, vs[0][0], vs[0][1]);
       scales_of(s0.w, vs[0][2], vs[0][3]);
@@ -392,20 +387,29 @@ __global__ void __launch_bounds__(kThreads, kCols == 1 ? 3 : 2) kv4_attn_kernel(
 #pragma unroll
             for (int g = 0; g < 4; ++g) vs[h][g] = 0.0f;
       }
+      uint32_t p0[kCols], p1[kCols];   // B operands: keys 0 to 7 and 8 to 15
 #pragma unroll
       for (int g = 0; g < 4; ++g) {
         const uint32_t a0 = g < 2 ? v0.x : v0.y, c0 = g < 2 ? v0.z : v0.w, a1 = g < 2 ? v1.x : v1.y, c1 = g < 2 ? v1.z : v1.w;
         uint32_t x[4], y[4];
         v_pairs(__byte_perm(a0, c0, g & 1 ? 0x7632 : 0x5410), x);
         v_pairs(__byte_perm(a1, c1, g & 1 ? 0x7632 : 0x5410), y);
-        const uint32_t ones = r == g ? 0x41c041c0u : 0u;   // 24 in row g
+        if (kFours == 1) {
+          if (g % 2 == 0) {
+            p0[0] = transpose8(pack_bf16x2(sc[0][0] * vs[0][g], sc[0][0] * vs[0][g + 1]));
+            p1[0] = transpose8(pack_bf16x2(sc[0][1] * vs[1][g], sc[0][1] * vs[1][g + 1]));
+          }
+        } else {
+#pragma unroll
+          for (int n = 0; n < kCols; ++n) {
+            p0[n] = transpose8(pack_bf16x2(sc[2 * n][0] * vs[0][g], sc[2 * n + 1][0] * vs[0][g]));
+            p1[n] = transpose8(pack_bf16x2(sc[2 * n][1] * vs[1][g], sc[2 * n + 1][1] * vs[1][g]));
+          }
+        }
 #pragma unroll
         for (int n = 0; n < kCols; ++n) {
-          const uint32_t p0 = transpose8(pack_bf16x2(sc[n][0] * vs[0][g], sc[n][1] * vs[0][g]));
-          const uint32_t p1 = transpose8(pack_bf16x2(sc[n][2] * vs[1][g], sc[n][3] * vs[1][g]));
-          mma_bf16(acc.o[g][0][n], x[0], x[1], y[0], y[1], p0, p1);
-          mma_bf16(acc.o[g][1][n], x[2], x[3], y[2], y[3], p0, p1);
-          mma_bf16(acc.sum[n], ones, 0u, ones, 0u, p0, p1);
+          mma_bf16(acc[g][0][n], x[0], x[1], y[0], y[1], p0[n], p1[n]);
+          mma_bf16(acc[g][1][n], x[2], x[3], y[2], y[3], p0[n], p1[n]);
         }
       }
     }
@@ -416,22 +420,18 @@ __global__ void __launch_bounds__(kThreads, kCols == 1 ? 3 : 2) kv4_attn_kernel(
     float* const mo = reinterpret_cast<float*>(mine);              // [kRows][kDim], then m and l
     float2* const ml = reinterpret_cast<float2*>(mo + kRows * kDim);
 #pragma unroll
-    for (int n = 0; n < kCols; ++n) {
+    for (int n = 0; n < kFours; ++n) {
 #pragma unroll
-      for (int c = 0; c < 2; ++c) {
-        float l = acc.l[n][c];
+      for (int o = 4; o < 32; o <<= 1) l[n] += __shfl_xor_sync(0xffffffffu, l[n], o);
+      const int row = 4 * n + t;
+      if (r == 0) ml[row] = make_float2(m[n], l[n]);
 #pragma unroll
-        for (int o = 4; o < 32; o <<= 1) l += __shfl_xor_sync(0xffffffffu, l, o);
-        const int col = 8 * n + 2 * t + c;
-        if (r == 0) ml[col] = make_float2(acc.m[n][c], l);
+      for (int g = 0; g < 4; ++g) {
+        const int c = kFours == 1 ? g & 1 : n & 1;
 #pragma unroll
-        for (int g = 0; g < 4; ++g) {
-          const float sum = __shfl_sync(0xffffffffu, acc.sum[n][c], 4 * g + t);
-#pragma unroll
-          for (int u = 0; u < 2; ++u)
-            *reinterpret_cast<float2*>(mo + col * kDim + 32 * g + 4 * r + 2 * u) =
-                make_float2(acc.o[g][u][n][c] - sum, acc.o[g][u][n][2 + c] - sum);
-        }
+        for (int u = 0; u < 2; ++u)
+          *reinterpret_cast<float2*>(mo + row * kDim + 32 * g + 4 * r + 2 * u) =
+              make_float2(acc[g][u][n / 2][c], acc[g][u][n / 2][2 + c]);
       }
     }
     __syncthreads();
@@ -533,27 +533,34 @@ __global__ void __launch_bounds__(256) kv4_join_kernel(const __grid_constant__ A
     p.lse[((long long)b * p.Hq + h) * p.S + s] = l > 0.0f ? (m + log2f(l)) * 0.6931471805599453f : -INFINITY;
 }
 
-// Columns of eight queries a CTA works on, and CTAs.
+// Queries a CTA works on, four at a time, tiles of them, and CTAs.
 struct Grid {
-  int cols, row_tiles, ctas;
+  int fours, row_tiles, ctas;
 };
 Grid grid_of(int B, int S, int Hq, int Hkv, int max_pages, int page_size) {
   Grid g;
   const long long rows = (long long)S * (Hq / Hkv);
-  g.cols = rows <= 8 ? 1 : 2;
-  g.row_tiles = (int)((rows + 8 * g.cols - 1) / (8 * g.cols));
+  g.fours = rows <= 4 ? 1 : rows <= 8 ? 2 : 4;
+  g.row_tiles = (int)((rows + 4 * g.fours - 1) / (4 * g.fours));
   // no more CTAs than the cache could give work to
   const double most = (double)max_pages * (page_size / kKvTile) * B * Hkv * g.row_tiles / kLeast + 1.0;
-  const int fit = 152 * (g.cols == 1 ? 3 : 2);
+  const int fit = 152 * (g.fours == 1 ? 4 : g.fours == 2 ? 3 : 2);
   g.ctas = most < fit ? (int)most : fit;
   return g;
+}
+
+template <int kFours>
+cudaError_t launch_both(const AttnParams& p, int ctas, cudaStream_t stream) {
+  const cudaError_t e = launch_dependent(kv4_attn_kernel<kFours>, dim3((unsigned)ctas), kThreads, 0, stream, p);
+  if (e != cudaSuccess) return e;
+  return launch_dependent(kv4_join_kernel<4 * kFours>, dim3((unsigned)ctas, 4 * kFours), 256, 0, stream, p);
 }
 
 }  // namespace
 
 size_t attn_kv4_workspace(int B, int S, int Hq, int Hkv, int max_pages, int page_size) {
   const Grid g = grid_of(B, S, Hq, Hkv, max_pages, page_size);
-  return (size_t)g.ctas * (16 + 2 * 8 * g.cols * (kDim * 4 + 8));
+  return (size_t)g.ctas * (16 + 2 * 4 * g.fours * (kDim * 4 + 8));
 }
 
 cudaError_t launch_attn_kv4(const Kv4Args& a, void* workspace, cudaStream_t stream) {
@@ -582,12 +589,12 @@ cudaError_t launch_attn_kv4(const Kv4Args& a, void* workspace, cudaStream_t stre
   p.c_log2 = a.c_log2;
   p.head = reinterpret_cast<int4*>(workspace);
   p.part_o = reinterpret_cast<float*>(p.head + g.ctas);
-  p.part_ml = reinterpret_cast<float2*>(p.part_o + (size_t)g.ctas * 2 * 8 * g.cols * kDim);
-  cudaError_t e = g.cols == 1 ? launch_dependent(kv4_attn_kernel<1>, dim3((unsigned)g.ctas), kThreads, 0, stream, p)
-                              : launch_dependent(kv4_attn_kernel<2>, dim3((unsigned)g.ctas), kThreads, 0, stream, p);
-  if (e != cudaSuccess) return e;
-  return g.cols == 1 ? launch_dependent(kv4_join_kernel<8>, dim3((unsigned)g.ctas, 8), 256, 0, stream, p)
-                     : launch_dependent(kv4_join_kernel<16>, dim3((unsigned)g.ctas, 16), 256, 0, stream, p);
+  p.part_ml = reinterpret_cast<float2*>(p.part_o + (size_t)g.ctas * 2 * 4 * g.fours * kDim);
+  switch (g.fours) {
+    case 1: return launch_both<1>(p, g.ctas, stream);
+    case 2: return launch_both<2>(p, g.ctas, stream);
+    default: return launch_both<4>(p, g.ctas, stream);
+  }
 }
 
 }  // namespace sa

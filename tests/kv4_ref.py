@@ -68,38 +68,35 @@ def steps(x):
 
 
 def held(k, v):
-    """What attention takes of K and V: the values that the codes stand for, and the scales by channel."""
-    return values(k), values(v), steps(k), steps(v)
+    """What attention takes of K and V: the values that the codes stand for, and K's scales by channel."""
+    return values(k), values(v), steps(k)
 
 
-def attention(q, k, v, step, v_step, seen, scale):
-    """One request: q [Sq, Hq, 128]; k, v, step and v_step as held() gives them, [n, Hkv, 128]; seen [Sq, n].  -> O, lse,
+def attention(q, k, v, step, seen, scale):
+    """One request: q [Sq, Hq, 128]; k, v and step as held() gives them, [n, Hkv, 128]; seen [Sq, n].  -> O, lse,
     their bounds.
 
-      scores   products with codes + 264 (at most 280) over 128 channels in FP32, sums of 16 channels rounded or cut
-               within 2^-22 of their largest part, a few of them: 2^-21 280 sum |q step|; Q's FP16 below 2^-25 of its
-               row's largest: 2^-24 max|q| sum |k|
+      scores   products with codes + 8 (at most 15, and 8 taken off) over 128 channels in FP32, sums of 32 channels rounded or
+               cut within 2^-22 of their parts, a few of them: 2^-21 23 sum |q step|; Q's two e4m3 terms, the second in
+               steps of 2^-9 / 32 where the row's largest is at least 2^7: off by 2^-15 / 2^7 of it: 2^-22 max|q| sum |k|
       P        scale and rounding to BF16, whose 8 significant bits are off by up to 2^-8 of the value (half of the 2^-7
                between 1 and the next): 2^-8 + 2^-22; its exponential 2^-21; sums 2^-18
-      P V      products with codes + 24 (at most 31), and 24 sum p step taken off again, in FP32 as the scores: of parts up to
-               31 sum p step, each of the two within 2^-21, so that a channel of zeros comes to 2^-20 31 sum p step
     """
     G = q.shape[1] // k.shape[1]
     q = q.double()
-    k, v, step, v_step = (t.repeat_interleave(G, 1) for t in (k, v, step, v_step))
+    k, v, step = (t.repeat_interleave(G, 1) for t in (k, v, step))
     s = torch.einsum("shd,nhd->hsn", q, k) * scale
     hidden = ~seen[None].expand_as(s)
     s = s.masked_fill(hidden, -math.inf)
     lse = torch.logsumexp(s, -1)
     p = torch.exp(s - torch.where(torch.isinf(lse), 0.0, lse)[..., None])
     o = torch.einsum("hsn,nhd->shd", p, v)
-    off = scale * (280 * 2.0 ** -21 * torch.einsum("shd,nhd->hsn", q.abs(), step.abs())
-                   + 2.0 ** -24 * q.abs().amax(-1).T[..., None] * k.abs().sum(-1).T[:, None])
+    off = scale * (23 * 2.0 ** -21 * torch.einsum("shd,nhd->hsn", q.abs(), step.abs())
+                   + 2.0 ** -22 * q.abs().amax(-1).T[..., None] * k.abs().sum(-1).T[:, None])
     off = off + s.abs().nan_to_num(posinf=0.0) * 2.0 ** -21
     off = off.masked_fill(hidden, 0.0).amax(-1) if s.shape[-1] else torch.zeros_like(lse)
     size = torch.einsum("hsn,nhd->shd", p, v.abs())
     bound = size * (2.0 ** -8 + 2.0 ** -18 + 2 * off.T[..., None])
-    bound = bound + 31 * 2.0 ** -20 * torch.einsum("hsn,nhd->shd", p, v_step.abs())
     return o, lse, bound, off + 2.0 ** -17 + lse.abs().nan_to_num(posinf=0.0) * 2.0 ** -22
 
 
