@@ -29,6 +29,7 @@ namespace {
 constexpr int kWarps = 4, kThreads = kWarps * 32;
 constexpr int kHeld = 6;            // records of a warp's ring
 constexpr int kLeast = 4;           // records a CTA takes at least
+constexpr int kStart = 16;          // what a segment's start and end cost beside its records, in records
 constexpr float kSlack = 8.0f;      // a row's reference maximum is raised when one passes it by more (log2 units)
 constexpr float kNone = -1.5e38f;    // a row's maximum before its first key (finite: differences of two are no NaN)
 constexpr int kDim = 128;
@@ -154,7 +155,10 @@ __global__ void __launch_bounds__(kThreads, kRows <= 8 ? 3 : 2) kv4_attn_kernel(
 
   // the CTA's share of the line
   long long total = 0, before = 0, first_sum;
-  auto work_of = [&](int b) { return b < p.B ? (long long)((tokens_of(p, b) + kKvTile - 1) / kKvTile) * p.segments : 0ll; };
+  auto work_of = [&](int b) {
+    const int n = b < p.B ? (tokens_of(p, b) + kKvTile - 1) / kKvTile : 0;
+    return n > 0 ? (long long)(n + kStart) * p.segments : 0ll;
+  };
   const long long first_work = work_of(threadIdx.x), first_scan = scan(first_work, warp_sums, first_sum);
   total = first_sum;
   for (int c = kThreads; c < p.B; c += kThreads) {
@@ -225,22 +229,27 @@ __global__ void __launch_bounds__(kThreads, kRows <= 8 ? 3 : 2) kv4_attn_kernel(
     }
     cp_async_commit();
   };
-  // Finds the segment that `at` is in and starts to load its records.
-  auto begin = [&] {
-    for (;; ++b) {
+  // Finds the segment that `at` is in and starts to load its records; whether there are any for this CTA.
+  auto begin = [&]() -> bool {
+    for (;;) {
+      if (at >= stop) return false;
       len = tokens_of(p, b);
       tiles = (len + kKvTile - 1) / kKvTile;
-      const long long whole = (long long)tiles * p.segments;
-      if (at < before + whole) break;
-      before += whole;
+      const long long whole = tiles > 0 ? (long long)(tiles + kStart) * p.segments : 0;
+      if (at >= before + whole) {
+        before += whole;
+        ++b;
+        continue;
+      }
+      seg = (int)((at - before) / (tiles + kStart));
+      seg_start = before + (long long)seg * (tiles + kStart) + kStart;
+      lo = (int)max(0ll, at - seg_start);
+      hi = (int)min((long long)tiles, stop - seg_start);
+      at = seg_start + hi;
+      if (hi > lo) break;   // (else the CTA's share ends before the segment's first record)
     }
-    seg = (int)((at - before) / tiles);
-    seg_start = before + (long long)seg * tiles;
-    lo = (int)(at - seg_start);
-    hi = (int)min((long long)tiles, stop - seg_start);
     head = div_by(seg, p.by_row_tiles);
     row0 = (seg - head * p.row_tiles) * kRows;
-    at = seg_start + hi;
     first = lo + (int)((long long)(hi - lo) * warp / kWarps);
     last = lo + (int)((long long)(hi - lo) * (warp + 1) / kWarps);
     there = 0;
@@ -251,9 +260,10 @@ __global__ void __launch_bounds__(kThreads, kRows <= 8 ? 3 : 2) kv4_attn_kernel(
     next = first < last ? kv_page(p.pages, b, first) : -1;
 #pragma unroll 1
     for (int i = 0; i < kStages - 1; ++i) load(i);
+    return true;
   };
-  begin();
-  for (;;) {
+  bool more = begin();
+  while (more) {
     // queries
     uint32_t qf[kCols][4][4];
     float off[kCols][kEach][4], factor[kCols][kEach];
@@ -467,8 +477,7 @@ __global__ void __launch_bounds__(kThreads, kRows <= 8 ? 3 : 2) kv4_attn_kernel(
     // the next segment's records are on their way while the warps' results are joined
     const int done_b = b, done_seg = seg, done_tiles = tiles, done_lo = lo, done_hi = hi, done_head = head, done_row0 = row0;
     const long long done_start = seg_start;
-    const bool more = at < stop;
-    if (more) begin();
+    more = begin();
     float* const mo = reinterpret_cast<float*>(rings + kWarps * kRing + warp * kJoin);   // [kRows][kDim], then m and l
     float2* const ml = reinterpret_cast<float2*>(mo + kRows * kDim);
 #pragma unroll
@@ -524,7 +533,6 @@ __global__ void __launch_bounds__(kThreads, kRows <= 8 ? 3 : 2) kv4_attn_kernel(
       if (lane == 0)
         p.lse[((long long)done_b * p.Hq + h) * p.S + s] = l > 0.0f ? (m + log2f(l)) * 0.6931471805599453f : -INFINITY;
     }
-    if (!more) break;
     __syncthreads();   // before the results' places are written again
   }
 }
@@ -597,7 +605,7 @@ Grid grid_of(int B, int S, int Hq, int Hkv, int max_pages, int page_size) {
   g.rows = rows <= 4 ? 4 : rows <= 8 ? 8 : 16;
   g.row_tiles = (int)((rows + g.rows - 1) / g.rows);
   // no more CTAs than the cache could give work to
-  const double most = (double)max_pages * (page_size / kKvTile) * B * Hkv * g.row_tiles / kLeast + 1.0;
+  const double most = ((double)max_pages * (page_size / kKvTile) + kStart) * B * Hkv * g.row_tiles / kLeast + 1.0;
   const int fit = 152 * (g.rows <= 8 ? 3 : 2);
   g.ctas = most < fit ? (int)most : fit;
   return g;
