@@ -13,10 +13,11 @@
 // largest magnitude in [1, 2): its own 8 bits stay (what is below 2^-14 of that magnitude is off by up to 2^-25 of it).
 // (e4m3 operands would need only masks, but mma.sync has no e4m3 on this machine: it came to 19 instructions a product.)
 //
-// Work.  The records of all requests and heads are one line of work; each CTA takes an equal share of it, found from the
-// lengths on the device, so that ragged batches are balanced and a graph serves any lengths.  A CTA's warps take its
-// records in turn, each through its own ring of cp.async copies, with a softmax of its own; they are joined in shared memory,
-// and pieces of a request's head that several CTAs share by a second kernel, in a fixed order.
+// Work.  The records of all requests and heads are one line of work, cut into items of equal length, found from the lengths on
+// the device, so that ragged batches are balanced and a graph serves any lengths.  A warp takes an item, through its own ring
+// of cp.async copies and with a softmax of its own, then the CTA's next one: the items are fixed, only who works on them is not
+// (an SM serves its older warps first: with equal shares for all warps the first ended at 152 us, the last at 207).  Where an
+// item holds a request's head only in part, its piece goes to the workspace, and a second kernel joins a head's pieces in order.
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
 
@@ -26,10 +27,11 @@
 namespace sa {
 namespace {
 
-constexpr int kWarps = 4, kThreads = kWarps * 32;
 constexpr int kHeld = 6;            // records of a warp's ring
-constexpr int kLeast = 4;           // records a CTA takes at least
-constexpr int kStart = 16;          // what a segment's start and end cost beside its records, in records
+constexpr int kLeast = 4;           // records of an item, at least
+constexpr int kStart = 4;           // what a segment's start and end cost beside its records, in records
+constexpr int kItems = 3;           // items for each warp
+constexpr int kCtas = 152;
 constexpr float kSlack = 8.0f;      // a row's reference maximum is raised when one passes it by more (log2 units)
 constexpr float kNone = -1.5e38f;    // a row's maximum before its first key (finite: differences of two are no NaN)
 constexpr int kDim = 128;
@@ -44,13 +46,14 @@ struct AttnParams {
   int B, S, Hq, rows;               // rows: queries of a key head, S * G
   int row_tiles, segments;          // segments: row tiles of a request over all its key heads
   int capacity;                     // tokens that a table row can hold
-  Div G, by_row_tiles;
+  Div G, by_row_tiles, by_segments;
   int causal;
   float c_log2;
-  // workspace: joined pieces, [CTA][2][rows of a tile]
-  float* part_o;
+  int ctas;
+  // workspace
+  int2* head;                       // [request][segment]: first item, pieces (1: complete)
+  float* part_o;                    // pieces, [item][2][rows of a tile]
   float2* part_ml;
-  int4* head;                       // [CTA]: request, segment, pieces of the segment that starts here (0: none)
 };
 
 // 16 bytes at src, or zeros (size = 0: nothing is read); where `on` is false nothing is written
@@ -111,64 +114,45 @@ __device__ __forceinline__ void scales_of(uint32_t w, float& a, float& b) {
 
 __device__ __forceinline__ int tokens_of(const AttnParams& p, int b) { return min(max(__ldg(p.kv_len + b), 0), p.capacity); }
 
-// Sums v over the CTA's threads up to and including this one; total: all of them.
-__device__ __forceinline__ long long scan(long long v, long long* warp_sums, long long& total) {
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-#pragma unroll
-  for (int o = 1; o < 32; o <<= 1) {
-    const long long up = __shfl_up_sync(0xffffffffu, v, o);
-    if (lane >= o) v += up;
-  }
-  __syncthreads();
-  if (lane == 31) warp_sums[warp] = v;
-  __syncthreads();
-  total = 0;
-#pragma unroll
-  for (int w = 0; w < kWarps; ++w) {
-    if (w < warp) v += warp_sums[w];
-    total += warp_sums[w];
-  }
-  return v;
-}
-
+// One CTA an SM, of as many warps as the registers allow.
+constexpr int warps(int rows) { return rows == 4 ? 12 : rows == 8 ? 11 : 8; }
 // Records that a warp works on at a time: two, whose products do not wait for one another (one: 8 x 131072 tokens 257 us, so
 // 243); one where the registers do not reach for two.
 constexpr int together(int rows) { return rows <= 8 ? 2 : 1; }
-// Shared memory of a warp: its ring; O, m and l of its part of a segment.
-constexpr int kRing = kHeld * kKvRecord;
-constexpr int join_bytes(int rows) { return (rows * kDim + 2 * rows) * 4; }
+constexpr int kRing = kHeld * kKvRecord;   // shared memory of a warp
 
 // kRows: queries of a CTA, 4, 8 or 16.  Four of them are the even columns of a product's eight, so that every lane has scores
 // of one.
 template <int kRows>
-__global__ void __launch_bounds__(kThreads, kRows <= 8 ? 3 : 2) kv4_attn_kernel(const __grid_constant__ AttnParams p) {
+__global__ void __launch_bounds__(32 * warps(kRows), 1) kv4_attn_kernel(const __grid_constant__ AttnParams p) {
+  constexpr int kWarps = warps(kRows), kThreads = 32 * kWarps;
   constexpr int kCols = (kRows + 7) / 8;                   // columns of eight
   constexpr int kEach = kRows == 4 ? 1 : 2;                // queries of a lane and column
-  constexpr int kPair = together(kRows), kStages = kHeld / kPair, kJoin = join_bytes(kRows);
+  constexpr int kPair = together(kRows), kStages = kHeld / kPair;
   extern __shared__ __align__(16) unsigned char rings[];
   __shared__ long long warp_sums[kWarps];
-  __shared__ long long s_before;
-  __shared__ int s_b;
+  __shared__ int s_ticket;
   griddep_wait();
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int r = lane >> 2, t = lane & 3;
 
-  // the CTA's share of the line
-  long long total = 0, before = 0, first_sum;
+  // the line's length, and an item's
   auto work_of = [&](int b) {
     const int n = b < p.B ? (tokens_of(p, b) + kKvTile - 1) / kKvTile : 0;
     return n > 0 ? (long long)(n + kStart) * p.segments : 0ll;
   };
-  const long long first_work = work_of(threadIdx.x), first_scan = scan(first_work, warp_sums, first_sum);
-  total = first_sum;
-  for (int c = kThreads; c < p.B; c += kThreads) {
-    long long more;
-    scan(work_of(c + threadIdx.x), warp_sums, more);
-    total += more;
-  }
-  const long long share = max((long long)kLeast, (total + gridDim.x - 1) / gridDim.x);
-  long long at = blockIdx.x * share;
-  const long long stop = min(at + share, total);
+  long long total = 0;
+  for (int b = threadIdx.x; b < p.B; b += kThreads) total += work_of(b);
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) total += __shfl_xor_sync(0xffffffffu, total, o);
+  if (lane == 0) warp_sums[warp] = total;
+  if (threadIdx.x == 0) s_ticket = kWarps;
+  __syncthreads();
+  total = 0;
+#pragma unroll
+  for (int w = 0; w < kWarps; ++w) total += warp_sums[w];
+  const long long most = (long long)p.ctas * kWarps * kItems;
+  const long long share = max((long long)kLeast, (total + most - 1) / most);
   // requests without a key: nobody's work
   for (int b = blockIdx.x; b < p.B; b += gridDim.x) {
     if (tokens_of(p, b) != 0) continue;
@@ -180,29 +164,13 @@ __global__ void __launch_bounds__(kThreads, kRows <= 8 ? 3 : 2) kv4_attn_kernel(
       if (i % (kDim / 8) == 0) p.lse[((long long)b * p.Hq + h) * p.S + s] = -INFINITY;
     }
   }
-  if (threadIdx.x == 0) p.head[blockIdx.x] = make_int4(0, 0, 0, 0);
-  if (at >= stop) return;
-  // the request that `at` is in
-  for (int c = 0;; c += kThreads) {
-    long long sum = first_sum, mine = first_work, incl = first_scan;
-    if (c > 0) {
-      mine = work_of(c + threadIdx.x);
-      incl = scan(mine, warp_sums, sum);
-    }
-    incl += before;
-    if (at >= incl - mine && at < incl) {
-      s_b = c + threadIdx.x;
-      s_before = incl - mine;
-    }
-    before += sum;
-    if (at < before || c + kThreads >= p.B) break;
-  }
-  __syncthreads();
 
-  // A segment's records: the CTA's are [lo, hi), the warp's [first, last)
-  int b = s_b, len, tiles, seg, lo, hi, head, row0, first, last;
+  // The warp's place in the line: request b starts at `before`.  CTA c has the items c, c + ctas, c + 2 ctas, ...
+  int b = 0, turn = warp;
+  long long before = 0, item = blockIdx.x + (long long)turn * p.ctas, at = item * share, stop = min(at + share, total);
+  // A segment's records: the item's are [first, last)
+  int len, tiles, seg, head, row0, first, last;
   long long seg_start;
-  before = s_before;
   unsigned char* const mine = rings + warp * kRing;
   uint32_t there;                                   // bit of a place in the ring: its record has a page
   int to_load, left, next;                          // left: records of the current page; next: the page after it
@@ -229,29 +197,45 @@ __global__ void __launch_bounds__(kThreads, kRows <= 8 ? 3 : 2) kv4_attn_kernel(
     }
     cp_async_commit();
   };
-  // Finds the segment that `at` is in and starts to load its records; whether there are any for this CTA.
+  // Finds the next segment of the warp's item, or of the CTA's next item, and starts to load its records; false at the end.
   auto begin = [&]() -> bool {
     for (;;) {
-      if (at >= stop) return false;
-      len = tokens_of(p, b);
-      tiles = (len + kKvTile - 1) / kKvTile;
-      const long long whole = tiles > 0 ? (long long)(tiles + kStart) * p.segments : 0;
-      if (at >= before + whole) {
-        before += whole;
-        ++b;
+      if (at >= stop) {
+        if (stop >= total) return false;
+        if (lane == 0) turn = atomicAdd(&s_ticket, 1);
+        turn = __shfl_sync(0xffffffffu, turn, 0);
+        item = blockIdx.x + (long long)turn * p.ctas;
+        at = item * share;
+        stop = min(at + share, total);
+        if (at >= total) return false;
+      }
+      // the request that `at` is in: 32 looked at together
+      long long work = work_of(b + lane), end = work;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const long long up = __shfl_up_sync(0xffffffffu, end, o);
+        if (lane >= o) end += up;
+      }
+      const uint32_t past = __ballot_sync(0xffffffffu, at < before + end);
+      const int step = past != 0 ? __ffs((int)past) - 1 : 31;
+      work = __shfl_sync(0xffffffffu, work, step);
+      before += __shfl_sync(0xffffffffu, end, step) - (past != 0 ? work : 0);
+      b += past != 0 ? step : 32;
+      if (past == 0) {
+        if (b >= p.B) return false;   // (lengths that changed under way)
         continue;
       }
+      len = tokens_of(p, b);
+      tiles = (len + kKvTile - 1) / kKvTile;
       seg = (int)((at - before) / (tiles + kStart));
       seg_start = before + (long long)seg * (tiles + kStart) + kStart;
-      lo = (int)max(0ll, at - seg_start);
-      hi = (int)min((long long)tiles, stop - seg_start);
-      at = seg_start + hi;
-      if (hi > lo) break;   // (else the CTA's share ends before the segment's first record)
+      first = (int)max(0ll, at - seg_start);
+      last = (int)min((long long)tiles, stop - seg_start);
+      at = seg_start + last;
+      if (last > first) break;   // (else the item ends before the segment's first record)
     }
     head = div_by(seg, p.by_row_tiles);
     row0 = (seg - head * p.row_tiles) * kRows;
-    first = lo + (int)((long long)(hi - lo) * warp / kWarps);
-    last = lo + (int)((long long)(hi - lo) * (warp + 1) / kWarps);
     there = 0;
     to_load = first;
     left = 0;
@@ -474,93 +458,75 @@ __global__ void __launch_bounds__(kThreads, kRows <= 8 ? 3 : 2) kv4_attn_kernel(
     cp_async_wait<0>();
     __syncwarp();
 
-    // the next segment's records are on their way while the warps' results are joined
-    const int done_b = b, done_seg = seg, done_tiles = tiles, done_lo = lo, done_hi = hi, done_head = head, done_row0 = row0;
-    const long long done_start = seg_start;
+    // the next segment's records are on their way while this one's results leave
+    const int done_b = b, done_head = head, done_row0 = row0;
+    const long long done_item = item;
+    const bool starts = first == 0, complete = starts && last == tiles;
+    if (starts && lane == 0) {
+      const long long end = (seg_start + tiles - 1) / share;   // the segment's last item
+      p.head[(long long)b * p.segments + seg] = make_int2((int)item, (int)(end - item) + 1);
+    }
     more = begin();
-    float* const mo = reinterpret_cast<float*>(rings + kWarps * kRing + warp * kJoin);   // [kRows][kDim], then m and l
-    float2* const ml = reinterpret_cast<float2*>(mo + kRows * kDim);
 #pragma unroll
     for (int n = 0; n < kCols; ++n)
 #pragma unroll
       for (int e = 0; e < kEach; ++e) {
 #pragma unroll
         for (int o = 4; o < 32; o <<= 1) l[n][e] += __shfl_xor_sync(0xffffffffu, l[n][e], o);
-        const int row = 8 * n + kEach * t + e;
-        if (r == 0) ml[row] = make_float2(m[n][e], l[n][e]);
+        const int in_tile = 8 * n + kEach * t + e, row = done_row0 + in_tile;
+        if (row >= p.rows) continue;
+        float4 v[4];   // of channels 32 g + 4 r and the next three
 #pragma unroll
         for (int g = 0; g < 4; ++g) {
           const int c = kEach == 1 ? g & 1 : e;
-#pragma unroll
-          for (int u = 0; u < 2; ++u)
-            *reinterpret_cast<float2*>(mo + row * kDim + 32 * g + 4 * r + 2 * u) =
-                make_float2(acc[g][u][n][c], acc[g][u][n][2 + c]);
+          v[g] = make_float4(acc[g][0][n][c], acc[g][0][n][2 + c], acc[g][1][n][c], acc[g][1][n][2 + c]);
         }
-      }
-    __syncthreads();
-    const bool complete = done_lo == 0 && done_hi == done_tiles;
-    const int piece = 2 * blockIdx.x + (done_lo == 0);
-    if (!complete && done_lo == 0 && threadIdx.x == 0) {
-      const long long last = done_start + done_tiles - 1;
-      p.head[blockIdx.x] = make_int4(done_b, done_seg, (int)(last / share - blockIdx.x) + 1, 0);
-    }
-    // a warp takes a row: four channels a lane
-    for (int row = warp; row < kRows && done_row0 + row < p.rows; row += kWarps) {
-      float m = kNone, l = 0.0f;
-      float2 each[kWarps];
+        if (!complete) {
+          const long long piece = (2 * done_item + starts) * kRows + in_tile;
 #pragma unroll
-      for (int w = 0; w < kWarps; ++w) {
-        each[w] = reinterpret_cast<const float2*>(reinterpret_cast<const float*>(rings + kWarps * kRing + w * kJoin) + kRows * kDim)[row];
-        m = fmaxf(m, each[w].x);
-      }
-      float4 sum = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+          for (int g = 0; g < 4; ++g) reinterpret_cast<float4*>(p.part_o + piece * kDim)[8 * g + r] = v[g];
+          if (r == 0) p.part_ml[piece] = make_float2(m[n][e], l[n][e]);
+          continue;
+        }
+        const int s = div_by(row, p.G), h = done_head * (int)p.G.d + row - s * (int)p.G.d;
+        const float inv = l[n][e] > 0.0f ? 1.0f / l[n][e] : 0.0f;
+        uint2* const o = reinterpret_cast<uint2*>(p.o + done_b * p.o_str[0] + s * p.o_str[1] + h * p.o_str[2]);
 #pragma unroll
-      for (int w = 0; w < kWarps; ++w) {
-        const float f = ex2_approx(each[w].x - m);
-        const float4 v = reinterpret_cast<const float4*>(reinterpret_cast<const float*>(rings + kWarps * kRing + w * kJoin) + row * kDim)[lane];
-        l = fmaf(f, each[w].y, l);
-        sum = make_float4(fmaf(f, v.x, sum.x), fmaf(f, v.y, sum.y), fmaf(f, v.z, sum.z), fmaf(f, v.w, sum.w));
+        for (int g = 0; g < 4; ++g)
+          o[8 * g + r] = make_uint2(pack_bf16x2(v[g].x * inv, v[g].y * inv), pack_bf16x2(v[g].z * inv, v[g].w * inv));
+        if (r == 0)
+          p.lse[((long long)done_b * p.Hq + h) * p.S + s] =
+              l[n][e] > 0.0f ? (m[n][e] + log2f(l[n][e])) * 0.6931471805599453f : -INFINITY;
       }
-      if (!complete) {
-        reinterpret_cast<float4*>(p.part_o + ((long long)piece * kRows + row) * kDim)[lane] = sum;
-        if (lane == 0) p.part_ml[(long long)piece * kRows + row] = make_float2(m, l);
-        continue;
-      }
-      const int s = div_by(done_row0 + row, p.G), h = done_head * (int)p.G.d + done_row0 + row - s * (int)p.G.d;
-      const float inv = l > 0.0f ? 1.0f / l : 0.0f;
-      reinterpret_cast<uint2*>(p.o + done_b * p.o_str[0] + s * p.o_str[1] + h * p.o_str[2])[lane] =
-          make_uint2(pack_bf16x2(sum.x * inv, sum.y * inv), pack_bf16x2(sum.z * inv, sum.w * inv));
-      if (lane == 0)
-        p.lse[((long long)done_b * p.Hq + h) * p.S + s] = l > 0.0f ? (m + log2f(l)) * 0.6931471805599453f : -INFINITY;
-    }
-    __syncthreads();   // before the results' places are written again
   }
 }
 
-// Segments that several CTAs share: a row's pieces, the CTAs' one after another.
+// A row of a segment in several items: its pieces, in order.
 template <int kRows>
 __global__ void __launch_bounds__(256) kv4_join_kernel(const __grid_constant__ AttnParams p) {
   __shared__ float4 sums[8][32];
   __shared__ float2 mls[8];
   griddep_wait();
-  const int4 what = p.head[blockIdx.x];
-  if (what.z == 0) return;
-  const int b = what.x, head = div_by(what.y, p.by_row_tiles), row0 = (what.y - head * p.row_tiles) * kRows;
+  const int b = div_by((int)blockIdx.x, p.by_segments), seg = (int)blockIdx.x - b * p.segments;
+  if (tokens_of(p, b) == 0) return;
+  const int2 what = p.head[blockIdx.x];   // first item, pieces
+  if (what.y <= 1) return;
+  const int head = div_by(seg, p.by_row_tiles), row0 = (seg - head * p.row_tiles) * kRows;
   const int row = blockIdx.y, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   if (row0 + row >= p.rows) return;
-  // (the first CTA's piece is its second: it may have another segment's end before)
-  auto place = [&](int i) { return (2ll * (blockIdx.x + i) + (i == 0)) * kRows + row; };
+  // (the first item's piece is its second: it may have another segment's end before)
+  auto place = [&](int i) { return (2ll * (what.x + i) + (i == 0)) * kRows + row; };
   float m = kNone, l = 0.0f;
   float4 sum = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
   constexpr int kTogether = 4;
-  for (int i0 = warp; i0 < what.z; i0 += 8 * kTogether) {
+  for (int i0 = warp; i0 < what.y; i0 += 8 * kTogether) {
     float2 ml[kTogether];
     float4 v[kTogether];
 #pragma unroll
     for (int u = 0; u < kTogether; ++u) {
       const int i = i0 + 8 * u;
-      ml[u] = i < what.z ? p.part_ml[place(i)] : make_float2(kNone, 0.0f);
-      v[u] = i < what.z ? reinterpret_cast<const float4*>(p.part_o + place(i) * kDim)[lane] : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+      ml[u] = i < what.y ? p.part_ml[place(i)] : make_float2(kNone, 0.0f);
+      v[u] = i < what.y ? reinterpret_cast<const float4*>(p.part_o + place(i) * kDim)[lane] : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
     }
 #pragma unroll
     for (int u = 0; u < kTogether; ++u) {
@@ -595,39 +561,41 @@ __global__ void __launch_bounds__(256) kv4_join_kernel(const __grid_constant__ A
     p.lse[((long long)b * p.Hq + h) * p.S + s] = l > 0.0f ? (m + log2f(l)) * 0.6931471805599453f : -INFINITY;
 }
 
-// Queries a CTA works on, tiles of them, and CTAs.
+// Queries of a segment, tiles of them, and CTAs.
 struct Grid {
   int rows, row_tiles, ctas;
+  size_t segments, items;   // of all requests
 };
 Grid grid_of(int B, int S, int Hq, int Hkv, int max_pages, int page_size) {
   Grid g;
   const long long rows = (long long)S * (Hq / Hkv);
   g.rows = rows <= 4 ? 4 : rows <= 8 ? 8 : 16;
   g.row_tiles = (int)((rows + g.rows - 1) / g.rows);
-  // no more CTAs than the cache could give work to
-  const double most = ((double)max_pages * (page_size / kKvTile) + kStart) * B * Hkv * g.row_tiles / kLeast + 1.0;
-  const int fit = 152 * (g.rows <= 8 ? 3 : 2);
-  g.ctas = most < fit ? (int)most : fit;
+  g.segments = (size_t)B * Hkv * g.row_tiles;
+  // no more CTAs than the cache could give items to
+  const double most = ((double)max_pages * (page_size / kKvTile) + kStart) * (double)g.segments / kLeast + 1.0;
+  g.ctas = most < kCtas ? (int)most : kCtas;
+  g.items = (size_t)g.ctas * warps(g.rows) * kItems;
   return g;
 }
 
 template <int kRows>
-cudaError_t launch_both(const AttnParams& p, int ctas, cudaStream_t stream) {
-  constexpr int kShared = kWarps * (kRing + join_bytes(kRows));
+cudaError_t launch_both(const AttnParams& p, const Grid& g, cudaStream_t stream) {
+  constexpr int kShared = warps(kRows) * kRing;
   static ContextOnce attr_done;
   cudaError_t e = attr_done.run([] {
     return cudaFuncSetAttribute(kv4_attn_kernel<kRows>, cudaFuncAttributeMaxDynamicSharedMemorySize, kShared);
   });
-  if (e == cudaSuccess) e = launch_dependent(kv4_attn_kernel<kRows>, dim3((unsigned)ctas), kThreads, kShared, stream, p);
+  if (e == cudaSuccess) e = launch_dependent(kv4_attn_kernel<kRows>, dim3((unsigned)g.ctas), 32 * warps(kRows), kShared, stream, p);
   if (e != cudaSuccess) return e;
-  return launch_dependent(kv4_join_kernel<kRows>, dim3((unsigned)ctas, kRows), 256, 0, stream, p);
+  return launch_dependent(kv4_join_kernel<kRows>, dim3((unsigned)g.segments, kRows), 256, 0, stream, p);
 }
 
 }  // namespace
 
 size_t attn_kv4_workspace(int B, int S, int Hq, int Hkv, int max_pages, int page_size) {
   const Grid g = grid_of(B, S, Hq, Hkv, max_pages, page_size);
-  return (size_t)g.ctas * (16 + 2 * g.rows * (kDim * 4 + 8));
+  return (g.segments * sizeof(int2) + 15) / 16 * 16 + g.items * 2 * g.rows * (kDim * sizeof(float) + sizeof(float2));
 }
 
 cudaError_t launch_attn_kv4(const Kv4Args& a, void* workspace, cudaStream_t stream) {
@@ -654,13 +622,15 @@ cudaError_t launch_attn_kv4(const Kv4Args& a, void* workspace, cudaStream_t stre
   p.by_row_tiles = make_div(g.row_tiles);
   p.causal = a.causal;
   p.c_log2 = a.c_log2;
-  p.head = reinterpret_cast<int4*>(workspace);
-  p.part_o = reinterpret_cast<float*>(p.head + g.ctas);
-  p.part_ml = reinterpret_cast<float2*>(p.part_o + (size_t)g.ctas * 2 * g.rows * kDim);
+  p.by_segments = make_div(p.segments);
+  p.ctas = g.ctas;
+  p.head = reinterpret_cast<int2*>(workspace);
+  p.part_o = reinterpret_cast<float*>(reinterpret_cast<char*>(workspace) + (g.segments * sizeof(int2) + 15) / 16 * 16);
+  p.part_ml = reinterpret_cast<float2*>(p.part_o + g.items * 2 * g.rows * kDim);
   switch (g.rows) {
-    case 4: return launch_both<4>(p, g.ctas, stream);
-    case 8: return launch_both<8>(p, g.ctas, stream);
-    default: return launch_both<16>(p, g.ctas, stream);
+    case 4: return launch_both<4>(p, g, stream);
+    case 8: return launch_both<8>(p, g, stream);
+    default: return launch_both<16>(p, g, stream);
   }
 }
 
