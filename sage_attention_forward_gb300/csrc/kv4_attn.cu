@@ -15,9 +15,10 @@
 //
 // Work.  The records of all requests and heads are one line of work, cut into items of equal length, found from the lengths on
 // the device, so that ragged batches are balanced and a graph serves any lengths.  A warp takes an item, through its own ring
-// of cp.async copies and with a softmax of its own, then the CTA's next one: the items are fixed, only who works on them is not
-// (an SM serves its older warps first: with equal shares for all warps the first ended at 152 us, the last at 207).  Where an
-// item holds a request's head only in part, its piece goes to the workspace, and a second kernel joins a head's pieces in order.
+// of cp.async copies and with a softmax of its own.  Where an item holds a request's head only in part, its piece goes to the
+// workspace, and a second kernel joins a head's pieces in order.  (All warps of an SM are one CTA's: of three CTAs of four warps
+// the first was served first and ended at 152 us, the last at 207.  Two and six shorter items a warp: 8 x 131072 tokens 210 and
+// 231 us in place of 205, an item's start and end taking 5 us.)
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
 
@@ -30,7 +31,6 @@ namespace {
 constexpr int kHeld = 6;            // records of a warp's ring
 constexpr int kLeast = 4;           // records of an item, at least
 constexpr int kStart = 4;           // what a segment's start and end cost beside its records, in records
-constexpr int kItems = 3;           // items for each warp
 constexpr int kCtas = 152;
 constexpr float kSlack = 8.0f;      // a row's reference maximum is raised when one passes it by more (log2 units)
 constexpr float kNone = -1.5e38f;    // a row's maximum before its first key (finite: differences of two are no NaN)
@@ -131,7 +131,6 @@ __global__ void __launch_bounds__(32 * warps(kRows), 1) kv4_attn_kernel(const __
   constexpr int kPair = together(kRows), kStages = kHeld / kPair;
   extern __shared__ __align__(16) unsigned char rings[];
   __shared__ long long warp_sums[kWarps];
-  __shared__ int s_ticket;
   griddep_wait();
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int r = lane >> 2, t = lane & 3;
@@ -146,12 +145,11 @@ __global__ void __launch_bounds__(32 * warps(kRows), 1) kv4_attn_kernel(const __
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) total += __shfl_xor_sync(0xffffffffu, total, o);
   if (lane == 0) warp_sums[warp] = total;
-  if (threadIdx.x == 0) s_ticket = kWarps;
   __syncthreads();
   total = 0;
 #pragma unroll
   for (int w = 0; w < kWarps; ++w) total += warp_sums[w];
-  const long long most = (long long)p.ctas * kWarps * kItems;
+  const long long most = (long long)p.ctas * kWarps;
   const long long share = max((long long)kLeast, (total + most - 1) / most);
   // requests without a key: nobody's work
   for (int b = blockIdx.x; b < p.B; b += gridDim.x) {
@@ -165,9 +163,11 @@ __global__ void __launch_bounds__(32 * warps(kRows), 1) kv4_attn_kernel(const __
     }
   }
 
-  // The warp's place in the line: request b starts at `before`.  CTA c has the items c, c + ctas, c + 2 ctas, ...
-  int b = 0, turn = warp;
-  long long before = 0, item = blockIdx.x + (long long)turn * p.ctas, at = item * share, stop = min(at + share, total);
+  // The warp's place in the line: request b starts at `before`
+  int b = 0;
+  const int item = blockIdx.x + warp * p.ctas;   // (few items: one for each CTA)
+  long long before = 0, at = item * share;
+  const long long stop = min(at + share, total);
   // A segment's records: the item's are [first, last)
   int len, tiles, seg, head, row0, first, last;
   long long seg_start;
@@ -197,18 +197,10 @@ __global__ void __launch_bounds__(32 * warps(kRows), 1) kv4_attn_kernel(const __
     }
     cp_async_commit();
   };
-  // Finds the next segment of the warp's item, or of the CTA's next item, and starts to load its records; false at the end.
+  // Finds the next segment of the item and starts to load its records; false at its end.
   auto begin = [&]() -> bool {
     for (;;) {
-      if (at >= stop) {
-        if (stop >= total) return false;
-        if (lane == 0) turn = atomicAdd(&s_ticket, 1);
-        turn = __shfl_sync(0xffffffffu, turn, 0);
-        item = blockIdx.x + (long long)turn * p.ctas;
-        at = item * share;
-        stop = min(at + share, total);
-        if (at >= total) return false;
-      }
+      if (at >= stop) return false;
       // the request that `at` is in: 32 looked at together
       long long work = work_of(b + lane), end = work;
 #pragma unroll
@@ -460,11 +452,10 @@ __global__ void __launch_bounds__(32 * warps(kRows), 1) kv4_attn_kernel(const __
 
     // the next segment's records are on their way while this one's results leave
     const int done_b = b, done_head = head, done_row0 = row0;
-    const long long done_item = item;
     const bool starts = first == 0, complete = starts && last == tiles;
     if (starts && lane == 0) {
       const long long end = (seg_start + tiles - 1) / share;   // the segment's last item
-      p.head[(long long)b * p.segments + seg] = make_int2((int)item, (int)(end - item) + 1);
+      p.head[(long long)b * p.segments + seg] = make_int2(item, (int)(end - item) + 1);
     }
     more = begin();
 #pragma unroll
@@ -482,7 +473,7 @@ __global__ void __launch_bounds__(32 * warps(kRows), 1) kv4_attn_kernel(const __
           v[g] = make_float4(acc[g][0][n][c], acc[g][0][n][2 + c], acc[g][1][n][c], acc[g][1][n][2 + c]);
         }
         if (!complete) {
-          const long long piece = (2 * done_item + starts) * kRows + in_tile;
+          const long long piece = (2ll * item + starts) * kRows + in_tile;
 #pragma unroll
           for (int g = 0; g < 4; ++g) reinterpret_cast<float4*>(p.part_o + piece * kDim)[8 * g + r] = v[g];
           if (r == 0) p.part_ml[piece] = make_float2(m[n][e], l[n][e]);
@@ -575,7 +566,7 @@ Grid grid_of(int B, int S, int Hq, int Hkv, int max_pages, int page_size) {
   // no more CTAs than the cache could give items to
   const double most = ((double)max_pages * (page_size / kKvTile) + kStart) * (double)g.segments / kLeast + 1.0;
   g.ctas = most < kCtas ? (int)most : kCtas;
-  g.items = (size_t)g.ctas * warps(g.rows) * kItems;
+  g.items = (size_t)g.ctas * warps(g.rows);
   return g;
 }
 
