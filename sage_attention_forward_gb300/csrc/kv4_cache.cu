@@ -16,7 +16,7 @@ namespace sa {
 namespace {
 
 constexpr int kWarps = 8;
-constexpr int kAhead = 8;   // tokens whose loads are under way
+constexpr int kAhead = 4;   // tokens whose loads are under way
 
 struct CacheParams {
   KvPages pages;
@@ -54,19 +54,39 @@ __device__ __forceinline__ Work work_of(const CacheParams& p, int unit) {
 }
 
 // Eight codes of one lane, bits 4 i.
-__device__ __forceinline__ uint32_t codes_of(const float (&x)[8], float scale, float inv) {
+__device__ __forceinline__ uint32_t codes_of(const float (&x)[8], float inv) {
   uint32_t out = 0;
 #pragma unroll
   for (int i = 0; i < 8; ++i) {
-    // The quotient by the reciprocal, its remainder taken off once (Markstein, "Computation of elementary functions on the
-    // IBM RISC System/6000 processor", 1990): where x / scale is half an integer, this is exact.
-    float q = x[i] * inv;
-    q = fmaf(fmaf(-q, scale, x[i]), inv, q);
-    q = fminf(fmaxf(q, -8.0f), 7.0f);
-    const uint32_t c = __float_as_uint(q + (12582912.0f + 8.0f));   // 1.5 2^23: rounds to even, the integer in the low bits
-    out |= (c & 15u) << (4 * i);
+    // x / scale is a quotient of two 8-bit significands: half an integer, or at least 2^-10 from one.  x inv is off by less than
+    // 2^-18, so that in steps of 2^-11 (6144 added) halves are exact again and no other quotient becomes one; then the sum with
+    // 1.5 2^23 + 8 rounds to even, and the integer stands in its low bits.
+    const float q = fminf(fmaf(x[i], inv, 6144.0f), 6144.0f + 7.0f);
+    const uint32_t c = __float_as_uint(q + (12582912.0f + 8.0f - 6144.0f));
+    out = c * (1u << (4 * i)) + out;
   }
-  return out;
+  constexpr uint32_t kMagic = 0x4b400000u;   // bits of 1.5 2^23, in `out` once for every code
+  return out - kMagic * 0x11111111u;
+}
+__device__ __forceinline__ uint32_t max2(uint32_t a, uint32_t b) {
+  uint32_t d;
+  asm("max.bf16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
+  return d;
+}
+__device__ __forceinline__ uint32_t min2(uint32_t a, uint32_t b) {
+  uint32_t d;
+  asm("min.bf16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
+  return d;
+}
+// The value of largest magnitude of a group (four lanes' eight BF16 values each), the positive one of two.
+__device__ __forceinline__ float extreme(const uint4& raw) {
+  const uint32_t top = max2(max2(raw.x, raw.y), max2(raw.z, raw.w));
+  const uint32_t low = min2(min2(raw.x, raw.y), min2(raw.z, raw.w)) ^ 0x80008000u;
+  uint32_t both = max2(__byte_perm(top, low, 0x5410), __byte_perm(top, low, 0x7632));   // largest, and the smallest negated
+#pragma unroll
+  for (int o = 1; o < 4; o <<= 1) both = max2(both, __shfl_xor_sync(0xffffffffu, both, o));
+  const float hi = __uint_as_float(both << 16), lo = __uint_as_float(both & 0xffff0000u);
+  return hi >= lo ? hi : -lo;
 }
 
 __global__ void __launch_bounds__(kWarps * 32) kv4_write_kernel(const __grid_constant__ CacheParams p) {
@@ -94,23 +114,12 @@ __global__ void __launch_bounds__(kWarps * 32) kv4_write_kernel(const __grid_con
     for (int u = 0; u < kAhead; ++u) {
       const int j = j0 + u;
       if (j >= hi) break;
-      float x[8];
-      unpack<__nv_bfloat16>(raw[u], x);
-      float top = x[0], low = x[0];
-#pragma unroll
-      for (int i = 1; i < 8; ++i) {
-        top = fmaxf(top, x[i]);
-        low = fminf(low, x[i]);
-      }
-#pragma unroll
-      for (int o = 1; o < 4; o <<= 1) {
-        top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
-        low = fminf(low, __shfl_xor_sync(0xffffffffu, low, o));
-      }
-      const float ext = top >= -low ? top : low;
+      const float ext = extreme(raw[u]);
       const bool none = fabsf(ext) < 0x1p-100f;
       const float scale = none ? 0.0f : ext * -0.125f;
-      const uint32_t c = none ? 0x88888888u : codes_of(x, scale, __fdividef(1.0f, scale));
+      float x[8];
+      unpack<__nv_bfloat16>(raw[u], x);
+      const uint32_t c = codes_of(x, none ? 0.0f : __fdividef(1.0f, scale));
       if (is_v) {
         // channels 8 t .. 8 t + 3 are r = 2 t's, the next four r = 2 t + 1's
         unsigned char* const at = tile + kKvV + (j >> 3) * 512 + (8 * t + (j & 7) / 2) * 16 + (j & 1) * 8 + g * 2;
@@ -177,12 +186,17 @@ __global__ void __launch_bounds__(kWarps * 32) kv4_read_kernel(const __grid_cons
       } else {
         c = *reinterpret_cast<const uint32_t*>(tile + j * 64 + t * 16 + g * 4);
       }
-      const float scale =
-          __bfloat162float(*reinterpret_cast<const __nv_bfloat16*>(tile + kKvScales + j * 16 + (is_v ? 8 : 0) + 2 * g));
-      float x[8];
+      const uint32_t scale = *reinterpret_cast<const unsigned short*>(tile + kKvScales + j * 16 + (is_v ? 8 : 0) + 2 * g) * 0x10001u;
+      uint32_t pair[4];   // channels (i, i + 4): 128 + c, less 136, times the scale: rounded once
 #pragma unroll
-      for (int i = 0; i < 8; ++i) x[i] = (float)((int)((c >> (4 * i)) & 15u) - 8) * scale;
-      row = pack<__nv_bfloat16>(x);
+      for (int i = 0; i < 4; ++i) {
+        uint32_t y;
+        asm("lop3.b32 %0, %1, 0x000f000f, %2, 0xEA;" : "=r"(y) : "r"(c >> (4 * i)), "r"(0x43004300u));
+        asm("add.rn.bf16x2 %0, %0, %1;" : "+r"(y) : "r"(0xc308c308u));
+        asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(pair[i]) : "r"(y), "r"(scale));
+      }
+      row = make_uint4(__byte_perm(pair[0], pair[1], 0x5410), __byte_perm(pair[2], pair[3], 0x5410),
+                       __byte_perm(pair[0], pair[1], 0x7632), __byte_perm(pair[2], pair[3], 0x7632));
     }
     __stcs(reinterpret_cast<uint4*>(out + (w.first + j) * step), row);
   }
