@@ -3,10 +3,9 @@
 //   rotation:   y = rope(x)             (its backward: the same with the angles negated)
 //   with norm:  y = rope(x r w),  r = 1 / sqrt(sum x^2 / N + eps)
 //
-// Bound by memory: x is read and y written once.  A unit is a warp's: some heads of one token, of Q or of K, the
-// token's cosines formed once for all of them (qk_rope.cuh).  A lane holds both channels of its pairs, 16 channels in
-// all, so the rotation takes no exchange; a head of 128 channels is 8 lanes', and a warp has four rows' worth of four
-// heads each under way.
+// Bound by memory: x is read and y written once.  A unit is a warp's: heads of one token, Q's and then K's, the token's
+// cosines formed once for all of them (qk_rope.cuh).  A lane holds both channels of its pairs, 16 channels in
+// all, so the rotation takes no exchange; a head of 128 channels is 8 lanes', and a warp works on four heads at a time.
 #include <cuda_runtime.h>
 
 #include "qk_rope.cuh"
@@ -14,81 +13,113 @@
 namespace sa {
 namespace {
 
+// Rows of a slot whose loads are under way, and CTAs an SM: loads in flight are what the kernels wait for, and more warps with
+// fewer rows each do better (76112 x 80 heads of 128 BF16: four rows, two CTAs 546 us; two, three 497; two, four 467).
+constexpr int rows_ahead(bool vec, int pairs, bool wide) { return vec ? (wide ? 1 : 2) : pairs == 2 ? 4 : 2; }
+constexpr int ctas_an_sm(bool vec, bool wide, bool norm) { return !vec ? 1 : !wide ? 4 : norm ? 2 : 3; }
+
 template <class T, int kMap, int kPairs, bool kNorm>
-__global__ void __launch_bounds__(kRopeThreads) rope_fwd_kernel(const __grid_constant__ RopeParams p) {
+__global__ void __launch_bounds__(kRopeThreads, ctas_an_sm(kMap < kAny, sizeof(T) == 4, kNorm))
+    rope_fwd_kernel(const __grid_constant__ RopeParams p) {
   using L = RopeLane<T, kMap, kPairs>;
-  constexpr int kAhead = sizeof(T) == 4 || (!L::kVec && kPairs == 8) ? 2 : 4;   // rows of a slot under way
-  extern __shared__ __align__(16) float2 tables[];
+  constexpr int kAhead = rows_ahead(L::kVec, kPairs, sizeof(T) == 4);
+  // kNorm: the weights of Q and of K by lanes, [2][kPairs / 2][lanes] of four (held in registers they take the warps that hide
+  // the loads); then the tables
+  extern __shared__ __align__(16) float4 shared[];
+  float2* const tables = reinterpret_cast<float2*>(shared + (kNorm ? kPairs * 32 : 0));
+  const float4* weights = shared;
   griddep_wait();
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  if constexpr (kNorm) {
+    const L ln(p, lane);
+    if (warp < 2 && (!L::kVec || lane < p.lanes)) {
+      float w[2 * kPairs];
+      ln.weights(p.side[warp].w, p, w);
+#pragma unroll
+      for (int k = 0; k < kPairs / 2; ++k)
+        shared[(warp * (kPairs / 2) * 32) + k * p.lanes + ln.l] = make_float4(w[4 * k], w[4 * k + 1], w[4 * k + 2], w[4 * k + 3]);
+    }
+    __syncthreads();
+  }
   const int unit = blockIdx.x * kRopeWarps + warp;
   const int token = div_by(unit, p.by_parts), part = unit - token * (int)p.by_parts.d;
   if (token >= p.tokens) return;
-  const int which = part >= p.side[0].parts;
-  const RopeSide& sd = p.side[which];
-  const int first = (which ? part - p.side[0].parts : part) * p.per_unit;
-  const int end = min(first + p.per_unit, sd.heads);
   const int b = div_by(token, p.S), s = token - b * (int)p.S.d;
   const L ln(p, lane);
   const int slot = L::kVec ? lane / p.lanes : 0;
   const bool mine = slot < p.slots && ln.some();
-  const T* const x = reinterpret_cast<const T*>(sd.x) + b * sd.xs[0] + s * sd.xs[1];
-  T* const y = reinterpret_cast<T*>(sd.y) + b * sd.ys[0] + s * sd.ys[1];
-  typename L::Raw raw[kAhead];
-  auto load = [&](int u, int h) {
-    if (mine && h < end) ln.load(x + h * sd.xs[2], p.pairs, raw[u]);
+  // the unit's share of Q's heads, then of K's, p.slots of them a turn
+  const int turns_q = p.side[0].turns, turns = turns_q + p.side[1].turns;
+  auto share = [&](RopeWalk<T>& w, int which, const void* base, const long long (&str)[3]) {
+    const RopeSide& sd = p.side[which];
+    w.start(base, str, b, s, part * sd.per_unit, min((part + 1) * sd.per_unit, sd.heads), slot);
   };
-  int h = first + slot;
+  RopeWalk<T> in, out;
+  int to_load = 0;
+  share(in, 0, p.side[0].x, p.side[0].xs);
+  share(out, 0, p.side[0].y, p.side[0].ys);
+  typename L::Raw raw[kAhead];
+  auto load = [&](int u) {
+    if (to_load == turns_q) share(in, 1, p.side[1].x, p.side[1].xs);
+    if (mine && in.head < in.end && to_load < turns) ln.load(in.row, raw[u]);
+    in.next(p.slots, p.side[to_load >= turns_q].x_step);
+    ++to_load;
+  };
 #pragma unroll
-  for (int u = 0; u < kAhead; ++u) load(u, h + u * p.slots);
+  for (int u = 0; u < kAhead; ++u) load(u);
 
   float2* const table = tables + warp * p.table;
   rope_table<L::kVec>(p, b, s, lane, table);
-  float cs[kPairs], sn[kPairs], wa[kPairs], wb[kPairs];
-#pragma unroll
-  for (int i = 0; i < kPairs; ++i) {
-    const int at = L::kVec ? (i / 2 * p.lanes + ln.l) * 2 + i % 2 : ln.pair(i);
-    const float2 t = ln.pair(i) < p.pairs ? table[at] : make_float2(1.0f, 0.0f);
-    cs[i] = t.x;
-    sn[i] = t.y;
-  }
-  if (kNorm) ln.weights(sd.w, p, wa, wb);
 
-  for (int base = first; base < end; base += kAhead * p.slots) {
+  for (int base = 0; base < turns; base += kAhead) {
 #pragma unroll
-    for (int u = 0; u < kAhead; ++u, h += p.slots) {
-      if (base + u * p.slots >= end) break;
+    for (int u = 0; u < kAhead; ++u) {
+      if (base + u >= turns) break;
+      if (base + u == turns_q) {
+        share(out, 1, p.side[1].y, p.side[1].ys);
+        if constexpr (kNorm) weights = shared + kPairs / 2 * 32;
+      }
       float a[kPairs], c[kPairs];
-      const bool in = mine && h < end;
-      if (in) {
+      const bool some = mine && out.head < out.end;
+      if (some) {
         ln.values(raw[u], a, c);
       } else {
 #pragma unroll
         for (int i = 0; i < kPairs; ++i) a[i] = c[i] = 0.0f;
       }
-      load(u, h + kAhead * p.slots);
-      if (kNorm) {
+      load(u);
+      if constexpr (kNorm) {
         float sum = 0.0f;
 #pragma unroll
         for (int i = 0; i < kPairs; ++i) sum = fmaf(a[i], a[i], fmaf(c[i], c[i], sum));
         sum = rope_row_sum(sum, p.lanes);
         const float r = rsqrtf(fmaf(sum, p.inv_n, p.eps));
 #pragma unroll
-        for (int i = 0; i < kPairs; ++i) {
-          a[i] = a[i] * r * wa[i];
-          c[i] = c[i] * r * wb[i];
+        for (int k = 0; k < kPairs / 2; ++k) {
+          const float4 w = load_shared(weights + k * p.lanes + ln.l);
+          a[2 * k] *= r * w.x;
+          c[2 * k] *= r * w.y;
+          a[2 * k + 1] *= r * w.z;
+          c[2 * k + 1] *= r * w.w;
         }
       }
-      if (in) {
+      if (some) {
 #pragma unroll
-        for (int i = 0; i < kPairs; ++i) {
-          if (ln.pair(i) >= p.pairs) continue;   // (an infinity beside a channel that passes stays out of it)
-          const float a0 = a[i];
-          a[i] = a0 * cs[i] - c[i] * sn[i];
-          c[i] = c[i] * cs[i] + a0 * sn[i];
+        for (int k = 0; k < kPairs / 2; ++k) {
+          float2 t[2];
+          two_angles(p, ln, table, k, t);
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            const int i = 2 * k + e;
+            if (ln.pair(i) >= p.pairs) continue;   // (an infinity beside a channel that passes stays out of it)
+            const float a0 = a[i];
+            a[i] = a0 * t[e].x - c[i] * t[e].y;
+            c[i] = c[i] * t[e].x + a0 * t[e].y;
+          }
         }
-        ln.store(y + h * sd.ys[2], p.pairs, a, c);
+        ln.store(out.row, a, c);
       }
+      out.next(p.slots, p.side[base + u >= turns_q].y_step);
     }
   }
 }
@@ -97,8 +128,9 @@ template <class T, bool kNorm>
 cudaError_t launch_fwd(RopeParams& p, bool vec, bool next, cudaStream_t stream) {
   const long long units = (long long)p.tokens * p.by_parts.d;
   return with_rope_map(vec, next, p.N, [&](auto map, auto pairs) {
-    return launch_dependent(rope_fwd_kernel<T, decltype(map)::value, decltype(pairs)::value, kNorm>, dim3((unsigned)((units + kRopeWarps - 1) / kRopeWarps)),
-                            kRopeThreads, (size_t)kRopeWarps * p.table * sizeof(float2), stream, p);
+    constexpr int kPairs = decltype(pairs)::value;
+    return launch_dependent(rope_fwd_kernel<T, decltype(map)::value, kPairs, kNorm>, dim3((unsigned)((units + kRopeWarps - 1) / kRopeWarps)),
+                            kRopeThreads, (kNorm ? kPairs * 32 * sizeof(float4) : 0) + kRopeWarps * p.table * sizeof(float2), stream, p);
   });
 }
 template <bool kNorm>
@@ -114,15 +146,16 @@ cudaError_t launch_rope_fwd(const RopeArgs& a, bool norm, cudaStream_t stream) {
   RopeParams p;
   rope_params(p, a);
   const bool vec = rope_shape(p, a, norm);
-  // All heads of a token in one unit, so that its cosines are formed once; fewer where that leaves warps idle.
-  const int heads = a.side[0].H > a.side[1].H ? a.side[0].H : a.side[1].H;
-  auto parts = [&](int H) { return (H + p.per_unit - 1) / p.per_unit; };
-  p.per_unit = (heads + p.slots - 1) / p.slots * p.slots;
-  while (p.per_unit > p.slots &&
-         (long long)p.tokens * (parts(a.side[0].H) + parts(a.side[1].H)) < 152 * 32)
-    p.per_unit = (p.per_unit / 2 + p.slots - 1) / p.slots * p.slots;
-  for (int i = 0; i < 2; ++i) p.side[i].parts = parts(a.side[i].H);
-  p.by_parts = make_div(p.side[0].parts + p.side[1].parts);
+  // All heads of a token in one unit, so that its cosines are formed once; parts of them where that leaves warps idle.
+  const int turns = (a.side[0].H + p.slots - 1) / p.slots + (a.side[1].H + p.slots - 1) / p.slots;
+  int parts = 1;
+  while (2 * parts <= turns && (long long)p.tokens * parts < 152 * 32) parts *= 2;
+  for (int i = 0; i < 2; ++i) {
+    RopeSide& s = p.side[i];
+    s.per_unit = ((a.side[i].H + parts - 1) / parts + p.slots - 1) / p.slots * p.slots;
+    s.turns = s.per_unit / p.slots;
+  }
+  p.by_parts = make_div(parts);
   return norm ? launch_typed<true>(p, a.type, vec, a.interleaved, stream)
               : launch_typed<false>(p, a.type, vec, a.interleaved, stream);
 }

@@ -23,7 +23,8 @@ struct RopeSide {
   const void* w;
   float* partial;                 // backward: [CTAs][N] sums of dw, or nullptr
   long long xs[3], ds[3], ys[3];  // element strides (b, s, h)
-  int heads, parts;               // parts: units that a token's heads are divided into
+  long long x_step, d_step, y_step;   // from a turn's heads to the next one's
+  int heads, per_unit, turns;     // heads of a unit, in turns of p.slots
 };
 struct RopeParams {
   RopeSide side[2];               // Q and K
@@ -31,10 +32,9 @@ struct RopeParams {
   const unsigned long long* freq;
   long long pos_str[3];           // element strides (b, s, axis)
   int tokens, N, pairs, axes;
-  int per_unit;                   // heads of a unit
   int table;                      // cosines and sines of a warp
   int lanes, slots;               // lanes a row, rows a warp takes at a time
-  Div S, by_parts;                // by_parts: units of a token
+  Div S, by_parts;                // by_parts: units that a token's heads are divided into
   float magnitude, eps, inv_n;
   int inverse, w_type, w_vec;     // w_vec: weights by 16 bytes
 };
@@ -52,6 +52,7 @@ struct RopeLane {
     T a[kVec ? 1 : kPairs], b[kVec ? 1 : kPairs];
   };
   int l, ca, cb, last;   // kVec: first channels of the two runs of eight; last: N
+  int at_a[kVec ? 1 : kPairs], at_b[kVec ? 1 : kPairs];   // else: the channels of each pair
 
   __device__ __forceinline__ RopeLane(const RopeParams& p, int lane) {
     l = kVec ? lane % p.lanes : lane;
@@ -59,23 +60,27 @@ struct RopeLane {
     const bool turned = kMap == kHalf && 8 * l < p.pairs;
     ca = turned ? 8 * l : 16 * l;
     cb = turned ? p.pairs + 8 * l : 16 * l + 8;
+    if constexpr (!kVec) {
+#pragma unroll
+      for (int i = 0; i < kPairs; ++i) {
+        const bool half = kMap == kAny && pair(i) < p.pairs;
+        at_a[i] = half ? pair(i) : 2 * pair(i);
+        at_b[i] = half ? pair(i) + p.pairs : 2 * pair(i) + 1;
+      }
+    }
   }
   // kVec: the lane has channels of a row
   __device__ __forceinline__ bool some() const { return !kVec || 16 * l < last; }
   __device__ __forceinline__ int pair(int i) const { return kVec ? 8 * l + i : l + 32 * i; }
-  __device__ __forceinline__ int first(int i, int pairs) const {
-    if (kMap == kHalf) return ca + i;
-    if (kMap == kNext) return 16 * l + 2 * i;
-    const int v = pair(i);
-    return kMap == kAny && v < pairs ? v : 2 * v;
+  __device__ __forceinline__ int first(int i) const {
+    if constexpr (kVec) return kMap == kHalf ? ca + i : 16 * l + 2 * i;
+    else return at_a[i];
   }
-  __device__ __forceinline__ int second(int i, int pairs) const {
-    if (kMap == kHalf) return cb + i;
-    if (kMap == kNext) return 16 * l + 2 * i + 1;
-    const int v = pair(i);
-    return kMap == kAny && v < pairs ? v + pairs : 2 * v + 1;
+  __device__ __forceinline__ int second(int i) const {
+    if constexpr (kVec) return kMap == kHalf ? cb + i : 16 * l + 2 * i + 1;
+    else return at_b[i];
   }
-  __device__ __forceinline__ void load(const T* row, int pairs, Raw& r) const {
+  __device__ __forceinline__ void load(const T* row, Raw& r) const {
     if constexpr (kVec) {
       constexpr int half = kPieces / 2;
 #pragma unroll
@@ -86,7 +91,7 @@ struct RopeLane {
     } else {
 #pragma unroll
       for (int i = 0; i < kPairs; ++i) {
-        const int a = first(i, pairs), b = second(i, pairs);
+        const int a = first(i), b = second(i);
         r.a[i] = a < last ? row[a] : T(0.0f);
         r.b[i] = b < last ? row[b] : T(0.0f);
       }
@@ -110,7 +115,7 @@ struct RopeLane {
       }
     }
   }
-  __device__ __forceinline__ void store(T* row, int pairs, const float (&a)[kPairs], const float (&b)[kPairs]) const {
+  __device__ __forceinline__ void store(T* row, const float (&a)[kPairs], const float (&b)[kPairs]) const {
     if constexpr (kVec) {
       float x[16];
 #pragma unroll
@@ -127,7 +132,7 @@ struct RopeLane {
     } else {
 #pragma unroll
       for (int i = 0; i < kPairs; ++i) {
-        const int ia = first(i, pairs), ib = second(i, pairs);
+        const int ia = first(i), ib = second(i);
         if (ia < last) row[ia] = T(a[i]);
         if (ib < last) row[ib] = T(b[i]);
       }
@@ -152,16 +157,16 @@ struct RopeLane {
     if constexpr (kVec) {
       if (p.w_vec) {
         if (p.w_type == kF32) {
-          RopeLane<float, kMap, 8>(p, l).take(reinterpret_cast<const float*>(w), p.pairs, a, b);
+          RopeLane<float, kMap, 8>(p, l).take(reinterpret_cast<const float*>(w), a, b);
         } else {
-          take(reinterpret_cast<const T*>(w), p.pairs, a, b);
+          take(reinterpret_cast<const T*>(w), a, b);
         }
         return;
       }
     }
 #pragma unroll
     for (int i = 0; i < kPairs; ++i) {
-      const int ia = first(i, p.pairs), ib = second(i, p.pairs);
+      const int ia = first(i), ib = second(i);
       if (p.w_type == kF32) {
         const float* f = reinterpret_cast<const float*>(w);
         if (ia < last) a[i] = f[ia];
@@ -173,10 +178,26 @@ struct RopeLane {
       }
     }
   }
-  __device__ __forceinline__ void take(const T* row, int pairs, float (&a)[kPairs], float (&b)[kPairs]) const {
+  __device__ __forceinline__ void take(const T* row, float (&a)[kPairs], float (&b)[kPairs]) const {
     Raw r;
-    load(row, pairs, r);
+    load(row, r);
     values(r, a, b);
+  }
+};
+
+// A lane's rows of a token, p.slots heads a turn: Q's from `first` on, then K's.
+template <class T>
+struct RopeWalk {
+  T* row;
+  int head, end;   // the lane's head of the next turn; heads end here
+  __device__ __forceinline__ void start(const void* base, const long long (&str)[3], int b, int s, int first, int stop, int slot) {
+    head = first + slot;
+    end = stop;
+    row = reinterpret_cast<T*>(const_cast<void*>(base)) + b * str[0] + s * str[1] + head * str[2];
+  }
+  __device__ __forceinline__ void next(int slots, long long step) {
+    row += step;
+    head += slots;
   }
 };
 
@@ -198,6 +219,35 @@ __device__ __forceinline__ void rope_table(const RopeParams& p, int b, int s, in
     table[kVec ? ((i % 8 / 2) * p.lanes + i / 8) * 2 + i % 2 : i] = make_float2(cs * p.magnitude, sn * (p.inverse ? -p.magnitude : p.magnitude));
   }
   __syncwarp();
+}
+
+// (volatile: held in registers over the rows, weights and cosines would spill)
+__device__ __forceinline__ float4 load_shared(const float4* at) {
+  float4 v;
+  asm volatile("ld.shared.v4.f32 {%0, %1, %2, %3}, [%4];"
+               : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
+               : "r"(smem_u32(at)));
+  return v;
+}
+
+__device__ __forceinline__ float2 load_shared(const float2* at) {
+  float2 v;
+  asm volatile("ld.shared.v2.f32 {%0, %1}, [%2];" : "=f"(v.x), "=f"(v.y) : "r"(smem_u32(at)));
+  return v;
+}
+
+// Cosines and sines of a lane's pairs 2 k and 2 k + 1 (where they are rotated).
+template <class L>
+__device__ __forceinline__ void two_angles(const RopeParams& p, const L& ln, const float2* table, int k, float2 (&t)[2]) {
+  if (L::kVec) {
+    const float4 two = load_shared(reinterpret_cast<const float4*>(table) + k * p.lanes + ln.l);
+    t[0] = make_float2(two.x, two.y);
+    t[1] = make_float2(two.z, two.w);
+  } else {
+#pragma unroll
+    for (int e = 0; e < 2; ++e)
+      if (ln.pair(2 * k + e) < p.pairs) t[e] = load_shared(table + ln.pair(2 * k + e));
+  }
 }
 
 // Sum over the lanes of a row (a power of two of them).
@@ -242,6 +292,11 @@ inline bool rope_shape(RopeParams& p, const RopeArgs& a, bool norm) {
   }
   p.slots = 32 / p.lanes;
   p.table = vec ? 8 * p.lanes : p.pairs;
+  for (RopeSide& s : p.side) {
+    s.x_step = s.xs[2] * p.slots;
+    s.d_step = s.ds[2] * p.slots;
+    s.y_step = s.ys[2] * p.slots;
+  }
   return vec;
 }
 

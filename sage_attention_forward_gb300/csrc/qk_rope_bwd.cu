@@ -9,30 +9,21 @@
 // the same bits every time.
 #include <cuda_runtime.h>
 
+#include <algorithm>
+
 #include "qk_rope.cuh"
 
 namespace sa {
 namespace {
 
-// (volatile: held in registers over the rows, weights and cosines would spill)
-__device__ __forceinline__ float4 load_shared(const float4* at) {
-  float4 v;
-  asm volatile("ld.shared.v4.f32 {%0, %1, %2, %3}, [%4];"
-               : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
-               : "r"(smem_u32(at)));
-  return v;
-}
-
-__device__ __forceinline__ float2 load_shared(const float2* at) {
-  float2 v;
-  asm volatile("ld.shared.v2.f32 {%0, %1}, [%2];" : "=f"(v.x), "=f"(v.y) : "r"(smem_u32(at)));
-  return v;
-}
+// Rows of a slot whose loads are under way, and CTAs an SM.
+constexpr int rows_ahead(bool vec, int pairs, bool wide) { return vec ? (wide ? 1 : 2) : pairs == 8 ? 1 : 2; }
+constexpr int ctas_an_sm(bool vec, int pairs) { return vec ? 2 : pairs == 2 ? 3 : pairs == 4 ? 2 : 1; }
 
 template <class T, int kMap, int kPairs>
-__global__ void __launch_bounds__(kRopeThreads, kMap >= kAny && kPairs == 8 ? 1 : 2) rope_bwd_kernel(const __grid_constant__ RopeParams p) {
+__global__ void __launch_bounds__(kRopeThreads, ctas_an_sm(kMap < kAny, kPairs)) rope_bwd_kernel(const __grid_constant__ RopeParams p) {
   using L = RopeLane<T, kMap, kPairs>;
-  constexpr int kAhead = sizeof(T) == 4 || (!L::kVec && kPairs == 8) ? 1 : 2;
+  constexpr int kAhead = rows_ahead(L::kVec, kPairs, sizeof(T) == 4);
   // the weights by lanes, [kPairs / 2][lanes] of four (registers do not reach for them); then the tables,
   // [warps][p.table], or at the end the warps' sums, [warps][N]
   extern __shared__ float4 shared[];
@@ -57,31 +48,33 @@ __global__ void __launch_bounds__(kRopeThreads, kMap >= kAny && kPairs == 8 ? 1 
         shared[k * p.lanes + ln.l] = make_float4(w[4 * k], w[4 * k + 1], w[4 * k + 2], w[4 * k + 3]);
     }
     __syncthreads();
-    const int units = p.tokens * sd.parts;
+    const int parts = (sd.heads + sd.per_unit - 1) / sd.per_unit, units = p.tokens * parts;
     for (int unit = blockIdx.x * kRopeWarps + warp; unit < units; unit += gridDim.x * kRopeWarps) {
-      const int token = sd.parts == 1 ? unit : unit / sd.parts, first = (unit - token * sd.parts) * p.per_unit;
-      const int end = min(first + p.per_unit, sd.heads);
+      const int token = parts == 1 ? unit : unit / parts, first = (unit - token * parts) * sd.per_unit;
+      const int end = min(first + sd.per_unit, sd.heads);
       const int b = div_by(token, p.S), s = token - b * (int)p.S.d;
-      const T* const x = reinterpret_cast<const T*>(sd.x) + b * sd.xs[0] + s * sd.xs[1];
-      const T* const dy = reinterpret_cast<const T*>(sd.dy) + b * sd.ds[0] + s * sd.ds[1];
-      T* const dx = reinterpret_cast<T*>(sd.y) + b * sd.ys[0] + s * sd.ys[1];
+      RopeWalk<T> x, dy, dx;
+      x.start(sd.x, sd.xs, b, s, first, end, slot);
+      dy.start(sd.dy, sd.ds, b, s, first, end, slot);
+      dx.start(sd.y, sd.ys, b, s, first, end, slot);
       typename L::Raw rx[kAhead], rd[kAhead];
-      auto load = [&](int u, int h) {
-        if (mine && h < end) {
-          ln.load(x + h * sd.xs[2], p.pairs, rx[u]);
-          ln.load(dy + h * sd.ds[2], p.pairs, rd[u]);
+      auto load = [&](int u) {
+        if (mine && x.head < end) {
+          ln.load(x.row, rx[u]);
+          ln.load(dy.row, rd[u]);
         }
+        x.next(p.slots, sd.x_step);
+        dy.next(p.slots, sd.d_step);
       };
-      int h = first + slot;
 #pragma unroll
-      for (int u = 0; u < kAhead; ++u) load(u, h + u * p.slots);
+      for (int u = 0; u < kAhead; ++u) load(u);
       rope_table<L::kVec>(p, b, s, lane, table);
       for (int base = first; base < end; base += kAhead * p.slots) {
 #pragma unroll
-        for (int u = 0; u < kAhead; ++u, h += p.slots) {
+        for (int u = 0; u < kAhead; ++u) {
           if (base + u * p.slots >= end) break;
           float a[kPairs], c[kPairs], ga[kPairs], gc[kPairs];
-          const bool in = mine && h < end;
+          const bool in = mine && dx.head < end;
           if (in) {
             ln.values(rx[u], a, c);
             ln.values(rd[u], ga, gc);
@@ -89,7 +82,7 @@ __global__ void __launch_bounds__(kRopeThreads, kMap >= kAny && kPairs == 8 ? 1 
 #pragma unroll
             for (int i = 0; i < kPairs; ++i) a[i] = c[i] = ga[i] = gc[i] = 0.0f;
           }
-          load(u, h + kAhead * p.slots);
+          load(u);
           float sum = 0.0f;
 #pragma unroll
           for (int i = 0; i < kPairs; ++i) sum = fmaf(a[i], a[i], fmaf(c[i], c[i], sum));
@@ -98,16 +91,8 @@ __global__ void __launch_bounds__(kRopeThreads, kMap >= kAny && kPairs == 8 ? 1 
 #pragma unroll
           for (int k = 0; k < kPairs / 2; ++k) {
             const float4 w = load_shared(shared + k * p.lanes + ln.l);
-            float2 t[2];   // cosines and sines
-            if (L::kVec) {
-              const float4 two = load_shared(reinterpret_cast<const float4*>(table) + k * p.lanes + ln.l);
-              t[0] = make_float2(two.x, two.y);
-              t[1] = make_float2(two.z, two.w);
-            } else {
-#pragma unroll
-              for (int e = 0; e < 2; ++e)
-                if (ln.pair(2 * k + e) < p.pairs) t[e] = load_shared(table + ln.pair(2 * k + e));
-            }
+            float2 t[2];
+            two_angles(p, ln, table, k, t);
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
               const int i = 2 * k + e;
@@ -132,8 +117,9 @@ __global__ void __launch_bounds__(kRopeThreads, kMap >= kAny && kPairs == 8 ? 1 
               a[i] = r * (ga[i] - a[i] * dot);
               c[i] = r * (gc[i] - c[i] * dot);
             }
-            ln.store(dx + h * sd.ys[2], p.pairs, a, c);
+            ln.store(dx.row, a, c);
           }
+          dx.next(p.slots, sd.y_step);
         }
       }
     }
@@ -150,7 +136,7 @@ __global__ void __launch_bounds__(kRopeThreads, kMap >= kAny && kPairs == 8 ? 1 
     if (slot == 0 && ln.some()) {
 #pragma unroll
       for (int i = 0; i < kPairs; ++i) {
-        const int ia = ln.first(i, p.pairs), ib = ln.second(i, p.pairs);
+        const int ia = ln.first(i), ib = ln.second(i);
         if (ia < p.N) sums[warp * p.N + ia] = da[i];
         if (ib < p.N) sums[warp * p.N + ib] = db[i];
       }
@@ -191,10 +177,11 @@ __global__ void __launch_bounds__(1024) rope_grad_kernel(const float* q_parts, c
 }
 
 template <class T>
-cudaError_t launch_bwd(const RopeParams& p, int ctas, bool vec, bool next, cudaStream_t stream) {
+cudaError_t launch_bwd(const RopeParams& p, int& ctas, bool vec, bool next, cudaStream_t stream) {
   return with_rope_map(vec, next, p.N, [&](auto map, auto pairs) {
     const size_t tables = (size_t)kRopeWarps * p.table * sizeof(float2), sums = (size_t)kRopeWarps * p.N * sizeof(float);
     constexpr int kPairs = decltype(pairs)::value;
+    ctas = std::min(ctas, 152 * ctas_an_sm(decltype(map)::value < kAny, kPairs));
     return launch_dependent(rope_bwd_kernel<T, decltype(map)::value, kPairs>, dim3((unsigned)ctas), kRopeThreads,
                             kPairs / 2 * 32 * sizeof(float4) + (tables > sums ? tables : sums), stream, p);
   });
@@ -202,24 +189,25 @@ cudaError_t launch_bwd(const RopeParams& p, int ctas, bool vec, bool next, cudaS
 
 }  // namespace
 
+// As many as the kernel with most CTAs an SM can have; a CTA may have no unit.
 int rope_bwd_ctas(int B, int S, int Hq, int Hk) {
   const long long warps = ((long long)B * S * (Hq > Hk ? Hq : Hk) + 3) / 4;
   const long long ctas = (warps + kRopeWarps - 1) / kRopeWarps;
-  return ctas < 2 * 152 ? (int)ctas : 2 * 152;
+  return ctas < 4 * 152 ? (int)ctas : 4 * 152;
 }
 
 cudaError_t launch_qk_norm_rope_bwd(const RopeArgs& a, float* workspace, cudaStream_t stream) {
   RopeParams p;
   rope_params(p, a);
   const bool vec = rope_shape(p, a, true);
-  const int ctas = rope_bwd_ctas(a.B, a.S, a.side[0].H, a.side[1].H);
-  const int heads = a.side[0].H > a.side[1].H ? a.side[0].H : a.side[1].H;
-  p.per_unit = (heads + p.slots - 1) / p.slots * p.slots;
-  while (p.per_unit > p.slots && (long long)p.tokens * ((heads + p.per_unit - 1) / p.per_unit) < 152 * 32)
-    p.per_unit = (p.per_unit / 2 + p.slots - 1) / p.slots * p.slots;
+  int ctas = rope_bwd_ctas(a.B, a.S, a.side[0].H, a.side[1].H);
   for (int i = 0; i < 2; ++i) {
-    p.side[i].parts = (a.side[i].H + p.per_unit - 1) / p.per_unit;
-    if (a.side[i].H > 0 && a.side[i].dw != nullptr) p.side[i].partial = workspace + (size_t)i * ctas * a.N;
+    RopeSide& s = p.side[i];
+    const int H = a.side[i].H;
+    s.per_unit = (H + p.slots - 1) / p.slots * p.slots;
+    while (s.per_unit > p.slots && (long long)p.tokens * ((H + s.per_unit - 1) / s.per_unit) < 152 * 32)
+      s.per_unit = (s.per_unit / 2 + p.slots - 1) / p.slots * p.slots;
+    if (H > 0 && a.side[i].dw != nullptr) s.partial = workspace + (size_t)i * ctas * a.N;
   }
   cudaError_t e = a.type == kF32    ? launch_bwd<float>(p, ctas, vec, a.interleaved, stream)
                   : a.type == kBF16 ? launch_bwd<__nv_bfloat16>(p, ctas, vec, a.interleaved, stream)

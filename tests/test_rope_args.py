@@ -72,7 +72,7 @@ def test_accepted_up_to_the_device():
 def test_workspace_sizes():
     size = sa.lib().qk_norm_rope_bwd_workspace_size
     assert size(0, 4, 2, 2, 128) == 0 and size(1, 4, 2, 2, 513) == 0 and size(1 << 20, 1 << 20, 1, 1, 8) == 0
-    assert 0 < size(1, 1, 1, 0, 1) <= 8 and size(1, 1 << 20, 32, 32, 128) == 2 * 304 * 128 * 4
+    assert 0 < size(1, 1, 1, 0, 1) <= 8 and size(1, 1 << 20, 32, 32, 128) == 2 * 608 * 128 * 4
 
 
 def test_frequencies():
