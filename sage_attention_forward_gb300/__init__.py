@@ -791,82 +791,104 @@ def rope_frequencies(rope_dim: int, theta: float = 10000.0, axes=None, scaling: 
     return torch.tensor(out, dtype=torch.int64, device=device), magnitude
 
 
-def _rope_args(q, k, freq, positions):
-    """Sizes, the device, and what positions come to: (sizes, N, dev, pointer, strides, axes)."""
+# The calls below are made for every layer of every token that is served: their checks are straight lines.
+_current_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
+_empty = torch.empty
+
+
+def _rope_rows(q, k):
+    """(type code, device, strides of q and k) of rows [B, S, heads, N], k or None."""
     if q.dim() != 4:
         raise ValueError(f"rows must be [B, S, H, N], got {tuple(q.shape)}")
-    if q.dtype not in _DTYPES:
+    code, dev = _DTYPES.get(q.dtype), q.get_device()
+    if code is None:
         raise ValueError(f"rows must be bfloat16, float16 or float32, got {q.dtype}")
-    B, S, Hq, N = q.shape
-    dev = _cuda_index("q", q)
-    Hk = 0
+    if dev < 0:
+        raise ValueError("q must be a CUDA tensor")
+    strides = q.stride()
     if k is not None:
-        if k.dim() != 4:
-            raise ValueError(f"rows must be [B, S, H, N], got {tuple(k.shape)}")
-        Hk = k.shape[2]
-        _expect("k", k, (B, S, Hk, N), q.dtype, dev)
-    if q.numel() > 0x7fffffff or (k is not None and k.numel() > 0x7fffffff):
-        _sizes(B, S, Hq, Hk, N)
-    if freq is not None:
-        _expect_dense("freq", freq, freq.shape[:1], torch.int64, dev)
+        B, S, H, N = q.shape
+        _expect("k", k, (B, S, k.shape[2] if k.dim() == 4 else H, N), q.dtype, dev)
+        strides += k.stride()
+        if k.numel() > 0x7fffffff:
+            _sizes(*k.shape)
+    if q.numel() > 0x7fffffff:
+        _sizes(*q.shape)
+    return code, dev, strides
+
+
+def _rope_positions(positions, B, S, dev):
+    """(pointer, strides, axes) of positions [S], [B, S] or [B, S, axes], B or 1 in front."""
     if positions is None:
-        return (B, S, Hq, Hk, N), dev, None, None, 1
+        return None, (0, 0, 0), 1
     if positions.dtype is not torch.int32:
         raise ValueError(f"positions must be int32, got {positions.dtype}")
     if positions.get_device() != dev:
         raise ValueError(f"positions is on {positions.device}, expected cuda:{dev}")
     shape, st = positions.shape, positions.stride()
-    if len(shape) == 1 and shape[0] == S:
-        strides, axes = (0, st[0], 0), 1
-    elif len(shape) in (2, 3) and shape[0] in (1, B) and shape[1] == S and (len(shape) == 2 or 1 <= shape[2] <= 4):
-        axes = shape[2] if len(shape) == 3 else 1
-        strides = (0 if shape[0] == 1 else st[0], st[1], st[2] if axes > 1 else 0)
-    else:
-        raise ValueError(f"positions must be [{S}], [{B}, {S}] or [{B}, {S}, axes], got {tuple(shape)}")
-    return (B, S, Hq, Hk, N), dev, positions.data_ptr(), array("q", strides), axes
+    n = len(shape)
+    if n == 2 and shape[1] == S and (shape[0] == B or shape[0] == 1):
+        return positions.data_ptr(), (st[0] if shape[0] > 1 else 0, st[1], 0), 1
+    if n == 3 and shape[1] == S and (shape[0] == B or shape[0] == 1) and 1 <= shape[2] <= 4:
+        return positions.data_ptr(), (st[0] if shape[0] > 1 else 0, st[1], st[2]), shape[2]
+    if n == 1 and shape[0] == S:
+        return positions.data_ptr(), (0, st[0], 0), 1
+    raise ValueError(f"positions must be [{S}], [{B}, {S}] or [{B}, {S}, axes], got {tuple(shape)}")
 
 
-def _rope_outputs(names: str, dev: int, *pairs):
-    """The outputs, made where they are not given: of each (rows, output)."""
-    out = []
-    for name, (x, o) in zip(names.split(), pairs):
-        if x is None:
-            if o is not None:
-                raise ValueError(f"{name} was given without its rows")
-        elif o is None:
-            o = torch.empty(x.shape, dtype=x.dtype, device=dev)
-        else:
-            _expect(name, o, x.shape, x.dtype, dev)
-        out.append(o)
+def _rope_freq(freq, dev):
+    """(pointer, rope_dim)"""
+    if freq is None:
+        return None, 0
+    if freq.dtype is not torch.int64 or freq.dim() != 1 or not freq.is_contiguous():
+        raise ValueError(f"freq must be contiguous int64 [rope_dim / 2], got {tuple(freq.shape)} {freq.dtype}")
+    if freq.get_device() != dev:
+        raise ValueError(f"freq is on {freq.device}, expected cuda:{dev}")
+    return freq.data_ptr(), 2 * freq.shape[0]
+
+
+def _rope_made(name, x, out, dev):
+    """The output for rows x, made where it is not given."""
+    if out is None:
+        return _empty(x.shape, dtype=x.dtype, device=dev)
+    _expect(name, out, x.shape, x.dtype, dev)
     return out
 
 
-def _ptr(t):
-    return None if t is None else t.data_ptr()
+def _unit_channels(N, strides) -> None:
+    """Four strides a tensor, the last of each 1 (a single channel may have any)."""
+    if N > 1 and strides[3::4].count(1) != len(strides) // 4:
+        raise ValueError("rows must have unit channel stride")
 
 
-def _rope_strides(names: str, *tensors):
-    """Addresses of the tensors' strides (None for a missing one) and the array that holds them."""
-    given = [(n, t) for n, t in zip(names.split(), tensors) if t is not None]
-    held = _norm_strides(" ".join(n for n, _ in given), *(t for _, t in given))
-    at = held.buffer_info()[0]
-    out = []
-    for t in tensors:
-        out.append(None if t is None else at)
-        at += 0 if t is None else 32
-    return out, held
-
-
-def _rope(call: str, q, k, freq, positions, interleaved, magnitude, q_out, k_out, stream):
-    sizes, dev, pos, pos_strides, axes = _rope_args(q, k, freq, positions)
-    if _elsewhere(dev, stream):
+def _rope(call, q, k, freq, positions, interleaved, magnitude, q_out, k_out, stream):
+    code, dev, strides = _rope_rows(q, k)
+    if stream is not None or dev != _current_device():
         with _there(dev, stream):
             return _rope(call, q, k, freq, positions, interleaved, magnitude, q_out, k_out, None)
-    q_out, k_out = _rope_outputs("q_out k_out", dev, (q, q_out), (k, k_out))
-    at, _held = _rope_strides("q k q_out k_out", q, k, q_out, k_out)
-    _check(getattr(lib(), call)(q.data_ptr(), _ptr(k), q_out.data_ptr(), _ptr(k_out), *sizes, *at, pos,
-                                pos_strides.buffer_info()[0] if pos_strides else None, axes, freq.data_ptr(),
-                                2 * freq.shape[0], interleaved, magnitude, _DTYPES[q.dtype], _current_stream(dev)))
+    B, S, Hq, N = q.shape
+    at, at_strides, axes = _rope_positions(positions, B, S, dev)
+    f, rope_dim = _rope_freq(freq, dev)
+    q_out = _rope_made("q_out", q, q_out, dev)
+    strides += q_out.stride()
+    if k is not None:
+        k_out = _rope_made("k_out", k, k_out, dev)
+        strides += k_out.stride()
+        _unit_channels(N, strides)
+        held = array("q", strides + at_strides)
+        p = held.buffer_info()[0]
+        status = call(q.data_ptr(), k.data_ptr(), q_out.data_ptr(), k_out.data_ptr(), B, S, Hq, k.shape[2], N, p, p + 32,
+                      p + 64, p + 96, at, p + 128, axes, f, rope_dim, interleaved, magnitude, code, _current_stream(dev))
+    else:
+        if k_out is not None:
+            raise ValueError("k_out was given without k")
+        _unit_channels(N, strides)
+        held = array("q", strides + at_strides)
+        p = held.buffer_info()[0]
+        status = call(q.data_ptr(), None, q_out.data_ptr(), None, B, S, Hq, 0, N, p, p, p + 32, p + 32, at, p + 64, axes, f,
+                      rope_dim, interleaved, magnitude, code, _current_stream(dev))
+    if status != 0:
+        _check(status)
     return q_out, k_out
 
 
@@ -879,7 +901,7 @@ def rope_fwd(q: torch.Tensor, k: torch.Tensor | None, freq: torch.Tensor, positi
     freq, magnitude: from rope_frequencies.  positions: int32 [S], [B, S] or [B, S, axes] (B may be 1); None: 0 to S - 1.
     interleaved: pairs of neighbouring channels; else of the two halves of the rotated part.  q_out and k_out may be q
     and k themselves."""
-    return _rope("rope_fwd", q, k, freq, positions, interleaved, magnitude, q_out, k_out, stream)
+    return _rope(lib().rope_fwd, q, k, freq, positions, interleaved, magnitude, q_out, k_out, stream)
 
 
 def rope_bwd(dq_out: torch.Tensor, dk_out: torch.Tensor | None, freq: torch.Tensor,
@@ -887,19 +909,27 @@ def rope_bwd(dq_out: torch.Tensor, dk_out: torch.Tensor | None, freq: torch.Tens
              dq: torch.Tensor | None = None, dk: torch.Tensor | None = None,
              stream=None) -> tuple[torch.Tensor, torch.Tensor | None]:
     """The gradients of rope_fwd, (dq, dk), from those of its outputs; the other arguments as it was given them."""
-    return _rope("rope_bwd", dq_out, dk_out, freq, positions, interleaved, magnitude, dq, dk, stream)
+    return _rope(lib().rope_bwd, dq_out, dk_out, freq, positions, interleaved, magnitude, dq, dk, stream)
 
 
-def _rope_weights(q, q_weight, k_weight, dev: int) -> torch.dtype:
-    """The type of the weights, each [N] of the rows' type or float32."""
+def _rope_weights(q, k, q_weight, k_weight, dev: int):
+    """(q_weight's pointer, k_weight's, type) of weights [N] of the rows' type or float32."""
     w_type = q.dtype
     if q_weight is not None:
-        _norm_weight("q_weight", q_weight, q, dev)
-        w_type = q_weight.dtype
+        if q_weight.dtype is torch.float32:
+            w_type = torch.float32
+        _expect_dense("q_weight", q_weight, q.shape[3:], w_type, dev)
     if k_weight is not None:
-        _norm_weight("k_weight", k_weight, q, dev, None if q_weight is None else w_type)
-        w_type = k_weight.dtype
-    return w_type
+        if k is None:
+            raise ValueError("k_weight was given without k")
+        if q_weight is None and k_weight.dtype is torch.float32:
+            w_type = torch.float32
+        _expect_dense("k_weight", k_weight, q.shape[3:], w_type, dev)
+    return _ptr(q_weight), _ptr(k_weight), w_type
+
+
+def _ptr(t):
+    return None if t is None else t.data_ptr()
 
 
 def qk_norm_rope_fwd(q: torch.Tensor, k: torch.Tensor | None, q_weight: torch.Tensor | None,
@@ -909,17 +939,33 @@ def qk_norm_rope_fwd(q: torch.Tensor, k: torch.Tensor | None, q_weight: torch.Te
                      stream=None) -> tuple[torch.Tensor, torch.Tensor | None]:
     """The RMS norm of each head of q and k, times its weight [N] (or None), and the rotation of rope_fwd, in one pass:
     (q', k').  freq None: the norm alone."""
-    sizes, dev, pos, pos_strides, axes = _rope_args(q, k, freq, positions)
-    if _elsewhere(dev, stream):
+    code, dev, strides = _rope_rows(q, k)
+    if stream is not None or dev != _current_device():
         with _there(dev, stream):
             return qk_norm_rope_fwd(q, k, q_weight, k_weight, freq, positions, eps, interleaved, magnitude, q_out, k_out)
-    w_type = _rope_weights(q, q_weight, k_weight, dev)
-    q_out, k_out = _rope_outputs("q_out k_out", dev, (q, q_out), (k, k_out))
-    at, _held = _rope_strides("q k q_out k_out", q, k, q_out, k_out)
-    _check(lib().qk_norm_rope_fwd(q.data_ptr(), _ptr(k), _ptr(q_weight), _ptr(k_weight), q_out.data_ptr(), _ptr(k_out),
-                                  *sizes, *at, eps, pos, pos_strides.buffer_info()[0] if pos_strides else None, axes,
-                                  _ptr(freq), 0 if freq is None else 2 * freq.shape[0], interleaved, magnitude,
-                                  _DTYPES[q.dtype], _DTYPES[w_type], _current_stream(dev)))
+    B, S, Hq, N = q.shape
+    at, at_strides, axes = _rope_positions(positions, B, S, dev)
+    f, rope_dim = _rope_freq(freq, dev)
+    qw, kw, w_type = _rope_weights(q, k, q_weight, k_weight, dev)
+    q_out = _rope_made("q_out", q, q_out, dev)
+    strides += q_out.stride()
+    if k is not None:
+        k_out = _rope_made("k_out", k, k_out, dev)
+        strides += k_out.stride()
+        Hk, step = k.shape[2], 32
+    elif k_out is not None:
+        raise ValueError("k_out was given without k")
+    else:
+        Hk = step = 0
+    _unit_channels(N, strides)
+    held = array("q", strides + at_strides)
+    p = held.buffer_info()[0]
+    o = p + 32 + step
+    status = lib().qk_norm_rope_fwd(q.data_ptr(), _ptr(k), qw, kw, q_out.data_ptr(), _ptr(k_out), B, S, Hq, Hk, N, p, p + step,
+                                    o, o + step, eps, at, o + 32 + step, axes, f, rope_dim, interleaved, magnitude, code,
+                                    _DTYPES[w_type], _current_stream(dev))
+    if status != 0:
+        _check(status)
     return q_out, k_out
 
 
@@ -931,6 +977,17 @@ def qk_norm_rope_bwd_workspace(q_shape, kv_heads: int, device) -> torch.Tensor:
     return torch.empty(lib().qk_norm_rope_bwd_workspace_size(B, S, Hq, kv_heads, N), dtype=torch.uint8, device=device)
 
 
+def _rope_grad(name, w, dw, w_type, dev):
+    if w is None:
+        if dw is not None:
+            raise ValueError(f"{name} was given without its weight")
+        return None
+    if dw is None:
+        return _empty(w.shape, dtype=w_type, device=dev)
+    _expect_dense(name, dw, w.shape, w_type, dev)
+    return dw
+
+
 def qk_norm_rope_bwd(dq_out: torch.Tensor, dk_out: torch.Tensor | None, q: torch.Tensor, k: torch.Tensor | None,
                      q_weight: torch.Tensor | None, k_weight: torch.Tensor | None, freq: torch.Tensor | None,
                      positions: torch.Tensor | None = None, eps: float = 1e-6, interleaved: bool = False,
@@ -940,38 +997,48 @@ def qk_norm_rope_bwd(dq_out: torch.Tensor, dk_out: torch.Tensor | None, q: torch
     """(dq, dk, dq_weight, dk_weight) of qk_norm_rope_fwd: dq_out and dk_out are the gradients of its outputs, the other
     arguments those it was given.  A weight's gradient has its type and is None without the weight.  The same inputs give
     the same bits."""
-    sizes, dev, pos, pos_strides, axes = _rope_args(q, k, freq, positions)
-    if _elsewhere(dev, stream):
+    code, dev, strides = _rope_rows(q, k)
+    if stream is not None or dev != _current_device():
         with _there(dev, stream):
             return qk_norm_rope_bwd(dq_out, dk_out, q, k, q_weight, k_weight, freq, positions, eps, interleaved,
                                     magnitude, dq, dk, dq_weight, dk_weight, workspace)
+    B, S, Hq, N = q.shape
+    at, at_strides, axes = _rope_positions(positions, B, S, dev)
+    f, rope_dim = _rope_freq(freq, dev)
+    qw, kw, w_type = _rope_weights(q, k, q_weight, k_weight, dev)
     _expect("dq_out", dq_out, q.shape, q.dtype, dev)
-    if k is None:
-        if not (dk_out is None and k_weight is None):
-            raise ValueError("dk_out and k_weight must be None without k")
-    else:
+    dq = _rope_made("dq", q, dq, dev)
+    if k is not None:
         _expect("dk_out", dk_out, k.shape, q.dtype, dev)
-    w_type = _rope_weights(q, q_weight, k_weight, dev)
-    dq, dk = _rope_outputs("dq dk", dev, (q, dq), (k, dk))
-    grads = []
-    for name, w, dw in (("dq_weight", q_weight, dq_weight), ("dk_weight", k_weight, dk_weight)):
-        if w is None and dw is not None:
-            raise ValueError(f"{name} was given without its weight")
-        if dw is not None:
-            _norm_weight(name, dw, q, dev, w_type)
-        grads.append(torch.empty(w.shape, dtype=w_type, device=dev) if w is not None and dw is None else dw)
-    size = 0
-    if q_weight is not None or k_weight is not None:
+        dk = _rope_made("dk", k, dk, dev)
+        strides += dq_out.stride() + dk_out.stride() + dq.stride() + dk.stride()
+        Hk, step = k.shape[2], 32
+    elif dk_out is not None or dk is not None:
+        raise ValueError("dk_out and dk must be None without k")
+    else:
+        strides += dq_out.stride() + dq.stride()
+        Hk = step = 0
+    dqw = _rope_grad("dq_weight", q_weight, dq_weight, w_type, dev)
+    dkw = _rope_grad("dk_weight", k_weight, dk_weight, w_type, dev)
+    L, size, scratch = lib(), 0, None
+    if dqw is not None or dkw is not None:
         if workspace is None:
-            workspace = qk_norm_rope_bwd_workspace(q.shape, sizes[3], dev)
-        size = _scratch("workspace", workspace, dev)
-    at, _held = _rope_strides("dq_out dk_out q k dq dk", dq_out, dk_out, q, k, dq, dk)
-    _check(lib().qk_norm_rope_bwd(dq_out.data_ptr(), _ptr(dk_out), q.data_ptr(), _ptr(k), _ptr(q_weight), _ptr(k_weight),
-                                  dq.data_ptr(), _ptr(dk), _ptr(grads[0]), _ptr(grads[1]), *sizes, *at, eps, pos,
-                                  pos_strides.buffer_info()[0] if pos_strides else None, axes, _ptr(freq),
-                                  0 if freq is None else 2 * freq.shape[0], interleaved, magnitude, _DTYPES[q.dtype],
-                                  _DTYPES[w_type], workspace.data_ptr() if size else None, size, _current_stream(dev)))
-    return dq, dk, grads[0], grads[1]
+            size = L.qk_norm_rope_bwd_workspace_size(B, S, Hq, Hk, N)
+            workspace = _empty(size, dtype=torch.uint8, device=dev)
+        else:
+            size = _scratch("workspace", workspace, dev)
+        scratch = workspace.data_ptr()
+    _unit_channels(N, strides)
+    held = array("q", strides + at_strides)
+    p = held.buffer_info()[0]
+    d, o = p + 32 + step, p + 64 + 2 * step
+    status = L.qk_norm_rope_bwd(dq_out.data_ptr(), _ptr(dk_out), q.data_ptr(), _ptr(k), qw, kw, dq.data_ptr(), _ptr(dk),
+                                _ptr(dqw), _ptr(dkw), B, S, Hq, Hk, N, d, d + step, p, p + step, o, o + step, eps, at,
+                                o + 32 + step, axes, f, rope_dim, interleaved, magnitude, code, _DTYPES[w_type], scratch, size,
+                                _current_stream(dev))
+    if status != 0:
+        _check(status)
+    return dq, dk, dqw, dkw
 
 
 _KV4_RECORD = 2304   # bytes of 16 tokens of a key head, K and V
@@ -987,24 +1054,39 @@ def kv4_cache(num_pages: int, kv_heads: int, page_size: int, device="cuda") -> t
 
 def _kv4_args(cache, page_table, B: int):
     """(pages, heads, page size, table's row stride, pages a request, device)."""
-    dev = _cuda_index("cache", cache)
-    if cache.dim() != 4 or cache.shape[3] != _KV4_RECORD or cache.dtype is not torch.uint8 or not cache.is_contiguous():
+    dev = cache.get_device()
+    if dev < 0:
+        raise ValueError("cache must be a CUDA tensor")
+    if cache.dim() != 4 or cache.dtype is not torch.uint8 or not cache.is_contiguous() or cache.shape[3] != _KV4_RECORD:
         raise ValueError(f"cache must be contiguous uint8 [pages, heads, page_size / 16, {_KV4_RECORD}], got "
                          f"{tuple(cache.shape)} {cache.dtype}")
-    if page_table.dim() != 2:
-        raise ValueError(f"page_table must be [B, pages], got {tuple(page_table.shape)}")
-    most = page_table.shape[1]
-    _expect("page_table", page_table, (B, most), torch.int32, dev)
-    if most > 1 and page_table.stride(1) != 1:
-        raise ValueError("page_table must have unit stride along a request's pages")
     pages, heads, tiles, _ = cache.shape
+    if page_table.dim() != 2 or page_table.dtype is not torch.int32 or page_table.shape[0] != B:
+        raise ValueError(f"page_table must be int32 [{B}, pages], got {tuple(page_table.shape)} {page_table.dtype}")
+    if page_table.get_device() != dev:
+        raise ValueError(f"page_table is on {page_table.device}, expected cuda:{dev}")
+    most, (table_str, unit) = page_table.shape[1], page_table.stride()
+    if unit != 1 and most > 1:
+        raise ValueError("page_table must have unit stride along a request's pages")
     if max(pages, heads, 16 * tiles, B, most) > 0x7fffffff:
         _sizes(pages, heads, 16 * tiles, B, most)
-    return pages, heads, 16 * tiles, page_table.stride(0), most, dev
+    return pages, heads, 16 * tiles, table_str, most, dev
 
 
-def _kv4_rows(name: str, t: torch.Tensor, shape, dev: int):
-    _expect(name, t, shape, torch.bfloat16, dev)
+def _kv4_counts(name, t, B, dev):
+    if t.dtype is not torch.int32 or t.dim() != 1 or t.shape[0] != B or not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous int32 [{B}], got {tuple(t.shape)} {t.dtype}")
+    if t.get_device() != dev:
+        raise ValueError(f"{name} is on {t.device}, expected cuda:{dev}")
+    return t.data_ptr()
+
+
+def _kv4_strides(*tensors):
+    """An array of four strides a tensor (the last of each 1)."""
+    strides = tensors[0].stride() + tensors[1].stride()
+    if strides[3] != 1 or strides[7] != 1:
+        raise ValueError("rows must have unit channel stride")
+    return array("q", strides)
 
 
 def kv4_write(k: torch.Tensor, v: torch.Tensor, cache: torch.Tensor, page_table: torch.Tensor, start: torch.Tensor,
@@ -1018,19 +1100,22 @@ def kv4_write(k: torch.Tensor, v: torch.Tensor, cache: torch.Tensor, page_table:
         raise ValueError(f"k must be [B, S, H, D], got {tuple(k.shape)}")
     B, S, _, D = k.shape
     pages, heads, page_size, table_str, most, dev = _kv4_args(cache, page_table, B)
-    if _elsewhere(dev, stream):
+    if stream is not None or dev != _current_device():
         with _there(dev, stream):
             return kv4_write(k, v, cache, page_table, start, count)
-    _sizes(S, D)
-    _kv4_rows("k", k, (B, S, heads, D), dev)
-    _kv4_rows("v", v, (B, S, heads, D), dev)
-    _expect_dense("start", start, (B,), torch.int32, dev)
-    if count is not None:
-        _expect_dense("count", count, (B,), torch.int32, dev)
-    strides = _strides("k v", k, v)
-    at = strides.buffer_info()[0]
-    _check(lib().kv4_write(k.data_ptr(), v.data_ptr(), cache.data_ptr(), pages, page_size, page_table.data_ptr(), table_str,
-                           most, start.data_ptr(), _ptr(count), B, S, heads, D, at, at + 32, _current_stream(dev)))
+    if S > 0x7fffffff or D > 0x7fffffff:
+        _sizes(S, D)
+    shape = (B, S, heads, D)
+    _expect("k", k, shape, torch.bfloat16, dev)
+    _expect("v", v, shape, torch.bfloat16, dev)
+    held = _kv4_strides(k, v)
+    at = held.buffer_info()[0]
+    status = lib().kv4_write(k.data_ptr(), v.data_ptr(), cache.data_ptr(), pages, page_size, page_table.data_ptr(), table_str,
+                             most, _kv4_counts("start", start, B, dev),
+                             None if count is None else _kv4_counts("count", count, B, dev), B, S, heads, D, at, at + 32,
+                             _current_stream(dev))
+    if status != 0:
+        _check(status)
 
 
 def kv4_read(cache: torch.Tensor, page_table: torch.Tensor, start: torch.Tensor, S: int,
@@ -1040,22 +1125,28 @@ def kv4_read(cache: torch.Tensor, page_table: torch.Tensor, start: torch.Tensor,
     count[b] on and where there is no page."""
     B = page_table.shape[0]
     pages, heads, page_size, table_str, most, dev = _kv4_args(cache, page_table, B)
-    if _elsewhere(dev, stream):
+    if stream is not None or dev != _current_device():
         with _there(dev, stream):
             return kv4_read(cache, page_table, start, S, count, k, v)
-    _sizes(S)
+    if S > 0x7fffffff:
+        _sizes(S)
     shape = (B, S, heads, 128)
-    k = torch.empty(shape, dtype=torch.bfloat16, device=dev) if k is None else k
-    v = torch.empty(shape, dtype=torch.bfloat16, device=dev) if v is None else v
-    _kv4_rows("k", k, shape, dev)
-    _kv4_rows("v", v, shape, dev)
-    _expect_dense("start", start, (B,), torch.int32, dev)
-    if count is not None:
-        _expect_dense("count", count, (B,), torch.int32, dev)
-    strides = _strides("k v", k, v)
-    at = strides.buffer_info()[0]
-    _check(lib().kv4_read(cache.data_ptr(), pages, page_size, page_table.data_ptr(), table_str, most, start.data_ptr(),
-                          _ptr(count), k.data_ptr(), v.data_ptr(), B, S, heads, 128, at, at + 32, _current_stream(dev)))
+    if k is None:
+        k = _empty(shape, dtype=torch.bfloat16, device=dev)
+    else:
+        _expect("k", k, shape, torch.bfloat16, dev)
+    if v is None:
+        v = _empty(shape, dtype=torch.bfloat16, device=dev)
+    else:
+        _expect("v", v, shape, torch.bfloat16, dev)
+    held = _kv4_strides(k, v)
+    at = held.buffer_info()[0]
+    status = lib().kv4_read(cache.data_ptr(), pages, page_size, page_table.data_ptr(), table_str, most,
+                            _kv4_counts("start", start, B, dev),
+                            None if count is None else _kv4_counts("count", count, B, dev), k.data_ptr(), v.data_ptr(), B, S,
+                            heads, 128, at, at + 32, _current_stream(dev))
+    if status != 0:
+        _check(status)
     return k, v
 
 
@@ -1078,32 +1169,36 @@ def attn_fwd_kv4(q: torch.Tensor, cache: torch.Tensor, page_table: torch.Tensor,
     a few tokens a request; for long pieces of a prompt see kv4_read.  The same inputs give the same bits."""
     if q.dim() != 4:
         raise ValueError(f"q must be [B, S, H, D], got {tuple(q.shape)}")
-    B, Sq, Hq, D = q.shape
+    B, Sq, Hq, D = shape = q.shape
     pages, heads, page_size, table_str, most, dev = _kv4_args(cache, page_table, B)
-    if _elsewhere(dev, stream):
+    if stream is not None or dev != _current_device():
         with _there(dev, stream):
             return attn_fwd_kv4(q, cache, page_table, kv_len, softmax_scale, causal, out, lse, workspace)
-    _sizes(Sq, Hq, D)
-    _kv4_rows("q", q, q.shape, dev)
-    _expect_dense("kv_len", kv_len, (B,), torch.int32, dev)
+    if q.numel() > 0x7fffffff:
+        _sizes(Sq, Hq, D)
+    _expect("q", q, shape, torch.bfloat16, dev)
     if out is None:
-        out = torch.empty(q.shape, dtype=torch.bfloat16, device=dev)
+        out = _empty(shape, dtype=torch.bfloat16, device=dev)
     else:
-        _expect("out", out, q.shape, torch.bfloat16, dev)
-    rows = (B, Hq, Sq)
+        _expect("out", out, shape, torch.bfloat16, dev)
     if lse is None:
-        lse = torch.empty(rows, dtype=torch.float32, device=dev)
+        lse = _empty((B, Hq, Sq), dtype=torch.float32, device=dev)
     else:
-        _expect_dense("lse", lse, rows, torch.float32, dev)
+        _expect_dense("lse", lse, (B, Hq, Sq), torch.float32, dev)
+    L = lib()
     if workspace is None:
-        workspace = torch.empty(lib().attn_fwd_kv4_workspace_size(B, Sq, Hq, heads, most, page_size), dtype=torch.uint8,
-                                device=dev)
-    strides = _strides("q out", q, out)
-    at = strides.buffer_info()[0]
-    _check(lib().attn_fwd_kv4(q.data_ptr(), cache.data_ptr(), pages, page_size, page_table.data_ptr(), table_str, most,
-                              kv_len.data_ptr(), out.data_ptr(), lse.data_ptr(), B, Sq, Hq, heads, D, at, at + 32,
-                              D ** -0.5 if softmax_scale is None else softmax_scale, causal, workspace.data_ptr(),
-                              _scratch("workspace", workspace, dev), _current_stream(dev)))
+        size = L.attn_fwd_kv4_workspace_size(B, Sq, Hq, heads, most, page_size)
+        workspace = _empty(size, dtype=torch.uint8, device=dev)
+    else:
+        size = _scratch("workspace", workspace, dev)
+    held = _kv4_strides(q, out)
+    at = held.buffer_info()[0]
+    status = L.attn_fwd_kv4(q.data_ptr(), cache.data_ptr(), pages, page_size, page_table.data_ptr(), table_str, most,
+                            _kv4_counts("kv_len", kv_len, B, dev), out.data_ptr(), lse.data_ptr(), B, Sq, Hq, heads, D, at,
+                            at + 32, D ** -0.5 if softmax_scale is None else softmax_scale, causal, workspace.data_ptr(), size,
+                            _current_stream(dev))
+    if status != 0:
+        _check(status)
     return out, lse
 
 
