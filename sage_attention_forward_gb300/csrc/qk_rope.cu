@@ -15,19 +15,20 @@ namespace {
 
 // Rows of a slot whose loads are under way, and CTAs an SM: loads in flight are what the kernels wait for, and more warps with
 // fewer rows each do better (76112 x 80 heads of 128 BF16: four rows, two CTAs 546 us; two, three 497; two, four 467).
-constexpr int rows_ahead(bool vec, int pairs, bool wide) { return vec ? (wide ? 1 : 2) : pairs == 2 ? 4 : 2; }
-constexpr int ctas_an_sm(bool vec, bool wide, bool norm) { return !vec ? 1 : !wide ? 4 : norm ? 2 : 3; }
+constexpr int rows_ahead(int map, int pairs, bool wide) { return map < kAny ? (wide ? 1 : 2) : pairs == 2 ? 4 : 2; }
+constexpr int ctas_an_sm(int map, bool wide, bool norm) {
+  return map >= kAny ? 1 : map == kApart ? (wide ? 2 : 3) : wide ? (norm ? 2 : 3) : map == kHalf && norm ? 3 : 4;
+}
 
 template <class T, int kMap, int kPairs, bool kNorm>
-__global__ void __launch_bounds__(kRopeThreads, ctas_an_sm(kMap < kAny, sizeof(T) == 4, kNorm))
+__global__ void __launch_bounds__(kRopeThreads, ctas_an_sm(kMap, sizeof(T) == 4, kNorm))
     rope_fwd_kernel(const __grid_constant__ RopeParams p) {
   using L = RopeLane<T, kMap, kPairs>;
-  constexpr int kAhead = rows_ahead(L::kVec, kPairs, sizeof(T) == 4);
+  constexpr int kAhead = rows_ahead(kMap, kPairs, sizeof(T) == 4);
   // kNorm: the weights of Q and of K by lanes, [2][kPairs / 2][lanes] of four (held in registers they take the warps that hide
   // the loads); then the tables
   extern __shared__ __align__(16) float4 shared[];
-  float2* const tables = reinterpret_cast<float2*>(shared + (kNorm ? kPairs * 32 : 0));
-  const float4* weights = shared;
+  unsigned char* const tables = reinterpret_cast<unsigned char*>(shared + (kNorm ? kPairs * 32 : 0));
   griddep_wait();
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   if constexpr (kNorm) {
@@ -68,17 +69,16 @@ __global__ void __launch_bounds__(kRopeThreads, ctas_an_sm(kMap < kAny, sizeof(T
 #pragma unroll
   for (int u = 0; u < kAhead; ++u) load(u);
 
-  float2* const table = tables + warp * p.table;
-  rope_table<L::kVec>(p, b, s, lane, table);
+  float2* const table = reinterpret_cast<float2*>(tables + warp * p.shared);
+  float* const swap = reinterpret_cast<float*>(table + p.table);
+  if (L::kExchange && lane == 0) swap[16 * 32] = 0.0f;
+  rope_table<kMap>(p, b, s, lane, table);
 
   for (int base = 0; base < turns; base += kAhead) {
 #pragma unroll
     for (int u = 0; u < kAhead; ++u) {
       if (base + u >= turns) break;
-      if (base + u == turns_q) {
-        share(out, 1, p.side[1].y, p.side[1].ys);
-        if constexpr (kNorm) weights = shared + kPairs / 2 * 32;
-      }
+      if (base + u == turns_q) share(out, 1, p.side[1].y, p.side[1].ys);
       float a[kPairs], c[kPairs];
       const bool some = mine && out.head < out.end;
       if (some) {
@@ -94,31 +94,18 @@ __global__ void __launch_bounds__(kRopeThreads, ctas_an_sm(kMap < kAny, sizeof(T
         for (int i = 0; i < kPairs; ++i) sum = fmaf(a[i], a[i], fmaf(c[i], c[i], sum));
         sum = rope_row_sum(sum, p.lanes);
         const float r = rsqrtf(fmaf(sum, p.inv_n, p.eps));
+        const float4* const weights = shared + (base + u >= turns_q ? kPairs / 2 * 32 : 0) + ln.l;
 #pragma unroll
         for (int k = 0; k < kPairs / 2; ++k) {
-          const float4 w = load_shared(weights + k * p.lanes + ln.l);
+          const float4 w = load_shared(weights + k * p.lanes);
           a[2 * k] *= r * w.x;
           c[2 * k] *= r * w.y;
           a[2 * k + 1] *= r * w.z;
           c[2 * k + 1] *= r * w.w;
         }
       }
-      if (some) {
-#pragma unroll
-        for (int k = 0; k < kPairs / 2; ++k) {
-          float2 t[2];
-          two_angles(p, ln, table, k, t);
-#pragma unroll
-          for (int e = 0; e < 2; ++e) {
-            const int i = 2 * k + e;
-            if (ln.pair(i) >= p.pairs) continue;   // (an infinity beside a channel that passes stays out of it)
-            const float a0 = a[i];
-            a[i] = a0 * t[e].x - c[i] * t[e].y;
-            c[i] = c[i] * t[e].x + a0 * t[e].y;
-          }
-        }
-        ln.store(out.row, a, c);
-      }
+      if (L::kExchange || some) rope_turn<kPairs>(p, ln, table, swap, lane, a, c);
+      if (some) ln.store(out.row, a, c);
       out.next(p.slots, p.side[base + u >= turns_q].y_step);
     }
   }
@@ -127,10 +114,10 @@ __global__ void __launch_bounds__(kRopeThreads, ctas_an_sm(kMap < kAny, sizeof(T
 template <class T, bool kNorm>
 cudaError_t launch_fwd(RopeParams& p, bool vec, bool next, cudaStream_t stream) {
   const long long units = (long long)p.tokens * p.by_parts.d;
-  return with_rope_map(vec, next, p.N, [&](auto map, auto pairs) {
+  return with_rope_map(p, vec, next, [&](auto map, auto pairs) {
     constexpr int kPairs = decltype(pairs)::value;
     return launch_dependent(rope_fwd_kernel<T, decltype(map)::value, kPairs, kNorm>, dim3((unsigned)((units + kRopeWarps - 1) / kRopeWarps)),
-                            kRopeThreads, (kNorm ? kPairs * 32 * sizeof(float4) : 0) + kRopeWarps * p.table * sizeof(float2), stream, p);
+                            kRopeThreads, (kNorm ? kPairs * 32 * sizeof(float4) : 0) + kRopeWarps * p.shared, stream, p);
   });
 }
 template <bool kNorm>

@@ -25,6 +25,7 @@ struct RopeSide {
   long long xs[3], ds[3], ys[3];  // element strides (b, s, h)
   long long x_step, d_step, y_step;   // from a turn's heads to the next one's
   int heads, per_unit, turns;     // heads of a unit, in turns of p.slots
+  int parts, units;               // backward: units of a token, and of all tokens
 };
 struct RopeParams {
   RopeSide side[2];               // Q and K
@@ -32,20 +33,22 @@ struct RopeParams {
   const unsigned long long* freq;
   long long pos_str[3];           // element strides (b, s, axis)
   int tokens, N, pairs, axes;
-  int table;                      // cosines and sines of a warp
+  int table, shared;              // cosines and sines of a warp; its bytes of shared memory
   int lanes, slots;               // lanes a row, rows a warp takes at a time
   Div S, by_parts;                // by_parts: units that a token's heads are divided into
   float magnitude, eps, inv_n;
   int inverse, w_type, w_vec;     // w_vec: weights by 16 bytes
 };
 
-// Where a lane's pairs are.  kHalf, kNext: 16-byte pieces, eight pairs a lane (R a multiple of 16 for kHalf);
-// kAny: pairs lane, lane + 32, ... by the channel.
-enum RopeMap : int { kHalf = 0, kNext = 1, kAny = 2, kAnyNext = 3 };
+// Where a lane's channels are.  By 16-byte pieces, 16 channels a lane: kNext, pairs of neighbours; kHalf, halves that are whole
+// pieces: both channels of eight pairs; kApart, other halves: 16 neighbours, whose partners come through shared memory.  By the
+// channel: kAny, kAnyNext: pairs lane, lane + 32, ...
+enum RopeMap : int { kHalf = 0, kNext = 1, kApart = 2, kAny = 3, kAnyNext = 4 };
+constexpr int kSwap = 17 * 32;   // kApart: floats of a warp's exchange: [16][lane], then a zero
 
 template <class T, int kMap, int kPairs>
 struct RopeLane {
-  static constexpr bool kVec = kMap == kHalf || kMap == kNext;
+  static constexpr bool kVec = kMap < kAny, kExchange = kMap == kApart;
   static constexpr int kPieces = kVec ? (int)sizeof(T) : 1;   // 16-byte pieces of a lane's 16 channels
   struct Raw {
     uint4 piece[kVec ? kPieces : 1];
@@ -53,6 +56,7 @@ struct RopeLane {
   };
   int l, ca, cb, last;   // kVec: first channels of the two runs of eight; last: N
   int at_a[kVec ? 1 : kPairs], at_b[kVec ? 1 : kPairs];   // else: the channels of each pair
+  int from[kMap == kApart ? 16 : 1];                      // kApart: where the exchange has the channels' partners
 
   __device__ __forceinline__ RopeLane(const RopeParams& p, int lane) {
     l = kVec ? lane % p.lanes : lane;
@@ -60,6 +64,13 @@ struct RopeLane {
     const bool turned = kMap == kHalf && 8 * l < p.pairs;
     ca = turned ? 8 * l : 16 * l;
     cb = turned ? p.pairs + 8 * l : 16 * l + 8;
+    if constexpr (kMap == kApart) {
+#pragma unroll
+      for (int i = 0; i < 16; ++i) {
+        const int c = 16 * l + i, t = c < p.pairs ? c + p.pairs : c - p.pairs;
+        from[i] = c < 2 * p.pairs ? (t & 15) * 32 + lane - l + (t >> 4) : 16 * 32;
+      }
+    }
     if constexpr (!kVec) {
 #pragma unroll
       for (int i = 0; i < kPairs; ++i) {
@@ -201,10 +212,12 @@ struct RopeWalk {
   }
 };
 
-// Cosine and sine (times the magnitude) of a token's pairs, to `table`; the sine negated for the backward.  kVec: in the
-// order in which lanes read them, [4][lanes] of two pairs; else pair by pair.
-template <bool kVec>
+// Cosine and sine (times the magnitude) of a token's pairs, to `table`; the sine negated for the backward.  By pieces: in the
+// order in which lanes read them, [4][lanes] of two pairs, or for kApart [8][lanes] of two channels, a first half's sine
+// negated and (1, 0) where a channel passes; else pair by pair.
+template <int kMap>
 __device__ __forceinline__ void rope_table(const RopeParams& p, int b, int s, int lane, float2* table) {
+  constexpr bool kVec = kMap < kAny;
   __syncwarp();   // the last token's are no longer read
   for (int i = lane; i < p.pairs; i += 32) {
     const unsigned long long f = __ldg(p.freq + i);
@@ -216,8 +229,19 @@ __device__ __forceinline__ void rope_table(const RopeParams& p, int b, int s, in
     const unsigned long long turns = (unsigned long long)(long long)at * (f & ~3ull);
     float sn, cs;   // of half turns in [-1, 1)
     sincospif((float)(int)(turns >> 32) * 0x1p-31f, &sn, &cs);
-    table[kVec ? ((i % 8 / 2) * p.lanes + i / 8) * 2 + i % 2 : i] = make_float2(cs * p.magnitude, sn * (p.inverse ? -p.magnitude : p.magnitude));
+    cs *= p.magnitude;
+    sn *= p.inverse ? -p.magnitude : p.magnitude;
+    if (kMap == kApart) {
+      const int c = i + p.pairs;
+      table[((i % 16 / 2) * p.lanes + i / 16) * 2 + i % 2] = make_float2(cs, -sn);
+      table[((c % 16 / 2) * p.lanes + c / 16) * 2 + c % 2] = make_float2(cs, sn);
+    } else {
+      table[kVec ? ((i % 8 / 2) * p.lanes + i / 8) * 2 + i % 2 : i] = make_float2(cs, sn);
+    }
   }
+  if (kMap == kApart)
+    for (int c = 2 * p.pairs + lane; c < 16 * p.lanes; c += 32)
+      table[((c % 16 / 2) * p.lanes + c / 16) * 2 + c % 2] = make_float2(1.0f, 0.0f);
   __syncwarp();
 }
 
@@ -236,17 +260,44 @@ __device__ __forceinline__ float2 load_shared(const float2* at) {
   return v;
 }
 
-// Cosines and sines of a lane's pairs 2 k and 2 k + 1 (where they are rotated).
-template <class L>
-__device__ __forceinline__ void two_angles(const RopeParams& p, const L& ln, const float2* table, int k, float2 (&t)[2]) {
-  if (L::kVec) {
-    const float4 two = load_shared(reinterpret_cast<const float4*>(table) + k * p.lanes + ln.l);
-    t[0] = make_float2(two.x, two.y);
-    t[1] = make_float2(two.z, two.w);
-  } else {
+// The rotation of a lane's channels (every lane of the warp takes part).
+template <int kPairs, class L>
+__device__ __forceinline__ void rope_turn(const RopeParams& p, const L& ln, const float2* table, float* swap, int lane,
+                                          float (&a)[kPairs], float (&b)[kPairs]) {
+  if constexpr (L::kExchange) {
+    __syncwarp();   // the last row's are no longer read
 #pragma unroll
-    for (int e = 0; e < 2; ++e)
-      if (ln.pair(2 * k + e) < p.pairs) t[e] = load_shared(table + ln.pair(2 * k + e));
+    for (int i = 0; i < kPairs; ++i) {
+      swap[2 * i * 32 + lane] = a[i];
+      swap[(2 * i + 1) * 32 + lane] = b[i];
+    }
+    __syncwarp();
+  }
+#pragma unroll
+  for (int k = 0; k < kPairs / (L::kExchange ? 1 : 2); ++k) {
+    float2 t[2];   // cosines and sines of two pairs, or of two channels
+    if (L::kVec) {
+      const float4 two = load_shared(reinterpret_cast<const float4*>(table) + k * p.lanes + ln.l);
+      t[0] = make_float2(two.x, two.y);
+      t[1] = make_float2(two.z, two.w);
+    } else {
+#pragma unroll
+      for (int e = 0; e < 2; ++e)
+        if (ln.pair(2 * k + e) < p.pairs) t[e] = load_shared(table + ln.pair(2 * k + e));
+    }
+    if constexpr (L::kExchange) {
+      a[k] = a[k] * t[0].x + swap[ln.from[2 * k]] * t[0].y;
+      b[k] = b[k] * t[1].x + swap[ln.from[2 * k + 1]] * t[1].y;
+    } else {
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        const int i = 2 * k + e;
+        if (ln.pair(i) >= p.pairs) continue;   // (an infinity beside a channel that passes stays out of it)
+        const float a0 = a[i];
+        a[i] = a0 * t[e].x - b[i] * t[e].y;
+        b[i] = b[i] * t[e].x + a0 * t[e].y;
+      }
+    }
   }
 }
 
@@ -258,21 +309,23 @@ __device__ __forceinline__ float rope_row_sum(float v, int lanes) {
 
 // Calls f with the map and the pairs a lane for this problem, as constants.
 template <class F>
-cudaError_t with_rope_map(bool vec, bool next, int N, F&& f) {
-  auto with = [&](auto half, auto nxt, auto pairs) { return next ? f(nxt, pairs) : f(half, pairs); };
+cudaError_t with_rope_map(const RopeParams& p, bool vec, bool next, F&& f) {
   using std::integral_constant;
-  constexpr integral_constant<int, kAny> any{};
-  constexpr integral_constant<int, kAnyNext> any_next{};
-  if (vec) return with(integral_constant<int, kHalf>{}, integral_constant<int, kNext>{}, integral_constant<int, 8>{});
-  if (N <= 128) return with(any, any_next, integral_constant<int, 2>{});
-  if (N <= 256) return with(any, any_next, integral_constant<int, 4>{});
-  return with(any, any_next, integral_constant<int, 8>{});
+  auto with = [&](auto pairs) {
+    return next ? f(integral_constant<int, kAnyNext>{}, pairs) : f(integral_constant<int, kAny>{}, pairs);
+  };
+  constexpr integral_constant<int, 8> eight{};
+  if (vec && next) return f(integral_constant<int, kNext>{}, eight);
+  if (vec) return p.pairs % 8 == 0 ? f(integral_constant<int, kHalf>{}, eight) : f(integral_constant<int, kApart>{}, eight);
+  if (p.N <= 128) return with(integral_constant<int, 2>{});
+  if (p.N <= 256) return with(integral_constant<int, 4>{});
+  return with(eight);
 }
 
-// 16-byte accesses are possible, with eight pairs a lane; lanes a row and rows a warp.
+// Whether 16-byte accesses are possible; lanes a row and rows a warp.
 inline bool rope_shape(RopeParams& p, const RopeArgs& a, bool norm) {
   const int piece = a.type == kF32 ? 4 : 8;
-  bool vec = a.N % 16 == 0 && (a.interleaved || a.R % 16 == 0);
+  bool vec = a.N % 16 == 0;
   for (int i = 0; i < 2; ++i) {
     const RopeArgs::Side& s = a.side[i];
     if (s.H == 0) continue;
@@ -291,7 +344,9 @@ inline bool rope_shape(RopeParams& p, const RopeArgs& a, bool norm) {
       while ((p.lanes & (p.lanes - 1)) != 0) ++p.lanes;
   }
   p.slots = 32 / p.lanes;
-  p.table = vec ? 8 * p.lanes : p.pairs;
+  const bool apart = vec && !a.interleaved && p.pairs % 8 != 0;
+  p.table = apart ? 16 * p.lanes : vec ? 8 * p.lanes : p.pairs;
+  p.shared = (p.table + (apart ? kSwap / 2 : 0)) * (int)sizeof(float2);
   for (RopeSide& s : p.side) {
     s.x_step = s.xs[2] * p.slots;
     s.d_step = s.ds[2] * p.slots;

@@ -17,23 +17,26 @@ namespace sa {
 namespace {
 
 // Rows of a slot whose loads are under way, and CTAs an SM.
-constexpr int rows_ahead(bool vec, int pairs, bool wide) { return vec ? (wide ? 1 : 2) : pairs == 8 ? 1 : 2; }
-constexpr int ctas_an_sm(bool vec, int pairs) { return vec ? 2 : pairs == 2 ? 3 : pairs == 4 ? 2 : 1; }
+constexpr int rows_ahead(int map, int pairs, bool wide) { return map < kAny ? (wide || map == kApart ? 1 : 2) : pairs == 8 ? 1 : 2; }
+constexpr int ctas_an_sm(int map, int pairs, bool wide) {
+  return map < kAny ? (map == kApart && wide ? 1 : 2) : pairs == 2 ? 3 : pairs == 4 ? 2 : 1;
+}
 
 template <class T, int kMap, int kPairs>
-__global__ void __launch_bounds__(kRopeThreads, ctas_an_sm(kMap < kAny, kPairs)) rope_bwd_kernel(const __grid_constant__ RopeParams p) {
+__global__ void __launch_bounds__(kRopeThreads, ctas_an_sm(kMap, kPairs, sizeof(T) == 4)) rope_bwd_kernel(const __grid_constant__ RopeParams p) {
   using L = RopeLane<T, kMap, kPairs>;
-  constexpr int kAhead = rows_ahead(L::kVec, kPairs, sizeof(T) == 4);
+  constexpr int kAhead = rows_ahead(kMap, kPairs, sizeof(T) == 4);
   // the weights by lanes, [kPairs / 2][lanes] of four (registers do not reach for them); then the tables,
-  // [warps][p.table], or at the end the warps' sums, [warps][N]
+  // [warps][p.shared bytes], or at the end the warps' sums, [warps][N]
   extern __shared__ float4 shared[];
-  float2* const tables = reinterpret_cast<float2*>(shared + kPairs / 2 * 32);
+  unsigned char* const tables = reinterpret_cast<unsigned char*>(shared + kPairs / 2 * 32);
   griddep_wait();
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const L ln(p, lane);
   const int slot = L::kVec ? lane / p.lanes : 0;
   const bool mine = slot < p.slots && ln.some();
-  float2* const table = tables + warp * p.table;
+  float2* const table = reinterpret_cast<float2*>(tables + warp * p.shared);
+  float* const swap = reinterpret_cast<float*>(table + p.table);
   float* const sums = reinterpret_cast<float*>(tables);
 
   for (int which = 0; which < 2; ++which) {
@@ -48,9 +51,8 @@ __global__ void __launch_bounds__(kRopeThreads, ctas_an_sm(kMap < kAny, kPairs))
         shared[k * p.lanes + ln.l] = make_float4(w[4 * k], w[4 * k + 1], w[4 * k + 2], w[4 * k + 3]);
     }
     __syncthreads();
-    const int parts = (sd.heads + sd.per_unit - 1) / sd.per_unit, units = p.tokens * parts;
-    for (int unit = blockIdx.x * kRopeWarps + warp; unit < units; unit += gridDim.x * kRopeWarps) {
-      const int token = parts == 1 ? unit : unit / parts, first = (unit - token * parts) * sd.per_unit;
+    for (int unit = blockIdx.x * kRopeWarps + warp; unit < sd.units; unit += gridDim.x * kRopeWarps) {
+      const int token = sd.parts == 1 ? unit : unit / sd.parts, first = (unit - token * sd.parts) * sd.per_unit;
       const int end = min(first + sd.per_unit, sd.heads);
       const int b = div_by(token, p.S), s = token - b * (int)p.S.d;
       RopeWalk<T> x, dy, dx;
@@ -68,7 +70,8 @@ __global__ void __launch_bounds__(kRopeThreads, ctas_an_sm(kMap < kAny, kPairs))
       };
 #pragma unroll
       for (int u = 0; u < kAhead; ++u) load(u);
-      rope_table<L::kVec>(p, b, s, lane, table);
+      if (L::kExchange && lane == 0) swap[16 * 32] = 0.0f;
+      rope_table<kMap>(p, b, s, lane, table);
       for (int base = first; base < end; base += kAhead * p.slots) {
 #pragma unroll
         for (int u = 0; u < kAhead; ++u) {
@@ -87,20 +90,14 @@ __global__ void __launch_bounds__(kRopeThreads, ctas_an_sm(kMap < kAny, kPairs))
 #pragma unroll
           for (int i = 0; i < kPairs; ++i) sum = fmaf(a[i], a[i], fmaf(c[i], c[i], sum));
           const float r = rsqrtf(fmaf(rope_row_sum(sum, p.lanes), p.inv_n, p.eps));
+          rope_turn<kPairs>(p, ln, table, swap, lane, ga, gc);
           float dot = 0.0f;
 #pragma unroll
           for (int k = 0; k < kPairs / 2; ++k) {
             const float4 w = load_shared(shared + k * p.lanes + ln.l);
-            float2 t[2];
-            two_angles(p, ln, table, k, t);
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
               const int i = 2 * k + e;
-              if (ln.pair(i) < p.pairs) {
-                const float g0 = ga[i];
-                ga[i] = g0 * t[e].x - gc[i] * t[e].y;
-                gc[i] = gc[i] * t[e].x + g0 * t[e].y;
-              }
               a[i] *= r;
               c[i] *= r;
               da[i] = fmaf(ga[i], a[i], da[i]);
@@ -152,25 +149,29 @@ __global__ void __launch_bounds__(kRopeThreads, ctas_an_sm(kMap < kAny, kPairs))
   }
 }
 
-// dw of 32 channels of Q (blockIdx.y = 0) or K: 32 threads a channel, each over its share of the CTAs in order.
-__global__ void __launch_bounds__(1024) rope_grad_kernel(const float* q_parts, const float* k_parts, int n_parts, int N,
-                                                         void* dqw, void* dkw, int type) {
-  __shared__ float sum[32][33];
+// dw of 8 channels of Q (blockIdx.y = 0) or K: 64 threads a channel, each over its share of the CTAs in order.
+__global__ void __launch_bounds__(512) rope_grad_kernel(const float* q_parts, const float* k_parts, int n_parts, int N, void* dqw,
+                                                        void* dkw, int type) {
+  __shared__ float sum[64][9];
   griddep_wait();
   const float* const parts = blockIdx.y ? k_parts : q_parts;
   void* const out = blockIdx.y ? dkw : dqw;
   if (parts == nullptr) return;
-  const int c = blockIdx.x * 32 + (threadIdx.x & 31), g = threadIdx.x >> 5;
+  const int c = blockIdx.x * 8 + (threadIdx.x & 7), g = threadIdx.x >> 3;
   float v = 0.0f;
-  if (c < N)
-    for (int i = g; i < n_parts; i += 32) v += parts[(long long)i * N + c];
-  sum[g][threadIdx.x & 31] = v;
+  if (c < N) {
+#pragma unroll 8
+    for (int i = g; i < n_parts; i += 64) v += __ldcs(parts + (long long)i * N + c);
+  }
+  sum[g][threadIdx.x & 7] = v;
   __syncthreads();
-  v = sum[threadIdx.x & 31][g];
+  if (threadIdx.x >= 256) return;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;   // a warp joins a channel
+  v = sum[lane][warp] + sum[lane + 32][warp];
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
-  const int mine = blockIdx.x * 32 + g;
-  if ((threadIdx.x & 31) != 0 || mine >= N) return;
+  const int mine = blockIdx.x * 8 + warp;
+  if (lane != 0 || mine >= N) return;
   if (type == kF32) reinterpret_cast<float*>(out)[mine] = v;
   else if (type == kBF16) reinterpret_cast<__nv_bfloat16*>(out)[mine] = __float2bfloat16(v);
   else reinterpret_cast<__half*>(out)[mine] = __float2half(v);
@@ -178,11 +179,11 @@ __global__ void __launch_bounds__(1024) rope_grad_kernel(const float* q_parts, c
 
 template <class T>
 cudaError_t launch_bwd(const RopeParams& p, int& ctas, bool vec, bool next, cudaStream_t stream) {
-  return with_rope_map(vec, next, p.N, [&](auto map, auto pairs) {
-    const size_t tables = (size_t)kRopeWarps * p.table * sizeof(float2), sums = (size_t)kRopeWarps * p.N * sizeof(float);
-    constexpr int kPairs = decltype(pairs)::value;
-    ctas = std::min(ctas, 152 * ctas_an_sm(decltype(map)::value < kAny, kPairs));
-    return launch_dependent(rope_bwd_kernel<T, decltype(map)::value, kPairs>, dim3((unsigned)ctas), kRopeThreads,
+  return with_rope_map(p, vec, next, [&](auto map, auto pairs) {
+    const size_t tables = (size_t)kRopeWarps * p.shared, sums = (size_t)kRopeWarps * p.N * sizeof(float);
+    constexpr int kMap = decltype(map)::value, kPairs = decltype(pairs)::value;
+    ctas = std::min(ctas, 152 * ctas_an_sm(kMap, kPairs, sizeof(T) == 4));
+    return launch_dependent(rope_bwd_kernel<T, kMap, kPairs>, dim3((unsigned)ctas), kRopeThreads,
                             kPairs / 2 * 32 * sizeof(float4) + (tables > sums ? tables : sums), stream, p);
   });
 }
@@ -207,13 +208,15 @@ cudaError_t launch_qk_norm_rope_bwd(const RopeArgs& a, float* workspace, cudaStr
     s.per_unit = (H + p.slots - 1) / p.slots * p.slots;
     while (s.per_unit > p.slots && (long long)p.tokens * ((H + s.per_unit - 1) / s.per_unit) < 152 * 32)
       s.per_unit = (s.per_unit / 2 + p.slots - 1) / p.slots * p.slots;
+    s.parts = (H + s.per_unit - 1) / std::max(s.per_unit, 1);
+    s.units = p.tokens * s.parts;
     if (H > 0 && a.side[i].dw != nullptr) s.partial = workspace + (size_t)i * ctas * a.N;
   }
   cudaError_t e = a.type == kF32    ? launch_bwd<float>(p, ctas, vec, a.interleaved, stream)
                   : a.type == kBF16 ? launch_bwd<__nv_bfloat16>(p, ctas, vec, a.interleaved, stream)
                                     : launch_bwd<__half>(p, ctas, vec, a.interleaved, stream);
   if (e != cudaSuccess || (p.side[0].partial == nullptr && p.side[1].partial == nullptr)) return e;
-  return launch_dependent(rope_grad_kernel, dim3((unsigned)(a.N + 31) / 32, 2), 1024, 0, stream,
+  return launch_dependent(rope_grad_kernel, dim3((unsigned)(a.N + 7) / 8, 2), 512, 0, stream,
                           static_cast<const float*>(p.side[0].partial), static_cast<const float*>(p.side[1].partial), ctas,
                           a.N, a.side[0].dw, a.side[1].dw, a.w_type);
 }

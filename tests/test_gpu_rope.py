@@ -37,6 +37,10 @@ CASES = [
     (1, 3, 2, 2, 511, 2, True, None, None),
     (1, 2, 70, 3, 16, 16, False, None, None),              # a lane a row, more heads than a pass
     (1, 400, 2, 0, 32, 32, False, None, None),             # no K
+    (2, 3, 7, 2, 80, 34, False, None, None),               # halves that are no whole pieces, five lanes a row
+    (1, 2, 3, 1, 512, 266, False, None, None),             # ... and all lanes one row's
+    (1, 3, 5, 2, 128, 2, False, None, None),
+    (2, 600, 4, 1, 32, 18, False, (6, 6, 6), None),        # ... sixteen rows a warp, many tokens
 ]
 
 
@@ -229,13 +233,13 @@ def test_same_bits_on_any_stream_and_in_graphs(dtype, cuda_dev):
 
 def test_infinities_and_nan_stay_in_their_pair(cuda_dev):
     """The rotation of a pair says nothing about the channels beside it."""
-    freq = sa.rope_frequencies(32, device=cuda_dev)[0]
-    for inter in (False, True):
+    for inter, R in ((False, 32), (True, 32), (False, 36)):
+        freq = sa.rope_frequencies(R, device=cuda_dev)[0]
         x = rows(110, 1, 2, 1, 64, dtype=torch.float32)
         x[0, 0, 0, 2], x[0, 1, 0, 40] = math.inf, math.nan
         y = sa.rope_fwd(x.to(cuda_dev), None, freq, interleaved=inter)[0].cpu()
         clean = torch.ones(64, dtype=torch.bool)
-        clean[[2, 3] if inter else [2, 18]] = False
+        clean[[2, 3] if inter else [2, 2 + R // 2]] = False
         assert torch.isfinite(y[0, 0, 0][clean]).all() and not torch.isfinite(y[0, 0, 0, 2])
         clean = torch.ones(64, dtype=torch.bool)
         clean[40] = False

@@ -67,7 +67,7 @@ def test_sizes():
     size = L.attn_fwd_kv4_workspace_size
     assert size(0, 1, 8, 8, 4, 16) == 0 and size(1, 1, 7, 2, 4, 16) == 0 and size(1, 1, 8, 8, 4, 24) == 0
     # pieces of at most all CTAs of a wave; few for a small cache
-    assert 0 < size(1, 1, 1, 1, 1, 16) < 20000 and size(64, 1, 32, 8, 1 << 12, 64) < 16 << 20
+    assert 0 < size(1, 1, 1, 1, 1, 16) < 200000 and size(64, 1, 32, 8, 1 << 12, 64) < 16 << 20
     with pytest.raises(ValueError):
         sa.kv4_cache(3, 8, 40, device="cpu")
 
