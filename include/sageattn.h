@@ -531,8 +531,7 @@ ATTN_API attn_status layer_norm_bwd(const void* dy, const void* x, const void* w
  *   (a, b) -> magnitude (a cos t - b sin t, b cos t + a sin t),  t = 2 pi freq[i] position / 2^64
  *   q, k    : dtype [B, S, Hq, N] and [B, S, Hk, N], element strides q_str / k_str (batch, sequence, head), channel
  *             stride 1; any alignment of the type, strides of 0 allowed.  Hq or Hk may be 0 (its pointers are not
- *             looked at).  16-byte accesses are used where pointers and strides allow them, N is a multiple of
- *             16 and, in the half layout, rope_dim is one.
+ *             looked at).  16-byte accesses are used where pointers and strides allow them and N is a multiple of 16.
  *   q_out, k_out : the same shapes, strides qo_str / ko_str; each may be its input itself (pointer and strides) and
  *             overlaps no tensor otherwise
  *   pos     : device int32 positions of (batch, token, axis), element strides pos_str (0 where one row serves all), or
@@ -657,9 +656,10 @@ ATTN_API size_t attn_fwd_kv4_workspace_size(int B, int Sq, int Hq, int Hkv, int 
  *   causal  : 0 or 1
  *   workspace : at least attn_fwd_kv4_workspace_size bytes, 16-byte aligned; overwritten; one for each call under way
  * Made for one or a few tokens a request: 16 queries (Sq * Hq / Hkv) share one read of the cache, more read it again.
- * For a long piece of a prompt, kv4_read and attn_fwd_bf16_lse.  Q takes part as two e4m3 terms: a row's values
- * keep 8 bits down to 2^-14 of its largest, smaller ones are off by up to 2^-22 of it.  Products with the codes are exact, P
- * times V's scale is rounded to BF16, sums are FP32 in a fixed order (the same inputs give the same bits), O is rounded once.  Enqueues two kernels on `stream`.
+ * For a long piece of a prompt, kv4_read and attn_fwd_bf16_lse.  Q takes part in FP16 with its row's largest magnitude
+ * scaled into [1, 2) (what is below 2^-14 of it is off by up to 2^-25 of it), products with the codes are exact, P times V's
+ * scale is rounded to BF16, sums are FP32 in a fixed order (the same inputs give the same bits), O is rounded once.
+ * Enqueues two kernels on `stream`.
  */
 ATTN_API attn_status attn_fwd_kv4(const void* q, const void* cache, int num_pages, int page_size,
                                   const int32_t* page_table, int64_t table_str, int max_pages, const int32_t* kv_len,

@@ -15,16 +15,16 @@ namespace {
 
 // Rows of a slot whose loads are under way, and CTAs an SM: loads in flight are what the kernels wait for, and more warps with
 // fewer rows each do better (76112 x 80 heads of 128 BF16: four rows, two CTAs 546 us; two, three 497; two, four 467).
-constexpr int rows_ahead(int map, int pairs, bool wide) { return map < kAny ? (wide ? 1 : 2) : pairs == 2 ? 4 : 2; }
-constexpr int ctas_an_sm(int map, bool wide, bool norm) {
-  return map >= kAny ? 1 : map == kApart ? (wide ? 2 : 3) : wide ? (norm ? 2 : 3) : map == kHalf && norm ? 3 : 4;
+constexpr int rows_ahead(int map, bool wide) { return map < kAny && wide ? 1 : 2; }
+constexpr int ctas_an_sm(int map, int pairs, bool wide, bool norm) {
+  return map >= kAny ? (pairs == 4 ? 3 : 1) : map == kApart ? (wide ? 2 : 3) : wide ? (norm ? 2 : 3) : map == kHalf && norm ? 3 : 4;
 }
 
 template <class T, int kMap, int kPairs, bool kNorm>
-__global__ void __launch_bounds__(kRopeThreads, ctas_an_sm(kMap, sizeof(T) == 4, kNorm))
+__global__ void __launch_bounds__(kRopeThreads, ctas_an_sm(kMap, kPairs, sizeof(T) == 4, kNorm))
     rope_fwd_kernel(const __grid_constant__ RopeParams p) {
   using L = RopeLane<T, kMap, kPairs>;
-  constexpr int kAhead = rows_ahead(kMap, kPairs, sizeof(T) == 4);
+  constexpr int kAhead = rows_ahead(kMap, sizeof(T) == 4);
   // kNorm: the weights of Q and of K by lanes, [2][kPairs / 2][lanes] of four (held in registers they take the warps that hide
   // the loads); then the tables
   extern __shared__ __align__(16) float4 shared[];
@@ -33,7 +33,7 @@ __global__ void __launch_bounds__(kRopeThreads, ctas_an_sm(kMap, sizeof(T) == 4,
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   if constexpr (kNorm) {
     const L ln(p, lane);
-    if (warp < 2 && (!L::kVec || lane < p.lanes)) {
+    if (warp < 2 && lane < p.lanes) {
       float w[2 * kPairs];
       ln.weights(p.side[warp].w, p, w);
 #pragma unroll
@@ -47,7 +47,7 @@ __global__ void __launch_bounds__(kRopeThreads, ctas_an_sm(kMap, sizeof(T) == 4,
   if (token >= p.tokens) return;
   const int b = div_by(token, p.S), s = token - b * (int)p.S.d;
   const L ln(p, lane);
-  const int slot = L::kVec ? lane / p.lanes : 0;
+  const int slot = lane / p.lanes;
   const bool mine = slot < p.slots && ln.some();
   // the unit's share of Q's heads, then of K's, p.slots of them a turn
   const int turns_q = p.side[0].turns, turns = turns_q + p.side[1].turns;

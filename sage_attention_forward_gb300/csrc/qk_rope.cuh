@@ -34,7 +34,8 @@ struct RopeParams {
   long long pos_str[3];           // element strides (b, s, axis)
   int tokens, N, pairs, axes;
   int table, shared;              // cosines and sines of a warp; its bytes of shared memory
-  int lanes, slots;               // lanes a row, rows a warp takes at a time
+  int lanes, slots, per, word;         // lanes a row, rows a warp takes at a time; by the channel:
+                                  // pairs a lane, pairs of neighbours aligned to their size
   Div S, by_parts;                // by_parts: units that a token's heads are divided into
   float magnitude, eps, inv_n;
   int inverse, w_type, w_vec;     // w_vec: weights by 16 bytes
@@ -42,7 +43,7 @@ struct RopeParams {
 
 // Where a lane's channels are.  By 16-byte pieces, 16 channels a lane: kNext, pairs of neighbours; kHalf, halves that are whole
 // pieces: both channels of eight pairs; kApart, other halves: 16 neighbours, whose partners come through shared memory.  By the
-// channel: kAny, kAnyNext: pairs lane, lane + 32, ...
+// channel: kAny, kAnyNext: pairs l, l + lanes, ... of a row's lanes l.
 enum RopeMap : int { kHalf = 0, kNext = 1, kApart = 2, kAny = 3, kAnyNext = 4 };
 constexpr int kSwap = 17 * 32;   // kApart: floats of a warp's exchange: [16][lane], then a zero
 
@@ -52,14 +53,19 @@ struct RopeLane {
   static constexpr int kPieces = kVec ? (int)sizeof(T) : 1;   // 16-byte pieces of a lane's 16 channels
   struct Raw {
     uint4 piece[kVec ? kPieces : 1];
-    T a[kVec ? 1 : kPairs], b[kVec ? 1 : kPairs];
+    uint32_t a[kVec ? 1 : kPairs], b[kVec ? 1 : kPairs];   // bits of the channels; 16-bit neighbours both in a
   };
+  static constexpr bool kShort = sizeof(T) == 2;
+  __device__ __forceinline__ bool neighbours() const { return kMap == kAnyNext && word; }
   int l, ca, cb, last;   // kVec: first channels of the two runs of eight; last: N
+  int step, word;        // else: pairs l, l + step, ...; pairs of neighbours as one access
   int at_a[kVec ? 1 : kPairs], at_b[kVec ? 1 : kPairs];   // else: the channels of each pair
   int from[kMap == kApart ? 16 : 1];                      // kApart: where the exchange has the channels' partners
 
   __device__ __forceinline__ RopeLane(const RopeParams& p, int lane) {
-    l = kVec ? lane % p.lanes : lane;
+    l = lane % p.lanes;
+    step = p.lanes;
+    word = p.word;
     last = p.N;
     const bool turned = kMap == kHalf && 8 * l < p.pairs;
     ca = turned ? 8 * l : 16 * l;
@@ -82,7 +88,7 @@ struct RopeLane {
   }
   // kVec: the lane has channels of a row
   __device__ __forceinline__ bool some() const { return !kVec || 16 * l < last; }
-  __device__ __forceinline__ int pair(int i) const { return kVec ? 8 * l + i : l + 32 * i; }
+  __device__ __forceinline__ int pair(int i) const { return kVec ? 8 * l + i : l + step * i; }
   __device__ __forceinline__ int first(int i) const {
     if constexpr (kVec) return kMap == kHalf ? ca + i : 16 * l + 2 * i;
     else return at_a[i];
@@ -103,8 +109,23 @@ struct RopeLane {
 #pragma unroll
       for (int i = 0; i < kPairs; ++i) {
         const int a = first(i), b = second(i);
-        r.a[i] = a < last ? row[a] : T(0.0f);
-        r.b[i] = b < last ? row[b] : T(0.0f);
+        if (neighbours()) {   // (N is even)
+          r.a[i] = r.b[i] = 0u;
+          if (a >= last) continue;
+          if constexpr (kShort) {
+            r.a[i] = *reinterpret_cast<const uint32_t*>(row + a);
+          } else {
+            const uint2 two = *reinterpret_cast<const uint2*>(row + a);
+            r.a[i] = two.x;
+            r.b[i] = two.y;
+          }
+        } else if constexpr (kShort) {
+          r.a[i] = a < last ? reinterpret_cast<const unsigned short*>(row)[a] : 0u;
+          r.b[i] = b < last ? reinterpret_cast<const unsigned short*>(row)[b] : 0u;
+        } else {
+          r.a[i] = a < last ? reinterpret_cast<const uint32_t*>(row)[a] : 0u;
+          r.b[i] = b < last ? reinterpret_cast<const uint32_t*>(row)[b] : 0u;
+        }
       }
     }
   }
@@ -121,8 +142,16 @@ struct RopeLane {
     } else {
 #pragma unroll
       for (int i = 0; i < kPairs; ++i) {
-        a[i] = (float)r.a[i];
-        b[i] = (float)r.b[i];
+        if constexpr (kShort) {
+          float two[2], other[2];
+          unpack_word(r.a[i], two, T());
+          unpack_word(r.b[i], other, T());
+          a[i] = two[0];
+          b[i] = neighbours() ? two[1] : other[0];
+        } else {
+          a[i] = __uint_as_float(r.a[i]);
+          b[i] = __uint_as_float(r.b[i]);
+        }
       }
     }
   }
@@ -144,8 +173,15 @@ struct RopeLane {
 #pragma unroll
       for (int i = 0; i < kPairs; ++i) {
         const int ia = first(i), ib = second(i);
-        if (ia < last) row[ia] = T(a[i]);
-        if (ib < last) row[ib] = T(b[i]);
+        if (neighbours()) {
+          const float two[2] = {a[i], b[i]};
+          if (ia >= last) continue;
+          if constexpr (kShort) *reinterpret_cast<uint32_t*>(row + ia) = pack_word(two, T());
+          else *reinterpret_cast<float2*>(row + ia) = make_float2(a[i], b[i]);
+        } else {
+          if (ia < last) row[ia] = T(a[i]);
+          if (ib < last) row[ib] = T(b[i]);
+        }
       }
     }
   }
@@ -317,15 +353,13 @@ cudaError_t with_rope_map(const RopeParams& p, bool vec, bool next, F&& f) {
   constexpr integral_constant<int, 8> eight{};
   if (vec && next) return f(integral_constant<int, kNext>{}, eight);
   if (vec) return p.pairs % 8 == 0 ? f(integral_constant<int, kHalf>{}, eight) : f(integral_constant<int, kApart>{}, eight);
-  if (p.N <= 128) return with(integral_constant<int, 2>{});
-  if (p.N <= 256) return with(integral_constant<int, 4>{});
-  return with(eight);
+  return p.per == 4 ? with(integral_constant<int, 4>{}) : with(eight);
 }
 
-// Whether 16-byte accesses are possible; lanes a row and rows a warp.
+// Whether rows go by 16 bytes (kApart while its shared memory stays below 48 KB); lanes a row and rows a warp.
 inline bool rope_shape(RopeParams& p, const RopeArgs& a, bool norm) {
   const int piece = a.type == kF32 ? 4 : 8;
-  bool vec = a.N % 16 == 0;
+  bool vec = a.N % 16 == 0 && (a.interleaved || a.R % 16 == 0 || a.N <= 256), word = a.N % 2 == 0;
   for (int i = 0; i < 2; ++i) {
     const RopeArgs::Side& s = a.side[i];
     if (s.H == 0) continue;
@@ -335,14 +369,20 @@ inline bool rope_shape(RopeParams& p, const RopeArgs& a, bool norm) {
       if (ptr[k] == nullptr) continue;
       vec = vec && (reinterpret_cast<uintptr_t>(ptr[k]) & 15u) == 0 && (a.B == 1 || str[k][0] % piece == 0) &&
             (a.S == 1 || str[k][1] % piece == 0) && (s.H == 1 || str[k][2] % piece == 0);
+      word = word && reinterpret_cast<uintptr_t>(ptr[k]) % (a.type == kF32 ? 8 : 4) == 0 && (a.B == 1 || str[k][0] % 2 == 0) &&
+             (a.S == 1 || str[k][1] % 2 == 0) && (s.H == 1 || str[k][2] % 2 == 0);
     }
   }
-  p.lanes = 32;
-  if (vec) {
-    p.lanes = a.N / 16;
-    if (norm)   // the row's sums go over a power of two of lanes
-      while ((p.lanes & (p.lanes - 1)) != 0) ++p.lanes;
-  }
+  p.word = word;
+  const int pairs = (a.N + 1) / 2;
+  auto lanes = [&](int n) {
+    while (norm && (n & (n - 1)) != 0) ++n;   // a norm's sums go over a power of two of lanes
+    return n;
+  };
+  // by the channel: four pairs a lane, or eight where that leaves fewer lanes idle (N = 130: a row takes 17 of 32, or 9)
+  const int four = lanes((pairs + 3) / 4), eight = lanes((pairs + 7) / 8);
+  p.per = !vec && four <= 32 && 5 * (32 / four) * 2 >= 4 * (32 / eight) ? 4 : 8;
+  p.lanes = vec ? lanes(a.N / 16) : p.per == 4 ? four : eight;
   p.slots = 32 / p.lanes;
   const bool apart = vec && !a.interleaved && p.pairs % 8 != 0;
   p.table = apart ? 16 * p.lanes : vec ? 8 * p.lanes : p.pairs;

@@ -19,7 +19,7 @@ namespace {
 // Rows of a slot whose loads are under way, and CTAs an SM.
 constexpr int rows_ahead(int map, int pairs, bool wide) { return map < kAny ? (wide || map == kApart ? 1 : 2) : pairs == 8 ? 1 : 2; }
 constexpr int ctas_an_sm(int map, int pairs, bool wide) {
-  return map < kAny ? (map == kApart && wide ? 1 : 2) : pairs == 2 ? 3 : pairs == 4 ? 2 : 1;
+  return map < kAny ? (map == kApart && wide ? 1 : 2) : pairs == 4 ? 2 : 1;
 }
 
 template <class T, int kMap, int kPairs>
@@ -33,7 +33,7 @@ __global__ void __launch_bounds__(kRopeThreads, ctas_an_sm(kMap, kPairs, sizeof(
   griddep_wait();
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const L ln(p, lane);
-  const int slot = L::kVec ? lane / p.lanes : 0;
+  const int slot = lane / p.lanes;
   const bool mine = slot < p.slots && ln.some();
   float2* const table = reinterpret_cast<float2*>(tables + warp * p.shared);
   float* const swap = reinterpret_cast<float*>(table + p.table);

@@ -76,9 +76,10 @@ def attention(q, k, v, step, seen, scale):
     """One request: q [Sq, Hq, 128]; k, v and step as held() gives them, [n, Hkv, 128]; seen [Sq, n].  -> O, lse,
     their bounds.
 
-      scores   products with codes + 8 (at most 15, and 8 taken off) over 128 channels in FP32, sums of 32 channels rounded or
-               cut within 2^-22 of their parts, a few of them: 2^-21 23 sum |q step|; Q's two e4m3 terms, the second in
-               steps of 2^-9 / 32 where the row's largest is at least 2^7: off by 2^-15 / 2^7 of it: 2^-22 max|q| sum |k|
+      scores   products with 256 + code for half of the channels and 16 + code for the others (at most 271; what the constants
+               and the codes' bias of 8 add is taken off again) over 128 channels in FP32, sums of 16 channels rounded or
+               cut within 2^-22 of their parts, a few of them: 2^-21 280 sum |q step|; Q's FP16, of a row whose largest
+               magnitude is at least 1, off by at most 2^-25: 2^-24 max|q| sum |k|
       P        scale and rounding to BF16, whose 8 significant bits are off by up to 2^-8 of the value (half of the 2^-7
                between 1 and the next): 2^-8 + 2^-22; its exponential 2^-21; sums 2^-18
     """
@@ -91,8 +92,8 @@ def attention(q, k, v, step, seen, scale):
     lse = torch.logsumexp(s, -1)
     p = torch.exp(s - torch.where(torch.isinf(lse), 0.0, lse)[..., None])
     o = torch.einsum("hsn,nhd->shd", p, v)
-    off = scale * (23 * 2.0 ** -21 * torch.einsum("shd,nhd->hsn", q.abs(), step.abs())
-                   + 2.0 ** -22 * q.abs().amax(-1).T[..., None] * k.abs().sum(-1).T[:, None])
+    off = scale * (280 * 2.0 ** -21 * torch.einsum("shd,nhd->hsn", q.abs(), step.abs())
+                   + 2.0 ** -24 * q.abs().amax(-1).T[..., None] * k.abs().sum(-1).T[:, None])
     off = off + s.abs().nan_to_num(posinf=0.0) * 2.0 ** -21
     off = off.masked_fill(hidden, 0.0).amax(-1) if s.shape[-1] else torch.zeros_like(lse)
     size = torch.einsum("hsn,nhd->shd", p, v.abs())
