@@ -6,11 +6,13 @@
 // columns, so that each code is unpacked once for all of them.  Codes become operands without a conversion: four bits put into
 // the mantissa of a constant are the value constant + code.
 //   S^T = sum_g scale_K[key, g] (codes_g q_g)        FP16, two products for each 32 channels, scaled in FP32
-//   O^T[group g] = sum_j codes (p_j scale_V[j, g])   BF16; P is scaled for each group in FP32, then rounded once
+//   O^T[group g] = sum_j codes (p_j scale_V[j, g])   FP16; P is scaled for each group in FP32, then rounded once
 // K's codes are 256 + c and 16 + c (one shift and one masked insert for two values); what the constants and the codes' bias add,
-// 264 q and 24 q summed over the channels, is taken off, formed by a product of the same operands.  V's are 128 + c, from
-// which 136 is subtracted, exactly: sums over many keys may be small beside their parts.  Q becomes FP16 with its row's
-// largest magnitude in [1, 2): its own 8 bits stay (what is below 2^-14 of that magnitude is off by up to 2^-25 of it).
+// 264 q and 24 q summed over the channels, is taken off, formed by a product of the same operands.  V's are 1024 + c and 64 + c
+// where they stand, from which 1032 and 72 are subtracted, exactly: sums over many keys may be small beside their parts.
+// Q becomes FP16 with its row's largest magnitude in [1, 2): its own 8 bits stay (what is below 2^-14 of that magnitude is off
+// by up to 2^-25 of it).  P scale_V becomes FP16 with the largest scale that the warp has met in [2^6, 2^7): a power of two
+// that is raised, and O with it, as a row's reference maximum is.
 // (e4m3 operands would need only masks, but mma.sync has no e4m3 on this machine: it came to 19 instructions a product.)
 //
 // Work.  The records of all requests and heads are one line of work, cut into items of equal length, found from the lengths on
@@ -29,7 +31,7 @@ namespace sa {
 namespace {
 
 constexpr int kHeld = 6;            // records of a warp's ring
-constexpr int kLeast = 4;           // records of an item, at least
+constexpr int kLeast = 2;           // records of an item, at least
 constexpr int kStart = 4;           // what a segment's start and end cost beside its records, in records
 constexpr int kCtas = 152;
 constexpr float kSlack = 8.0f;      // a row's reference maximum is raised when one passes it by more (log2 units)
@@ -75,28 +77,34 @@ __device__ __forceinline__ void mma_f16(float (&d)[4], uint32_t a0, uint32_t a1,
       : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
       : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
-__device__ __forceinline__ void mma_bf16(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
-                                         uint32_t b1) {
-  asm volatile(
-      "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
-      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
-      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
-}
 // An 8 x 8 matrix of 16-bit values, a row to four lanes, transposed.
 __device__ __forceinline__ uint32_t transpose8(uint32_t x) {
   uint32_t y;
   asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
   return y;
 }
-// V: four codes of each of two tokens, 4 bits each in halves of x, as BF16 pairs of code - 8.
-// bias: BF16 128 twice, in a register (an instruction takes one constant).
-__device__ __forceinline__ void v_pairs(uint32_t x, uint32_t bias, uint32_t (&a)[4]) {
+// V: four codes of each of two tokens, 4 bits each in halves of x, as FP16 pairs of code - 8.  low, high: FP16 1024 and 64 twice, in
+// registers (an instruction takes one constant).
+__device__ __forceinline__ void v_pairs(uint32_t x, uint32_t low, uint32_t high, uint32_t (&a)[4]) {
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    uint32_t y;
-    asm("lop3.b32 %0, %1, 0x000f000f, %2, 0xEA;" : "=r"(y) : "r"(x >> (4 * i)), "r"(bias));   // (x & mask) | bias
-    asm("add.rn.bf16x2 %0, %1, %2;" : "=r"(a[i]) : "r"(y), "r"(0xc308c308u));                 // y - 136
+  for (int i = 0; i < 2; ++i) {
+    const uint32_t y = i == 0 ? x : x >> 8;
+    asm("lop3.b32 %0, %1, 0x000f000f, %2, 0xEA;" : "=r"(a[2 * i]) : "r"(y), "r"(low));        // (y & mask) | 1024
+    asm("lop3.b32 %0, %1, 0x00f000f0, %2, 0xEA;" : "=r"(a[2 * i + 1]) : "r"(y), "r"(high));
+    asm("add.rn.f16x2 %0, %0, %1;" : "+r"(a[2 * i]) : "r"(0xe408e408u));                      // - 1032
+    asm("add.rn.f16x2 %0, %0, %1;" : "+r"(a[2 * i + 1]) : "r"(0xd480d480u));                  // - 72
   }
+}
+// The larger magnitude of each half (its sign is of no use).
+__device__ __forceinline__ uint32_t larger(uint32_t a, uint32_t b) {
+  uint32_t d;
+  asm("max.xorsign.abs.bf16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
+  return d;
+}
+__device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
+  uint32_t d;
+  asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(d) : "f"(hi), "f"(lo));
+  return d;
 }
 // K: eight codes as FP16 pairs (i, i + 4): 256 + c for i = 0 and 2, 16 + c for i = 1 and 3.  wide, near: FP16 256 and 16 twice.
 __device__ __forceinline__ void k_pairs(uint32_t w, uint32_t wide, uint32_t near, uint32_t (&a)[4]) {
@@ -305,8 +313,12 @@ __global__ void __launch_bounds__(32 * warps(kRows), 1) kv4_attn_kernel(const __
         l[n][c] = 0.0f;
       }
 
-    uint32_t bias, wide, near;   // (registers: an instruction takes one constant)
-    asm volatile("mov.b32 %0, 0x43004300;\n\tmov.b32 %1, 0x5c005c00;\n\tmov.b32 %2, 0x4c004c00;" : "=r"(bias), "=r"(wide), "=r"(near));
+    uint32_t low, high, wide, near;
+    asm volatile("mov.b32 %0, 0x64006400;\n\tmov.b32 %1, 0x54005400;" : "=r"(low), "=r"(high));
+    asm volatile("mov.b32 %0, 0x5c005c00;\n\tmov.b32 %1, 0x4c004c00;" : "=r"(wide), "=r"(near));
+    // V's scales met so far are below 2^7 / down, bits of which, as BF16's, are in `most_v`
+    float down = 1.0f;
+    uint32_t most_v = 0;
     int slot = 0;
 #pragma unroll 1
     for (int tile = first; tile < last; tile += kPair) {
@@ -319,7 +331,7 @@ __global__ void __launch_bounds__(32 * warps(kRows), 1) kv4_attn_kernel(const __
 
       // scores of keys r and r + 8 (h) of each record
       float sc[kCols][kEach][2 * kPair] = {};
-      float vs[2 * kPair][4];
+      uint32_t vs[2 * kPair][2];   // BF16 scales of V's groups (0, 1) and (2, 3)
 #pragma unroll
       for (int j = 0; j < kPair; ++j) {
         const unsigned char* const rec = recs + j * kKvRecord;
@@ -333,10 +345,10 @@ __global__ void __launch_bounds__(32 * warps(kRows), 1) kv4_attn_kernel(const __
         scales_of(s0.y, ks[0][2], ks[0][3]);
         scales_of(s1.x, ks[1][0], ks[1][1]);
         scales_of(s1.y, ks[1][2], ks[1][3]);
-        scales_of(s0.z, vs[2 * j][0], vs[2 * j][1]);
-        scales_of(s0.w, vs[2 * j][2], vs[2 * j][3]);
-        scales_of(s1.z, vs[2 * j + 1][0], vs[2 * j + 1][1]);
-        scales_of(s1.w, vs[2 * j + 1][2], vs[2 * j + 1][3]);
+        vs[2 * j][0] = s0.z;
+        vs[2 * j][1] = s0.w;
+        vs[2 * j + 1][0] = s1.z;
+        vs[2 * j + 1][1] = s1.w;
 #pragma unroll
         for (int g = 0; g < 4; ++g) {
           uint32_t a[4], c[4];
@@ -374,9 +386,7 @@ __global__ void __launch_bounds__(32 * warps(kRows), 1) kv4_attn_kernel(const __
             for (int e = 0; e < kEach; ++e)
               if (none || key >= limit[n][e]) sc[n][e][i] = -INFINITY;
           // what a token that is not there holds as scales may be anything
-          if (none || key >= len)
-#pragma unroll
-            for (int g = 0; g < 4; ++g) vs[i][g] = 0.0f;
+          if (none || key >= len) vs[i][0] = vs[i][1] = 0u;
         }
       }
       bool raise = false;
@@ -390,7 +400,18 @@ __global__ void __launch_bounds__(32 * warps(kRows), 1) kv4_attn_kernel(const __
           for (int i = 2; i < 2 * kPair; i += 2) most[n][e] = fmax3(most[n][e], sc[n][e][i], sc[n][e][i + 1]);
           raise = raise || most[n][e] > m[n][e] + kSlack;
         }
+      uint32_t scale = larger(vs[0][0], vs[0][1]);
+#pragma unroll
+      for (int i = 1; i < 2 * kPair; ++i) scale = larger(scale, larger(vs[i][0], vs[i][1]));
+      scale = larger(scale, scale >> 16) & 0x7fffu;
+      raise = raise || scale > most_v;
       if (__any_sync(0xffffffffu, raise)) {
+        const uint32_t largest = max(most_v, __reduce_max_sync(0xffffffffu, scale));
+        // 2^(6 - e) for scales below 2^(e + 1); BF16's exponent field is bits 7 to 14
+        const int field = max((int)(largest >> 7), 33);   // (down at most 2^100: P times it stays finite)
+        const float next_down = __uint_as_float((uint32_t)(260 - field) << 23), change = next_down / down;
+        most_v = (uint32_t)field << 7 | 0x7fu;
+        down = next_down;
 #pragma unroll
         for (int n = 0; n < kCols; ++n)
 #pragma unroll
@@ -407,7 +428,7 @@ __global__ void __launch_bounds__(32 * warps(kRows), 1) kv4_attn_kernel(const __
               for (int u = 0; u < 2; ++u)
 #pragma unroll
                 for (int i = 0; i < 4; ++i)
-                  if (kEach == 1 || (i & 1) == e) acc[g][u][n][i] *= shrink;
+                  if (kEach == 1 || (i & 1) == e) acc[g][u][n][i] *= shrink * change;
           }
       }
 #pragma unroll
@@ -418,31 +439,37 @@ __global__ void __launch_bounds__(32 * warps(kRows), 1) kv4_attn_kernel(const __
           for (int i = 0; i < 2 * kPair; ++i) {
             sc[n][e][i] = ex2_approx(sc[n][e][i] - m[n][e]);
             l[n][e] += sc[n][e][i];
+            sc[n][e][i] *= down;
           }
 #pragma unroll
       for (int j = 0; j < kPair; ++j) {
         const unsigned char* const rec = recs + j * kKvRecord;
         const uint4 v0 = *reinterpret_cast<const uint4*>(rec + kKvV + lane * 16);
         const uint4 v1 = *reinterpret_cast<const uint4*>(rec + kKvV + 512 + lane * 16);
+        float v[2][4];
+        scales_of(vs[2 * j][0], v[0][0], v[0][1]);
+        scales_of(vs[2 * j][1], v[0][2], v[0][3]);
+        scales_of(vs[2 * j + 1][0], v[1][0], v[1][1]);
+        scales_of(vs[2 * j + 1][1], v[1][2], v[1][3]);
         uint32_t p0[kCols], p1[kCols];   // B operands: keys 0 to 7 and 8 to 15
 #pragma unroll
         for (int g = 0; g < 4; ++g) {
           const uint32_t a0 = g < 2 ? v0.x : v0.y, c0 = g < 2 ? v0.z : v0.w, a1 = g < 2 ? v1.x : v1.y, c1 = g < 2 ? v1.z : v1.w;
           uint32_t x[4], y[4];
-          v_pairs(__byte_perm(a0, c0, g & 1 ? 0x7632 : 0x5410), bias, x);
-          v_pairs(__byte_perm(a1, c1, g & 1 ? 0x7632 : 0x5410), bias, y);
+          v_pairs(__byte_perm(a0, c0, g & 1 ? 0x7632 : 0x5410), low, high, x);
+          v_pairs(__byte_perm(a1, c1, g & 1 ? 0x7632 : 0x5410), low, high, y);
           if (kEach == 2 || g % 2 == 0) {
 #pragma unroll
             for (int n = 0; n < kCols; ++n) {
               const int g2 = kEach == 1 ? g + 1 : g, i = 2 * j;
-              p0[n] = transpose8(pack_bf16x2(sc[n][0][i] * vs[i][g], sc[n][kEach - 1][i] * vs[i][g2]));
-              p1[n] = transpose8(pack_bf16x2(sc[n][0][i + 1] * vs[i + 1][g], sc[n][kEach - 1][i + 1] * vs[i + 1][g2]));
+              p0[n] = transpose8(pack_f16x2(sc[n][0][i] * v[0][g], sc[n][kEach - 1][i] * v[0][g2]));
+              p1[n] = transpose8(pack_f16x2(sc[n][0][i + 1] * v[1][g], sc[n][kEach - 1][i + 1] * v[1][g2]));
             }
           }
 #pragma unroll
           for (int n = 0; n < kCols; ++n) {
-            mma_bf16(acc[g][0][n], x[0], x[1], y[0], y[1], p0[n], p1[n]);
-            mma_bf16(acc[g][1][n], x[2], x[3], y[2], y[3], p0[n], p1[n]);
+            mma_f16(acc[g][0][n], x[0], x[1], y[0], y[1], p0[n], p1[n]);
+            mma_f16(acc[g][1][n], x[2], x[3], y[2], y[3], p0[n], p1[n]);
           }
         }
       }
@@ -458,6 +485,7 @@ __global__ void __launch_bounds__(32 * warps(kRows), 1) kv4_attn_kernel(const __
       p.head[(long long)b * p.segments + seg] = make_int2(item, (int)(end - item) + 1);
     }
     more = begin();
+    const float up = 1.0f / down;
 #pragma unroll
     for (int n = 0; n < kCols; ++n)
 #pragma unroll
@@ -470,7 +498,7 @@ __global__ void __launch_bounds__(32 * warps(kRows), 1) kv4_attn_kernel(const __
 #pragma unroll
         for (int g = 0; g < 4; ++g) {
           const int c = kEach == 1 ? g & 1 : e;
-          v[g] = make_float4(acc[g][0][n][c], acc[g][0][n][2 + c], acc[g][1][n][c], acc[g][1][n][2 + c]);
+          v[g] = make_float4(acc[g][0][n][c] * up, acc[g][0][n][2 + c] * up, acc[g][1][n][c] * up, acc[g][1][n][2 + c] * up);
         }
         if (!complete) {
           const long long piece = (2ll * item + starts) * kRows + in_tile;
@@ -608,7 +636,7 @@ cudaError_t launch_attn_kv4(const Kv4Args& a, void* workspace, cudaStream_t stre
   p.row_tiles = g.row_tiles;
   p.segments = g.row_tiles * a.Hkv;
   const long long capacity = (long long)a.max_pages * a.page_size;
-  p.capacity = capacity < (1ll << 30) ? (int)capacity : 1 << 30;
+  p.capacity = a.num_pages > 0 ? (int)capacity : 0;   // (at most 2^30)
   p.G = make_div(a.Hq / a.Hkv);
   p.by_row_tiles = make_div(g.row_tiles);
   p.causal = a.causal;

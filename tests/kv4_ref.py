@@ -68,22 +68,24 @@ def steps(x):
 
 
 def held(k, v):
-    """What attention takes of K and V: the values that the codes stand for, and K's scales by channel."""
-    return values(k), values(v), steps(k)
+    """What attention takes of K and V: the values that the codes stand for, and the scales by channel."""
+    return values(k), values(v), steps(k), steps(v)
 
 
-def attention(q, k, v, step, seen, scale):
-    """One request: q [Sq, Hq, 128]; k, v and step as held() gives them, [n, Hkv, 128]; seen [Sq, n].  -> O, lse,
+def attention(q, k, v, step, v_step, seen, scale):
+    """One request: q [Sq, Hq, 128]; k, v, step and v_step as held() gives them, [n, Hkv, 128]; seen [Sq, n].  -> O, lse,
     their bounds.
 
       scores   products with 256 + code for half of the channels and 16 + code for the others (at most 271; what the constants
                and the codes' bias of 8 add is taken off again) over 128 channels in FP32, sums of 16 channels rounded or
                cut within 2^-22 of their parts, a few of them: 2^-21 280 sum |q step|; Q's FP16, of a row whose largest
                magnitude is at least 1, off by at most 2^-25: 2^-24 max|q| sum |k|
-      P        scale and rounding to BF16, whose 8 significant bits are off by up to 2^-8 of the value (half of the 2^-7
-               between 1 and the next): 2^-8 + 2^-22; its exponential 2^-21; sums 2^-18
+      P        scale and rounding to FP16: half a step, 2^-11 of the value, + 2^-22; below 2^-14 (the largest scale being at
+               least 2^6 there, for a probability of 1) up to 2^-25 a key, of a code of at most 8: n 2^-28 max(step_v);
+               its exponential 2^-21; sums 2^-18
     """
     G = q.shape[1] // k.shape[1]
+    v_step = float(v_step.abs().max()) if v_step.numel() else 0.0
     q = q.double()
     k, v, step = (t.repeat_interleave(G, 1) for t in (k, v, step))
     s = torch.einsum("shd,nhd->hsn", q, k) * scale
@@ -97,7 +99,8 @@ def attention(q, k, v, step, seen, scale):
     off = off + s.abs().nan_to_num(posinf=0.0) * 2.0 ** -21
     off = off.masked_fill(hidden, 0.0).amax(-1) if s.shape[-1] else torch.zeros_like(lse)
     size = torch.einsum("hsn,nhd->shd", p, v.abs())
-    bound = size * (2.0 ** -8 + 2.0 ** -18 + 2 * off.T[..., None])
+    bound = size * (2.0 ** -11 + 2.0 ** -18 + 2 * off.T[..., None])
+    bound = bound + v.shape[0] * 2.0 ** -28 * v_step
     return o, lse, bound, off + 2.0 ** -17 + lse.abs().nan_to_num(posinf=0.0) * 2.0 ** -22
 
 

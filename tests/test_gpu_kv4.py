@@ -157,6 +157,21 @@ def test_growing_and_falling_scores(cuda_dev):
         verify(got, q, (n,), ref.held(k, v), True)
 
 
+@pytest.mark.parametrize("sizes", [(0.0, 0.0), (1e-28, 1e-20), (1e-20, 1e20), (1e20, 1e-20), (1e30, 1e30)])
+def test_sizes_of_values(sizes, cuda_dev):
+    """Values that grow and fall along the context, tiny, huge and zero ones."""
+    n, lens = 300, (300, 77)
+    k, v = rows(45, 2, n, 2, 128), rows(46, 2, n, 2, 128, dtype=torch.float64)
+    step = torch.linspace(0, 1, n, dtype=torch.float64)[None, :, None, None]
+    v = (v * (sizes[0] ** (1 - step) * sizes[1] ** step if sizes[0] else 0 * step)).to(torch.bfloat16)
+    table, cache = pages(47, 2, 19).to(cuda_dev), sa.kv4_cache(41, 2, 16)
+    sa.kv4_write(k.to(cuda_dev), v.to(cuda_dev), cache, table, ints(0, 0).to(cuda_dev))
+    for Hq in (2, 12, 20):   # each form: 4, 8 and 16 queries
+        q = rows(48 + Hq, 2, 1, Hq, 128).to(cuda_dev)
+        got = sa.attn_fwd_kv4(q, cache, table, ints(*lens).to(cuda_dev))
+        verify(got, q, lens, ref.held(k, v), True)
+
+
 def test_pages_that_are_none(cuda_dev):
     """Their keys are not seen: holes anywhere, a request of nothing but holes."""
     lens = (200, 64, 90)
