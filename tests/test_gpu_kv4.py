@@ -232,6 +232,40 @@ def test_strides_streams_and_graphs(cuda_dev):
         k.mul_(-1.5)
 
 
+def test_thousands_of_requests(cuda_dev):
+    """More requests than a warp looks at together, many without a key; some of them checked."""
+    g = torch.Generator().manual_seed(75)
+    lens = tuple(torch.randint(-20, 60, (3000,), generator=g).clamp(min=0).tolist())
+    B, H, size = len(lens), 1, 16
+    k, v = rows(76, B, 60, H, 128), rows(77, B, 60, H, 128)
+    table = pages(78, B, 4).to(cuda_dev)
+    cache, n = sa.kv4_cache(B * 4 + 3, H, size, cuda_dev), ints(*lens).to(cuda_dev)
+    sa.kv4_write(k.to(cuda_dev), v.to(cuda_dev), cache, table, torch.zeros_like(n), n)
+    q = rows(79, B, 1, 2, 128).to(cuda_dev)
+    o, lse = sa.attn_fwd_kv4(q, cache, table, n)
+    some = list(range(0, B, 43)) + [B - 1]
+    verify((o[some], lse[some]), q[some], [lens[b] for b in some], [t[some] for t in ref.held(k, v)], True)
+    empty = (n == 0).nonzero()[:, 0]
+    assert not o[empty].any() and (lse[empty] == -math.inf).all()
+
+
+def test_two_calls_at_once(cuda_dev):
+    """On two streams, each with its own workspace, again and again: the bits of one call alone."""
+    problems = []
+    for seed, lens, H in ((110, (2000, 7, 650), 2), (120, (333, 4000), 1)):
+        cache, table, *_ = filled(seed, lens, H, 32, cuda_dev)
+        q, n = rows(seed + 9, len(lens), 2, 4, 128).to(cuda_dev), ints(*lens).to(cuda_dev)
+        problems.append((q, cache, table, n))
+    want = [sa.attn_fwd_kv4(*p) for p in problems]
+    streams = [torch.cuda.Stream() for _ in problems]
+    torch.cuda.synchronize()
+    for _ in range(20):
+        got = [sa.attn_fwd_kv4(*p, stream=s) for p, s in zip(problems, streams)]
+        torch.cuda.synchronize()
+        for a, b in zip(got, want):
+            assert torch.equal(a[0], b[0]) and torch.equal(a[1], b[1])
+
+
 def test_many_rounds_give_the_same_bits(cuda_dev):
     lens = (3000, 5, 800)
     cache, table, *_ = filled(80, lens, 2, 64, cuda_dev)

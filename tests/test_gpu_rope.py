@@ -231,6 +231,20 @@ def test_same_bits_on_any_stream_and_in_graphs(dtype, cuda_dev):
         assert all(torch.equal(a, b) for a, b in zip(want + fwd, out))
 
 
+def test_two_calls_at_once(cuda_dev):
+    """On two streams, each with its own workspace: the bits of one call alone."""
+    freq = sa.rope_frequencies(64, device=cuda_dev)[0]
+    w = (1 + rows(105, 64, dtype=torch.float32, gain=0.2)).to(cuda_dev)
+    tensors = [[rows(106 + 4 * j + i, 2, 900, 6, 64, dtype=torch.bfloat16).to(cuda_dev) for i in range(4)] for j in range(2)]
+    want = [sa.qk_norm_rope_bwd(*t, w, w, freq) for t in tensors]
+    streams = [torch.cuda.Stream() for _ in tensors]
+    torch.cuda.synchronize()
+    for _ in range(20):
+        got = [sa.qk_norm_rope_bwd(*t, w, w, freq, stream=s) for t, s in zip(tensors, streams)]
+        torch.cuda.synchronize()
+        assert all(torch.equal(x, y) for a, b in zip(got, want) for x, y in zip(a, b))
+
+
 def test_infinities_and_nan_stay_in_their_pair(cuda_dev):
     """The rotation of a pair says nothing about the channels beside it."""
     for inter, R in ((False, 32), (True, 32), (False, 36)):
