@@ -27,6 +27,7 @@ from __future__ import annotations
 
 import contextlib
 import ctypes
+import functools
 import math
 import os
 from array import array
@@ -793,7 +794,7 @@ def rope_frequencies(rope_dim: int, theta: float = 10000.0, axes=None, scaling: 
 
 # The calls below are made for every layer of every token that is served: their checks are straight lines.
 _current_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
-_empty = torch.empty
+_empty, _empty_like, _contiguous = torch.empty, torch.empty_like, torch.contiguous_format
 
 
 def _rope_rows(q, k):
@@ -850,7 +851,7 @@ def _rope_freq(freq, dev):
 def _rope_made(name, x, out, dev):
     """The output for rows x, made where it is not given."""
     if out is None:
-        return _empty(x.shape, dtype=x.dtype, device=dev)
+        return _empty_like(x, memory_format=_contiguous)
     _expect(name, out, x.shape, x.dtype, dev)
     return out
 
@@ -1020,10 +1021,10 @@ def qk_norm_rope_bwd(dq_out: torch.Tensor, dk_out: torch.Tensor | None, q: torch
         Hk = step = 0
     dqw = _rope_grad("dq_weight", q_weight, dq_weight, w_type, dev)
     dkw = _rope_grad("dk_weight", k_weight, dk_weight, w_type, dev)
-    L, size, scratch = lib(), 0, None
+    size, scratch = 0, None
     if dqw is not None or dkw is not None:
         if workspace is None:
-            size = L.qk_norm_rope_bwd_workspace_size(B, S, Hq, Hk, N)
+            size = lib().qk_norm_rope_bwd_workspace_size(B, S, Hq, Hk, N)
             workspace = _empty(size, dtype=torch.uint8, device=dev)
         else:
             size = _scratch("workspace", workspace, dev)
@@ -1032,10 +1033,10 @@ def qk_norm_rope_bwd(dq_out: torch.Tensor, dk_out: torch.Tensor | None, q: torch
     held = array("q", strides + at_strides)
     p = held.buffer_info()[0]
     d, o = p + 32 + step, p + 64 + 2 * step
-    status = L.qk_norm_rope_bwd(dq_out.data_ptr(), _ptr(dk_out), q.data_ptr(), _ptr(k), qw, kw, dq.data_ptr(), _ptr(dk),
-                                _ptr(dqw), _ptr(dkw), B, S, Hq, Hk, N, d, d + step, p, p + step, o, o + step, eps, at,
-                                o + 32 + step, axes, f, rope_dim, interleaved, magnitude, code, _DTYPES[w_type], scratch, size,
-                                _current_stream(dev))
+    status = lib().qk_norm_rope_bwd(dq_out.data_ptr(), _ptr(dk_out), q.data_ptr(), _ptr(k), qw, kw, dq.data_ptr(), _ptr(dk),
+                                    _ptr(dqw), _ptr(dkw), B, S, Hq, Hk, N, d, d + step, p, p + step, o, o + step, eps, at,
+                                    o + 32 + step, axes, f, rope_dim, interleaved, magnitude, code, _DTYPES[w_type], scratch, size,
+                                    _current_stream(dev))
     if status != 0:
         _check(status)
     return dq, dk, dqw, dkw
@@ -1157,6 +1158,11 @@ def attn_fwd_kv4_workspace(B: int, Sq: int, Hq: int, cache: torch.Tensor, page_t
     return torch.empty(lib().attn_fwd_kv4_workspace_size(B, Sq, Hq, heads, most, page_size), dtype=torch.uint8, device=dev)
 
 
+@functools.lru_cache(maxsize=256)
+def _attn_fwd_kv4_bytes(*sizes) -> int:
+    return lib().attn_fwd_kv4_workspace_size(*sizes)
+
+
 def attn_fwd_kv4(q: torch.Tensor, cache: torch.Tensor, page_table: torch.Tensor, kv_len: torch.Tensor,
                  softmax_scale: float | None = None, causal: bool = True, out: torch.Tensor | None = None,
                  lse: torch.Tensor | None = None, workspace: torch.Tensor | None = None,
@@ -1185,18 +1191,17 @@ def attn_fwd_kv4(q: torch.Tensor, cache: torch.Tensor, page_table: torch.Tensor,
         lse = _empty((B, Hq, Sq), dtype=torch.float32, device=dev)
     else:
         _expect_dense("lse", lse, (B, Hq, Sq), torch.float32, dev)
-    L = lib()
     if workspace is None:
-        size = L.attn_fwd_kv4_workspace_size(B, Sq, Hq, heads, most, page_size)
+        size = _attn_fwd_kv4_bytes(B, Sq, Hq, heads, most, page_size)
         workspace = _empty(size, dtype=torch.uint8, device=dev)
     else:
         size = _scratch("workspace", workspace, dev)
     held = _kv4_strides(q, out)
     at = held.buffer_info()[0]
-    status = L.attn_fwd_kv4(q.data_ptr(), cache.data_ptr(), pages, page_size, page_table.data_ptr(), table_str, most,
-                            _kv4_counts("kv_len", kv_len, B, dev), out.data_ptr(), lse.data_ptr(), B, Sq, Hq, heads, D, at,
-                            at + 32, D ** -0.5 if softmax_scale is None else softmax_scale, causal, workspace.data_ptr(), size,
-                            _current_stream(dev))
+    status = lib().attn_fwd_kv4(q.data_ptr(), cache.data_ptr(), pages, page_size, page_table.data_ptr(), table_str, most,
+                                _kv4_counts("kv_len", kv_len, B, dev), out.data_ptr(), lse.data_ptr(), B, Sq, Hq, heads, D, at,
+                                at + 32, D ** -0.5 if softmax_scale is None else softmax_scale, causal, workspace.data_ptr(), size,
+                                _current_stream(dev))
     if status != 0:
         _check(status)
     return out, lse

@@ -83,8 +83,8 @@ __device__ __forceinline__ uint32_t transpose8(uint32_t x) {
   asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
   return y;
 }
-// V: four codes of each of two tokens, 4 bits each in halves of x, as FP16 pairs of code - 8.  low, high: FP16 1024 and 64 twice, in
-// registers (an instruction takes one constant).
+// V: four codes of each of two tokens, 4 bits each in halves of x, as FP16 pairs of code - 8.  low, high: FP16 1024 and 64
+// twice, in registers (an instruction takes one constant).
 __device__ __forceinline__ void v_pairs(uint32_t x, uint32_t low, uint32_t high, uint32_t (&a)[4]) {
 #pragma unroll
   for (int i = 0; i < 2; ++i) {
@@ -124,13 +124,13 @@ __device__ __forceinline__ int tokens_of(const AttnParams& p, int b) { return mi
 
 // One CTA an SM, of as many warps as the registers allow.
 constexpr int warps(int rows) { return rows == 4 ? 12 : rows == 8 ? 11 : 8; }
-// Records that a warp works on at a time: two, whose products do not wait for one another (one: 8 x 131072 tokens 257 us, so
-// 243); one where the registers do not reach for two.
+// Records that a warp works on at a time: two, whose products do not wait for one another (8 x 131072 tokens, three CTAs of four
+// warps: one at a time 257 us, two 243); one where the registers do not reach for two.
 constexpr int together(int rows) { return rows <= 8 ? 2 : 1; }
 constexpr int kRing = kHeld * kKvRecord;   // shared memory of a warp
 
-// kRows: queries of a CTA, 4, 8 or 16.  Four of them are the even columns of a product's eight, so that every lane has scores
-// of one.
+// kRows: queries that an item's records are read for, 4, 8 or 16.  Four of them are the even columns of a product's eight, so
+// that every lane has scores of one.
 template <int kRows>
 __global__ void __launch_bounds__(32 * warps(kRows), 1) kv4_attn_kernel(const __grid_constant__ AttnParams p) {
   constexpr int kWarps = warps(kRows), kThreads = 32 * kWarps;
@@ -605,7 +605,8 @@ cudaError_t launch_both(const AttnParams& p, const Grid& g, cudaStream_t stream)
   cudaError_t e = attr_done.run([] {
     return cudaFuncSetAttribute(kv4_attn_kernel<kRows>, cudaFuncAttributeMaxDynamicSharedMemorySize, kShared);
   });
-  if (e == cudaSuccess) e = launch_dependent(kv4_attn_kernel<kRows>, dim3((unsigned)g.ctas), 32 * warps(kRows), kShared, stream, p);
+  if (e == cudaSuccess)
+    e = launch_dependent(kv4_attn_kernel<kRows>, dim3((unsigned)g.ctas), 32 * warps(kRows), kShared, stream, p);
   if (e != cudaSuccess) return e;
   return launch_dependent(kv4_join_kernel<kRows>, dim3((unsigned)g.segments, kRows), 256, 0, stream, p);
 }
