@@ -63,6 +63,7 @@ __global__ void __launch_bounds__(kRopeThreads, ctas_an_sm(kMap, kPairs, sizeof(
   auto load = [&](int u) {
     if (to_load == turns_q) share(in, 1, p.side[1].x, p.side[1].xs);
     if (mine && in.head < in.end && to_load < turns) ln.load(in.row, raw[u]);
+    else raw[u] = {};
     in.next(p.slots, p.side[to_load >= turns_q].x_step);
     ++to_load;
   };
@@ -81,27 +82,18 @@ __global__ void __launch_bounds__(kRopeThreads, ctas_an_sm(kMap, kPairs, sizeof(
       if (base + u == turns_q) share(out, 1, p.side[1].y, p.side[1].ys);
       float a[kPairs], c[kPairs];
       const bool some = mine && out.head < out.end;
-      if (some) {
-        ln.values(raw[u], a, c);
-      } else {
-#pragma unroll
-        for (int i = 0; i < kPairs; ++i) a[i] = c[i] = 0.0f;
-      }
+      ln.values(raw[u], a, c);
       load(u);
       if constexpr (kNorm) {
-        float sum = 0.0f;
-#pragma unroll
-        for (int i = 0; i < kPairs; ++i) sum = fmaf(a[i], a[i], fmaf(c[i], c[i], sum));
-        sum = rope_row_sum(sum, p.lanes);
-        const float r = rsqrtf(fmaf(sum, p.inv_n, p.eps));
+        const float sum = rope_row_sum(rope_squares(a, c), p.lanes), r = rsqrtf(fmaf(sum, p.inv_n, p.eps));
         const float4* const weights = shared + (base + u >= turns_q ? kPairs / 2 * 32 : 0) + ln.l;
 #pragma unroll
         for (int k = 0; k < kPairs / 2; ++k) {
-          const float4 w = load_shared(weights + k * p.lanes);
-          a[2 * k] *= r * w.x;
-          c[2 * k] *= r * w.y;
-          a[2 * k + 1] *= r * w.z;
-          c[2 * k + 1] *= r * w.w;
+          float4 w = load_shared(weights + k * p.lanes);
+          fmul2(w.x, w.y, w.x, w.y, r, r);
+          fmul2(w.z, w.w, w.z, w.w, r, r);
+          fmul2(a[2 * k], a[2 * k + 1], a[2 * k], a[2 * k + 1], w.x, w.y);
+          fmul2(c[2 * k], c[2 * k + 1], c[2 * k], c[2 * k + 1], w.z, w.w);
         }
       }
       if (L::kExchange || some) rope_turn<kPairs>(p, ln, table, swap, lane, a, c);

@@ -12,6 +12,7 @@
 
 #include "kernels.h"
 #include "pieces.cuh"
+#include "ptx_train.cuh"
 
 namespace sa {
 
@@ -186,14 +187,14 @@ struct RopeLane {
     }
   }
   // The weights of the lane's channels (1 without weights, or where there is no channel).
-  // Those of pair i in v[2 i], v[2 i + 1].
+  // Those of pairs i and i + 1 (i even) in v[2 i], v[2 i + 1], then their second channels'.
   __device__ __forceinline__ void weights(const void* w, const RopeParams& p, float (&v)[2 * kPairs]) const {
     float a[kPairs], b[kPairs];
     weights(w, p, a, b);
 #pragma unroll
     for (int i = 0; i < kPairs; ++i) {
-      v[2 * i] = a[i];
-      v[2 * i + 1] = b[i];
+      v[i / 2 * 4 + i % 2] = a[i];
+      v[i / 2 * 4 + 2 + i % 2] = b[i];
     }
   }
   __device__ __forceinline__ void weights(const void* w, const RopeParams& p, float (&a)[kPairs],
@@ -249,8 +250,8 @@ struct RopeWalk {
 };
 
 // Cosine and sine (times the magnitude) of a token's pairs, to `table`; the sine negated for the backward.  By pieces: in the
-// order in which lanes read them, [4][lanes] of two pairs, or for kApart [8][lanes] of two channels, a first half's sine
-// negated and (1, 0) where a channel passes; else pair by pair.
+// order in which lanes read them, [4][lanes] of two pairs (both cosines, both sines), or for kApart [8][lanes] of two channels, a
+// first half's sine negated and (1, 0) where a channel passes; else pair by pair.
 template <int kMap>
 __device__ __forceinline__ void rope_table(const RopeParams& p, int b, int s, int lane, float2* table) {
   constexpr bool kVec = kMap < kAny;
@@ -271,8 +272,12 @@ __device__ __forceinline__ void rope_table(const RopeParams& p, int b, int s, in
       const int c = i + p.pairs;
       table[((i % 16 / 2) * p.lanes + i / 16) * 2 + i % 2] = make_float2(cs, -sn);
       table[((c % 16 / 2) * p.lanes + c / 16) * 2 + c % 2] = make_float2(cs, sn);
+    } else if (kVec) {
+      float* const two = reinterpret_cast<float*>(table + ((i % 8 / 2) * p.lanes + i / 8) * 2);
+      two[i % 2] = cs;
+      two[2 + i % 2] = sn;
     } else {
-      table[kVec ? ((i % 8 / 2) * p.lanes + i / 8) * 2 + i % 2 : i] = make_float2(cs, sn);
+      table[i] = make_float2(cs, sn);
     }
   }
   if (kMap == kApart)
@@ -296,6 +301,18 @@ __device__ __forceinline__ float2 load_shared(const float2* at) {
   return v;
 }
 
+// The sum of squares of a lane's channels.
+template <int kPairs>
+__device__ __forceinline__ float rope_squares(const float (&a)[kPairs], const float (&b)[kPairs]) {
+  float x = 0.0f, y = 0.0f;
+#pragma unroll
+  for (int i = 0; i < kPairs; i += 2) {
+    ffma2(x, y, a[i], a[i + 1], a[i], a[i + 1], x, y);
+    ffma2(x, y, b[i], b[i + 1], b[i], b[i + 1], x, y);
+  }
+  return x + y;
+}
+
 // The rotation of a lane's channels (every lane of the warp takes part).
 template <int kPairs, class L>
 __device__ __forceinline__ void rope_turn(const RopeParams& p, const L& ln, const float2* table, float* swap, int lane,
@@ -308,30 +325,42 @@ __device__ __forceinline__ void rope_turn(const RopeParams& p, const L& ln, cons
       swap[(2 * i + 1) * 32 + lane] = b[i];
     }
     __syncwarp();
-  }
 #pragma unroll
-  for (int k = 0; k < kPairs / (L::kExchange ? 1 : 2); ++k) {
-    float2 t[2];   // cosines and sines of two pairs, or of two channels
-    if (L::kVec) {
-      const float4 two = load_shared(reinterpret_cast<const float4*>(table) + k * p.lanes + ln.l);
-      t[0] = make_float2(two.x, two.y);
-      t[1] = make_float2(two.z, two.w);
-    } else {
-#pragma unroll
-      for (int e = 0; e < 2; ++e)
-        if (ln.pair(2 * k + e) < p.pairs) t[e] = load_shared(table + ln.pair(2 * k + e));
+    for (int k = 0; k < kPairs; ++k) {
+      const float4 t = load_shared(reinterpret_cast<const float4*>(table) + k * p.lanes + ln.l);   // of two channels
+      a[k] = a[k] * t.x + swap[ln.from[2 * k]] * t.y;
+      b[k] = b[k] * t.z + swap[ln.from[2 * k + 1]] * t.w;
     }
-    if constexpr (L::kExchange) {
-      a[k] = a[k] * t[0].x + swap[ln.from[2 * k]] * t[0].y;
-      b[k] = b[k] * t[1].x + swap[ln.from[2 * k + 1]] * t[1].y;
+  } else {
+    // (pairs that pass: an infinity beside a channel that passes stays out of it)
+    auto turn = [&](int i, float cs, float sn) {
+      const float a0 = a[i];
+      a[i] = a0 * cs - b[i] * sn;
+      b[i] = b[i] * cs + a0 * sn;
+    };
+    if constexpr (L::kVec) {
+      const int turned = p.pairs - ln.pair(0);   // of the lane's eight
+      if (turned <= 0) return;
+#pragma unroll
+      for (int k = 0; k < kPairs / 2; ++k) {
+        const float4 t = load_shared(reinterpret_cast<const float4*>(table) + k * p.lanes + ln.l);
+        float &a0 = a[2 * k], &a1 = a[2 * k + 1], &b0 = b[2 * k], &b1 = b[2 * k + 1];
+        if (turned > 2 * k + 1) {
+          float x0, x1;   // two products in one instruction; one of a sign that it does not have in two
+          const float y0 = -b0 * t.z, y1 = -b1 * t.w;
+          fmul2(x0, x1, a0, a1, t.z, t.w);
+          ffma2(a0, a1, a0, a1, t.x, t.y, y0, y1);
+          ffma2(b0, b1, b0, b1, t.x, t.y, x0, x1);
+        } else if (turned == 2 * k + 1) {
+          turn(2 * k, t.x, t.z);
+        }
+      }
     } else {
 #pragma unroll
-      for (int e = 0; e < 2; ++e) {
-        const int i = 2 * k + e;
-        if (ln.pair(i) >= p.pairs) continue;   // (an infinity beside a channel that passes stays out of it)
-        const float a0 = a[i];
-        a[i] = a0 * t[e].x - b[i] * t[e].y;
-        b[i] = b[i] * t[e].x + a0 * t[e].y;
+      for (int i = 0; i < kPairs; ++i) {
+        if (ln.pair(i) >= p.pairs) continue;
+        const float2 t = load_shared(table + ln.pair(i));
+        turn(i, t.x, t.y);
       }
     }
   }

@@ -64,6 +64,8 @@ __global__ void __launch_bounds__(kRopeThreads, ctas_an_sm(kMap, kPairs, sizeof(
         if (mine && x.head < end) {
           ln.load(x.row, rx[u]);
           ln.load(dy.row, rd[u]);
+        } else {
+          rx[u] = rd[u] = {};
         }
         x.next(p.slots, sd.x_step);
         dy.next(p.slots, sd.d_step);
@@ -78,41 +80,32 @@ __global__ void __launch_bounds__(kRopeThreads, ctas_an_sm(kMap, kPairs, sizeof(
           if (base + u * p.slots >= end) break;
           float a[kPairs], c[kPairs], ga[kPairs], gc[kPairs];
           const bool in = mine && dx.head < end;
-          if (in) {
-            ln.values(rx[u], a, c);
-            ln.values(rd[u], ga, gc);
-          } else {
-#pragma unroll
-            for (int i = 0; i < kPairs; ++i) a[i] = c[i] = ga[i] = gc[i] = 0.0f;
-          }
+          ln.values(rx[u], a, c);
+          ln.values(rd[u], ga, gc);
           load(u);
-          float sum = 0.0f;
-#pragma unroll
-          for (int i = 0; i < kPairs; ++i) sum = fmaf(a[i], a[i], fmaf(c[i], c[i], sum));
-          const float r = rsqrtf(fmaf(rope_row_sum(sum, p.lanes), p.inv_n, p.eps));
+          const float r = rsqrtf(fmaf(rope_row_sum(rope_squares(a, c), p.lanes), p.inv_n, p.eps));
           rope_turn<kPairs>(p, ln, table, swap, lane, ga, gc);
-          float dot = 0.0f;
+          float dot0 = 0.0f, dot1 = 0.0f;
 #pragma unroll
-          for (int k = 0; k < kPairs / 2; ++k) {
-            const float4 w = load_shared(shared + k * p.lanes + ln.l);
-#pragma unroll
-            for (int e = 0; e < 2; ++e) {
-              const int i = 2 * k + e;
-              a[i] *= r;
-              c[i] *= r;
-              da[i] = fmaf(ga[i], a[i], da[i]);
-              db[i] = fmaf(gc[i], c[i], db[i]);
-              ga[i] *= e ? w.z : w.x;
-              gc[i] *= e ? w.w : w.y;
-              dot = fmaf(ga[i], a[i], fmaf(gc[i], c[i], dot));
-            }
+          for (int i = 0; i < kPairs; i += 2) {
+            const float4 w = load_shared(shared + i / 2 * p.lanes + ln.l);
+            fmul2(a[i], a[i + 1], a[i], a[i + 1], r, r);
+            fmul2(c[i], c[i + 1], c[i], c[i + 1], r, r);
+            ffma2(da[i], da[i + 1], ga[i], ga[i + 1], a[i], a[i + 1], da[i], da[i + 1]);
+            ffma2(db[i], db[i + 1], gc[i], gc[i + 1], c[i], c[i + 1], db[i], db[i + 1]);
+            fmul2(ga[i], ga[i + 1], ga[i], ga[i + 1], w.x, w.y);
+            fmul2(gc[i], gc[i + 1], gc[i], gc[i + 1], w.z, w.w);
+            ffma2(dot0, dot1, ga[i], ga[i + 1], a[i], a[i + 1], dot0, dot1);
+            ffma2(dot0, dot1, gc[i], gc[i + 1], c[i], c[i + 1], dot0, dot1);
           }
-          dot = rope_row_sum(dot, p.lanes) * p.inv_n;
+          const float dot = rope_row_sum(dot0 + dot1, p.lanes) * -p.inv_n;
           if (in) {
 #pragma unroll
-            for (int i = 0; i < kPairs; ++i) {
-              a[i] = r * (ga[i] - a[i] * dot);
-              c[i] = r * (gc[i] - c[i] * dot);
+            for (int i = 0; i < kPairs; i += 2) {
+              ffma2(a[i], a[i + 1], a[i], a[i + 1], dot, dot, ga[i], ga[i + 1]);
+              ffma2(c[i], c[i + 1], c[i], c[i + 1], dot, dot, gc[i], gc[i + 1]);
+              fmul2(a[i], a[i + 1], a[i], a[i + 1], r, r);
+              fmul2(c[i], c[i + 1], c[i], c[i + 1], r, r);
             }
             ln.store(dx.row, a, c);
           }
