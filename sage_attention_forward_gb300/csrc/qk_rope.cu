@@ -14,16 +14,17 @@ namespace sa {
 namespace {
 
 // Rows of a slot whose loads are under way, and CTAs an SM: loads in flight are what the kernels wait for, and more warps with
-// fewer rows each do better (76112 x 80 heads of 128 BF16: four rows, two CTAs 546 us; two, three 497; two, four 467).
+// fewer rows each do better (76112 x 80 heads of 128 BF16: four rows, two CTAs 546 us; two, three 497; two, four 467; with the
+// norm, 33000 x 40 heads in halves: two, three 106.5; two, four 102.9).
 constexpr int rows_ahead(int map, bool wide) { return map < kAny && wide ? 1 : 2; }
-constexpr int ctas_an_sm(int map, int pairs, bool wide, bool norm) {
-  return map >= kAny ? (pairs == 4 ? 3 : 1) : map == kApart ? (wide ? 2 : 3) : wide ? (norm ? 2 : 3) : map == kHalf && norm ? 3 : 4;
+constexpr int ctas_an_sm(int map, int pairs, bool wide) {
+  return map >= kAny ? (pairs == 4 ? 3 : 1) : map == kApart ? (wide ? 2 : 3) : wide ? 3 : 4;
 }
 
-template <class T, int kMap, int kPairs, bool kNorm>
-__global__ void __launch_bounds__(kRopeThreads, ctas_an_sm(kMap, kPairs, sizeof(T) == 4, kNorm))
+template <class T, int kMap, int kPairs, int kLanes, bool kNorm>
+__global__ void __launch_bounds__(kRopeThreads, ctas_an_sm(kMap, kPairs, sizeof(T) == 4))
     rope_fwd_kernel(const __grid_constant__ RopeParams p) {
-  using L = RopeLane<T, kMap, kPairs>;
+  using L = RopeLane<T, kMap, kPairs, kLanes>;
   constexpr int kAhead = rows_ahead(kMap, sizeof(T) == 4);
   // kNorm: the weights of Q and of K by lanes, [2][kPairs / 2][lanes] of four (held in registers they take the warps that hide
   // the loads); then the tables
@@ -33,12 +34,12 @@ __global__ void __launch_bounds__(kRopeThreads, ctas_an_sm(kMap, kPairs, sizeof(
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   if constexpr (kNorm) {
     const L ln(p, lane);
-    if (warp < 2 && lane < p.lanes) {
+    if (warp < 2 && lane < ln.lanes) {
       float w[2 * kPairs];
       ln.weights(p.side[warp].w, p, w);
 #pragma unroll
       for (int k = 0; k < kPairs / 2; ++k)
-        shared[(warp * (kPairs / 2) * 32) + k * p.lanes + ln.l] = make_float4(w[4 * k], w[4 * k + 1], w[4 * k + 2], w[4 * k + 3]);
+        shared[(warp * (kPairs / 2) * 32) + k * ln.lanes + ln.l] = make_float4(w[4 * k], w[4 * k + 1], w[4 * k + 2], w[4 * k + 3]);
     }
     __syncthreads();
   }
@@ -47,8 +48,8 @@ __global__ void __launch_bounds__(kRopeThreads, ctas_an_sm(kMap, kPairs, sizeof(
   if (token >= p.tokens) return;
   const int b = div_by(token, p.S), s = token - b * (int)p.S.d;
   const L ln(p, lane);
-  const int slot = lane / p.lanes;
-  const bool mine = slot < p.slots && ln.some();
+  const int slot = lane / ln.lanes;
+  const bool mine = slot < ln.slots && ln.some();
   // the unit's share of Q's heads, then of K's, p.slots of them a turn
   const int turns_q = p.side[0].turns, turns = turns_q + p.side[1].turns;
   auto share = [&](RopeWalk<T>& w, int which, const void* base, const long long (&str)[3]) {
@@ -64,7 +65,7 @@ __global__ void __launch_bounds__(kRopeThreads, ctas_an_sm(kMap, kPairs, sizeof(
     if (to_load == turns_q) share(in, 1, p.side[1].x, p.side[1].xs);
     if (mine && in.head < in.end && to_load < turns) ln.load(in.row, raw[u]);
     else raw[u] = {};
-    in.next(p.slots, p.side[to_load >= turns_q].x_step);
+    in.next(ln.slots, p.side[to_load >= turns_q].x_step);
     ++to_load;
   };
 #pragma unroll
@@ -73,7 +74,7 @@ __global__ void __launch_bounds__(kRopeThreads, ctas_an_sm(kMap, kPairs, sizeof(
   float2* const table = reinterpret_cast<float2*>(tables + warp * p.shared);
   float* const swap = reinterpret_cast<float*>(table + p.table);
   if (L::kExchange && lane == 0) swap[16 * 32] = 0.0f;
-  rope_table<kMap>(p, b, s, lane, table);
+  rope_table<kMap>(p, ln.lanes, b, s, lane, table);
 
   for (int base = 0; base < turns; base += kAhead) {
 #pragma unroll
@@ -85,11 +86,11 @@ __global__ void __launch_bounds__(kRopeThreads, ctas_an_sm(kMap, kPairs, sizeof(
       ln.values(raw[u], a, c);
       load(u);
       if constexpr (kNorm) {
-        const float sum = rope_row_sum(rope_squares(a, c), p.lanes), r = rsqrtf(fmaf(sum, p.inv_n, p.eps));
+        const float sum = rope_row_sum<kLanes>(rope_squares(a, c), ln.lanes, ln.l), r = rsqrtf(fmaf(sum, p.inv_n, p.eps));
         const float4* const weights = shared + (base + u >= turns_q ? kPairs / 2 * 32 : 0) + ln.l;
 #pragma unroll
         for (int k = 0; k < kPairs / 2; ++k) {
-          float4 w = load_shared(weights + k * p.lanes);
+          float4 w = load_shared(weights + k * ln.lanes);
           fmul2(w.x, w.y, w.x, w.y, r, r);
           fmul2(w.z, w.w, w.z, w.w, r, r);
           fmul2(a[2 * k], a[2 * k + 1], a[2 * k], a[2 * k + 1], w.x, w.y);
@@ -98,7 +99,7 @@ __global__ void __launch_bounds__(kRopeThreads, ctas_an_sm(kMap, kPairs, sizeof(
       }
       if (L::kExchange || some) rope_turn<kPairs>(p, ln, table, swap, lane, a, c);
       if (some) ln.store(out.row, a, c);
-      out.next(p.slots, p.side[base + u >= turns_q].y_step);
+      out.next(ln.slots, p.side[base + u >= turns_q].y_step);
     }
   }
 }
@@ -106,10 +107,11 @@ __global__ void __launch_bounds__(kRopeThreads, ctas_an_sm(kMap, kPairs, sizeof(
 template <class T, bool kNorm>
 cudaError_t launch_fwd(RopeParams& p, bool vec, bool next, cudaStream_t stream) {
   const long long units = (long long)p.tokens * p.by_parts.d;
-  return with_rope_map(p, vec, next, [&](auto map, auto pairs) {
+  return with_rope_map<kNorm>(p, vec, next, [&](auto map, auto pairs, auto lanes) {
     constexpr int kPairs = decltype(pairs)::value;
-    return launch_dependent(rope_fwd_kernel<T, decltype(map)::value, kPairs, kNorm>, dim3((unsigned)((units + kRopeWarps - 1) / kRopeWarps)),
-                            kRopeThreads, (kNorm ? kPairs * 32 * sizeof(float4) : 0) + kRopeWarps * p.shared, stream, p);
+    return launch_dependent(rope_fwd_kernel<T, decltype(map)::value, kPairs, decltype(lanes)::value, kNorm>,
+                            dim3((unsigned)((units + kRopeWarps - 1) / kRopeWarps)), kRopeThreads,
+                            (kNorm ? kPairs * 32 * sizeof(float4) : 0) + kRopeWarps * p.shared, stream, p);
   });
 }
 template <bool kNorm>

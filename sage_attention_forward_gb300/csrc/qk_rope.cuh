@@ -48,7 +48,8 @@ struct RopeParams {
 enum RopeMap : int { kHalf = 0, kNext = 1, kApart = 2, kAny = 3, kAnyNext = 4 };
 constexpr int kSwap = 17 * 32;   // kApart: floats of a warp's exchange: [16][lane], then a zero
 
-template <class T, int kMap, int kPairs>
+// kLanes: lanes a row where the kernel is made for that number (sums over them unrolled, offsets known), or 0.
+template <class T, int kMap, int kPairs, int kLanes>
 struct RopeLane {
   static constexpr bool kVec = kMap < kAny, kExchange = kMap == kApart;
   static constexpr int kPieces = kVec ? (int)sizeof(T) : 1;   // 16-byte pieces of a lane's 16 channels
@@ -59,13 +60,15 @@ struct RopeLane {
   static constexpr bool kShort = sizeof(T) == 2;
   __device__ __forceinline__ bool neighbours() const { return kMap == kAnyNext && word; }
   int l, ca, cb, last;   // kVec: first channels of the two runs of eight; last: N
-  int step, word;        // else: pairs l, l + step, ...; pairs of neighbours as one access
+  int lanes, slots;      // p.lanes, p.slots
+  int word;              // else: pairs l, l + lanes, ...; pairs of neighbours as one access
   int at_a[kVec ? 1 : kPairs], at_b[kVec ? 1 : kPairs];   // else: the channels of each pair
   int from[kMap == kApart ? 16 : 1];                      // kApart: where the exchange has the channels' partners
 
   __device__ __forceinline__ RopeLane(const RopeParams& p, int lane) {
-    l = lane % p.lanes;
-    step = p.lanes;
+    lanes = kLanes > 0 ? kLanes : p.lanes;
+    slots = kLanes > 0 ? 32 / kLanes : p.slots;
+    l = lane % lanes;
     word = p.word;
     last = p.N;
     const bool turned = kMap == kHalf && 8 * l < p.pairs;
@@ -89,7 +92,7 @@ struct RopeLane {
   }
   // kVec: the lane has channels of a row
   __device__ __forceinline__ bool some() const { return !kVec || 16 * l < last; }
-  __device__ __forceinline__ int pair(int i) const { return kVec ? 8 * l + i : l + step * i; }
+  __device__ __forceinline__ int pair(int i) const { return kVec ? 8 * l + i : l + lanes * i; }
   __device__ __forceinline__ int first(int i) const {
     if constexpr (kVec) return kMap == kHalf ? ca + i : 16 * l + 2 * i;
     else return at_a[i];
@@ -205,7 +208,7 @@ struct RopeLane {
     if constexpr (kVec) {
       if (p.w_vec) {
         if (p.w_type == kF32) {
-          RopeLane<float, kMap, 8>(p, l).take(reinterpret_cast<const float*>(w), a, b);
+          RopeLane<float, kMap, 8, kLanes>(p, l).take(reinterpret_cast<const float*>(w), a, b);
         } else {
           take(reinterpret_cast<const T*>(w), a, b);
         }
@@ -253,7 +256,7 @@ struct RopeWalk {
 // order in which lanes read them, [4][lanes] of two pairs (both cosines, both sines), or for kApart [8][lanes] of two channels, a
 // first half's sine negated and (1, 0) where a channel passes; else pair by pair.
 template <int kMap>
-__device__ __forceinline__ void rope_table(const RopeParams& p, int b, int s, int lane, float2* table) {
+__device__ __forceinline__ void rope_table(const RopeParams& p, int lanes, int b, int s, int lane, float2* table) {
   constexpr bool kVec = kMap < kAny;
   __syncwarp();   // the last token's are no longer read
   for (int i = lane; i < p.pairs; i += 32) {
@@ -270,10 +273,10 @@ __device__ __forceinline__ void rope_table(const RopeParams& p, int b, int s, in
     sn *= p.inverse ? -p.magnitude : p.magnitude;
     if (kMap == kApart) {
       const int c = i + p.pairs;
-      table[((i % 16 / 2) * p.lanes + i / 16) * 2 + i % 2] = make_float2(cs, -sn);
-      table[((c % 16 / 2) * p.lanes + c / 16) * 2 + c % 2] = make_float2(cs, sn);
+      table[((i % 16 / 2) * lanes + i / 16) * 2 + i % 2] = make_float2(cs, -sn);
+      table[((c % 16 / 2) * lanes + c / 16) * 2 + c % 2] = make_float2(cs, sn);
     } else if (kVec) {
-      float* const two = reinterpret_cast<float*>(table + ((i % 8 / 2) * p.lanes + i / 8) * 2);
+      float* const two = reinterpret_cast<float*>(table + ((i % 8 / 2) * lanes + i / 8) * 2);
       two[i % 2] = cs;
       two[2 + i % 2] = sn;
     } else {
@@ -281,8 +284,8 @@ __device__ __forceinline__ void rope_table(const RopeParams& p, int b, int s, in
     }
   }
   if (kMap == kApart)
-    for (int c = 2 * p.pairs + lane; c < 16 * p.lanes; c += 32)
-      table[((c % 16 / 2) * p.lanes + c / 16) * 2 + c % 2] = make_float2(1.0f, 0.0f);
+    for (int c = 2 * p.pairs + lane; c < 16 * lanes; c += 32)
+      table[((c % 16 / 2) * lanes + c / 16) * 2 + c % 2] = make_float2(1.0f, 0.0f);
   __syncwarp();
 }
 
@@ -327,7 +330,7 @@ __device__ __forceinline__ void rope_turn(const RopeParams& p, const L& ln, cons
     __syncwarp();
 #pragma unroll
     for (int k = 0; k < kPairs; ++k) {
-      const float4 t = load_shared(reinterpret_cast<const float4*>(table) + k * p.lanes + ln.l);   // of two channels
+      const float4 t = load_shared(reinterpret_cast<const float4*>(table) + k * ln.lanes + ln.l);   // of two channels
       a[k] = a[k] * t.x + swap[ln.from[2 * k]] * t.y;
       b[k] = b[k] * t.z + swap[ln.from[2 * k + 1]] * t.w;
     }
@@ -343,7 +346,7 @@ __device__ __forceinline__ void rope_turn(const RopeParams& p, const L& ln, cons
       if (turned <= 0) return;
 #pragma unroll
       for (int k = 0; k < kPairs / 2; ++k) {
-        const float4 t = load_shared(reinterpret_cast<const float4*>(table) + k * p.lanes + ln.l);
+        const float4 t = load_shared(reinterpret_cast<const float4*>(table) + k * ln.lanes + ln.l);
         float &a0 = a[2 * k], &a1 = a[2 * k + 1], &b0 = b[2 * k], &b1 = b[2 * k + 1];
         if (turned > 2 * k + 1) {
           float x0, x1;   // two products in one instruction; one of a sign that it does not have in two
@@ -366,23 +369,46 @@ __device__ __forceinline__ void rope_turn(const RopeParams& p, const L& ln, cons
   }
 }
 
-// Sum over the lanes of a row (a power of two of them).
-__device__ __forceinline__ float rope_row_sum(float v, int lanes) {
-  for (int o = 1; o < lanes; o <<= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
-  return v;
+// Sum over the lanes of a row, the same in all of them.
+template <int kLanes>
+__device__ __forceinline__ float rope_row_sum(float v, int lanes, int l) {
+  const int n = kLanes > 0 ? kLanes : lanes;
+  if ((n & (n - 1)) == 0) {
+#pragma unroll
+    for (int o = 1; o < n; o <<= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+    return v;
+  }
+  float sum = v;   // in a row's first lane
+#pragma unroll
+  for (int o = 1; o < n; ++o) sum += __shfl_down_sync(0xffffffffu, v, o);
+  return __shfl_sync(0xffffffffu, sum, (int)(threadIdx.x & 31) - l);
 }
 
-// Calls f with the map and the pairs a lane for this problem, as constants.
-template <class F>
+// Calls f with the map, the pairs a lane and, for a norm, the lanes a row where they are usual ones (8: 128 channels; by pieces
+// 4 and 5, too: 64 and 80; else 0), as constants.
+template <bool kNorm, class F>
 cudaError_t with_rope_map(const RopeParams& p, bool vec, bool next, F&& f) {
   using std::integral_constant;
-  auto with = [&](auto pairs) {
-    return next ? f(integral_constant<int, kAnyNext>{}, pairs) : f(integral_constant<int, kAny>{}, pairs);
-  };
+  constexpr integral_constant<int, 0> any{};
   constexpr integral_constant<int, 8> eight{};
-  if (vec && next) return f(integral_constant<int, kNext>{}, eight);
-  if (vec) return p.pairs % 8 == 0 ? f(integral_constant<int, kHalf>{}, eight) : f(integral_constant<int, kApart>{}, eight);
-  return p.per == 4 ? with(integral_constant<int, 4>{}) : with(eight);
+  auto pieces = [&](auto map) {
+    if constexpr (kNorm) {
+      if (p.lanes == 8) return f(map, eight, eight);
+      if (p.lanes == 4) return f(map, eight, integral_constant<int, 4>{});
+      if (p.lanes == 5) return f(map, eight, integral_constant<int, 5>{});
+    }
+    return f(map, eight, any);
+  };
+  auto channels = [&](auto pairs, auto lanes) {
+    return next ? f(integral_constant<int, kAnyNext>{}, pairs, lanes) : f(integral_constant<int, kAny>{}, pairs, lanes);
+  };
+  if (vec && next) return pieces(integral_constant<int, kNext>{});
+  if (vec) return p.pairs % 8 == 0 ? pieces(integral_constant<int, kHalf>{}) : pieces(integral_constant<int, kApart>{});
+  if (p.per == 8) return channels(eight, any);
+  if constexpr (kNorm) {
+    if (p.lanes == 8) return channels(integral_constant<int, 4>{}, eight);
+  }
+  return channels(integral_constant<int, 4>{}, any);
 }
 
 // Whether rows go by 16 bytes (kApart while its shared memory stays below 48 KB); lanes a row and rows a warp.
@@ -405,8 +431,11 @@ inline bool rope_shape(RopeParams& p, const RopeArgs& a, bool norm) {
   p.word = word;
   const int pairs = (a.N + 1) / 2;
   auto lanes = [&](int n) {
-    while (norm && (n & (n - 1)) != 0) ++n;   // a norm's sums go over a power of two of lanes
-    return n;
+    // a norm's sums go over a power of two of lanes, unless more rows a turn pay for the longer way: three in place of two do
+    // (33000 x 40 heads of 80 BF16, backward: 157 -> 148 us), five in place of four do not (96 channels: 163 -> 169)
+    int up = n;
+    while (norm && (up & (up - 1)) != 0) ++up;
+    return 2 * (32 / n) >= 3 * (32 / up) ? n : up;
   };
   // by the channel: four pairs a lane, or eight where that leaves fewer lanes idle (N = 130: a row takes 17 of 32, or 9)
   const int four = lanes((pairs + 3) / 4), eight = lanes((pairs + 7) / 8);

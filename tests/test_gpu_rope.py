@@ -37,6 +37,9 @@ CASES = [
     (1, 3, 2, 2, 511, 2, True, None, None),
     (1, 2, 70, 3, 16, 16, False, None, None),              # a lane a row, more heads than a pass
     (1, 400, 2, 0, 32, 32, False, None, None),             # no K
+    (1, 19, 23, 11, 48, 48, False, None, None),            # three lanes a row, ten rows a turn
+    (1, 11, 7, 4, 144, 144, False, None, None),            # nine lanes a row
+    (2, 5, 4, 4, 160, 64, True, None, None),
     (2, 3, 7, 2, 80, 34, False, None, None),               # halves that are no whole pieces, five lanes a row
     (1, 2, 3, 1, 512, 266, False, None, None),             # ... and all lanes one row's
     (1, 3, 5, 2, 128, 2, False, None, None),
