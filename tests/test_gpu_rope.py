@@ -40,6 +40,9 @@ CASES = [
     (1, 19, 23, 11, 48, 48, False, None, None),            # three lanes a row, ten rows a turn
     (1, 11, 7, 4, 144, 144, False, None, None),            # nine lanes a row
     (2, 5, 4, 4, 160, 64, True, None, None),
+    (1, 13, 9, 2, 80, 80, True, None, None),               # five lanes, six rows a turn
+    (2, 31, 13, 3, 58, 58, True, None, None),              # by the channel, eight lanes a row
+    (1, 7, 6, 5, 61, 40, False, None, None),
     (2, 3, 7, 2, 80, 34, False, None, None),               # halves that are no whole pieces, five lanes a row
     (1, 2, 3, 1, 512, 266, False, None, None),             # ... and all lanes one row's
     (1, 3, 5, 2, 128, 2, False, None, None),
