@@ -133,7 +133,10 @@ __global__ void __launch_bounds__(kRopeThreads, ctas_an_sm(kMap, kPairs, sizeof(
         }
       }
     }
-    if (sd.partial == nullptr) continue;
+    if (sd.partial == nullptr) {
+      __syncthreads();   // Q's weights are no longer read
+      continue;
+    }
     // the warp's slots, then the CTA's warps, in order
 #pragma unroll
     for (int i = 0; i < kPairs; ++i) {

@@ -1,0 +1,76 @@
+"""qk_norm_rope_bwd with weights and gradients left out, eps = 0 and expanded inputs, against its definition in 64 bits."""
+import ctypes
+
+import pytest
+import torch
+
+import rope_ref as ref
+import sage_attention_forward_gb300 as sa
+
+pytestmark = pytest.mark.gpu
+TYPES = {torch.bfloat16: 0, torch.float16: 1, torch.float32: 2}
+
+
+def rows(seed, *shape, dtype, gain=1.0):
+    g = torch.Generator().manual_seed(seed)
+    return (torch.randn(shape, generator=g) * gain).to(dtype)
+
+
+def strides(t):
+    return (ctypes.c_int64 * 3)(*t.stride()[:3])
+
+
+def backward(dq_out, dk_out, q, k, q_weight, k_weight, freq, eps, interleaved, wanted):
+    """The C call, float32 weights; wanted: which of dq_weight and dk_weight are asked for (the others are NULL)."""
+    B, S, Hq, N = q.shape
+    L, dq, dk = sa.lib(), torch.empty_like(q), torch.empty_like(k)
+    dw = [torch.empty(N, device=q.device) if w else None for w in wanted]
+    ws = torch.empty(L.qk_norm_rope_bwd_workspace_size(B, S, Hq, k.shape[2], N), dtype=torch.uint8, device=q.device)
+    ptr = lambda t: None if t is None else t.data_ptr()  # noqa: E731
+    held = [strides(t) for t in (dq_out, dk_out, q, k, dq, dk)]
+    status = L.qk_norm_rope_bwd(
+        dq_out.data_ptr(), dk_out.data_ptr(), q.data_ptr(), k.data_ptr(), ptr(q_weight), ptr(k_weight), dq.data_ptr(),
+        dk.data_ptr(), *map(ptr, dw), B, S, Hq, k.shape[2], N, *held, eps, None, None, 1, ptr(freq), 2 * len(freq), interleaved,
+        1.0, TYPES[q.dtype], 2, ws.data_ptr() if any(wanted) else None, ws.numel() if any(wanted) else 0,
+        torch.cuda.current_stream().cuda_stream)
+    assert status == 0, L.attn_last_error()
+    return dq, dk, *dw
+
+
+def check(got, x, dy, weights, freq, eps, interleaved):
+    """got: dq, dk, dq_weight, dk_weight (a None is not looked at); x, dy: Q's and K's, on the CPU."""
+    B, S, _, N = x[0].shape
+    cos, sin = ref.cos_sin(freq.cpu(), None, B, S, 1.0)
+    for i, name in enumerate("qk"):
+        w = torch.ones(N, dtype=torch.float64) if weights[i] is None else weights[i].cpu().double()
+        dx, bound, dw, dw_bound = ref.norm_rope_bwd(dy[i].double(), x[i].double(), w, eps, cos, sin, interleaved, 1.0)
+        ref.near(got[i], dx, bound, "d" + name)
+        if got[2 + i] is not None:
+            ref.near(got[2 + i], dw, dw_bound, f"d{name}_weight")
+
+
+# channels, rotated, interleaved, type: halves, neighbours, halves that are no whole pieces, by the channel
+MAPS = [(128, 128, False, torch.bfloat16), (128, 64, True, torch.bfloat16), (128, 90, False, torch.float16),
+        (77, 30, False, torch.bfloat16), (64, 64, False, torch.float32)]
+
+
+@pytest.mark.parametrize("weighted,wanted", [((1, 1), (0, 1)), ((1, 1), (1, 0)), ((1, 1), (0, 0)), ((0, 1), (0, 1)),
+                                             ((1, 0), (1, 0))])
+@pytest.mark.parametrize("N,R,interleaved,dtype", MAPS)
+def test_weights_and_gradients_left_out(N, R, interleaved, dtype, weighted, wanted, cuda_dev):
+    """Q's and K's weights far apart, several units a warp: each side's gradients are formed with its own weights."""
+    B, S, Hq, Hk = 1, 3001, 6, 5
+    freq = sa.rope_frequencies(R, device=cuda_dev)[0]
+    x = rows(1, B, S, Hq, N, dtype=dtype), rows(2, B, S, Hk, N, dtype=dtype)
+    dy = rows(3, B, S, Hq, N, dtype=dtype, gain=0.1), rows(4, B, S, Hk, N, dtype=dtype, gain=0.1)
+    weights = [(gain + rows(5 + i, N, dtype=torch.float32, gain=0.2)).to(cuda_dev) if weighted[i] else None
+               for i, gain in enumerate((1.0, 9.0))]
+    dev = [t.to(cuda_dev) for t in (*dy, *x)]
+    got = backward(*dev, *weights, freq, 1e-5, interleaved, wanted)
+    check(got, x, dy, weights, freq, 1e-5, interleaved)
+    for _ in range(5):
+        again = backward(*dev, *weights, freq, 1e-5, interleaved, wanted)
+        assert all(a is b is None or torch.equal(a, b) for a, b in zip(again, got))
+    if weighted == wanted:
+        bound = sa.qk_norm_rope_bwd(*dev, *weights, freq, eps=1e-5, interleaved=interleaved)
+        assert all(a is b is None or torch.equal(a, b) for a, b in zip(bound, got))
