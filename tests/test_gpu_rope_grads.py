@@ -74,3 +74,37 @@ def test_weights_and_gradients_left_out(N, R, interleaved, dtype, weighted, want
     if weighted == wanted:
         bound = sa.qk_norm_rope_bwd(*dev, *weights, freq, eps=1e-5, interleaved=interleaved)
         assert all(a is b is None or torch.equal(a, b) for a, b in zip(bound, got))
+
+
+@pytest.mark.parametrize("dtype", TYPES, ids=str)
+@pytest.mark.parametrize("heads", [(1, 3), (3, 5), (5, 1), (7, 2)])
+@pytest.mark.parametrize("N,R,interleaved", [(128, 128, False), (128, 90, False), (80, 32, True), (64, 64, False), (58, 58, True),
+                                             (160, 64, False), (61, 40, False)])
+def test_eps_of_zero(N, R, interleaved, heads, dtype, cuda_dev):
+    """Rows that are not zeros have finite results, however many of a warp's places have no head."""
+    B, S = 2, 7
+    freq = sa.rope_frequencies(R, device=cuda_dev)[0]
+    x = [rows(20 + i, B, S, H, N, dtype=dtype) for i, H in enumerate(heads)]
+    dy = [rows(22 + i, B, S, H, N, dtype=dtype, gain=0.1) for i, H in enumerate(heads)]
+    weights = [(1 + rows(24 + i, N, dtype=torch.float32, gain=0.2)).to(cuda_dev) for i in range(2)]
+    dev = [t.to(cuda_dev) for t in (*dy, *x)]
+    check(sa.qk_norm_rope_bwd(*dev, *weights, freq, eps=0.0, interleaved=interleaved), x, dy, weights, freq, 0.0, interleaved)
+    cos, sin = ref.cos_sin(freq.cpu(), None, B, S, 1.0)
+    for t, y, w in zip(x, sa.qk_norm_rope_fwd(*dev[2:], *weights, freq, eps=0.0, interleaved=interleaved), weights):
+        ref.near(y, *ref.norm_rope(t.double(), w.cpu().double(), 0.0, cos, sin, interleaved, 1.0), "y")
+
+
+def test_eps_of_zero_and_a_row_of_zeros(cuda_dev):
+    """Zeros come out, and the other rows' part of dw is what it is without that row."""
+    freq = sa.rope_frequencies(128, device=cuda_dev)[0]
+    x = rows(30, 1, 9, 3, 128, dtype=torch.float32).to(cuda_dev)
+    dy = rows(31, 1, 9, 3, 128, dtype=torch.float32).to(cuda_dev)
+    w = torch.ones(128, device=cuda_dev)
+    x[0, 4] = 0
+    y = sa.qk_norm_rope_fwd(x, None, w, None, freq, eps=0.0)[0]
+    assert not y[0, 4].any() and torch.isfinite(y).all()
+    dx, _, dw, _ = sa.qk_norm_rope_bwd(dy, None, x, None, w, None, freq, eps=0.0)
+    dy[0, 4] = 0
+    other, _, dw_other, _ = sa.qk_norm_rope_bwd(dy, None, x, None, w, None, freq, eps=0.0)
+    seen = [s for s in range(9) if s != 4]
+    assert torch.equal(dw, dw_other) and torch.equal(dx[0, seen], other[0, seen]) and torch.isfinite(dx).all()
