@@ -649,7 +649,8 @@ ATTN_API size_t attn_fwd_kv4_workspace_size(int B, int Sq, int Hq, int Hkv, int 
  * attn_fwd_kv4 -- attention of the last Sq tokens of each request over its cache:
  *   query i of request b sees the keys j < kv_len[b], with causal those j < kv_len[b] - Sq + i + 1
  *   lse, O  : as attn_fwd_bf16_lse, of the values that the cache stands for; a row that sees no key has O = 0, lse = -inf
- *   q, o    : BF16 [B, Sq, Hq, 128], strides q_str / o_str, q finite; o does not overlap q
+ *   q, o    : BF16 [B, Sq, Hq, 128], strides q_str / o_str, q finite (a row that is not has NaN as O and lse); o does not
+ *             overlap q
  *   lse     : float [B, Hq, Sq] output, contiguous
  *   kv_len  : device int32 [B], each request's tokens in the cache, the new ones included; clamped to
  *             [0, max_pages * page_size]; it does not change while the call is under way

@@ -508,14 +508,14 @@ __global__ void __launch_bounds__(32 * warps(kRows), 1) kv4_attn_kernel(const __
           continue;
         }
         const int s = div_by(row, p.G), h = done_head * (int)p.G.d + row - s * (int)p.G.d;
-        const float inv = l[n][e] > 0.0f ? 1.0f / l[n][e] : 0.0f;
+        const float inv = l[n][e] == 0.0f ? 0.0f : 1.0f / l[n][e];   // (a NaN stays one, here and in lse)
         uint2* const o = reinterpret_cast<uint2*>(p.o + done_b * p.o_str[0] + s * p.o_str[1] + h * p.o_str[2]);
 #pragma unroll
         for (int g = 0; g < 4; ++g)
           o[8 * g + r] = make_uint2(pack_bf16x2(v[g].x * inv, v[g].y * inv), pack_bf16x2(v[g].z * inv, v[g].w * inv));
         if (r == 0)
           p.lse[((long long)done_b * p.Hq + h) * p.S + s] =
-              l[n][e] > 0.0f ? (m[n][e] + log2f(l[n][e])) * 0.6931471805599453f : -INFINITY;
+              l[n][e] == 0.0f ? -INFINITY : (m[n][e] + log2f(l[n][e])) * 0.6931471805599453f;
       }
   }
 }
@@ -573,11 +573,11 @@ __global__ void __launch_bounds__(256) kv4_join_kernel(const __grid_constant__ A
     sum = make_float4(fmaf(f, v.x, sum.x), fmaf(f, v.y, sum.y), fmaf(f, v.z, sum.z), fmaf(f, v.w, sum.w));
   }
   const int s = div_by(row0 + row, p.G), h = head * (int)p.G.d + row0 + row - s * (int)p.G.d;
-  const float inv = l > 0.0f ? 1.0f / l : 0.0f;
+  const float inv = l == 0.0f ? 0.0f : 1.0f / l;
   reinterpret_cast<uint2*>(p.o + b * p.o_str[0] + s * p.o_str[1] + h * p.o_str[2])[lane] =
       make_uint2(pack_bf16x2(sum.x * inv, sum.y * inv), pack_bf16x2(sum.z * inv, sum.w * inv));
   if (lane == 0)
-    p.lse[((long long)b * p.Hq + h) * p.S + s] = l > 0.0f ? (m + log2f(l)) * 0.6931471805599453f : -INFINITY;
+    p.lse[((long long)b * p.Hq + h) * p.S + s] = l == 0.0f ? -INFINITY : (m + log2f(l)) * 0.6931471805599453f;
 }
 
 // Queries of a segment, tiles of them, and CTAs.
