@@ -1007,6 +1007,8 @@ def qk_norm_rope_bwd(dq_out: torch.Tensor, dk_out: torch.Tensor | None, q: torch
     at, at_strides, axes = _rope_positions(positions, B, S, dev)
     f, rope_dim = _rope_freq(freq, dev)
     qw, kw, w_type = _rope_weights(q, k, q_weight, k_weight, dev)
+    if dq_out is None or (dk_out is None and k is not None):
+        raise ValueError("dq_out, and dk_out beside a k, must be given")
     _expect("dq_out", dq_out, q.shape, q.dtype, dev)
     dq = _rope_made("dq", q, dq, dev)
     if k is not None:

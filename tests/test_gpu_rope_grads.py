@@ -108,3 +108,10 @@ def test_eps_of_zero_and_a_row_of_zeros(cuda_dev):
     other, _, dw_other, _ = sa.qk_norm_rope_bwd(dy, None, x, None, w, None, freq, eps=0.0)
     seen = [s for s in range(9) if s != 4]
     assert torch.equal(dw, dw_other) and torch.equal(dx[0, seen], other[0, seen]) and torch.isfinite(dx).all()
+
+
+def test_gradients_that_must_be_given(cuda_dev):
+    x, w = torch.ones((1, 2, 2, 64), device=cuda_dev), torch.ones(64, device=cuda_dev)
+    for dq_out, dk_out, k in ((None, x, x), (x, None, x), (None, None, None), (x, x, None)):
+        with pytest.raises(ValueError, match="dq_out|dk_out"):
+            sa.qk_norm_rope_bwd(dq_out, dk_out, x, k, w, None, None)
