@@ -217,14 +217,17 @@ attn_status qk_norm_rope_bwd(const void* dq_out, const void* dk_out, const void*
       return fail(ATTN_ERR_ALIGNMENT, "a weight's gradient is not aligned to its type");
     a.side[i].dw = dw[i];
   }
-  // sums over no rows
-  for (int i = 0; i < 2; ++i) {
-    if (dw[i] == nullptr || !(empty || a.side[i].H == 0)) continue;
-    TRY(check_device());
-    const cudaError_t e = cudaMemsetAsync(dw[i], 0, w_size * N, (cudaStream_t)stream);
-    if (e != cudaSuccess) return fail_cuda(e, "qk_norm_rope_bwd");
-  }
-  if (empty) return ATTN_OK;
+  // sums over no rows (after the last check: a refused call writes nothing)
+  auto zeros = [&]() -> attn_status {
+    for (int i = 0; i < 2; ++i) {
+      if (dw[i] == nullptr || !(empty || a.side[i].H == 0)) continue;
+      TRY(check_device());
+      const cudaError_t e = cudaMemsetAsync(dw[i], 0, w_size * N, (cudaStream_t)stream);
+      if (e != cudaSuccess) return fail_cuda(e, "qk_norm_rope_bwd");
+    }
+    return ATTN_OK;
+  };
+  if (empty) return zeros();
   a.inverse = 1;
   TRY(rope_side(a, 0, names[0], q, q_str, dq_out, dqo_str, dq, dq_str, true));
   TRY(rope_side(a, 1, names[1], k, k_str, dk_out, dko_str, dk, dk_str, true));
@@ -237,6 +240,7 @@ attn_status qk_norm_rope_bwd(const void* dq_out, const void* dk_out, const void*
       return fail(ATTN_ERR_INVALID_ARG, "qk_norm_rope_bwd: workspace_bytes=%zu < %zu required", workspace_bytes, need);
   }
   TRY(check_device());
+  TRY(zeros());
   const cudaError_t e = sa::launch_qk_norm_rope_bwd(a, reinterpret_cast<float*>(workspace), (cudaStream_t)stream);
   if (e != cudaSuccess) return fail_cuda(e, "qk_norm_rope_bwd");
   return ATTN_OK;
