@@ -560,7 +560,7 @@ ATTN_API attn_status rope_bwd(const void* dq_out, const void* dk_out, void* dq, 
 /*
  * qk_norm_rope_fwd -- the norm of each head of Q and K and its rotation in one pass:
  *   r = 1 / sqrt(sum x^2 / N + eps),  y = rope(x r weight)
- *   q_weight, k_weight : w_dtype [N], each or NULL (1).  w_dtype is dtype or ATTN_F32.
+ *   q_weight, k_weight : w_dtype [N], each or NULL (1); not looked at for a side without heads.  w_dtype is dtype or ATTN_F32.
  *   eps     : finite, >= 0; 0 counts as 2^-149 (a row of zeros has zeros, and the gradients of that r)
  *   the rest as rope_fwd (rope_dim = 0: the norm alone, freq and pos are not looked at)
  * FP32 between load and store, each result rounded once.  Enqueues one kernel on `stream`.

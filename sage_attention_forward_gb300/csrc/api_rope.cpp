@@ -122,10 +122,13 @@ attn_status rope_weights(sa::RopeArgs& a, const void* qw, const void* kw, float 
   if (w_dtype != a.type && w_dtype != ATTN_F32)
     return fail(ATTN_ERR_INVALID_ARG, "w_dtype=%d must be the rows' type or ATTN_F32", w_dtype);
   const uintptr_t align = w_dtype == ATTN_F32 ? 4 : 2;
-  if (reinterpret_cast<uintptr_t>(qw) % align != 0 || reinterpret_cast<uintptr_t>(kw) % align != 0)
-    return fail(ATTN_ERR_ALIGNMENT, "a weight is not aligned to its type");
-  a.side[0].w = qw;
-  a.side[1].w = kw;
+  const void* const w[2] = {qw, kw};
+  for (int i = 0; i < 2; ++i) {
+    if (a.side[i].H == 0) continue;   // (nothing of that side is looked at)
+    if (reinterpret_cast<uintptr_t>(w[i]) % align != 0)
+      return fail(ATTN_ERR_ALIGNMENT, "a weight is not aligned to its type");
+    a.side[i].w = w[i];
+  }
   a.eps = eps;
   a.w_type = w_dtype;
   return ATTN_OK;
