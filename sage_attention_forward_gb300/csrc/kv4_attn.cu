@@ -11,8 +11,9 @@
 // 264 q and 24 q summed over the channels, is taken off, formed by a product of the same operands.  V's are 1024 + c and 64 + c
 // where they stand, from which 1032 and 72 are subtracted, exactly: sums over many keys may be small beside their parts.
 // Q becomes FP16 with its row's largest magnitude in [1, 2): its own 8 bits stay (what is below 2^-14 of that magnitude is off
-// by up to 2^-25 of it).  P scale_V becomes FP16 with the largest scale that the warp has met in [2^6, 2^7): a power of two
-// that is raised, and O with it, as a row's reference maximum is.
+// by up to 2^-25 of it).  P scale_V becomes FP16 with the largest scale of its group that the warp has met in [2^6, 2^7): a power
+// of two that follows, and O's channels with it, as a row's reference maximum does.  (What is below 2^-14 then is off by up to
+// 2^-25: by 2^-31 of the group's largest scale.)
 // (e4m3 operands would need only masks, but mma.sync has no e4m3 on this machine: it came to 19 instructions a product.)
 //
 // Work.  The records of all requests and heads are one line of work, cut into items of equal length, found from the lengths on
@@ -101,6 +102,11 @@ __device__ __forceinline__ uint32_t larger(uint32_t a, uint32_t b) {
   asm("max.xorsign.abs.bf16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
   return d;
 }
+__device__ __forceinline__ uint32_t mul_bf16x2(uint32_t a, uint32_t b) {
+  uint32_t d;
+  asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
+  return d;
+}
 __device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
   uint32_t d;
   asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(d) : "f"(hi), "f"(lo));
@@ -137,6 +143,11 @@ __global__ void __launch_bounds__(32 * warps(kRows), 1) kv4_attn_kernel(const __
   constexpr int kCols = (kRows + 7) / 8;                   // columns of eight
   constexpr int kEach = kRows == 4 ? 1 : 2;                // queries of a lane and column
   constexpr int kPair = together(kRows), kStages = kHeld / kPair;
+  // V's scales times their power of two: as they are loaded, or where they are used (8 x 131072 tokens, one query token of 32 and of
+  // 64 heads on 8, and 8 x 65536 tokens, four of 32: loaded 193, 244, 189 us; used 199, 237, 183)
+  constexpr bool kEarly = kRows == 4;
+  auto early = [](uint32_t x, uint32_t d) { return kEarly ? mul_bf16x2(x, d) : x; };
+  auto late = [](uint32_t x, uint32_t d) { return kEarly ? x : mul_bf16x2(x, d); };
   extern __shared__ __align__(16) unsigned char rings[];
   __shared__ long long warp_sums[kWarps];
   griddep_wait();
@@ -316,9 +327,8 @@ __global__ void __launch_bounds__(32 * warps(kRows), 1) kv4_attn_kernel(const __
     uint32_t low, high, wide, near;
     asm volatile("mov.b32 %0, 0x64006400;\n\tmov.b32 %1, 0x54005400;" : "=r"(low), "=r"(high));
     asm volatile("mov.b32 %0, 0x5c005c00;\n\tmov.b32 %1, 0x4c004c00;" : "=r"(wide), "=r"(near));
-    // V's scales met so far are below 2^7 / down, bits of which, as BF16's, are in `most_v`
-    float down = 1.0f;
-    uint32_t most_v = 0;
+    // BF16 pairs of groups (0, 1) and (2, 3) of V: powers of two, 2^100 at most, that bring the scales met so far below 2^7
+    uint32_t down[2] = {0x71807180u, 0x71807180u};
     int slot = 0;
 #pragma unroll 1
     for (int tile = first; tile < last; tile += kPair) {
@@ -345,10 +355,10 @@ __global__ void __launch_bounds__(32 * warps(kRows), 1) kv4_attn_kernel(const __
         scales_of(s0.y, ks[0][2], ks[0][3]);
         scales_of(s1.x, ks[1][0], ks[1][1]);
         scales_of(s1.y, ks[1][2], ks[1][3]);
-        vs[2 * j][0] = s0.z;
-        vs[2 * j][1] = s0.w;
-        vs[2 * j + 1][0] = s1.z;
-        vs[2 * j + 1][1] = s1.w;
+        vs[2 * j][0] = early(s0.z, down[0]);
+        vs[2 * j][1] = early(s0.w, down[1]);
+        vs[2 * j + 1][0] = early(s1.z, down[0]);
+        vs[2 * j + 1][1] = early(s1.w, down[1]);
 #pragma unroll
         for (int g = 0; g < 4; ++g) {
           uint32_t a[4], c[4];
@@ -400,18 +410,42 @@ __global__ void __launch_bounds__(32 * warps(kRows), 1) kv4_attn_kernel(const __
           for (int i = 2; i < 2 * kPair; i += 2) most[n][e] = fmax3(most[n][e], sc[n][e][i], sc[n][e][i + 1]);
           raise = raise || most[n][e] > m[n][e] + kSlack;
         }
-      uint32_t scale = larger(vs[0][0], vs[0][1]);
+      uint32_t top[2] = {vs[0][0], vs[0][1]};
 #pragma unroll
-      for (int i = 1; i < 2 * kPair; ++i) scale = larger(scale, larger(vs[i][0], vs[i][1]));
-      scale = larger(scale, scale >> 16) & 0x7fffu;
-      raise = raise || scale > most_v;
+      for (int i = 1; i < 2 * kPair; ++i)
+#pragma unroll
+        for (int w = 0; w < 2; ++w) top[w] = larger(top[w], vs[i][w]);
+      const uint32_t top_v = larger(late(top[0], down[0]), late(top[1], down[1]));
+      raise = raise || (((top_v & 0x7fff7fffu) + 0x3d003d00u) & 0x80008000u) != 0;   // one is 2^7 or more (BF16 0x4300)
       if (__any_sync(0xffffffffu, raise)) {
-        const uint32_t largest = max(most_v, __reduce_max_sync(0xffffffffu, scale));
-        // 2^(6 - e) for scales below 2^(e + 1); BF16's exponent field is bits 7 to 14
-        const int field = max((int)(largest >> 7), 33);   // (down at most 2^100: P times it stays finite)
-        const float next_down = __uint_as_float((uint32_t)(260 - field) << 23), change = next_down / down;
-        most_v = (uint32_t)field << 7 | 0x7fu;
-        down = next_down;
+        float change[4];
+        if (kEarly) {   // the scales again, as the record has them, and each group's largest
+          top[0] = top[1] = 0u;
+#pragma unroll
+          for (int i = 0; i < 2 * kPair; ++i) {
+            const uint2 two = *reinterpret_cast<const uint2*>(recs + i / 2 * kKvRecord + kKvScales + i % 2 * 128 + r * 16 + 8);
+            const bool seen = ((held >> (i / 2)) & 1) && tile * kKvTile + r + 8 * i < len;
+            vs[i][0] = seen ? two.x : 0u;
+            vs[i][1] = seen ? two.y : 0u;
+#pragma unroll
+            for (int w = 0; w < 2; ++w) top[w] = larger(top[w], vs[i][w]);
+          }
+        }
+#pragma unroll
+        for (int w = 0; w < 2; ++w) {
+          uint32_t pair = 0;
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            // 2^(6 - e) for scales below 2^(e + 1); BF16's exponent field is bits 7 to 14
+            const uint32_t field = __reduce_max_sync(0xffffffffu, top[w] >> (16 * h + 7) & 0xffu);
+            const uint32_t was = down[w] >> (16 * h + 7) & 0xffu, now = min(was, 260 - field);
+            pair |= now << (16 * h + 7);
+            change[2 * w + h] = __uint_as_float(now << 23) * __uint_as_float((254 - was) << 23);
+          }
+          down[w] = pair;
+#pragma unroll
+          for (int i = 0; i < 2 * kPair; ++i) vs[i][w] = early(vs[i][w], pair);
+        }
 #pragma unroll
         for (int n = 0; n < kCols; ++n)
 #pragma unroll
@@ -428,7 +462,7 @@ __global__ void __launch_bounds__(32 * warps(kRows), 1) kv4_attn_kernel(const __
               for (int u = 0; u < 2; ++u)
 #pragma unroll
                 for (int i = 0; i < 4; ++i)
-                  if (kEach == 1 || (i & 1) == e) acc[g][u][n][i] *= shrink * change;
+                  if (kEach == 1 || (i & 1) == e) acc[g][u][n][i] *= shrink * change[g];
           }
       }
 #pragma unroll
@@ -439,7 +473,6 @@ __global__ void __launch_bounds__(32 * warps(kRows), 1) kv4_attn_kernel(const __
           for (int i = 0; i < 2 * kPair; ++i) {
             sc[n][e][i] = ex2_approx(sc[n][e][i] - m[n][e]);
             l[n][e] += sc[n][e][i];
-            sc[n][e][i] *= down;
           }
 #pragma unroll
       for (int j = 0; j < kPair; ++j) {
@@ -451,6 +484,18 @@ __global__ void __launch_bounds__(32 * warps(kRows), 1) kv4_attn_kernel(const __
         scales_of(vs[2 * j][1], v[0][2], v[0][3]);
         scales_of(vs[2 * j + 1][0], v[1][0], v[1][1]);
         scales_of(vs[2 * j + 1][1], v[1][2], v[1][3]);
+        if constexpr (!kEarly) {
+#pragma unroll
+          for (int w = 0; w < 2; ++w) {
+            float d[2];
+            scales_of(down[w], d[0], d[1]);
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+              v[h][2 * w] *= d[0];
+              v[h][2 * w + 1] *= d[1];
+            }
+          }
+        }
         uint32_t p0[kCols], p1[kCols];   // B operands: keys 0 to 7 and 8 to 15
 #pragma unroll
         for (int g = 0; g < 4; ++g) {
@@ -485,7 +530,9 @@ __global__ void __launch_bounds__(32 * warps(kRows), 1) kv4_attn_kernel(const __
       p.head[(long long)b * p.segments + seg] = make_int2(item, (int)(end - item) + 1);
     }
     more = begin();
-    const float up = 1.0f / down;
+    float up[4];
+#pragma unroll
+    for (int g = 0; g < 4; ++g) up[g] = __uint_as_float((254 - (down[g / 2] >> (16 * (g % 2) + 7) & 0xffu)) << 23);
 #pragma unroll
     for (int n = 0; n < kCols; ++n)
 #pragma unroll
@@ -498,7 +545,8 @@ __global__ void __launch_bounds__(32 * warps(kRows), 1) kv4_attn_kernel(const __
 #pragma unroll
         for (int g = 0; g < 4; ++g) {
           const int c = kEach == 1 ? g & 1 : e;
-          v[g] = make_float4(acc[g][0][n][c] * up, acc[g][0][n][2 + c] * up, acc[g][1][n][c] * up, acc[g][1][n][2 + c] * up);
+          v[g] = make_float4(acc[g][0][n][c] * up[g], acc[g][0][n][2 + c] * up[g], acc[g][1][n][c] * up[g],
+                             acc[g][1][n][2 + c] * up[g]);
         }
         if (!complete) {
           const long long piece = (2ll * item + starts) * kRows + in_tile;

@@ -26,3 +26,24 @@ def test_a_query_that_is_no_number(Hq, lens, cuda_dev):
         seen = torch.ones((1, lens[b]), dtype=torch.bool)
         want = ref.attention(q[b, :, keep].cpu(), *(t[b, :lens[b]] for t in kv), seen, 128 ** -0.5)
         ref.check(o[b, :, keep], lse[b, keep], *want)
+
+
+@pytest.mark.parametrize("gains", [(1.0, 2.0 ** -16, 2.0 ** -32, 2.0 ** -64), (2.0 ** -40, 2.0 ** 60, 0.0, 1.0)])
+@pytest.mark.parametrize("Hq", [4, 8, 16])
+@pytest.mark.parametrize("lens", [(40, 5), (6000, 300)])
+def test_groups_of_values_of_unlike_sizes(lens, Hq, gains, cuda_dev):
+    """V's groups of 32 channels have scales of their own: what one holds is no matter of another's size."""
+    B, n, most = len(lens), max(lens), -(-max(lens) // 16)
+    size = torch.tensor(gains, dtype=torch.float64).repeat_interleave(32)
+    k, v = rows(20, B, n, 1, 128), (rows(21, B, n, 1, 128, dtype=torch.float64) * size).to(torch.bfloat16)
+    table, cache = torch.arange(B * most, dtype=torch.int32).view(B, most).to(cuda_dev), sa.kv4_cache(B * most, 1, 16, cuda_dev)
+    sa.kv4_write(k.to(cuda_dev), v.to(cuda_dev), cache, table, ints(*[0] * B).to(cuda_dev), ints(*lens).to(cuda_dev))
+    kv, q = ref.held(k, v), rows(22, B, 1, Hq, 128).to(cuda_dev)
+    o, lse = sa.attn_fwd_kv4(q, cache, table, ints(*lens).to(cuda_dev))
+    for b, m in enumerate(lens):
+        seen = torch.ones((1, m), dtype=torch.bool)
+        for g in range(4):
+            part = slice(32 * g, 32 * g + 32)
+            kb, vb, ks, vs = (t[b, :m] for t in kv)
+            want = ref.attention(q[b].cpu(), kb, vb[..., part], ks, vs[..., part], seen, 128 ** -0.5)
+            ref.check(o[b][..., part], lse[b], *want)
