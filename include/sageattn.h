@@ -659,9 +659,11 @@ ATTN_API size_t attn_fwd_kv4_workspace_size(int B, int Sq, int Hq, int Hkv, int 
  *   workspace : at least attn_fwd_kv4_workspace_size bytes, 16-byte aligned; overwritten; one for each call under way
  * Made for one or a few tokens a request: 16 queries (Sq * Hq / Hkv) share one read of the cache, more read it again.
  * For a long piece of a prompt, kv4_read and attn_fwd_bf16_lse.  Q takes part in FP16 with its row's largest magnitude
- * scaled into [1, 2) (what is below 2^-14 of it is off by up to 2^-25 of it), products with the codes are exact, P times V's
+ * scaled into [1, 2) (what is below 2^-14 of it is off by up to 2^-25 of it); products with the codes are exact, their sums over a
+ * group are rounded in FP32 beside parts of up to 271 |q|, which are taken off again (a score is off by up to 2^-12.8 sum |q
+ * scale_K|; of sum |q k| that came to 5 10^-7 rms and 4 10^-6 at most for normal values, with and without a mean).  P times V's
  * scale is rounded to FP16 beside the largest scale of its group of 32 channels (off by up to 2^-11 of itself, or 2^-31 of that
- * scale where this is more), sums are FP32 in a fixed order (the same inputs give the same bits), O is rounded once.  Enqueues
+ * scale where this is more); sums are FP32 in a fixed order (the same inputs give the same bits), O is rounded once.  Enqueues
  * two kernels on `stream`.
  */
 ATTN_API attn_status attn_fwd_kv4(const void* q, const void* cache, int num_pages, int page_size,

@@ -47,3 +47,36 @@ def test_groups_of_values_of_unlike_sizes(lens, Hq, gains, cuda_dev):
             kb, vb, ks, vs = (t[b, :m] for t in kv)
             want = ref.attention(q[b].cpu(), kb, vb[..., part], ks, vs[..., part], seen, 128 ** -0.5)
             ref.check(o[b][..., part], lse[b], *want)
+
+
+def tight(q, k, v, step, v_step, seen, scale):
+    """O, lse and their bounds for queries of whole numbers up to 127 (scaled by a power of two): every product with a code and every
+    sum of a group, the constants 264 and 24 and all, is a whole multiple of one unit below 2^24 (32 x 271 x 127 < 2^20.1), exact in
+    FP32 in any order.  What is left of a score's error, u = 2^-24: three additions of the groups' sums and their four products,
+    fused (4 u of the sum of |q k|), the factor of query, scale and log2 e (rounded: 2 u, and its product: 1 u), and the difference
+    to the reference maximum (1 u of each): 9 u sum |q k|, times the scale.  exp2 within 2^-22.  P as tests/kv4_ref.py has it."""
+    G = q.shape[1] // k.shape[1]
+    q = q.double()
+    kk, vv, st = (t.repeat_interleave(G, 1) for t in (k, v, v_step))
+    s = torch.einsum("shd,nhd->hsn", q, kk) * scale
+    s = s.masked_fill(~seen[None], -math.inf)
+    lse = torch.logsumexp(s, -1)
+    p = torch.exp(s - lse[..., None])
+    o = torch.einsum("hsn,nhd->shd", p, vv)
+    off = (scale * 9 * 2.0 ** -24 * torch.einsum("shd,nhd->hsn", q.abs(), kk.abs())).masked_fill(~seen[None], 0.0).amax(-1)
+    size = torch.einsum("hsn,nhd->shd", p, vv.abs())
+    bound = size * (2.0 ** -11 + 2.0 ** -18 + 2 * off.T[..., None]) + v.shape[0] * 2.0 ** -28 * float(st.abs().max())
+    return o, lse, bound, off + 2.0 ** -19 + lse.abs() * 2.0 ** -22
+
+
+@pytest.mark.parametrize("Hq", [4, 8, 16])
+@pytest.mark.parametrize("gain,scale", [(1.0, 0.001), (1.0, 0.0884), (2.0 ** -7, 0.0884), (1.0, 0.3), (2.0 ** 10, 2.0 ** -12)])
+def test_scores_of_whole_queries(gain, scale, Hq, cuda_dev):
+    """Flat and sharp rows (scores up to some hundreds apart), within about 10^-6 of the largest scores."""
+    lens = (90, 700)
+    cache, table, *kv = filled(40, lens, 1, 16, cuda_dev)
+    g = torch.Generator().manual_seed(41)
+    q = (torch.randint(-127, 128, (2, 1, Hq, 128), generator=g).double() * gain).to(torch.bfloat16)
+    o, lse = sa.attn_fwd_kv4(q.to(cuda_dev), cache, table, ints(*lens).to(cuda_dev), softmax_scale=scale)
+    for b, n in enumerate(lens):
+        ref.check(o[b], lse[b], *tight(q[b], *(t[b, :n] for t in kv), torch.ones((1, n), dtype=torch.bool), scale))
