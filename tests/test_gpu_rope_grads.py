@@ -115,3 +115,23 @@ def test_gradients_that_must_be_given(cuda_dev):
     for dq_out, dk_out, k in ((None, x, x), (x, None, x), (None, None, None), (x, x, None)):
         with pytest.raises(ValueError, match="dq_out|dk_out"):
             sa.qk_norm_rope_bwd(dq_out, dk_out, x, k, w, None, None)
+
+
+@pytest.mark.parametrize("interleaved", [False, True])
+@pytest.mark.parametrize("N,R", [(128, 128), (128, 90), (77, 30)])
+def test_expanded_gradients_and_inputs(N, R, interleaved, cuda_dev):
+    """Strides of 0 (a gradient that a sum or a mean hands on, one row for all heads) give the bits of the same tensor written out."""
+    B, S, H = 2, 5, 3
+    freq = sa.rope_frequencies(R, device=cuda_dev)[0]
+    w = (1 + rows(40, N, dtype=torch.float32, gain=0.2)).to(cuda_dev)
+    x, y = (rows(41 + i, B, S, H, N, dtype=torch.bfloat16).to(cuda_dev) for i in range(2))
+    one = rows(43, N, dtype=torch.bfloat16).to(cuda_dev)
+    shapes = [one.expand(B, S, H, N), x[:, :1].expand(B, S, H, N), x[:, :, 1:2].expand(B, S, H, N), x[:1].expand(B, S, H, N)]
+    same = lambda a, b: all(p is q is None or torch.equal(p, q) for p, q in zip(a, b))  # noqa: E731
+    for t in shapes:
+        assert t.stride(3) == 1 and 0 in t.stride()
+        full = t.clone(memory_format=torch.contiguous_format)
+        assert same(sa.rope_bwd(t, y, freq, interleaved=interleaved), sa.rope_bwd(full, y, freq, interleaved=interleaved))
+        for a, b in (((t, y, x, y), (full, y, x, y)), ((y, x, t, y), (y, x, full, y)), ((t, t, t, t), (full, full, full, full))):
+            assert same(sa.qk_norm_rope_bwd(*a, w, w, freq, interleaved=interleaved),
+                        sa.qk_norm_rope_bwd(*b, w, w, freq, interleaved=interleaved))
