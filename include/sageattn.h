@@ -539,7 +539,8 @@ ATTN_API attn_status layer_norm_bwd(const void* dy, const void* x, const void* w
  *   axes    : position axes in pos, 1 to 4 (video: frame, row, column)
  *   freq    : device uint64 [rope_dim / 2]: turns a position times 2^64, rounded, modulo 2^64; the two lowest bits are
  *             the pair's axis (an axis past the last one is the last).  The product with a position wraps to the angle's
- *             fraction of a turn, off by at most 2^-31 turns for every int32 position.
+ *             fraction of a turn: table and product together are off by less than 2^-30 turns for every int32 position, and
+ *             the fraction is taken with 24 bits (2^-26 turns at most).
  *   magnitude : finite factor of cosine and sine (1, or the attention factor of a scaled rotation)
  *   1 <= N <= 512, rope_dim even, 0 <= rope_dim <= N, B * S * (Hq + Hk) <= 2^30 rows (0: nothing is done)
  * FP32 between load and store, each result rounded once.  Enqueues one kernel on `stream`.

@@ -5,7 +5,8 @@
 //
 // Bound by memory: x is read and y written once.  A unit is a warp's: heads of one token, Q's and then K's, the token's
 // cosines formed once for all of them (qk_rope.cuh).  A lane holds both channels of its pairs, 16 channels in
-// all, so the rotation takes no exchange; a head of 128 channels is 8 lanes', and a warp works on four heads at a time.
+// all, so the rotation takes no exchange (but of halves that are no whole pieces: their partners come through shared
+// memory); a head of 128 channels is 8 lanes', and a warp works on four heads at a time.
 #include <cuda_runtime.h>
 
 #include "qk_rope.cuh"

@@ -3,9 +3,10 @@
 //   angle(t, i) = position(t, axis(i)) w_i         y = m (a cos - b sin, b cos + a sin) of each pair (a, b) of channels
 //
 // Frequencies come as turns a position in units of 2^-64, so that the whole turns of an angle fall off in the
-// product of two integers: the remainder is exact to 2^-33 turns for any position of 31 bits, without tables of
-// cosines in memory and without 64-bit floating point (of which an SM has little).  A warp forms the cosines of one
-// token once, in shared memory, and takes them for all of the token's heads.
+// product of two integers, for any position of 32 bits, without tables of cosines in memory and without 64-bit floating
+// point (of which an SM has little).  What is left is off by less than 2^-30 turns (the table's entries by up to 3.5 units,
+// the axis being in two bits, times 2^31; the product is cut at 2^-32), and then rounded to 24 bits: 2^-26 turns at most.  A
+// warp forms the cosines of one token once, in shared memory, and takes them for all of the token's heads.
 #pragma once
 
 #include <algorithm>

@@ -207,7 +207,8 @@ cudaError_t launch_bwd(const RopeParams& p, int& ctas, bool vec, bool next, cuda
 
 }  // namespace
 
-// As many as the kernel with most CTAs an SM can have; a CTA may have no unit.
+// What the workspace has room for, of any kernel: up to four CTAs an SM, of which the present ones take two at most (launch_bwd;
+// the size is the interface's and stays).  K's sums begin where Q's would end at that number.  A CTA may have no unit.
 int rope_bwd_ctas(int B, int S, int Hq, int Hk) {
   const long long warps = ((long long)B * S * (Hq > Hk ? Hq : Hk) + 3) / 4;
   const long long ctas = (warps + kRopeWarps - 1) / kRopeWarps;
