@@ -38,6 +38,7 @@ constexpr int kStart = 4;           // what a segment's start and end cost besid
 constexpr int kCtas = 152;
 constexpr float kSlack = 8.0f;      // a row's reference maximum is raised when one passes it by more (log2 units)
 constexpr float kNone = -1.5e38f;    // a row's maximum before its first key (finite: differences of two are no NaN)
+constexpr float kPart = 0x1p-30f;   // O's sums are taken times this: those of many keys of V's largest values stay finite
 constexpr int kDim = 128;
 
 struct AttnParams {
@@ -533,7 +534,7 @@ __global__ void __launch_bounds__(32 * warps(kRows), 1) kv4_attn_kernel(const __
     more = begin();
     float up[4];
 #pragma unroll
-    for (int g = 0; g < 4; ++g) up[g] = __uint_as_float((254 - (down[g / 2] >> (16 * (g % 2) + 7) & 0xffu)) << 23);
+    for (int g = 0; g < 4; ++g) up[g] = __uint_as_float((254 - (down[g / 2] >> (16 * (g % 2) + 7) & 0xffu)) << 23) * kPart;
 #pragma unroll
     for (int n = 0; n < kCols; ++n)
 #pragma unroll
@@ -557,7 +558,7 @@ __global__ void __launch_bounds__(32 * warps(kRows), 1) kv4_attn_kernel(const __
           continue;
         }
         const int s = div_by(row, p.G), h = done_head * (int)p.G.d + row - s * (int)p.G.d;
-        const float inv = l[n][e] == 0.0f ? 0.0f : 1.0f / l[n][e];   // (a NaN stays one, here and in lse)
+        const float inv = l[n][e] == 0.0f ? 0.0f : 1.0f / (l[n][e] * kPart);   // (a NaN stays one, here and in lse)
         uint2* const o = reinterpret_cast<uint2*>(p.o + done_b * p.o_str[0] + s * p.o_str[1] + h * p.o_str[2]);
 #pragma unroll
         for (int g = 0; g < 4; ++g)
@@ -622,7 +623,7 @@ __global__ void __launch_bounds__(256) kv4_join_kernel(const __grid_constant__ A
     sum = make_float4(fmaf(f, v.x, sum.x), fmaf(f, v.y, sum.y), fmaf(f, v.z, sum.z), fmaf(f, v.w, sum.w));
   }
   const int s = div_by(row0 + row, p.G), h = head * (int)p.G.d + row0 + row - s * (int)p.G.d;
-  const float inv = l == 0.0f ? 0.0f : 1.0f / l;
+  const float inv = l == 0.0f ? 0.0f : 1.0f / (l * kPart);
   reinterpret_cast<uint2*>(p.o + b * p.o_str[0] + s * p.o_str[1] + h * p.o_str[2])[lane] =
       make_uint2(pack_bf16x2(sum.x * inv, sum.y * inv), pack_bf16x2(sum.z * inv, sum.w * inv));
   if (lane == 0)

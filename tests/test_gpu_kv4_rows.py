@@ -80,3 +80,21 @@ def test_scores_of_whole_queries(gain, scale, Hq, cuda_dev):
     o, lse = sa.attn_fwd_kv4(q.to(cuda_dev), cache, table, ints(*lens).to(cuda_dev), softmax_scale=scale)
     for b, n in enumerate(lens):
         ref.check(o[b], lse[b], *tight(q[b], *(t[b, :n] for t in kv), torch.ones((1, n), dtype=torch.bool), scale))
+
+
+@pytest.mark.parametrize("size", [3e38, 1e33, 2.0 ** -97])
+@pytest.mark.parametrize("Hq", [4, 8, 16])
+@pytest.mark.parametrize("lens", [(40, 5), (6000, 300)])
+def test_values_at_the_ends_of_the_range(lens, Hq, size, cuda_dev):
+    """Sums over many keys pass what FP32 holds where their mean does not; the other end has no bits to spare."""
+    B, n, most = len(lens), max(lens), -(-max(lens) // 16)
+    k, v = rows(50, B, n, 1, 128), rows(51, B, n, 1, 128, dtype=torch.float64).abs().clamp(0.05, 1.0)
+    v = (v * size).to(torch.bfloat16)
+    table, cache = torch.arange(B * most, dtype=torch.int32).view(B, most).to(cuda_dev), sa.kv4_cache(B * most, 1, 16, cuda_dev)
+    sa.kv4_write(k.to(cuda_dev), v.to(cuda_dev), cache, table, ints(*[0] * B).to(cuda_dev), ints(*lens).to(cuda_dev))
+    kv, q = ref.held(k, v), rows(52, B, 1, Hq, 128).to(cuda_dev)
+    o, lse = sa.attn_fwd_kv4(q, cache, table, ints(*lens).to(cuda_dev))
+    assert torch.isfinite(o).all()
+    for b, m in enumerate(lens):
+        seen = torch.ones((1, m), dtype=torch.bool)
+        ref.check(o[b], lse[b], *ref.attention(q[b].cpu(), *(t[b, :m] for t in kv), seen, 128 ** -0.5))
